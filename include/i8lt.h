@@ -19,8 +19,10 @@
  * Beside it: the MLP's SiLU (with an optional fusion into the forward
  * epilogue), a token-sharded forward, the weight gradient of the
  * trainable-weight mode, the 4-bit (NF4 and FP4) weight-only layers of QLoRA
- * fine-tuning, an entry point that allocates nothing, per-launch timing and
- * a diagnostic of the bounded waits (each documented below).
+ * fine-tuning, an entry point that allocates nothing, the operators that
+ * fine-tune on top of the frozen layers (low-rank adapters, layer norm,
+ * AdamW), per-launch timing and a diagnostic of the bounded waits (each
+ * documented below).
  *
  * Conventions for every entry point:
  *   - Matrices are row-major and contiguous.  Device pointers unless stated.
@@ -69,7 +71,8 @@ typedef enum { I8LT_F16 = 0, I8LT_BF16 = 1, I8LT_F32 = 2 } i8lt_dtype;
 
 /* Version of this ABI; bumped on any incompatible change (3: the 4-bit
  * input gradients take grad_bias; 4: the double-quantized absmax entry
- * points and their kernel id, I8LT_K_COUNT = 21). */
+ * points and their kernel id.  New entry points and kernel ids that leave
+ * the existing ones as they are keep the version). */
 int i8lt_abi_version(void);
 
 /* Human-readable name of a status code (static storage). */
@@ -467,6 +470,124 @@ int i8lt_absmax8_dequantize(const uint8_t* q, const float* absmax2,
                             const float* offset, int64_t count, float* out,
                             void* stream);
 
+/*
+ * ---- Fine-tuning on top of the frozen layers ------------------------------
+ *
+ * Layer norm over the last dimension of x [M, N]:
+ *   mean[m] = sum_n x[m,n] / N
+ *   rstd[m] = 1 / sqrt(sum_n (x[m,n] - mean[m])^2 / N + eps)
+ *   y[m,n]  = (x[m,n] - mean[m]) * rstd[m] * w[n] + b[n]
+ *   x, y [M, N] dtype xt; w, b [N] dtype wt, each may be NULL (1 and 0);
+ *   mean, rstd [M] fp32 (written, each may be NULL).  eps >= 0.
+ * Backward, h = (x - mean) * rstd:
+ *   gx = rstd * (g w - mean_n(g w) - h * mean_n(g w h))   [M, N] dtype xt
+ *   gw[n] = sum_m g h, gb[n] = sum_m g                     [N] dtype wt
+ *   g [M, N] dtype xt; mean and rstd from the forward; gx, gw, gb each may be
+ *   NULL (at least one is not); ws of i8lt_layer_norm_backward_workspace_size
+ *   bytes, 256-byte aligned, when gw or gb is given.
+ * All arithmetic is fp32, every output is rounded once; the sums over the
+ * tokens are taken in a fixed order (no atomics): equal inputs give equal
+ * bits.  M == 0 writes zeros to gw and gb.
+ */
+int i8lt_layer_norm_forward(const void* x, int xt, int64_t M, int64_t N,
+                            const void* w, const void* b, int wt, float eps,
+                            void* y, float* mean, float* rstd, void* stream);
+size_t i8lt_layer_norm_backward_workspace_size(int64_t M, int64_t N);
+int i8lt_layer_norm_backward(const void* g, const void* x, int xt, int64_t M,
+                             int64_t N, const float* mean, const float* rstd,
+                             const void* w, int wt, void* gx, void* gw,
+                             void* gb, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Low-rank adapters of many requests at once, beside a shared projection
+ * K -> N.  Token m uses adapter e = index[m]; a value outside [0, E) means
+ * none (its y is base, its gx is addend):
+ *   t[m]  = x[m] A[e]^T                     y[m]  = base[m] + scale[e] t[m] B[e]^T
+ *   u[m]  = scale[e] g[m] B[e]              gx[m] = addend[m] + u[m] A[e]
+ *   gA[e] = sum over e's tokens u[m]^T x[m] gB[e] = scale[e] sum g[m]^T t[m]
+ *   x [M, K], g, base, y [M, N], addend, gx [M, K], t [M, r],
+ *   A and gA [E, r, K], B and gB [E, N, r]: all of dtype dt (I8LT_F16 or
+ *   I8LT_BF16, the compute types of the 4-bit layers); index [M] int32;
+ *   scale [E] fp32, or NULL (1).  1 <= r <= I8LT_MAX_RANK.
+ *   base and addend may be NULL (0) and may be the same buffer as y and gx.
+ * Sums are fp32.  t and u are rounded to dt; y, gx, gA and gB are rounded
+ * once.  An adapter without tokens gets zero gradients.  Equal inputs give
+ * equal bits.
+ *
+ * i8lt_adapter_plan sorts the tokens of a batch by adapter (on the device,
+ * asynchronously) into `plan` (i8lt_adapter_plan_bytes(M, E) bytes, 256-byte
+ * aligned); every call on tokens of that batch takes it, in all layers and
+ * in both directions.  index NULL: all tokens use adapter 0.
+ * The sizes M, E, r of a call must be those of its plan, A, B and ws
+ * (i8lt_adapters_workspace_size bytes, 256-byte aligned, status word first;
+ * either direction).
+ * gx, gA, gB may each be NULL (at least one is not); x is read for gA only
+ * and t for gB only.
+ */
+#define I8LT_MAX_RANK 128
+size_t i8lt_adapter_plan_bytes(int64_t M, int64_t E);
+int i8lt_adapter_plan(const int32_t* index, int64_t M, int64_t E, void* plan,
+                      size_t plan_bytes, void* stream);
+size_t i8lt_adapters_workspace_size(int64_t M, int64_t K, int64_t N, int64_t E,
+                                    int64_t r);
+int i8lt_adapters_forward(const void* x, int dt, int64_t M, int64_t K,
+                          const void* A, const void* B, int64_t E, int64_t r,
+                          int64_t N, const float* scale, const void* plan,
+                          const void* base, void* y, void* t, void* ws,
+                          size_t ws_bytes, void* stream);
+int i8lt_adapters_backward(const void* g, const void* x, const void* t, int dt,
+                           int64_t M, int64_t K, const void* A, const void* B,
+                           int64_t E, int64_t r, int64_t N, const float* scale,
+                           const void* plan, const void* addend, void* gx,
+                           void* gA, void* gB, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/*
+ * One AdamW step (decoupled weight decay) over `count` tensors at once:
+ *   g' = grad_scale * g
+ *   m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ *   params, grads, sizes   HOST arrays of `count` device pointers and element
+ *            counts (read during the call); parameters of dtype pt (updated
+ *            in place), gradients of dtype gt, each aligned to its element;
+ *            a tensor whose gradient is NULL stays as it is, its states too
+ *   step     this step's number, from 1
+ *   grad_scale, found_inf  optional device fp32 scalars (NULL: 1 and 0): the
+ *            factor of every gradient (1 / loss scale, a clip factor), and a
+ *            value that, when it is not 0, makes the call change nothing
+ * The states of all tensors lie in flat buffers, in the order of the tensors,
+ * each tensor's start rounded up to a multiple of I8LT_ADAMW_BLOCK elements
+ * (the buffers' length: the sum of the sizes rounded up so; elements past a
+ * tensor's end are not used and end up 0 in 8 bits).
+ *   i8lt_adamw_step       m, v fp32
+ *   i8lt_adamw_step_8bit  m and r = sqrt(v) in FP8 E4M3, with one fp32 absmax
+ *            per I8LT_ADAMW_BLOCK elements: value = fp32(E4M3(code) *
+ *            fp32(absmax * fp32(1/448))), code = E4M3(value * fp32(448 *
+ *            fp32(1/absmax))), rounded to nearest even; an r above 0 takes
+ *            no code below the smallest, 2^-9; a block with absmax < 2^-100
+ *            takes the code of 0.  The parameter uses the moments before
+ *            they are rounded.
+ * State arithmetic is single IEEE fp32 operations in the order above (r is
+ * squared to give v), so the states' bits follow from the formulas.
+ * Non-finite gradients make the states of their block non-finite; skip such
+ * a step with found_inf.
+ */
+#define I8LT_ADAMW_BLOCK 256
+int i8lt_adamw_step(void* const* params, int pt, const void* const* grads,
+                    int gt, const int64_t* sizes, int64_t count, float* m,
+                    float* v, int64_t step, double lr, double beta1,
+                    double beta2, double eps, double weight_decay,
+                    const float* grad_scale, const float* found_inf,
+                    void* stream);
+int i8lt_adamw_step_8bit(void* const* params, int pt, const void* const* grads,
+                         int gt, const int64_t* sizes, int64_t count,
+                         uint8_t* m, float* m_absmax, uint8_t* r,
+                         float* r_absmax, int64_t step, double lr,
+                         double beta1, double beta2, double eps,
+                         double weight_decay, const float* grad_scale,
+                         const float* found_inf, void* stream);
+
 /* SiLU between the two layers of an MLP: out = h * sigmoid(h), and its
  * backward out = g * silu'(h).  n elements of dtype dt. */
 int i8lt_silu_forward(const void* h, int dt, int64_t n, void* out, void* stream);
@@ -487,7 +608,8 @@ typedef enum {
   I8LT_K_BWD_GEMM = 8, I8LT_K_SILU = 9, I8LT_K_SILU_BACKWARD = 10, I8LT_K_WIDEN_CODES = 11,
   I8LT_K_DEQUANT_WEIGHT = 12, I8LT_K_COL_QUANTIZE = 13, I8LT_K_WGRAD_GEMM = 14, I8LT_K_UNIT_PLAN = 15,
   I8LT_K_NF4_QUANTIZE = 16, I8LT_K_NF4_DEQUANTIZE = 17, I8LT_K_NF4_GEMM_FWD = 18, I8LT_K_NF4_GEMM_BWD = 19,
-  I8LT_K_ABSMAX8 = 20, I8LT_K_COUNT = 21
+  I8LT_K_ABSMAX8 = 20, I8LT_K_LAYER_NORM = 21, I8LT_K_LAYER_NORM_BWD = 22, I8LT_K_LAYER_NORM_GRAD_SUM = 23,
+  I8LT_K_ADAPTER_PLAN = 24, I8LT_K_ADAPTERS = 25, I8LT_K_ADAPTERS_GRAD = 26, I8LT_K_ADAMW = 27, I8LT_K_COUNT = 28
 } i8lt_kernel_id;
 typedef struct {
   int kernel;

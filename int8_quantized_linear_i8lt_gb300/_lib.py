@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from ctypes import POINTER, Structure, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, Structure, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libi8lt.so")
@@ -31,6 +31,8 @@ I8LT_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 I8LT_F16, I8LT_BF16, I8LT_F32 = 0, 1, 2
 I8LT_MAX_K = 133144
+I8LT_MAX_RANK = 128
+I8LT_ADAMW_BLOCK = 256
 
 
 class i8lt_fwd_layout(Structure):
@@ -51,7 +53,8 @@ class i8lt_kernel_time(Structure):
 KERNELS = ("quantize_weight", "colmax", "outlier_index", "row_quantize", "build_subB", "fwd_gemm",
            "gradout_prepass", "grad_bias_finalize", "bwd_gemm", "silu", "silu_backward", "widen_codes",
            "dequant_weight", "col_quantize", "wgrad_gemm", "unit_plan", "nf4_quantize", "nf4_dequantize",
-           "nf4_gemm_fwd", "nf4_gemm_bwd")
+           "nf4_gemm_fwd", "nf4_gemm_bwd", "absmax8", "layer_norm", "layer_norm_backward", "layer_norm_grad_sum",
+           "adapter_plan", "adapters", "adapters_grad", "adamw")
 
 
 # name -> (restype, argtypes); the same names and order as include/i8lt.h
@@ -109,6 +112,25 @@ SIGNATURES = {
     "i8lt_absmax8_quantize": (c_int, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                                       c_void_p]),
     "i8lt_absmax8_dequantize": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p]),
+    "i8lt_layer_norm_forward": (c_int, [c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p, c_int, c_float,
+                                        c_void_p, c_void_p, c_void_p, c_void_p]),
+    "i8lt_layer_norm_backward_workspace_size": (c_size_t, [c_int64, c_int64]),
+    "i8lt_layer_norm_backward": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
+                                         c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "i8lt_adapter_plan_bytes": (c_size_t, [c_int64, c_int64]),
+    "i8lt_adapter_plan": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_size_t, c_void_p]),
+    "i8lt_adapters_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int64, c_int64]),
+    "i8lt_adapters_forward": (c_int, [c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p, c_int64, c_int64,
+                                      c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                      c_void_p]),
+    "i8lt_adapters_backward": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p,
+                                       c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                       c_void_p, c_void_p, c_size_t, c_void_p]),
+    "i8lt_adamw_step": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_int64, c_void_p, c_void_p, c_int64,
+                                c_double, c_double, c_double, c_double, c_double, c_void_p, c_void_p, c_void_p]),
+    "i8lt_adamw_step_8bit": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_int64, c_void_p, c_void_p,
+                                     c_void_p, c_void_p, c_int64, c_double, c_double, c_double, c_double, c_double,
+                                     c_void_p, c_void_p, c_void_p]),
     "i8lt_silu_forward": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_void_p]),
     "i8lt_silu_backward": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_void_p, c_void_p]),
     "i8lt_profile_start": (c_int, [c_int]),
@@ -330,6 +352,57 @@ def i8lt_absmax8_quantize(absmax, count, q, absmax2, offset, ws, ws_bytes, strea
 
 def i8lt_absmax8_dequantize(q, absmax2, offset, count, out, stream=None) -> int:
     return load().i8lt_absmax8_dequantize(_p(q), _p(absmax2), _p(offset), int(count), _p(out), _p(stream))
+
+
+def i8lt_layer_norm_forward(x, xt, M, N, w, b, wt, eps, y, mean, rstd, stream=None) -> int:
+    return load().i8lt_layer_norm_forward(_p(x), xt, M, N, _p(w), _p(b), wt, eps, _p(y), _p(mean), _p(rstd),
+                                          _p(stream))
+
+
+def i8lt_layer_norm_backward_workspace_size(M, N) -> int:
+    return load().i8lt_layer_norm_backward_workspace_size(M, N)
+
+
+def i8lt_layer_norm_backward(g, x, xt, M, N, mean, rstd, w, wt, gx, gw, gb, ws, ws_bytes, stream=None) -> int:
+    return load().i8lt_layer_norm_backward(_p(g), _p(x), xt, M, N, _p(mean), _p(rstd), _p(w), wt, _p(gx), _p(gw),
+                                           _p(gb), _p(ws), ws_bytes, _p(stream))
+
+
+def i8lt_adapter_plan_bytes(M, E) -> int:
+    return load().i8lt_adapter_plan_bytes(M, E)
+
+
+def i8lt_adapter_plan(index, M, E, plan, plan_bytes, stream=None) -> int:
+    return load().i8lt_adapter_plan(_p(index), M, E, _p(plan), plan_bytes, _p(stream))
+
+
+def i8lt_adapters_workspace_size(M, K, N, E, r) -> int:
+    return load().i8lt_adapters_workspace_size(M, K, N, E, r)
+
+
+def i8lt_adapters_forward(x, dt, M, K, A, B, E, r, N, scale, plan, base, y, t, ws, ws_bytes, stream=None) -> int:
+    return load().i8lt_adapters_forward(_p(x), dt, M, K, _p(A), _p(B), E, r, N, _p(scale), _p(plan), _p(base), _p(y),
+                                        _p(t), _p(ws), ws_bytes, _p(stream))
+
+
+def i8lt_adapters_backward(g, x, t, dt, M, K, A, B, E, r, N, scale, plan, addend, gx, gA, gB, ws, ws_bytes,
+                           stream=None) -> int:
+    return load().i8lt_adapters_backward(_p(g), _p(x), _p(t), dt, M, K, _p(A), _p(B), E, r, N, _p(scale), _p(plan),
+                                         _p(addend), _p(gx), _p(gA), _p(gB), _p(ws), ws_bytes, _p(stream))
+
+
+def i8lt_adamw_step(params, pt, grads, gt, sizes, count, m, v, step, lr, beta1, beta2, eps, weight_decay,
+                    grad_scale=None, found_inf=None, stream=None) -> int:
+    """params, grads: ctypes arrays of device addresses; sizes: of int64."""
+    return load().i8lt_adamw_step(params, pt, grads, gt, sizes, count, _p(m), _p(v), step, lr, beta1, beta2, eps,
+                                  weight_decay, _p(grad_scale), _p(found_inf), _p(stream))
+
+
+def i8lt_adamw_step_8bit(params, pt, grads, gt, sizes, count, m, m_absmax, r, r_absmax, step, lr, beta1, beta2, eps,
+                         weight_decay, grad_scale=None, found_inf=None, stream=None) -> int:
+    return load().i8lt_adamw_step_8bit(params, pt, grads, gt, sizes, count, _p(m), _p(m_absmax), _p(r), _p(r_absmax),
+                                       step, lr, beta1, beta2, eps, weight_decay, _p(grad_scale), _p(found_inf),
+                                       _p(stream))
 
 
 def i8lt_silu_forward(h, dt, n, out, stream=None) -> int:

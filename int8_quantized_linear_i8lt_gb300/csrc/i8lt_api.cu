@@ -16,17 +16,23 @@ using namespace i8lt;
 
 namespace {
 
-constexpr int kAbiVersion = 4;
-constexpr size_t kAlign = 256;
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
 
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+}  // namespace
 
-bool valid_dt(int dt) { return dt == DT_F16 || dt == DT_BF16 || dt == DT_F32; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool threshold_enabled(float t) { return std::isfinite(t) && t > 0.0f; }
-
-int64_t cap_pad_of(int64_t cap) { return cap > 0 ? round_up(cap, 64) : 0; }
+namespace i8lt {
 
 // Device check: the kernels are built for sm_103a only.
 int check_device() {
@@ -46,20 +52,6 @@ int check_device() {
   return c == 1 ? I8LT_OK : I8LT_ERR_DEVICE;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
 // 2-D row-major tensor (inner x outer elements, row pitch in bytes) with a
 // box of box_inner x box_outer elements.
 bool make_tmap(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
@@ -75,7 +67,18 @@ bool make_tmap(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, uint64
   return r == CUDA_SUCCESS;
 }
 
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? I8LT_OK : I8LT_ERR_CUDA; }
+}  // namespace i8lt
+
+namespace {
+
+constexpr int kAbiVersion = 4;
+constexpr size_t kAlign = 256;
+
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+bool threshold_enabled(float t) { return std::isfinite(t) && t > 0.0f; }
+
+int64_t cap_pad_of(int64_t cap) { return cap > 0 ? round_up(cap, 64) : 0; }
 
 i8lt_fwd_layout fwd_layout(int64_t M, int64_t K, int64_t N, int64_t cap) {
   i8lt_fwd_layout L;
@@ -845,7 +848,8 @@ const char* i8lt_kernel_name(int k) {
                                 "bwd_gemm",        "silu",            "silu_backward",      "widen_codes",
                                 "dequant_weight",  "col_quantize",    "wgrad_gemm",         "unit_plan",
                                 "nf4_quantize",    "nf4_dequantize",  "nf4_gemm_fwd",       "nf4_gemm_bwd",
-                                "absmax8"};
+                                "absmax8",        "layer_norm",    "layer_norm_backward", "layer_norm_grad_sum",
+                                "adapter_plan",   "adapters",      "adapters_grad",      "adamw"};
   return (k >= 0 && k < K_COUNT) ? names[k] : "unknown";
 }
 

@@ -13,6 +13,17 @@ namespace i8lt {
 inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 inline int64_t ceil_div(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
+inline bool valid_dt(int dt) { return dt == DT_F16 || dt == DT_BF16 || dt == DT_F32; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? ST_OK : ST_CUDA; }
+
+// ST_OK when the current device is sm_103, the only target of the kernels.
+int check_device();
+// 2-D row-major tensor (inner x outer elements, row pitch in bytes) with a
+// box of box_inner x box_outer elements.
+bool make_tmap(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
+               uint64_t pitch, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);
+
 // ---- kernel timing (i8lt_api.cu): no-ops unless i8lt_profile_start ran ----
 void prof_begin(int kernel_id, cudaStream_t s);
 void prof_end(cudaStream_t s);
@@ -245,7 +256,8 @@ cudaError_t gemm_launch_shape(int kernel_id, int* ctas, int* threads, int* smem_
 enum KernelId {
   K_QUANTIZE_WEIGHT = 0, K_COLMAX, K_OUTLIER_INDEX, K_ROW_QUANTIZE, K_SUBB, K_FWD_GEMM, K_GRADOUT_PREPASS,
   K_GRAD_BIAS_FINALIZE, K_BWD_GEMM, K_SILU, K_SILU_BACKWARD, K_WIDEN_CODES, K_DEQUANT_WEIGHT, K_COL_QUANTIZE,
-  K_WGRAD_GEMM, K_UNIT_PLAN, K_NF4_QUANTIZE, K_NF4_DEQUANTIZE, K_NF4_GEMM_FWD, K_NF4_GEMM_BWD, K_ABSMAX8, K_COUNT
+  K_WGRAD_GEMM, K_UNIT_PLAN, K_NF4_QUANTIZE, K_NF4_DEQUANTIZE, K_NF4_GEMM_FWD, K_NF4_GEMM_BWD, K_ABSMAX8, K_LAYER_NORM,
+  K_LAYER_NORM_BWD, K_LAYER_NORM_GRAD_SUM, K_ADAPTER_PLAN, K_ADAPTERS, K_ADAPTERS_GRAD, K_ADAMW, K_COUNT
 };
 
 // Box sizes of the tensor maps (each CTA of a pair stages 128 rows of each

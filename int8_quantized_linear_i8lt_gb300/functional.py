@@ -609,3 +609,344 @@ class Linear4bitFunction(torch.autograd.Function):
 
 # the NF4 layer's function under its own name
 NF4LinearFunction = Linear4bitFunction
+
+
+# ---------------------------------------------------------------------------
+# fine-tuning on top of the frozen layers: layer norm, low-rank adapters, AdamW
+# ---------------------------------------------------------------------------
+
+def _same_device(what: str, first: torch.Tensor, *ts):
+    """All given tensors on one CUDA device."""
+    for t in ts:
+        if t is not None and t.device != first.device:
+            raise I8LTError(f"{what}: tensors on {first.device} and {t.device}")
+
+
+def _expect(what: str, t, shape, dtype):
+    """Shape and dtype of an optional argument."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise I8LTError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise I8LTError(f"{what}: dtype {t.dtype}, expected {dtype}")
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+               eps: float = 1e-5, out: torch.Tensor | None = None):
+    """(y, mean, rstd) of the layer norm over the last dimension of x [..., N]
+    (f16 / bf16 / f32); weight and bias [N] of one dtype (any of the three).
+    mean and rstd are fp32 with x's leading shape, for the backward."""
+    _require_cuda(x, weight, bias, out)
+    if x.dim() == 0:
+        raise I8LTError("layer_norm: x has no dimension to normalise")
+    N = x.shape[-1]
+    par = weight if weight is not None else bias
+    _same_device("layer_norm", x, weight, bias, out)
+    _expect("layer_norm weight", weight, (N,), None)
+    _expect("layer_norm bias", bias, (N,), None if par is None else par.dtype)
+    _expect("layer_norm out", out, x.shape, x.dtype)
+    if out is not None and not out.is_contiguous():
+        raise I8LTError("layer_norm: out is not contiguous")
+    x = x.contiguous()
+    weight = None if weight is None else weight.contiguous()
+    bias = None if bias is None else bias.contiguous()
+    M = x.numel() // N if N else 0
+    y = torch.empty_like(x) if out is None else out
+    stats = torch.empty(2, *x.shape[:-1], dtype=torch.float32, device=x.device)
+    mean, rstd = stats[0], stats[1]
+    _check(_lib.i8lt_layer_norm_forward(x.data_ptr(), _code(x.dtype), M, N, _ptr(weight), _ptr(bias),
+                                        _code(par.dtype) if par is not None else 0, eps, y.data_ptr(),
+                                        mean.data_ptr(), rstd.data_ptr(), _stream(x)), "i8lt_layer_norm_forward")
+    return y, mean, rstd
+
+
+def layer_norm_backward(g: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight: torch.Tensor | None = None, need_x: bool = True, need_weight: bool = True,
+                        need_bias: bool = True, param_dtype: torch.dtype | None = None):
+    """(gx, gw, gb) of ``layer_norm`` (None where not needed).  gw and gb have
+    ``param_dtype`` (default: weight's, else x's)."""
+    _require_cuda(g, x, mean, rstd, weight)
+    _same_device("layer_norm_backward", x, g, mean, rstd, weight)
+    N = x.shape[-1]
+    _expect("layer_norm_backward g", g, x.shape, x.dtype)
+    _expect("layer_norm_backward mean", mean, x.shape[:-1], torch.float32)
+    _expect("layer_norm_backward rstd", rstd, x.shape[:-1], torch.float32)
+    _expect("layer_norm_backward weight", weight, (N,), None)
+    if weight is not None and param_dtype not in (None, weight.dtype):
+        raise I8LTError(f"layer_norm_backward: param_dtype {param_dtype} with a weight of {weight.dtype}")
+    dtype = weight.dtype if weight is not None else (param_dtype or x.dtype)
+    if not (need_x or need_weight or need_bias):
+        return None, None, None
+    g, x, mean, rstd = g.contiguous(), x.contiguous(), mean.contiguous(), rstd.contiguous()
+    weight = None if weight is None else weight.contiguous()
+    M = x.numel() // N if N else 0
+    gx = torch.empty_like(x) if need_x else None
+    gw = torch.empty(N, dtype=dtype, device=x.device) if need_weight else None
+    gb = torch.empty(N, dtype=dtype, device=x.device) if need_bias else None
+    ws = None
+    if need_weight or need_bias:
+        ws = torch.empty(max(_lib.i8lt_layer_norm_backward_workspace_size(M, N), 256), dtype=torch.uint8,
+                         device=x.device)
+    _check(_lib.i8lt_layer_norm_backward(g.data_ptr(), x.data_ptr(), _code(x.dtype), M, N, mean.data_ptr(),
+                                         rstd.data_ptr(), _ptr(weight), _code(dtype), _ptr(gx), _ptr(gw), _ptr(gb),
+                                         _ptr(ws), 0 if ws is None else ws.numel(), _stream(x)),
+           "i8lt_layer_norm_backward")
+    return gx, gw, gb
+
+
+class LayerNormFunction(torch.autograd.Function):
+    """y = layer norm of x over its last dimension."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        y, mean, rstd = layer_norm(x, weight, bias, eps)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.param_dtype = None if bias is None or weight is not None else bias.dtype
+        ctx.has_bias = bias is not None
+        return y
+
+    @staticmethod
+    def backward(ctx, g):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        gx, gw, gb = layer_norm_backward(g, x, mean, rstd, weight, need_x=need[0],
+                                         need_weight=need[1] and weight is not None,
+                                         need_bias=need[2] and ctx.has_bias, param_dtype=ctx.param_dtype)
+        return gx, gw, gb, None
+
+
+class AdapterPlan:
+    """The tokens of a batch sorted by adapter (``adapter_plan``): made once
+    per batch, used by every layer and both directions."""
+
+    def __init__(self, data: torch.Tensor, tokens: int, adapters: int):
+        self.data, self.tokens, self.adapters = data, tokens, adapters
+
+
+def adapter_plan(index: torch.Tensor | None, adapters: int, tokens: int | None = None,
+                 device=None) -> AdapterPlan:
+    """The plan of a batch whose token m uses adapter index[m] (int32; a value
+    outside [0, adapters) uses none).  index None: ``tokens`` tokens on
+    ``device`` that all use adapter 0."""
+    if index is None:
+        if tokens is None or device is None:
+            raise I8LTError("adapter_plan: without an index it needs tokens and device")
+        device = torch.device(device)
+        if device.type != "cuda":
+            raise I8LTError("libi8lt runs on CUDA tensors only (no CPU path)")
+        M = int(tokens)
+    else:
+        _require_cuda(index)
+        if index.dtype != torch.int32:
+            raise I8LTError(f"adapter_plan: index has dtype {index.dtype}, expected torch.int32")
+        index = index.reshape(-1).contiguous()
+        M, device = index.numel(), index.device
+        if tokens is not None and tokens != M:
+            raise I8LTError(f"adapter_plan: {M} indices for {tokens} tokens")
+    n = _lib.i8lt_adapter_plan_bytes(M, adapters)
+    data = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    _check(_lib.i8lt_adapter_plan(_ptr(index), M, adapters, data.data_ptr(), data.numel(), _stream(data)),
+           "i8lt_adapter_plan")
+    return AdapterPlan(data, M, adapters)
+
+
+def _adapter_args(what, x, A, B, scale, plan):
+    """Checked sizes (M, K, E, r, N) of an adapter call on x [M, K or N]."""
+    if A.dim() != 3 or B.dim() != 3:
+        raise I8LTError(f"{what}: A and B are [adapters, rank, in] and [adapters, out, rank]")
+    E, r, K = A.shape
+    N = B.shape[1]
+    _expect(f"{what} B", B, (E, N, r), A.dtype)
+    _expect(f"{what} scale", scale, (E,), torch.float32)
+    if x.dtype != A.dtype:
+        raise I8LTError(f"{what}: tokens of dtype {x.dtype}, adapters of {A.dtype}")
+    if plan.adapters != E or plan.tokens != x.shape[0]:
+        raise I8LTError(f"{what}: a plan of {plan.tokens} tokens and {plan.adapters} adapters for {x.shape[0]} tokens "
+                        f"and {E} adapters")
+    return x.shape[0], K, E, r, N
+
+
+def _adapter_workspace(M, K, N, E, r, device):
+    return torch.empty(max(_lib.i8lt_adapters_workspace_size(M, K, N, E, r), 256), dtype=torch.uint8, device=device)
+
+
+def adapters_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor | None,
+                     plan: AdapterPlan, base: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """(y, t) with t = x A[e]^T and y = base + scale[e] t B[e]^T for each
+    token's adapter e (i8lt_adapters_forward): x [M, K] (f16 / bf16),
+    A [E, r, K], B [E, N, r], scale fp32 [E] or None, base [M, N] or None.
+    ``out`` may be base itself.  t [M, r] is what the backward needs."""
+    _require_cuda(x, A, B, scale, plan.data, base, out)
+    _same_device("adapters_forward", x, A, B, scale, plan.data, base, out)
+    if x.dim() != 2:
+        raise I8LTError("adapters_forward: x is [tokens, features]")
+    M, K, E, r, N = _adapter_args("adapters_forward", x, A, B, scale, plan)
+    _expect("adapters_forward x", x, (M, K), None)
+    _expect("adapters_forward base", base, (M, N), x.dtype)
+    _expect("adapters_forward out", out, (M, N), x.dtype)
+    if out is not None and not out.is_contiguous():
+        raise I8LTError("adapters_forward: out is not contiguous")
+    x, A, B = x.contiguous(), A.contiguous(), B.contiguous()
+    scale = None if scale is None else scale.contiguous()
+    base = None if base is None else base.contiguous()
+    y = torch.empty(M, N, dtype=x.dtype, device=x.device) if out is None else out
+    t = torch.empty(M, r, dtype=x.dtype, device=x.device)
+    ws = _adapter_workspace(M, K, N, E, r, x.device)
+    _check(_lib.i8lt_adapters_forward(x.data_ptr(), _code(x.dtype), M, K, A.data_ptr(), B.data_ptr(), E, r, N,
+                                      _ptr(scale), plan.data.data_ptr(), _ptr(base), y.data_ptr(), t.data_ptr(),
+                                      ws.data_ptr(), ws.numel(), _stream(x)), "i8lt_adapters_forward")
+    return y, t
+
+
+def adapters_backward(g: torch.Tensor, x: torch.Tensor | None, t: torch.Tensor | None, A: torch.Tensor,
+                      B: torch.Tensor, scale: torch.Tensor | None, plan: AdapterPlan,
+                      addend: torch.Tensor | None = None, need_x: bool = True, need_A: bool = True,
+                      need_B: bool = True):
+    """(gx, gA, gB) of ``adapters_forward`` (None where not needed), gx with
+    ``addend`` (the shared projection's input gradient) added.  x is used for
+    gA only, t for gB only."""
+    _require_cuda(g, x, t, A, B, scale, plan.data, addend)
+    _same_device("adapters_backward", g, x, t, A, B, scale, plan.data, addend)
+    if g.dim() != 2:
+        raise I8LTError("adapters_backward: g is [tokens, features]")
+    M, K, E, r, N = _adapter_args("adapters_backward", g, A, B, scale, plan)
+    _expect("adapters_backward g", g, (M, N), None)
+    if need_A and x is None or need_B and t is None:
+        raise I8LTError("adapters_backward: gA needs x and gB needs t")
+    _expect("adapters_backward x", x, (M, K), g.dtype)
+    _expect("adapters_backward t", t, (M, r), g.dtype)
+    _expect("adapters_backward addend", addend, (M, K), g.dtype)
+    if not (need_x or need_A or need_B):
+        return None, None, None
+    g, A, B = g.contiguous(), A.contiguous(), B.contiguous()
+    x = None if x is None else x.contiguous()
+    t = None if t is None else t.contiguous()
+    scale = None if scale is None else scale.contiguous()
+    addend = None if addend is None else addend.contiguous()
+    gx = torch.empty(M, K, dtype=g.dtype, device=g.device) if need_x else None
+    gA = torch.empty_like(A) if need_A else None
+    gB = torch.empty_like(B) if need_B else None
+    ws = _adapter_workspace(M, K, N, E, r, g.device)
+    _check(_lib.i8lt_adapters_backward(g.data_ptr(), _ptr(x), _ptr(t), _code(g.dtype), M, K, A.data_ptr(),
+                                       B.data_ptr(), E, r, N, _ptr(scale), plan.data.data_ptr(), _ptr(addend),
+                                       _ptr(gx), _ptr(gA), _ptr(gB), ws.data_ptr(), ws.numel(), _stream(g)),
+           "i8lt_adapters_backward")
+    return gx, gA, gB
+
+
+class AdaptersFunction(torch.autograd.Function):
+    """y = base + the low-rank adapters' product of x (the gradient passes to
+    base unchanged)."""
+
+    @staticmethod
+    def forward(ctx, x, base, A, B, scale, plan):
+        x2 = x.reshape(-1, x.shape[-1])
+        b2 = None if base is None else base.reshape(x2.shape[0], -1)
+        y, t = adapters_forward(x2, A, B, scale, plan, base=b2)
+        ctx.save_for_backward(x2, t, A, B, scale)
+        ctx.plan, ctx.x_shape = plan, x.shape
+        return y.reshape(*x.shape[:-1], B.shape[1])
+
+    @staticmethod
+    def backward(ctx, gy):
+        x2, t, A, B, scale = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        gx = gA = gB = None
+        if need[0] or need[2] or need[3]:
+            gx, gA, gB = adapters_backward(gy.reshape(x2.shape[0], -1), x2, t, A, B, scale, ctx.plan, need_x=need[0],
+                                           need_A=need[2], need_B=need[3])
+        if gx is not None:
+            gx = gx.reshape(ctx.x_shape)
+        return gx, (gy if need[1] else None), gA, gB, None, None
+
+
+def adamw_state_size(params) -> int:
+    """Elements of the flat AdamW states of ``params``: each tensor's start is
+    a multiple of 256."""
+    blk = _lib.I8LT_ADAMW_BLOCK
+    return sum(-(-p.numel() // blk) * blk for p in params)
+
+
+def _adamw_lists(what, params, grads):
+    """ctypes arrays of the device addresses and sizes, and the dtypes."""
+    if len(params) != len(grads):
+        raise I8LTError(f"{what}: {len(params)} parameters, {len(grads)} gradients")
+    if not params:
+        return None
+    p0 = params[0]
+    pt, gt, dev = p0.dtype, None, p0.device
+    held = []
+    for p, g in zip(params, grads):
+        if p.dtype != pt or p.device != dev:
+            raise I8LTError(f"{what}: parameters of one dtype on one device are expected")
+        if not p.is_contiguous():
+            raise I8LTError(f"{what}: a parameter is not contiguous")
+        if g is not None:
+            gt = gt or g.dtype
+            if g.dtype != gt or g.device != dev:
+                raise I8LTError(f"{what}: gradients of one dtype on the parameters' device are expected")
+            if p.shape != g.shape:
+                raise I8LTError(f"{what}: a parameter of shape {tuple(p.shape)} with a gradient of {tuple(g.shape)}")
+            g = g if g.is_contiguous() else g.contiguous()
+        held.append(g)
+    _require_cuda(p0)
+    if gt is None:
+        return None
+    n = len(params)
+    return (p0, held, n, (_lib.c_void_p * n)(*[p.data_ptr() for p in params]),
+            (_lib.c_void_p * n)(*[_ptr(g) for g in held]),
+            (_lib.c_int64 * n)(*[p.numel() for p in params]), _code(pt), _code(gt))
+
+
+def _adamw_state(what, size, dtype, device, *ts):
+    for t in ts:
+        if t.dtype != dtype or t.numel() != size or not t.is_contiguous() or t.device != device:
+            raise I8LTError(f"{what}: a state of {t.numel()} {t.dtype} on {t.device}, expected {size} contiguous "
+                            f"{dtype} on {device}")
+
+
+def _adamw_scalar(what, t, device):
+    if t is not None and (t.dtype != torch.float32 or t.numel() != 1 or t.device != device):
+        raise I8LTError(f"{what}: grad_scale and found_inf are fp32 tensors of one element on {device}")
+
+
+def adamw_step(params, grads, m: torch.Tensor, v: torch.Tensor, step: int, lr: float, beta1: float = 0.9,
+               beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01,
+               grad_scale: torch.Tensor | None = None, found_inf: torch.Tensor | None = None) -> None:
+    """One AdamW step, in place, over all ``params`` at once (i8lt_adamw_step).
+    m and v: flat fp32 states of ``adamw_state_size(params)`` elements.
+    A parameter whose gradient is None stays as it is.  grad_scale multiplies
+    every gradient; a found_inf other than 0 makes the step change nothing
+    (both fp32 CUDA tensors of one element)."""
+    size = adamw_state_size(params)
+    lists = _adamw_lists("adamw_step", params, grads)
+    if lists is None:
+        return
+    p0, held, n, pp, gp, sizes, pt, gt = lists
+    _adamw_state("adamw_step", size, torch.float32, p0.device, m, v)
+    _adamw_scalar("adamw_step", grad_scale, p0.device)
+    _adamw_scalar("adamw_step", found_inf, p0.device)
+    _check(_lib.i8lt_adamw_step(pp, pt, gp, gt, sizes, n, m.data_ptr(), v.data_ptr(), step, lr, beta1, beta2, eps,
+                                weight_decay, _ptr(grad_scale), _ptr(found_inf), _stream(p0)), "i8lt_adamw_step")
+
+
+def adamw_step_8bit(params, grads, m: torch.Tensor, m_absmax: torch.Tensor, r: torch.Tensor, r_absmax: torch.Tensor,
+                    step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                    weight_decay: float = 0.01, grad_scale: torch.Tensor | None = None,
+                    found_inf: torch.Tensor | None = None) -> None:
+    """``adamw_step`` with 8-bit states (i8lt_adamw_step_8bit): m and
+    r = sqrt(v) as flat float8_e4m3fn tensors of ``adamw_state_size(params)``
+    elements, m_absmax and r_absmax fp32, one per 256 elements."""
+    size = adamw_state_size(params)
+    lists = _adamw_lists("adamw_step_8bit", params, grads)
+    if lists is None:
+        return
+    p0, held, n, pp, gp, sizes, pt, gt = lists
+    _adamw_state("adamw_step_8bit", size, torch.float8_e4m3fn, p0.device, m, r)
+    _adamw_state("adamw_step_8bit", size // _lib.I8LT_ADAMW_BLOCK, torch.float32, p0.device, m_absmax, r_absmax)
+    _adamw_scalar("adamw_step_8bit", grad_scale, p0.device)
+    _adamw_scalar("adamw_step_8bit", found_inf, p0.device)
+    _check(_lib.i8lt_adamw_step_8bit(pp, pt, gp, gt, sizes, n, m.data_ptr(), m_absmax.data_ptr(), r.data_ptr(),
+                                     r_absmax.data_ptr(), step, lr, beta1, beta2, eps, weight_decay, _ptr(grad_scale),
+                                     _ptr(found_inf), _stream(p0)), "i8lt_adamw_step_8bit")

@@ -182,3 +182,107 @@ class LinearNF4(Linear4bit):
 class LinearFP4(Linear4bit):
     """The 4-bit floating-point (E2M1) layer (bnb.fp4)."""
     fmt = "fp4"
+
+
+class LayerNorm(torch.nn.Module):
+    """Layer norm over the last dimension with trainable weight and bias."""
+
+    def __init__(self, features: int, eps: float = 1e-5, bias: bool = True, device=None,
+                 dtype: torch.dtype = torch.float32):
+        super().__init__()
+        self.features = features
+        self.eps = float(eps)
+        self.weight = torch.nn.Parameter(torch.ones(features, dtype=dtype, device=device))
+        if bias:
+            self.bias = torch.nn.Parameter(torch.zeros(features, dtype=dtype, device=device))
+        else:
+            self.register_parameter("bias", None)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        return F.LayerNormFunction.apply(x, self.weight, self.bias, self.eps)
+
+    def extra_repr(self) -> str:
+        return f"{self.features}, eps={self.eps}, bias={self.bias is not None}"
+
+
+class LowRankAdapters(torch.nn.Module):
+    """``adapters`` low-rank adapters beside a shared, frozen layer ``base``
+    (Linear8bitLt, LinearNF4, ...): y = base(x) + scale[e] (x A[e]^T) B[e]^T
+    for each token's adapter e.  A starts as N(0, 1 / in_features), B as
+    zeros; ``dtype`` (f16 or bf16) is the compute type of the tokens.
+    ``forward`` takes the batch's ``plan`` (``adapter_plan(index, adapters)``,
+    shared by the layers of a model); without one all tokens use adapter 0."""
+
+    def __init__(self, base: torch.nn.Module, rank: int, adapters: int = 1, scale: float = 1.0, device=None,
+                 dtype: torch.dtype = torch.bfloat16):
+        super().__init__()
+        self.base = base
+        self.rank, self.adapters = rank, adapters
+        K, N = base.in_features, base.out_features
+        self.A = torch.nn.Parameter((torch.randn(adapters, rank, K, device=device) * K ** -0.5).to(dtype))
+        self.B = torch.nn.Parameter(torch.zeros(adapters, N, rank, dtype=dtype, device=device))
+        self.register_buffer("scale", torch.full((adapters,), float(scale), dtype=torch.float32, device=device))
+
+    def forward(self, x: torch.Tensor, plan: F.AdapterPlan | None = None) -> torch.Tensor:
+        if plan is None:
+            plan = F.adapter_plan(None, self.adapters, x.numel() // x.shape[-1], x.device)
+        return F.AdaptersFunction.apply(x, self.base(x), self.A, self.B, self.scale, plan)
+
+    def extra_repr(self) -> str:
+        return f"rank={self.rank}, adapters={self.adapters}"
+
+
+class AdamW:
+    """AdamW over all its parameters in one launch per dtype, with the states
+    in 32 bits or (``bits=8``) as FP8 E4M3 with one fp32 absmax per 256
+    elements.  A parameter without a gradient is left as it is.  step() takes
+    the optional device scalars of a loss scaler or a gradient clip:
+    ``grad_scale`` multiplies every gradient, a ``found_inf`` other than 0
+    makes the step change nothing (the step still counts)."""
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+                 bits: int = 32):
+        if bits not in (8, 32):
+            raise F.I8LTError(f"AdamW: states in 8 or 32 bits, not {bits}")
+        self.lr, self.betas, self.eps, self.weight_decay, self.bits = lr, betas, eps, weight_decay, bits
+        self.steps = 0
+        lists: dict = {}
+        for p in params:
+            lists.setdefault((p.dtype, p.device), []).append(p)
+        self.params = list(lists.values())
+        self.states = []
+        for ps in self.params:
+            n, dev = F.adamw_state_size(ps), ps[0].device
+            if bits == 8:
+                # codes are set as bytes: 0 is E4M3's zero
+                q = [torch.zeros(n, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2)]
+                top = [torch.zeros(n // 256, dtype=torch.float32, device=dev) for _ in range(2)]
+                self.states.append((q[0], top[0], q[1], top[1]))
+            else:
+                self.states.append(tuple(torch.zeros(n, dtype=torch.float32, device=dev) for _ in range(2)))
+
+    @torch.no_grad()
+    def step(self, grad_scale: torch.Tensor | None = None, found_inf: torch.Tensor | None = None) -> None:
+        self.steps += 1
+        call = F.adamw_step_8bit if self.bits == 8 else F.adamw_step
+        for ps, st in zip(self.params, self.states):
+            call(ps, [p.grad for p in ps], *st, step=self.steps, lr=self.lr, beta1=self.betas[0],
+                 beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay, grad_scale=grad_scale,
+                 found_inf=found_inf)
+
+    def zero_grad(self) -> None:
+        for ps in self.params:
+            for p in ps:
+                p.grad = None
+
+    def state_dict(self) -> dict:
+        return {"steps": self.steps, "bits": self.bits, "states": [tuple(t.clone() for t in st) for st in self.states]}
+
+    def load_state_dict(self, d: dict) -> None:
+        if d["bits"] != self.bits or [[t.shape for t in st] for st in d["states"]] != \
+                [[t.shape for t in st] for st in self.states]:
+            raise F.I8LTError("AdamW: the state was saved for other parameters")
+        self.steps = d["steps"]
+        for st, src in zip(self.states, d["states"]):
+            for t, v in zip(st, src):
+                t.copy_(v)
