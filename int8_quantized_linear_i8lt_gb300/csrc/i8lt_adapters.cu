@@ -87,132 +87,689 @@ __global__ void __launch_bounds__(kThreads) adapter_plan_kernel(const int32_t* i
   }
 }
 
-// out[m, j] = (scaled ? scale[e] : 1) * sum_c X[m, c] W(e, j, c) for the
-// tokens of one tile slot; W(e, j, c) at e R C + (w_rank_major ? j C + c :
-// c R + j).  One warp per (token, j) in turn.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) shrink_kernel(const T* X, int64_t C, const T* W, int R, bool w_rank_major,
-                                                          int E, const float* scale, const Tile* tiles,
-                                                          const int* perm, T* out) {
-  const Tile t = tiles[blockIdx.x];
-  const int lane = threadIdx.x & 31;
-  for (int i = threadIdx.x >> 5; i < t.count * R; i += kThreads / 32) {
-    const int64_t m = perm[t.start + i / R];
-    const int j = i % R;
-    float s = 0.f;
-    if (t.group < E) {
-      const T* w = W + static_cast<int64_t>(t.group) * R * C + (w_rank_major ? j * C : j);
-      const int64_t step = w_rank_major ? 1 : R;
-      for (int64_t c = lane; c < C; c += 32) s += to_float(X[m * C + c]) * to_float(w[c * step]);
+// ---- shared pieces of the three products ----------------------------------
+//
+// All three run on the tensor cores (tcgen05, 128-row tiles, fp32 accumulators
+// in TMEM) on operands staged in shared memory with 16-byte (narrower for
+// rows that are not 16-byte aligned) asynchronous copies, which gather the
+// tokens of a tile wherever they lie and fill what is past an edge with
+// zeros.  Matrices of a width C have rows of C 16-bit elements; an operand
+// tile is rows of 64 elements (128 bytes) in the 128-byte swizzle, either
+// with the reduction along the row ("K-major") or across the rows
+// ("MN-major").
+
+constexpr int kRowBytes = 128;
+
+__device__ __forceinline__ float to_f32(uint16_t v, bool bf16) {
+  return bf16 ? __uint_as_float(static_cast<uint32_t>(v) << 16) : __half2float(__ushort_as_half(v));
+}
+__device__ __forceinline__ uint16_t to_16(float v, bool bf16) {
+  return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool take) {
+  const int n = take ? kBytes : 0;
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// Copies 8 elements to the 16 bytes at `dst`, of which the first `valid`
+// exist (the others are zeros; valid <= 0: none, `row` is then not read).
+// `width`: the bytes that every row start and row length is a multiple of.
+__device__ __forceinline__ void load_chunk(uint32_t dst, const uint16_t* row, int64_t at, int64_t valid, int width) {
+  const uint16_t* src = row + (valid > 0 ? at : 0);
+  if (width == 16) {
+    cp_async<16>(dst, src, valid > 0);
+  } else if (width == 8) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (scale != nullptr) s *= scale[t.group];
+    for (int i = 0; i < 2; ++i) cp_async<8>(dst + 8 * i, valid > 4 * i ? src + 4 * i : src, valid > 4 * i);
+  } else if (width == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cp_async<4>(dst + 4 * i, valid > 2 * i ? src + 2 * i : src, valid > 2 * i);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = valid > 2 * i ? src[2 * i] : 0, hi = valid > 2 * i + 1 ? src[2 * i + 1] : 0;
+      w[i] = lo | (hi << 16);
     }
-    if (lane == 0) out[m * R + j] = from_float<T>(s);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
   }
 }
 
-// out[m, c] = addend[m, c] + (scaled ? scale[e] : 1) * sum_j X[m, j] W(e, j, c).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) expand_kernel(const T* X, int R, const T* W, int64_t C, bool w_rank_major,
-                                                          int E, const float* scale, const Tile* tiles,
-                                                          const int* perm, const T* addend, T* out) {
-  const Tile t = tiles[blockIdx.x];
-  const int64_t c = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x;
-  if (c >= C) return;
-  for (int i = 0; i < t.count; ++i) {
-    const int64_t m = perm[t.start + i];
-    float s = 0.f;
-    if (t.group < E) {
-      const T* w = W + static_cast<int64_t>(t.group) * R * C + (w_rank_major ? c : c * R);
-      const int64_t step = w_rank_major ? C : 1;
-      for (int j = 0; j < R; ++j) s += to_float(X[m * R + j]) * to_float(w[j * step]);
-      if (scale != nullptr) s *= scale[t.group];
-    }
-    if (addend != nullptr) s += to_float(addend[m * C + c]);
-    out[m * C + c] = from_float<T>(s);
-  }
+// Byte offset of 16-byte chunk `c` (0-7) of row `i` in a swizzled tile.
+__device__ __forceinline__ uint32_t swizzled(int i, int c) {
+  return static_cast<uint32_t>(i * kRowBytes + ((c ^ (i & 7)) << 4));
 }
 
-// grad(e, j, c) = (scaled ? scale[e] : 1) * sum over the tokens of group e of
-// P[m, j] X[m, c], stored as W above.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) grad_kernel(const T* P, int R, const T* X, int64_t C, bool w_rank_major,
-                                                        const float* scale, const int* offset, const int* perm,
-                                                        T* grad) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (c >= C) return;
-  const int j = blockIdx.y;
-  const int64_t e = blockIdx.z;
+__device__ __forceinline__ uint32_t align1024(uint32_t a) { return (a + 1023u) & ~1023u; }
+
+__device__ __forceinline__ uint32_t instruction(int n, bool a_mn, bool b_mn, bool bf16) {
+  return make_idesc_f16(128, n, a_mn, b_mn) | (bf16 ? (1u << 7) | (1u << 10) : 0u);
+}
+// K-major: 8-row atoms 1024 bytes apart, 32 bytes along the row per MMA.
+__device__ __forceinline__ uint64_t desc_k(uint32_t a, int k) { return make_sdesc(a + 32 * k, 16, 1024, kSwizzle128B); }
+// MN-major: blocks of 64 MN elements `block` bytes apart, 8-row atoms of the
+// reduction 1024 bytes apart, 16 rows per MMA.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t a, int k, uint32_t block) {
+  return make_sdesc(a + 2048 * k, block, 1024, kSwizzle128B);
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t map_cluster(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+
+// Barriers, the abort flag of the bounded waits and the TMEM address.
+constexpr int kMaxStages = 4;
+struct Sync {
+  uint64_t done[kMaxStages];
+  uint32_t tmem;
+  int abort;
+};
+__device__ __forceinline__ void sync_setup(Sync& y, uint32_t columns) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMaxStages; ++i) mbar_init(&y.done[i], 1);
+    y.abort = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 32) {
+    tmem_alloc(&y.tmem, columns);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+}
+__device__ __forceinline__ void sync_end(const Sync& y, uint32_t columns) {
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x < 32) tmem_dealloc(y.tmem, columns);
+}
+
+__host__ __device__ constexpr int rank16(int r) { return (r + 15) & ~15; }
+__host__ __device__ constexpr uint32_t tmem_columns(int r16) { return r16 <= 32 ? 32u : r16 <= 64 ? 64u : 128u; }
+// Row pitch (floats) of the accumulator copy that the CTAs of a cluster add
+// up: 16-byte accesses of 8 rows hit 8 different bank groups.
+__host__ __device__ constexpr int red_pitch(int r16) { return r16 + 4; }
+
+// The CTA's accumulator (128 rows x r16) into shared memory.
+__device__ __forceinline__ void spill(uint32_t tmem, int r16, float* red) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = (warp & 3) * 32 + lane;
+  for (int c = (warp >> 2) * 16; c < r16; c += 32) {
+    uint32_t v[16];
+    tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c, v);
+    float4* p = reinterpret_cast<float4*>(red + row * red_pitch(r16) + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                         __uint_as_float(v[4 * i + 3]));
+  }
+}
+// The sum over the cluster of one element of it, in the order of the ranks.
+__device__ __forceinline__ float cluster_sum(uint32_t red, int at, int ranks) {
   float s = 0.f;
-  for (int i = offset[e]; i < offset[e + 1]; ++i) {
-    const int64_t m = perm[i];
-    s += to_float(P[m * R + j]) * to_float(X[m * C + c]);
-  }
-  if (scale != nullptr) s *= scale[e];
-  grad[e * R * C + (w_rank_major ? j * C + c : c * R + j)] = from_float<T>(s);
+  for (int q = 0; q < ranks; ++q) s += ld_cluster(map_cluster(red + 4u * at, q));
+  return s;
 }
+
+// ---- mid = X W^T (t and u) -------------------------------------------------
+
+struct ShrinkArgs {
+  const uint16_t* X;      // [M, C]
+  const uint16_t* W;      // per group [R, C] (K-major) or [C, R] (MN-major)
+  uint16_t* mid;          // [M, R]
+  const float* scale;     // applied when not NULL
+  const Tile* tiles;
+  const int* perm;
+  DevStatus* st;
+  int64_t C;
+  int R, E, cw, rw;       // cw, rw: copy widths of rows of C and of R elements
+  int ranks;              // CTAs per cluster
+  bool bf16;
+};
+
+__host__ __device__ constexpr int shrink_stage_bytes(int r16, bool mn) {
+  return 128 * kRowBytes + (mn ? (r16 > 64 ? 2 : 1) * 64 * kRowBytes : r16 * kRowBytes);
+}
+
+// One cluster per tile of 128 tokens; its CTAs split the reduction, each
+// accumulating in TMEM, and add up in the order of their ranks.  Bound by
+// reading X once.
+template <bool kMN, int kStages>
+__global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const ShrinkArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Sync y;
+  const int ranks = a.ranks, rank = blockIdx.x % ranks;
+  const Tile t = a.tiles[blockIdx.x / ranks];
+  if (t.count == 0) return;
+  const int tid = threadIdx.x, R = a.R, r16 = rank16(R);
+  if (t.group >= a.E) {
+    if (rank == 0)
+      for (int i = tid; i < t.count * R; i += kThreads)
+        a.mid[static_cast<int64_t>(a.perm[t.start + i / R]) * R + i % R] = 0;
+    return;
+  }
+  const uint32_t base = align1024(smem_u32(smem_raw));
+  const int stage_bytes = shrink_stage_bytes(r16, kMN);
+  const int nb = static_cast<int>((a.C + 63) / 64);
+  const int b0 = static_cast<int>(static_cast<int64_t>(nb) * rank / ranks);
+  const int n = static_cast<int>(static_cast<int64_t>(nb) * (rank + 1) / ranks) - b0;
+  const int64_t C = a.C;
+  const uint16_t* W = a.W + static_cast<int64_t>(t.group) * R * C;
+  // this thread's rows of X: 8 threads a row
+  const uint16_t* xrow[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = (tid >> 3) + 32 * i;
+    xrow[i] = row < t.count ? a.X + static_cast<int64_t>(a.perm[t.start + row]) * C : nullptr;
+  }
+  sync_setup(y, tmem_columns(r16));
+
+  auto load = [&](int b, int s) {
+    const int64_t c0 = static_cast<int64_t>(b0 + b) * 64;
+    const uint32_t xs = base + s * stage_bytes, ws = xs + 128 * kRowBytes;
+    const int64_t at = c0 + (tid & 7) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)   // rows past the tile's tokens are not read: their products go nowhere
+      if (xrow[i] != nullptr) load_chunk(xs + swizzled((tid >> 3) + 32 * i, tid & 7), xrow[i], at, C - at, a.cw);
+    if constexpr (kMN) {
+      const int chunks = r16 / 8;
+      for (int i = tid; i < 64 * chunks; i += kThreads) {
+        const int k = i / chunks, c = i % chunks;
+        load_chunk(ws + (c >> 3) * 64 * kRowBytes + swizzled(k, c & 7), W + min(c0 + k, C - 1) * R, c * 8,
+                   c0 + k < C ? R - c * 8 : 0, a.rw);
+      }
+    } else {
+      for (int j = tid >> 3; j < r16; j += kThreads / 8)
+        load_chunk(ws + swizzled(j, tid & 7), W + min(j, R - 1) * C, at, j < R ? C - at : 0, a.cw);
+    }
+  };
+
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (i < n) load(i, i);
+    cp_async_commit();
+  }
+  const uint32_t idesc = instruction(r16, false, kMN, a.bf16);
+  for (int it = 0; it < n; ++it) {
+    const int s = it % kStages;
+    cp_async_wait<kStages - 2>();
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      const uint32_t xs = base + s * stage_bytes, ws = xs + 128 * kRowBytes;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        umma_f16(y.tmem, desc_k(xs, k), kMN ? desc_mn(ws, k, 64 * kRowBytes) : desc_k(ws, k), idesc,
+                 it > 0 || k > 0 ? 1u : 0u);
+      umma_commit(&y.done[s]);
+    }
+    const int next = it + kStages - 1;
+    if (next < n) {
+      // the stage to refill was read by the products of step it - 1
+      if (it > 0) mbar_wait(&y.done[(it - 1) % kStages], ((it - 1) / kStages) & 1, &y.abort, a.st, 20);
+      load(next, next % kStages);
+    }
+    cp_async_commit();
+  }
+  mbar_wait(&y.done[(n - 1) % kStages], ((n - 1) / kStages) & 1, &y.abort, a.st, 21);
+  cp_async_wait<0>();
+  tc_fence_after();
+  float* red = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)));
+  __syncthreads();
+  spill(y.tmem, r16, red);
+  sync_end(y, tmem_columns(r16));
+  cluster_sync();
+  const int rows = 128 / ranks, row0 = rank * rows;
+  const float scale = a.scale != nullptr ? a.scale[t.group] : 1.f;
+  for (int i = tid; i < rows * R; i += kThreads) {
+    const int row = row0 + i / R, j = i % R;
+    if (row < t.count)
+      a.mid[static_cast<int64_t>(a.perm[t.start + row]) * R + j] =
+          to_16(scale * cluster_sum(base, row * red_pitch(r16) + j, ranks), a.bf16);
+  }
+  cluster_sync();   // the other CTAs have read this one's sums
+}
+
+// ---- out = addend + scale mid W^T (y and gx) --------------------------------
+
+struct ExpandArgs {
+  const uint16_t* mid;     // [M, R]
+  const uint16_t* W;       // per group [C, R] (K-major) or [R, C] (MN-major)
+  const uint16_t* addend;  // [M, C] or NULL; may be out
+  uint16_t* out;           // [M, C]
+  const float* scale;
+  const Tile* tiles;
+  const int* perm;
+  DevStatus* st;
+  int64_t C;
+  int R, E, cw, rw;
+  int col_tiles;           // 128-column tiles per CTA
+  bool bf16;
+};
+
+__host__ __device__ constexpr int expand_operand_bytes(int r16) { return (r16 > 64 ? 2 : 1) * 128 * kRowBytes; }
+
+// One CTA per (tile of 128 tokens, run of 128-column tiles): mid stays in
+// shared memory; per column tile W is read from L2, the addend tile arrives
+// two tiles ahead, is updated in place and leaves in whole rows.  Bound by
+// reading the addend and writing out.
+template <bool kMN>
+__global__ void __launch_bounds__(kThreads, 2) expand_kernel(const ExpandArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Sync y;
+  const Tile t = a.tiles[blockIdx.x];
+  if (t.count == 0) return;
+  const bool adapter = t.group < a.E;
+  if (!adapter && a.addend == a.out) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = a.R, r16 = rank16(R);
+  const int64_t C = a.C;
+  const int tiles_all = static_cast<int>((C + 127) / 128);
+  const int j0 = blockIdx.y * a.col_tiles, n = min(a.col_tiles, tiles_all - j0);
+  const uint32_t mids = align1024(smem_u32(smem_raw)), ws = mids + expand_operand_bytes(r16);
+  const uint32_t bufs = ws + expand_operand_bytes(r16);
+  constexpr uint32_t kBufBytes = 128 * 256;
+  const uint16_t* W = a.W + static_cast<int64_t>(adapter ? t.group : 0) * R * C;
+  const float scale = a.scale != nullptr && adapter ? a.scale[t.group] : 1.f;
+  sync_setup(y, 128);
+
+  // a thread loads and stores the same 16-byte chunks of a tile: chunk
+  // tid % 16 of rows tid / 16 + 16 i
+  int64_t row_at[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = (tid >> 4) + 16 * i;
+    row_at[i] = row < t.count ? static_cast<int64_t>(a.perm[t.start + row]) * C : -1;
+  }
+  auto chunk_at = [&](int row, int c) { return static_cast<uint32_t>(row * 256 + ((c ^ (row & 7)) << 4)); };
+  auto load_addend = [&](int j) {
+    if (a.addend == nullptr) return;
+    const int64_t at = static_cast<int64_t>(j0 + j) * 128 + (tid & 15) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (row_at[i] >= 0)
+        load_chunk(bufs + (j & 1) * kBufBytes + chunk_at((tid >> 4) + 16 * i, tid & 15), a.addend + row_at[i], at,
+                   C - at, a.cw);
+  };
+  auto load_w = [&](int j) {
+    if (!adapter) return;
+    const int64_t c0 = static_cast<int64_t>(j0 + j) * 128;
+    const int chunks = r16 / 8;
+    if constexpr (kMN) {
+      // blocks of 64 columns, r16 rows each
+      for (int i = tid; i < r16 * 16; i += kThreads) {
+        const int k = i >> 4, c = i & 15;
+        load_chunk(ws + (c >> 3) * r16 * kRowBytes + swizzled(k, c & 7), W + min(k, R - 1) * C, c0 + c * 8,
+                   k < R ? C - (c0 + c * 8) : 0, a.cw);
+      }
+    } else {
+      for (int i = tid; i < 128 * chunks; i += kThreads) {
+        const int row = i / chunks, c = i % chunks;
+        load_chunk(ws + (c >> 3) * 128 * kRowBytes + swizzled(row, c & 7), W + min(c0 + row, C - 1) * R, c * 8,
+                   c0 + row < C ? R - c * 8 : 0, a.rw);
+      }
+    }
+  };
+  if (adapter) {
+    const int chunks = r16 / 8;
+    for (int i = tid; i < t.count * chunks; i += kThreads) {
+      const int row = i / chunks, c = i % chunks;
+      load_chunk(mids + (c >> 3) * 128 * kRowBytes + swizzled(row, c & 7),
+                 a.mid + static_cast<int64_t>(a.perm[t.start + row]) * R, c * 8, R - c * 8, a.rw);
+    }
+  }
+  load_w(0);
+  load_addend(0);
+  cp_async_commit();
+  if (n > 1) load_addend(1);
+  cp_async_commit();
+
+  const uint32_t idesc = instruction(128, false, kMN, a.bf16);
+  for (int j = 0; j < n; ++j) {
+    cp_async_wait<1>();
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (adapter) {
+      if (tid == 0) {
+        tc_fence_after();
+        for (int k = 0; k < r16 / 16; ++k) {
+          const uint32_t kb = static_cast<uint32_t>(k >> 2) * 128 * kRowBytes;
+          umma_f16(y.tmem, desc_k(mids + kb, k & 3),
+                   kMN ? desc_mn(ws, k, r16 * kRowBytes) : desc_k(ws + kb, k & 3), idesc, k > 0 ? 1u : 0u);
+        }
+        umma_commit(&y.done[0]);
+      }
+      mbar_wait(&y.done[0], j & 1, &y.abort, a.st, 22);
+      tc_fence_after();
+    }
+    if (j + 1 < n) load_w(j + 1);
+    cp_async_commit();
+    const uint32_t buf = bufs + (j & 1) * kBufBytes;
+    const int row = (warp & 3) * 32 + lane;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c0 = (warp >> 2) * 64 + h * 32;
+      uint32_t v[32];
+      if (adapter) {
+        tmem_ld32(y.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0u;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint8_t* p = smem_raw + (buf - smem_u32(smem_raw)) + chunk_at(row, c0 / 8 + q);
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (a.addend != nullptr) w = ld_shared_v4(p);
+        uint32_t* e = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float lo = fmaf(scale, __uint_as_float(v[8 * q + 2 * i]), to_f32(e[i] & 0xffffu, a.bf16));
+          const float hi = fmaf(scale, __uint_as_float(v[8 * q + 2 * i + 1]), to_f32(e[i] >> 16, a.bf16));
+          e[i] = to_16(lo, a.bf16) | (static_cast<uint32_t>(to_16(hi, a.bf16)) << 16);
+        }
+        st_shared_v4(p, w);
+      }
+    }
+    __syncthreads();
+    const int64_t at = static_cast<int64_t>(j0 + j) * 128 + (tid & 15) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (row_at[i] < 0 || at >= C) continue;
+      const uint4 w = ld_shared_v4(smem_raw + (buf - smem_u32(smem_raw)) + chunk_at((tid >> 4) + 16 * i, tid & 15));
+      uint16_t* o = a.out + row_at[i] + at;
+      const uint32_t* e = reinterpret_cast<const uint32_t*>(&w);
+      if (a.cw == 16) {
+        *reinterpret_cast<uint4*>(o) = w;
+      } else {
+        const int64_t valid = C - at;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < valid) o[k] = static_cast<uint16_t>(e[k >> 1] >> (16 * (k & 1)));
+      }
+    }
+    if (j + 2 < n) load_addend(j + 2);
+    cp_async_commit();
+  }
+  cp_async_wait<0>();
+  sync_end(y, 128);
+}
+
+// ---- gradients of A and B ---------------------------------------------------
+
+struct GradArgs {
+  const uint16_t* mid;    // [M, R]
+  const uint16_t* X;      // [M, C]
+  uint16_t* grad;         // per group [R, C] (kRankMajor) or [C, R]
+  const float* scale;
+  const int* offset;
+  const int* perm;
+  DevStatus* st;
+  int64_t C;
+  int R, cw, rw;
+  bool bf16;
+};
+
+__host__ __device__ constexpr int grad_stage_bytes(int r16) {
+  return 2 * 64 * kRowBytes + (r16 > 64 ? 2 : 1) * 64 * kRowBytes;
+}
+
+// grad[c, j] = scale sum_m X[m, c] mid[m, j] over a group's tokens: one
+// cluster per (128 columns of X, group), its CTAs splitting the tokens.
+// Bound by reading X once.
+template <bool kRankMajor, int kStages>
+__global__ void __launch_bounds__(kThreads, 2) grad_kernel(const GradArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Sync y;
+  const int tid = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x, R = a.R, r16 = rank16(R);
+  const int64_t C = a.C, c0 = static_cast<int64_t>(blockIdx.y) * 128;
+  const int64_t e = blockIdx.z;
+  const int start = a.offset[e], tokens = a.offset[e + 1] - start;
+  const int cols = static_cast<int>(min(static_cast<int64_t>(128), C - c0));
+  uint16_t* grad = a.grad + e * R * C;
+  if (tokens == 0) {
+    if (rank == 0)
+      for (int i = tid; i < cols * R; i += kThreads)
+        grad[kRankMajor ? i / cols * C + c0 + i % cols : c0 * R + i] = 0;
+    return;
+  }
+  const uint32_t base = align1024(smem_u32(smem_raw));
+  const int stage_bytes = grad_stage_bytes(r16);
+  const int nb = (tokens + 63) / 64;
+  const int b0 = static_cast<int>(static_cast<int64_t>(nb) * rank / ranks);
+  const int n = static_cast<int>(static_cast<int64_t>(nb) * (rank + 1) / ranks) - b0;
+  const int chunks = r16 / 8;
+  sync_setup(y, tmem_columns(r16));
+
+  auto load = [&](int b, int s) {
+    const int m0 = (b0 + b) * 64;
+    const uint32_t xs = base + s * stage_bytes, us = xs + 2 * 64 * kRowBytes;
+    const int c = tid & 15;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = (tid >> 4) + 16 * i;
+      const bool in = m0 + k < tokens;
+      const int64_t m = in ? a.perm[start + m0 + k] : 0;
+      load_chunk(xs + (c >> 3) * 64 * kRowBytes + swizzled(k, c & 7), a.X + m * C, c0 + c * 8,
+                 in ? C - (c0 + c * 8) : 0, a.cw);
+    }
+    for (int i = tid; i < 64 * chunks; i += kThreads) {
+      const int k = i / chunks, q = i % chunks;
+      const bool in = m0 + k < tokens;
+      const int64_t m = in ? a.perm[start + m0 + k] : 0;
+      load_chunk(us + (q >> 3) * 64 * kRowBytes + swizzled(k, q & 7), a.mid + m * R, q * 8, in ? R - q * 8 : 0, a.rw);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (i < n) load(i, i);
+    cp_async_commit();
+  }
+  const uint32_t idesc = instruction(r16, true, true, a.bf16);
+  for (int it = 0; it < n; ++it) {
+    const int s = it % kStages;
+    cp_async_wait<kStages - 2>();
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      const uint32_t xs = base + s * stage_bytes, us = xs + 2 * 64 * kRowBytes;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        umma_f16(y.tmem, desc_mn(xs, k, 64 * kRowBytes), desc_mn(us, k, 64 * kRowBytes), idesc,
+                 it > 0 || k > 0 ? 1u : 0u);
+      umma_commit(&y.done[s]);
+    }
+    const int next = it + kStages - 1;
+    if (next < n) {
+      if (it > 0) mbar_wait(&y.done[(it - 1) % kStages], ((it - 1) / kStages) & 1, &y.abort, a.st, 23);
+      load(next, next % kStages);
+    }
+    cp_async_commit();
+  }
+  float* red = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)));
+  if (n > 0) {
+    mbar_wait(&y.done[(n - 1) % kStages], ((n - 1) / kStages) & 1, &y.abort, a.st, 24);
+    cp_async_wait<0>();
+    tc_fence_after();
+    __syncthreads();
+    spill(y.tmem, r16, red);
+  } else {   // a group with fewer token blocks than CTAs
+    for (int i = tid; i < 128 * red_pitch(r16); i += kThreads) red[i] = 0.f;
+  }
+  sync_end(y, tmem_columns(r16));
+  cluster_sync();
+  const int rows = 128 / ranks, row0 = rank * rows;
+  const float scale = a.scale != nullptr ? a.scale[e] : 1.f;
+  for (int i = tid; i < rows * R; i += kThreads) {
+    const int row = row0 + (kRankMajor ? i % rows : i / R), j = kRankMajor ? i / rows : i % R;
+    if (row < cols)
+      grad[kRankMajor ? j * C + c0 + row : (c0 + row) * R + j] =
+          to_16(scale * cluster_sum(base, row * red_pitch(r16) + j, ranks), a.bf16);
+  }
+  cluster_sync();
+}
+
+// ---- launches ---------------------------------------------------------------
 
 struct Problem {
   int64_t M, K, N, E;
   int R;
+  bool bf16;
   const float* scale;
   Plan plan;
+  DevStatus* st;
   cudaStream_t s;
 };
 
-template <typename T>
-cudaError_t shrink(const Problem& p, const void* X, int64_t C, const void* W, bool rank_major, const float* scale,
-                   void* out) {
-  ProfScope ps(K_ADAPTERS, p.s);
-  shrink_kernel<T><<<static_cast<unsigned>(p.plan.slots), kThreads, 0, p.s>>>(
-      static_cast<const T*>(X), C, static_cast<const T*>(W), p.R, rank_major, static_cast<int>(p.E), scale,
-      p.plan.tiles, p.plan.perm, static_cast<T*>(out));
-  return cudaGetLastError();
+// Bytes that every row start of a matrix with rows of C 16-bit elements is a
+// multiple of (the base is 16-byte aligned).
+int copy_width(int64_t C) { return C % 8 == 0 ? 16 : C % 4 == 0 ? 8 : C % 2 == 0 ? 4 : 2; }
+
+int sm_count() {
+  int dev = 0, sms = 152;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
 }
 
-template <typename T>
-cudaError_t expand(const Problem& p, const void* X, const void* W, int64_t C, bool rank_major, const float* scale,
+// CTAs that share one tile: enough for two per SM over the whole grid, each
+// with at least two reduction steps.
+int split(int64_t tiles, int64_t steps) {
+  int s = 1;
+  while (s < 8 && tiles * s * 2 <= 2 * sm_count() && steps >= 4 * s) s *= 2;
+  return s;
+}
+
+template <typename Args>
+cudaError_t launch(void (*kernel)(Args), const Args& a, dim3 grid, int cluster, int smem, int prof, cudaStream_t s) {
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  ProfScope ps(prof, s);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+cudaError_t shrink(const Problem& p, const void* X, int64_t C, const void* W, bool mn, const float* scale,
+                   void* mid) {
+  ShrinkArgs a;
+  a.X = static_cast<const uint16_t*>(X);
+  a.W = static_cast<const uint16_t*>(W);
+  a.mid = static_cast<uint16_t*>(mid);
+  a.scale = scale;
+  a.tiles = p.plan.tiles;
+  a.perm = p.plan.perm;
+  a.st = p.st;
+  a.C = C;
+  a.R = p.R;
+  a.E = static_cast<int>(p.E);
+  a.cw = copy_width(C);
+  a.rw = copy_width(p.R);
+  a.bf16 = p.bf16;
+  const int r16 = rank16(p.R), ranks = split(p.plan.slots, ceil_div(C, 64));
+  const int stages = r16 > 64 ? 3 : 4;
+  const int smem = 1024 + std::max(stages * shrink_stage_bytes(r16, mn), 128 * red_pitch(r16) * 4);
+  a.ranks = ranks;
+  const dim3 grid(static_cast<unsigned>(ranks * p.plan.slots));
+  if (stages == 4)
+    return launch(mn ? shrink_kernel<true, 4> : shrink_kernel<false, 4>, a, grid, ranks, smem, K_ADAPTERS, p.s);
+  return launch(mn ? shrink_kernel<true, 3> : shrink_kernel<false, 3>, a, grid, ranks, smem, K_ADAPTERS, p.s);
+}
+
+cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, bool mn, const float* scale,
                    const void* addend, void* out) {
-  ProfScope ps(K_ADAPTERS, p.s);
-  const dim3 grid(static_cast<unsigned>(p.plan.slots), static_cast<unsigned>(ceil_div(C, kThreads)));
-  expand_kernel<T><<<grid, kThreads, 0, p.s>>>(static_cast<const T*>(X), p.R, static_cast<const T*>(W), C, rank_major,
-                                               static_cast<int>(p.E), scale, p.plan.tiles, p.plan.perm,
-                                               static_cast<const T*>(addend), static_cast<T*>(out));
-  return cudaGetLastError();
+  ExpandArgs a;
+  a.mid = static_cast<const uint16_t*>(mid);
+  a.W = static_cast<const uint16_t*>(W);
+  a.addend = static_cast<const uint16_t*>(addend);
+  a.out = static_cast<uint16_t*>(out);
+  a.scale = scale;
+  a.tiles = p.plan.tiles;
+  a.perm = p.plan.perm;
+  a.st = p.st;
+  a.C = C;
+  a.R = p.R;
+  a.E = static_cast<int>(p.E);
+  a.cw = copy_width(C);
+  a.rw = copy_width(p.R);
+  a.bf16 = p.bf16;
+  const int64_t col_tiles = ceil_div(C, 128);
+  a.col_tiles = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, p.plan.slots * col_tiles /
+                                                                               (4 * sm_count()))));
+  const int smem = 1024 + 2 * expand_operand_bytes(rank16(p.R)) + 2 * 128 * 256;
+  const dim3 grid(static_cast<unsigned>(p.plan.slots), static_cast<unsigned>(ceil_div(col_tiles, a.col_tiles)));
+  return launch(mn ? expand_kernel<true> : expand_kernel<false>, a, grid, 1, smem, K_ADAPTERS, p.s);
 }
 
-template <typename T>
-cudaError_t grad(const Problem& p, const void* P, const void* X, int64_t C, bool rank_major, const float* scale,
+cudaError_t grad(const Problem& p, const void* mid, const void* X, int64_t C, bool rank_major, const float* scale,
                  void* out) {
-  ProfScope ps(K_ADAPTERS_GRAD, p.s);
-  const dim3 grid(static_cast<unsigned>(ceil_div(C, kThreads)), static_cast<unsigned>(p.R),
-                  static_cast<unsigned>(p.E));
-  grad_kernel<T><<<grid, kThreads, 0, p.s>>>(static_cast<const T*>(P), p.R, static_cast<const T*>(X), C, rank_major,
-                                             scale, p.plan.offset, p.plan.perm, static_cast<T*>(out));
-  return cudaGetLastError();
+  GradArgs a;
+  a.mid = static_cast<const uint16_t*>(mid);
+  a.X = static_cast<const uint16_t*>(X);
+  a.grad = static_cast<uint16_t*>(out);
+  a.scale = scale;
+  a.offset = p.plan.offset;
+  a.perm = p.plan.perm;
+  a.st = p.st;
+  a.C = C;
+  a.R = p.R;
+  a.cw = copy_width(C);
+  a.rw = copy_width(p.R);
+  a.bf16 = p.bf16;
+  const int r16 = rank16(p.R), ranks = split(ceil_div(C, 128) * p.E, ceil_div(ceil_div(p.M, p.E), 64));
+  const int stages = r16 > 64 ? 3 : 4;
+  const int smem = 1024 + std::max(stages * grad_stage_bytes(r16), 128 * red_pitch(r16) * 4);
+  const dim3 grid(static_cast<unsigned>(ranks), static_cast<unsigned>(ceil_div(C, 128)), static_cast<unsigned>(p.E));
+  if (stages == 4)
+    return launch(rank_major ? grad_kernel<true, 4> : grad_kernel<false, 4>, a, grid, ranks, smem, K_ADAPTERS_GRAD,
+                  p.s);
+  return launch(rank_major ? grad_kernel<true, 3> : grad_kernel<false, 3>, a, grid, ranks, smem, K_ADAPTERS_GRAD, p.s);
 }
 
-template <typename T>
 cudaError_t forward(const Problem& p, const void* x, const void* A, const void* B, const void* base, void* y,
                     void* t) {
-  if (cudaError_t e = shrink<T>(p, x, p.K, A, true, nullptr, t)) return e;
-  return expand<T>(p, t, B, p.N, false, p.scale, base, y);
+  if (cudaError_t e = shrink(p, x, p.K, A, false, nullptr, t)) return e;
+  return expand(p, t, B, p.N, false, p.scale, base, y);
 }
 
-template <typename T>
 cudaError_t backward(const Problem& p, const void* g, const void* x, const void* t, const void* A, const void* B,
                      const void* addend, void* gx, void* gA, void* gB, void* u) {
   if (gx != nullptr || gA != nullptr) {
-    if (cudaError_t e = shrink<T>(p, g, p.N, B, false, p.scale, u)) return e;
+    if (cudaError_t e = shrink(p, g, p.N, B, true, p.scale, u)) return e;
   }
   if (gx != nullptr) {
-    if (cudaError_t e = expand<T>(p, u, A, p.K, true, nullptr, addend, gx)) return e;
+    if (cudaError_t e = expand(p, u, A, p.K, true, nullptr, addend, gx)) return e;
   }
   if (gA != nullptr) {
-    if (cudaError_t e = grad<T>(p, u, x, p.K, true, nullptr, gA)) return e;
+    if (cudaError_t e = grad(p, u, x, p.K, true, nullptr, gA)) return e;
   }
-  if (gB != nullptr) return grad<T>(p, t, g, p.N, false, p.scale, gB);
+  if (gB != nullptr) return grad(p, t, g, p.N, false, p.scale, gB);
   return cudaSuccess;
 }
 
@@ -220,7 +777,7 @@ constexpr int64_t kMaxRank = 128, kMaxAdapters = 65535;
 
 bool valid_sizes(int64_t M, int64_t K, int64_t N, int64_t E, int64_t r) {
   return M >= 0 && K > 0 && N > 0 && E > 0 && r > 0 && r <= kMaxRank && E <= kMaxAdapters && M <= INT32_MAX / 2 &&
-         K <= (1 << 23) && N <= (1 << 23);
+         K <= (1 << 22) && N <= (1 << 22);
 }
 
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
@@ -270,9 +827,9 @@ int i8lt_adapters_forward(const void* x, int dt, int64_t M, int64_t K, const voi
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(ws, 0, sizeof(DevStatus), s) != cudaSuccess) return I8LT_ERR_CUDA;
   if (M == 0) return I8LT_OK;
-  const Problem p{M, K, N, E, static_cast<int>(r), scale, plan_layout(const_cast<void*>(plan), M, E), s};
-  return cuda_status(dt == DT_F16 ? forward<__half>(p, x, A, B, base, y, t)
-                                  : forward<__nv_bfloat16>(p, x, A, B, base, y, t));
+  const Problem p{M, K, N, E, static_cast<int>(r), dt == DT_BF16, scale, plan_layout(const_cast<void*>(plan), M, E),
+                  static_cast<DevStatus*>(ws), s};
+  return cuda_status(forward(p, x, A, B, base, y, t));
 }
 
 int i8lt_adapters_backward(const void* g, const void* x, const void* t, int dt, int64_t M, int64_t K, const void* A,
@@ -299,10 +856,10 @@ int i8lt_adapters_backward(const void* g, const void* x, const void* t, int dt, 
       return I8LT_ERR_CUDA;
     return I8LT_OK;
   }
-  const Problem p{M, K, N, E, static_cast<int>(r), scale, plan_layout(const_cast<void*>(plan), M, E), s};
+  const Problem p{M, K, N, E, static_cast<int>(r), dt == DT_BF16, scale, plan_layout(const_cast<void*>(plan), M, E),
+                  static_cast<DevStatus*>(ws), s};
   void* u = static_cast<uint8_t*>(ws) + 256;
-  return cuda_status(dt == DT_F16 ? backward<__half>(p, g, x, t, A, B, addend, gx, gA, gB, u)
-                                  : backward<__nv_bfloat16>(p, g, x, t, A, B, addend, gx, gA, gB, u));
+  return cuda_status(backward(p, g, x, t, A, B, addend, gx, gA, gB, u));
 }
 
 }  // extern "C"
