@@ -484,7 +484,7 @@ int i8lt_absmax8_dequantize(const uint8_t* q, const float* absmax2,
  *   gw[n] = sum_m g h, gb[n] = sum_m g                     [N] dtype wt
  *   g [M, N] dtype xt; mean and rstd from the forward; gx, gw, gb each may be
  *   NULL (at least one is not); ws of i8lt_layer_norm_backward_workspace_size
- *   bytes, 256-byte aligned, when gw or gb is given.
+ *   bytes, 256-byte aligned, status word first.
  * All arithmetic is fp32, every output is rounded once; the sums over the
  * tokens are taken in a fixed order (no atomics): equal inputs give equal
  * bits.  M == 0 writes zeros to gw and gb.

@@ -684,14 +684,10 @@ def layer_norm_backward(g: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rs
     gx = torch.empty_like(x) if need_x else None
     gw = torch.empty(N, dtype=dtype, device=x.device) if need_weight else None
     gb = torch.empty(N, dtype=dtype, device=x.device) if need_bias else None
-    ws = None
-    if need_weight or need_bias:
-        ws = torch.empty(max(_lib.i8lt_layer_norm_backward_workspace_size(M, N), 256), dtype=torch.uint8,
-                         device=x.device)
+    ws = torch.empty(max(_lib.i8lt_layer_norm_backward_workspace_size(M, N), 256), dtype=torch.uint8, device=x.device)
     _check(_lib.i8lt_layer_norm_backward(g.data_ptr(), x.data_ptr(), _code(x.dtype), M, N, mean.data_ptr(),
                                          rstd.data_ptr(), _ptr(weight), _code(dtype), _ptr(gx), _ptr(gw), _ptr(gb),
-                                         _ptr(ws), 0 if ws is None else ws.numel(), _stream(x)),
-           "i8lt_layer_norm_backward")
+                                         ws.data_ptr(), ws.numel(), _stream(x)), "i8lt_layer_norm_backward")
     return gx, gw, gb
 
 
