@@ -8,6 +8,7 @@
 // reads x and g and writes gx, each once; everything between stays in
 // registers and shared memory.
 #include <algorithm>
+#include <mutex>
 #include <type_traits>
 
 #include "i8lt.h"
@@ -27,32 +28,66 @@ __device__ __forceinline__ void store_any(void* p, int dt, int64_t i, float v) {
   else static_cast<float*>(p)[i] = v;
 }
 
-// W consecutive elements held in their storage type: one 16-byte access, or
-// a single element in rows that are not 16-byte aligned.
+// ---- packs -----------------------------------------------------------------
+//
+// A thread reads and writes packs of W consecutive elements: 16 bytes, or a
+// single element in rows that are not 16-byte aligned.  Pack i of thread
+// `lane` of kLanes starts at column (lane + i * kLanes) * W.
+
 template <typename T, int W>
-struct Pack {
+struct alignas(W == 1 ? sizeof(T) : 16) Pack {
   T v[W];
 };
 template <typename T, int W>
 __device__ __forceinline__ Pack<T, W> load_pack(const T* p) {
-  Pack<T, W> r;
-  if constexpr (W == 1) {
-    r.v[0] = p[0];
+  return *reinterpret_cast<const Pack<T, W>*>(p);
+}
+// Both halves of a 16-bit pair widen and narrow at once.
+template <typename T, int W>
+__device__ __forceinline__ void widen(const Pack<T, W>& p, float* f) {
+  if constexpr (W == 1 || sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) f[k] = to_float(p.v[k]);
   } else {
-    static_assert(W * sizeof(T) == 16, "one 16-byte access");
-    *reinterpret_cast<uint4*>(r.v) = *reinterpret_cast<const uint4*>(p);
+#pragma unroll
+    for (int k = 0; k < W; k += 2) {
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(p.v + k);
+      if constexpr (std::is_same<T, __half>::value) {
+        const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&u));
+        f[k] = q.x;
+        f[k + 1] = q.y;
+      } else {
+        f[k] = __uint_as_float(u << 16);
+        f[k + 1] = __uint_as_float(u & 0xffff0000u);
+      }
+    }
   }
-  return r;
 }
 template <typename T, int W>
-__device__ __forceinline__ void store_pack(T* p, const Pack<T, W>& r) {
-  if constexpr (W == 1) p[0] = r.v[0];
-  else *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(r.v);
+__device__ __forceinline__ void store_floats(T* dst, const float* f) {
+  Pack<T, W> p;
+  if constexpr (W == 1 || sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) p.v[k] = from_float<T>(f[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < W; k += 2) {
+      if constexpr (std::is_same<T, __half>::value)
+        *reinterpret_cast<__half2*>(p.v + k) = __floats2half2_rn(f[k], f[k + 1]);
+      else
+        *reinterpret_cast<__nv_bfloat162*>(p.v + k) = __floats2bfloat162_rn(f[k], f[k + 1]);
+    }
+  }
+  *reinterpret_cast<Pack<T, W>*>(dst) = p;
 }
-// W elements of a parameter vector of runtime type, widened.
+// W elements of a parameter vector of runtime type, widened; `none` for a
+// vector that is absent.
 template <int W>
-__device__ __forceinline__ void load_param(const void* p, int dt, int64_t i, float (&f)[W]) {
-  if constexpr (W == 1) {
+__device__ __forceinline__ void load_param(const void* p, int dt, int64_t i, float none, float* f) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) f[k] = none;
+  } else if constexpr (W == 1) {
     f[0] = load_any(p, dt, i);
   } else if (dt == DT_F32) {
 #pragma unroll
@@ -61,43 +96,130 @@ __device__ __forceinline__ void load_param(const void* p, int dt, int64_t i, flo
   } else {
     using U = typename std::conditional<W == 8, uint4, uint2>::type;
     const U u = __ldg(reinterpret_cast<const U*>(static_cast<const uint16_t*>(p) + i));
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(&u);
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(&u);
 #pragma unroll
-    for (int k = 0; k < W; ++k)
-      f[k] = dt == DT_BF16 ? __uint_as_float(static_cast<uint32_t>(q[k]) << 16) : __half2float(__ushort_as_half(q[k]));
+    for (int k = 0; k < W / 2; ++k) {
+      if (dt == DT_BF16) {
+        f[2 * k] = __uint_as_float(q[k] << 16);
+        f[2 * k + 1] = __uint_as_float(q[k] & 0xffff0000u);
+      } else {
+        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(q + k));
+        f[2 * k] = h.x;
+        f[2 * k + 1] = h.y;
+      }
+    }
   }
 }
 
 // A row is shared by kLanes threads: kLanes <= 32 lanes of a warp, or a block
-// of kLanes threads.  Sum of `kN` values over them, the same bits in every
-// thread; scratch: kN * kLanes / 32 floats (block rows only), which the next
-// but one call may reuse after another barrier.
-template <int kLanes, int kN>
-__device__ __forceinline__ void row_sum(float (&v)[kN], float* scratch) {
+// of kLanes threads.  The sum of a value over them, the same bits in every
+// thread; scratch: kLanes / 32 floats (block rows only), free again after the
+// block's next barrier.
+template <int kLanes>
+__device__ __forceinline__ float row_sum(float v, float* scratch) {
 #pragma unroll
-  for (int o = (kLanes < 32 ? kLanes : 32) / 2; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < kN; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  for (int o = (kLanes < 32 ? kLanes : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (kLanes > 32) {
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-      for (int i = 0; i < kN; ++i) scratch[i * (kLanes / 32) + (threadIdx.x >> 5)] = v[i];
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
     __syncthreads();
+    v = 0.f;
+    if constexpr (kLanes == 64) {
+      v = scratch[0] + scratch[1];
+    } else {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      float s = 0.f;
-      if constexpr (kLanes == 64) {
-        s = scratch[2 * i] + scratch[2 * i + 1];
-      } else {
-#pragma unroll
-        for (int k = 0; k < kLanes / 32; k += 4) {
-          const float4 q = *reinterpret_cast<const float4*>(scratch + i * (kLanes / 32) + k);
-          s += (q.x + q.y) + (q.z + q.w);
-        }
+      for (int k = 0; k < kLanes / 32; k += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(scratch + k);
+        v += (q.x + q.y) + (q.z + q.w);
       }
-      v[i] = s;
     }
   }
+  return v;
+}
+
+// ---- the ring --------------------------------------------------------------
+//
+// Rows of more than 512 (backward: 256) elements: every block walks over rows,
+// or over the same slice of rows, in turn; bulk copies bring the next rows
+// into a ring of shared-memory stages while this row is worked on, so that
+// the bytes in flight do not depend on how many rows a block's registers
+// hold.  Rows that do not start on 16 bytes are copied from the boundary below
+// them and read element by element.
+constexpr int kMaxStages = 8;
+constexpr int kRingBytes = 200 * 1024;   // shared memory per SM given to the rings
+
+struct RingLayout {
+  int cols;         // columns per block
+  int slot_bytes;   // bytes of one slice of one matrix in a stage
+  unsigned stages;
+};
+
+template <typename T, int kMats>
+struct Ring {
+  const uint8_t* mat[kMats];
+  uint8_t* base;
+  uint64_t* full;
+  RingLayout L;
+  int64_t N, n0, step, rows;
+  unsigned long long end;   // bytes of a matrix
+  int cols;
+
+  __device__ __forceinline__ int64_t row(int64_t i) const { return blockIdx.x + i * step; }
+  __device__ __forceinline__ unsigned long long start(int64_t i) const {
+    return static_cast<unsigned long long>((row(i) * N + n0) * static_cast<int64_t>(sizeof(T)));
+  }
+  // the end of the copy of a slice that starts at byte b: the boundary above
+  // its end, or the last one inside the matrix
+  __device__ __forceinline__ unsigned long long stop(unsigned long long b) const {
+    return min((b + cols * sizeof(T) + 15ull) & ~15ull, end & ~15ull);
+  }
+  __device__ __forceinline__ void issue(int64_t i) {   // one thread
+    const unsigned long long b = start(i), lo = b & ~15ull, hi = stop(b);
+    const uint32_t bytes = hi > lo ? static_cast<uint32_t>(hi - lo) : 0u;
+    const int s = static_cast<int>(static_cast<unsigned>(i) % L.stages);
+    mbar_arrive_expect_tx(&full[s], kMats * bytes);
+    if (bytes != 0)
+#pragma unroll
+      for (int k = 0; k < kMats; ++k)
+        bulk_load(base + (static_cast<size_t>(s) * kMats + k) * L.slot_bytes, mat[k] + lo, bytes, &full[s]);
+  }
+};
+
+// A row's slice in its stage: elements [0, have) lie in shared memory, the
+// last few of the matrix, which no 16-byte copy covers, in global memory.
+template <typename T>
+struct Slice {
+  const T *near, *far;
+  int have;
+};
+template <typename T, int W, int kMats>
+__device__ __forceinline__ Slice<T> slice_of(const Ring<T, kMats>& r, int k, int64_t i, int stage) {
+  const unsigned long long b = r.start(i);
+  Slice<T> s;
+  s.near = reinterpret_cast<const T*>(r.base + (static_cast<size_t>(stage) * kMats + k) * r.L.slot_bytes + (b & 15));
+  s.far = reinterpret_cast<const T*>(r.mat[k] + b);
+  s.have = r.cols;
+  if constexpr (W == 1) {
+    const unsigned long long e = r.stop(b);
+    s.have = e > b ? static_cast<int>(min((e - b) / sizeof(T), static_cast<unsigned long long>(r.cols))) : 0;
+  }
+  return s;
+}
+// The pack at column c of a slice of `cols` columns; zeros past the end.
+template <typename T, int W>
+__device__ __forceinline__ void read(const Slice<T>& s, int c, int cols, float* f) {
+  if (c < cols) {
+    if constexpr (W == 1) f[0] = to_float(c < s.have ? s.near[c] : s.far[c]);
+    else widen<T, W>(load_pack<T, W>(s.near + c), f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < W; ++k) f[k] = 0.f;
+  }
+}
+
+__device__ __forceinline__ void ring_setup(uint64_t* full, unsigned stages, int* abort_flag) {
+  for (unsigned i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+  *abort_flag = 0;
+  fence_mbar_init();
 }
 
 // ---- forward ---------------------------------------------------------------
@@ -112,69 +234,49 @@ struct ForwardArgs {
   float eps;
 };
 
-// The whole row in registers: kVec packs of W elements per thread, read once;
-// the variance is summed around the mean.  Blocks of 256 threads hold
-// 256 / kLanes short rows, longer ones a block each.
-template <typename T, int W, int kLanes, int kVec>
-__global__ void __launch_bounds__(kLanes < 256 ? 256 : kLanes) norm_forward_kernel(const ForwardArgs a) {
-  constexpr int kRows = kLanes < 256 ? (kLanes > 32 ? 1 : 256 / kLanes) : 1;
-  __shared__ __align__(16) float scratch[2][kLanes > 32 ? kLanes / 32 : 1];
-  const int lane = threadIdx.x % kLanes;
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kLanes;
+// Short rows: kLanes lanes of a warp hold a row in registers; the variance is
+// summed around the mean.
+template <typename T, int W, int kLanes, int kE>
+__global__ void __launch_bounds__(256) norm_forward_short_kernel(const ForwardArgs a) {
+  const int lane = threadIdx.x % kLanes, N = static_cast<int>(a.N);
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
   const bool live = m < a.M;
-  const int64_t N = a.N;
   const T* x = static_cast<const T*>(a.x) + (live ? m : 0) * N;
-  Pack<T, W> p[kVec];
-  float s[1] = {0.f};
+  float v[kE];
+  float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int64_t n = static_cast<int64_t>(lane + i * kLanes) * W;
-    if (n < N) p[i] = load_pack<T, W>(x + n);
+  for (int i = 0; i < kE / W; ++i) {
+    const int c = (lane + i * kLanes) * W;
+    if (c < N) widen<T, W>(load_pack<T, W>(x + c), v + i * W);
   }
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int64_t n = static_cast<int64_t>(lane + i * kLanes) * W;
-    if (n < N)
+  for (int i = 0; i < kE / W; ++i)
+    if ((lane + i * kLanes) * W < N)
 #pragma unroll
-      for (int k = 0; k < W; ++k) s[0] += to_float(p[i].v[k]);
-  }
-  row_sum<kLanes, 1>(s, scratch[0]);
-  const float mu = s[0] / static_cast<float>(N);
-  s[0] = 0.f;
+      for (int k = 0; k < W; ++k) s += v[i * W + k];
+  const float mu = row_sum<kLanes>(s, nullptr) / static_cast<float>(N);
+  s = 0.f;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int64_t n = static_cast<int64_t>(lane + i * kLanes) * W;
-    if (n < N)
+  for (int i = 0; i < kE / W; ++i)
+    if ((lane + i * kLanes) * W < N)
 #pragma unroll
       for (int k = 0; k < W; ++k) {
-        const float d = to_float(p[i].v[k]) - mu;
-        s[0] += d * d;
+        v[i * W + k] -= mu;
+        s += v[i * W + k] * v[i * W + k];
       }
-  }
-  row_sum<kLanes, 1>(s, scratch[1]);
-  const float r = 1.0f / sqrtf(s[0] / static_cast<float>(N) + a.eps);
+  const float r = 1.0f / sqrtf(row_sum<kLanes>(s, nullptr) / static_cast<float>(N) + a.eps);
   if (!live) return;
   T* y = static_cast<T*>(a.y) + m * N;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int64_t n = static_cast<int64_t>(lane + i * kLanes) * W;
-    if (n >= N) continue;
-    float f[W], q[W];
+  for (int i = 0; i < kE / W; ++i) {
+    const int c = (lane + i * kLanes) * W;
+    if (c >= N) continue;
+    float w[W], b[W];
+    load_param<W>(a.w, a.wt, c, 1.f, w);
+    load_param<W>(a.b, a.wt, c, 0.f, b);
 #pragma unroll
-    for (int k = 0; k < W; ++k) f[k] = (to_float(p[i].v[k]) - mu) * r;
-    if (a.w != nullptr) {
-      load_param<W>(a.w, a.wt, n, q);
-#pragma unroll
-      for (int k = 0; k < W; ++k) f[k] *= q[k];
-    }
-    if (a.b != nullptr) {
-      load_param<W>(a.b, a.wt, n, q);
-#pragma unroll
-      for (int k = 0; k < W; ++k) f[k] += q[k];
-    }
-#pragma unroll
-    for (int k = 0; k < W; ++k) p[i].v[k] = from_float<T>(f[k]);
-    store_pack<T, W>(y + n, p[i]);
+    for (int k = 0; k < W; ++k) v[i * W + k] = fmaf(v[i * W + k] * r, w[k], b[k]);
+    store_floats<T, W>(y + c, v + i * W);
   }
   if (lane == 0) {
     if (a.mean != nullptr) a.mean[m] = mu;
@@ -182,27 +284,160 @@ __global__ void __launch_bounds__(kLanes < 256 ? 256 : kLanes) norm_forward_kern
   }
 }
 
-// Rows that do not fit the registers of a block: three passes over the row,
-// the later ones from L1 / L2.
-constexpr int kLongThreads = 1024;
+// Rows of up to 8192 elements: 32 elements, and their w and b, in each
+// thread's registers.
+template <typename T, int W, int kLanes, int kE>
+__global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel(const ForwardArgs a,
+                                                                                const RingLayout L) {
+  extern __shared__ __align__(128) uint8_t stages[];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ __align__(16) float scratch[2][kLanes / 32];
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, N = static_cast<int>(a.N);
+  Ring<T, 1> ring{{static_cast<const uint8_t*>(a.x)}, stages, full, L, a.N, 0, gridDim.x,
+                  (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
+                  static_cast<unsigned long long>(a.M) * a.N * sizeof(T), N};
+  if (tid == 0) {
+    ring_setup(full, L.stages, &abort_flag);
+    for (int64_t i = 0; i < L.stages && i < ring.rows; ++i) ring.issue(i);
+  }
+  __syncthreads();
+  float w[kE], b[kE], v[kE];
+#pragma unroll
+  for (int i = 0; i < kE / W; ++i) {
+    const int c = (tid + i * kLanes) * W;
+    if (c < N) {
+      load_param<W>(a.w, a.wt, c, 1.f, w + i * W);
+      load_param<W>(a.b, a.wt, c, 0.f, b + i * W);
+    }
+  }
+  const float inv_n = 1.0f / static_cast<float>(N);
+  unsigned s = 0;
+  uint32_t phase = 0;
+  for (int64_t i = 0; i < ring.rows; ++i) {
+    mbar_wait(&full[s], phase, &abort_flag, nullptr, 31);
+    const Slice<T> x = slice_of<T, W>(ring, 0, i, s);
+    float t = 0.f;
+#pragma unroll
+    for (int e = 0; e < kE / W; ++e) {
+      read<T, W>(x, (tid + e * kLanes) * W, N, v + e * W);
+#pragma unroll
+      for (int k = 0; k < W; ++k) t += v[e * W + k];
+    }
+    const float mu = row_sum<kLanes>(t, scratch[0]) * inv_n;   // its barrier: every thread has read the stage
+    if (tid == 0 && i + L.stages < ring.rows) ring.issue(i + L.stages);
+    if (++s == L.stages) {
+      s = 0;
+      phase ^= 1;
+    }
+    t = 0.f;
+#pragma unroll
+    for (int e = 0; e < kE / W; ++e)
+      if ((tid + e * kLanes) * W < N)
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          v[e * W + k] -= mu;
+          t += v[e * W + k] * v[e * W + k];
+        }
+    const float r = 1.0f / sqrtf(row_sum<kLanes>(t, scratch[1]) * inv_n + a.eps);
+    const int64_t m = ring.row(i);
+    T* y = static_cast<T*>(a.y) + m * N;
+#pragma unroll
+    for (int e = 0; e < kE / W; ++e) {
+      const int c = (tid + e * kLanes) * W;
+      if (c >= N) continue;
+#pragma unroll
+      for (int k = 0; k < W; ++k) v[e * W + k] = fmaf(v[e * W + k] * r, w[e * W + k], b[e * W + k]);
+      store_floats<T, W>(y + c, v + e * W);
+    }
+    if (tid == 0) {
+      if (a.mean != nullptr) a.mean[m] = mu;
+      if (a.rstd != nullptr) a.rstd[m] = r;
+    }
+  }
+}
+
+// Longer rows: three passes over the row's stage in shared memory.
+constexpr int kWideThreads = 1024;
+template <typename T, int W>
+__global__ void __launch_bounds__(kWideThreads) norm_forward_wide_kernel(const ForwardArgs a, const RingLayout L) {
+  extern __shared__ __align__(128) uint8_t stages[];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ __align__(16) float scratch[2][kWideThreads / 32];
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, N = static_cast<int>(a.N);
+  Ring<T, 1> ring{{static_cast<const uint8_t*>(a.x)}, stages, full, L, a.N, 0, gridDim.x,
+                  (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
+                  static_cast<unsigned long long>(a.M) * a.N * sizeof(T), N};
+  if (tid == 0) {
+    ring_setup(full, L.stages, &abort_flag);
+    for (int64_t i = 0; i < L.stages && i < ring.rows; ++i) ring.issue(i);
+  }
+  __syncthreads();
+  const float inv_n = 1.0f / static_cast<float>(N);
+  unsigned s = 0;
+  uint32_t phase = 0;
+  for (int64_t i = 0; i < ring.rows; ++i) {
+    mbar_wait(&full[s], phase, &abort_flag, nullptr, 31);
+    const Slice<T> x = slice_of<T, W>(ring, 0, i, s);
+    float t = 0.f, v[W];
+#pragma unroll 4
+    for (int c = tid * W; c < N; c += kWideThreads * W) {
+      read<T, W>(x, c, N, v);
+#pragma unroll
+      for (int k = 0; k < W; ++k) t += v[k];
+    }
+    const float mu = row_sum<kWideThreads>(t, scratch[0]) * inv_n;
+    // every thread is past the stage of the row before this one
+    if (tid == 0 && i > 0 && i - 1 + L.stages < ring.rows) ring.issue(i - 1 + L.stages);
+    t = 0.f;
+#pragma unroll 4
+    for (int c = tid * W; c < N; c += kWideThreads * W) {
+      read<T, W>(x, c, N, v);
+#pragma unroll
+      for (int k = 0; k < W; ++k) t += (v[k] - mu) * (v[k] - mu);
+    }
+    const float r = 1.0f / sqrtf(row_sum<kWideThreads>(t, scratch[1]) * inv_n + a.eps);
+    const int64_t m = ring.row(i);
+    T* y = static_cast<T*>(a.y) + m * N;
+#pragma unroll 4
+    for (int c = tid * W; c < N; c += kWideThreads * W) {
+      float w[W], b[W];
+      load_param<W>(a.w, a.wt, c, 1.f, w);
+      load_param<W>(a.b, a.wt, c, 0.f, b);
+      read<T, W>(x, c, N, v);
+#pragma unroll
+      for (int k = 0; k < W; ++k) v[k] = fmaf((v[k] - mu) * r, w[k], b[k]);
+      store_floats<T, W>(y + c, v);
+    }
+    if (tid == 0) {
+      if (a.mean != nullptr) a.mean[m] = mu;
+      if (a.rstd != nullptr) a.rstd[m] = r;
+    }
+    if (++s == L.stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+}
+
+// Rows that do not fit shared memory twice: three passes over global memory.
 template <typename T>
-__global__ void __launch_bounds__(kLongThreads) norm_forward_long_kernel(const ForwardArgs a) {
-  __shared__ __align__(16) float scratch[2][kLongThreads / 32];
+__global__ void __launch_bounds__(kWideThreads) norm_forward_long_kernel(const ForwardArgs a) {
+  __shared__ __align__(16) float scratch[2][kWideThreads / 32];
   const int64_t m = blockIdx.x, N = a.N;
   const T* x = static_cast<const T*>(a.x) + m * N;
   T* y = static_cast<T*>(a.y) + m * N;
-  float s[1] = {0.f};
-  for (int64_t n = threadIdx.x; n < N; n += kLongThreads) s[0] += to_float(x[n]);
-  row_sum<kLongThreads, 1>(s, scratch[0]);
-  const float mu = s[0] / static_cast<float>(N);
-  s[0] = 0.f;
-  for (int64_t n = threadIdx.x; n < N; n += kLongThreads) {
+  float t = 0.f;
+  for (int64_t n = threadIdx.x; n < N; n += kWideThreads) t += to_float(x[n]);
+  const float mu = row_sum<kWideThreads>(t, scratch[0]) / static_cast<float>(N);
+  t = 0.f;
+  for (int64_t n = threadIdx.x; n < N; n += kWideThreads) {
     const float d = to_float(x[n]) - mu;
-    s[0] += d * d;
+    t += d * d;
   }
-  row_sum<kLongThreads, 1>(s, scratch[1]);
-  const float r = 1.0f / sqrtf(s[0] / static_cast<float>(N) + a.eps);
-  for (int64_t n = threadIdx.x; n < N; n += kLongThreads) {
+  const float r = 1.0f / sqrtf(row_sum<kWideThreads>(t, scratch[1]) / static_cast<float>(N) + a.eps);
+  for (int64_t n = threadIdx.x; n < N; n += kWideThreads) {
     float v = (to_float(x[n]) - mu) * r;
     if (a.w != nullptr) v *= load_any(a.w, a.wt, n);
     if (a.b != nullptr) v += load_any(a.b, a.wt, n);
@@ -214,26 +449,59 @@ __global__ void __launch_bounds__(kLongThreads) norm_forward_long_kernel(const F
   }
 }
 
-template <typename T, int W, int kLanes, int kVec>
-cudaError_t launch_forward(const ForwardArgs& a, cudaStream_t s) {
-  constexpr int kRows = kLanes > 32 ? 1 : 256 / kLanes;
-  norm_forward_kernel<T, W, kLanes, kVec>
-      <<<static_cast<unsigned>(ceil_div(a.M, kRows)), kLanes > 32 ? kLanes : 256, 0, s>>>(a);
+int sm_count() {
+  int dev = 0, sms = 152;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+// Stages of `mats` slices of `cols` elements, for per_sm blocks per SM.
+RingLayout ring_layout(int64_t cols, int elem, int mats, int per_sm) {
+  RingLayout L;
+  L.cols = static_cast<int>(cols);
+  // up to 15 bytes before a slice that starts off a boundary
+  L.slot_bytes = static_cast<int>(round_up(cols * elem + 16, 128));
+  L.stages = static_cast<unsigned>(std::min(kMaxStages, kRingBytes / per_sm / (mats * L.slot_bytes)));
+  return L;
+}
+
+template <typename T, int W, int kLanes, int kE>
+cudaError_t launch_forward_short(const ForwardArgs& a, cudaStream_t s) {
+  norm_forward_short_kernel<T, W, kLanes, kE>
+      <<<static_cast<unsigned>(ceil_div(a.M, 256 / kLanes)), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-// The fewest threads that hold a row with 32 elements each (8 in rows of up
-// to 256): fewer partial sums to exchange, and enough rows in flight per SM.
+template <typename T, int W, int kLanes, int kE>
+cudaError_t launch_forward_ring(const ForwardArgs& a, cudaStream_t s) {
+  auto kernel = norm_forward_ring_kernel<T, W, kLanes, kE>;
+  constexpr int per_sm = 512 / kLanes;
+  const RingLayout L = ring_layout(a.N, sizeof(T), 1, per_sm);
+  const int smem = static_cast<int>(L.stages) * L.slot_bytes;
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
+  kernel<<<static_cast<unsigned>(std::min<int64_t>(a.M, sm_count() * per_sm)), kLanes, smem, s>>>(a, L);
+  return cudaGetLastError();
+}
+
 template <typename T, int W>
 cudaError_t forward_sized(const ForwardArgs& a, cudaStream_t s) {
-  if (a.N <= 64) return launch_forward<T, W, 8, 8 / W>(a, s);
-  if (a.N <= 256) return launch_forward<T, W, 32, 8 / W>(a, s);
-  if (a.N <= 1024) return launch_forward<T, W, 32, 32 / W>(a, s);
-  if (a.N <= 4096) return launch_forward<T, W, 128, 32 / W>(a, s);
-  if (a.N <= 8192) return launch_forward<T, W, 256, 32 / W>(a, s);
-  if (a.N <= 16384) return launch_forward<T, W, 512, 32 / W>(a, s);
-  if (a.N <= 32768) return launch_forward<T, W, 1024, 32 / W>(a, s);
-  norm_forward_long_kernel<T><<<static_cast<unsigned>(a.M), kLongThreads, 0, s>>>(a);
+  if (a.N <= 64) return launch_forward_short<T, W, 8, 8>(a, s);
+  if (a.N <= 256) return launch_forward_short<T, W, 32, 8>(a, s);
+  if (a.N <= 512) return launch_forward_short<T, W, 32, 16>(a, s);
+  if (a.N <= 1024) return launch_forward_ring<T, W, 64, 16>(a, s);
+  if (a.N <= 2048) return launch_forward_ring<T, W, 64, 32>(a, s);
+  if (a.N <= 4096) return launch_forward_ring<T, W, 128, 32>(a, s);
+  if (a.N <= 8192) return launch_forward_ring<T, W, 256, 32>(a, s);
+  if (a.N * static_cast<int64_t>(sizeof(T)) <= kRingBytes / 2 - 256) {
+    auto kernel = norm_forward_wide_kernel<T, W>;
+    const RingLayout L = ring_layout(a.N, sizeof(T), 1, 1);
+    const int smem = static_cast<int>(L.stages) * L.slot_bytes;
+    if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
+    kernel<<<static_cast<unsigned>(std::min<int64_t>(a.M, sm_count())), kWideThreads, smem, s>>>(a, L);
+    return cudaGetLastError();
+  }
+  norm_forward_long_kernel<T><<<static_cast<unsigned>(a.M), kWideThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -260,30 +528,25 @@ struct BackwardArgs {
 // Short rows: kLanes lanes of a warp per row, rows dealt out in turn, the
 // next row's loads issued before this row's arithmetic; every lane sums its
 // own columns' gradients over its rows, the block adds them up at the end.
-template <typename T, int W, int kLanes, int kVec>
-__global__ void __launch_bounds__(256) norm_backward_short_kernel(const BackwardArgs a) {
-  constexpr int kSlots = 256 / kLanes;
-  constexpr int kElems = kVec * W;
-  __shared__ float sums[kSlots][kLanes * kElems];
-  const int lane = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
-  const int64_t N = a.N, step = static_cast<int64_t>(gridDim.x) * kSlots;
-  const T* x = static_cast<const T*>(a.x);
-  const T* g = static_cast<const T*>(a.g);
-  float w[kElems], aw[kElems], ab[kElems];
+template <typename T, int W, int kLanes>
+__global__ void __launch_bounds__(256, 2) norm_backward_short_kernel(const BackwardArgs a) {
+  constexpr int kE = 8, kSlots = 256 / kLanes, kVec = kE / W;
+  __shared__ float sums[kSlots][kLanes * kE];
+  const int lane = threadIdx.x % kLanes, slot = threadIdx.x / kLanes, N = static_cast<int>(a.N);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kSlots;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.st = DevStatus{0, 0, 0, 0};
+  float w[kE], aw[kE], ab[kE];
+  Pack<T, W> px[kVec], pg[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    const int64_t n = static_cast<int64_t>(lane + i * kLanes) * W;
-    float q[W];
-#pragma unroll
-    for (int k = 0; k < W; ++k) q[k] = n < N ? 1.f : 0.f;
-    if (a.w != nullptr && n < N) load_param<W>(a.w, a.wt, n, q);
+    const int c = (lane + i * kLanes) * W;
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-      w[i * W + k] = q[k];
-      aw[i * W + k] = ab[i * W + k] = 0.f;
+      px[i].v[k] = pg[i].v[k] = from_float<T>(0.f);
+      w[i * W + k] = aw[i * W + k] = ab[i * W + k] = 0.f;
     }
+    if (c < N) load_param<W>(a.w, a.wt, c, 1.f, w + i * W);
   }
-  Pack<T, W> px[kVec], pg[kVec];
   float mu = 0.f, r = 0.f;
   auto fetch = [&](int64_t m) {
     if (m >= a.M) return;
@@ -291,52 +554,51 @@ __global__ void __launch_bounds__(256) norm_backward_short_kernel(const Backward
     r = a.rstd[m];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const int64_t n = static_cast<int64_t>(lane + i * kLanes) * W;
-      if (n < N) {
-        px[i] = load_pack<T, W>(x + m * N + n);
-        pg[i] = load_pack<T, W>(g + m * N + n);
+      const int c = (lane + i * kLanes) * W;
+      if (c < N) {
+        px[i] = load_pack<T, W>(static_cast<const T*>(a.x) + m * N + c);
+        pg[i] = load_pack<T, W>(static_cast<const T*>(a.g) + m * N + c);
       }
     }
   };
   int64_t m = static_cast<int64_t>(blockIdx.x) * kSlots + slot;
-  // every lane of a warp makes the same number of turns
+  // every lane of a warp makes the same number of turns; a lane group without
+  // a row of its own repeats what it holds and keeps nothing of it
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kSlots + (threadIdx.x & ~31) / kLanes;
   fetch(m);
   for (int64_t turn = first; turn < a.M; turn += step, m += step) {
     const bool live = m < a.M;
-    float h[kElems], gv[kElems];
-    const float cmu = mu, cr = r;
+    float h[kE], g[kE];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const bool in = live && static_cast<int64_t>(lane + i * kLanes) * W < N;
-#pragma unroll
-      for (int k = 0; k < W; ++k) {
-        h[i * W + k] = in ? (to_float(px[i].v[k]) - cmu) * cr : 0.f;
-        gv[i * W + k] = in ? to_float(pg[i].v[k]) : 0.f;
-      }
+      widen<T, W>(px[i], h + i * W);
+      widen<T, W>(pg[i], g + i * W);
     }
+    const float cmu = mu, cr = r;
     fetch(m + step);
-    float s[2] = {0.f, 0.f};
+    float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-    for (int e = 0; e < kElems; ++e) {
-      aw[e] += gv[e] * h[e];
-      ab[e] += gv[e];
-      gv[e] *= w[e];
-      s[0] += gv[e];
-      s[1] += gv[e] * h[e];
+    for (int e = 0; e < kE; ++e) {
+      h[e] = (h[e] - cmu) * cr;
+      if (live) {
+        aw[e] += g[e] * h[e];
+        ab[e] += g[e];
+      }
+      g[e] *= w[e];
+      s0 += g[e];
+      s1 += g[e] * h[e];
     }
     if (a.gx == nullptr) continue;
-    row_sum<kLanes, 2>(s, nullptr);
-    const float c1 = s[0] / static_cast<float>(N), c2 = s[1] / static_cast<float>(N);
+    const float c1 = row_sum<kLanes>(s0, nullptr) / static_cast<float>(N);
+    const float c2 = row_sum<kLanes>(s1, nullptr) / static_cast<float>(N);
     if (!live) continue;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const int64_t n = static_cast<int64_t>(lane + i * kLanes) * W;
-      if (n >= N) continue;
-      Pack<T, W> o;
+      const int c = (lane + i * kLanes) * W;
+      if (c >= N) continue;
 #pragma unroll
-      for (int k = 0; k < W; ++k) o.v[k] = from_float<T>(cr * (gv[i * W + k] - c1 - h[i * W + k] * c2));
-      store_pack<T, W>(static_cast<T*>(a.gx) + m * N + n, o);
+      for (int k = 0; k < W; ++k) g[i * W + k] = cr * (g[i * W + k] - c1 - h[i * W + k] * c2);
+      store_floats<T, W>(static_cast<T*>(a.gx) + m * N + c, g + i * W);
     }
   }
   if (a.partial == nullptr) return;
@@ -357,197 +619,317 @@ __global__ void __launch_bounds__(256) norm_backward_short_kernel(const Backward
   }
 }
 
-// Longer rows: a block per row slice of up to kLanes * 16 columns, a cluster
-// of blocks per row when one does not cover it.  Every block walks over rows
-// in turn; bulk copies bring the x and g slices of the next rows into a ring
-// of shared-memory stages while this row is worked on; each thread keeps the
-// gradient sums of its 16 columns in registers over all its rows.  Rows that
-// do not start on 16 bytes are copied from the boundary below them and read
-// element by element.
-constexpr int kElems = 16;
-constexpr int kMaxStages = 8;
+// Sums kN values over a warp with kN - 1 + 5 - log2(kN) shuffles: each step
+// halves the values a lane carries before it halves the lanes.  Value v's sum
+// ends in the lanes with lane / (32 / kN) == v.
+template <int kN>
+__device__ __forceinline__ float warp_sums(float (&v)[kN]) {
+  const int lane = threadIdx.x & 31;
+  int n = kN;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+#pragma unroll
+      for (int i = 0; i < kN / 2; ++i) {
+        if (i >= n) break;
+        const bool upper = (lane & o) != 0;
+        const float send = upper ? v[i] : v[i + n];
+        v[i] = (upper ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, send, o);
+      }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
+  }
+  return v[0];
+}
 
-struct RingLayout {
-  int cols;         // columns per block
-  int slot_bytes;   // bytes of one slice in a stage
-  int stages;
-};
-
-template <typename T, int W, int kLanes>
-__global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kernel(const BackwardArgs a, const RingLayout L) {
-  extern __shared__ __align__(128) uint8_t ring[];
+// Rows of up to 8192 elements through the ring, a block per row: 16 elements
+// in each thread's registers, with w and the gradient sums of their columns
+// over all the block's rows.  kFull: the threads' packs cover the row exactly.
+template <typename T, int W, int kLanes, int kE, bool kFull>
+__global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kernel(const BackwardArgs a,
+                                                                                 const RingLayout L) {
+  extern __shared__ __align__(128) uint8_t stages[];
+  constexpr int kWarps = kLanes / 32, kVec = kE / W;
   __shared__ uint64_t full[kMaxStages];
-  __shared__ __align__(16) float scratch[2][2 * (kLanes / 32)];
-  __shared__ float2 peer[2][8];    // the cluster's slice sums of a row, by rank
+  __shared__ __align__(16) float2 scratch[2][kWarps];
   __shared__ int abort_flag;
-  constexpr int kVec = kElems / W;
-  const int tid = threadIdx.x;
-  const int ranks = static_cast<int>(gridDim.y), rank = static_cast<int>(blockIdx.y);
-  const int64_t N = a.N, n0 = static_cast<int64_t>(rank) * L.cols;
-  const int cols = static_cast<int>(min(static_cast<int64_t>(L.cols), N - n0));
-  const int64_t row_step = gridDim.x;
-  const int64_t rows = blockIdx.x < a.M ? (a.M - blockIdx.x + row_step - 1) / row_step : 0;
+  const int tid = threadIdx.x, cols = kFull ? kLanes * kE : L.cols;
+  Ring<T, 2> ring{{static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.g)},
+                  stages, full, L, a.N, 0, gridDim.x,
+                  (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
+                  static_cast<unsigned long long>(a.M) * a.N * sizeof(T), cols};
+  const int rows = static_cast<int>(ring.rows);
   if (tid == 0) {
-    for (int i = 0; i < L.stages; ++i) mbar_init(&full[i], 1);
-    abort_flag = 0;
-    fence_mbar_init();
-    if (blockIdx.x == 0 && rank == 0) *a.st = DevStatus{0, 0, 0, 0};
+    ring_setup(full, L.stages, &abort_flag);
+    if (blockIdx.x == 0) *a.st = DevStatus{0, 0, 0, 0};
+    for (int i = 0; i < static_cast<int>(L.stages) && i < rows; ++i) ring.issue(i);
   }
   __syncthreads();
 
-  // Slice of row number i (of this block's rows): the bytes from the 16-byte
-  // boundary below it to the one above its end, or below where that would be
-  // past the end of the matrix; the elements not covered are read directly.
-  using u64 = unsigned long long;
-  const u64 end_bytes = static_cast<u64>(a.M) * N * sizeof(T);
-  auto start_byte = [&](int64_t i) {
-    return static_cast<u64>(((blockIdx.x + i * row_step) * N + n0) * static_cast<int64_t>(sizeof(T)));
-  };
-  auto slice_end = [&](u64 b) { return min((b + cols * sizeof(T) + 15ull) & ~15ull, end_bytes & ~15ull); };
-  auto issue = [&](int64_t i) {   // thread 0
-    const u64 b = start_byte(i), lo = b & ~15ull, hi = slice_end(b);
-    const uint32_t bytes = hi > lo ? static_cast<uint32_t>(hi - lo) : 0u;
-    const int s = static_cast<int>(i % L.stages);
-    uint8_t* slot = ring + static_cast<size_t>(s) * 2 * L.slot_bytes;
-    mbar_arrive_expect_tx(&full[s], 2 * bytes);
-    if (bytes != 0) {
-      bulk_load(slot, static_cast<const uint8_t*>(a.x) + lo, bytes, &full[s]);
-      bulk_load(slot + L.slot_bytes, static_cast<const uint8_t*>(a.g) + lo, bytes, &full[s]);
-    }
-  };
-  if (tid == 0)
-    for (int64_t i = 0; i < L.stages && i < rows; ++i) issue(i);
-
-  float w[kElems], aw[kElems], ab[kElems];
+  float w[kE], aw[kE], ab[kE];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int c = (tid + i * kLanes) * W;
-    float q[W];
 #pragma unroll
-    for (int k = 0; k < W; ++k) q[k] = c < cols ? 1.f : 0.f;
-    if (a.w != nullptr && c < cols) load_param<W>(a.w, a.wt, n0 + c, q);
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      w[i * W + k] = q[k];
-      aw[i * W + k] = ab[i * W + k] = 0.f;
-    }
+    for (int k = 0; k < W; ++k) w[i * W + k] = aw[i * W + k] = ab[i * W + k] = 0.f;
+    if (kFull || c < cols) load_param<W>(a.w, a.wt, c, 1.f, w + i * W);
   }
-
-  const float inv_n = 1.0f / static_cast<float>(N);
-  float mu = 0.f, r = 0.f;
-  if (rows > 0) {
-    mu = a.mean[blockIdx.x];
-    r = a.rstd[blockIdx.x];
-  }
-  int s = 0;
+  const float inv_n = 1.0f / static_cast<float>(a.N);
+  const bool want_x = a.gx != nullptr;
+  const float *mean = a.mean + blockIdx.x, *rstd = a.rstd + blockIdx.x;
+  T* out = static_cast<T*>(a.gx) + (want_x ? blockIdx.x * a.N : 0);
+  float mu = mean[0], r = rstd[0];
+  unsigned s = 0;
   uint32_t phase = 0;
-  for (int64_t i = 0; i < rows; ++i) {
-    const int64_t m = blockIdx.x + i * row_step;
+  for (int i = 0; i < rows; ++i) {
     const float cmu = mu, cr = r;
     if (i + 1 < rows) {
-      mu = a.mean[m + row_step];
-      r = a.rstd[m + row_step];
+      mean += gridDim.x;
+      rstd += gridDim.x;
+      mu = *mean;
+      r = *rstd;
     }
     mbar_wait(&full[s], phase, &abort_flag, a.st, 30);
-    const u64 b = start_byte(i);
-    const uint8_t* xs = ring + static_cast<size_t>(s) * 2 * L.slot_bytes + (b & 15);
-    const uint8_t* gs = xs + L.slot_bytes;
-    float h[kElems], gv[kElems];
-    const int have = W == 1 ? static_cast<int>((slice_end(b) - min(slice_end(b), b)) / sizeof(T)) : cols;
+    float h[kE], g[kE], t0 = 0.f, t1 = 0.f;
+    Slice<T> xs, gs;
+    if constexpr (W == 1) {
+      xs = slice_of<T, W>(ring, 0, i, s);
+      gs = slice_of<T, W>(ring, 1, i, s);
+    } else {
+      xs.near = reinterpret_cast<const T*>(stages + 2 * s * L.slot_bytes);
+      gs.near = reinterpret_cast<const T*>(stages + (2 * s + 1) * L.slot_bytes);
+    }
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
-      const int c = (tid + v * kLanes) * W;
-      Pack<T, W> px, pg;
-      if (c < cols) {
-        if (W == 1 && c >= have) {   // the last elements of the matrix
-          px.v[0] = static_cast<const T*>(a.x)[m * N + n0 + c];
-          pg.v[0] = static_cast<const T*>(a.g)[m * N + n0 + c];
-        } else {
-          px = load_pack<T, W>(reinterpret_cast<const T*>(xs) + c);
-          pg = load_pack<T, W>(reinterpret_cast<const T*>(gs) + c);
-        }
-      }
+    for (int e = 0; e < kVec; ++e) {
+      const int c = (tid + e * kLanes) * W;
+      read<T, W>(xs, c, kFull ? c + 1 : cols, h + e * W);
+      read<T, W>(gs, c, kFull ? c + 1 : cols, g + e * W);
 #pragma unroll
-      for (int k = 0; k < W; ++k) {
-        h[v * W + k] = c < cols ? (to_float(px.v[k]) - cmu) * cr : 0.f;
-        gv[v * W + k] = c < cols ? to_float(pg.v[k]) : 0.f;
+      for (int k = e * W; k < (e + 1) * W; ++k) {
+        h[k] = (h[k] - cmu) * cr;
+        aw[k] += g[k] * h[k];
+        ab[k] += g[k];
+        g[k] *= w[k];
+        t0 += g[k];
+        t1 += g[k] * h[k];
       }
     }
-    float t[2] = {0.f, 0.f};
-#pragma unroll
-    for (int e = 0; e < kElems; ++e) {
-      aw[e] += gv[e] * h[e];
-      ab[e] += gv[e];
-      gv[e] *= w[e];
-      t[0] += gv[e];
-      t[1] += gv[e] * h[e];
-    }
-    row_sum<kLanes, 2>(t, scratch[i & 1]);   // its barrier: every thread has read the stage
-    if (tid == 0 && i + L.stages < rows) issue(i + L.stages);
+    float v[2] = {t0, t1};
+    const float t = warp_sums<2>(v);
+    if ((tid & 15) == 0) reinterpret_cast<float*>(&scratch[i & 1][tid >> 5])[(tid >> 4) & 1] = t;
+    __syncthreads();   // every thread has read the stage
+    if (tid == 0 && i + static_cast<int>(L.stages) < rows) ring.issue(i + L.stages);
     if (++s == L.stages) {
       s = 0;
       phase ^= 1;
     }
-    if (a.gx == nullptr) continue;
-    if (ranks > 1) {
-      // each block sends its sums to all, and adds them in the order of the ranks
-      if (tid < ranks) {
-        const uint32_t dst = mapa_shared(&peer[i & 1][rank], tid);
-        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(t[0]), "f"(t[1]) : "memory");
-      }
-      cluster_sync();
-      t[0] = t[1] = 0.f;
-      for (int q = 0; q < ranks; ++q) {
-        t[0] += peer[i & 1][q].x;
-        t[1] += peer[i & 1][q].y;
+    if (!want_x) continue;
+    t0 = t1 = 0.f;
+    if constexpr (kWarps == 2) {
+      t0 = scratch[i & 1][0].x + scratch[i & 1][1].x;
+      t1 = scratch[i & 1][0].y + scratch[i & 1][1].y;
+    } else {
+#pragma unroll
+      for (int k = 0; k < kWarps; k += 2) {
+        const float4 q = *reinterpret_cast<const float4*>(&scratch[i & 1][k]);
+        t0 += q.x + q.z;
+        t1 += q.y + q.w;
       }
     }
-    const float c1 = t[0] * inv_n, c2 = t[1] * inv_n;
-    T* gx = static_cast<T*>(a.gx) + m * N + n0;
+    const float c1 = -cr * (t0 * inv_n), c2 = -cr * (t1 * inv_n);
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
-      const int c = (tid + v * kLanes) * W;
-      if (c >= cols) continue;
-      Pack<T, W> o;
+    for (int e = 0; e < kVec; ++e) {
+      const int c = (tid + e * kLanes) * W;
 #pragma unroll
-      for (int k = 0; k < W; ++k) o.v[k] = from_float<T>(cr * (gv[v * W + k] - c1 - h[v * W + k] * c2));
-      store_pack<T, W>(gx + c, o);
+      for (int k = e * W; k < (e + 1) * W; ++k) g[k] = fmaf(h[k], c2, fmaf(g[k], cr, c1));
+      if (kFull || c < cols) store_floats<T, W>(out + c, g + e * W);
+    }
+    out += gridDim.x * a.N;
+  }
+  if (a.partial == nullptr) return;
+  float* pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.N;
+  float* pb = pw + static_cast<int64_t>(gridDim.x) * a.N;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int c = (tid + i * kLanes) * W;
+    if (!kFull && c >= cols) continue;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      pw[c + k] = aw[i * W + k];
+      pb[c + k] = ab[i * W + k];
     }
   }
-  if (ranks > 1 && a.gx != nullptr) cluster_sync();   // no block leaves while a peer may write to it
-  if (a.partial == nullptr) return;
-  float* pw = a.partial + static_cast<int64_t>(blockIdx.x) * N + n0;
-  float* pb = pw + static_cast<int64_t>(gridDim.x) * N;
+}
+
+// Longer rows: a cluster of blocks per row, each on a slice of it.  kRows
+// rows are worked on between two barriers: their stages are read twice, for
+// the rows' two sums and for gx, so that registers hold only w and the
+// gradient sums of the thread's columns.  The blocks send each other their
+// sums without waiting: gx follows one step later.
+template <typename T, int W, int kLanes, int kE, int kRows>
+__global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_kernel(const BackwardArgs a,
+                                                                                 const RingLayout L) {
+  extern __shared__ __align__(128) uint8_t stages[];
+  constexpr int kWarps = kLanes / 32, kVec = kE / W, kSums = 2 * kRows;
+  __shared__ uint64_t full[kMaxStages], sent[4];
+  __shared__ float scratch[2][kSums][kWarps];
+  __shared__ __align__(16) float peer[4][8][kSums];   // the cluster's slice sums of a step, by rank
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ranks = static_cast<int>(gridDim.y), rank = static_cast<int>(blockIdx.y);
+  const int64_t n0 = static_cast<int64_t>(rank) * L.cols;
+  const int cols = static_cast<int>(min(static_cast<int64_t>(L.cols), a.N - n0));
+  Ring<T, 2> ring{{static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.g)},
+                  stages, full, L, a.N, n0, gridDim.x,
+                  (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
+                  static_cast<unsigned long long>(a.M) * a.N * sizeof(T), cols};
+  const int64_t rows = ring.rows, steps = (rows + kRows - 1) / kRows;
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) mbar_init(&sent[i], 1);
+    ring_setup(full, L.stages, &abort_flag);
+    if (blockIdx.x == 0 && rank == 0) *a.st = DevStatus{0, 0, 0, 0};
+    for (int64_t i = 0; i < L.stages && i < rows; ++i) ring.issue(i);
+  }
+  __syncthreads();
+  if (ranks > 1) cluster_sync();   // the peers' barriers are ready
+
+  float w[kE], aw[kE], ab[kE];
 #pragma unroll
-  for (int v = 0; v < kVec; ++v) {
-    const int c = (tid + v * kLanes) * W;
+  for (int i = 0; i < kVec; ++i) {
+    const int c = (tid + i * kLanes) * W;
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[i * W + k] = aw[i * W + k] = ab[i * W + k] = 0.f;
+    if (c < cols) load_param<W>(a.w, a.wt, n0 + c, 1.f, w + i * W);
+  }
+  const float inv_n = 1.0f / static_cast<float>(a.N);
+  const bool want_x = a.gx != nullptr;
+  const int lag = ranks > 1 && want_x ? 1 : 0;
+  for (int64_t i = 0; i < steps + lag; ++i) {
+    if (i < steps) {
+      float sums[kSums];
+#pragma unroll
+      for (int q = 0; q < kRows; ++q) {
+        sums[2 * q] = sums[2 * q + 1] = 0.f;
+        const int64_t row = i * kRows + q;
+        if (row >= rows) continue;
+        const int s = static_cast<int>(static_cast<unsigned>(row) % L.stages);
+        mbar_wait(&full[s], static_cast<unsigned>(row) / L.stages & 1, &abort_flag, a.st, 30);
+        if (!want_x) continue;
+        const float mu = __ldg(a.mean + ring.row(row)), r = __ldg(a.rstd + ring.row(row));
+        const Slice<T> xs = slice_of<T, W>(ring, 0, row, s), gs = slice_of<T, W>(ring, 1, row, s);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          float x[W], g[W];
+          read<T, W>(xs, (tid + e * kLanes) * W, cols, x);
+          read<T, W>(gs, (tid + e * kLanes) * W, cols, g);
+#pragma unroll
+          for (int k = 0; k < W; ++k) {
+            g[k] *= w[e * W + k];
+            sums[2 * q] += g[k];
+            sums[2 * q + 1] += g[k] * (x[k] - mu);
+          }
+        }
+        sums[2 * q + 1] *= r;
+      }
+      if (want_x) {
+        const float t = warp_sums<kSums>(sums);
+        if ((lane & (32 / kSums - 1)) == 0) scratch[i & 1][lane / (32 / kSums)][warp] = t;
+      }
+    }
+    __syncthreads();
+    // every thread is done with the rows of step i - 1 - lag
+    if (tid == 0 && i > lag)
+      for (int q = 0; q < kRows; ++q) {
+        const int64_t next = (i - 1 - lag) * kRows + q + L.stages;
+        if (next < rows) ring.issue(next);
+      }
+    // The totals of a step: value v in the lanes with lane / (32 / kSums) == v.
+    float total = 0.f;
+    const int v = lane / (32 / kSums), sub = lane & (32 / kSums - 1);
+    if (want_x && i < steps) {
+      for (int k = sub; k < kWarps; k += 32 / kSums) total += scratch[i & 1][v][k];
+#pragma unroll
+      for (int o = 16 / kSums; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (lag != 0 && i < steps && warp == 0) {
+      if (lane == 0) mbar_arrive_expect_tx(&sent[i & 3], 4u * kSums * ranks);
+      // lane group v sends value v, lane `sub` of it to rank sub
+      if (sub < ranks)
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                         mapa_shared(&peer[i & 3][rank][v], sub)),
+                     "r"(__float_as_uint(total)), "r"(mapa_shared(&sent[i & 3], sub))
+                     : "memory");
+    }
+    const int64_t j = i - lag;
+    if (j < 0) continue;
+    if (lag != 0) {
+      mbar_wait(&sent[j & 3], static_cast<uint32_t>(j >> 2) & 1, &abort_flag, a.st, 32);
+      total = 0.f;
+      for (int k = 0; k < ranks; ++k) total += peer[j & 3][k][v];
+    }
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+      const int64_t row = j * kRows + q;
+      if (row >= rows) break;
+      const int s = static_cast<int>(static_cast<unsigned>(row) % L.stages);
+      const float mu = __ldg(a.mean + ring.row(row)), r = __ldg(a.rstd + ring.row(row));
+      const float c1 = -r * inv_n * __shfl_sync(0xffffffffu, total, 2 * q * (32 / kSums));
+      const float c2 = -r * inv_n * __shfl_sync(0xffffffffu, total, (2 * q + 1) * (32 / kSums));
+      const Slice<T> xs = slice_of<T, W>(ring, 0, row, s), gs = slice_of<T, W>(ring, 1, row, s);
+      T* out = static_cast<T*>(a.gx) + ring.row(row) * a.N + n0;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const int c = (tid + e * kLanes) * W;
+        float x[W], g[W];
+        read<T, W>(xs, c, cols, x);
+        read<T, W>(gs, c, cols, g);
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          x[k] = (x[k] - mu) * r;
+          aw[e * W + k] += g[k] * x[k];
+          ab[e * W + k] += g[k];
+          g[k] = fmaf(x[k], c2, fmaf(g[k] * w[e * W + k], r, c1));
+        }
+        if (want_x && c < cols) store_floats<T, W>(out + c, g);
+      }
+    }
+  }
+  if (ranks > 1) cluster_sync();   // no block leaves while a peer may write to it
+  if (a.partial == nullptr) return;
+  float* pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.N + n0;
+  float* pb = pw + static_cast<int64_t>(gridDim.x) * a.N;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int c = (tid + i * kLanes) * W;
     if (c >= cols) continue;
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-      pw[c + k] = aw[v * W + k];
-      pb[c + k] = ab[v * W + k];
+      pw[c + k] = aw[i * W + k];
+      pb[c + k] = ab[i * W + k];
     }
   }
 }
 
 // Rows beyond a cluster's reach: passes over global memory.
 template <typename T>
-__global__ void __launch_bounds__(kLongThreads) norm_backward_long_kernel(const BackwardArgs a) {
-  __shared__ __align__(16) float scratch[2 * (kLongThreads / 32)];
+__global__ void __launch_bounds__(kWideThreads) norm_backward_long_kernel(const BackwardArgs a) {
+  __shared__ __align__(16) float scratch[2][kWideThreads / 32];
   const int64_t m = blockIdx.x, N = a.N;
   const T* g = static_cast<const T*>(a.g) + m * N;
   const T* x = static_cast<const T*>(a.x) + m * N;
   T* gx = static_cast<T*>(a.gx) + m * N;
   const float mu = a.mean[m], r = a.rstd[m];
-  float s[2] = {0.f, 0.f};
-  for (int64_t n = threadIdx.x; n < N; n += kLongThreads) {
+  float s0 = 0.f, s1 = 0.f;
+  for (int64_t n = threadIdx.x; n < N; n += kWideThreads) {
     const float gw = to_float(g[n]) * (a.w != nullptr ? load_any(a.w, a.wt, n) : 1.f);
-    s[0] += gw;
-    s[1] += gw * ((to_float(x[n]) - mu) * r);
+    s0 += gw;
+    s1 += gw * ((to_float(x[n]) - mu) * r);
   }
-  row_sum<kLongThreads, 2>(s, scratch);
-  const float c1 = s[0] / static_cast<float>(N), c2 = s[1] / static_cast<float>(N);
-  for (int64_t n = threadIdx.x; n < N; n += kLongThreads) {
+  const float c1 = row_sum<kWideThreads>(s0, scratch[0]) / static_cast<float>(N);
+  const float c2 = row_sum<kWideThreads>(s1, scratch[1]) / static_cast<float>(N);
+  for (int64_t n = threadIdx.x; n < N; n += kWideThreads) {
     const float gw = to_float(g[n]) * (a.w != nullptr ? load_any(a.w, a.wt, n) : 1.f);
     gx[n] = from_float<T>(r * (gw - c1 - ((to_float(x[n]) - mu) * r) * c2));
   }
@@ -591,18 +973,10 @@ __global__ void __launch_bounds__(1024) norm_grad_sum_kernel(const float* partia
   if (lane == 0 && col < N) store_any(out, wt, col, s);
 }
 
-constexpr int kShortRow = 512;         // columns up to which a warp takes a row
-constexpr int kSliceCols = 8192;       // columns a block of the ring kernel covers
+constexpr int kShortRow = 256;         // columns up to which a warp takes a row
+constexpr int kSliceCols = 8192;       // largest slice of a row per block of the ring kernel
 constexpr int kMaxCluster = 8;
-constexpr int kRingBytes = 200 * 1024; // shared memory per SM given to the ring
 constexpr int kMaxBlocks = 1216;       // eight blocks of each of 152 SMs
-
-int sm_count() {
-  int dev = 0, sms = 152;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
 
 // Rows of partial sums the workspace has room for.
 int64_t partial_rows(int64_t M, int64_t N) {
@@ -617,9 +991,9 @@ struct Shape {
   cudaStream_t s;
 };
 
-template <typename T, int W, int kLanes, int kVec>
+template <typename T, int W, int kLanes>
 cudaError_t launch_short(Shape& h) {
-  auto kernel = norm_backward_short_kernel<T, W, kLanes, kVec>;
+  auto kernel = norm_backward_short_kernel<T, W, kLanes>;
   const int per_sm = std::min(4, cached_blocks_per_sm(reinterpret_cast<const void*>(kernel), 256, 0));
   h.blocks = static_cast<int>(std::min<int64_t>(
       {ceil_div(h.a.M, 256 / kLanes), static_cast<int64_t>(h.sms) * per_sm, partial_rows(h.a.M, h.a.N)}));
@@ -628,24 +1002,56 @@ cudaError_t launch_short(Shape& h) {
   return cudaGetLastError();
 }
 
-template <typename T, int W, int kLanes>
+template <typename T, int W, int kLanes, int kE>
 cudaError_t launch_ring(Shape& h) {
-  auto kernel = norm_backward_ring_kernel<T, W, kLanes>;
-  const int64_t N = h.a.N;
-  RingLayout L;
-  const int ranks = static_cast<int>(ceil_div(N, kSliceCols));
-  // slices start on 16 bytes of an aligned row
-  L.cols = static_cast<int>(round_up(ceil_div(N, ranks), 8));
-  L.slot_bytes = static_cast<int>(round_up(L.cols * static_cast<int64_t>(sizeof(T)) + 16, 128));
-  const int per_sm = 512 / kLanes;
-  L.stages = std::min(kMaxStages, kRingBytes / per_sm / (2 * L.slot_bytes));
-  const int smem = L.stages * 2 * L.slot_bytes;
+  constexpr int per_sm = 512 / kLanes;
+  const RingLayout L = ring_layout(h.a.N, sizeof(T), 2, per_sm);
+  auto kernel = W > 1 && h.a.N == kLanes * kE ? norm_backward_ring_kernel<T, W, kLanes, kE, W != 1>
+                                              : norm_backward_ring_kernel<T, W, kLanes, kE, false>;
+  const int smem = static_cast<int>(L.stages) * 2 * L.slot_bytes;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
-  const int64_t resident = std::max(1, h.sms * per_sm / ranks);
-  h.blocks = static_cast<int>(std::min<int64_t>({h.a.M, resident, partial_rows(h.a.M, N)}));
+  h.blocks = static_cast<int>(
+      std::min<int64_t>({h.a.M, static_cast<int64_t>(h.sms) * per_sm, partial_rows(h.a.M, h.a.N)}));
+  ProfScope ps(K_LAYER_NORM_BWD, h.s);
+  kernel<<<h.blocks, kLanes, smem, h.s>>>(h.a, L);
+  return cudaGetLastError();
+}
+
+// Clusters of a kernel resident at once, asked for once per (kernel, device,
+// shared memory, cluster size).
+template <typename Query>
+int cached_clusters(const void* fn, int smem, int ranks, Query query) {
+  struct Entry {
+    const void* fn;
+    int dev, smem, ranks, n;
+  };
+  static Entry cache[64];
+  static int used = 0;
+  static std::mutex mu;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < used; ++i)
+    if (cache[i].fn == fn && cache[i].dev == dev && cache[i].smem == smem && cache[i].ranks == ranks)
+      return cache[i].n;
+  const int n = query();
+  if (n == 0) cudaGetLastError();
+  if (used < 64) cache[used++] = Entry{fn, dev, smem, ranks, n};
+  return n;
+}
+
+// Two rows per step where the ring holds the rows of a step, of the one
+// before it and of the next.
+template <typename T, int W>
+cudaError_t launch_cluster(Shape& h, int ranks, int cols) {
+  const RingLayout L = ring_layout(cols, sizeof(T), 2, 1);
+  auto kernel = L.stages >= 6u ? norm_backward_cluster_kernel<T, W, 512, 16, 2>
+                               : norm_backward_cluster_kernel<T, W, 512, 16, 1>;
+  const int smem = static_cast<int>(L.stages) * 2 * L.slot_bytes;
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(h.blocks), static_cast<unsigned>(ranks));
-  cfg.blockDim = dim3(kLanes);
+  cfg.gridDim = dim3(1, static_cast<unsigned>(ranks));
+  cfg.blockDim = dim3(512);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = h.s;
   cudaLaunchAttribute attr[1];
@@ -655,6 +1061,19 @@ cudaError_t launch_ring(Shape& h) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  // as many clusters as fit at once (a processor group whose SMs are no
+  // multiple of the cluster leaves some idle): one more would wait for a
+  // whole pass of the others
+  const int resident = cached_clusters(reinterpret_cast<const void*>(kernel), smem, ranks, [&] {
+    int n = 0;
+    cudaLaunchConfig_t q = cfg;
+    q.gridDim.x = static_cast<unsigned>(std::max(1, h.sms / ranks));
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &q) == cudaSuccess ? n : 0;
+  });
+  h.blocks = static_cast<int>(
+      std::min<int64_t>({h.a.M, static_cast<int64_t>(std::max(1, std::min(resident, h.sms / ranks))),
+                         partial_rows(h.a.M, h.a.N)}));
+  cfg.gridDim.x = static_cast<unsigned>(h.blocks);
   ProfScope ps(K_LAYER_NORM_BWD, h.s);
   return cudaLaunchKernelEx(&cfg, kernel, h.a, L);
 }
@@ -662,16 +1081,22 @@ cudaError_t launch_ring(Shape& h) {
 template <typename T, int W>
 cudaError_t backward_sized(Shape& h) {
   const int64_t N = h.a.N;
-  if (N <= 64) return launch_short<T, W, 8, 8 / W>(h);
-  if (N <= 256) return launch_short<T, W, 32, 8 / W>(h);
-  if (N <= kShortRow) return launch_short<T, W, 32, 16 / W>(h);
-  if (N <= 1024) return launch_ring<T, W, 64>(h);
-  if (N <= 2048) return launch_ring<T, W, 128>(h);
-  if (N <= 4096) return launch_ring<T, W, 256>(h);
-  if (N <= static_cast<int64_t>(kSliceCols) * kMaxCluster) return launch_ring<T, W, 512>(h);
+  if (N <= 64) return launch_short<T, W, 8>(h);
+  if (N <= kShortRow) return launch_short<T, W, 32>(h);
+  if (N <= 512) return launch_ring<T, W, 64, 8>(h);
+  if (N <= 1024) return launch_ring<T, W, 64, 16>(h);
+  if (N <= 2048) return launch_ring<T, W, 128, 16>(h);
+  if (N <= 4096) return launch_ring<T, W, 256, 16>(h);
+  if (N <= kSliceCols) return launch_ring<T, W, 512, 16>(h);
+  const int64_t ranks = ceil_div(N, kSliceCols);
+  if (ranks <= kMaxCluster) {
+    // slices of 8 columns' multiples start on 16 bytes of an aligned row
+    const int64_t cols = round_up(ceil_div(N, ranks), 8);
+    return launch_cluster<T, W>(h, static_cast<int>(ceil_div(N, cols)), static_cast<int>(cols));
+  }
   if (h.a.gx != nullptr) {
     ProfScope ps(K_LAYER_NORM_BWD, h.s);
-    norm_backward_long_kernel<T><<<static_cast<unsigned>(h.a.M), kLongThreads, 0, h.s>>>(h.a);
+    norm_backward_long_kernel<T><<<static_cast<unsigned>(h.a.M), kWideThreads, 0, h.s>>>(h.a);
     if (cudaError_t e = cudaGetLastError()) return e;
   }
   if (h.a.partial == nullptr) return cudaSuccess;
