@@ -69,8 +69,60 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-__device__ __forceinline__ float e4m3_float(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+// 4 consecutive elements: one access when `whole` (they exist and are aligned
+// to their size together), else the first `valid` one by one.
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, bool whole, int valid, float (&f)[4]) {
+  if (whole) {
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(p);
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      const T* q = reinterpret_cast<const T*>(&u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = to_float(q[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = i < valid ? to_float(p[i]) : 0.f;
+  }
+}
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, __half*) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, __nv_bfloat16*) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, bool whole, int valid, const float (&f)[4]) {
+  if (whole) {
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    else
+      *reinterpret_cast<uint2*>(p) = make_uint2(pack16(f[0], f[1], p), pack16(f[2], f[3], p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < valid) p[i] = from_float<T>(f[i]);
+  }
+}
+
+// 4 E4M3 codes to their values (exact in fp16) and back (nearest even).
+__device__ __forceinline__ void decode4(uint32_t c, float d, float (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2 h(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c >> (16 * i)), __NV_E4M3));
+    const float2 v = __half22float2(h);
+    f[2 * i] = __fmul_rn(v.x, d);
+    f[2 * i + 1] = __fmul_rn(v.y, d);
+  }
+}
+__device__ __forceinline__ uint32_t encode4(const float (&f)[4]) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
 }
 
 // 448 / absmax as the product with the rounded reciprocal.  A block whose
@@ -80,76 +132,102 @@ __device__ __forceinline__ float code_scale(float top) {
   return top >= 0x1p-100f ? __fmul_rn(kE4M3Max, __frcp_rn(top)) : 0.f;
 }
 
-// The moments after this step's gradient, then the parameter.
+// The moments after this step's gradient, then the parameter.  The
+// parameter's division is the fast one (2 ulp of the update).
 __device__ __forceinline__ void moments(const Hyper& h, float g, float& m, float& v) {
   m = __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.c1));
   v = __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, g), h.c2));
 }
 __device__ __forceinline__ float updated(const Hyper& h, float p, float m, float r) {
-  return __fsub_rn(__fmul_rn(p, h.keep), __fdiv_rn(__fmul_rn(m, h.size), __fadd_rn(__fmul_rn(r, h.root), h.eps)));
+  return fmaf(p, h.keep, -__fdividef(m * h.size, fmaf(r, h.root, h.eps)));
 }
 
-// One warp per block of 256 elements, lane l on elements l, l + 32, ...
+// One warp per block of 256 elements, lane l on the elements 4 l .. 4 l + 3
+// and 128 more on: every access of a warp is one run of memory, and the
+// block's absmax is a reduction over the warp's registers.  A warp takes
+// kPerWarp blocks in turn, so that the search for its tensor is paid once.
+// Bound by HBM: the tensors and states are read and written once.
+constexpr int kPerWarp = 4;
 template <int kCap, typename P, typename G, bool k8>
 __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constant__ TensorList<kCap> L,
                                                             const __grid_constant__ Hyper h, void* mv, void* rv,
                                                             float* m_top, float* r_top) {
-  const int b = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (b >= L.first[L.count]) return;
+  int b = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kPerWarp;
+  const int end = min(b + kPerWarp, L.first[L.count]);
+  if (b >= end) return;
   if (h.found_inf != nullptr && *h.found_inf != 0.f) return;
   const float gs = h.grad_scale != nullptr ? *h.grad_scale : 1.f;
-  const int t = find_tensor(L, b);
-  if (L.g[t] == nullptr) return;   // no gradient: the tensor and its states stay
-  const int64_t e0 = static_cast<int64_t>(b - L.first[t]) * kBlockElems;
-  const int valid = static_cast<int>(min(L.n[t] - e0, static_cast<int64_t>(kBlockElems)));
-  P* p = static_cast<P*>(L.p[t]) + e0;
-  const G* g = static_cast<const G*>(L.g[t]) + e0;
-  const int64_t sb = L.block0 + b, s0 = sb * kBlockElems;
-  float m[8], r[8];
-  float mt = 0.f, rt = 0.f;
-  const float md = k8 ? __fmul_rn(m_top[sb], 1.0f / kE4M3Max) : 0.f;
-  const float rd = k8 ? __fmul_rn(r_top[sb], 1.0f / kE4M3Max) : 0.f;
+  int t = find_tensor(L, b);
+  for (; b < end; ++b) {
+    while (b >= L.first[t + 1]) ++t;
+    const G* g = static_cast<const G*>(L.g[t]);
+    if (g == nullptr) continue;   // no gradient: the tensor and its states stay
+    const int64_t e0 = static_cast<int64_t>(b - L.first[t]) * kBlockElems;
+    const int valid = static_cast<int>(min(L.n[t] - e0, static_cast<int64_t>(kBlockElems)));
+    P* p = static_cast<P*>(L.p[t]) + e0;
+    g += e0;
+    const bool pw = (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(P) - 1)) == 0;
+    const bool gw = (reinterpret_cast<uintptr_t>(g) & (4 * sizeof(G) - 1)) == 0;
+    const int64_t sb = L.block0 + b, s0 = sb * kBlockElems;
+    float gv[2][4], pv[2][4], m[2][4], v[2][4];
+    const float md = k8 ? __fmul_rn(m_top[sb], 1.0f / kE4M3Max) : 0.f;
+    const float rd = k8 ? __fmul_rn(r_top[sb], 1.0f / kE4M3Max) : 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = lane + 32 * i;
-    m[i] = r[i] = 0.f;
-    if (e < valid) {
-      float v;
-      if (k8) {
-        m[i] = __fmul_rn(e4m3_float(static_cast<const uint8_t*>(mv)[s0 + e]), md);
-        const float r0 = __fmul_rn(e4m3_float(static_cast<const uint8_t*>(rv)[s0 + e]), rd);
-        v = __fmul_rn(r0, r0);
+    for (int i = 0; i < 2; ++i) {
+      const int e = 4 * (lane + 32 * i);
+      load4(g + e, gw && e + 4 <= valid, valid - e, gv[i]);
+      load4(p + e, pw && e + 4 <= valid, valid - e, pv[i]);
+      if constexpr (k8) {
+        decode4(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(mv) + s0 + e), md, m[i]);
+        decode4(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(rv) + s0 + e), rd, v[i]);
       } else {
-        m[i] = static_cast<const float*>(mv)[s0 + e];
-        v = static_cast<const float*>(rv)[s0 + e];
-      }
-      moments(h, __fmul_rn(to_float(g[e]), gs), m[i], v);
-      r[i] = __fsqrt_rn(v);
-      p[e] = from_float<P>(updated(h, to_float(p[e]), m[i], r[i]));
-      if (!k8) {
-        static_cast<float*>(mv)[s0 + e] = m[i];
-        static_cast<float*>(rv)[s0 + e] = v;
+        *reinterpret_cast<float4*>(m[i]) = *reinterpret_cast<const float4*>(static_cast<const float*>(mv) + s0 + e);
+        *reinterpret_cast<float4*>(v[i]) = *reinterpret_cast<const float4*>(static_cast<const float*>(rv) + s0 + e);
       }
     }
-    mt = fmaxf(mt, fabsf(m[i]));
-    rt = fmaxf(rt, r[i]);
-  }
-  if constexpr (k8) {
-    mt = warp_max(mt);
-    rt = warp_max(rt);
-    const float ms = code_scale(mt), rs = code_scale(rt);
-    if (lane == 0) {
-      m_top[sb] = mt;
-      r_top[sb] = rt;
-    }
+    float mt = 0.f, rt = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t e = s0 + lane + 32 * i;
-      static_cast<uint8_t*>(mv)[e] = __nv_cvt_float_to_fp8(__fmul_rn(m[i], ms), __NV_SATFINITE, __NV_E4M3);
-      float y = __fmul_rn(r[i], rs);
-      if (r[i] > 0.f) y = fmaxf(y, kE4M3Min);
-      static_cast<uint8_t*>(rv)[e] = __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 2; ++i) {
+      const int e = 4 * (lane + 32 * i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (k8) v[i][k] = __fmul_rn(v[i][k], v[i][k]);
+        moments(h, __fmul_rn(gv[i][k], gs), m[i][k], v[i][k]);
+        const float r = __fsqrt_rn(v[i][k]);
+        pv[i][k] = updated(h, pv[i][k], m[i][k], r);
+        if constexpr (k8) {
+          v[i][k] = r;
+          mt = fmaxf(mt, fabsf(m[i][k]));
+          rt = fmaxf(rt, r);
+        }
+      }
+      store4(p + e, pw && e + 4 <= valid, valid - e, pv[i]);
+      if constexpr (!k8) {
+        *reinterpret_cast<float4*>(static_cast<float*>(mv) + s0 + e) = *reinterpret_cast<const float4*>(m[i]);
+        *reinterpret_cast<float4*>(static_cast<float*>(rv) + s0 + e) = *reinterpret_cast<const float4*>(v[i]);
+      }
+    }
+    if constexpr (k8) {
+      mt = warp_max(mt);
+      rt = warp_max(rt);
+      const float ms = code_scale(mt), rs = code_scale(rt);
+      if (lane == 0) {
+        m_top[sb] = mt;
+        r_top[sb] = rt;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int e = 4 * (lane + 32 * i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          m[i][k] = __fmul_rn(m[i][k], ms);
+          const float y = __fmul_rn(v[i][k], rs);
+          v[i][k] = v[i][k] > 0.f ? fmaxf(y, kE4M3Min) : y;
+        }
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(mv) + s0 + e) = encode4(m[i]);
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(rv) + s0 + e) = encode4(v[i]);
+      }
     }
   }
 }
@@ -160,7 +238,7 @@ cudaError_t launch_list(const TensorList<kCap>& L, const Hyper& h, void* m, void
   const int blocks = L.first[L.count];
   if (blocks == 0) return cudaSuccess;
   ProfScope ps(K_ADAMW, s);
-  adamw_kernel<kCap, P, G, k8><<<static_cast<unsigned>(ceil_div(blocks, kWarps)), kWarps * 32, 0, s>>>(L, h, m, r, mt,
+  adamw_kernel<kCap, P, G, k8><<<static_cast<unsigned>(ceil_div(blocks, kWarps * kPerWarp)), kWarps * 32, 0, s>>>(L, h, m, r, mt,
                                                                                                       rt);
   return cudaGetLastError();
 }
