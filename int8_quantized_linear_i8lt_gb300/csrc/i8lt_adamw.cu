@@ -13,7 +13,9 @@
 // follow from the formulas alone.
 #include <cuda_fp8.h>
 
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "i8lt.h"
 #include "i8lt_internal.h"
@@ -50,8 +52,7 @@ constexpr int kFewTensors = 32;
 constexpr int kMaxTensors = 1024;
 static_assert(sizeof(TensorList<kMaxTensors>) + sizeof(Hyper) + 64 <= 32764, "kernel parameter space");
 
-// The tensor that holds block `b`: the last one whose first block is <= b
-// and that is not empty.
+// The tensor that holds block `b` (a list holds no empty tensors).
 template <int kCap>
 __device__ __forceinline__ int find_tensor(const TensorList<kCap>& L, int b) {
   int lo = 0, hi = L.count;   // first[lo] <= b < first[hi]
@@ -69,60 +70,87 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// 4 consecutive elements: one access when `whole` (they exist and are aligned
-// to their size together), else the first `valid` one by one.
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, bool whole, int valid, float (&f)[4]) {
+// N consecutive elements as fp32: 16-byte accesses when `whole` (they exist
+// and start on min(16, their size) bytes), else the first `valid` one by one.
+template <typename T, int N>
+struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Run {
+  T v[N];
+};
+template <typename T, int N>
+__device__ __forceinline__ Run<T, N> load_run(const T* p, bool whole, int valid) {
+  Run<T, N> r;
   if (whole) {
+    r = *reinterpret_cast<const Run<T, N>*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.v[i] = i < valid ? p[i] : from_float<T>(0.f);
+  }
+  return r;
+}
+template <typename T, int N>
+__device__ __forceinline__ void widen(const Run<T, N>& r, float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
     if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(p);
+      f[i] = r.v[i];
+      f[i + 1] = r.v[i + 1];
     } else {
-      const uint2 u = *reinterpret_cast<const uint2*>(p);
-      const T* q = reinterpret_cast<const T*>(&u);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = to_float(q[i]);
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(r.v + i);
+      if constexpr (std::is_same<T, __half>::value) {
+        const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&u));
+        f[i] = q.x;
+        f[i + 1] = q.y;
+      } else {
+        f[i] = __uint_as_float(u << 16);
+        f[i + 1] = __uint_as_float(u & 0xffff0000u);
+      }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = i < valid ? to_float(p[i]) : 0.f;
   }
 }
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, __half*) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, __nv_bfloat16*) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <typename T>
-__device__ __forceinline__ void store4(T* p, bool whole, int valid, const float (&f)[4]) {
+template <typename T, int N>
+__device__ __forceinline__ void store_run(T* p, bool whole, int valid, const float (&f)[N]) {
+  Run<T, N> r;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    if constexpr (sizeof(T) == 4) {
+      r.v[i] = f[i];
+      r.v[i + 1] = f[i + 1];
+    } else if constexpr (std::is_same<T, __half>::value) {
+      *reinterpret_cast<__half2*>(r.v + i) = __floats2half2_rn(f[i], f[i + 1]);
+    } else {
+      *reinterpret_cast<__nv_bfloat162*>(r.v + i) = __floats2bfloat162_rn(f[i], f[i + 1]);
+    }
+  }
   if (whole) {
-    if constexpr (sizeof(T) == 4)
-      *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    else
-      *reinterpret_cast<uint2*>(p) = make_uint2(pack16(f[0], f[1], p), pack16(f[2], f[3], p));
+    *reinterpret_cast<Run<T, N>*>(p) = r;
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < valid) p[i] = from_float<T>(f[i]);
+    for (int i = 0; i < N; ++i)
+      if (i < valid) p[i] = r.v[i];
   }
+}
+template <typename T, int N>
+__device__ __forceinline__ bool aligned_run(const T* p) {
+  return (reinterpret_cast<uintptr_t>(p) & (alignof(Run<T, N>) - 1)) == 0;
 }
 
-// 4 E4M3 codes to their values (exact in fp16) and back (nearest even).
-__device__ __forceinline__ void decode4(uint32_t c, float d, float (&f)[4]) {
+// 8 E4M3 codes to their values (exact in fp16) and back (nearest even).
+__device__ __forceinline__ void decode8(uint2 c, float d, float (&f)[8]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const __half2 h(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c >> (16 * i)), __NV_E4M3));
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = i < 2 ? c.x : c.y;
+    const __half2 h(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * (i & 1))), __NV_E4M3));
     const float2 v = __half22float2(h);
     f[2 * i] = __fmul_rn(v.x, d);
     f[2 * i + 1] = __fmul_rn(v.y, d);
   }
 }
-__device__ __forceinline__ uint32_t encode4(const float (&f)[4]) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
+__device__ __forceinline__ uint2 encode8(const float (&f)[8]) {
+  uint32_t q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    q[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i], f[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
 }
 
 // 448 / absmax as the product with the rounded reciprocal.  A block whose
@@ -132,104 +160,198 @@ __device__ __forceinline__ float code_scale(float top) {
   return top >= 0x1p-100f ? __fmul_rn(kE4M3Max, __frcp_rn(top)) : 0.f;
 }
 
-// The moments after this step's gradient, then the parameter.  The
-// parameter's division is the fast one (2 ulp of the update).
+// The correctly rounded square root of a v >= kRootMin: the approximate one
+// after one Newton step on the residual v - s^2, which an fma gives exactly.
+// (Equal to __fsqrt_rn for every significand; smaller v lose residual bits.)
+constexpr float kRootMin = 0x1p-90f;
+__device__ __forceinline__ float root_of(float v) {
+  float y;
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(v));
+  const float s = __fmul_rn(v, y);
+  return __fmaf_rn(__fmaf_rn(-s, s, v), __fmul_rn(0.5f, y), s);
+}
+
+// The moments after this step's gradient, then the parameter, whose division
+// is a product with the hardware's reciprocal (1 ulp; the update is a small
+// part of the parameter).
 __device__ __forceinline__ void moments(const Hyper& h, float g, float& m, float& v) {
   m = __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.c1));
   v = __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, g), h.c2));
 }
 __device__ __forceinline__ float updated(const Hyper& h, float p, float m, float r) {
-  return fmaf(p, h.keep, -__fdividef(m * h.size, fmaf(r, h.root, h.eps)));
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(r, h.root, h.eps)));
+  return fmaf(-(m * h.size), inv, p * h.keep);
 }
 
-// One warp per block of 256 elements, lane l on the elements 4 l .. 4 l + 3
-// and 128 more on: every access of a warp is one run of memory, and the
-// block's absmax is a reduction over the warp's registers.  A warp takes
-// kPerWarp blocks in turn, so that the search for its tensor is paid once.
-// Bound by HBM: the tensors and states are read and written once.
-constexpr int kPerWarp = 4;
-template <int kCap, typename P, typename G, bool k8>
+// The blocks [b, end) of a list, tensor by tensor: f(p, g, valid, blocks, state)
+// with the run's first block, its elements left in the tensor and its place in
+// the flat state.  Tensors without a gradient are left out.
+template <int kCap, typename P, typename G, typename F>
+__device__ __forceinline__ void each_run(const TensorList<kCap>& L, int b, int end, F f) {
+  for (int t = find_tensor(L, b); b < end; ++t) {
+    const int stop = min(end, L.first[t + 1]);
+    if (stop <= b) continue;
+    const int64_t e0 = static_cast<int64_t>(b - L.first[t]) * kBlockElems;
+    if (L.g[t] != nullptr)
+      f(static_cast<P*>(L.p[t]) + e0, static_cast<const G*>(L.g[t]) + e0, L.n[t] - e0, stop - b, L.block0 + b);
+    b = stop;
+  }
+}
+
+// 32-bit states.  One warp per block of 256 elements, lane l on the elements
+// 4 l .. 4 l + 3 and 128 more on: every access of a warp is one run of
+// memory.  A warp takes `per_warp` blocks in turn, so that the search for its
+// tensor is paid once.  Bound by HBM: 16 bytes of states, and the parameter
+// and gradient, read or written once.
+template <int kCap, typename P, typename G>
 __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constant__ TensorList<kCap> L,
-                                                            const __grid_constant__ Hyper h, void* mv, void* rv,
-                                                            float* m_top, float* r_top) {
+                                                            const __grid_constant__ Hyper h, float* mv, float* rv,
+                                                            int per_warp) {
   const int lane = threadIdx.x & 31;
-  int b = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kPerWarp;
-  const int end = min(b + kPerWarp, L.first[L.count]);
+  const int b = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * per_warp;
+  const int end = min(b + per_warp, L.first[L.count]);
   if (b >= end) return;
   if (h.found_inf != nullptr && *h.found_inf != 0.f) return;
   const float gs = h.grad_scale != nullptr ? *h.grad_scale : 1.f;
-  int t = find_tensor(L, b);
-  for (; b < end; ++b) {
-    while (b >= L.first[t + 1]) ++t;
-    const G* g = static_cast<const G*>(L.g[t]);
-    if (g == nullptr) continue;   // no gradient: the tensor and its states stay
-    const int64_t e0 = static_cast<int64_t>(b - L.first[t]) * kBlockElems;
-    const int valid = static_cast<int>(min(L.n[t] - e0, static_cast<int64_t>(kBlockElems)));
-    P* p = static_cast<P*>(L.p[t]) + e0;
-    g += e0;
-    const bool pw = (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(P) - 1)) == 0;
-    const bool gw = (reinterpret_cast<uintptr_t>(g) & (4 * sizeof(G) - 1)) == 0;
-    const int64_t sb = L.block0 + b, s0 = sb * kBlockElems;
-    float gv[2][4], pv[2][4], m[2][4], v[2][4];
-    const float md = k8 ? __fmul_rn(m_top[sb], 1.0f / kE4M3Max) : 0.f;
-    const float rd = k8 ? __fmul_rn(r_top[sb], 1.0f / kE4M3Max) : 0.f;
+  each_run<kCap, P, G>(L, b, end, [&](P* p, const G* g, int64_t left, int blocks, int64_t state) {
+    const bool pa = aligned_run<P, 4>(p), ga = aligned_run<G, 4>(g);
+    float *ms = mv + state * kBlockElems, *vs = rv + state * kBlockElems;
+    for (; blocks > 0; --blocks, p += kBlockElems, g += kBlockElems, ms += kBlockElems, vs += kBlockElems,
+                       left -= kBlockElems) {
+      const int valid = static_cast<int>(min(left, static_cast<int64_t>(kBlockElems)));
+      float gv[2][4], pv[2][4], m[2][4], v[2][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int e = 4 * (lane + 32 * i);
-      load4(g + e, gw && e + 4 <= valid, valid - e, gv[i]);
-      load4(p + e, pw && e + 4 <= valid, valid - e, pv[i]);
-      if constexpr (k8) {
-        decode4(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(mv) + s0 + e), md, m[i]);
-        decode4(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(rv) + s0 + e), rd, v[i]);
-      } else {
-        *reinterpret_cast<float4*>(m[i]) = *reinterpret_cast<const float4*>(static_cast<const float*>(mv) + s0 + e);
-        *reinterpret_cast<float4*>(v[i]) = *reinterpret_cast<const float4*>(static_cast<const float*>(rv) + s0 + e);
-      }
-    }
-    float mt = 0.f, rt = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int e = 4 * (lane + 32 * i);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if constexpr (k8) v[i][k] = __fmul_rn(v[i][k], v[i][k]);
-        moments(h, __fmul_rn(gv[i][k], gs), m[i][k], v[i][k]);
-        const float r = __fsqrt_rn(v[i][k]);
-        pv[i][k] = updated(h, pv[i][k], m[i][k], r);
-        if constexpr (k8) {
-          v[i][k] = r;
-          mt = fmaxf(mt, fabsf(m[i][k]));
-          rt = fmaxf(rt, r);
-        }
-      }
-      store4(p + e, pw && e + 4 <= valid, valid - e, pv[i]);
-      if constexpr (!k8) {
-        *reinterpret_cast<float4*>(static_cast<float*>(mv) + s0 + e) = *reinterpret_cast<const float4*>(m[i]);
-        *reinterpret_cast<float4*>(static_cast<float*>(rv) + s0 + e) = *reinterpret_cast<const float4*>(v[i]);
-      }
-    }
-    if constexpr (k8) {
-      mt = warp_max(mt);
-      rt = warp_max(rt);
-      const float ms = code_scale(mt), rs = code_scale(rt);
-      if (lane == 0) {
-        m_top[sb] = mt;
-        r_top[sb] = rt;
+      for (int i = 0; i < 2; ++i) {
+        const int e = 4 * (lane + 32 * i);
+        const bool in = e + 4 <= valid;
+        widen(load_run<G, 4>(g + e, ga && in, valid - e), gv[i]);
+        widen(load_run<P, 4>(p + e, pa && in, valid - e), pv[i]);
+        *reinterpret_cast<float4*>(m[i]) = *reinterpret_cast<const float4*>(ms + e);
+        *reinterpret_cast<float4*>(v[i]) = *reinterpret_cast<const float4*>(vs + e);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int e = 4 * (lane + 32 * i);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          m[i][k] = __fmul_rn(m[i][k], ms);
-          const float y = __fmul_rn(v[i][k], rs);
-          v[i][k] = v[i][k] > 0.f ? fmaxf(y, kE4M3Min) : y;
+          moments(h, __fmul_rn(gv[i][k], gs), m[i][k], v[i][k]);
+          pv[i][k] = updated(h, pv[i][k], m[i][k], sqrtf(v[i][k]));
         }
-        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(mv) + s0 + e) = encode4(m[i]);
-        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(rv) + s0 + e) = encode4(v[i]);
+        store_run<P, 4>(p + e, pa && e + 4 <= valid, valid - e, pv[i]);
+        *reinterpret_cast<float4*>(ms + e) = *reinterpret_cast<const float4*>(m[i]);
+        *reinterpret_cast<float4*>(vs + e) = *reinterpret_cast<const float4*>(v[i]);
       }
     }
-  }
+  });
+}
+
+// 8-bit states.  One warp per block, lane l on the elements 8 l .. 8 l + 7:
+// the block's two absmax are reductions over the warp's registers.  With 4
+// bytes of states per element the arithmetic weighs as much as HBM: two
+// blocks are loaded before either is worked on, and what only small second
+// moments need (a root of full range, codes of zero) is behind branches that
+// a block of ordinary values does not take.
+template <int kCap, typename P, typename G>
+__global__ void __launch_bounds__(kWarps * 32, 3) adamw8_kernel(const __grid_constant__ TensorList<kCap> L,
+                                                                const __grid_constant__ Hyper h, uint8_t* mv,
+                                                                uint8_t* rv, float* m_top, float* r_top,
+                                                                int per_warp) {
+  const int lane = threadIdx.x & 31;
+  const int b = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * per_warp;
+  const int end = min(b + per_warp, L.first[L.count]);
+  if (b >= end) return;
+  if (h.found_inf != nullptr && *h.found_inf != 0.f) return;
+  const bool scaled = h.grad_scale != nullptr;
+  const float gs = scaled ? *h.grad_scale : 1.f;
+  struct Loaded {
+    Run<G, 8> g;
+    Run<P, 8> p;
+    uint2 m, r;
+    float mt, rt;
+  };
+  each_run<kCap, P, G>(L, b, end, [&](P* p, const G* g, int64_t left, int blocks, int64_t state) {
+    const bool pa = aligned_run<P, 8>(p), ga = aligned_run<G, 8>(g);
+    p += 8 * lane;
+    g += 8 * lane;
+    left -= 8 * lane;   // of this lane's place on
+    uint8_t *ms = mv + state * kBlockElems + 8 * lane, *rs = rv + state * kBlockElems + 8 * lane;
+    float *mt = m_top + state, *rt = r_top + state;
+    auto fetch = [&](int i, Loaded& x) {
+      const int valid = static_cast<int>(min(left - i * kBlockElems, static_cast<int64_t>(8)));
+      x.g = load_run<G, 8>(g + i * kBlockElems, ga && valid == 8, valid);
+      x.p = load_run<P, 8>(p + i * kBlockElems, pa && valid == 8, valid);
+      x.m = *reinterpret_cast<const uint2*>(ms + i * kBlockElems);
+      x.r = *reinterpret_cast<const uint2*>(rs + i * kBlockElems);
+      x.mt = mt[i];
+      x.rt = rt[i];
+    };
+    auto work = [&](int i, const Loaded& x) {
+      float gv[8], pv[8], m[8], v[8];
+      widen(x.g, gv);
+      widen(x.p, pv);
+      decode8(x.m, __fmul_rn(x.mt, 1.0f / kE4M3Max), m);
+      decode8(x.r, __fmul_rn(x.rt, 1.0f / kE4M3Max), v);
+      if (scaled)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) gv[k] = __fmul_rn(gv[k], gs);
+      float low = INFINITY, mtop = 0.f, vtop = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] = __fmul_rn(v[k], v[k]);
+        moments(h, gv[k], m[k], v[k]);
+        low = fminf(low, v[k]);
+        mtop = fmaxf(mtop, fabsf(m[k]));
+      }
+      const bool ordinary = low >= kRootMin;
+      if (ordinary) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = root_of(v[k]);
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) v[k] = __fsqrt_rn(v[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        vtop = fmaxf(vtop, v[k]);
+        pv[k] = updated(h, pv[k], m[k], v[k]);
+      }
+      const int valid = static_cast<int>(min(left - i * kBlockElems, static_cast<int64_t>(8)));
+      store_run<P, 8>(p + i * kBlockElems, pa && valid == 8, valid, pv);
+      mtop = warp_max(mtop);
+      vtop = warp_max(vtop);
+      const float mscale = code_scale(mtop), rscale = code_scale(vtop);
+      if (lane == 0) {
+        mt[i] = mtop;
+        rt[i] = vtop;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m[k] = __fmul_rn(m[k], mscale);
+      if (ordinary) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = fmaxf(__fmul_rn(v[k], rscale), kE4M3Min);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = v[k] > 0.f ? fmaxf(__fmul_rn(v[k], rscale), kE4M3Min) : 0.f;
+      }
+      *reinterpret_cast<uint2*>(ms + i * kBlockElems) = encode8(m);
+      *reinterpret_cast<uint2*>(rs + i * kBlockElems) = encode8(v);
+    };
+    for (; blocks > 0; blocks -= 2) {
+      Loaded x, z;
+      fetch(0, x);
+      if (blocks > 1) fetch(1, z);
+      work(0, x);
+      if (blocks > 1) work(1, z);
+      p += 2 * kBlockElems;
+      g += 2 * kBlockElems;
+      ms += 2 * kBlockElems;
+      rs += 2 * kBlockElems;
+      mt += 2;
+      rt += 2;
+      left -= 2 * kBlockElems;
+    }
+  });
 }
 
 template <int kCap, typename P, typename G, bool k8>
@@ -237,9 +359,16 @@ cudaError_t launch_list(const TensorList<kCap>& L, const Hyper& h, void* m, void
                         cudaStream_t s) {
   const int blocks = L.first[L.count];
   if (blocks == 0) return cudaSuccess;
+  // more blocks per warp only when every SM still gets several rounds of warps
+  const int per_warp = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(k8 ? 8 : 4, blocks / (152 * 64))));
+  const unsigned grid = static_cast<unsigned>(ceil_div(blocks, kWarps * per_warp));
   ProfScope ps(K_ADAMW, s);
-  adamw_kernel<kCap, P, G, k8><<<static_cast<unsigned>(ceil_div(blocks, kWarps * kPerWarp)), kWarps * 32, 0, s>>>(L, h, m, r, mt,
-                                                                                                      rt);
+  if constexpr (k8)
+    adamw8_kernel<kCap, P, G><<<grid, kWarps * 32, 0, s>>>(L, h, static_cast<uint8_t*>(m), static_cast<uint8_t*>(r),
+                                                           mt, rt, per_warp);
+  else
+    adamw_kernel<kCap, P, G><<<grid, kWarps * 32, 0, s>>>(L, h, static_cast<float*>(m), static_cast<float*>(r),
+                                                          per_warp);
   return cudaGetLastError();
 }
 
