@@ -64,10 +64,10 @@ __device__ __forceinline__ int find_tensor(const TensorList<kCap>& L, int b) {
   return lo;
 }
 
+// Maximum over the warp of values >= 0: their bits are ordered like integers
+// (a NaN above all).
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 
 // N consecutive elements as fp32: 16-byte accesses when `whole` (they exist
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constan
 // moments need (a root of full range, codes of zero) is behind branches that
 // a block of ordinary values does not take.
 template <int kCap, typename P, typename G>
-__global__ void __launch_bounds__(kWarps * 32, 3) adamw8_kernel(const __grid_constant__ TensorList<kCap> L,
+__global__ void __launch_bounds__(kWarps * 32, 4) adamw8_kernel(const __grid_constant__ TensorList<kCap> L,
                                                                 const __grid_constant__ Hyper h, uint8_t* mv,
                                                                 uint8_t* rv, float* m_top, float* r_top,
                                                                 int per_warp) {
@@ -274,19 +274,21 @@ __global__ void __launch_bounds__(kWarps * 32, 3) adamw8_kernel(const __grid_con
     const bool pa = aligned_run<P, 8>(p), ga = aligned_run<G, 8>(g);
     p += 8 * lane;
     g += 8 * lane;
-    left -= 8 * lane;   // of this lane's place on
+    // this lane's elements from here to the tensor's end
+    int rest = static_cast<int>(min(left, static_cast<int64_t>(1) << 30)) - 8 * lane;
     uint8_t *ms = mv + state * kBlockElems + 8 * lane, *rs = rv + state * kBlockElems + 8 * lane;
     float *mt = m_top + state, *rt = r_top + state;
-    auto fetch = [&](int i, Loaded& x) {
-      const int valid = static_cast<int>(min(left - i * kBlockElems, static_cast<int64_t>(8)));
-      x.g = load_run<G, 8>(g + i * kBlockElems, ga && valid == 8, valid);
-      x.p = load_run<P, 8>(p + i * kBlockElems, pa && valid == 8, valid);
+    // whole: every access is of 8 aligned elements
+    auto fetch = [&](auto whole, int i, Loaded& x) {
+      const int valid = whole ? 8 : min(rest - i * kBlockElems, 8);
+      x.g = load_run<G, 8>(g + i * kBlockElems, whole || (ga && valid == 8), valid);
+      x.p = load_run<P, 8>(p + i * kBlockElems, whole || (pa && valid == 8), valid);
       x.m = *reinterpret_cast<const uint2*>(ms + i * kBlockElems);
       x.r = *reinterpret_cast<const uint2*>(rs + i * kBlockElems);
       x.mt = mt[i];
       x.rt = rt[i];
     };
-    auto work = [&](int i, const Loaded& x) {
+    auto work = [&](auto whole, int i, const Loaded& x) {
       float gv[8], pv[8], m[8], v[8];
       widen(x.g, gv);
       widen(x.p, pv);
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) adamw8_kernel(const __grid_con
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = root_of(v[k]);
       } else {
-#pragma unroll 1
+#pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = __fsqrt_rn(v[k]);
       }
 #pragma unroll
@@ -316,15 +318,14 @@ __global__ void __launch_bounds__(kWarps * 32, 3) adamw8_kernel(const __grid_con
         vtop = fmaxf(vtop, v[k]);
         pv[k] = updated(h, pv[k], m[k], v[k]);
       }
-      const int valid = static_cast<int>(min(left - i * kBlockElems, static_cast<int64_t>(8)));
-      store_run<P, 8>(p + i * kBlockElems, pa && valid == 8, valid, pv);
+      const int valid = whole ? 8 : min(rest - i * kBlockElems, 8);
+      store_run<P, 8>(p + i * kBlockElems, whole || (pa && valid == 8), valid, pv);
       mtop = warp_max(mtop);
       vtop = warp_max(vtop);
-      const float mscale = code_scale(mtop), rscale = code_scale(vtop);
-      if (lane == 0) {
-        mt[i] = mtop;
-        rt[i] = vtop;
-      }
+      // even lanes work out m's scale, odd lanes r's
+      const float top = lane & 1 ? vtop : mtop, scale = code_scale(top);
+      const float mscale = __shfl_sync(0xffffffffu, scale, 0), rscale = __shfl_sync(0xffffffffu, scale, 1);
+      if (lane < 2) (lane == 0 ? mt : rt)[i] = top;
 #pragma unroll
       for (int k = 0; k < 8; ++k) m[k] = __fmul_rn(m[k], mscale);
       if (ordinary) {
@@ -337,20 +338,24 @@ __global__ void __launch_bounds__(kWarps * 32, 3) adamw8_kernel(const __grid_con
       *reinterpret_cast<uint2*>(ms + i * kBlockElems) = encode8(m);
       *reinterpret_cast<uint2*>(rs + i * kBlockElems) = encode8(v);
     };
-    for (; blocks > 0; blocks -= 2) {
-      Loaded x, z;
-      fetch(0, x);
-      if (blocks > 1) fetch(1, z);
-      work(0, x);
-      if (blocks > 1) work(1, z);
-      p += 2 * kBlockElems;
-      g += 2 * kBlockElems;
-      ms += 2 * kBlockElems;
-      rs += 2 * kBlockElems;
-      mt += 2;
-      rt += 2;
-      left -= 2 * kBlockElems;
-    }
+    auto run = [&](auto whole) {
+      for (; blocks > 0; blocks -= 2) {
+        Loaded x, z;
+        fetch(whole, 0, x);
+        if (blocks > 1) fetch(whole, 1, z);
+        work(whole, 0, x);
+        if (blocks > 1) work(whole, 1, z);
+        p += 2 * kBlockElems;
+        g += 2 * kBlockElems;
+        ms += 2 * kBlockElems;
+        rs += 2 * kBlockElems;
+        mt += 2;
+        rt += 2;
+        rest -= 2 * kBlockElems;
+      }
+    };
+    if (pa && ga && left >= static_cast<int64_t>(blocks) * kBlockElems) run(std::true_type());
+    else run(std::false_type());
   });
 }
 
