@@ -123,19 +123,19 @@ __global__ void __launch_bounds__(kThreadsPlan) adapter_plan_kernel(const int32_
 // ---- shared pieces of the three products ----------------------------------
 //
 // All three run on the tensor cores (tcgen05, 128-row tiles, fp32 accumulators
-// in TMEM) on operands staged in shared memory with 16-byte (narrower for
-// rows that are not 16-byte aligned) asynchronous copies, which gather the
-// tokens of a tile wherever they lie and fill what is past an edge with
-// zeros.  Matrices of a width C have rows of C 16-bit elements; an operand
+// in TMEM) on operands staged in shared memory.  Where the tokens of a tile
+// are consecutive (one request, one adapter) and every row starts on 16
+// bytes, one thread fetches the operands by TMA and one issues the products;
+// else all threads gather them with 16-byte (narrower for unaligned rows)
+// asynchronous copies that fill what is past an edge with zeros.  The gather
+// costs issue slots: 4096 -> 11008 at rank 64 on 8192 tokens took 28 + 92 us
+// by it.  Matrices of a width C have rows of C 16-bit elements; an operand
 // tile is rows of 64 elements (128 bytes) in the 128-byte swizzle, either
 // with the reduction along the row ("K-major") or across the rows
 // ("MN-major").
 
 constexpr int kRowBytes = 128;
 
-__device__ __forceinline__ float to_f32(uint16_t v, bool bf16) {
-  return bf16 ? __uint_as_float(static_cast<uint32_t>(v) << 16) : __half2float(__ushort_as_half(v));
-}
 __device__ __forceinline__ uint16_t to_16(float v, bool bf16) {
   return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
@@ -211,13 +211,19 @@ __device__ __forceinline__ uint32_t map_cluster(uint32_t a, uint32_t rank) {
 // Barriers, the abort flag of the bounded waits and the TMEM address.
 constexpr int kMaxStages = 4;
 struct Sync {
-  uint64_t done[kMaxStages];
+  uint64_t done[kMaxStages];    // the products that read a stage have completed
+  uint64_t full[kMaxStages];    // a stage's TMA copies have arrived
+  uint64_t last;                // all products have completed
   uint32_t tmem;
   int abort;
 };
 __device__ __forceinline__ void sync_setup(Sync& y, uint32_t columns) {
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kMaxStages; ++i) mbar_init(&y.done[i], 1);
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(&y.done[i], 1);
+      mbar_init(&y.full[i], 1);
+    }
+    mbar_init(&y.last, 1);
     y.abort = 0;
     fence_mbar_init();
   }
@@ -265,6 +271,7 @@ __device__ __forceinline__ float cluster_sum(uint32_t red, int at, int ranks) {
 // ---- mid = X W^T (t and u) -------------------------------------------------
 
 struct ShrinkArgs {
+  CUtensorMap tmX, tmW;   // with kTma: X, box 64 x 128; W, box 64 x r16 (K-major) or 64 x 64
   const uint16_t* X;      // [M, C]
   const uint16_t* W;      // per group [R, C] (K-major) or [C, R] (MN-major)
   uint16_t* mid;          // [M, R]
@@ -285,8 +292,8 @@ __host__ __device__ constexpr int shrink_stage_bytes(int r16, bool mn) {
 // One cluster per tile of 128 tokens; its CTAs split the reduction, each
 // accumulating in TMEM, and add up in the order of their ranks.  Bound by
 // reading X once.
-template <bool kMN, int kStages>
-__global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const ShrinkArgs a) {
+template <bool kMN, int kStages, bool kTma>
+__global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_constant__ ShrinkArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Sync y;
   const int ranks = a.ranks, rank = blockIdx.x % ranks;
@@ -306,63 +313,91 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const ShrinkArgs a)
   const int n = static_cast<int>(static_cast<int64_t>(nb) * (rank + 1) / ranks) - b0;
   const int64_t C = a.C;
   const uint16_t* W = a.W + static_cast<int64_t>(t.group) * R * C;
-  // this thread's rows of X: 8 threads a row
-  const uint16_t* xrow[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = (tid >> 3) + 32 * i;
-    xrow[i] = row < t.count ? a.X + static_cast<int64_t>(a.perm[t.start + row]) * C : nullptr;
-  }
   sync_setup(y, tmem_columns(r16));
 
-  auto load = [&](int b, int s) {
-    const int64_t c0 = static_cast<int64_t>(b0 + b) * 64;
+  const uint32_t idesc = instruction(r16, false, kMN, a.bf16);
+  auto multiply = [&](int it) {   // one thread: the products of a stage
+    const int s = it % kStages;
     const uint32_t xs = base + s * stage_bytes, ws = xs + 128 * kRowBytes;
-    const int64_t at = c0 + (tid & 7) * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)   // rows past the tile's tokens are not read: their products go nowhere
-      if (xrow[i] != nullptr) load_chunk(xs + swizzled((tid >> 3) + 32 * i, tid & 7), xrow[i], at, C - at, a.cw);
-    if constexpr (kMN) {
-      const int chunks = r16 / 8;
-      for (int i = tid; i < 64 * chunks; i += kThreads) {
-        const int k = i / chunks, c = i % chunks;
-        load_chunk(ws + (c >> 3) * 64 * kRowBytes + swizzled(k, c & 7), W + min(c0 + k, C - 1) * R, c * 8,
-                   c0 + k < C ? R - c * 8 : 0, a.rw);
-      }
-    } else {
-      for (int j = tid >> 3; j < r16; j += kThreads / 8)
-        load_chunk(ws + swizzled(j, tid & 7), W + min(j, R - 1) * C, at, j < R ? C - at : 0, a.cw);
-    }
+    for (int k = 0; k < 4; ++k)
+      umma_f16(y.tmem, desc_k(xs, k), kMN ? desc_mn(ws, k, 64 * kRowBytes) : desc_k(ws, k), idesc,
+               it > 0 || k > 0 ? 1u : 0u);
+    umma_commit(&y.done[s]);
+    if (it == n - 1) umma_commit(&y.last);
   };
+  if (kTma && t.row0 >= 0) {
+    if (tid == 0) {
+      uint8_t* stages = smem_raw + (base - smem_u32(smem_raw));
+      for (int it = 0; it < n; ++it) {
+        const int s = it % kStages, c0 = (b0 + it) * 64;
+        uint8_t *xs = stages + s * stage_bytes, *ws = xs + 128 * kRowBytes;
+        if (it >= kStages) mbar_wait(&y.done[s], (it / kStages - 1) & 1, &y.abort, a.st, 20);
+        mbar_arrive_expect_tx(&y.full[s], stage_bytes);
+        tma_load_2d(xs, &a.tmX, c0, t.row0, &y.full[s]);
+        if constexpr (kMN) {
+          tma_load_3d(ws, &a.tmW, 0, c0, t.group, &y.full[s]);
+          if (r16 > 64) tma_load_3d(ws + 64 * kRowBytes, &a.tmW, 64, c0, t.group, &y.full[s]);
+        } else {
+          tma_load_3d(ws, &a.tmW, c0, 0, t.group, &y.full[s]);
+        }
+      }
+    } else if (tid == 32) {
+      for (int it = 0; it < n; ++it) {
+        mbar_wait(&y.full[it % kStages], (it / kStages) & 1, &y.abort, a.st, 25);
+        tc_fence_after();
+        multiply(it);
+      }
+    }
+    __syncwarp();
+  } else {
+    // this thread's rows of X: 8 threads a row
+    const uint16_t* xrow[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = (tid >> 3) + 32 * i;
+      xrow[i] = row < t.count ? a.X + static_cast<int64_t>(a.perm[t.start + row]) * C : nullptr;
+    }
+    auto load = [&](int b, int s) {
+      const int64_t c0 = static_cast<int64_t>(b0 + b) * 64;
+      const uint32_t xs = base + s * stage_bytes, ws = xs + 128 * kRowBytes;
+      const int64_t at = c0 + (tid & 7) * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)   // rows past the tile's tokens are not read: their products go nowhere
+        if (xrow[i] != nullptr) load_chunk(xs + swizzled((tid >> 3) + 32 * i, tid & 7), xrow[i], at, C - at, a.cw);
+      if constexpr (kMN) {
+        const int chunks = r16 / 8;
+        for (int i = tid; i < 64 * chunks; i += kThreads) {
+          const int k = i / chunks, c = i % chunks;
+          load_chunk(ws + (c >> 3) * 64 * kRowBytes + swizzled(k, c & 7), W + min(c0 + k, C - 1) * R, c * 8,
+                     c0 + k < C ? R - c * 8 : 0, a.rw);
+        }
+      } else {
+        for (int j = tid >> 3; j < r16; j += kThreads / 8)
+          load_chunk(ws + swizzled(j, tid & 7), W + min(j, R - 1) * C, at, j < R ? C - at : 0, a.cw);
+      }
+    };
 
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    if (i < n) load(i, i);
-    cp_async_commit();
-  }
-  const uint32_t idesc = instruction(r16, false, kMN, a.bf16);
-  for (int it = 0; it < n; ++it) {
-    const int s = it % kStages;
-    cp_async_wait<kStages - 2>();
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-      const uint32_t xs = base + s * stage_bytes, ws = xs + 128 * kRowBytes;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        umma_f16(y.tmem, desc_k(xs, k), kMN ? desc_mn(ws, k, 64 * kRowBytes) : desc_k(ws, k), idesc,
-                 it > 0 || k > 0 ? 1u : 0u);
-      umma_commit(&y.done[s]);
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (i < n) load(i, i);
+      cp_async_commit();
     }
-    const int next = it + kStages - 1;
-    if (next < n) {
-      // the stage to refill was read by the products of step it - 1
-      if (it > 0) mbar_wait(&y.done[(it - 1) % kStages], ((it - 1) / kStages) & 1, &y.abort, a.st, 20);
-      load(next, next % kStages);
+    for (int it = 0; it < n; ++it) {
+      cp_async_wait<kStages - 2>();
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (tid == 0) multiply(it);
+      const int next = it + kStages - 1;
+      if (next < n) {
+        // the stage to refill was read by the products of step it - 1
+        if (it > 0) mbar_wait(&y.done[(it - 1) % kStages], ((it - 1) / kStages) & 1, &y.abort, a.st, 20);
+        load(next, next % kStages);
+      }
+      cp_async_commit();
     }
-    cp_async_commit();
   }
-  mbar_wait(&y.done[(n - 1) % kStages], ((n - 1) / kStages) & 1, &y.abort, a.st, 21);
+  mbar_wait(&y.last, 0, &y.abort, a.st, 21);
   cp_async_wait<0>();
   tc_fence_after();
   float* red = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)));
@@ -384,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const ShrinkArgs a)
 // ---- out = addend + scale mid W^T (y and gx) --------------------------------
 
 struct ExpandArgs {
+  CUtensorMap tmMid, tmW, tmAdd, tmOut;   // with kTma: mid, addend and out, box 64 x 128; W, box 64 x 64 or 64 x r16
   const uint16_t* mid;     // [M, R]
   const uint16_t* W;       // per group [C, R] (K-major) or [R, C] (MN-major)
   const uint16_t* addend;  // [M, C] or NULL; may be out
@@ -393,162 +429,282 @@ struct ExpandArgs {
   const int* perm;
   DevStatus* st;
   int64_t C;
-  int R, E, cw, rw;
-  int col_tiles;           // 128-column tiles per CTA
+  int M, R, E, cw, rw;
+  int col_tiles;           // 64-column tiles per CTA
   bool bf16;
 };
 
-__host__ __device__ constexpr int expand_operand_bytes(int r16) { return (r16 > 64 ? 2 : 1) * 128 * kRowBytes; }
+constexpr int kCols = 64;                                  // columns per tile
+constexpr uint32_t kTileBytes = 128 * kRowBytes;           // addend / out tile: 128 tokens x 64 columns
+__host__ __device__ constexpr int expand_blocks(int r16) { return r16 > 64 ? 2 : 1; }
+__host__ __device__ constexpr int expand_mid_bytes(int r16) { return expand_blocks(r16) * 128 * kRowBytes; }
+__host__ __device__ constexpr int expand_w_bytes(int r16) { return expand_blocks(r16) * 64 * kRowBytes; }
+__host__ __device__ constexpr int expand_tiles(int r16) { return r16 > 64 ? 2 : 4; }   // addend tiles in flight
 
-// One CTA per (tile of 128 tokens, run of 128-column tiles): mid stays in
+struct ExpandSync {
+  uint64_t w_full[2], w_free[2], acc_full[2], acc_free[2], add_full[4], add_free[4], mid_full;
+  uint32_t tmem;
+  int abort;
+};
+
+// One CTA per (tile of 128 tokens, run of 64-column tiles): mid stays in
 // shared memory; per column tile W is read from L2, the addend tile arrives
-// two tiles ahead, is updated in place and leaves in whole rows.  Bound by
-// reading the addend and writing out.
-template <bool kMN>
-__global__ void __launch_bounds__(kThreads, 2) expand_kernel(const ExpandArgs a) {
+// several tiles ahead, is updated in place and leaves as a whole.  Warps 0-7
+// turn the accumulators into output, thread 256 fetches, thread 288 issues
+// the products.  Bound by reading the addend and writing out.
+constexpr int kExpandThreads = 320;
+template <bool kMN, bool kTma>
+__global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_constant__ ExpandArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Sync y;
+  __shared__ ExpandSync y;
   const Tile t = a.tiles[blockIdx.x];
   if (t.count == 0) return;
   const bool adapter = t.group < a.E;
   if (!adapter && a.addend == a.out) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = a.R, r16 = rank16(R);
   const int64_t C = a.C;
-  const int tiles_all = static_cast<int>((C + 127) / 128);
-  const int j0 = blockIdx.y * a.col_tiles, n = min(a.col_tiles, tiles_all - j0);
-  const uint32_t mids = align1024(smem_u32(smem_raw)), ws = mids + expand_operand_bytes(r16);
-  const uint32_t bufs = ws + expand_operand_bytes(r16);
-  constexpr uint32_t kBufBytes = 128 * 256;
-  const uint16_t* W = a.W + static_cast<int64_t>(adapter ? t.group : 0) * R * C;
+  const int j0 = blockIdx.y * a.col_tiles;
+  const int n = min(a.col_tiles, static_cast<int>((C + kCols - 1) / kCols) - j0);
+  const int bufs = expand_tiles(r16);
+  uint8_t* mids = smem_raw + (align1024(smem_u32(smem_raw)) - smem_u32(smem_raw));
+  uint8_t* wbuf = mids + expand_mid_bytes(r16);
+  uint8_t* tiles = wbuf + 2 * expand_w_bytes(r16);
   const float scale = a.scale != nullptr && adapter ? a.scale[t.group] : 1.f;
-  sync_setup(y, 128);
-
-  // a thread loads and stores the same 16-byte chunks of a tile: chunk
-  // tid % 16 of rows tid / 16 + 16 i
-  int64_t row_at[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = (tid >> 4) + 16 * i;
-    row_at[i] = row < t.count ? static_cast<int64_t>(a.perm[t.start + row]) * C : -1;
+  const bool tma = kTma && t.row0 >= 0;
+  // a tile that ends inside the batch is stored row by row
+  const bool tma_out = tma && (t.count == 128 || t.row0 + t.count == a.M);
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&y.w_full[i], 1);
+      mbar_init(&y.w_free[i], 1);
+      mbar_init(&y.acc_full[i], 1);
+      mbar_init(&y.acc_free[i], 256);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&y.add_full[i], 1);
+      mbar_init(&y.add_free[i], 1);
+    }
+    mbar_init(&y.mid_full, 1);
+    y.abort = 0;
+    fence_mbar_init();
   }
-  auto chunk_at = [&](int row, int c) { return static_cast<uint32_t>(row * 256 + ((c ^ (row & 7)) << 4)); };
-  auto load_addend = [&](int j) {
-    if (a.addend == nullptr) return;
-    const int64_t at = static_cast<int64_t>(j0 + j) * 128 + (tid & 15) * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (row_at[i] >= 0)
-        load_chunk(bufs + (j & 1) * kBufBytes + chunk_at((tid >> 4) + 16 * i, tid & 15), a.addend + row_at[i], at,
-                   C - at, a.cw);
-  };
-  auto load_w = [&](int j) {
-    if (!adapter) return;
-    const int64_t c0 = static_cast<int64_t>(j0 + j) * 128;
-    const int chunks = r16 / 8;
-    if constexpr (kMN) {
-      // blocks of 64 columns, r16 rows each
-      for (int i = tid; i < r16 * 16; i += kThreads) {
-        const int k = i >> 4, c = i & 15;
-        load_chunk(ws + (c >> 3) * r16 * kRowBytes + swizzled(k, c & 7), W + min(k, R - 1) * C, c0 + c * 8,
-                   k < R ? C - (c0 + c * 8) : 0, a.cw);
-      }
-    } else {
-      for (int i = tid; i < 128 * chunks; i += kThreads) {
-        const int row = i / chunks, c = i % chunks;
-        load_chunk(ws + (c >> 3) * 128 * kRowBytes + swizzled(row, c & 7), W + min(c0 + row, C - 1) * R, c * 8,
-                   c0 + row < C ? R - c * 8 : 0, a.rw);
-      }
-    }
-  };
-  if (adapter) {
-    const int chunks = r16 / 8;
-    for (int i = tid; i < t.count * chunks; i += kThreads) {
-      const int row = i / chunks, c = i % chunks;
-      load_chunk(mids + (c >> 3) * 128 * kRowBytes + swizzled(row, c & 7),
-                 a.mid + static_cast<int64_t>(a.perm[t.start + row]) * R, c * 8, R - c * 8, a.rw);
-    }
+  if (warp == 0) {
+    tmem_alloc(&y.tmem, 128);
+    tmem_relinquish();
   }
-  load_w(0);
-  load_addend(0);
-  cp_async_commit();
-  if (n > 1) load_addend(1);
-  cp_async_commit();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
 
-  const uint32_t idesc = instruction(128, false, kMN, a.bf16);
-  for (int j = 0; j < n; ++j) {
-    cp_async_wait<1>();
-    fence_proxy_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    if (adapter) {
-      if (tid == 0) {
-        tc_fence_after();
-        for (int k = 0; k < r16 / 16; ++k) {
-          const uint32_t kb = static_cast<uint32_t>(k >> 2) * 128 * kRowBytes;
-          umma_f16(y.tmem, desc_k(mids + kb, k & 3),
-                   kMN ? desc_mn(ws, k, r16 * kRowBytes) : desc_k(ws + kb, k & 3), idesc, k > 0 ? 1u : 0u);
-        }
-        umma_commit(&y.done[0]);
-      }
-      mbar_wait(&y.done[0], j & 1, &y.abort, a.st, 22);
-      tc_fence_after();
-    }
-    if (j + 1 < n) load_w(j + 1);
-    cp_async_commit();
-    const uint32_t buf = bufs + (j & 1) * kBufBytes;
-    const int row = (warp & 3) * 32 + lane;
+  const uint32_t idesc = instruction(kCols, false, kMN, a.bf16);
+  auto multiply = [&](int j) {   // one thread: accumulator j & 1 = mid W^T
+    const uint32_t ms = smem_u32(mids), ws = smem_u32(wbuf) + (j & 1) * expand_w_bytes(r16);
+    for (int k = 0; k < r16 / 16; ++k)
+      umma_f16(y.tmem + (j & 1) * kCols, desc_k(ms + (k >> 2) * 128 * kRowBytes, k & 3),
+               kMN ? desc_mn(ws, k, 0) : desc_k(ws + (k >> 2) * 64 * kRowBytes, k & 3), idesc, k > 0 ? 1u : 0u);
+    umma_commit(&y.w_free[j & 1]);
+    umma_commit(&y.acc_full[j & 1]);
+  };
+  // 8 columns of a token: addend + scale * accumulator
+  auto combine = [&](uint4 w, const uint32_t* v) {
+    uint32_t* e = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c0 = (warp >> 2) * 64 + h * 32;
-      uint32_t v[32];
-      if (adapter) {
-        tmem_ld32(y.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, v);
+    for (int i = 0; i < 4; ++i) {
+      const float lo = __uint_as_float(v[2 * i]), hi = __uint_as_float(v[2 * i + 1]);
+      if (a.bf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(fmaf(scale, lo, __uint_as_float(e[i] << 16)),
+                                                       fmaf(scale, hi, __uint_as_float(e[i] & 0xffff0000u)));
+        e[i] = *reinterpret_cast<const uint32_t*>(&h);
       } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0u;
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint8_t* p = smem_raw + (buf - smem_u32(smem_raw)) + chunk_at(row, c0 / 8 + q);
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (a.addend != nullptr) w = ld_shared_v4(p);
-        uint32_t* e = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float lo = fmaf(scale, __uint_as_float(v[8 * q + 2 * i]), to_f32(e[i] & 0xffffu, a.bf16));
-          const float hi = fmaf(scale, __uint_as_float(v[8 * q + 2 * i + 1]), to_f32(e[i] >> 16, a.bf16));
-          e[i] = to_16(lo, a.bf16) | (static_cast<uint32_t>(to_16(hi, a.bf16)) << 16);
-        }
-        st_shared_v4(p, w);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&e[i]));
+        const __half2 h = __floats2half2_rn(fmaf(scale, lo, f.x), fmaf(scale, hi, f.y));
+        e[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
-    __syncthreads();
-    const int64_t at = static_cast<int64_t>(j0 + j) * 128 + (tid & 15) * 8;
+    return w;
+  };
+  // warps 0-7: tile j into its buffer, in place of the addend
+  auto finish = [&](int j, uint8_t* buf) {
+    const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * 32;
+    uint32_t v[32];
+    if (adapter) {
+      mbar_wait(&y.acc_full[j & 1], (j >> 1) & 1, &y.abort, a.st, 22);
+      __syncwarp();
+      tc_fence_after();
+      tmem_ld32(y.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (j & 1) * kCols + c0, v);
+      tc_fence_before();
+      mbar_arrive(&y.acc_free[j & 1]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (row_at[i] < 0 || at >= C) continue;
-      const uint4 w = ld_shared_v4(smem_raw + (buf - smem_u32(smem_raw)) + chunk_at((tid >> 4) + 16 * i, tid & 15));
-      uint16_t* o = a.out + row_at[i] + at;
-      const uint32_t* e = reinterpret_cast<const uint32_t*>(&w);
+      for (int i = 0; i < 32; ++i) v[i] = 0u;
+    }
+    if (tma && a.addend != nullptr) mbar_wait(&y.add_full[j % bufs], (j / bufs) & 1, &y.abort, a.st, 27);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint8_t* p = buf + swizzled(row, c0 / 8 + q);
+      st_shared_v4(p, combine(a.addend != nullptr ? ld_shared_v4(p) : make_uint4(0, 0, 0, 0), v + 8 * q));
+    }
+  };
+  // rows of a finished tile: chunk tid % 8 of rows tid / 8 + 32 i
+  auto store_rows = [&](int j, const uint8_t* buf) {
+    const int64_t at = static_cast<int64_t>(j0 + j) * kCols + (tid & 7) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = (tid >> 3) + 32 * i;
+      if (row >= t.count || at >= C) continue;
+      const uint4 w = ld_shared_v4(buf + swizzled(row, tid & 7));
+      uint16_t* o = a.out + static_cast<int64_t>(tma ? t.row0 + row : a.perm[t.start + row]) * C + at;
       if (a.cw == 16) {
         *reinterpret_cast<uint4*>(o) = w;
       } else {
-        const int64_t valid = C - at;
+        const uint32_t* e = reinterpret_cast<const uint32_t*>(&w);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (k < valid) o[k] = static_cast<uint16_t>(e[k >> 1] >> (16 * (k & 1)));
+          if (k < C - at) o[k] = static_cast<uint16_t>(e[k >> 1] >> (16 * (k & 1)));
       }
     }
-    if (j + 2 < n) load_addend(j + 2);
+  };
+
+  if (tma) {
+    if (tid == 256) {
+      if (adapter) {
+        mbar_arrive_expect_tx(&y.mid_full, expand_mid_bytes(r16));
+        for (int k = 0; k < expand_blocks(r16); ++k)
+          tma_load_2d(mids + k * 128 * kRowBytes, &a.tmMid, 64 * k, t.row0, &y.mid_full);
+      }
+      for (int j = 0; j < n; ++j) {
+        const int c0 = (j0 + j) * kCols;
+        if (adapter) {
+          uint8_t* ws = wbuf + (j & 1) * expand_w_bytes(r16);
+          if (j >= 2) mbar_wait(&y.w_free[j & 1], ((j >> 1) - 1) & 1, &y.abort, a.st, 28);
+          if constexpr (kMN) {
+            mbar_arrive_expect_tx(&y.w_full[j & 1], r16 * kRowBytes);
+            tma_load_3d(ws, &a.tmW, c0, 0, t.group, &y.w_full[j & 1]);
+          } else {
+            mbar_arrive_expect_tx(&y.w_full[j & 1], expand_w_bytes(r16));
+            for (int k = 0; k < expand_blocks(r16); ++k)
+              tma_load_3d(ws + k * 64 * kRowBytes, &a.tmW, 64 * k, c0, t.group, &y.w_full[j & 1]);
+          }
+        }
+        if (a.addend != nullptr) {
+          if (j >= bufs) mbar_wait(&y.add_free[j % bufs], (j / bufs - 1) & 1, &y.abort, a.st, 29);
+          mbar_arrive_expect_tx(&y.add_full[j % bufs], kTileBytes);
+          tma_load_2d(tiles + (j % bufs) * kTileBytes, &a.tmAdd, c0, t.row0, &y.add_full[j % bufs]);
+        }
+      }
+    } else if (tid == 288) {
+      if (adapter) {
+        mbar_wait(&y.mid_full, 0, &y.abort, a.st, 30);
+        for (int j = 0; j < n; ++j) {
+          mbar_wait(&y.w_full[j & 1], (j >> 1) & 1, &y.abort, a.st, 31);
+          if (j >= 2) mbar_wait(&y.acc_free[j & 1], ((j >> 1) - 1) & 1, &y.abort, a.st, 32);
+          tc_fence_after();
+          multiply(j);
+        }
+      }
+    } else if (warp < 8) {
+      for (int j = 0; j < n; ++j) {
+        uint8_t* buf = tiles + (j % bufs) * kTileBytes;
+        // without an addend nothing else keeps this buffer's last store ahead
+        if (a.addend == nullptr && j >= bufs)
+          mbar_wait(&y.add_free[j % bufs], (j / bufs - 1) & 1, &y.abort, a.st, 29);
+        finish(j, buf);
+        if (tma_out) {
+          fence_proxy_async_smem();
+          named_bar_sync(1, 256);
+          if (tid == 0) {
+            tma_store_2d(&a.tmOut, (j0 + j) * kCols, t.row0, buf);
+            bulk_commit();
+            bulk_wait_read<1>();   // the store of tile j - 1 has read its buffer
+            if (j > 0) mbar_arrive(&y.add_free[(j - 1) % bufs]);
+          }
+          __syncwarp();
+        } else {
+          named_bar_sync(1, 256);
+          store_rows(j, buf);
+          named_bar_sync(1, 256);
+          if (tid == 0) mbar_arrive(&y.add_free[j % bufs]);
+        }
+      }
+      if (tma_out && tid == 0) bulk_wait_all();
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // the same, gathered by all of warps 0-7, one tile ahead
+    auto load_addend = [&](int j) {
+      if (a.addend == nullptr) return;
+      const uint32_t buf = smem_u32(tiles) + (j % bufs) * kTileBytes;
+      const int64_t at = static_cast<int64_t>(j0 + j) * kCols + (tid & 7) * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = (tid >> 3) + 32 * i;
+        if (row < t.count)
+          load_chunk(buf + swizzled(row, tid & 7), a.addend + static_cast<int64_t>(a.perm[t.start + row]) * C, at,
+                     C - at, a.cw);
+      }
+    };
+    const int chunks = r16 / 8;
+    const uint16_t* W = a.W + static_cast<int64_t>(adapter ? t.group : 0) * R * C;
+    auto load_w = [&](int j) {
+      if (!adapter) return;
+      const int64_t c0 = static_cast<int64_t>(j0 + j) * kCols;
+      const uint32_t ws = smem_u32(wbuf) + (j & 1) * expand_w_bytes(r16);
+      if constexpr (kMN) {
+        for (int i = tid; i < r16 * 8; i += kThreads) {
+          const int k = i >> 3, c = i & 7;
+          load_chunk(ws + swizzled(k, c), W + min(k, R - 1) * C, c0 + c * 8, k < R ? C - (c0 + c * 8) : 0, a.cw);
+        }
+      } else {
+        for (int i = tid; i < 64 * chunks; i += kThreads) {
+          const int row = i / chunks, c = i % chunks;
+          load_chunk(ws + (c >> 3) * 64 * kRowBytes + swizzled(row, c & 7), W + min(c0 + row, C - 1) * R, c * 8,
+                     c0 + row < C ? R - c * 8 : 0, a.rw);
+        }
+      }
+    };
+    if (adapter)
+      for (int i = tid; i < t.count * chunks; i += kThreads) {
+        const int row = i / chunks, c = i % chunks;
+        load_chunk(smem_u32(mids) + (c >> 3) * 128 * kRowBytes + swizzled(row, c & 7),
+                   a.mid + static_cast<int64_t>(a.perm[t.start + row]) * R, c * 8, R - c * 8, a.rw);
+      }
+    load_w(0);
+    load_addend(0);
     cp_async_commit();
+    for (int j = 0; j < n; ++j) {
+      // buffers of tile j + 1: w of tile j - 1 was read by products that tile
+      // j - 1's outputs waited for, its addend buffer left before the barrier
+      // that ended tile j + 1 - bufs
+      if (j + 1 < n) {
+        load_w(j + 1);
+        load_addend(j + 1);
+      }
+      cp_async_commit();
+      cp_async_wait<1>();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      named_bar_sync(1, 256);
+      if (adapter && tid == 0) {
+        tc_fence_after();
+        multiply(j);
+      }
+      uint8_t* buf = tiles + (j % bufs) * kTileBytes;
+      finish(j, buf);
+      named_bar_sync(1, 256);
+      store_rows(j, buf);
+      named_bar_sync(1, 256);
+    }
+    cp_async_wait<0>();
   }
-  cp_async_wait<0>();
-  sync_end(y, 128);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(y.tmem, 128);
 }
 
 // ---- gradients of A and B ---------------------------------------------------
 
 struct GradArgs {
+  CUtensorMap tmX, tmU;   // with kTma: X and mid, box 64 x 64
   const uint16_t* mid;    // [M, R]
   const uint16_t* X;      // [M, C]
   uint16_t* grad;         // per group [R, C] (kRankMajor) or [C, R]
@@ -557,7 +713,7 @@ struct GradArgs {
   const int* perm;
   DevStatus* st;
   int64_t C;
-  int R, cw, rw;
+  int M, R, cw, rw;
   bool bf16;
 };
 
@@ -568,8 +724,8 @@ __host__ __device__ constexpr int grad_stage_bytes(int r16) {
 // grad[c, j] = scale sum_m X[m, c] mid[m, j] over a group's tokens: one
 // cluster per (128 columns of X, group), its CTAs splitting the tokens.
 // Bound by reading X once.
-template <bool kRankMajor, int kStages>
-__global__ void __launch_bounds__(kThreads, 2) grad_kernel(const GradArgs a) {
+template <bool kRankMajor, int kStages, bool kTma>
+__global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant__ GradArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Sync y;
   const int tid = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x, R = a.R, r16 = rank16(R);
@@ -592,72 +748,99 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const GradArgs a) {
   const int chunks = r16 / 8;
   sync_setup(y, tmem_columns(r16));
 
-  // A group whose tokens are consecutive needs no table; else the tokens of a
-  // step are read one step before their copies are issued.
   const int first = a.perm[start];
-  const bool run = a.perm[start + tokens - 1] - first == tokens - 1;
-  constexpr int kMidPer = 4;   // up to 64 rows x 16 chunks of mid over 256 threads
-  int xm[4], um[kMidPer];
-  auto rows_of = [&](int b) {
-    const int m0 = (b0 + b) * 64;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = m0 + (tid >> 4) + 16 * i;
-      xm[i] = k < tokens ? (run ? first + k : a.perm[start + k]) : -1;
-    }
-#pragma unroll
-    for (int i = 0; i < kMidPer; ++i) {
-      const int k = m0 + (tid + i * kThreads) / chunks;
-      um[i] = tid + i * kThreads < 64 * chunks && k < tokens ? (run ? first + k : a.perm[start + k]) : -1;
-    }
-  };
-  auto load = [&](int b, int s) {   // of the rows that rows_of(b) found
-    const uint32_t xs = base + s * stage_bytes, us = xs + 2 * 64 * kRowBytes;
-    const int c = tid & 15;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      load_chunk(xs + (c >> 3) * 64 * kRowBytes + swizzled((tid >> 4) + 16 * i, c & 7),
-                 a.X + static_cast<int64_t>(max(xm[i], 0)) * C, c0 + c * 8, xm[i] >= 0 ? C - (c0 + c * 8) : 0, a.cw);
-#pragma unroll
-    for (int i = 0; i < kMidPer; ++i) {
-      const int at = tid + i * kThreads;
-      if (at >= 64 * chunks) break;
-      const int k = at / chunks, q = at % chunks;
-      load_chunk(us + (q >> 3) * 64 * kRowBytes + swizzled(k, q & 7),
-                 a.mid + static_cast<int64_t>(max(um[i], 0)) * R, q * 8, um[i] >= 0 ? R - q * 8 : 0, a.rw);
-    }
-    rows_of(b + 1);
-  };
-  rows_of(0);
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    if (i < n) load(i, i);
-    cp_async_commit();
-  }
+  const bool run = a.perm[start + tokens - 1] - first == tokens - 1;   // consecutive tokens
   const uint32_t idesc = instruction(r16, true, true, a.bf16);
-  for (int it = 0; it < n; ++it) {
+  auto multiply = [&](int it) {   // one thread: the products of a stage
     const int s = it % kStages;
-    cp_async_wait<kStages - 2>();
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-      const uint32_t xs = base + s * stage_bytes, us = xs + 2 * 64 * kRowBytes;
+    const uint32_t xs = base + s * stage_bytes, us = xs + 2 * 64 * kRowBytes;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        umma_f16(y.tmem, desc_mn(xs, k, 64 * kRowBytes), desc_mn(us, k, 64 * kRowBytes), idesc,
-                 it > 0 || k > 0 ? 1u : 0u);
-      umma_commit(&y.done[s]);
+    for (int k = 0; k < 4; ++k)
+      umma_f16(y.tmem, desc_mn(xs, k, 64 * kRowBytes), desc_mn(us, k, 64 * kRowBytes), idesc,
+               it > 0 || k > 0 ? 1u : 0u);
+    umma_commit(&y.done[s]);
+    if (it == n - 1) umma_commit(&y.last);
+  };
+  // The reduction runs over tokens, so a last block of fewer than 64 must not
+  // reach into the next group's rows: such a group is gathered unless it ends
+  // where the batch does, where the copies fill zeros.
+  if (kTma && run && (tokens % 64 == 0 || first + tokens == a.M)) {
+    if (tid == 0) {
+      uint8_t* stages = smem_raw + (base - smem_u32(smem_raw));
+      for (int it = 0; it < n; ++it) {
+        const int s = it % kStages, m0 = first + (b0 + it) * 64;
+        uint8_t *xs = stages + s * stage_bytes, *us = xs + 2 * 64 * kRowBytes;
+        if (it >= kStages) mbar_wait(&y.done[s], (it / kStages - 1) & 1, &y.abort, a.st, 23);
+        mbar_arrive_expect_tx(&y.full[s], stage_bytes);
+        tma_load_2d(xs, &a.tmX, static_cast<int>(c0), m0, &y.full[s]);
+        tma_load_2d(xs + 64 * kRowBytes, &a.tmX, static_cast<int>(c0) + 64, m0, &y.full[s]);
+        tma_load_2d(us, &a.tmU, 0, m0, &y.full[s]);
+        if (r16 > 64) tma_load_2d(us + 64 * kRowBytes, &a.tmU, 64, m0, &y.full[s]);
+      }
+    } else if (tid == 32) {
+      for (int it = 0; it < n; ++it) {
+        mbar_wait(&y.full[it % kStages], (it / kStages) & 1, &y.abort, a.st, 26);
+        tc_fence_after();
+        multiply(it);
+      }
     }
-    const int next = it + kStages - 1;
-    if (next < n) {
-      if (it > 0) mbar_wait(&y.done[(it - 1) % kStages], ((it - 1) / kStages) & 1, &y.abort, a.st, 23);
-      load(next, next % kStages);
+    __syncwarp();
+  } else {
+    // the tokens of a step are read one step before their copies are issued
+    constexpr int kMidPer = 4;   // up to 64 rows x 16 chunks of mid over 256 threads
+    int xm[4], um[kMidPer];
+    auto rows_of = [&](int b) {
+      const int m0 = (b0 + b) * 64;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = m0 + (tid >> 4) + 16 * i;
+        xm[i] = k < tokens ? (run ? first + k : a.perm[start + k]) : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < kMidPer; ++i) {
+        const int k = m0 + (tid + i * kThreads) / chunks;
+        um[i] = tid + i * kThreads < 64 * chunks && k < tokens ? (run ? first + k : a.perm[start + k]) : -1;
+      }
+    };
+    auto load = [&](int b, int s) {   // of the rows that rows_of(b) found
+      const uint32_t xs = base + s * stage_bytes, us = xs + 2 * 64 * kRowBytes;
+      const int c = tid & 15;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        load_chunk(xs + (c >> 3) * 64 * kRowBytes + swizzled((tid >> 4) + 16 * i, c & 7),
+                   a.X + static_cast<int64_t>(max(xm[i], 0)) * C, c0 + c * 8, xm[i] >= 0 ? C - (c0 + c * 8) : 0, a.cw);
+#pragma unroll
+      for (int i = 0; i < kMidPer; ++i) {
+        const int at = tid + i * kThreads;
+        if (at >= 64 * chunks) break;
+        const int k = at / chunks, q = at % chunks;
+        load_chunk(us + (q >> 3) * 64 * kRowBytes + swizzled(k, q & 7),
+                   a.mid + static_cast<int64_t>(max(um[i], 0)) * R, q * 8, um[i] >= 0 ? R - q * 8 : 0, a.rw);
+      }
+      rows_of(b + 1);
+    };
+    rows_of(0);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (i < n) load(i, i);
+      cp_async_commit();
     }
-    cp_async_commit();
+    for (int it = 0; it < n; ++it) {
+      cp_async_wait<kStages - 2>();
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (tid == 0) multiply(it);
+      const int next = it + kStages - 1;
+      if (next < n) {
+        if (it > 0) mbar_wait(&y.done[(it - 1) % kStages], ((it - 1) / kStages) & 1, &y.abort, a.st, 23);
+        load(next, next % kStages);
+      }
+      cp_async_commit();
+    }
   }
   float* red = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)));
   if (n > 0) {
-    mbar_wait(&y.done[(n - 1) % kStages], ((n - 1) / kStages) & 1, &y.abort, a.st, 24);
+    mbar_wait(&y.last, 0, &y.abort, a.st, 24);
     cp_async_wait<0>();
     tc_fence_after();
     __syncthreads();
@@ -709,11 +892,12 @@ int split(int64_t tiles, int64_t steps) {
 }
 
 template <typename Args>
-cudaError_t launch(void (*kernel)(Args), const Args& a, dim3 grid, int cluster, int smem, int prof, cudaStream_t s) {
+cudaError_t launch(void (*kernel)(Args), const Args& a, dim3 grid, int threads, int cluster, int smem, int prof,
+                   cudaStream_t s) {
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -725,6 +909,13 @@ cudaError_t launch(void (*kernel)(Args), const Args& a, dim3 grid, int cluster, 
   ProfScope ps(prof, s);
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
+
+constexpr CUtensorMapSwizzle kSwz = CU_TENSOR_MAP_SWIZZLE_128B;
+CUtensorMapDataType map_type(const Problem& p) {
+  return p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+// Rows of C and of R elements that start on 16 bytes: what tensor maps need.
+bool tma_rows(const Problem& p, int64_t C) { return C % 8 == 0 && p.R % 8 == 0; }
 
 cudaError_t shrink(const Problem& p, const void* X, int64_t C, const void* W, bool mn, const float* scale,
                    void* mid) {
@@ -743,13 +934,20 @@ cudaError_t shrink(const Problem& p, const void* X, int64_t C, const void* W, bo
   a.rw = copy_width(p.R);
   a.bf16 = p.bf16;
   const int r16 = rank16(p.R), ranks = split(p.plan.slots, ceil_div(C, 64));
+  a.ranks = ranks;
   const int stages = r16 > 64 ? 3 : 4;
   const int smem = 1024 + std::max(stages * shrink_stage_bytes(r16, mn), 128 * red_pitch(r16) * 4);
-  a.ranks = ranks;
   const dim3 grid(static_cast<unsigned>(ranks * p.plan.slots));
-  if (stages == 4)
-    return launch(mn ? shrink_kernel<true, 4> : shrink_kernel<false, 4>, a, grid, ranks, smem, K_ADAPTERS, p.s);
-  return launch(mn ? shrink_kernel<true, 3> : shrink_kernel<false, 3>, a, grid, ranks, smem, K_ADAPTERS, p.s);
+  const bool tma = tma_rows(p, C);
+  if (tma && (!make_tmap(&a.tmX, map_type(p), X, C, p.M, C * 2, 64, 128, kSwz) ||
+              !(mn ? make_tmap_3d(&a.tmW, map_type(p), W, p.R, C, p.E, 2, 64, 64, kSwz)
+                   : make_tmap_3d(&a.tmW, map_type(p), W, C, p.R, p.E, 2, 64, r16, kSwz))))
+    return cudaErrorUnknown;
+  auto k4 = tma ? (mn ? shrink_kernel<true, 4, true> : shrink_kernel<false, 4, true>)
+                : (mn ? shrink_kernel<true, 4, false> : shrink_kernel<false, 4, false>);
+  auto k3 = tma ? (mn ? shrink_kernel<true, 3, true> : shrink_kernel<false, 3, true>)
+                : (mn ? shrink_kernel<true, 3, false> : shrink_kernel<false, 3, false>);
+  return launch(stages == 4 ? k4 : k3, a, grid, kThreads, ranks, smem, K_ADAPTERS, p.s);
 }
 
 cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, bool mn, const float* scale,
@@ -764,17 +962,29 @@ cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, 
   a.perm = p.plan.perm;
   a.st = p.st;
   a.C = C;
+  a.M = static_cast<int>(p.M);
   a.R = p.R;
   a.E = static_cast<int>(p.E);
   a.cw = copy_width(C);
   a.rw = copy_width(p.R);
   a.bf16 = p.bf16;
-  const int64_t col_tiles = ceil_div(C, 128);
-  a.col_tiles = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, p.plan.slots * col_tiles /
+  const int r16 = rank16(p.R);
+  const int64_t col_tiles = ceil_div(C, kCols);
+  a.col_tiles = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, p.plan.slots * col_tiles /
                                                                                (4 * sm_count()))));
-  const int smem = 1024 + 2 * expand_operand_bytes(rank16(p.R)) + 2 * 128 * 256;
+  const int smem = 1024 + expand_mid_bytes(r16) + 2 * expand_w_bytes(r16) +
+                   expand_tiles(r16) * static_cast<int>(kTileBytes);
   const dim3 grid(static_cast<unsigned>(p.plan.slots), static_cast<unsigned>(ceil_div(col_tiles, a.col_tiles)));
-  return launch(mn ? expand_kernel<true> : expand_kernel<false>, a, grid, 1, smem, K_ADAPTERS, p.s);
+  const bool tma = tma_rows(p, C);
+  if (tma && (!make_tmap(&a.tmMid, map_type(p), mid, p.R, p.M, p.R * 2, 64, 128, kSwz) ||
+              !make_tmap(&a.tmAdd, map_type(p), addend != nullptr ? addend : out, C, p.M, C * 2, 64, 128, kSwz) ||
+              !make_tmap(&a.tmOut, map_type(p), out, C, p.M, C * 2, 64, 128, kSwz) ||
+              !(mn ? make_tmap_3d(&a.tmW, map_type(p), W, C, p.R, p.E, 2, 64, r16, kSwz)
+                   : make_tmap_3d(&a.tmW, map_type(p), W, p.R, C, p.E, 2, 64, 64, kSwz))))
+    return cudaErrorUnknown;
+  auto kernel = tma ? (mn ? expand_kernel<true, true> : expand_kernel<false, true>)
+                    : (mn ? expand_kernel<true, false> : expand_kernel<false, false>);
+  return launch(kernel, a, grid, kExpandThreads, 1, smem, K_ADAPTERS, p.s);
 }
 
 cudaError_t grad(const Problem& p, const void* mid, const void* X, int64_t C, bool rank_major, const float* scale,
@@ -788,6 +998,7 @@ cudaError_t grad(const Problem& p, const void* mid, const void* X, int64_t C, bo
   a.perm = p.plan.perm;
   a.st = p.st;
   a.C = C;
+  a.M = static_cast<int>(p.M);
   a.R = p.R;
   a.cw = copy_width(C);
   a.rw = copy_width(p.R);
@@ -796,10 +1007,15 @@ cudaError_t grad(const Problem& p, const void* mid, const void* X, int64_t C, bo
   const int stages = r16 > 64 ? 3 : 4;
   const int smem = 1024 + std::max(stages * grad_stage_bytes(r16), 128 * red_pitch(r16) * 4);
   const dim3 grid(static_cast<unsigned>(ranks), static_cast<unsigned>(ceil_div(C, 128)), static_cast<unsigned>(p.E));
-  if (stages == 4)
-    return launch(rank_major ? grad_kernel<true, 4> : grad_kernel<false, 4>, a, grid, ranks, smem, K_ADAPTERS_GRAD,
-                  p.s);
-  return launch(rank_major ? grad_kernel<true, 3> : grad_kernel<false, 3>, a, grid, ranks, smem, K_ADAPTERS_GRAD, p.s);
+  const bool tma = tma_rows(p, C);
+  if (tma && (!make_tmap(&a.tmX, map_type(p), X, C, p.M, C * 2, 64, 64, kSwz) ||
+              !make_tmap(&a.tmU, map_type(p), mid, p.R, p.M, p.R * 2, 64, 64, kSwz)))
+    return cudaErrorUnknown;
+  auto k4 = tma ? (rank_major ? grad_kernel<true, 4, true> : grad_kernel<false, 4, true>)
+                : (rank_major ? grad_kernel<true, 4, false> : grad_kernel<false, 4, false>);
+  auto k3 = tma ? (rank_major ? grad_kernel<true, 3, true> : grad_kernel<false, 3, true>)
+                : (rank_major ? grad_kernel<true, 3, false> : grad_kernel<false, 3, false>);
+  return launch(stages == 4 ? k4 : k3, a, grid, kThreads, ranks, smem, K_ADAPTERS_GRAD, p.s);
 }
 
 cudaError_t forward(const Problem& p, const void* x, const void* A, const void* B, const void* base, void* y,

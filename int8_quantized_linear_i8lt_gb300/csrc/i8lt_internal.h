@@ -23,6 +23,10 @@ int check_device();
 // box of box_inner x box_outer elements.
 bool make_tmap(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                uint64_t pitch, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);
+// `count` dense matrices (inner x outer elements of `elem` bytes) one after
+// another, with a box inside one of them.
+bool make_tmap_3d(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
+                  uint64_t count, uint64_t elem, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);
 
 // ---- kernel timing (i8lt_api.cu): no-ops unless i8lt_profile_start ran ----
 void prof_begin(int kernel_id, cudaStream_t s);
