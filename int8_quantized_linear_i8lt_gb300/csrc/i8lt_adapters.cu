@@ -123,13 +123,13 @@ __global__ void __launch_bounds__(kThreadsPlan) adapter_plan_kernel(const int32_
 // ---- shared pieces of the three products ----------------------------------
 //
 // All three run on the tensor cores (tcgen05, 128-row tiles, fp32 accumulators
-// in TMEM) on operands staged in shared memory.  Where the tokens of a tile
-// are consecutive (one request, one adapter) and every row starts on 16
-// bytes, one thread fetches the operands by TMA and one issues the products;
-// else all threads gather them with 16-byte (narrower for unaligned rows)
-// asynchronous copies that fill what is past an edge with zeros.  The gather
-// costs issue slots: 4096 -> 11008 at rank 64 on 8192 tokens took 28 + 92 us
-// by it.  Matrices of a width C have rows of C 16-bit elements; an operand
+// in TMEM) on operands staged in shared memory.  Where every row starts on 16
+// bytes, one warp fetches the operands by TMA, a tile of consecutive tokens
+// (one request, one adapter) as a box and others four rows at a time, and one
+// thread issues the products; else all threads gather them with narrower
+// asynchronous copies that fill what is past an edge with zeros.  Those cost
+// issue slots: 4096 -> 11008 at rank 64 on 8192 tokens took 28 + 92 us by
+// them, 24 + 63 us by TMA.  Matrices of a width C have rows of C 16-bit elements; an operand
 // tile is rows of 64 elements (128 bytes) in the 128-byte swizzle, either
 // with the reduction along the row ("K-major") or across the rows
 // ("MN-major").
@@ -247,6 +247,14 @@ __host__ __device__ constexpr uint32_t tmem_columns(int r16) { return r16 <= 32 
 // up: 16-byte accesses of 8 rows hit 8 different bank groups.
 __host__ __device__ constexpr int red_pitch(int r16) { return r16 + 4; }
 
+// The tokens at places 4 lane .. 4 lane + 3 of a tile, its last one repeated
+// past its end (whose products go nowhere).
+__device__ __forceinline__ void tile_rows(const int* perm, int start, int count, int (&rows)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) rows[i] = perm[start + min(4 * lane + i, count - 1)];
+}
+
 // The CTA's accumulator (128 rows x r16) into shared memory.
 __device__ __forceinline__ void spill(uint32_t tmem, int r16, float* red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -271,7 +279,7 @@ __device__ __forceinline__ float cluster_sum(uint32_t red, int at, int ranks) {
 // ---- mid = X W^T (t and u) -------------------------------------------------
 
 struct ShrinkArgs {
-  CUtensorMap tmX, tmW;   // with kTma: X, box 64 x 128; W, box 64 x r16 (K-major) or 64 x 64
+  CUtensorMap tmX, tmX1, tmW;   // with kTma: X, box 64 x 128 and 64 x 1; W, box 64 x r16 (K-major) or 64 x 64
   const uint16_t* X;      // [M, C]
   const uint16_t* W;      // per group [R, C] (K-major) or [C, R] (MN-major)
   uint16_t* mid;          // [M, R]
@@ -301,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
   if (t.count == 0) return;
   const int tid = threadIdx.x, R = a.R, r16 = rank16(R);
   if (t.group >= a.E) {
+    grid_dependency_wait();
     if (rank == 0)
       for (int i = tid; i < t.count * R; i += kThreads)
         a.mid[static_cast<int64_t>(a.perm[t.start + i / R]) * R + i % R] = 0;
@@ -326,21 +335,28 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
     umma_commit(&y.done[s]);
     if (it == n - 1) umma_commit(&y.last);
   };
-  if (kTma && t.row0 >= 0) {
-    if (tid == 0) {
+  if constexpr (kTma) {
+    if (tid < 32) {
       uint8_t* stages = smem_raw + (base - smem_u32(smem_raw));
+      int rows[4];
+      if (t.row0 < 0) tile_rows(a.perm, t.start, t.count, rows);
+      grid_dependency_wait();
       for (int it = 0; it < n; ++it) {
         const int s = it % kStages, c0 = (b0 + it) * 64;
         uint8_t *xs = stages + s * stage_bytes, *ws = xs + 128 * kRowBytes;
         if (it >= kStages) mbar_wait(&y.done[s], (it / kStages - 1) & 1, &y.abort, a.st, 20);
-        mbar_arrive_expect_tx(&y.full[s], stage_bytes);
-        tma_load_2d(xs, &a.tmX, c0, t.row0, &y.full[s]);
-        if constexpr (kMN) {
-          tma_load_3d(ws, &a.tmW, 0, c0, t.group, &y.full[s]);
-          if (r16 > 64) tma_load_3d(ws + 64 * kRowBytes, &a.tmW, 64, c0, t.group, &y.full[s]);
-        } else {
-          tma_load_3d(ws, &a.tmW, c0, 0, t.group, &y.full[s]);
+        if (tid == 0) {
+          mbar_arrive_expect_tx(&y.full[s], stage_bytes);
+          if (t.row0 >= 0) tma_load_2d(xs, &a.tmX, c0, t.row0, &y.full[s]);
+          if constexpr (kMN) {
+            tma_load_3d(ws, &a.tmW, 0, c0, t.group, &y.full[s]);
+            if (r16 > 64) tma_load_3d(ws + 64 * kRowBytes, &a.tmW, 64, c0, t.group, &y.full[s]);
+          } else {
+            tma_load_3d(ws, &a.tmW, c0, 0, t.group, &y.full[s]);
+          }
         }
+        __syncwarp();   // the stage is armed before its gathers arrive
+        if (t.row0 < 0) tma_gather4(xs + tid * 4 * kRowBytes, &a.tmX1, c0, rows, &y.full[s]);
       }
     } else if (tid == 32) {
       for (int it = 0; it < n; ++it) {
@@ -351,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
     }
     __syncwarp();
   } else {
+    grid_dependency_wait();
     // this thread's rows of X: 8 threads a row
     const uint16_t* xrow[4];
 #pragma unroll
@@ -399,7 +416,9 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
   }
   mbar_wait(&y.last, 0, &y.abort, a.st, 21);
   cp_async_wait<0>();
+  __syncwarp();
   tc_fence_after();
+  grid_dependents_launch();
   float* red = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)));
   __syncthreads();
   spill(y.tmem, r16, red);
@@ -419,7 +438,8 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
 // ---- out = addend + scale mid W^T (y and gx) --------------------------------
 
 struct ExpandArgs {
-  CUtensorMap tmMid, tmW, tmAdd, tmOut;   // with kTma: mid, addend and out, box 64 x 128; W, box 64 x 64 or 64 x r16
+  // with kTma: mid, addend and out, box 64 x 128 (the first two also 64 x 1); W, box 64 x 64 or 64 x r16
+  CUtensorMap tmMid, tmMid1, tmW, tmAdd, tmAdd1, tmOut;
   const uint16_t* mid;     // [M, R]
   const uint16_t* W;       // per group [C, R] (K-major) or [R, C] (MN-major)
   const uint16_t* addend;  // [M, C] or NULL; may be out
@@ -460,7 +480,10 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
   const Tile t = a.tiles[blockIdx.x];
   if (t.count == 0) return;
   const bool adapter = t.group < a.E;
-  if (!adapter && a.addend == a.out) return;
+  if (!adapter && a.addend == a.out) {
+    grid_dependency_wait();
+    return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = a.R, r16 = rank16(R);
   const int64_t C = a.C;
   const int j0 = blockIdx.y * a.col_tiles;
@@ -470,9 +493,8 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
   uint8_t* wbuf = mids + expand_mid_bytes(r16);
   uint8_t* tiles = wbuf + 2 * expand_w_bytes(r16);
   const float scale = a.scale != nullptr && adapter ? a.scale[t.group] : 1.f;
-  const bool tma = kTma && t.row0 >= 0;
-  // a tile that ends inside the batch is stored row by row
-  const bool tma_out = tma && (t.count == 128 || t.row0 + t.count == a.M);
+  // a tile that ends inside the batch or is no run of tokens is stored row by row
+  const bool tma_out = kTma && t.row0 >= 0 && (t.count == 128 || t.row0 + t.count == a.M);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&y.w_full[i], 1);
@@ -538,7 +560,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = 0u;
     }
-    if (tma && a.addend != nullptr) mbar_wait(&y.add_full[j % bufs], (j / bufs) & 1, &y.abort, a.st, 27);
+    if (kTma && a.addend != nullptr) mbar_wait(&y.add_full[j % bufs], (j / bufs) & 1, &y.abort, a.st, 27);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       uint8_t* p = buf + swizzled(row, c0 / 8 + q);
@@ -553,7 +575,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
       const int row = (tid >> 3) + 32 * i;
       if (row >= t.count || at >= C) continue;
       const uint4 w = ld_shared_v4(buf + swizzled(row, tid & 7));
-      uint16_t* o = a.out + static_cast<int64_t>(tma ? t.row0 + row : a.perm[t.start + row]) * C + at;
+      uint16_t* o = a.out + static_cast<int64_t>(a.perm[t.start + row]) * C + at;
       if (a.cw == 16) {
         *reinterpret_cast<uint4*>(o) = w;
       } else {
@@ -565,16 +587,13 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
     }
   };
 
-  if (tma) {
-    if (tid == 256) {
-      if (adapter) {
-        mbar_arrive_expect_tx(&y.mid_full, expand_mid_bytes(r16));
-        for (int k = 0; k < expand_blocks(r16); ++k)
-          tma_load_2d(mids + k * 128 * kRowBytes, &a.tmMid, 64 * k, t.row0, &y.mid_full);
-      }
+  if constexpr (kTma) {
+    if (warp == 8) {
+      int rows[4];
+      if (t.row0 < 0) tile_rows(a.perm, t.start, t.count, rows);
       for (int j = 0; j < n; ++j) {
         const int c0 = (j0 + j) * kCols;
-        if (adapter) {
+        if (adapter && lane == 0) {
           uint8_t* ws = wbuf + (j & 1) * expand_w_bytes(r16);
           if (j >= 2) mbar_wait(&y.w_free[j & 1], ((j >> 1) - 1) & 1, &y.abort, a.st, 28);
           if constexpr (kMN) {
@@ -587,9 +606,27 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
           }
         }
         if (a.addend != nullptr) {
-          if (j >= bufs) mbar_wait(&y.add_free[j % bufs], (j / bufs - 1) & 1, &y.abort, a.st, 29);
-          mbar_arrive_expect_tx(&y.add_full[j % bufs], kTileBytes);
-          tma_load_2d(tiles + (j % bufs) * kTileBytes, &a.tmAdd, c0, t.row0, &y.add_full[j % bufs]);
+          uint64_t* bar = &y.add_full[j % bufs];
+          uint8_t* buf = tiles + (j % bufs) * kTileBytes;
+          if (lane == 0) {
+            if (j >= bufs) mbar_wait(&y.add_free[j % bufs], (j / bufs - 1) & 1, &y.abort, a.st, 29);
+            mbar_arrive_expect_tx(bar, kTileBytes);
+            if (t.row0 >= 0) tma_load_2d(buf, &a.tmAdd, c0, t.row0, bar);
+          }
+          __syncwarp();
+          if (t.row0 < 0) tma_gather4(buf + lane * 4 * kRowBytes, &a.tmAdd1, c0, rows, bar);
+        }
+        // mid, the output of the kernel before this one, after the first
+        // tile's W and addend are on their way
+        if (j == 0 && adapter) {
+          grid_dependency_wait();
+          if (lane == 0) mbar_arrive_expect_tx(&y.mid_full, expand_mid_bytes(r16));
+          __syncwarp();
+          for (int k = 0; k < expand_blocks(r16); ++k) {
+            uint8_t* ms = mids + k * 128 * kRowBytes;
+            if (t.row0 < 0) tma_gather4(ms + lane * 4 * kRowBytes, &a.tmMid1, 64 * k, rows, &y.mid_full);
+            else if (lane == 0) tma_load_2d(ms, &a.tmMid, 64 * k, t.row0, &y.mid_full);
+          }
         }
       }
     } else if (tid == 288) {
@@ -631,6 +668,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
     __syncwarp();
   } else if (warp < 8) {
     // the same, gathered by all of warps 0-7, one tile ahead
+    grid_dependency_wait();
     auto load_addend = [&](int j) {
       if (a.addend == nullptr) return;
       const uint32_t buf = smem_u32(tiles) + (j % bufs) * kTileBytes;
@@ -696,6 +734,8 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
     }
     cp_async_wait<0>();
   }
+  grid_dependents_launch();
+  grid_dependency_wait();   // what follows this kernel may rely on what came before it
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(y.tmem, 128);
@@ -704,7 +744,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
 // ---- gradients of A and B ---------------------------------------------------
 
 struct GradArgs {
-  CUtensorMap tmX, tmU;   // with kTma: X and mid, box 64 x 64
+  CUtensorMap tmX, tmU, tmX1, tmU1;   // with kTma: X and mid, box 64 x 64 and 64 x 1
   const uint16_t* mid;    // [M, R]
   const uint16_t* X;      // [M, C]
   uint16_t* grad;         // per group [R, C] (kRankMajor) or [C, R]
@@ -713,8 +753,9 @@ struct GradArgs {
   const int* perm;
   DevStatus* st;
   int64_t C;
-  int M, R, cw, rw;
+  int R, cw, rw;
   bool bf16;
+  bool wait;              // mid is the output of the kernel before this one
 };
 
 __host__ __device__ constexpr int grad_stage_bytes(int r16) {
@@ -735,6 +776,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
   const int cols = static_cast<int>(min(static_cast<int64_t>(128), C - c0));
   uint16_t* grad = a.grad + e * R * C;
   if (tokens == 0) {
+    grid_dependency_wait();
     if (rank == 0)
       for (int i = tid; i < cols * R; i += kThreads)
         grad[kRankMajor ? i / cols * C + c0 + i % cols : c0 * R + i] = 0;
@@ -762,30 +804,60 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
     if (it == n - 1) umma_commit(&y.last);
   };
   // The reduction runs over tokens, so a last block of fewer than 64 must not
-  // reach into the next group's rows: such a group is gathered unless it ends
-  // where the batch does, where the copies fill zeros.
-  if (kTma && run && (tokens % 64 == 0 || first + tokens == a.M)) {
-    if (tid == 0) {
+  // reach into the next group's rows: it is gathered, its last token repeated,
+  // and the repeated rows of mid are set to zero before its products.
+  if constexpr (kTma) {
+    if (tid < 32) {
       uint8_t* stages = smem_raw + (base - smem_u32(smem_raw));
+      const int half = tid >> 4, quad = tid & 15;   // lanes 0-15 fetch the first 64 columns, 16-31 the others
+      if (a.wait) grid_dependency_wait();
       for (int it = 0; it < n; ++it) {
-        const int s = it % kStages, m0 = first + (b0 + it) * 64;
+        const int s = it % kStages, m0 = (b0 + it) * 64;
         uint8_t *xs = stages + s * stage_bytes, *us = xs + 2 * 64 * kRowBytes;
+        const bool box = run && m0 + 64 <= tokens;
+        int rows[4];
+        if (!box)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) rows[i] = a.perm[start + min(m0 + 4 * quad + i, tokens - 1)];
         if (it >= kStages) mbar_wait(&y.done[s], (it / kStages - 1) & 1, &y.abort, a.st, 23);
-        mbar_arrive_expect_tx(&y.full[s], stage_bytes);
-        tma_load_2d(xs, &a.tmX, static_cast<int>(c0), m0, &y.full[s]);
-        tma_load_2d(xs + 64 * kRowBytes, &a.tmX, static_cast<int>(c0) + 64, m0, &y.full[s]);
-        tma_load_2d(us, &a.tmU, 0, m0, &y.full[s]);
-        if (r16 > 64) tma_load_2d(us + 64 * kRowBytes, &a.tmU, 64, m0, &y.full[s]);
+        if (tid == 0) {
+          mbar_arrive_expect_tx(&y.full[s], stage_bytes);
+          if (box) {
+            tma_load_2d(xs, &a.tmX, static_cast<int>(c0), first + m0, &y.full[s]);
+            tma_load_2d(xs + 64 * kRowBytes, &a.tmX, static_cast<int>(c0) + 64, first + m0, &y.full[s]);
+            tma_load_2d(us, &a.tmU, 0, first + m0, &y.full[s]);
+            if (r16 > 64) tma_load_2d(us + 64 * kRowBytes, &a.tmU, 64, first + m0, &y.full[s]);
+          }
+        }
+        __syncwarp();   // the stage is armed before its gathers arrive
+        if (!box) {
+          const int at = (half * 64 + quad * 4) * kRowBytes;
+          tma_gather4(xs + at, &a.tmX1, static_cast<int>(c0) + 64 * half, rows, &y.full[s]);
+          if (half == 0 || r16 > 64) tma_gather4(us + at, &a.tmU1, 64 * half, rows, &y.full[s]);
+        }
       }
-    } else if (tid == 32) {
+    } else if (tid < 64) {
       for (int it = 0; it < n; ++it) {
         mbar_wait(&y.full[it % kStages], (it / kStages) & 1, &y.abort, a.st, 26);
-        tc_fence_after();
-        multiply(it);
+        const int left = tokens - (b0 + it) * 64;
+        if (left < 64) {
+          uint8_t* us = smem_raw + (base - smem_u32(smem_raw)) + it % kStages * stage_bytes + 2 * 64 * kRowBytes;
+          for (int i = left * 8 + (tid & 31); i < 64 * 8; i += 32)
+            for (int k = 0; k < (r16 > 64 ? 2 : 1); ++k)
+              st_shared_v4(us + k * 64 * kRowBytes + i * 16, make_uint4(0, 0, 0, 0));
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (tid == 32) {
+          tc_fence_after();
+          multiply(it);
+        }
+        __syncwarp();
       }
     }
     __syncwarp();
   } else {
+    if (a.wait) grid_dependency_wait();
     // the tokens of a step are read one step before their copies are issued
     constexpr int kMidPer = 4;   // up to 64 rows x 16 chunks of mid over 256 threads
     int xm[4], um[kMidPer];
@@ -842,6 +914,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
   if (n > 0) {
     mbar_wait(&y.last, 0, &y.abort, a.st, 24);
     cp_async_wait<0>();
+    __syncwarp();
     tc_fence_after();
     __syncthreads();
     spill(y.tmem, r16, red);
@@ -849,6 +922,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
     for (int i = tid; i < 128 * red_pitch(r16); i += kThreads) red[i] = 0.f;
   }
   sync_end(y, tmem_columns(r16));
+  grid_dependents_launch();
   cluster_sync();
   const int rows = (128 + ranks - 1) / ranks, row0 = rank * rows;
   const float scale = a.scale != nullptr ? a.scale[e] : 1.f;
@@ -858,6 +932,8 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
       grad[kRankMajor ? j * C + c0 + row : (c0 + row) * R + j] =
           to_16(scale * cluster_sum(base, row * red_pitch(r16) + j, ranks), a.bf16);
   }
+  // what follows this kernel may rely on what came before it
+  grid_dependency_wait();
   cluster_sync();
 }
 
@@ -891,21 +967,25 @@ int split(int64_t tiles, int64_t steps) {
   return static_cast<int>(std::max<int64_t>(1, s));
 }
 
+// after: the kernel before this one in the call's sequence lets it start early
+// (and it waits where it needs that kernel's output).
 template <typename Args>
 cudaError_t launch(void (*kernel)(Args), const Args& a, dim3 grid, int threads, int cluster, int smem, int prof,
-                   cudaStream_t s) {
+                   bool after, cudaStream_t s) {
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = after ? 1 : 0;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   ProfScope ps(prof, s);
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
@@ -940,6 +1020,7 @@ cudaError_t shrink(const Problem& p, const void* X, int64_t C, const void* W, bo
   const dim3 grid(static_cast<unsigned>(ranks * p.plan.slots));
   const bool tma = tma_rows(p, C);
   if (tma && (!make_tmap(&a.tmX, map_type(p), X, C, p.M, C * 2, 64, 128, kSwz) ||
+              !make_tmap(&a.tmX1, map_type(p), X, C, p.M, C * 2, 64, 1, kSwz) ||
               !(mn ? make_tmap_3d(&a.tmW, map_type(p), W, p.R, C, p.E, 2, 64, 64, kSwz)
                    : make_tmap_3d(&a.tmW, map_type(p), W, C, p.R, p.E, 2, 64, r16, kSwz))))
     return cudaErrorUnknown;
@@ -947,7 +1028,7 @@ cudaError_t shrink(const Problem& p, const void* X, int64_t C, const void* W, bo
                 : (mn ? shrink_kernel<true, 4, false> : shrink_kernel<false, 4, false>);
   auto k3 = tma ? (mn ? shrink_kernel<true, 3, true> : shrink_kernel<false, 3, true>)
                 : (mn ? shrink_kernel<true, 3, false> : shrink_kernel<false, 3, false>);
-  return launch(stages == 4 ? k4 : k3, a, grid, kThreads, ranks, smem, K_ADAPTERS, p.s);
+  return launch(stages == 4 ? k4 : k3, a, grid, kThreads, ranks, smem, K_ADAPTERS, false, p.s);
 }
 
 cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, bool mn, const float* scale,
@@ -977,18 +1058,20 @@ cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, 
   const dim3 grid(static_cast<unsigned>(p.plan.slots), static_cast<unsigned>(ceil_div(col_tiles, a.col_tiles)));
   const bool tma = tma_rows(p, C);
   if (tma && (!make_tmap(&a.tmMid, map_type(p), mid, p.R, p.M, p.R * 2, 64, 128, kSwz) ||
+              !make_tmap(&a.tmMid1, map_type(p), mid, p.R, p.M, p.R * 2, 64, 1, kSwz) ||
               !make_tmap(&a.tmAdd, map_type(p), addend != nullptr ? addend : out, C, p.M, C * 2, 64, 128, kSwz) ||
+              !make_tmap(&a.tmAdd1, map_type(p), addend != nullptr ? addend : out, C, p.M, C * 2, 64, 1, kSwz) ||
               !make_tmap(&a.tmOut, map_type(p), out, C, p.M, C * 2, 64, 128, kSwz) ||
               !(mn ? make_tmap_3d(&a.tmW, map_type(p), W, C, p.R, p.E, 2, 64, r16, kSwz)
                    : make_tmap_3d(&a.tmW, map_type(p), W, p.R, C, p.E, 2, 64, 64, kSwz))))
     return cudaErrorUnknown;
   auto kernel = tma ? (mn ? expand_kernel<true, true> : expand_kernel<false, true>)
                     : (mn ? expand_kernel<true, false> : expand_kernel<false, false>);
-  return launch(kernel, a, grid, kExpandThreads, 1, smem, K_ADAPTERS, p.s);
+  return launch(kernel, a, grid, kExpandThreads, 1, smem, K_ADAPTERS, true, p.s);
 }
 
 cudaError_t grad(const Problem& p, const void* mid, const void* X, int64_t C, bool rank_major, const float* scale,
-                 void* out) {
+                 void* out, bool after, bool wait) {
   GradArgs a;
   a.mid = static_cast<const uint16_t*>(mid);
   a.X = static_cast<const uint16_t*>(X);
@@ -998,7 +1081,7 @@ cudaError_t grad(const Problem& p, const void* mid, const void* X, int64_t C, bo
   a.perm = p.plan.perm;
   a.st = p.st;
   a.C = C;
-  a.M = static_cast<int>(p.M);
+  a.wait = wait;
   a.R = p.R;
   a.cw = copy_width(C);
   a.rw = copy_width(p.R);
@@ -1009,13 +1092,15 @@ cudaError_t grad(const Problem& p, const void* mid, const void* X, int64_t C, bo
   const dim3 grid(static_cast<unsigned>(ranks), static_cast<unsigned>(ceil_div(C, 128)), static_cast<unsigned>(p.E));
   const bool tma = tma_rows(p, C);
   if (tma && (!make_tmap(&a.tmX, map_type(p), X, C, p.M, C * 2, 64, 64, kSwz) ||
-              !make_tmap(&a.tmU, map_type(p), mid, p.R, p.M, p.R * 2, 64, 64, kSwz)))
+              !make_tmap(&a.tmU, map_type(p), mid, p.R, p.M, p.R * 2, 64, 64, kSwz) ||
+              !make_tmap(&a.tmX1, map_type(p), X, C, p.M, C * 2, 64, 1, kSwz) ||
+              !make_tmap(&a.tmU1, map_type(p), mid, p.R, p.M, p.R * 2, 64, 1, kSwz)))
     return cudaErrorUnknown;
   auto k4 = tma ? (rank_major ? grad_kernel<true, 4, true> : grad_kernel<false, 4, true>)
                 : (rank_major ? grad_kernel<true, 4, false> : grad_kernel<false, 4, false>);
   auto k3 = tma ? (rank_major ? grad_kernel<true, 3, true> : grad_kernel<false, 3, true>)
                 : (rank_major ? grad_kernel<true, 3, false> : grad_kernel<false, 3, false>);
-  return launch(stages == 4 ? k4 : k3, a, grid, kThreads, ranks, smem, K_ADAPTERS_GRAD, p.s);
+  return launch(stages == 4 ? k4 : k3, a, grid, kThreads, ranks, smem, K_ADAPTERS_GRAD, after, p.s);
 }
 
 cudaError_t forward(const Problem& p, const void* x, const void* A, const void* B, const void* base, void* y,
@@ -1026,16 +1111,19 @@ cudaError_t forward(const Problem& p, const void* x, const void* A, const void* 
 
 cudaError_t backward(const Problem& p, const void* g, const void* x, const void* t, const void* A, const void* B,
                      const void* addend, void* gx, void* gA, void* gB, void* u) {
-  if (gx != nullptr || gA != nullptr) {
+  const bool need_u = gx != nullptr || gA != nullptr;
+  if (need_u) {
     if (cudaError_t e = shrink(p, g, p.N, B, true, p.scale, u)) return e;
+  }
+  // right after the pass over g, of which a part is still in L2; it reads
+  // nothing that the pass wrote
+  if (gB != nullptr) {
+    if (cudaError_t e = grad(p, t, g, p.N, false, p.scale, gB, need_u, false)) return e;
   }
   if (gx != nullptr) {
     if (cudaError_t e = expand(p, u, A, p.K, true, nullptr, addend, gx)) return e;
   }
-  if (gA != nullptr) {
-    if (cudaError_t e = grad(p, u, x, p.K, true, nullptr, gA)) return e;
-  }
-  if (gB != nullptr) return grad(p, t, g, p.N, false, p.scale, gB);
+  if (gA != nullptr) return grad(p, u, x, p.K, true, nullptr, gA, true, true);
   return cudaSuccess;
 }
 

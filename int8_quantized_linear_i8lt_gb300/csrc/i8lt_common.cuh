@@ -320,6 +320,23 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, in
       : "memory");
 }
 
+// 2-D load of 4 rows (y[0..3], each inside the tensor) of one box width at
+// element x into 4 consecutive rows of shared memory; the map's box is one row.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* tm, int x, const int (&y)[4],
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Programmatic dependent launch: wait for the kernel before this one in the
+// stream to complete (at once when this one was launched without the
+// attribute), and let the next one start its prologue.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // 2-D tiled store of a box from shared memory, tracked in the issuing
 // thread's bulk-async groups like bulk_store; what lies outside the tensor is
 // not written.
