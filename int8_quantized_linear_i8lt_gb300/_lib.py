@@ -354,9 +354,12 @@ def i8lt_absmax8_dequantize(q, absmax2, offset, count, out, stream=None) -> int:
     return load().i8lt_absmax8_dequantize(_p(q), _p(absmax2), _p(offset), int(count), _p(out), _p(stream))
 
 
+# The fine-tuning calls are made once per layer and token: addresses go to
+# ctypes as plain ints (None for a NULL).
+
 def i8lt_layer_norm_forward(x, xt, M, N, w, b, wt, eps, y, mean, rstd, stream=None) -> int:
-    return load().i8lt_layer_norm_forward(_p(x), xt, M, N, _p(w), _p(b), wt, eps, _p(y), _p(mean), _p(rstd),
-                                          _p(stream))
+    return load().i8lt_layer_norm_forward(x, xt, M, N, w, b, wt, eps, y, mean, rstd,
+                                          stream)
 
 
 def i8lt_layer_norm_backward_workspace_size(M, N) -> int:
@@ -364,8 +367,8 @@ def i8lt_layer_norm_backward_workspace_size(M, N) -> int:
 
 
 def i8lt_layer_norm_backward(g, x, xt, M, N, mean, rstd, w, wt, gx, gw, gb, ws, ws_bytes, stream=None) -> int:
-    return load().i8lt_layer_norm_backward(_p(g), _p(x), xt, M, N, _p(mean), _p(rstd), _p(w), wt, _p(gx), _p(gw),
-                                           _p(gb), _p(ws), ws_bytes, _p(stream))
+    return load().i8lt_layer_norm_backward(g, x, xt, M, N, mean, rstd, w, wt, gx, gw,
+                                           gb, ws, ws_bytes, stream)
 
 
 def i8lt_adapter_plan_bytes(M, E) -> int:
@@ -373,7 +376,7 @@ def i8lt_adapter_plan_bytes(M, E) -> int:
 
 
 def i8lt_adapter_plan(index, M, E, plan, plan_bytes, stream=None) -> int:
-    return load().i8lt_adapter_plan(_p(index), M, E, _p(plan), plan_bytes, _p(stream))
+    return load().i8lt_adapter_plan(index, M, E, plan, plan_bytes, stream)
 
 
 def i8lt_adapters_workspace_size(M, K, N, E, r) -> int:
@@ -381,28 +384,28 @@ def i8lt_adapters_workspace_size(M, K, N, E, r) -> int:
 
 
 def i8lt_adapters_forward(x, dt, M, K, A, B, E, r, N, scale, plan, base, y, t, ws, ws_bytes, stream=None) -> int:
-    return load().i8lt_adapters_forward(_p(x), dt, M, K, _p(A), _p(B), E, r, N, _p(scale), _p(plan), _p(base), _p(y),
-                                        _p(t), _p(ws), ws_bytes, _p(stream))
+    return load().i8lt_adapters_forward(x, dt, M, K, A, B, E, r, N, scale, plan, base, y,
+                                        t, ws, ws_bytes, stream)
 
 
 def i8lt_adapters_backward(g, x, t, dt, M, K, A, B, E, r, N, scale, plan, addend, gx, gA, gB, ws, ws_bytes,
                            stream=None) -> int:
-    return load().i8lt_adapters_backward(_p(g), _p(x), _p(t), dt, M, K, _p(A), _p(B), E, r, N, _p(scale), _p(plan),
-                                         _p(addend), _p(gx), _p(gA), _p(gB), _p(ws), ws_bytes, _p(stream))
+    return load().i8lt_adapters_backward(g, x, t, dt, M, K, A, B, E, r, N, scale, plan,
+                                         addend, gx, gA, gB, ws, ws_bytes, stream)
 
 
 def i8lt_adamw_step(params, pt, grads, gt, sizes, count, m, v, step, lr, beta1, beta2, eps, weight_decay,
                     grad_scale=None, found_inf=None, stream=None) -> int:
     """params, grads: ctypes arrays of device addresses; sizes: of int64."""
-    return load().i8lt_adamw_step(params, pt, grads, gt, sizes, count, _p(m), _p(v), step, lr, beta1, beta2, eps,
-                                  weight_decay, _p(grad_scale), _p(found_inf), _p(stream))
+    return load().i8lt_adamw_step(params, pt, grads, gt, sizes, count, m, v, step, lr, beta1, beta2, eps,
+                                  weight_decay, grad_scale, found_inf, stream)
 
 
 def i8lt_adamw_step_8bit(params, pt, grads, gt, sizes, count, m, m_absmax, r, r_absmax, step, lr, beta1, beta2, eps,
                          weight_decay, grad_scale=None, found_inf=None, stream=None) -> int:
-    return load().i8lt_adamw_step_8bit(params, pt, grads, gt, sizes, count, _p(m), _p(m_absmax), _p(r), _p(r_absmax),
-                                       step, lr, beta1, beta2, eps, weight_decay, _p(grad_scale), _p(found_inf),
-                                       _p(stream))
+    return load().i8lt_adamw_step_8bit(params, pt, grads, gt, sizes, count, m, m_absmax, r, r_absmax,
+                                       step, lr, beta1, beta2, eps, weight_decay, grad_scale, found_inf,
+                                       stream)
 
 
 def i8lt_silu_forward(h, dt, n, out, stream=None) -> int:

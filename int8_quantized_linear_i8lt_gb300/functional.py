@@ -10,6 +10,7 @@ efficient backward" (see include/i8lt.h for the formulas).
 from __future__ import annotations
 
 import math
+import operator
 import warnings
 
 import torch
@@ -36,7 +37,8 @@ def _code(dtype: torch.dtype) -> int:
 
 
 def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+    # the handle of torch.cuda.current_stream(t.device) without the object around it
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _ptr(t):
@@ -615,48 +617,49 @@ NF4LinearFunction = Linear4bitFunction
 # fine-tuning on top of the frozen layers: layer norm, low-rank adapters, AdamW
 # ---------------------------------------------------------------------------
 
-def _same_device(what: str, first: torch.Tensor, *ts):
-    """All given tensors on one CUDA device."""
-    for t in ts:
-        if t is not None and t.device != first.device:
-            raise I8LTError(f"{what}: tensors on {first.device} and {t.device}")
-
-
-def _expect(what: str, t, shape, dtype):
-    """Shape and dtype of an optional argument."""
+def _arg(what: str, t, dev: int, shape, dtype):
+    """An optional argument after its checks, contiguous: on CUDA device
+    ``dev``, of ``shape`` and of ``dtype`` (None: any)."""
     if t is None:
-        return
-    if tuple(t.shape) != tuple(shape):
+        return None
+    if t.get_device() != dev:
+        raise I8LTError(f"{what}: a tensor on {t.device}, expected cuda:{dev}" if t.is_cuda else
+                        "libi8lt runs on CUDA tensors only (no CPU path)")
+    if t.shape != shape:
         raise I8LTError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise I8LTError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _out(what: str, t: torch.Tensor, dev: int, shape, dtype):
+    """A caller's output buffer after its checks."""
+    if not t.is_contiguous():
+        raise I8LTError(f"{what}: not contiguous")
+    return _arg(what, t, dev, shape, dtype)
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                eps: float = 1e-5, out: torch.Tensor | None = None):
     """(y, mean, rstd) of the layer norm over the last dimension of x [..., N]
     (f16 / bf16 / f32); weight and bias [N] of one dtype (any of the three).
-    mean and rstd are fp32 with x's leading shape, for the backward."""
-    _require_cuda(x, weight, bias, out)
-    if x.dim() == 0:
+    mean and rstd are fp32 with x's leading shape, for the backward.  ``out``
+    may be x itself."""
+    _require_cuda(x)
+    shape = x.shape
+    if not shape:
         raise I8LTError("layer_norm: x has no dimension to normalise")
-    N = x.shape[-1]
+    dev, dtype, N = x.get_device(), x.dtype, shape[-1]
+    if not x.is_contiguous():
+        x = x.contiguous()
+    weight = _arg("layer_norm weight", weight, dev, (N,), None)
     par = weight if weight is not None else bias
-    _same_device("layer_norm", x, weight, bias, out)
-    _expect("layer_norm weight", weight, (N,), None)
-    _expect("layer_norm bias", bias, (N,), None if par is None else par.dtype)
-    _expect("layer_norm out", out, x.shape, x.dtype)
-    if out is not None and not out.is_contiguous():
-        raise I8LTError("layer_norm: out is not contiguous")
-    x = x.contiguous()
-    weight = None if weight is None else weight.contiguous()
-    bias = None if bias is None else bias.contiguous()
-    M = x.numel() // N if N else 0
-    y = torch.empty_like(x) if out is None else out
-    stats = torch.empty(2, *x.shape[:-1], dtype=torch.float32, device=x.device)
-    mean, rstd = stats[0], stats[1]
-    _check(_lib.i8lt_layer_norm_forward(x.data_ptr(), _code(x.dtype), M, N, _ptr(weight), _ptr(bias),
-                                        _code(par.dtype) if par is not None else 0, eps, y.data_ptr(),
+    bias = _arg("layer_norm bias", bias, dev, (N,), None if par is None else par.dtype)
+    y = torch.empty_like(x) if out is None else _out("layer_norm out", out, dev, shape, dtype)
+    mean = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    _check(_lib.i8lt_layer_norm_forward(x.data_ptr(), _code(dtype), x.numel() // N if N else 0, N, _ptr(weight),
+                                        _ptr(bias), 0 if par is None else _code(par.dtype), eps, y.data_ptr(),
                                         mean.data_ptr(), rstd.data_ptr(), _stream(x)), "i8lt_layer_norm_forward")
     return y, mean, rstd
 
@@ -666,28 +669,32 @@ def layer_norm_backward(g: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rs
                         need_bias: bool = True, param_dtype: torch.dtype | None = None):
     """(gx, gw, gb) of ``layer_norm`` (None where not needed).  gw and gb have
     ``param_dtype`` (default: weight's, else x's)."""
-    _require_cuda(g, x, mean, rstd, weight)
-    _same_device("layer_norm_backward", x, g, mean, rstd, weight)
-    N = x.shape[-1]
-    _expect("layer_norm_backward g", g, x.shape, x.dtype)
-    _expect("layer_norm_backward mean", mean, x.shape[:-1], torch.float32)
-    _expect("layer_norm_backward rstd", rstd, x.shape[:-1], torch.float32)
-    _expect("layer_norm_backward weight", weight, (N,), None)
-    if weight is not None and param_dtype not in (None, weight.dtype):
+    _require_cuda(x)
+    shape = x.shape
+    dev, dtype, N = x.get_device(), x.dtype, shape[-1]
+    if not x.is_contiguous():
+        x = x.contiguous()
+    g = _arg("layer_norm_backward g", g, dev, shape, dtype)
+    mean = _arg("layer_norm_backward mean", mean, dev, shape[:-1], torch.float32)
+    rstd = _arg("layer_norm_backward rstd", rstd, dev, shape[:-1], torch.float32)
+    weight = _arg("layer_norm_backward weight", weight, dev, (N,), None)
+    if weight is None:
+        ptype = param_dtype or dtype
+    elif param_dtype not in (None, weight.dtype):
         raise I8LTError(f"layer_norm_backward: param_dtype {param_dtype} with a weight of {weight.dtype}")
-    dtype = weight.dtype if weight is not None else (param_dtype or x.dtype)
+    else:
+        ptype = weight.dtype
     if not (need_x or need_weight or need_bias):
         return None, None, None
-    g, x, mean, rstd = g.contiguous(), x.contiguous(), mean.contiguous(), rstd.contiguous()
-    weight = None if weight is None else weight.contiguous()
     M = x.numel() // N if N else 0
     gx = torch.empty_like(x) if need_x else None
-    gw = torch.empty(N, dtype=dtype, device=x.device) if need_weight else None
-    gb = torch.empty(N, dtype=dtype, device=x.device) if need_bias else None
-    ws = torch.empty(max(_lib.i8lt_layer_norm_backward_workspace_size(M, N), 256), dtype=torch.uint8, device=x.device)
-    _check(_lib.i8lt_layer_norm_backward(g.data_ptr(), x.data_ptr(), _code(x.dtype), M, N, mean.data_ptr(),
-                                         rstd.data_ptr(), _ptr(weight), _code(dtype), _ptr(gx), _ptr(gw), _ptr(gb),
-                                         ws.data_ptr(), ws.numel(), _stream(x)), "i8lt_layer_norm_backward")
+    gw = torch.empty(N, dtype=ptype, device=x.device) if need_weight else None
+    gb = torch.empty(N, dtype=ptype, device=x.device) if need_bias else None
+    n = _lib.i8lt_layer_norm_backward_workspace_size(M, N)
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    _check(_lib.i8lt_layer_norm_backward(g.data_ptr(), x.data_ptr(), _code(dtype), M, N, mean.data_ptr(),
+                                         rstd.data_ptr(), _ptr(weight), _code(ptype), _ptr(gx), _ptr(gw), _ptr(gb),
+                                         ws.data_ptr(), n, _stream(x)), "i8lt_layer_norm_backward")
     return gx, gw, gb
 
 
@@ -736,7 +743,8 @@ def adapter_plan(index: torch.Tensor | None, adapters: int, tokens: int | None =
         _require_cuda(index)
         if index.dtype != torch.int32:
             raise I8LTError(f"adapter_plan: index has dtype {index.dtype}, expected torch.int32")
-        index = index.reshape(-1).contiguous()
+        if not index.is_contiguous():
+            index = index.contiguous()
         M, device = index.numel(), index.device
         if tokens is not None and tokens != M:
             raise I8LTError(f"adapter_plan: {M} indices for {tokens} tokens")
@@ -747,20 +755,23 @@ def adapter_plan(index: torch.Tensor | None, adapters: int, tokens: int | None =
     return AdapterPlan(data, M, adapters)
 
 
-def _adapter_args(what, x, A, B, scale, plan):
-    """Checked sizes (M, K, E, r, N) of an adapter call on x [M, K or N]."""
+def _adapter_args(what, tokens, A, B, scale, plan):
+    """(device, M, K, E, r, N, A, B, scale) of an adapter call, checked, on
+    tokens [M, K or N]."""
+    _require_cuda(tokens, plan.data)
+    dev, dtype = tokens.get_device(), tokens.dtype
+    if tokens.dim() != 2:
+        raise I8LTError(f"{what}: {tokens.dim()}-dimensional tokens, expected [tokens, features]")
     if A.dim() != 3 or B.dim() != 3:
         raise I8LTError(f"{what}: A and B are [adapters, rank, in] and [adapters, out, rank]")
     E, r, K = A.shape
-    N = B.shape[1]
-    _expect(f"{what} B", B, (E, N, r), A.dtype)
-    _expect(f"{what} scale", scale, (E,), torch.float32)
-    if x.dtype != A.dtype:
-        raise I8LTError(f"{what}: tokens of dtype {x.dtype}, adapters of {A.dtype}")
-    if plan.adapters != E or plan.tokens != x.shape[0]:
-        raise I8LTError(f"{what}: a plan of {plan.tokens} tokens and {plan.adapters} adapters for {x.shape[0]} tokens "
-                        f"and {E} adapters")
-    return x.shape[0], K, E, r, N
+    N, M = B.shape[1], tokens.shape[0]
+    if plan.adapters != E or plan.tokens != M or plan.data.get_device() != dev:
+        raise I8LTError(f"{what}: a plan of {plan.tokens} tokens and {plan.adapters} adapters on {plan.data.device} "
+                        f"for {M} tokens and {E} adapters on {tokens.device}")
+    A = _arg(f"{what} A", A, dev, A.shape, dtype)
+    B = _arg(f"{what} B", B, dev, (E, N, r), dtype)
+    return dev, M, K, E, r, N, A, B, _arg(f"{what} scale", scale, dev, (E,), torch.float32)
 
 
 def _adapter_workspace(M, K, N, E, r, device):
@@ -772,24 +783,17 @@ def adapters_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: t
     """(y, t) with t = x A[e]^T and y = base + scale[e] t B[e]^T for each
     token's adapter e (i8lt_adapters_forward): x [M, K] (f16 / bf16),
     A [E, r, K], B [E, N, r], scale fp32 [E] or None, base [M, N] or None.
-    ``out`` may be base itself.  t [M, r] is what the backward needs."""
-    _require_cuda(x, A, B, scale, plan.data, base, out)
-    _same_device("adapters_forward", x, A, B, scale, plan.data, base, out)
-    if x.dim() != 2:
-        raise I8LTError("adapters_forward: x is [tokens, features]")
-    M, K, E, r, N = _adapter_args("adapters_forward", x, A, B, scale, plan)
-    _expect("adapters_forward x", x, (M, K), None)
-    _expect("adapters_forward base", base, (M, N), x.dtype)
-    _expect("adapters_forward out", out, (M, N), x.dtype)
-    if out is not None and not out.is_contiguous():
-        raise I8LTError("adapters_forward: out is not contiguous")
-    x, A, B = x.contiguous(), A.contiguous(), B.contiguous()
-    scale = None if scale is None else scale.contiguous()
-    base = None if base is None else base.contiguous()
-    y = torch.empty(M, N, dtype=x.dtype, device=x.device) if out is None else out
-    t = torch.empty(M, r, dtype=x.dtype, device=x.device)
-    ws = _adapter_workspace(M, K, N, E, r, x.device)
-    _check(_lib.i8lt_adapters_forward(x.data_ptr(), _code(x.dtype), M, K, A.data_ptr(), B.data_ptr(), E, r, N,
+    ``out`` may be base itself (not x).  t [M, r] is what the backward needs."""
+    what = "adapters_forward"
+    dev, M, K, E, r, N, A, B, scale = _adapter_args(what, x, A, B, scale, plan)
+    dtype, device = x.dtype, x.device
+    x = _arg(what, x, dev, (M, K), None)
+    base = _arg("adapters_forward base", base, dev, (M, N), dtype)
+    y = torch.empty((M, N), dtype=dtype, device=device) if out is None else \
+        _out("adapters_forward out", out, dev, (M, N), dtype)
+    t = torch.empty((M, r), dtype=dtype, device=device)
+    ws = _adapter_workspace(M, K, N, E, r, device)
+    _check(_lib.i8lt_adapters_forward(x.data_ptr(), _code(dtype), M, K, A.data_ptr(), B.data_ptr(), E, r, N,
                                       _ptr(scale), plan.data.data_ptr(), _ptr(base), y.data_ptr(), t.data_ptr(),
                                       ws.data_ptr(), ws.numel(), _stream(x)), "i8lt_adapters_forward")
     return y, t
@@ -802,29 +806,22 @@ def adapters_backward(g: torch.Tensor, x: torch.Tensor | None, t: torch.Tensor |
     """(gx, gA, gB) of ``adapters_forward`` (None where not needed), gx with
     ``addend`` (the shared projection's input gradient) added.  x is used for
     gA only, t for gB only."""
-    _require_cuda(g, x, t, A, B, scale, plan.data, addend)
-    _same_device("adapters_backward", g, x, t, A, B, scale, plan.data, addend)
-    if g.dim() != 2:
-        raise I8LTError("adapters_backward: g is [tokens, features]")
-    M, K, E, r, N = _adapter_args("adapters_backward", g, A, B, scale, plan)
-    _expect("adapters_backward g", g, (M, N), None)
+    what = "adapters_backward"
+    dev, M, K, E, r, N, A, B, scale = _adapter_args(what, g, A, B, scale, plan)
     if need_A and x is None or need_B and t is None:
         raise I8LTError("adapters_backward: gA needs x and gB needs t")
-    _expect("adapters_backward x", x, (M, K), g.dtype)
-    _expect("adapters_backward t", t, (M, r), g.dtype)
-    _expect("adapters_backward addend", addend, (M, K), g.dtype)
+    dtype, device = g.dtype, g.device
+    g = _arg("adapters_backward g", g, dev, (M, N), None)
+    x = _arg("adapters_backward x", x, dev, (M, K), dtype)
+    t = _arg("adapters_backward t", t, dev, (M, r), dtype)
+    addend = _arg("adapters_backward addend", addend, dev, (M, K), dtype)
     if not (need_x or need_A or need_B):
         return None, None, None
-    g, A, B = g.contiguous(), A.contiguous(), B.contiguous()
-    x = None if x is None else x.contiguous()
-    t = None if t is None else t.contiguous()
-    scale = None if scale is None else scale.contiguous()
-    addend = None if addend is None else addend.contiguous()
-    gx = torch.empty(M, K, dtype=g.dtype, device=g.device) if need_x else None
+    gx = torch.empty((M, K), dtype=dtype, device=device) if need_x else None
     gA = torch.empty_like(A) if need_A else None
     gB = torch.empty_like(B) if need_B else None
-    ws = _adapter_workspace(M, K, N, E, r, g.device)
-    _check(_lib.i8lt_adapters_backward(g.data_ptr(), _ptr(x), _ptr(t), _code(g.dtype), M, K, A.data_ptr(),
+    ws = _adapter_workspace(M, K, N, E, r, device)
+    _check(_lib.i8lt_adapters_backward(g.data_ptr(), _ptr(x), _ptr(t), _code(dtype), M, K, A.data_ptr(),
                                        B.data_ptr(), E, r, N, _ptr(scale), plan.data.data_ptr(), _ptr(addend),
                                        _ptr(gx), _ptr(gA), _ptr(gB), ws.data_ptr(), ws.numel(), _stream(g)),
            "i8lt_adapters_backward")
@@ -864,35 +861,42 @@ def adamw_state_size(params) -> int:
     return sum(-(-p.numel() // blk) * blk for p in params)
 
 
+_data_ptr, _size, _get_device = torch.Tensor.data_ptr, torch.Tensor.size, torch.Tensor.get_device
+_is_contiguous, _numel, _dtype_of = torch.Tensor.is_contiguous, torch.Tensor.numel, operator.attrgetter("dtype")
+
+
 def _adamw_lists(what, params, grads):
-    """ctypes arrays of the device addresses and sizes, and the dtypes."""
-    if len(params) != len(grads):
-        raise I8LTError(f"{what}: {len(params)} parameters, {len(grads)} gradients")
-    if not params:
-        return None
-    p0 = params[0]
-    pt, gt, dev = p0.dtype, None, p0.device
-    held = []
-    for p, g in zip(params, grads):
-        if p.dtype != pt or p.device != dev:
-            raise I8LTError(f"{what}: parameters of one dtype on one device are expected")
-        if not p.is_contiguous():
-            raise I8LTError(f"{what}: a parameter is not contiguous")
-        if g is not None:
-            gt = gt or g.dtype
-            if g.dtype != gt or g.device != dev:
-                raise I8LTError(f"{what}: gradients of one dtype on the parameters' device are expected")
-            if p.shape != g.shape:
-                raise I8LTError(f"{what}: a parameter of shape {tuple(p.shape)} with a gradient of {tuple(g.shape)}")
-            g = g if g.is_contiguous() else g.contiguous()
-        held.append(g)
-    _require_cuda(p0)
-    if gt is None:
-        return None
+    """(a parameter, what must outlive the call, count, ctypes arrays of the
+    device addresses and sizes, dtypes, elements of a state), checked.  Called
+    for hundreds of tensors per step: each property is read in one sweep."""
     n = len(params)
-    return (p0, held, n, (_lib.c_void_p * n)(*[p.data_ptr() for p in params]),
-            (_lib.c_void_p * n)(*[_ptr(g) for g in held]),
-            (_lib.c_int64 * n)(*[p.numel() for p in params]), _code(pt), _code(gt))
+    if n != len(grads):
+        raise I8LTError(f"{what}: {n} parameters, {len(grads)} gradients")
+    present = params, grads
+    if any([g is None for g in grads]):
+        pairs = [(p, g) for p, g in zip(params, grads) if g is not None]
+        present = [p for p, _ in pairs], [g for _, g in pairs]
+    if not present[1]:
+        return None
+    p0, g0 = params[0], present[1][0]
+    _require_cuda(p0)
+    if set(map(_dtype_of, params)) != {p0.dtype} or set(map(_dtype_of, present[1])) != {g0.dtype}:
+        raise I8LTError(f"{what}: parameters of one dtype and gradients of one dtype are expected")
+    if set(map(_get_device, params)) | set(map(_get_device, present[1])) != {p0.get_device()}:
+        raise I8LTError(f"{what}: tensors on {p0.device} and another device")
+    if not all(map(_is_contiguous, params)):
+        raise I8LTError(f"{what}: a parameter is not contiguous")
+    if list(map(_size, present[0])) != list(map(_size, present[1])):
+        raise I8LTError(f"{what}: a gradient has another shape than its parameter")
+    held = grads
+    if not all(map(_is_contiguous, present[1])):
+        held = [None if g is None else g.contiguous() for g in grads]
+    sizes = list(map(_numel, params))
+    blk = _lib.I8LT_ADAMW_BLOCK
+    total = sum([(k + blk - 1) // blk for k in sizes]) * blk
+    addresses = map(_data_ptr, held) if present[1] is grads else map(_ptr, held)
+    return (p0, held, n, (_lib.c_void_p * n)(*map(_data_ptr, params)), (_lib.c_void_p * n)(*addresses),
+            (_lib.c_int64 * n)(*sizes), _code(p0.dtype), _code(g0.dtype), total)
 
 
 def _adamw_state(what, size, dtype, device, *ts):
@@ -915,11 +919,10 @@ def adamw_step(params, grads, m: torch.Tensor, v: torch.Tensor, step: int, lr: f
     A parameter whose gradient is None stays as it is.  grad_scale multiplies
     every gradient; a found_inf other than 0 makes the step change nothing
     (both fp32 CUDA tensors of one element)."""
-    size = adamw_state_size(params)
     lists = _adamw_lists("adamw_step", params, grads)
     if lists is None:
         return
-    p0, held, n, pp, gp, sizes, pt, gt = lists
+    p0, held, n, pp, gp, sizes, pt, gt, size = lists
     _adamw_state("adamw_step", size, torch.float32, p0.device, m, v)
     _adamw_scalar("adamw_step", grad_scale, p0.device)
     _adamw_scalar("adamw_step", found_inf, p0.device)
@@ -934,11 +937,10 @@ def adamw_step_8bit(params, grads, m: torch.Tensor, m_absmax: torch.Tensor, r: t
     """``adamw_step`` with 8-bit states (i8lt_adamw_step_8bit): m and
     r = sqrt(v) as flat float8_e4m3fn tensors of ``adamw_state_size(params)``
     elements, m_absmax and r_absmax fp32, one per 256 elements."""
-    size = adamw_state_size(params)
     lists = _adamw_lists("adamw_step_8bit", params, grads)
     if lists is None:
         return
-    p0, held, n, pp, gp, sizes, pt, gt = lists
+    p0, held, n, pp, gp, sizes, pt, gt, size = lists
     _adamw_state("adamw_step_8bit", size, torch.float8_e4m3fn, p0.device, m, r)
     _adamw_state("adamw_step_8bit", size // _lib.I8LT_ADAMW_BLOCK, torch.float32, p0.device, m_absmax, r_absmax)
     _adamw_scalar("adamw_step_8bit", grad_scale, p0.device)
