@@ -16,7 +16,13 @@ namespace i8lt {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 128;   // tokens per tile of the plan
+constexpr int kTile = 128;       // tokens per tile of the plan
+constexpr int kFewTile = 8;      // tokens per tile of a small batch's second list
+// Batches of up to this many tokens take the kernel for few tokens.  256
+// tokens of one adapter, 4096 -> 4096, rank 16: 11 us by it, 25 us by the two
+// kernels of long batches; 512 tokens, 4096 -> 11008, rank 64: 49 us against
+// 33 us.
+constexpr int64_t kFewTokens = 256;
 
 // The plan: tokens sorted by adapter, those without one (group E) last, and
 // tiles of at most kTile tokens of one group.  Group e's tiles take the slots
@@ -31,7 +37,8 @@ struct Plan {
   int* offset;    // [E + 2]
   int* perm;      // [M] token at each sorted place
   Tile* tiles;    // [slots]
-  int64_t slots;
+  Tile* few;      // [few_slots] up to kFewTokens tokens: tiles of kFewTile, one after another, then empty ones
+  int64_t slots, few_slots;
   size_t bytes;
 };
 
@@ -46,6 +53,9 @@ Plan plan_layout(void* base, int64_t M, int64_t E) {
   off += round_up(M * 4, 256);
   p.tiles = reinterpret_cast<Tile*>(b + off);
   off += round_up(p.slots * static_cast<int64_t>(sizeof(Tile)), 256);
+  p.few_slots = M <= kFewTokens ? std::min(M, M / kFewTile + E + 1) : 0;
+  p.few = reinterpret_cast<Tile*>(b + off);
+  off += round_up(p.few_slots * static_cast<int64_t>(sizeof(Tile)), 256);
   p.bytes = off;
   return p;
 }
@@ -53,24 +63,31 @@ Plan plan_layout(void* base, int64_t M, int64_t E) {
 // One block per group: counts the tokens of the groups before it, then places
 // its own in order (a stable sort, the same on every run) and fills its slots.
 // A thread takes 8 consecutive tokens per pass, so that a batch of 8192 is one
-// pass of 1024 threads: 6 us, against 35 us for a warp per group.
-template <int kThreadsPlan>
-__global__ void __launch_bounds__(kThreadsPlan) adapter_plan_kernel(const int32_t* index, int M, int E, int* offset,
+// pass of 1024 threads (FIGURE us, against 35 us for a warp per group).
+constexpr int kPlanThreads = 1024;
+__global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const int32_t* index, int M, int E, int* offset,
                                                                     int* perm, Tile* tiles) {
-  constexpr int kWarpsPlan = kThreadsPlan / 32, kPer = 8;
+  constexpr int kWarpsPlan = kPlanThreads / 32, kPer = 8;
   __shared__ int counts[2][kWarpsPlan];
   const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto load = [&](int m0, int(&v)[kPer]) {   // the groups of 8 tokens, -1 past the end
+    if (index == nullptr) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int m = m0 + i, g = m >= M ? -1 : index != nullptr ? index[m] : 0;
-      v[i] = m >= M ? -1 : g >= 0 && g < E ? g : E;
+      for (int i = 0; i < kPer; ++i) v[i] = 0;
+    } else if (m0 + kPer <= M && (reinterpret_cast<uintptr_t>(index) & 15u) == 0) {
+      *reinterpret_cast<int4*>(v) = __ldg(reinterpret_cast<const int4*>(index + m0));
+      *reinterpret_cast<int4*>(v + 4) = __ldg(reinterpret_cast<const int4*>(index + m0 + 4));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] = m0 + i < M ? index[m0 + i] : 0;
     }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = m0 + i >= M ? -1 : v[i] >= 0 && v[i] < E ? v[i] : E;
   };
-  int v[kPer];
+  __align__(16) int v[kPer];
   // tokens of the groups before e
   int n = 0;
-  for (int m0 = tid * kPer; m0 < M; m0 += kThreadsPlan * kPer) {
+  for (int m0 = tid * kPer; m0 < M; m0 += kPlanThreads * kPer) {
     load(m0, v);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) n += v[i] >= 0 && v[i] < e;
@@ -81,7 +98,7 @@ __global__ void __launch_bounds__(kThreadsPlan) adapter_plan_kernel(const int32_
   int before = 0;
   for (int k = 0; k < kWarpsPlan; ++k) before += counts[0][k];
   int placed = 0;
-  for (int base = 0, turn = 1; base < M; base += kThreadsPlan * kPer, ++turn) {
+  for (int base = 0, turn = 1; base < M; base += kPlanThreads * kPer, ++turn) {
     load(base + tid * kPer, v);
     int mine = 0;
 #pragma unroll
@@ -111,13 +128,79 @@ __global__ void __launch_bounds__(kThreadsPlan) adapter_plan_kernel(const int32_
     if (e == E) offset[E + 1] = M;
   }
   const int slot0 = before / kTile + e, slot1 = (before + placed) / kTile + e + 1;
-  for (int s = slot0 + tid; s < slot1; s += kThreadsPlan) {
+  for (int s = slot0 + tid; s < slot1; s += kPlanThreads) {
     const int start = before + (s - slot0) * kTile;
     const int count = max(0, min(kTile, before + placed - start));
     int row0 = -1;
     if (count > 0 && perm[start + count - 1] - perm[start] == count - 1) row0 = perm[start];
     tiles[s] = Tile{e, start, count, row0};
   }
+}
+
+// The plan of up to kFewTokens tokens, by one block whatever the number of
+// adapters: a token's place is the number of tokens before it in (group,
+// index) order.
+__global__ void __launch_bounds__(kFewTokens) adapter_plan_few_kernel(const int32_t* index, int M, int E, int* offset,
+                                                                      int* perm, Tile* tiles, Tile* few,
+                                                                      int few_slots) {
+  __shared__ __align__(16) int group[kFewTokens];
+  __shared__ int sorted[kFewTokens], place[kFewTokens], counts[kFewTokens / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int g = E + 1;   // past the end: after every token
+  if (tid < M) {
+    const int i = index != nullptr ? index[tid] : 0;
+    g = i >= 0 && i < E ? i : E;
+  }
+  group[tid] = g;
+  __syncthreads();
+  if (tid < M) {
+    int at = 0;
+#pragma unroll 4
+    for (int j = 0; j < M; j += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(group + j);
+      at += (o.x < g || (o.x == g && j < tid)) + (o.y < g || (o.y == g && j + 1 < tid)) +
+            (o.z < g || (o.z == g && j + 2 < tid)) + (o.w < g || (o.w == g && j + 3 < tid));
+    }
+    sorted[at] = g;
+    place[at] = tid;
+    perm[at] = tid;
+  }
+  __syncthreads();
+  auto first_of = [&](int e) {   // the first place whose group is e or later
+    int lo = 0, hi = M;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sorted[mid] < e) lo = mid + 1;
+      else hi = mid;
+    }
+    return lo;
+  };
+  for (int e = tid; e <= E; e += kFewTokens) {
+    const int before = first_of(e), end = first_of(e + 1);
+    offset[e] = before;
+    if (e == E) offset[E + 1] = M;
+    for (int s = before / kTile + e, start = before; s <= end / kTile + e; ++s, start += kTile) {
+      const int count = max(0, min(kTile, end - start));
+      const bool run = count > 0 && place[start + count - 1] - place[start] == count - 1;
+      tiles[s] = Tile{e, start, count, run ? place[start] : -1};
+    }
+  }
+  bool head = false;
+  int end = 0;
+  if (tid < M) {
+    head = (tid - first_of(sorted[tid])) % kFewTile == 0;
+    end = first_of(sorted[tid] + 1);
+  }
+  const unsigned heads = __ballot_sync(0xffffffffu, head);
+  if (lane == 0) counts[warp] = __popc(heads);
+  __syncthreads();
+  int at = __popc(heads & ((1u << lane) - 1)), all = 0;
+  for (int k = 0; k < static_cast<int>(kFewTokens) / 32; ++k) {
+    if (k < warp) at += counts[k];
+    all += counts[k];
+  }
+  if (head) few[at] = Tile{sorted[tid], tid, min(kFewTile, end - tid), -1};
+  for (int s = all + tid; s < few_slots; s += kFewTokens) few[s] = Tile{E, 0, 0, -1};
 }
 
 // ---- shared pieces of the three products ----------------------------------
@@ -286,7 +369,7 @@ struct ShrinkArgs {
   const float* scale;     // applied when not NULL
   const Tile* tiles;
   const int* perm;
-  DevStatus* st;
+  DevStatus* st;          // cleared by the first kernel of a call
   int64_t C;
   int R, E, cw, rw;       // cw, rw: copy widths of rows of C and of R elements
   int ranks;              // CTAs per cluster
@@ -305,11 +388,12 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   __shared__ Sync y;
   const int ranks = a.ranks, rank = blockIdx.x % ranks;
+  grid_dependency_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.st = DevStatus{0, 0, 0, 0};
   const Tile t = a.tiles[blockIdx.x / ranks];
   if (t.count == 0) return;
   const int tid = threadIdx.x, R = a.R, r16 = rank16(R);
   if (t.group >= a.E) {
-    grid_dependency_wait();
     if (rank == 0)
       for (int i = tid; i < t.count * R; i += kThreads)
         a.mid[static_cast<int64_t>(a.perm[t.start + i / R]) * R + i % R] = 0;
@@ -340,7 +424,6 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
       uint8_t* stages = smem_raw + (base - smem_u32(smem_raw));
       int rows[4];
       if (t.row0 < 0) tile_rows(a.perm, t.start, t.count, rows);
-      grid_dependency_wait();
       for (int it = 0; it < n; ++it) {
         const int s = it % kStages, c0 = (b0 + it) * 64;
         uint8_t *xs = stages + s * stage_bytes, *ws = xs + 128 * kRowBytes;
@@ -367,7 +450,6 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
     }
     __syncwarp();
   } else {
-    grid_dependency_wait();
     // this thread's rows of X: 8 threads a row
     const uint16_t* xrow[4];
 #pragma unroll
@@ -755,6 +837,7 @@ struct GradArgs {
   int64_t C;
   int R, cw, rw;
   bool bf16;
+  bool first;             // the call's first kernel: clears the status
   bool wait;              // mid is the output of the kernel before this one
 };
 
@@ -772,6 +855,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
   const int tid = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x, R = a.R, r16 = rank16(R);
   const int64_t C = a.C, c0 = static_cast<int64_t>(blockIdx.y) * 128;
   const int64_t e = blockIdx.z;
+  if (a.first && blockIdx.x == 0 && blockIdx.y == 0 && e == 0 && tid == 0) *a.st = DevStatus{0, 0, 0, 0};
   const int start = a.offset[e], tokens = a.offset[e + 1] - start;
   const int cols = static_cast<int>(min(static_cast<int64_t>(128), C - c0));
   uint16_t* grad = a.grad + e * R * C;
@@ -937,6 +1021,169 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
   cluster_sync();
 }
 
+// ---- few tokens: t and y in one launch --------------------------------------
+
+struct FewArgs {
+  const uint16_t *x, *A, *B, *base;   // base or NULL; may be y
+  uint16_t *y, *t;
+  const float* scale;
+  const Tile* tiles;
+  const int* perm;
+  DevStatus* st;
+  int64_t K, N;
+  int R, E;
+};
+
+// D (16 x 8) += A (16 x 16) B (16 x 8).  A thread's 4 + 4 elements of a row of
+// A and of a column of B may stand for any 4 of the 16 places of the
+// reduction, as long as both take the same: it holds consecutive ones.
+template <bool kBf16>
+__device__ __forceinline__ void mma_16x8(float (&d)[4], uint2 a0, uint2 a1, uint2 b) {
+  if constexpr (kBf16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0.x), "r"(a1.x), "r"(a0.y), "r"(a1.y), "r"(b.x), "r"(b.y));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0.x), "r"(a1.x), "r"(a0.y), "r"(a1.y), "r"(b.x), "r"(b.y));
+}
+
+// One cluster of 8 CTAs per tile of up to 8 tokens of one adapter.  Each CTA
+// reads an eighth of A[e] and of the tokens' features straight into the
+// operands of warp products (ranks as the rows, tokens as the columns), the
+// cluster adds up t, then each CTA turns an eighth of B[e] into an eighth of
+// y.  Bound by reading A[e] and B[e] once; B's part is on its way to L2 while
+// t is formed.  A tensor-memory tile would be empty but for these 8 rows of
+// 128, and the two kernels of long batches cost two launches: 64 tokens of 64
+// adapters, 4096 -> 4096, rank 16, took 18 + 29 us by them.
+constexpr int kFewRanks = 8;
+template <bool kBf16, int kMaxRankTiles>   // tiles of 16 ranks
+__global__ void __launch_bounds__(kThreads, kMaxRankTiles > 4 ? 2 : kMaxRankTiles > 1 ? 3 : 4) few_kernel(const FewArgs a) {
+  __shared__ __align__(16) float part[kThreads / 32][kMaxRankTiles * 16 * kFewTile];   // per warp, then the CTA's sum
+  __shared__ __align__(16) uint16_t ts[kFewTile][kMaxRankTiles * 16 + 8];
+  __shared__ __align__(16) float ys[2][kFewTile][128 + 4];
+  grid_dependency_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.st = DevStatus{0, 0, 0, 0};
+  const Tile tile = a.tiles[blockIdx.x / kFewRanks];
+  if (tile.count == 0) return;
+  const int rank = blockIdx.x % kFewRanks, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, q = lane & 3;
+  const int R = a.R, r16 = rank16(R), tiles16 = r16 / 16;
+  const bool adapter = tile.group < a.E;
+  const int64_t K = a.K, N = a.N;
+  // this CTA's columns of y, in steps of 128
+  const int64_t steps = (N + 127) / 128;
+  const int64_t s0 = steps * rank / kFewRanks, s1 = steps * (rank + 1) / kFewRanks;
+  const uint16_t* B = a.B + static_cast<int64_t>(adapter ? tile.group : 0) * N * R;
+  const int64_t m_of = a.perm[tile.start + min(g, tile.count - 1)];
+  if (adapter) {
+    if (tid == 0 && s1 > s0) {
+      const int64_t bytes = (min(s1 * 128, N) - s0 * 128) * R * 2;   // rows of B are whole 16-byte units
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(B + s0 * 128 * R),
+                   "r"(static_cast<uint32_t>(min(bytes, static_cast<int64_t>(1) << 22)))
+                   : "memory");
+    }
+    const uint16_t* A = a.A + static_cast<int64_t>(tile.group) * R * K;
+    const uint16_t* x = a.x + m_of * K;
+    const int64_t blocks = (K + 31) / 32;
+    const int64_t k1 = blocks * (rank + 1) / kFewRanks;
+    float d[kMaxRankTiles][4];
+#pragma unroll
+    for (int i = 0; i < kMaxRankTiles; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 2
+    for (int64_t kb = blocks * rank / kFewRanks + warp; kb < k1; kb += kThreads / 32) {
+      const int64_t k = kb * 32 + q * 8;
+      const bool in = k < K;
+      const uint4 b = in && g < tile.count ? __ldg(reinterpret_cast<const uint4*>(x + k)) : zero;
+#pragma unroll
+      for (int i = 0; i < kMaxRankTiles; ++i) {
+        if (i >= tiles16) break;
+        const int r0 = i * 16 + g, r1 = r0 + 8;
+        const uint4 u = in && r0 < R ? __ldg(reinterpret_cast<const uint4*>(A + r0 * K + k)) : zero;
+        const uint4 v = in && r1 < R ? __ldg(reinterpret_cast<const uint4*>(A + r1 * K + k)) : zero;
+        mma_16x8<kBf16>(d[i], make_uint2(u.x, u.y), make_uint2(v.x, v.y), make_uint2(b.x, b.y));
+        mma_16x8<kBf16>(d[i], make_uint2(u.z, u.w), make_uint2(v.z, v.w), make_uint2(b.z, b.w));
+      }
+    }
+    // d: ranks g and g + 8 of each 16, tokens 2 q and 2 q + 1
+#pragma unroll
+    for (int i = 0; i < kMaxRankTiles; ++i) {
+      if (i >= tiles16) break;
+      *reinterpret_cast<float2*>(&part[warp][(i * 16 + g) * kFewTile + 2 * q]) = make_float2(d[i][0], d[i][1]);
+      *reinterpret_cast<float2*>(&part[warp][(i * 16 + g + 8) * kFewTile + 2 * q]) = make_float2(d[i][2], d[i][3]);
+    }
+    __syncthreads();
+    for (int i = tid; i < r16 * kFewTile; i += kThreads) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) s += part[w][i];
+      part[0][i] = s;   // read and written by this thread alone
+    }
+    cluster_sync();
+    for (int i = tid; i < r16 * kFewTile; i += kThreads) {
+      const float s = cluster_sum(smem_u32(part[0]), i, kFewRanks);
+      ts[i % kFewTile][i / kFewTile] = to_16(s, kBf16);
+    }
+    __syncthreads();
+  }
+  if (rank == 0)
+    for (int i = tid; i < tile.count * R; i += kThreads)
+      a.t[static_cast<int64_t>(a.perm[tile.start + i / R]) * R + i % R] = adapter ? ts[i / R][i % R] : uint16_t(0);
+  // y: warp w on columns 16 w .. 16 w + 15 of a step, then every warp on a token
+  const float scale = adapter ? (a.scale != nullptr ? a.scale[tile.group] : 1.f) : 0.f;
+  const int64_t m = a.perm[tile.start + min(warp, tile.count - 1)];
+  for (int64_t s = s0; s < s1; ++s) {
+    const int64_t col = s * 128 + lane * 4;
+    const bool out = warp < tile.count && col < N;
+    uint2 base = make_uint2(0, 0);
+    if (out && a.base != nullptr) base = *reinterpret_cast<const uint2*>(a.base + m * N + col);
+    if (adapter) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      const int64_t c0 = s * 128 + warp * 16 + g, c1 = c0 + 8;
+      const uint2 zero = make_uint2(0, 0);
+#pragma unroll 4
+      for (int i = 0; i < tiles16; ++i) {
+        const int k = i * 16 + q * 4;
+        const bool in = k < R;
+        const uint2 u = in && c0 < N ? __ldg(reinterpret_cast<const uint2*>(B + c0 * R + k)) : zero;
+        const uint2 v = in && c1 < N ? __ldg(reinterpret_cast<const uint2*>(B + c1 * R + k)) : zero;
+        mma_16x8<kBf16>(d, u, v, in ? *reinterpret_cast<const uint2*>(&ts[g][k]) : zero);
+      }
+      float(*buf)[128 + 4] = ys[s & 1];
+      const int c = warp * 16 + g;
+      buf[2 * q][c] = d[0];
+      buf[2 * q + 1][c] = d[1];
+      buf[2 * q][c + 8] = d[2];
+      buf[2 * q + 1][c + 8] = d[3];
+      __syncthreads();
+    }
+    if (!out) continue;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (adapter) v = *reinterpret_cast<const float4*>(&ys[s & 1][warp][lane * 4]);
+    float f[4] = {v.x, v.y, v.z, v.w};
+    uint32_t* w = reinterpret_cast<uint32_t*>(&base);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float lo, hi;
+      if constexpr (kBf16) {
+        lo = __uint_as_float(w[i] << 16);
+        hi = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        lo = h.x;
+        hi = h.y;
+      }
+      lo = fmaf(scale, f[2 * i], lo);
+      hi = fmaf(scale, f[2 * i + 1], hi);
+      w[i] = to_16(lo, kBf16) | (static_cast<uint32_t>(to_16(hi, kBf16)) << 16);
+    }
+    *reinterpret_cast<uint2*>(a.y + m * N + col) = base;
+  }
+  if (adapter) cluster_sync();   // the other CTAs have read this one's sums
+}
+
 // ---- launches ---------------------------------------------------------------
 
 struct Problem {
@@ -967,8 +1214,8 @@ int split(int64_t tiles, int64_t steps) {
   return static_cast<int>(std::max<int64_t>(1, s));
 }
 
-// after: the kernel before this one in the call's sequence lets it start early
-// (and it waits where it needs that kernel's output).
+// after: it may start before the kernel ahead of it in the stream has ended
+// (it waits for that where it first needs anything written before it).
 template <typename Args>
 cudaError_t launch(void (*kernel)(Args), const Args& a, dim3 grid, int threads, int cluster, int smem, int prof,
                    bool after, cudaStream_t s) {
@@ -1028,7 +1275,7 @@ cudaError_t shrink(const Problem& p, const void* X, int64_t C, const void* W, bo
                 : (mn ? shrink_kernel<true, 4, false> : shrink_kernel<false, 4, false>);
   auto k3 = tma ? (mn ? shrink_kernel<true, 3, true> : shrink_kernel<false, 3, true>)
                 : (mn ? shrink_kernel<true, 3, false> : shrink_kernel<false, 3, false>);
-  return launch(stages == 4 ? k4 : k3, a, grid, kThreads, ranks, smem, K_ADAPTERS, false, p.s);
+  return launch(stages == 4 ? k4 : k3, a, grid, kThreads, ranks, smem, K_ADAPTERS, true, p.s);
 }
 
 cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, bool mn, const float* scale,
@@ -1082,6 +1329,7 @@ cudaError_t grad(const Problem& p, const void* mid, const void* X, int64_t C, bo
   a.st = p.st;
   a.C = C;
   a.wait = wait;
+  a.first = !after;
   a.R = p.R;
   a.cw = copy_width(C);
   a.rw = copy_width(p.R);
@@ -1105,6 +1353,17 @@ cudaError_t grad(const Problem& p, const void* mid, const void* X, int64_t C, bo
 
 cudaError_t forward(const Problem& p, const void* x, const void* A, const void* B, const void* base, void* y,
                     void* t) {
+  if (p.plan.few_slots > 0 && p.K % 8 == 0 && p.N % 8 == 0 && p.R % 8 == 0) {
+    const FewArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(A),
+                    static_cast<const uint16_t*>(B), static_cast<const uint16_t*>(base),
+                    static_cast<uint16_t*>(y), static_cast<uint16_t*>(t), p.scale, p.plan.few, p.plan.perm,
+                    p.st, p.K, p.N, p.R, static_cast<int>(p.E)};
+    const dim3 grid(static_cast<unsigned>(p.plan.few_slots * kFewRanks));
+    auto kernel = p.R <= 16   ? (p.bf16 ? few_kernel<true, 1> : few_kernel<false, 1>)
+                  : p.R <= 64 ? (p.bf16 ? few_kernel<true, 4> : few_kernel<false, 4>)
+                              : (p.bf16 ? few_kernel<true, 8> : few_kernel<false, 8>);
+    return launch(kernel, a, grid, kThreads, kFewRanks, 0, K_ADAPTERS, true, p.s);
+  }
   if (cudaError_t e = shrink(p, x, p.K, A, false, nullptr, t)) return e;
   return expand(p, t, B, p.N, false, p.scale, base, y);
 }
@@ -1156,13 +1415,12 @@ int i8lt_adapter_plan(const int32_t* index, int64_t M, int64_t E, void* plan, si
   const Plan p = plan_layout(plan, M, E);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ProfScope ps(K_ADAPTER_PLAN, s);
-  const unsigned groups = static_cast<unsigned>(E + 1);
-  if (M <= 2048)
-    adapter_plan_kernel<256><<<groups, 256, 0, s>>>(index, static_cast<int>(M), static_cast<int>(E), p.offset, p.perm,
-                                                    p.tiles);
+  if (p.few_slots > 0 || M == 0)
+    adapter_plan_few_kernel<<<1, kFewTokens, 0, s>>>(index, static_cast<int>(M), static_cast<int>(E), p.offset, p.perm,
+                                                     p.tiles, p.few, static_cast<int>(p.few_slots));
   else
-    adapter_plan_kernel<1024><<<groups, 1024, 0, s>>>(index, static_cast<int>(M), static_cast<int>(E), p.offset,
-                                                      p.perm, p.tiles);
+    adapter_plan_kernel<<<static_cast<unsigned>(E + 1), kPlanThreads, 0, s>>>(
+        index, static_cast<int>(M), static_cast<int>(E), p.offset, p.perm, p.tiles);
   return cuda_status(cudaGetLastError());
 }
 
@@ -1184,8 +1442,7 @@ int i8lt_adapters_forward(const void* x, int dt, int64_t M, int64_t K, const voi
   if (ws == nullptr || ws_bytes < i8lt_adapters_workspace_size(M, K, N, E, r)) return I8LT_ERR_WORKSPACE;
   if (int d = check_device()) return d;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(ws, 0, sizeof(DevStatus), s) != cudaSuccess) return I8LT_ERR_CUDA;
-  if (M == 0) return I8LT_OK;
+  if (M == 0) return cuda_status(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s));
   const Problem p{M, K, N, E, static_cast<int>(r), dt == DT_BF16, scale, plan_layout(const_cast<void*>(plan), M, E),
                   static_cast<DevStatus*>(ws), s};
   return cuda_status(forward(p, x, A, B, base, y, t));
@@ -1207,8 +1464,8 @@ int i8lt_adapters_backward(const void* g, const void* x, const void* t, int dt, 
   if (ws == nullptr || ws_bytes < i8lt_adapters_workspace_size(M, K, N, E, r)) return I8LT_ERR_WORKSPACE;
   if (int d = check_device()) return d;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(ws, 0, sizeof(DevStatus), s) != cudaSuccess) return I8LT_ERR_CUDA;
   if (M == 0) {   // no tokens: the weight gradients are zeros
+    if (cudaMemsetAsync(ws, 0, sizeof(DevStatus), s) != cudaSuccess) return I8LT_ERR_CUDA;
     if (gA != nullptr && cudaMemsetAsync(gA, 0, static_cast<size_t>(E * r * K) * 2, s) != cudaSuccess)
       return I8LT_ERR_CUDA;
     if (gB != nullptr && cudaMemsetAsync(gB, 0, static_cast<size_t>(E * r * N) * 2, s) != cudaSuccess)

@@ -49,6 +49,14 @@ int check_device() {
     c = (major == 10 && minor == 3) ? 1 : 2;
     cached[dev].store(c);
   }
+  // A thread that has made no runtime call on this device yet (autograd's
+  // backward threads) has no current context for the tensor-map encoder, a
+  // driver call, to run in.
+  static thread_local int bound = -1;
+  if (bound != dev) {
+    if (cudaSetDevice(dev) != cudaSuccess) return I8LT_ERR_CUDA;
+    bound = dev;
+  }
   return c == 1 ? I8LT_OK : I8LT_ERR_DEVICE;
 }
 

@@ -748,6 +748,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
     }
     out += gridDim.x * a.N;
   }
+  grid_dependents_launch();
   if (a.partial == nullptr) return;
   float* pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.N;
   float* pb = pw + static_cast<int64_t>(gridDim.x) * a.N;
@@ -957,6 +958,7 @@ __global__ void __launch_bounds__(1024) norm_grad_sum_kernel(const float* partia
   const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
   void* out = blockIdx.y == 0 ? gw : gb;
   if (out == nullptr) return;
+  grid_dependency_wait();
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   const float* p = partial + static_cast<int64_t>(blockIdx.y) * blocks * N + n;
   float s = 0.f;
@@ -1114,9 +1116,18 @@ cudaError_t backward(const BackwardArgs& a, void* gw, void* gb, cudaStream_t s) 
   if (cudaError_t e = a.N % kW == 0 ? backward_sized<T, kW>(h) : backward_sized<T, 1>(h)) return e;
   if (a.partial == nullptr) return cudaSuccess;
   ProfScope ps(K_LAYER_NORM_GRAD_SUM, s);
-  norm_grad_sum_kernel<<<dim3(static_cast<unsigned>(ceil_div(a.N, 32)), 2), 1024, 0, s>>>(a.partial, h.blocks, a.N,
-                                                                                         a.wt, gw, gb);
-  return cudaGetLastError();
+  // started while the backward kernel's last blocks run
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(a.N, 32)), 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_grad_sum_kernel, static_cast<const float*>(a.partial), h.blocks, a.N, a.wt, gw,
+                            gb);
 }
 
 }  // namespace
