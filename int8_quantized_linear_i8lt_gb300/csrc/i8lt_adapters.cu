@@ -68,7 +68,10 @@ constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const int32_t* index, int M, int E, int* offset,
                                                                     int* perm, Tile* tiles) {
   constexpr int kWarpsPlan = kPlanThreads / 32, kPer = 8;
-  __shared__ int counts[2][kWarpsPlan];
+  // the group's first tokens, so that its tiles and whole runs of perm need no
+  // second trip to memory
+  constexpr int kStaged = kPlanThreads * kPer;
+  __shared__ int counts[2][kWarpsPlan], own[kStaged];
   const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto load = [&](int m0, int(&v)[kPer]) {   // the groups of 8 tokens, -1 past the end
     if (index == nullptr) {
@@ -119,20 +122,26 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const int32_
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (v[i] == e) perm[at++] = base + tid * kPer + i;
+      if (v[i] == e) {
+        if (at - before < kStaged) own[at - before] = base + tid * kPer + i;
+        else perm[at] = base + tid * kPer + i;
+        ++at;
+      }
     placed += all;
   }
-  __syncthreads();   // perm of this block is visible to it
+  __syncthreads();   // own and perm are visible to the block
+  for (int i = tid; i < min(placed, kStaged); i += kPlanThreads) perm[before + i] = own[i];
   if (tid == 0) {
     offset[e] = before;
     if (e == E) offset[E + 1] = M;
   }
+  auto token = [&](int place) { return place - before < kStaged ? own[place - before] : perm[place]; };
   const int slot0 = before / kTile + e, slot1 = (before + placed) / kTile + e + 1;
   for (int s = slot0 + tid; s < slot1; s += kPlanThreads) {
     const int start = before + (s - slot0) * kTile;
     const int count = max(0, min(kTile, before + placed - start));
     int row0 = -1;
-    if (count > 0 && perm[start + count - 1] - perm[start] == count - 1) row0 = perm[start];
+    if (count > 0 && token(start + count - 1) - token(start) == count - 1) row0 = token(start);
     tiles[s] = Tile{e, start, count, row0};
   }
 }
@@ -280,9 +289,12 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t a, int k, uint32_t block) {
   return make_sdesc(a + 2048 * k, block, 1024, kSwizzle128B);
 }
 
-__device__ __forceinline__ float ld_cluster(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t map_cluster(uint32_t a, uint32_t rank) {
@@ -352,11 +364,23 @@ __device__ __forceinline__ void spill(uint32_t tmem, int r16, float* red) {
                          __uint_as_float(v[4 * i + 3]));
   }
 }
-// The sum over the cluster of one element of it, in the order of the ranks.
-__device__ __forceinline__ float cluster_sum(uint32_t red, int at, int ranks) {
-  float s = 0.f;
-  for (int q = 0; q < ranks; ++q) s += ld_cluster(map_cluster(red + 4u * at, q));
-  return s;
+// The sums over the cluster of 4 elements of it, in the order of the ranks.
+// The loads of all ranks are under way before the first is used: one at a
+// time, they made up half of a small product's time.
+__device__ __forceinline__ void cluster_sum4(uint32_t red, int at, int ranks, float (&s)[4]) {
+  float4 v[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    if (q < ranks) v[q] = ld_cluster4(map_cluster(red + 4u * at, q));
+  s[0] = s[1] = s[2] = s[3] = 0.f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    if (q < ranks) {
+      s[0] += v[q].x;
+      s[1] += v[q].y;
+      s[2] += v[q].z;
+      s[3] += v[q].w;
+    }
 }
 
 // ---- mid = X W^T (t and u) -------------------------------------------------
@@ -508,11 +532,22 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
   cluster_sync();
   const int rows = (128 + ranks - 1) / ranks, row0 = rank * rows;
   const float scale = a.scale != nullptr ? a.scale[t.group] : 1.f;
-  for (int i = tid; i < rows * R; i += kThreads) {
-    const int row = row0 + i / R, j = i % R;
-    if (row < t.count)
-      a.mid[static_cast<int64_t>(a.perm[t.start + row]) * R + j] =
-          to_16(scale * cluster_sum(base, row * red_pitch(r16) + j, ranks), a.bf16);
+  const int quads = r16 / 4;
+  for (int i = tid; i < rows * quads; i += kThreads) {
+    const int row = row0 + i / quads, j = i % quads * 4;
+    if (row >= t.count || j >= R) continue;
+    float s[4];
+    cluster_sum4(base, row * red_pitch(r16) + j, ranks, s);
+    uint16_t* o = a.mid + static_cast<int64_t>(a.perm[t.start + row]) * R + j;
+    if (R % 4 == 0) {
+      *reinterpret_cast<uint2*>(o) =
+          make_uint2(to_16(scale * s[0], a.bf16) | static_cast<uint32_t>(to_16(scale * s[1], a.bf16)) << 16,
+                     to_16(scale * s[2], a.bf16) | static_cast<uint32_t>(to_16(scale * s[3], a.bf16)) << 16);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + k < R) o[k] = to_16(scale * s[k], a.bf16);
+    }
   }
   cluster_sync();   // the other CTAs have read this one's sums
 }
@@ -1010,11 +1045,23 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
   cluster_sync();
   const int rows = (128 + ranks - 1) / ranks, row0 = rank * rows;
   const float scale = a.scale != nullptr ? a.scale[e] : 1.f;
-  for (int i = tid; i < rows * R; i += kThreads) {
-    const int row = row0 + (kRankMajor ? i % rows : i / R), j = kRankMajor ? i / rows : i % R;
-    if (row < cols && row < 128)
-      grad[kRankMajor ? j * C + c0 + row : (c0 + row) * R + j] =
-          to_16(scale * cluster_sum(base, row * red_pitch(r16) + j, ranks), a.bf16);
+  const int quads = r16 / 4;
+  for (int i = tid; i < rows * quads; i += kThreads) {
+    // neighbouring threads on neighbouring elements of the gradient
+    const int row = row0 + (kRankMajor ? i % rows : i / quads), j = (kRankMajor ? i / rows : i % quads) * 4;
+    if (row >= cols || row >= 128 || j >= R) continue;
+    float s[4];
+    cluster_sum4(base, row * red_pitch(r16) + j, ranks, s);
+    if (!kRankMajor && R % 4 == 0) {
+      *reinterpret_cast<uint2*>(grad + (c0 + row) * R + j) =
+          make_uint2(to_16(scale * s[0], a.bf16) | static_cast<uint32_t>(to_16(scale * s[1], a.bf16)) << 16,
+                     to_16(scale * s[2], a.bf16) | static_cast<uint32_t>(to_16(scale * s[3], a.bf16)) << 16);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + k < R)
+          grad[kRankMajor ? (j + k) * C + c0 + row : (c0 + row) * R + j + k] = to_16(scale * s[k], a.bf16);
+    }
   }
   // what follows this kernel may rely on what came before it
   grid_dependency_wait();
@@ -1122,9 +1169,11 @@ __global__ void __launch_bounds__(kThreads, kMaxRankTiles > 4 ? 2 : kMaxRankTile
       part[0][i] = s;   // read and written by this thread alone
     }
     cluster_sync();
-    for (int i = tid; i < r16 * kFewTile; i += kThreads) {
-      const float s = cluster_sum(smem_u32(part[0]), i, kFewRanks);
-      ts[i % kFewTile][i / kFewTile] = to_16(s, kBf16);
+    for (int i = tid * 4; i < r16 * kFewTile; i += kThreads * 4) {
+      float s[4];
+      cluster_sum4(smem_u32(part[0]), i, kFewRanks, s);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) ts[i % kFewTile + k][i / kFewTile] = to_16(s[k], kBf16);
     }
     __syncthreads();
   }
