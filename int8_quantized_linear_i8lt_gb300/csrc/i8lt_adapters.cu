@@ -90,8 +90,8 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const int32_
   __align__(16) int v[kPer];
   // tokens of the groups before e
   int n = 0;
-  for (int m0 = tid * kPer; m0 < M; m0 += kPlanThreads * kPer) {
-    load(m0, v);
+  for (int base = 0; base < M; base += kPlanThreads * kPer) {
+    load(base + tid * kPer, v);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) n += v[i] >= 0 && v[i] < e;
   }
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const int32_
   for (int k = 0; k < kWarpsPlan; ++k) before += counts[0][k];
   int placed = 0;
   for (int base = 0, turn = 1; base < M; base += kPlanThreads * kPer, ++turn) {
-    load(base + tid * kPer, v);
+    if (M > kPlanThreads * kPer) load(base + tid * kPer, v);   // else v still holds them
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) mine += v[i] == e;
@@ -412,6 +412,10 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   __shared__ Sync y;
   const int ranks = a.ranks, rank = blockIdx.x % ranks;
+  if (kTma && threadIdx.x == 0) {
+    tma_prefetch_desc(&a.tmX);
+    tma_prefetch_desc(&a.tmW);
+  }
   grid_dependency_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.st = DevStatus{0, 0, 0, 0};
   const Tile t = a.tiles[blockIdx.x / ranks];
@@ -594,6 +598,12 @@ template <bool kMN, bool kTma>
 __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_constant__ ExpandArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ ExpandSync y;
+  if (kTma && threadIdx.x == 256) {
+    tma_prefetch_desc(&a.tmW);
+    tma_prefetch_desc(&a.tmAdd);
+    tma_prefetch_desc(&a.tmMid);
+    tma_prefetch_desc(&a.tmOut);
+  }
   const Tile t = a.tiles[blockIdx.x];
   if (t.count == 0) return;
   const bool adapter = t.group < a.E;
@@ -780,7 +790,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
           if (tid == 0) mbar_arrive(&y.add_free[j % bufs]);
         }
       }
-      if (tma_out && tid == 0) bulk_wait_all();
+      if (tma_out && tid == 0) bulk_wait_read<0>();   // shared memory is read; the writes end with the kernel
     }
     __syncwarp();
   } else if (warp < 8) {
@@ -890,6 +900,10 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
   const int tid = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x, R = a.R, r16 = rank16(R);
   const int64_t C = a.C, c0 = static_cast<int64_t>(blockIdx.y) * 128;
   const int64_t e = blockIdx.z;
+  if (kTma && tid == 0) {
+    tma_prefetch_desc(&a.tmX);
+    tma_prefetch_desc(&a.tmU);
+  }
   if (a.first && blockIdx.x == 0 && blockIdx.y == 0 && e == 0 && tid == 0) *a.st = DevStatus{0, 0, 0, 0};
   const int start = a.offset[e], tokens = a.offset[e + 1] - start;
   const int cols = static_cast<int>(min(static_cast<int64_t>(128), C - c0));
@@ -1347,8 +1361,11 @@ cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, 
   a.bf16 = p.bf16;
   const int r16 = rank16(p.R);
   const int64_t col_tiles = ceil_div(C, kCols);
-  a.col_tiles = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, p.plan.slots * col_tiles /
-                                                                               (4 * sm_count()))));
+  // whole waves of two CTAs per SM, of at most 12 tiles each; about half of
+  // the groups' last slots are taken to be empty
+  const int64_t work = std::min<int64_t>(p.plan.slots, ceil_div(p.M, kTile) + (p.E + 1) / 2) * col_tiles;
+  const int64_t waves = ceil_div(work, 2 * sm_count() * 12);
+  a.col_tiles = static_cast<int>(ceil_div(work, 2 * sm_count() * waves));
   const int smem = 1024 + expand_mid_bytes(r16) + 2 * expand_w_bytes(r16) +
                    expand_tiles(r16) * static_cast<int>(kTileBytes);
   const dim3 grid(static_cast<unsigned>(p.plan.slots), static_cast<unsigned>(ceil_div(col_tiles, a.col_tiles)));

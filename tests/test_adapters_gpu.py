@@ -129,6 +129,19 @@ def test_forward_and_backward(M, K, N, r, E, order, dt):
     _check(_run(d), _reference(d), dt)
 
 
+# long batches: tiles of two accumulators, strips of 256 columns
+LONG = [(6500, 256, 320, 16, 3, "mixed"), (6144, 512, 264, 64, 1, "one"), (7001, 320, 384, 128, 2, "runs"),
+        (6300, 2056, 2048, 8, 5, "runs"), (6200, 1024, 2048, 72, 5, "mixed"), (6400, 130, 77, 12, 2, "mixed"),
+        (6500, 128, 128, 16, 300, "mixed"), (6145, 9736, 72, 16, 1, "one")]
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("M,K,N,r,E,order", LONG)
+def test_long_batches(M, K, N, r, E, order, dt):
+    d = _data(M, K, N, r, E, dt, order, seed=M + K)
+    _check(_run(d), _reference(d), dt)
+
+
 @pytest.mark.parametrize("M", [40, 700])
 def test_absent_base_addend_and_scale(M):
     d = _data(M, 512, 384, 16, 3, BF16, "mixed", 4)
