@@ -559,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
 // ---- out = addend + scale mid W^T (y and gx) --------------------------------
 
 struct ExpandArgs {
-  // with kTma: mid, addend and out, box 64 x 128 (the first two also 64 x 1); W, box 64 x 64 or 64 x r16
-  CUtensorMap tmMid, tmMid1, tmW, tmAdd, tmAdd1, tmOut;
+  // with kTma: mid, addend and out, box 64 x 128 (mid also 64 x 1); W, box 64 x 64 or 64 x r16
+  CUtensorMap tmMid, tmMid1, tmW, tmAdd, tmOut;
   const uint16_t* mid;     // [M, R]
   const uint16_t* W;       // per group [C, R] (K-major) or [R, C] (MN-major)
   const uint16_t* addend;  // [M, C] or NULL; may be out
@@ -687,22 +687,38 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = 0u;
     }
-    if (kTma && a.addend != nullptr) mbar_wait(&y.add_full[j % bufs], (j / bufs) & 1, &y.abort, a.st, 27);
+    if (tma_out && a.addend != nullptr) mbar_wait(&y.add_full[j % bufs], (j / bufs) & 1, &y.abort, a.st, 27);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       uint8_t* p = buf + swizzled(row, c0 / 8 + q);
       st_shared_v4(p, combine(a.addend != nullptr ? ld_shared_v4(p) : make_uint4(0, 0, 0, 0), v + 8 * q));
     }
   };
-  // rows of a finished tile: chunk tid % 8 of rows tid / 8 + 32 i
+  // The addend's rows of tile j, and rows of a finished tile: a thread has
+  // chunk tid % 8 of rows tid / 8 + 32 i in both, so that it may fetch into
+  // what it has stored.
+  int token[4] = {-1, -1, -1, -1};
+  if (!tma_out && warp < 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if ((tid >> 3) + 32 * i < t.count) token[i] = a.perm[t.start + (tid >> 3) + 32 * i];
+  auto load_addend = [&](int j) {
+    if (a.addend == nullptr || j >= n) return;
+    const uint32_t buf = smem_u32(tiles) + (j % bufs) * kTileBytes;
+    const int64_t at = static_cast<int64_t>(j0 + j) * kCols + (tid & 7) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (token[i] >= 0)
+        load_chunk(buf + swizzled((tid >> 3) + 32 * i, tid & 7), a.addend + static_cast<int64_t>(token[i]) * C, at,
+                   C - at, a.cw);
+  };
   auto store_rows = [&](int j, const uint8_t* buf) {
     const int64_t at = static_cast<int64_t>(j0 + j) * kCols + (tid & 7) * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = (tid >> 3) + 32 * i;
-      if (row >= t.count || at >= C) continue;
-      const uint4 w = ld_shared_v4(buf + swizzled(row, tid & 7));
-      uint16_t* o = a.out + static_cast<int64_t>(a.perm[t.start + row]) * C + at;
+      if (token[i] < 0 || at >= C) continue;
+      const uint4 w = ld_shared_v4(buf + swizzled((tid >> 3) + 32 * i, tid & 7));
+      uint16_t* o = a.out + static_cast<int64_t>(token[i]) * C + at;
       if (a.cw == 16) {
         *reinterpret_cast<uint4*>(o) = w;
       } else {
@@ -732,17 +748,13 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
               tma_load_3d(ws + k * 64 * kRowBytes, &a.tmW, 64 * k, c0, t.group, &y.w_full[j & 1]);
           }
         }
-        if (a.addend != nullptr) {
+        if (a.addend != nullptr && tma_out && lane == 0) {
           uint64_t* bar = &y.add_full[j % bufs];
-          uint8_t* buf = tiles + (j % bufs) * kTileBytes;
-          if (lane == 0) {
-            if (j >= bufs) mbar_wait(&y.add_free[j % bufs], (j / bufs - 1) & 1, &y.abort, a.st, 29);
-            mbar_arrive_expect_tx(bar, kTileBytes);
-            if (t.row0 >= 0) tma_load_2d(buf, &a.tmAdd, c0, t.row0, bar);
-          }
-          __syncwarp();
-          if (t.row0 < 0) tma_gather4(buf + lane * 4 * kRowBytes, &a.tmAdd1, c0, rows, bar);
+          if (j >= bufs) mbar_wait(&y.add_free[j % bufs], (j / bufs - 1) & 1, &y.abort, a.st, 29);
+          mbar_arrive_expect_tx(bar, kTileBytes);
+          tma_load_2d(tiles + (j % bufs) * kTileBytes, &a.tmAdd, c0, t.row0, bar);
         }
+        __syncwarp();
         // mid, the output of the kernel before this one, after the first
         // tile's W and addend are on their way
         if (j == 0 && adapter) {
@@ -766,48 +778,48 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
           multiply(j);
         }
       }
-    } else if (warp < 8) {
+    } else if (warp < 8 && tma_out) {
       for (int j = 0; j < n; ++j) {
         uint8_t* buf = tiles + (j % bufs) * kTileBytes;
         // without an addend nothing else keeps this buffer's last store ahead
         if (a.addend == nullptr && j >= bufs)
           mbar_wait(&y.add_free[j % bufs], (j / bufs - 1) & 1, &y.abort, a.st, 29);
         finish(j, buf);
-        if (tma_out) {
-          fence_proxy_async_smem();
-          named_bar_sync(1, 256);
-          if (tid == 0) {
-            tma_store_2d(&a.tmOut, (j0 + j) * kCols, t.row0, buf);
-            bulk_commit();
-            bulk_wait_read<1>();   // the store of tile j - 1 has read its buffer
-            if (j > 0) mbar_arrive(&y.add_free[(j - 1) % bufs]);
-          }
-          __syncwarp();
-        } else {
-          named_bar_sync(1, 256);
-          store_rows(j, buf);
-          named_bar_sync(1, 256);
-          if (tid == 0) mbar_arrive(&y.add_free[j % bufs]);
+        fence_proxy_async_smem();
+        named_bar_sync(1, 256);
+        if (tid == 0) {
+          tma_store_2d(&a.tmOut, (j0 + j) * kCols, t.row0, buf);
+          bulk_commit();
+          bulk_wait_read<1>();   // the store of tile j - 1 has read its buffer
+          if (j > 0) mbar_arrive(&y.add_free[(j - 1) % bufs]);
         }
+        __syncwarp();
       }
-      if (tma_out && tid == 0) bulk_wait_read<0>();   // shared memory is read; the writes end with the kernel
+      if (tid == 0) bulk_wait_read<0>();   // shared memory is read; the writes end with the kernel
+    } else if (warp < 8) {
+      // rows here and there: by the threads themselves (their 128-byte rows
+      // are faster fetched and stored so than four at a time by TMA)
+      for (int j = 0; j < bufs - 1; ++j) {
+        load_addend(j);
+        cp_async_commit();
+      }
+      for (int j = 0; j < n; ++j) {
+        uint8_t* buf = tiles + (j % bufs) * kTileBytes;
+        load_addend(j + bufs - 1);
+        cp_async_commit();
+        if (bufs == 4) cp_async_wait<3>();
+        else cp_async_wait<1>();
+        named_bar_sync(1, 256);
+        finish(j, buf);
+        named_bar_sync(1, 256);
+        store_rows(j, buf);
+      }
+      cp_async_wait<0>();
     }
     __syncwarp();
   } else if (warp < 8) {
     // the same, gathered by all of warps 0-7, one tile ahead
     grid_dependency_wait();
-    auto load_addend = [&](int j) {
-      if (a.addend == nullptr) return;
-      const uint32_t buf = smem_u32(tiles) + (j % bufs) * kTileBytes;
-      const int64_t at = static_cast<int64_t>(j0 + j) * kCols + (tid & 7) * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = (tid >> 3) + 32 * i;
-        if (row < t.count)
-          load_chunk(buf + swizzled(row, tid & 7), a.addend + static_cast<int64_t>(a.perm[t.start + row]) * C, at,
-                     C - at, a.cw);
-      }
-    };
     const int chunks = r16 / 8;
     const uint16_t* W = a.W + static_cast<int64_t>(adapter ? t.group : 0) * R * C;
     auto load_w = [&](int j) {
@@ -1373,7 +1385,6 @@ cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, 
   if (tma && (!make_tmap(&a.tmMid, map_type(p), mid, p.R, p.M, p.R * 2, 64, 128, kSwz) ||
               !make_tmap(&a.tmMid1, map_type(p), mid, p.R, p.M, p.R * 2, 64, 1, kSwz) ||
               !make_tmap(&a.tmAdd, map_type(p), addend != nullptr ? addend : out, C, p.M, C * 2, 64, 128, kSwz) ||
-              !make_tmap(&a.tmAdd1, map_type(p), addend != nullptr ? addend : out, C, p.M, C * 2, 64, 1, kSwz) ||
               !make_tmap(&a.tmOut, map_type(p), out, C, p.M, C * 2, 64, 128, kSwz) ||
               !(mn ? make_tmap_3d(&a.tmW, map_type(p), W, C, p.R, p.E, 2, 64, r16, kSwz)
                    : make_tmap_3d(&a.tmW, map_type(p), W, p.R, C, p.E, 2, 64, 64, kSwz))))
