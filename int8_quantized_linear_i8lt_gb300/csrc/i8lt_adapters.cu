@@ -3,10 +3,13 @@
 //   t[m] = x[m] A[e]^T,            y[m]  = base[m] + scale[e] t[m] B[e]^T,
 //   u[m] = scale[e] g[m] B[e],     gx[m] = addend[m] + u[m] A[e],
 //   gA[e] = sum_m u[m]^T x[m],     gB[e] = scale[e] sum_m g[m]^T t[m],
-// with A [E, r, K], B [E, N, r].  Every sum is fp32.  t and u are rounded to
-// the 16-bit compute type (each is the operand of a second product, as the
-// 16-bit activations are of the layers' own products); y, gx, gA and gB are
-// rounded once.
+// with A [E, r, K], B [E, N, r].  Every sum is fp32; y, gx, gA and gB are
+// rounded once.  t and u are operands of a second 16-bit product.  For gA and
+// gB they are kept as two 16-bit values whose sum is t (u) to twice the
+// type's precision, and both take part: a rounded t would be off by as much
+// as the gradient's own rounding (and by more where few tokens make it up).
+// y and gx take the first value alone: its error is the type's rounding of a
+// correction to base and addend.
 #include <algorithm>
 
 #include "i8lt.h"
@@ -232,6 +235,15 @@ __device__ __forceinline__ uint16_t to_16(float v, bool bf16) {
   return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
 
+__device__ __forceinline__ float from_16(uint16_t v, bool bf16) {
+  return bf16 ? __uint_as_float(static_cast<uint32_t>(v) << 16) : __half2float(__ushort_as_half(v));
+}
+// What rounding v to hi left over, rounded (0 where hi overflowed).
+__device__ __forceinline__ uint16_t rest_16(float v, uint16_t hi, bool bf16) {
+  const float h = from_16(hi, bf16);
+  return isfinite(h) ? to_16(v - h, bf16) : uint16_t(0);
+}
+
 template <int kBytes>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool take) {
   const int n = take ? kBytes : 0;
@@ -389,7 +401,8 @@ struct ShrinkArgs {
   CUtensorMap tmX, tmX1, tmW;   // with kTma: X, box 64 x 128 and 64 x 1; W, box 64 x r16 (K-major) or 64 x 64
   const uint16_t* X;      // [M, C]
   const uint16_t* W;      // per group [R, C] (K-major) or [C, R] (MN-major)
-  uint16_t* mid;          // [M, R]
+  uint16_t* mid;          // [2, M, R]: the values, and what their rounding left
+  int64_t plane;          // M R
   const float* scale;     // applied when not NULL
   const Tile* tiles;
   const int* perm;
@@ -423,8 +436,10 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
   const int tid = threadIdx.x, R = a.R, r16 = rank16(R);
   if (t.group >= a.E) {
     if (rank == 0)
-      for (int i = tid; i < t.count * R; i += kThreads)
-        a.mid[static_cast<int64_t>(a.perm[t.start + i / R]) * R + i % R] = 0;
+      for (int i = tid; i < t.count * R; i += kThreads) {
+        uint16_t* o = a.mid + static_cast<int64_t>(a.perm[t.start + i / R]) * R + i % R;
+        o[0] = o[a.plane] = 0;
+      }
     return;
   }
   const uint32_t base = align1024(smem_u32(smem_raw));
@@ -543,14 +558,22 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
     float s[4];
     cluster_sum4(base, row * red_pitch(r16) + j, ranks, s);
     uint16_t* o = a.mid + static_cast<int64_t>(a.perm[t.start + row]) * R + j;
+    uint16_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      hi[k] = to_16(scale * s[k], a.bf16);
+      lo[k] = rest_16(scale * s[k], hi[k], a.bf16);
+    }
     if (R % 4 == 0) {
-      *reinterpret_cast<uint2*>(o) =
-          make_uint2(to_16(scale * s[0], a.bf16) | static_cast<uint32_t>(to_16(scale * s[1], a.bf16)) << 16,
-                     to_16(scale * s[2], a.bf16) | static_cast<uint32_t>(to_16(scale * s[3], a.bf16)) << 16);
+      *reinterpret_cast<uint2*>(o) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+      *reinterpret_cast<uint2*>(o + a.plane) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (j + k < R) o[k] = to_16(scale * s[k], a.bf16);
+        if (j + k < R) {
+          o[k] = hi[k];
+          o[a.plane + k] = lo[k];
+        }
     }
   }
   cluster_sync();   // the other CTAs have read this one's sums
@@ -884,7 +907,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
 
 struct GradArgs {
   CUtensorMap tmX, tmU, tmX1, tmU1;   // with kTma: X and mid, box 64 x 64 and 64 x 1
-  const uint16_t* mid;    // [M, R]
+  const uint16_t* mid;    // [2, M, R]
   const uint16_t* X;      // [M, C]
   uint16_t* grad;         // per group [R, C] (kRankMajor) or [C, R]
   const float* scale;
@@ -892,15 +915,14 @@ struct GradArgs {
   const int* perm;
   DevStatus* st;
   int64_t C;
-  int R, cw, rw;
+  int M, R, cw, rw, mw;   // mw: the copy width of mid's second part
   bool bf16;
   bool first;             // the call's first kernel: clears the status
   bool wait;              // mid is the output of the kernel before this one
 };
 
-__host__ __device__ constexpr int grad_stage_bytes(int r16) {
-  return 2 * 64 * kRowBytes + (r16 > 64 ? 2 : 1) * 64 * kRowBytes;
-}
+__host__ __device__ constexpr int grad_mid_bytes(int r16) { return (r16 > 64 ? 2 : 1) * 64 * kRowBytes; }
+__host__ __device__ constexpr int grad_stage_bytes(int r16) { return 2 * 64 * kRowBytes + 2 * grad_mid_bytes(r16); }
 
 // grad[c, j] = scale sum_m X[m, c] mid[m, j] over a group's tokens: one
 // cluster per (128 columns of X, group), its CTAs splitting the tokens.
@@ -942,9 +964,11 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
     const int s = it % kStages;
     const uint32_t xs = base + s * stage_bytes, us = xs + 2 * 64 * kRowBytes;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      umma_f16(y.tmem, desc_mn(xs, k, 64 * kRowBytes), desc_mn(us, k, 64 * kRowBytes), idesc,
-               it > 0 || k > 0 ? 1u : 0u);
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t x = desc_mn(xs, k, 64 * kRowBytes);
+      umma_f16(y.tmem, x, desc_mn(us, k, 64 * kRowBytes), idesc, it > 0 || k > 0 ? 1u : 0u);
+      umma_f16(y.tmem, x, desc_mn(us + grad_mid_bytes(r16), k, 64 * kRowBytes), idesc, 1u);
+    }
     umma_commit(&y.done[s]);
     if (it == n - 1) umma_commit(&y.last);
   };
@@ -970,15 +994,22 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
           if (box) {
             tma_load_2d(xs, &a.tmX, static_cast<int>(c0), first + m0, &y.full[s]);
             tma_load_2d(xs + 64 * kRowBytes, &a.tmX, static_cast<int>(c0) + 64, first + m0, &y.full[s]);
-            tma_load_2d(us, &a.tmU, 0, first + m0, &y.full[s]);
-            if (r16 > 64) tma_load_2d(us + 64 * kRowBytes, &a.tmU, 64, first + m0, &y.full[s]);
+            for (int k = 0; k < 2; ++k) {
+              uint8_t* u = us + k * grad_mid_bytes(r16);
+              tma_load_2d(u, &a.tmU, 0, k * a.M + first + m0, &y.full[s]);
+              if (r16 > 64) tma_load_2d(u + 64 * kRowBytes, &a.tmU, 64, k * a.M + first + m0, &y.full[s]);
+            }
           }
         }
         __syncwarp();   // the stage is armed before its gathers arrive
         if (!box) {
           const int at = (half * 64 + quad * 4) * kRowBytes;
           tma_gather4(xs + at, &a.tmX1, static_cast<int>(c0) + 64 * half, rows, &y.full[s]);
-          if (half == 0 || r16 > 64) tma_gather4(us + at, &a.tmU1, 64 * half, rows, &y.full[s]);
+          const int rest[4] = {a.M + rows[0], a.M + rows[1], a.M + rows[2], a.M + rows[3]};
+          if (half == 0 || r16 > 64) {
+            tma_gather4(us + at, &a.tmU1, 64 * half, rows, &y.full[s]);
+            tma_gather4(us + grad_mid_bytes(r16) + at, &a.tmU1, 64 * half, rest, &y.full[s]);
+          }
         }
       }
     } else if (tid < 64) {
@@ -988,8 +1019,8 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
         if (left < 64) {
           uint8_t* us = smem_raw + (base - smem_u32(smem_raw)) + it % kStages * stage_bytes + 2 * 64 * kRowBytes;
           for (int i = left * 8 + (tid & 31); i < 64 * 8; i += 32)
-            for (int k = 0; k < (r16 > 64 ? 2 : 1); ++k)
-              st_shared_v4(us + k * 64 * kRowBytes + i * 16, make_uint4(0, 0, 0, 0));
+            for (int k = 0; k < 2 * grad_mid_bytes(r16); k += 64 * kRowBytes)
+              st_shared_v4(us + k + i * 16, make_uint4(0, 0, 0, 0));
           fence_proxy_async_smem();
         }
         __syncwarp();
@@ -1031,8 +1062,11 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
         const int at = tid + i * kThreads;
         if (at >= 64 * chunks) break;
         const int k = at / chunks, q = at % chunks;
-        load_chunk(us + (q >> 3) * 64 * kRowBytes + swizzled(k, q & 7),
-                   a.mid + static_cast<int64_t>(max(um[i], 0)) * R, q * 8, um[i] >= 0 ? R - q * 8 : 0, a.rw);
+        const uint32_t dst = us + (q >> 3) * 64 * kRowBytes + swizzled(k, q & 7);
+        const uint16_t* row = a.mid + static_cast<int64_t>(max(um[i], 0)) * R;
+        load_chunk(dst, row, q * 8, um[i] >= 0 ? R - q * 8 : 0, a.rw);
+        load_chunk(dst + grad_mid_bytes(r16), row + static_cast<int64_t>(a.M) * R, q * 8,
+                   um[i] >= 0 ? R - q * 8 : 0, a.mw);
       }
       rows_of(b + 1);
     };
@@ -1098,7 +1132,8 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
 
 struct FewArgs {
   const uint16_t *x, *A, *B, *base;   // base or NULL; may be y
-  uint16_t *y, *t;
+  uint16_t *y, *t;                    // t [2, M, R]
+  int64_t plane;                      // M R
   const float* scale;
   const Tile* tiles;
   const int* perm;
@@ -1198,14 +1233,26 @@ __global__ void __launch_bounds__(kThreads, kMaxRankTiles > 4 ? 2 : kMaxRankTile
     for (int i = tid * 4; i < r16 * kFewTile; i += kThreads * 4) {
       float s[4];
       cluster_sum4(smem_u32(part[0]), i, kFewRanks, s);
+      const int j = i / kFewTile;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) ts[i % kFewTile + k][i / kFewTile] = to_16(s[k], kBf16);
+      for (int k = 0; k < 4; ++k) {
+        const int tok = i % kFewTile + k;
+        const uint16_t hi = to_16(s[k], kBf16);
+        ts[tok][j] = hi;
+        if (rank == 0 && tok < tile.count && j < R) {
+          uint16_t* o = a.t + static_cast<int64_t>(a.perm[tile.start + tok]) * R + j;
+          o[0] = hi;
+          o[a.plane] = rest_16(s[k], hi, kBf16);
+        }
+      }
     }
     __syncthreads();
+  } else if (rank == 0) {
+    for (int i = tid; i < tile.count * R; i += kThreads) {
+      uint16_t* o = a.t + static_cast<int64_t>(a.perm[tile.start + i / R]) * R + i % R;
+      o[0] = o[a.plane] = 0;
+    }
   }
-  if (rank == 0)
-    for (int i = tid; i < tile.count * R; i += kThreads)
-      a.t[static_cast<int64_t>(a.perm[tile.start + i / R]) * R + i % R] = adapter ? ts[i / R][i % R] : uint16_t(0);
   // y: warp w on columns 16 w .. 16 w + 15 of a step, then every warp on a token
   const float scale = adapter ? (a.scale != nullptr ? a.scale[tile.group] : 1.f) : 0.f;
   const int64_t m = a.perm[tile.start + min(warp, tile.count - 1)];
@@ -1325,6 +1372,7 @@ cudaError_t shrink(const Problem& p, const void* X, int64_t C, const void* W, bo
   a.X = static_cast<const uint16_t*>(X);
   a.W = static_cast<const uint16_t*>(W);
   a.mid = static_cast<uint16_t*>(mid);
+  a.plane = p.M * p.R;
   a.scale = scale;
   a.tiles = p.plan.tiles;
   a.perm = p.plan.perm;
@@ -1407,25 +1455,27 @@ cudaError_t grad(const Problem& p, const void* mid, const void* X, int64_t C, bo
   a.C = C;
   a.wait = wait;
   a.first = !after;
+  a.M = static_cast<int>(p.M);
+  a.mw = std::min(copy_width(p.R), copy_width(p.M * p.R));
   a.R = p.R;
   a.cw = copy_width(C);
   a.rw = copy_width(p.R);
   a.bf16 = p.bf16;
   const int r16 = rank16(p.R), ranks = split(ceil_div(C, 128) * p.E, ceil_div(ceil_div(p.M, p.E), 64));
-  const int stages = r16 > 64 ? 3 : 4;
+  const int stages = r16 > 64 ? 2 : 3;
   const int smem = 1024 + std::max(stages * grad_stage_bytes(r16), 128 * red_pitch(r16) * 4);
   const dim3 grid(static_cast<unsigned>(ranks), static_cast<unsigned>(ceil_div(C, 128)), static_cast<unsigned>(p.E));
   const bool tma = tma_rows(p, C);
   if (tma && (!make_tmap(&a.tmX, map_type(p), X, C, p.M, C * 2, 64, 64, kSwz) ||
-              !make_tmap(&a.tmU, map_type(p), mid, p.R, p.M, p.R * 2, 64, 64, kSwz) ||
+              !make_tmap(&a.tmU, map_type(p), mid, p.R, 2 * p.M, p.R * 2, 64, 64, kSwz) ||
               !make_tmap(&a.tmX1, map_type(p), X, C, p.M, C * 2, 64, 1, kSwz) ||
-              !make_tmap(&a.tmU1, map_type(p), mid, p.R, p.M, p.R * 2, 64, 1, kSwz)))
+              !make_tmap(&a.tmU1, map_type(p), mid, p.R, 2 * p.M, p.R * 2, 64, 1, kSwz)))
     return cudaErrorUnknown;
-  auto k4 = tma ? (rank_major ? grad_kernel<true, 4, true> : grad_kernel<false, 4, true>)
-                : (rank_major ? grad_kernel<true, 4, false> : grad_kernel<false, 4, false>);
   auto k3 = tma ? (rank_major ? grad_kernel<true, 3, true> : grad_kernel<false, 3, true>)
                 : (rank_major ? grad_kernel<true, 3, false> : grad_kernel<false, 3, false>);
-  return launch(stages == 4 ? k4 : k3, a, grid, kThreads, ranks, smem, K_ADAPTERS_GRAD, after, p.s);
+  auto k2 = tma ? (rank_major ? grad_kernel<true, 2, true> : grad_kernel<false, 2, true>)
+                : (rank_major ? grad_kernel<true, 2, false> : grad_kernel<false, 2, false>);
+  return launch(stages == 3 ? k3 : k2, a, grid, kThreads, ranks, smem, K_ADAPTERS_GRAD, after, p.s);
 }
 
 cudaError_t forward(const Problem& p, const void* x, const void* A, const void* B, const void* base, void* y,
@@ -1433,7 +1483,7 @@ cudaError_t forward(const Problem& p, const void* x, const void* A, const void* 
   if (p.plan.few_slots > 0 && p.K % 8 == 0 && p.N % 8 == 0 && p.R % 8 == 0) {
     const FewArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(A),
                     static_cast<const uint16_t*>(B), static_cast<const uint16_t*>(base),
-                    static_cast<uint16_t*>(y), static_cast<uint16_t*>(t), p.scale, p.plan.few, p.plan.perm,
+                    static_cast<uint16_t*>(y), static_cast<uint16_t*>(t), p.M * p.R, p.scale, p.plan.few, p.plan.perm,
                     p.st, p.K, p.N, p.R, static_cast<int>(p.E)};
     const dim3 grid(static_cast<unsigned>(p.plan.few_slots * kFewRanks));
     auto kernel = p.R <= 16   ? (p.bf16 ? few_kernel<true, 1> : few_kernel<false, 1>)
@@ -1503,7 +1553,7 @@ int i8lt_adapter_plan(const int32_t* index, int64_t M, int64_t E, void* plan, si
 
 size_t i8lt_adapters_workspace_size(int64_t M, int64_t K, int64_t N, int64_t E, int64_t r) {
   if (!valid_sizes(M, K, N, E, r)) return 0;
-  return 256 + static_cast<size_t>(round_up(M * r * 2, 256));
+  return 256 + static_cast<size_t>(round_up(M * r * 4, 256));
 }
 
 int i8lt_adapters_forward(const void* x, int dt, int64_t M, int64_t K, const void* A, const void* B, int64_t E,

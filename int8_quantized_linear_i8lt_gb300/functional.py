@@ -783,7 +783,8 @@ def adapters_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: t
     """(y, t) with t = x A[e]^T and y = base + scale[e] t B[e]^T for each
     token's adapter e (i8lt_adapters_forward): x [M, K] (f16 / bf16),
     A [E, r, K], B [E, N, r], scale fp32 [E] or None, base [M, N] or None.
-    ``out`` may be base itself (not x).  t [M, r] is what the backward needs."""
+    ``out`` may be base itself (not x).  t [2, M, r], two 16-bit parts of one
+    value, is what the backward needs."""
     what = "adapters_forward"
     dev, M, K, E, r, N, A, B, scale = _adapter_args(what, x, A, B, scale, plan)
     dtype, device = x.dtype, x.device
@@ -791,7 +792,7 @@ def adapters_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: t
     base = _arg("adapters_forward base", base, dev, (M, N), dtype)
     y = torch.empty((M, N), dtype=dtype, device=device) if out is None else \
         _out("adapters_forward out", out, dev, (M, N), dtype)
-    t = torch.empty((M, r), dtype=dtype, device=device)
+    t = torch.empty((2, M, r), dtype=dtype, device=device)
     ws = _adapter_workspace(M, K, N, E, r, device)
     _check(_lib.i8lt_adapters_forward(x.data_ptr(), _code(dtype), M, K, A.data_ptr(), B.data_ptr(), E, r, N,
                                       _ptr(scale), plan.data.data_ptr(), _ptr(base), y.data_ptr(), t.data_ptr(),
@@ -813,7 +814,7 @@ def adapters_backward(g: torch.Tensor, x: torch.Tensor | None, t: torch.Tensor |
     dtype, device = g.dtype, g.device
     g = _arg("adapters_backward g", g, dev, (M, N), None)
     x = _arg("adapters_backward x", x, dev, (M, K), dtype)
-    t = _arg("adapters_backward t", t, dev, (M, r), dtype)
+    t = _arg("adapters_backward t", t, dev, (2, M, r), dtype)
     addend = _arg("adapters_backward addend", addend, dev, (M, K), dtype)
     if not (need_x or need_A or need_B):
         return None, None, None
