@@ -8,6 +8,7 @@ no fallback of any kind when it is missing.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from ctypes import POINTER, Structure, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
@@ -362,6 +363,7 @@ def i8lt_layer_norm_forward(x, xt, M, N, w, b, wt, eps, y, mean, rstd, stream=No
                                           stream)
 
 
+@functools.lru_cache(maxsize=1024)   # a function of the sizes alone
 def i8lt_layer_norm_backward_workspace_size(M, N) -> int:
     return load().i8lt_layer_norm_backward_workspace_size(M, N)
 
@@ -371,6 +373,7 @@ def i8lt_layer_norm_backward(g, x, xt, M, N, mean, rstd, w, wt, gx, gw, gb, ws, 
                                            gb, ws, ws_bytes, stream)
 
 
+@functools.lru_cache(maxsize=1024)   # a function of the sizes alone
 def i8lt_adapter_plan_bytes(M, E) -> int:
     return load().i8lt_adapter_plan_bytes(M, E)
 
@@ -379,6 +382,7 @@ def i8lt_adapter_plan(index, M, E, plan, plan_bytes, stream=None) -> int:
     return load().i8lt_adapter_plan(index, M, E, plan, plan_bytes, stream)
 
 
+@functools.lru_cache(maxsize=1024)   # a function of the sizes alone
 def i8lt_adapters_workspace_size(M, K, N, E, r) -> int:
     return load().i8lt_adapters_workspace_size(M, K, N, E, r)
 

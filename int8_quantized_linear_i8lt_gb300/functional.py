@@ -658,9 +658,9 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     y = torch.empty_like(x) if out is None else _out("layer_norm out", out, dev, shape, dtype)
     mean = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
     rstd = torch.empty_like(mean)
-    _check(_lib.i8lt_layer_norm_forward(x.data_ptr(), _code(dtype), x.numel() // N if N else 0, N, _ptr(weight),
-                                        _ptr(bias), 0 if par is None else _code(par.dtype), eps, y.data_ptr(),
-                                        mean.data_ptr(), rstd.data_ptr(), _stream(x)), "i8lt_layer_norm_forward")
+    _check(_lib.i8lt_layer_norm_forward(x.data_ptr(), _code(dtype), mean.numel(), N, _ptr(weight), _ptr(bias),
+                                        0 if par is None else _code(par.dtype), eps, y.data_ptr(), mean.data_ptr(),
+                                        rstd.data_ptr(), _stream(x)), "i8lt_layer_norm_forward")
     return y, mean, rstd
 
 
@@ -790,8 +790,10 @@ def adapters_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: t
     dtype, device = x.dtype, x.device
     x = _arg(what, x, dev, (M, K), None)
     base = _arg("adapters_forward base", base, dev, (M, N), dtype)
-    y = torch.empty((M, N), dtype=dtype, device=device) if out is None else \
-        _out("adapters_forward out", out, dev, (M, N), dtype)
+    if out is not None:
+        y = _out("adapters_forward out", out, dev, (M, N), dtype)
+    else:
+        y = torch.empty((M, N), dtype=dtype, device=device) if base is None else torch.empty_like(base)
     t = torch.empty((2, M, r), dtype=dtype, device=device)
     ws = _adapter_workspace(M, K, N, E, r, device)
     _check(_lib.i8lt_adapters_forward(x.data_ptr(), _code(dtype), M, K, A.data_ptr(), B.data_ptr(), E, r, N,
@@ -818,7 +820,10 @@ def adapters_backward(g: torch.Tensor, x: torch.Tensor | None, t: torch.Tensor |
     addend = _arg("adapters_backward addend", addend, dev, (M, K), dtype)
     if not (need_x or need_A or need_B):
         return None, None, None
-    gx = torch.empty((M, K), dtype=dtype, device=device) if need_x else None
+    gx = None
+    if need_x:
+        like = addend if addend is not None else x
+        gx = torch.empty((M, K), dtype=dtype, device=device) if like is None else torch.empty_like(like)
     gA = torch.empty_like(A) if need_A else None
     gB = torch.empty_like(B) if need_B else None
     ws = _adapter_workspace(M, K, N, E, r, device)
