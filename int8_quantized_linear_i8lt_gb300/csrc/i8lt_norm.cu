@@ -204,16 +204,19 @@ __device__ __forceinline__ Slice<T> slice_of(const Ring<T, kMats>& r, int k, int
   }
   return s;
 }
-// The pack at column c of a slice of `cols` columns; zeros past the end.
+// The pack at column c of a slice of `cols` columns; zeros past the end,
+// which a stage of aligned rows holds itself (zero_tails).
 template <typename T, int W>
 __device__ __forceinline__ void read(const Slice<T>& s, int c, int cols, float* f) {
-  if (c < cols) {
-    if constexpr (W == 1) f[0] = to_float(c < s.have ? s.near[c] : s.far[c]);
-    else widen<T, W>(load_pack<T, W>(s.near + c), f);
-  } else {
-#pragma unroll
-    for (int k = 0; k < W; ++k) f[k] = 0.f;
-  }
+  if constexpr (W == 1) f[0] = c >= cols ? 0.f : to_float(c < s.have ? s.near[c] : s.far[c]);
+  else widen<T, W>(load_pack<T, W>(s.near + c), f);
+}
+// Zeros behind the slices of all stages (the copies never write there).
+template <typename T, int kMats>
+__device__ __forceinline__ void zero_tails(const Ring<T, kMats>& r, int threads) {
+  const int tail = (r.L.slot_bytes - r.cols * static_cast<int>(sizeof(T))) / 16;
+  for (int i = threadIdx.x; i < tail * static_cast<int>(r.L.stages) * kMats; i += threads)
+    *reinterpret_cast<uint4*>(r.base + (i / tail + 1) * r.L.slot_bytes - (i % tail + 1) * 16) = make_uint4(0, 0, 0, 0);
 }
 
 __device__ __forceinline__ void ring_setup(uint64_t* full, unsigned stages, int* abort_flag) {
@@ -234,12 +237,15 @@ struct ForwardArgs {
   float eps;
 };
 
-// Short rows: kLanes lanes of a warp hold a row in registers; the variance is
-// summed around the mean.
+// One row per kLanes threads (lanes of a warp for short rows, a block for rows
+// of 8192 to 16384), held in registers; the variance is summed around the
+// mean.  The block form has no ring, but several blocks per SM.
 template <typename T, int W, int kLanes, int kE>
-__global__ void __launch_bounds__(256) norm_forward_short_kernel(const ForwardArgs a) {
+__global__ void __launch_bounds__(kLanes > 32 ? kLanes : 256) norm_forward_row_kernel(const ForwardArgs a) {
+  constexpr int kRows = kLanes > 32 ? 1 : 256 / kLanes;
+  __shared__ __align__(16) float scratch[2][kLanes > 32 ? kLanes / 32 : 1];
   const int lane = threadIdx.x % kLanes, N = static_cast<int>(a.N);
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kLanes;
   const bool live = m < a.M;
   const T* x = static_cast<const T*>(a.x) + (live ? m : 0) * N;
   float v[kE];
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(256) norm_forward_short_kernel(const ForwardAr
     if ((lane + i * kLanes) * W < N)
 #pragma unroll
       for (int k = 0; k < W; ++k) s += v[i * W + k];
-  const float mu = row_sum<kLanes>(s, nullptr) / static_cast<float>(N);
+  const float mu = row_sum<kLanes>(s, scratch[0]) / static_cast<float>(N);
   s = 0.f;
 #pragma unroll
   for (int i = 0; i < kE / W; ++i)
@@ -264,7 +270,7 @@ __global__ void __launch_bounds__(256) norm_forward_short_kernel(const ForwardAr
         v[i * W + k] -= mu;
         s += v[i * W + k] * v[i * W + k];
       }
-  const float r = 1.0f / sqrtf(row_sum<kLanes>(s, nullptr) / static_cast<float>(N) + a.eps);
+  const float r = 1.0f / sqrtf(row_sum<kLanes>(s, scratch[1]) / static_cast<float>(N) + a.eps);
   if (!live) return;
   T* y = static_cast<T*>(a.y) + m * N;
 #pragma unroll
@@ -320,7 +326,15 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel
     float t = 0.f;
 #pragma unroll
     for (int e = 0; e < kE / W; ++e) {
-      read<T, W>(x, (tid + e * kLanes) * W, N, v + e * W);
+      const int c = (tid + e * kLanes) * W;
+      // (a branch per pack, which keeps the loads apart: without it, on zeros
+      // behind the row, 16384 x 8192 bf16 took 99 us instead of 90)
+      if (c < N) {
+        read<T, W>(x, c, N, v + e * W);
+      } else {
+#pragma unroll
+        for (int k = 0; k < W; ++k) v[e * W + k] = 0.f;
+      }
 #pragma unroll
       for (int k = 0; k < W; ++k) t += v[e * W + k];
     }
@@ -457,19 +471,21 @@ int sm_count() {
 }
 
 // Stages of `mats` slices of `cols` elements, for per_sm blocks per SM.
-RingLayout ring_layout(int64_t cols, int elem, int mats, int per_sm) {
+// width: the elements that the block's threads read of a slice.
+RingLayout ring_layout(int64_t cols, int64_t width, bool aligned, int elem, int mats, int per_sm) {
   RingLayout L;
   L.cols = static_cast<int>(cols);
   // up to 15 bytes before a slice that starts off a boundary
-  L.slot_bytes = static_cast<int>(round_up(cols * elem + 16, 128));
+  L.slot_bytes = static_cast<int>(aligned ? width * elem : round_up(cols * elem + 16, 128));
   L.stages = static_cast<unsigned>(std::min(kMaxStages, kRingBytes / per_sm / (mats * L.slot_bytes)));
   return L;
 }
 
 template <typename T, int W, int kLanes, int kE>
-cudaError_t launch_forward_short(const ForwardArgs& a, cudaStream_t s) {
-  norm_forward_short_kernel<T, W, kLanes, kE>
-      <<<static_cast<unsigned>(ceil_div(a.M, 256 / kLanes)), 256, 0, s>>>(a);
+cudaError_t launch_forward_row(const ForwardArgs& a, cudaStream_t s) {
+  constexpr int kThreads = kLanes > 32 ? kLanes : 256;
+  norm_forward_row_kernel<T, W, kLanes, kE>
+      <<<static_cast<unsigned>(ceil_div(a.M, kThreads / kLanes)), kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -477,7 +493,7 @@ template <typename T, int W, int kLanes, int kE>
 cudaError_t launch_forward_ring(const ForwardArgs& a, cudaStream_t s) {
   auto kernel = norm_forward_ring_kernel<T, W, kLanes, kE>;
   constexpr int per_sm = 512 / kLanes;
-  const RingLayout L = ring_layout(a.N, sizeof(T), 1, per_sm);
+  const RingLayout L = ring_layout(a.N, round_up(a.N, 64), W > 1, sizeof(T), 1, per_sm);
   const int smem = static_cast<int>(L.stages) * L.slot_bytes;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
   kernel<<<static_cast<unsigned>(std::min<int64_t>(a.M, sm_count() * per_sm)), kLanes, smem, s>>>(a, L);
@@ -486,16 +502,18 @@ cudaError_t launch_forward_ring(const ForwardArgs& a, cudaStream_t s) {
 
 template <typename T, int W>
 cudaError_t forward_sized(const ForwardArgs& a, cudaStream_t s) {
-  if (a.N <= 64) return launch_forward_short<T, W, 8, 8>(a, s);
-  if (a.N <= 256) return launch_forward_short<T, W, 32, 8>(a, s);
-  if (a.N <= 512) return launch_forward_short<T, W, 32, 16>(a, s);
+  if (a.N <= 64) return launch_forward_row<T, W, 8, 8>(a, s);
+  if (a.N <= 256) return launch_forward_row<T, W, 32, 8>(a, s);
+  if (a.N <= 512) return launch_forward_row<T, W, 32, 16>(a, s);
   if (a.N <= 1024) return launch_forward_ring<T, W, 64, 16>(a, s);
   if (a.N <= 2048) return launch_forward_ring<T, W, 64, 32>(a, s);
   if (a.N <= 4096) return launch_forward_ring<T, W, 128, 32>(a, s);
   if (a.N <= 8192) return launch_forward_ring<T, W, 256, 32>(a, s);
+  if constexpr (W > 1)
+    if (a.N <= 16384) return launch_forward_row<T, W, 512, 32>(a, s);
   if (a.N * static_cast<int64_t>(sizeof(T)) <= kRingBytes / 2 - 256) {
     auto kernel = norm_forward_wide_kernel<T, W>;
-    const RingLayout L = ring_layout(a.N, sizeof(T), 1, 1);
+    const RingLayout L = ring_layout(a.N, round_up(a.N, 64), W > 1, sizeof(T), 1, 1);
     const int smem = static_cast<int>(L.stages) * L.slot_bytes;
     if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
     kernel<<<static_cast<unsigned>(std::min<int64_t>(a.M, sm_count())), kWideThreads, smem, s>>>(a, L);
@@ -646,8 +664,8 @@ __device__ __forceinline__ float warp_sums(float (&v)[kN]) {
 
 // Rows of up to 8192 elements through the ring, a block per row: 16 elements
 // in each thread's registers, with w and the gradient sums of their columns
-// over all the block's rows.  kFull: the threads' packs cover the row exactly.
-template <typename T, int W, int kLanes, int kE, bool kFull>
+// over all the block's rows.
+template <typename T, int W, int kLanes, int kE>
 __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kernel(const BackwardArgs a,
                                                                                  const RingLayout L) {
   extern __shared__ __align__(128) uint8_t stages[];
@@ -655,12 +673,13 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
   __shared__ uint64_t full[kMaxStages];
   __shared__ __align__(16) float2 scratch[2][kWarps];
   __shared__ int abort_flag;
-  const int tid = threadIdx.x, cols = kFull ? kLanes * kE : L.cols;
+  const int tid = threadIdx.x, cols = L.cols;
   Ring<T, 2> ring{{static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.g)},
                   stages, full, L, a.N, 0, gridDim.x,
                   (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
                   static_cast<unsigned long long>(a.M) * a.N * sizeof(T), cols};
   const int rows = static_cast<int>(ring.rows);
+  if constexpr (W > 1) zero_tails(ring, kLanes);
   if (tid == 0) {
     ring_setup(full, L.stages, &abort_flag);
     if (blockIdx.x == 0) *a.st = DevStatus{0, 0, 0, 0};
@@ -674,7 +693,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
     const int c = (tid + i * kLanes) * W;
 #pragma unroll
     for (int k = 0; k < W; ++k) w[i * W + k] = aw[i * W + k] = ab[i * W + k] = 0.f;
-    if (kFull || c < cols) load_param<W>(a.w, a.wt, c, 1.f, w + i * W);
+    if (c < cols) load_param<W>(a.w, a.wt, c, 1.f, w + i * W);
   }
   const float inv_n = 1.0f / static_cast<float>(a.N);
   const bool want_x = a.gx != nullptr;
@@ -704,8 +723,8 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
       const int c = (tid + e * kLanes) * W;
-      read<T, W>(xs, c, kFull ? c + 1 : cols, h + e * W);
-      read<T, W>(gs, c, kFull ? c + 1 : cols, g + e * W);
+      read<T, W>(xs, c, cols, h + e * W);
+      read<T, W>(gs, c, cols, g + e * W);
 #pragma unroll
       for (int k = e * W; k < (e + 1) * W; ++k) {
         h[k] = (h[k] - cmu) * cr;
@@ -744,7 +763,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
       const int c = (tid + e * kLanes) * W;
 #pragma unroll
       for (int k = e * W; k < (e + 1) * W; ++k) g[k] = fmaf(h[k], c2, fmaf(g[k], cr, c1));
-      if (kFull || c < cols) store_floats<T, W>(out + c, g + e * W);
+      if (c < cols) store_floats<T, W>(out + c, g + e * W);
     }
     out += gridDim.x * a.N;
   }
@@ -755,7 +774,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int c = (tid + i * kLanes) * W;
-    if (!kFull && c >= cols) continue;
+    if (c >= cols) continue;
 #pragma unroll
     for (int k = 0; k < W; ++k) {
       pw[c + k] = aw[i * W + k];
@@ -787,6 +806,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
                   (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
                   static_cast<unsigned long long>(a.M) * a.N * sizeof(T), cols};
   const int64_t rows = ring.rows, steps = (rows + kRows - 1) / kRows;
+  if constexpr (W > 1) zero_tails(ring, kLanes);
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) mbar_init(&sent[i], 1);
     ring_setup(full, L.stages, &abort_flag);
@@ -1007,9 +1027,8 @@ cudaError_t launch_short(Shape& h) {
 template <typename T, int W, int kLanes, int kE>
 cudaError_t launch_ring(Shape& h) {
   constexpr int per_sm = 512 / kLanes;
-  const RingLayout L = ring_layout(h.a.N, sizeof(T), 2, per_sm);
-  auto kernel = W > 1 && h.a.N == kLanes * kE ? norm_backward_ring_kernel<T, W, kLanes, kE, W != 1>
-                                              : norm_backward_ring_kernel<T, W, kLanes, kE, false>;
+  const RingLayout L = ring_layout(h.a.N, kLanes * kE, W > 1, sizeof(T), 2, per_sm);
+  auto kernel = norm_backward_ring_kernel<T, W, kLanes, kE>;
   const int smem = static_cast<int>(L.stages) * 2 * L.slot_bytes;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
   h.blocks = static_cast<int>(
@@ -1046,7 +1065,7 @@ int cached_clusters(const void* fn, int smem, int ranks, Query query) {
 // before it and of the next.
 template <typename T, int W>
 cudaError_t launch_cluster(Shape& h, int ranks, int cols) {
-  const RingLayout L = ring_layout(cols, sizeof(T), 2, 1);
+  const RingLayout L = ring_layout(cols, 512 * 16, W > 1, sizeof(T), 2, 1);
   auto kernel = L.stages >= 6u ? norm_backward_cluster_kernel<T, W, 512, 16, 2>
                                : norm_backward_cluster_kernel<T, W, 512, 16, 1>;
   const int smem = static_cast<int>(L.stages) * 2 * L.slot_bytes;
@@ -1089,6 +1108,7 @@ cudaError_t backward_sized(Shape& h) {
   if (N <= 1024) return launch_ring<T, W, 64, 16>(h);
   if (N <= 2048) return launch_ring<T, W, 128, 16>(h);
   if (N <= 4096) return launch_ring<T, W, 256, 16>(h);
+  if (N <= 6144) return launch_ring<T, W, 384, 16>(h);
   if (N <= kSliceCols) return launch_ring<T, W, 512, 16>(h);
   const int64_t ranks = ceil_div(N, kSliceCols);
   if (ranks <= kMaxCluster) {
