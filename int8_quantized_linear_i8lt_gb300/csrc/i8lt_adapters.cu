@@ -9,7 +9,10 @@
 // type's precision, and both take part: a rounded t would be off by as much
 // as the gradient's own rounding (and by more where few tokens make it up).
 // y and gx take the first value alone: its error is the type's rounding of a
-// correction to base and addend.
+// correction to base and addend.  Their rows are in the plan's order, so that
+// the tokens of a tile are a box of consecutive rows whatever the batch's
+// order: 8192 interleaved tokens of 8 adapters, 4096 -> 11008, rank 64, took
+// 349 us forward and backward with t and u gathered by token, 290 us so.
 #include <algorithm>
 
 #include "i8lt.h"
@@ -66,7 +69,7 @@ Plan plan_layout(void* base, int64_t M, int64_t E) {
 // One block per group: counts the tokens of the groups before it, then places
 // its own in order (a stable sort, the same on every run) and fills its slots.
 // A thread takes 8 consecutive tokens per pass, so that a batch of 8192 is one
-// pass of 1024 threads (FIGURE us, against 35 us for a warp per group).
+// pass of 1024 threads (8 us, against 35 us for a warp per group).
 constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const int32_t* index, int M, int E, int* offset,
                                                                     int* perm, Tile* tiles) {
@@ -401,7 +404,7 @@ struct ShrinkArgs {
   CUtensorMap tmX, tmX1, tmW;   // with kTma: X, box 64 x 128 and 64 x 1; W, box 64 x r16 (K-major) or 64 x 64
   const uint16_t* X;      // [M, C]
   const uint16_t* W;      // per group [R, C] (K-major) or [C, R] (MN-major)
-  uint16_t* mid;          // [2, M, R]: the values, and what their rounding left
+  uint16_t* mid;          // [2, M, R] in the plan's order: the values, and what their rounding left
   int64_t plane;          // M R
   const float* scale;     // applied when not NULL
   const Tile* tiles;
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
   if (t.group >= a.E) {
     if (rank == 0)
       for (int i = tid; i < t.count * R; i += kThreads) {
-        uint16_t* o = a.mid + static_cast<int64_t>(a.perm[t.start + i / R]) * R + i % R;
+        uint16_t* o = a.mid + static_cast<int64_t>(t.start) * R + i;
         o[0] = o[a.plane] = 0;
       }
     return;
@@ -445,8 +448,8 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
   const uint32_t base = align1024(smem_u32(smem_raw));
   const int stage_bytes = shrink_stage_bytes(r16, kMN);
   const int nb = static_cast<int>((a.C + 63) / 64);
-  const int b0 = static_cast<int>(static_cast<int64_t>(nb) * rank / ranks);
-  const int n = static_cast<int>(static_cast<int64_t>(nb) * (rank + 1) / ranks) - b0;
+  const int n = (nb - rank + ranks - 1) / ranks;   // blocks rank, rank + ranks, ...
+  auto column = [&](int it) { return static_cast<int64_t>(rank + it * ranks) * 64; };
   const int64_t C = a.C;
   const uint16_t* W = a.W + static_cast<int64_t>(t.group) * R * C;
   sync_setup(y, tmem_columns(r16));
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
       int rows[4];
       if (t.row0 < 0) tile_rows(a.perm, t.start, t.count, rows);
       for (int it = 0; it < n; ++it) {
-        const int s = it % kStages, c0 = (b0 + it) * 64;
+        const int s = it % kStages, c0 = static_cast<int>(column(it));
         uint8_t *xs = stages + s * stage_bytes, *ws = xs + 128 * kRowBytes;
         if (it >= kStages) mbar_wait(&y.done[s], (it / kStages - 1) & 1, &y.abort, a.st, 20);
         if (tid == 0) {
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
       xrow[i] = row < t.count ? a.X + static_cast<int64_t>(a.perm[t.start + row]) * C : nullptr;
     }
     auto load = [&](int b, int s) {
-      const int64_t c0 = static_cast<int64_t>(b0 + b) * 64;
+      const int64_t c0 = column(b);
       const uint32_t xs = base + s * stage_bytes, ws = xs + 128 * kRowBytes;
       const int64_t at = c0 + (tid & 7) * 8;
 #pragma unroll
@@ -557,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
     if (row >= t.count || j >= R) continue;
     float s[4];
     cluster_sum4(base, row * red_pitch(r16) + j, ranks, s);
-    uint16_t* o = a.mid + static_cast<int64_t>(a.perm[t.start + row]) * R + j;
+    uint16_t* o = a.mid + static_cast<int64_t>(t.start + row) * R + j;
     uint16_t hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -582,9 +585,8 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
 // ---- out = addend + scale mid W^T (y and gx) --------------------------------
 
 struct ExpandArgs {
-  // with kTma: mid, addend and out, box 64 x 128 (mid also 64 x 1); W, box 64 x 64 or 64 x r16
-  CUtensorMap tmMid, tmMid1, tmW, tmAdd, tmOut;
-  const uint16_t* mid;     // [M, R]
+  CUtensorMap tmMid, tmW, tmAdd, tmOut;   // with kTma: mid, addend and out, box 64 x 128; W, box 64 x 64 or 64 x r16
+  const uint16_t* mid;     // [M, R], in the plan's order
   const uint16_t* W;       // per group [C, R] (K-major) or [R, C] (MN-major)
   const uint16_t* addend;  // [M, C] or NULL; may be out
   uint16_t* out;           // [M, C]
@@ -755,8 +757,6 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
 
   if constexpr (kTma) {
     if (warp == 8) {
-      int rows[4];
-      if (t.row0 < 0) tile_rows(a.perm, t.start, t.count, rows);
       for (int j = 0; j < n; ++j) {
         const int c0 = (j0 + j) * kCols;
         if (adapter && lane == 0) {
@@ -782,12 +782,10 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
         // tile's W and addend are on their way
         if (j == 0 && adapter) {
           grid_dependency_wait();
-          if (lane == 0) mbar_arrive_expect_tx(&y.mid_full, expand_mid_bytes(r16));
-          __syncwarp();
-          for (int k = 0; k < expand_blocks(r16); ++k) {
-            uint8_t* ms = mids + k * 128 * kRowBytes;
-            if (t.row0 < 0) tma_gather4(ms + lane * 4 * kRowBytes, &a.tmMid1, 64 * k, rows, &y.mid_full);
-            else if (lane == 0) tma_load_2d(ms, &a.tmMid, 64 * k, t.row0, &y.mid_full);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&y.mid_full, expand_mid_bytes(r16));
+            for (int k = 0; k < expand_blocks(r16); ++k)
+              tma_load_2d(mids + k * 128 * kRowBytes, &a.tmMid, 64 * k, t.start, &y.mid_full);
           }
         }
       }
@@ -866,7 +864,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
       for (int i = tid; i < t.count * chunks; i += kThreads) {
         const int row = i / chunks, c = i % chunks;
         load_chunk(smem_u32(mids) + (c >> 3) * 128 * kRowBytes + swizzled(row, c & 7),
-                   a.mid + static_cast<int64_t>(a.perm[t.start + row]) * R, c * 8, R - c * 8, a.rw);
+                   a.mid + static_cast<int64_t>(t.start + row) * R, c * 8, R - c * 8, a.rw);
       }
     load_w(0);
     load_addend(0);
@@ -905,20 +903,27 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
 
 // ---- gradients of A and B ---------------------------------------------------
 
-struct GradArgs {
-  CUtensorMap tmX, tmU, tmX1, tmU1;   // with kTma: X and mid, box 64 x 64 and 64 x 1
-  const uint16_t* mid;    // [2, M, R]
+struct GradSide {   // gB (of g and t) or gA (of x and u)
+  CUtensorMap tmX, tmX1, tmU;   // with kTma: X, box 64 x 64 and 64 x 1; mid, box 64 x 64
+  const uint16_t* mid;    // [2, M, R], in the plan's order
   const uint16_t* X;      // [M, C]
-  uint16_t* grad;         // per group [R, C] (kRankMajor) or [C, R]
+  uint16_t* grad;         // per group [R, C] (rank_major) or [C, R]
   const float* scale;
+  int64_t C;
+  int64_t tiles;          // clusters: strips of 128 columns times groups
+  int strips, cw;
+  bool rank_major;
+  bool wait;              // mid is the output of the kernel before this one
+};
+struct GradArgs {
+  GradSide side[2];       // the second one's clusters follow the first one's
   const int* offset;
   const int* perm;
   DevStatus* st;
-  int64_t C;
-  int M, R, cw, rw, mw;   // mw: the copy width of mid's second part
+  int M, R, rw, mw;       // mw: the copy width of mid's second part
+  int ranks;              // CTAs per cluster
   bool bf16;
   bool first;             // the call's first kernel: clears the status
-  bool wait;              // mid is the output of the kernel before this one
 };
 
 __host__ __device__ constexpr int grad_mid_bytes(int r16) { return (r16 > 64 ? 2 : 1) * 64 * kRowBytes; }
@@ -927,26 +932,30 @@ __host__ __device__ constexpr int grad_stage_bytes(int r16) { return 2 * 64 * kR
 // grad[c, j] = scale sum_m X[m, c] mid[m, j] over a group's tokens: one
 // cluster per (128 columns of X, group), its CTAs splitting the tokens.
 // Bound by reading X once.
-template <bool kRankMajor, int kStages, bool kTma>
+template <int kStages, bool kTma>
 __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant__ GradArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Sync y;
-  const int tid = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x, R = a.R, r16 = rank16(R);
-  const int64_t C = a.C, c0 = static_cast<int64_t>(blockIdx.y) * 128;
-  const int64_t e = blockIdx.z;
+  const int tid = threadIdx.x, ranks = a.ranks, rank = blockIdx.x % ranks, R = a.R, r16 = rank16(R);
+  int64_t tile = blockIdx.x / ranks;
+  const bool second = tile >= a.side[0].tiles;
+  const GradSide& d = a.side[second ? 1 : 0];
+  if (second) tile -= a.side[0].tiles;
+  const int64_t C = d.C, e = tile / d.strips, c0 = tile % d.strips * 128;
+  const bool rank_major = d.rank_major;
   if (kTma && tid == 0) {
-    tma_prefetch_desc(&a.tmX);
-    tma_prefetch_desc(&a.tmU);
+    tma_prefetch_desc(&d.tmX);
+    tma_prefetch_desc(&d.tmU);
   }
-  if (a.first && blockIdx.x == 0 && blockIdx.y == 0 && e == 0 && tid == 0) *a.st = DevStatus{0, 0, 0, 0};
+  if (a.first && blockIdx.x == 0 && tid == 0) *a.st = DevStatus{0, 0, 0, 0};
   const int start = a.offset[e], tokens = a.offset[e + 1] - start;
   const int cols = static_cast<int>(min(static_cast<int64_t>(128), C - c0));
-  uint16_t* grad = a.grad + e * R * C;
+  uint16_t* grad = d.grad + e * R * C;
   if (tokens == 0) {
     grid_dependency_wait();
     if (rank == 0)
       for (int i = tid; i < cols * R; i += kThreads)
-        grad[kRankMajor ? i / cols * C + c0 + i % cols : c0 * R + i] = 0;
+        grad[rank_major ? i / cols * C + c0 + i % cols : c0 * R + i] = 0;
     return;
   }
   const uint32_t base = align1024(smem_u32(smem_raw));
@@ -972,45 +981,50 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
     umma_commit(&y.done[s]);
     if (it == n - 1) umma_commit(&y.last);
   };
-  // The reduction runs over tokens, so a last block of fewer than 64 must not
-  // reach into the next group's rows: it is gathered, its last token repeated,
-  // and the repeated rows of mid are set to zero before its products.
+  // A block of consecutive tokens of X is fetched as a box, others four rows
+  // at a time.  The reduction runs over tokens, so a last block of fewer than
+  // 64 must not reach into other groups' rows of X (whatever they hold would
+  // be multiplied by zero): its last token is repeated, and the rows of mid
+  // past it are set to zero before its products.
   if constexpr (kTma) {
     if (tid < 32) {
       uint8_t* stages = smem_raw + (base - smem_u32(smem_raw));
       const int half = tid >> 4, quad = tid & 15;   // lanes 0-15 fetch the first 64 columns, 16-31 the others
-      if (a.wait) grid_dependency_wait();
+      auto rows_of = [&](int it, int(&rows)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = min((b0 + it) * 64 + 4 * quad + i, tokens - 1);
+          rows[i] = run ? first + k : a.perm[start + k];
+        }
+      };
+      int rows[4], next[4];
+      rows_of(0, next);
+      if (d.wait) grid_dependency_wait();
       for (int it = 0; it < n; ++it) {
         const int s = it % kStages, m0 = (b0 + it) * 64;
         uint8_t *xs = stages + s * stage_bytes, *us = xs + 2 * 64 * kRowBytes;
-        const bool box = run && m0 + 64 <= tokens;
-        int rows[4];
-        if (!box)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) rows[i] = a.perm[start + min(m0 + 4 * quad + i, tokens - 1)];
+        for (int i = 0; i < 4; ++i) rows[i] = next[i];
+        rows_of(it + 1, next);
+        const int row0 = __shfl_sync(0xffffffffu, rows[0], 0);
+        const bool box = __all_sync(0xffffffffu, rows[0] == row0 + 4 * quad && rows[3] == rows[0] + 3);   // ascending
         if (it >= kStages) mbar_wait(&y.done[s], (it / kStages - 1) & 1, &y.abort, a.st, 23);
         if (tid == 0) {
           mbar_arrive_expect_tx(&y.full[s], stage_bytes);
+          for (int k = 0; k < 2; ++k) {
+            uint8_t* u = us + k * grad_mid_bytes(r16);
+            tma_load_2d(u, &d.tmU, 0, k * a.M + start + m0, &y.full[s]);
+            if (r16 > 64) tma_load_2d(u + 64 * kRowBytes, &d.tmU, 64, k * a.M + start + m0, &y.full[s]);
+          }
           if (box) {
-            tma_load_2d(xs, &a.tmX, static_cast<int>(c0), first + m0, &y.full[s]);
-            tma_load_2d(xs + 64 * kRowBytes, &a.tmX, static_cast<int>(c0) + 64, first + m0, &y.full[s]);
-            for (int k = 0; k < 2; ++k) {
-              uint8_t* u = us + k * grad_mid_bytes(r16);
-              tma_load_2d(u, &a.tmU, 0, k * a.M + first + m0, &y.full[s]);
-              if (r16 > 64) tma_load_2d(u + 64 * kRowBytes, &a.tmU, 64, k * a.M + first + m0, &y.full[s]);
-            }
+            tma_load_2d(xs, &d.tmX, static_cast<int>(c0), row0, &y.full[s]);
+            tma_load_2d(xs + 64 * kRowBytes, &d.tmX, static_cast<int>(c0) + 64, row0, &y.full[s]);
           }
         }
         __syncwarp();   // the stage is armed before its gathers arrive
-        if (!box) {
-          const int at = (half * 64 + quad * 4) * kRowBytes;
-          tma_gather4(xs + at, &a.tmX1, static_cast<int>(c0) + 64 * half, rows, &y.full[s]);
-          const int rest[4] = {a.M + rows[0], a.M + rows[1], a.M + rows[2], a.M + rows[3]};
-          if (half == 0 || r16 > 64) {
-            tma_gather4(us + at, &a.tmU1, 64 * half, rows, &y.full[s]);
-            tma_gather4(us + grad_mid_bytes(r16) + at, &a.tmU1, 64 * half, rest, &y.full[s]);
-          }
-        }
+        if (!box)
+          tma_gather4(xs + (half * 64 + quad * 4) * kRowBytes, &d.tmX1, static_cast<int>(c0) + 64 * half, rows,
+                      &y.full[s]);
       }
     } else if (tid < 64) {
       for (int it = 0; it < n; ++it) {
@@ -1033,7 +1047,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
     }
     __syncwarp();
   } else {
-    if (a.wait) grid_dependency_wait();
+    if (d.wait) grid_dependency_wait();
     // the tokens of a step are read one step before their copies are issued
     constexpr int kMidPer = 4;   // up to 64 rows x 16 chunks of mid over 256 threads
     int xm[4], um[kMidPer];
@@ -1047,7 +1061,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
 #pragma unroll
       for (int i = 0; i < kMidPer; ++i) {
         const int k = m0 + (tid + i * kThreads) / chunks;
-        um[i] = tid + i * kThreads < 64 * chunks && k < tokens ? (run ? first + k : a.perm[start + k]) : -1;
+        um[i] = tid + i * kThreads < 64 * chunks && k < tokens ? start + k : -1;
       }
     };
     auto load = [&](int b, int s) {   // of the rows that rows_of(b) found
@@ -1056,14 +1070,14 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         load_chunk(xs + (c >> 3) * 64 * kRowBytes + swizzled((tid >> 4) + 16 * i, c & 7),
-                   a.X + static_cast<int64_t>(max(xm[i], 0)) * C, c0 + c * 8, xm[i] >= 0 ? C - (c0 + c * 8) : 0, a.cw);
+                   d.X + static_cast<int64_t>(max(xm[i], 0)) * C, c0 + c * 8, xm[i] >= 0 ? C - (c0 + c * 8) : 0, d.cw);
 #pragma unroll
       for (int i = 0; i < kMidPer; ++i) {
         const int at = tid + i * kThreads;
         if (at >= 64 * chunks) break;
         const int k = at / chunks, q = at % chunks;
         const uint32_t dst = us + (q >> 3) * 64 * kRowBytes + swizzled(k, q & 7);
-        const uint16_t* row = a.mid + static_cast<int64_t>(max(um[i], 0)) * R;
+        const uint16_t* row = d.mid + static_cast<int64_t>(max(um[i], 0)) * R;
         load_chunk(dst, row, q * 8, um[i] >= 0 ? R - q * 8 : 0, a.rw);
         load_chunk(dst + grad_mid_bytes(r16), row + static_cast<int64_t>(a.M) * R, q * 8,
                    um[i] >= 0 ? R - q * 8 : 0, a.mw);
@@ -1104,15 +1118,15 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
   grid_dependents_launch();
   cluster_sync();
   const int rows = (128 + ranks - 1) / ranks, row0 = rank * rows;
-  const float scale = a.scale != nullptr ? a.scale[e] : 1.f;
+  const float scale = d.scale != nullptr ? d.scale[e] : 1.f;
   const int quads = r16 / 4;
   for (int i = tid; i < rows * quads; i += kThreads) {
     // neighbouring threads on neighbouring elements of the gradient
-    const int row = row0 + (kRankMajor ? i % rows : i / quads), j = (kRankMajor ? i / rows : i % quads) * 4;
+    const int row = row0 + (rank_major ? i % rows : i / quads), j = (rank_major ? i / rows : i % quads) * 4;
     if (row >= cols || row >= 128 || j >= R) continue;
     float s[4];
     cluster_sum4(base, row * red_pitch(r16) + j, ranks, s);
-    if (!kRankMajor && R % 4 == 0) {
+    if (!rank_major && R % 4 == 0) {
       *reinterpret_cast<uint2*>(grad + (c0 + row) * R + j) =
           make_uint2(to_16(scale * s[0], a.bf16) | static_cast<uint32_t>(to_16(scale * s[1], a.bf16)) << 16,
                      to_16(scale * s[2], a.bf16) | static_cast<uint32_t>(to_16(scale * s[3], a.bf16)) << 16);
@@ -1120,7 +1134,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (j + k < R)
-          grad[kRankMajor ? (j + k) * C + c0 + row : (c0 + row) * R + j + k] = to_16(scale * s[k], a.bf16);
+          grad[rank_major ? (j + k) * C + c0 + row : (c0 + row) * R + j + k] = to_16(scale * s[k], a.bf16);
     }
   }
   // what follows this kernel may rely on what came before it
@@ -1240,7 +1254,7 @@ __global__ void __launch_bounds__(kThreads, kMaxRankTiles > 4 ? 2 : kMaxRankTile
         const uint16_t hi = to_16(s[k], kBf16);
         ts[tok][j] = hi;
         if (rank == 0 && tok < tile.count && j < R) {
-          uint16_t* o = a.t + static_cast<int64_t>(a.perm[tile.start + tok]) * R + j;
+          uint16_t* o = a.t + static_cast<int64_t>(tile.start + tok) * R + j;
           o[0] = hi;
           o[a.plane] = rest_16(s[k], hi, kBf16);
         }
@@ -1249,7 +1263,7 @@ __global__ void __launch_bounds__(kThreads, kMaxRankTiles > 4 ? 2 : kMaxRankTile
     __syncthreads();
   } else if (rank == 0) {
     for (int i = tid; i < tile.count * R; i += kThreads) {
-      uint16_t* o = a.t + static_cast<int64_t>(a.perm[tile.start + i / R]) * R + i % R;
+      uint16_t* o = a.t + static_cast<int64_t>(tile.start) * R + i;
       o[0] = o[a.plane] = 0;
     }
   }
@@ -1431,7 +1445,6 @@ cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, 
   const dim3 grid(static_cast<unsigned>(p.plan.slots), static_cast<unsigned>(ceil_div(col_tiles, a.col_tiles)));
   const bool tma = tma_rows(p, C);
   if (tma && (!make_tmap(&a.tmMid, map_type(p), mid, p.R, p.M, p.R * 2, 64, 128, kSwz) ||
-              !make_tmap(&a.tmMid1, map_type(p), mid, p.R, p.M, p.R * 2, 64, 1, kSwz) ||
               !make_tmap(&a.tmAdd, map_type(p), addend != nullptr ? addend : out, C, p.M, C * 2, 64, 128, kSwz) ||
               !make_tmap(&a.tmOut, map_type(p), out, C, p.M, C * 2, 64, 128, kSwz) ||
               !(mn ? make_tmap_3d(&a.tmW, map_type(p), W, C, p.R, p.E, 2, 64, r16, kSwz)
@@ -1442,40 +1455,55 @@ cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, 
   return launch(kernel, a, grid, kExpandThreads, 1, smem, K_ADAPTERS, true, p.s);
 }
 
-cudaError_t grad(const Problem& p, const void* mid, const void* X, int64_t C, bool rank_major, const float* scale,
-                 void* out, bool after, bool wait) {
+// One side of the gradients; count 0 when it is not wanted.
+bool grad_side(const Problem& p, const void* mid, const void* X, int64_t C, bool rank_major, const float* scale,
+               void* out, bool wait, bool tma, GradSide* d) {
+  d->tiles = 0;
+  d->strips = 1;
+  if (out == nullptr) return true;
+  d->mid = static_cast<const uint16_t*>(mid);
+  d->X = static_cast<const uint16_t*>(X);
+  d->grad = static_cast<uint16_t*>(out);
+  d->scale = scale;
+  d->C = C;
+  d->strips = static_cast<int>(ceil_div(C, 128));
+  d->tiles = p.E * d->strips;
+  d->cw = copy_width(C);
+  d->rank_major = rank_major;
+  d->wait = wait;
+  return !tma || (make_tmap(&d->tmX, map_type(p), X, C, p.M, C * 2, 64, 64, kSwz) &&
+                  make_tmap(&d->tmU, map_type(p), mid, p.R, 2 * p.M, p.R * 2, 64, 64, kSwz) &&
+                  make_tmap(&d->tmX1, map_type(p), X, C, p.M, C * 2, 64, 1, kSwz));
+}
+
+// Both gradients in one launch: gB needs nothing of this call, gA the u of the
+// kernel before (after).
+cudaError_t grads(const Problem& p, const void* g, const void* t, void* gB, const void* x, const void* u, void* gA,
+                  bool after) {
   GradArgs a;
-  a.mid = static_cast<const uint16_t*>(mid);
-  a.X = static_cast<const uint16_t*>(X);
-  a.grad = static_cast<uint16_t*>(out);
-  a.scale = scale;
+  const bool tma = tma_rows(p, gB != nullptr ? p.N : 8) && tma_rows(p, gA != nullptr ? p.K : 8);
+  if (!grad_side(p, t, g, p.N, false, p.scale, gB, false, tma, &a.side[0]) ||
+      !grad_side(p, u, x, p.K, true, nullptr, gA, true, tma, &a.side[1]))
+    return cudaErrorUnknown;
   a.offset = p.plan.offset;
   a.perm = p.plan.perm;
   a.st = p.st;
-  a.C = C;
-  a.wait = wait;
-  a.first = !after;
   a.M = static_cast<int>(p.M);
-  a.mw = std::min(copy_width(p.R), copy_width(p.M * p.R));
   a.R = p.R;
-  a.cw = copy_width(C);
   a.rw = copy_width(p.R);
+  a.mw = std::min(copy_width(p.R), copy_width(p.M * p.R));
   a.bf16 = p.bf16;
-  const int r16 = rank16(p.R), ranks = split(ceil_div(C, 128) * p.E, ceil_div(ceil_div(p.M, p.E), 64));
+  a.first = !after;
+  const int r16 = rank16(p.R);
+  const int64_t tiles = a.side[0].tiles + a.side[1].tiles;
+  a.ranks = split(tiles, ceil_div(ceil_div(p.M, p.E), 64));
+  if (tiles > INT32_MAX / a.ranks) return cudaErrorInvalidValue;
   const int stages = r16 > 64 ? 2 : 3;
   const int smem = 1024 + std::max(stages * grad_stage_bytes(r16), 128 * red_pitch(r16) * 4);
-  const dim3 grid(static_cast<unsigned>(ranks), static_cast<unsigned>(ceil_div(C, 128)), static_cast<unsigned>(p.E));
-  const bool tma = tma_rows(p, C);
-  if (tma && (!make_tmap(&a.tmX, map_type(p), X, C, p.M, C * 2, 64, 64, kSwz) ||
-              !make_tmap(&a.tmU, map_type(p), mid, p.R, 2 * p.M, p.R * 2, 64, 64, kSwz) ||
-              !make_tmap(&a.tmX1, map_type(p), X, C, p.M, C * 2, 64, 1, kSwz) ||
-              !make_tmap(&a.tmU1, map_type(p), mid, p.R, 2 * p.M, p.R * 2, 64, 1, kSwz)))
-    return cudaErrorUnknown;
-  auto k3 = tma ? (rank_major ? grad_kernel<true, 3, true> : grad_kernel<false, 3, true>)
-                : (rank_major ? grad_kernel<true, 3, false> : grad_kernel<false, 3, false>);
-  auto k2 = tma ? (rank_major ? grad_kernel<true, 2, true> : grad_kernel<false, 2, true>)
-                : (rank_major ? grad_kernel<true, 2, false> : grad_kernel<false, 2, false>);
-  return launch(stages == 3 ? k3 : k2, a, grid, kThreads, ranks, smem, K_ADAPTERS_GRAD, after, p.s);
+  const dim3 grid(static_cast<unsigned>(tiles * a.ranks));
+  auto kernel = tma ? (stages == 3 ? grad_kernel<3, true> : grad_kernel<2, true>)
+                    : (stages == 3 ? grad_kernel<3, false> : grad_kernel<2, false>);
+  return launch(kernel, a, grid, kThreads, a.ranks, smem, K_ADAPTERS_GRAD, after, p.s);
 }
 
 cudaError_t forward(const Problem& p, const void* x, const void* A, const void* B, const void* base, void* y,
@@ -1501,16 +1529,11 @@ cudaError_t backward(const Problem& p, const void* g, const void* x, const void*
   if (need_u) {
     if (cudaError_t e = shrink(p, g, p.N, B, true, p.scale, u)) return e;
   }
-  // right after the pass over g, of which a part is still in L2; it reads
-  // nothing that the pass wrote
-  if (gB != nullptr) {
-    if (cudaError_t e = grad(p, t, g, p.N, false, p.scale, gB, need_u, false)) return e;
+  // right after the pass over g, of which a part is still in L2
+  if (gA != nullptr || gB != nullptr) {
+    if (cudaError_t e = grads(p, g, t, gB, x, u, gA, need_u)) return e;
   }
-  if (gx != nullptr) {
-    if (cudaError_t e = expand(p, u, A, p.K, true, nullptr, addend, gx)) return e;
-  }
-  if (gA != nullptr) return grad(p, u, x, p.K, true, nullptr, gA, true, true);
-  return cudaSuccess;
+  return gx != nullptr ? expand(p, u, A, p.K, true, nullptr, addend, gx) : cudaSuccess;
 }
 
 constexpr int64_t kMaxRank = 128, kMaxAdapters = 65535;

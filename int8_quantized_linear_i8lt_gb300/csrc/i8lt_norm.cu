@@ -723,8 +723,15 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
       const int c = (tid + e * kLanes) * W;
-      read<T, W>(xs, c, cols, h + e * W);
-      read<T, W>(gs, c, cols, g + e * W);
+      // Packs are read with the zeros behind their row: a branch per pack took
+      // 16384 x 8192 bf16 from 143 to 186 us. Single columns have more to skip:
+      // 8192 x 5001 bf16 takes 103 us with the branch and 130 us without.
+      if (W > 1 || c < cols) {
+        read<T, W>(xs, c, cols, h + e * W);
+        read<T, W>(gs, c, cols, g + e * W);
+      } else {
+        h[e] = g[e] = 0.f;
+      }
 #pragma unroll
       for (int k = e * W; k < (e + 1) * W; ++k) {
         h[k] = (h[k] - cmu) * cr;

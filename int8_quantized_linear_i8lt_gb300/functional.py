@@ -784,7 +784,7 @@ def adapters_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: t
     token's adapter e (i8lt_adapters_forward): x [M, K] (f16 / bf16),
     A [E, r, K], B [E, N, r], scale fp32 [E] or None, base [M, N] or None.
     ``out`` may be base itself (not x).  t [2, M, r], two 16-bit parts of one
-    value, is what the backward needs."""
+    value with the tokens in the plan's order, is what the backward needs."""
     what = "adapters_forward"
     dev, M, K, E, r, N, A, B, scale = _adapter_args(what, x, A, B, scale, plan)
     dtype, device = x.dtype, x.device
