@@ -1142,6 +1142,212 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
   cluster_sync();
 }
 
+// The same for more strips than CTAs (many adapters, or wide layers of few):
+// each CTA takes strip after strip, whole, with the fetches of the next one
+// under way while the last one leaves tensor memory.  Warps 0-3 turn
+// accumulators into gradients, warp 4 fetches, warp 5 issues the products.
+// 8192 tokens of 32 adapters, 4096 -> 11008, rank 64: both gradients take 81 us
+// by it and 159 us by one CTA per strip; 8 adapters 70 us and 76 us.
+constexpr int kManyThreads = 192;
+struct ManySync {
+  uint64_t full[kMaxStages], done[kMaxStages], acc_full[2], acc_free[2];
+  uint32_t tmem;
+  int abort;
+};
+template <int kStages>
+__global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid_constant__ GradArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ ManySync y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = a.R, r16 = rank16(R);
+  if (a.first && blockIdx.x == 0 && tid == 0) *a.st = DevStatus{0, 0, 0, 0};
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&y.full[i], 1);
+      mbar_init(&y.done[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&y.acc_full[i], 1);
+      mbar_init(&y.acc_free[i], 128);
+    }
+    y.abort = 0;
+    fence_mbar_init();
+  }
+  const uint32_t columns = tmem_columns(r16);   // of one accumulator
+  if (warp == 0) {
+    tmem_alloc(&y.tmem, 2 * columns);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  const int stage_bytes = grad_stage_bytes(r16);
+  uint8_t* stages = smem_raw + (align1024(smem_u32(smem_raw)) - smem_u32(smem_raw));
+  struct Strip {
+    bool second;
+    int e, start, tokens;
+    int64_t c0;
+  };
+  const int64_t strips = a.side[0].tiles + a.side[1].tiles;
+  auto strip_of = [&](int64_t i) {
+    Strip t{i >= a.side[0].tiles, 0, 0, 0, 0};
+    if (i >= strips) return t;
+    const GradSide& d = a.side[t.second];
+    if (t.second) i -= a.side[0].tiles;
+    t.e = static_cast<int>(i / d.strips);
+    t.c0 = i % d.strips * 128;
+    t.start = a.offset[t.e];
+    t.tokens = a.offset[t.e + 1] - t.start;
+    return t;
+  };
+  const int64_t step = gridDim.x;
+  if (warp == 4) {
+    const int half = lane >> 4, quad = lane & 15;   // lanes 0-15 fetch the first 64 columns, 16-31 the others
+    int rows[4], next[4];
+    auto rows_of = [&](const Strip& t, int it) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t.tokens > 0) next[i] = a.perm[t.start + min(it * 64 + 4 * quad + i, t.tokens - 1)];
+    };
+    Strip t = strip_of(blockIdx.x);
+    rows_of(t, 0);
+    bool waited = false;
+    int at = 0;   // steps so far
+    for (int64_t i = blockIdx.x; i < strips; i += step) {
+      const Strip after = strip_of(i + step);
+      const GradSide& d = a.side[t.second];
+      const int n = (t.tokens + 63) / 64, c0 = static_cast<int>(t.c0);
+      if (d.wait && !waited) {
+        grid_dependency_wait();
+        waited = true;
+      }
+      for (int it = 0; it < n; ++it, ++at) {
+        const int s = at % kStages;
+        uint8_t *xs = stages + s * stage_bytes, *us = xs + 2 * 64 * kRowBytes;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) rows[k] = next[k];
+        if (it + 1 < n) rows_of(t, it + 1);
+        else rows_of(after, 0);
+        const int row0 = __shfl_sync(0xffffffffu, rows[0], 0);
+        const bool box = __all_sync(0xffffffffu, rows[0] == row0 + 4 * quad && rows[3] == rows[0] + 3);   // ascending
+        if (at >= kStages) mbar_wait(&y.done[s], (at / kStages - 1) & 1, &y.abort, a.st, 23);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&y.full[s], stage_bytes);
+          for (int k = 0; k < 2; ++k) {
+            uint8_t* u = us + k * grad_mid_bytes(r16);
+            tma_load_2d(u, &d.tmU, 0, k * a.M + t.start + it * 64, &y.full[s]);
+            if (r16 > 64) tma_load_2d(u + 64 * kRowBytes, &d.tmU, 64, k * a.M + t.start + it * 64, &y.full[s]);
+          }
+          if (box) {
+            tma_load_2d(xs, &d.tmX, c0, row0, &y.full[s]);
+            tma_load_2d(xs + 64 * kRowBytes, &d.tmX, c0 + 64, row0, &y.full[s]);
+          }
+        }
+        __syncwarp();   // the stage is armed before its gathers arrive
+        if (!box) tma_gather4(xs + (half * 64 + quad * 4) * kRowBytes, &d.tmX1, c0 + 64 * half, rows, &y.full[s]);
+      }
+      if (n == 0) rows_of(after, 0);
+      t = after;
+    }
+  } else if (warp == 5) {
+    const uint32_t idesc = instruction(r16, true, true, a.bf16);
+    int at = 0, acc = 0;   // steps and strips with tokens so far
+    Strip t = strip_of(blockIdx.x);
+    for (int64_t i = blockIdx.x; i < strips; i += step) {
+      const Strip after = strip_of(i + step);
+      const int n = (t.tokens + 63) / 64;
+      if (n > 0 && acc >= 2) {
+        mbar_wait(&y.acc_free[acc & 1], ((acc >> 1) - 1) & 1, &y.abort, a.st, 33);
+        tc_fence_after();
+      }
+      for (int it = 0; it < n; ++it, ++at) {
+        const int s = at % kStages;
+        mbar_wait(&y.full[s], (at / kStages) & 1, &y.abort, a.st, 26);
+        uint8_t* us = stages + s * stage_bytes + 2 * 64 * kRowBytes;
+        const int left = t.tokens - it * 64;
+        if (left < 64) {
+          for (int j = left * 8 + lane; j < 64 * 8; j += 32)
+            for (int k = 0; k < 2 * grad_mid_bytes(r16); k += 64 * kRowBytes)
+              st_shared_v4(us + k + j * 16, make_uint4(0, 0, 0, 0));
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t x0 = smem_u32(us) - 2 * 64 * kRowBytes, u0 = smem_u32(us);
+          const uint32_t out = y.tmem + (acc & 1) * columns;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t x = desc_mn(x0, k, 64 * kRowBytes);
+            umma_f16(out, x, desc_mn(u0, k, 64 * kRowBytes), idesc, it > 0 || k > 0 ? 1u : 0u);
+            umma_f16(out, x, desc_mn(u0 + grad_mid_bytes(r16), k, 64 * kRowBytes), idesc, 1u);
+          }
+          umma_commit(&y.done[s]);
+          if (it == n - 1) umma_commit(&y.acc_full[acc & 1]);
+        }
+        __syncwarp();
+      }
+      if (n > 0) ++acc;
+      t = after;
+    }
+  } else if (warp < 4) {
+    int acc = 0;
+    Strip t = strip_of(blockIdx.x);
+    for (int64_t i = blockIdx.x; i < strips; i += step) {
+      const Strip after = strip_of(i + step);
+      const GradSide& d = a.side[t.second];
+      const int64_t C = d.C, c = t.c0 + tid;
+      uint16_t* grad = d.grad + t.e * R * C;
+      const float scale = d.scale != nullptr ? d.scale[t.e] : 1.f;
+      if (t.tokens > 0) {
+        mbar_wait(&y.acc_full[acc & 1], (acc >> 1) & 1, &y.abort, a.st, 24);
+        __syncwarp();
+        tc_fence_after();
+      }
+      for (int j = 0; j < r16; j += 16) {
+        uint32_t v[16];
+        __syncwarp();
+        if (t.tokens > 0) {
+          tmem_ld16(y.tmem + (static_cast<uint32_t>(warp * 32) << 16) + (acc & 1) * columns + j, v);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = 0u;
+        }
+        if (c >= C) continue;
+        if (d.rank_major) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (j + k < R) grad[(j + k) * C + c] = to_16(scale * __uint_as_float(v[k]), a.bf16);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = to_16(scale * __uint_as_float(v[8 * q + 2 * k]), a.bf16) |
+                     static_cast<uint32_t>(to_16(scale * __uint_as_float(v[8 * q + 2 * k + 1]), a.bf16)) << 16;
+            if (j + 8 * q < R) *reinterpret_cast<uint4*>(grad + c * R + j + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (t.tokens > 0) {
+        __syncwarp();
+        tc_fence_before();
+        mbar_arrive(&y.acc_free[acc & 1]);
+        ++acc;
+      }
+      t = after;
+    }
+  }
+  __syncwarp();
+  grid_dependents_launch();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(y.tmem, 2 * columns);
+  // what follows this kernel may rely on what came before it
+  grid_dependency_wait();
+}
+
 // ---- few tokens: t and y in one launch --------------------------------------
 
 struct FewArgs {
@@ -1499,6 +1705,11 @@ cudaError_t grads(const Problem& p, const void* g, const void* t, void* gB, cons
   a.ranks = split(tiles, ceil_div(ceil_div(p.M, p.E), 64));
   if (tiles > INT32_MAX / a.ranks) return cudaErrorInvalidValue;
   const int stages = r16 > 64 ? 2 : 3;
+  if (tma && a.ranks == 1) {
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(tiles, 2 * sm_count())));
+    return launch(stages == 3 ? grad_many_kernel<3> : grad_many_kernel<2>, a, grid, kManyThreads, 1,
+                  1024 + stages * grad_stage_bytes(r16), K_ADAPTERS_GRAD, after, p.s);
+  }
   const int smem = 1024 + std::max(stages * grad_stage_bytes(r16), 128 * red_pitch(r16) * 4);
   const dim3 grid(static_cast<unsigned>(tiles * a.ranks));
   auto kernel = tma ? (stages == 3 ? grad_kernel<3, true> : grad_kernel<2, true>)

@@ -142,6 +142,21 @@ def test_long_batches(M, K, N, r, E, order, dt):
     _check(_run(d), _reference(d), dt)
 
 
+# more strips of 128 columns than CTAs: adapters without tokens among others
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("M,K,N,r,E,order", [(1500, 2056, 4104, 64, 24, "runs"), (900, 4104, 1032, 128, 40, "mixed"),
+                                             (2000, 1544, 2048, 8, 70, "runs"), (300, 520, 4360, 24, 200, "one")])
+def test_many_strips(M, K, N, r, E, order, dt):
+    d = _data(M, K, N, r, E, dt, order, seed=M + N)
+    got, want = _run(d), _reference(d)
+    _check(got, want, dt)
+    _, t = I.adapters_forward(d["x"], d["A"], d["B"], d["scale"], I.adapter_plan(d["index"], E))
+    for need in ("gA", "gB"):               # one gradient alone: the same bits
+        some = I.adapters_backward(d["g"], d["x"], t, d["A"], d["B"], d["scale"], I.adapter_plan(d["index"], E),
+                                   need_x=False, need_A=need == "gA", need_B=need == "gB")
+        assert torch.equal(some[1 if need == "gA" else 2], got[need])
+
+
 @pytest.mark.parametrize("M", [40, 700])
 def test_absent_base_addend_and_scale(M):
     d = _data(M, 512, 384, 16, 3, BF16, "mixed", 4)
