@@ -261,29 +261,92 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
-// Copies 8 elements to the 16 bytes at `dst`, of which the first `valid`
-// exist (the others are zeros; valid <= 0: none, `row` is then not read).
-// `width`: the bytes that every row start and row length is a multiple of.
-__device__ __forceinline__ void load_chunk(uint32_t dst, const uint16_t* row, int64_t at, int64_t valid, int width) {
-  const uint16_t* src = row + (valid > 0 ? at : 0);
-  if (width == 16) {
-    cp_async<16>(dst, src, valid > 0);
-  } else if (width == 8) {
+// The 16 bytes that start `shift` (0, 2 .. 14) bytes into lo, hi.
+__device__ __forceinline__ uint4 realign(uint4 lo, uint4 hi, int shift) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) cp_async<8>(dst + 8 * i, valid > 4 * i ? src + 4 * i : src, valid > 4 * i);
-  } else if (width == 4) {
+  for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) cp_async<4>(dst + 4 * i, valid > 2 * i ? src + 2 * i : src, valid > 2 * i);
-  } else {
-    uint32_t w[4];
+  for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = valid > 2 * i ? src[2 * i] : 0, hi = valid > 2 * i + 1 ? src[2 * i + 1] : 0;
-      w[i] = lo | (hi << 16);
-    }
+  for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (shift & 2) * 8);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 8 elements at any address, of which the first `valid` exist: the aligned 16
+// bytes that hold the first one and, where they reach into them, the next 16.
+struct Unaligned {
+  uint4 lo, hi;
+  __device__ __forceinline__ void fetch(const uint16_t* src, int64_t valid) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(src);
+    const uint4* q = reinterpret_cast<const uint4*>(p & ~static_cast<uintptr_t>(15));
+    lo = hi = make_uint4(0, 0, 0, 0);
+    if (valid > 0) lo = q[0];
+    if (static_cast<int>(p & 15) + 2 * min(valid, static_cast<int64_t>(8)) > 16) hi = q[1];
+  }
+  __device__ __forceinline__ void put(uint32_t dst, const uint16_t* src, int64_t valid) const {
+    const uint4 v = realign(lo, hi, static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15));
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (valid < 8)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] &= valid > 2 * i + 1 ? 0xffffffffu : valid > 2 * i ? 0xffffu : 0u;
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                  : "memory");
   }
+};
+
+// How operands reach shared memory: tiles by TMA, or chunks of 8 elements by
+// asynchronous copies of `width` bytes, which every row start and row length
+// is a multiple of, or, where that is 2, as aligned 16 bytes that go through
+// registers (8192 tokens, 4097 -> 5001, rank 64, take 380 us forward and
+// backward so and 642 us by single elements).
+enum Copy { kByTma, kByAsync, kByRegisters };
+
+// 8 elements for the 16 bytes at `dst`, of which the first `valid` exist (the
+// others are zeros; valid <= 0: none, `row` is then not read).
+struct Chunk {
+  uint32_t dst;
+  const uint16_t* row;
+  int64_t at, valid;
+};
+// n chunks, those that chunk(i) gives; through registers they are fetched
+// together, before the first is stored.
+template <Copy kCopy, int n, typename F>
+__device__ __forceinline__ void load_chunks(int width, F chunk) {
+  if constexpr (kCopy == kByRegisters) {
+    Unaligned u[n];
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const Chunk c = chunk(i);
+      u[i].fetch(c.row + (c.valid > 0 ? c.at : 0), c.valid);
+    }
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const Chunk c = chunk(i);
+      u[i].put(c.dst, c.row + (c.valid > 0 ? c.at : 0), c.valid);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const Chunk c = chunk(i);
+      const uint16_t* src = c.row + (c.valid > 0 ? c.at : 0);
+      if (width == 16) {
+        cp_async<16>(c.dst, src, c.valid > 0);
+      } else if (width == 8) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) cp_async<8>(c.dst + 8 * k, c.valid > 4 * k ? src + 4 * k : src, c.valid > 4 * k);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) cp_async<4>(c.dst + 4 * k, c.valid > 2 * k ? src + 2 * k : src, c.valid > 2 * k);
+      }
+    }
+  }
+}
+// One of a second operand, whose width may be another one.
+template <Copy kCopy>
+__device__ __forceinline__ void load_chunk(int width, const Chunk& c) {
+  if (kCopy == kByRegisters && width == 2) load_chunks<kByRegisters, 1>(width, [&](int) { return c; });
+  else load_chunks<kByAsync, 1>(width, [&](int) { return c; });
 }
 
 // Byte offset of 16-byte chunk `c` (0-7) of row `i` in a swizzled tile.
@@ -423,8 +486,9 @@ __host__ __device__ constexpr int shrink_stage_bytes(int r16, bool mn) {
 // One cluster per tile of 128 tokens; its CTAs split the reduction, each
 // accumulating in TMEM, and add up in the order of their ranks.  Bound by
 // reading X once.
-template <bool kMN, int kStages, bool kTma>
+template <bool kMN, int kStages, Copy kCopy>
 __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_constant__ ShrinkArgs a) {
+  constexpr bool kTma = kCopy == kByTma;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Sync y;
   const int ranks = a.ranks, rank = blockIdx.x % ranks;
@@ -501,25 +565,26 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = (tid >> 3) + 32 * i;
-      xrow[i] = row < t.count ? a.X + static_cast<int64_t>(a.perm[t.start + row]) * C : nullptr;
+      xrow[i] = row < t.count ? a.X + static_cast<int64_t>(a.perm[t.start + row]) * C : a.X;
     }
     auto load = [&](int b, int s) {
       const int64_t c0 = column(b);
       const uint32_t xs = base + s * stage_bytes, ws = xs + 128 * kRowBytes;
       const int64_t at = c0 + (tid & 7) * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)   // rows past the tile's tokens are not read: their products go nowhere
-        if (xrow[i] != nullptr) load_chunk(xs + swizzled((tid >> 3) + 32 * i, tid & 7), xrow[i], at, C - at, a.cw);
+      load_chunks<kCopy, 4>(a.cw, [&](int i) {   // of rows past the tile's tokens nothing is read
+        const int row = (tid >> 3) + 32 * i;
+        return Chunk{xs + swizzled(row, tid & 7), xrow[i], at, row < t.count ? C - at : 0};
+      });
       if constexpr (kMN) {
         const int chunks = r16 / 8;
         for (int i = tid; i < 64 * chunks; i += kThreads) {
           const int k = i / chunks, c = i % chunks;
-          load_chunk(ws + (c >> 3) * 64 * kRowBytes + swizzled(k, c & 7), W + min(c0 + k, C - 1) * R, c * 8,
-                     c0 + k < C ? R - c * 8 : 0, a.rw);
+          load_chunk<kCopy>(a.rw, Chunk{ws + (c >> 3) * 64 * kRowBytes + swizzled(k, c & 7),
+                                        W + min(c0 + k, C - 1) * R, c * 8, c0 + k < C ? R - c * 8 : 0});
         }
       } else {
         for (int j = tid >> 3; j < r16; j += kThreads / 8)
-          load_chunk(ws + swizzled(j, tid & 7), W + min(j, R - 1) * C, at, j < R ? C - at : 0, a.cw);
+          load_chunk<kCopy>(a.cw, Chunk{ws + swizzled(j, tid & 7), W + min(j, R - 1) * C, at, j < R ? C - at : 0});
       }
     };
 
@@ -619,8 +684,9 @@ struct ExpandSync {
 // turn the accumulators into output, thread 256 fetches, thread 288 issues
 // the products.  Bound by reading the addend and writing out.
 constexpr int kExpandThreads = 320;
-template <bool kMN, bool kTma>
+template <bool kMN, Copy kCopy>
 __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_constant__ ExpandArgs a) {
+  constexpr bool kTma = kCopy == kByTma;
   extern __shared__ uint8_t smem_raw[];
   __shared__ ExpandSync y;
   if (kTma && threadIdx.x == 256) {
@@ -722,6 +788,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
   // The addend's rows of tile j, and rows of a finished tile: a thread has
   // chunk tid % 8 of rows tid / 8 + 32 i in both, so that it may fetch into
   // what it has stored.
+  const int cw = kTma ? 16 : a.cw;
   int token[4] = {-1, -1, -1, -1};
   if (!tma_out && warp < 8)
 #pragma unroll
@@ -731,27 +798,43 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
     if (a.addend == nullptr || j >= n) return;
     const uint32_t buf = smem_u32(tiles) + (j % bufs) * kTileBytes;
     const int64_t at = static_cast<int64_t>(j0 + j) * kCols + (tid & 7) * 8;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (token[i] >= 0)
-        load_chunk(buf + swizzled((tid >> 3) + 32 * i, tid & 7), a.addend + static_cast<int64_t>(token[i]) * C, at,
-                   C - at, a.cw);
+    load_chunks<kCopy, 4>(cw, [&](int i) {
+      return Chunk{buf + swizzled((tid >> 3) + 32 * i, tid & 7), a.addend + static_cast<int64_t>(max(token[i], 0)) * C,
+                   at, token[i] >= 0 ? C - at : 0};
+    });
   };
   auto store_rows = [&](int j, const uint8_t* buf) {
     const int64_t at = static_cast<int64_t>(j0 + j) * kCols + (tid & 7) * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (token[i] < 0 || at >= C) continue;
-      const uint4 w = ld_shared_v4(buf + swizzled((tid >> 3) + 32 * i, tid & 7));
+      const int row = (tid >> 3) + 32 * i, q = tid & 7;
+      const uint4 w = ld_shared_v4(buf + swizzled(row, q));
       uint16_t* o = a.out + static_cast<int64_t>(token[i]) * C + at;
-      if (a.cw == 16) {
+      if (cw == 16) {
         *reinterpret_cast<uint4*>(o) = w;
-      } else {
-        const uint32_t* e = reinterpret_cast<const uint32_t*>(&w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < C - at) o[k] = static_cast<uint16_t>(e[k >> 1] >> (16 * (k & 1)));
+        continue;
       }
+      const int s = static_cast<int>(reinterpret_cast<uintptr_t>(o) & 15) / 2;
+      if (s == 0 && C - at >= 8) {
+        *reinterpret_cast<uint4*>(o) = w;
+        continue;
+      }
+      // the aligned 16 bytes that hold this chunk's first element: its first
+      // 8 - s elements after the last s of the chunk before
+      const bool whole = q > 0 && C - at >= 8 - s;
+      if (whole) {
+        const uint4 before = ld_shared_v4(buf + swizzled(row, q - 1));
+        *reinterpret_cast<uint4*>(o - s) = realign(before, w, 16 - 2 * s);
+      }
+      // what no whole 16 bytes of this tile hold
+      const int from = whole ? 8 - s : 0, to = static_cast<int>(min(C - at, static_cast<int64_t>(8)));
+      const bool next = q < 7 && C - at >= 16 - s;   // the next chunk's thread stores the rest
+      const int end = next ? min(to, 8 - s) : to;
+      const uint32_t* e = reinterpret_cast<const uint32_t*>(&w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k >= from && k < end) o[k] = static_cast<uint16_t>(e[k >> 1] >> (16 * (k & 1)));
     }
   };
 
@@ -850,35 +933,43 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
       if constexpr (kMN) {
         for (int i = tid; i < r16 * 8; i += kThreads) {
           const int k = i >> 3, c = i & 7;
-          load_chunk(ws + swizzled(k, c), W + min(k, R - 1) * C, c0 + c * 8, k < R ? C - (c0 + c * 8) : 0, a.cw);
+          load_chunk<kCopy>(a.cw, Chunk{ws + swizzled(k, c), W + min(k, R - 1) * C, c0 + c * 8,
+                                        k < R ? C - (c0 + c * 8) : 0});
         }
       } else {
         for (int i = tid; i < 64 * chunks; i += kThreads) {
           const int row = i / chunks, c = i % chunks;
-          load_chunk(ws + (c >> 3) * 64 * kRowBytes + swizzled(row, c & 7), W + min(c0 + row, C - 1) * R, c * 8,
-                     c0 + row < C ? R - c * 8 : 0, a.rw);
+          load_chunk<kCopy>(a.rw, Chunk{ws + (c >> 3) * 64 * kRowBytes + swizzled(row, c & 7),
+                                        W + min(c0 + row, C - 1) * R, c * 8, c0 + row < C ? R - c * 8 : 0});
         }
       }
     };
     if (adapter)
       for (int i = tid; i < t.count * chunks; i += kThreads) {
         const int row = i / chunks, c = i % chunks;
-        load_chunk(smem_u32(mids) + (c >> 3) * 128 * kRowBytes + swizzled(row, c & 7),
-                   a.mid + static_cast<int64_t>(t.start + row) * R, c * 8, R - c * 8, a.rw);
+        load_chunk<kCopy>(a.rw, Chunk{smem_u32(mids) + (c >> 3) * 128 * kRowBytes + swizzled(row, c & 7),
+                                      a.mid + static_cast<int64_t>(t.start + row) * R, c * 8, R - c * 8});
       }
-    load_w(0);
-    load_addend(0);
-    cp_async_commit();
-    for (int j = 0; j < n; ++j) {
-      // buffers of tile j + 1: w of tile j - 1 was read by products that tile
-      // j - 1's outputs waited for, its addend buffer left before the barrier
-      // that ended tile j + 1 - bufs
-      if (j + 1 < n) {
-        load_w(j + 1);
-        load_addend(j + 1);
+    // Buffers of tile j + 1: w of tile j - 1 was read by products that tile
+    // j - 1's outputs waited for, its addend buffer left before the barrier
+    // that ended tile j + 1 - bufs.  Copies that go through registers are
+    // waited for while the tile's products run.
+    constexpr bool ahead = kCopy == kByAsync;
+    auto fetch = [&](int j) {
+      if (j < n) {
+        load_w(j);
+        load_addend(j);
       }
       cp_async_commit();
-      cp_async_wait<1>();
+    };
+    fetch(0);
+    for (int j = 0; j < n; ++j) {
+      if (ahead) {
+        fetch(j + 1);
+        cp_async_wait<1>();
+      } else {
+        cp_async_wait<0>();
+      }
       fence_proxy_async_smem();
       tc_fence_before();
       named_bar_sync(1, 256);
@@ -886,6 +977,8 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
         tc_fence_after();
         multiply(j);
       }
+      __syncwarp();
+      if (!ahead) fetch(j + 1);
       uint8_t* buf = tiles + (j % bufs) * kTileBytes;
       finish(j, buf);
       named_bar_sync(1, 256);
@@ -932,8 +1025,9 @@ __host__ __device__ constexpr int grad_stage_bytes(int r16) { return 2 * 64 * kR
 // grad[c, j] = scale sum_m X[m, c] mid[m, j] over a group's tokens: one
 // cluster per (128 columns of X, group), its CTAs splitting the tokens.
 // Bound by reading X once.
-template <int kStages, bool kTma>
+template <int kStages, Copy kCopy>
 __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant__ GradArgs a) {
+  constexpr bool kTma = kCopy == kByTma;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Sync y;
   const int tid = threadIdx.x, ranks = a.ranks, rank = blockIdx.x % ranks, R = a.R, r16 = rank16(R);
@@ -1067,10 +1161,10 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
     auto load = [&](int b, int s) {   // of the rows that rows_of(b) found
       const uint32_t xs = base + s * stage_bytes, us = xs + 2 * 64 * kRowBytes;
       const int c = tid & 15;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        load_chunk(xs + (c >> 3) * 64 * kRowBytes + swizzled((tid >> 4) + 16 * i, c & 7),
-                   d.X + static_cast<int64_t>(max(xm[i], 0)) * C, c0 + c * 8, xm[i] >= 0 ? C - (c0 + c * 8) : 0, d.cw);
+      load_chunks<kCopy, 4>(d.cw, [&](int i) {
+        return Chunk{xs + (c >> 3) * 64 * kRowBytes + swizzled((tid >> 4) + 16 * i, c & 7),
+                     d.X + static_cast<int64_t>(max(xm[i], 0)) * C, c0 + c * 8, xm[i] >= 0 ? C - (c0 + c * 8) : 0};
+      });
 #pragma unroll
       for (int i = 0; i < kMidPer; ++i) {
         const int at = tid + i * kThreads;
@@ -1078,9 +1172,9 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
         const int k = at / chunks, q = at % chunks;
         const uint32_t dst = us + (q >> 3) * 64 * kRowBytes + swizzled(k, q & 7);
         const uint16_t* row = d.mid + static_cast<int64_t>(max(um[i], 0)) * R;
-        load_chunk(dst, row, q * 8, um[i] >= 0 ? R - q * 8 : 0, a.rw);
-        load_chunk(dst + grad_mid_bytes(r16), row + static_cast<int64_t>(a.M) * R, q * 8,
-                   um[i] >= 0 ? R - q * 8 : 0, a.mw);
+        const int64_t valid = um[i] >= 0 ? R - q * 8 : 0;
+        load_chunk<kCopy>(a.rw, Chunk{dst, row, q * 8, valid});
+        load_chunk<kCopy>(a.mw, Chunk{dst + grad_mid_bytes(r16), row + static_cast<int64_t>(a.M) * R, q * 8, valid});
       }
       rows_of(b + 1);
     };
@@ -1583,8 +1677,18 @@ constexpr CUtensorMapSwizzle kSwz = CU_TENSOR_MAP_SWIZZLE_128B;
 CUtensorMapDataType map_type(const Problem& p) {
   return p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
-// Rows of C and of R elements that start on 16 bytes: what tensor maps need.
-bool tma_rows(const Problem& p, int64_t C) { return C % 8 == 0 && p.R % 8 == 0; }
+// Tensor maps need rows of C and of R elements that start on 16 bytes.
+Copy copy_of(const Problem& p, int64_t C) {
+  return C % 8 == 0 && p.R % 8 == 0 ? kByTma : C % 2 == 0 && p.R % 2 == 0 ? kByAsync : kByRegisters;
+}
+template <bool kMN, Copy kCopy>
+auto shrink_of(int stages) {
+  return stages == 4 ? shrink_kernel<kMN, 4, kCopy> : shrink_kernel<kMN, 3, kCopy>;
+}
+template <Copy kCopy>
+auto grad_of(int stages) {
+  return stages == 3 ? grad_kernel<3, kCopy> : grad_kernel<2, kCopy>;
+}
 
 cudaError_t shrink(const Problem& p, const void* X, int64_t C, const void* W, bool mn, const float* scale,
                    void* mid) {
@@ -1608,17 +1712,17 @@ cudaError_t shrink(const Problem& p, const void* X, int64_t C, const void* W, bo
   const int stages = r16 > 64 ? 3 : 4;
   const int smem = 1024 + std::max(stages * shrink_stage_bytes(r16, mn), 128 * red_pitch(r16) * 4);
   const dim3 grid(static_cast<unsigned>(ranks * p.plan.slots));
-  const bool tma = tma_rows(p, C);
-  if (tma && (!make_tmap(&a.tmX, map_type(p), X, C, p.M, C * 2, 64, 128, kSwz) ||
+  const Copy copy = copy_of(p, C);
+  if (copy == kByTma && (!make_tmap(&a.tmX, map_type(p), X, C, p.M, C * 2, 64, 128, kSwz) ||
               !make_tmap(&a.tmX1, map_type(p), X, C, p.M, C * 2, 64, 1, kSwz) ||
               !(mn ? make_tmap_3d(&a.tmW, map_type(p), W, p.R, C, p.E, 2, 64, 64, kSwz)
                    : make_tmap_3d(&a.tmW, map_type(p), W, C, p.R, p.E, 2, 64, r16, kSwz))))
     return cudaErrorUnknown;
-  auto k4 = tma ? (mn ? shrink_kernel<true, 4, true> : shrink_kernel<false, 4, true>)
-                : (mn ? shrink_kernel<true, 4, false> : shrink_kernel<false, 4, false>);
-  auto k3 = tma ? (mn ? shrink_kernel<true, 3, true> : shrink_kernel<false, 3, true>)
-                : (mn ? shrink_kernel<true, 3, false> : shrink_kernel<false, 3, false>);
-  return launch(stages == 4 ? k4 : k3, a, grid, kThreads, ranks, smem, K_ADAPTERS, true, p.s);
+  auto kernel = copy == kByTma     ? (mn ? shrink_of<true, kByTma>(stages) : shrink_of<false, kByTma>(stages))
+                : copy == kByAsync ? (mn ? shrink_of<true, kByAsync>(stages) : shrink_of<false, kByAsync>(stages))
+                : mn               ? shrink_of<true, kByRegisters>(stages)
+                                   : shrink_of<false, kByRegisters>(stages);
+  return launch(kernel, a, grid, kThreads, ranks, smem, K_ADAPTERS, true, p.s);
 }
 
 cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, bool mn, const float* scale,
@@ -1649,15 +1753,16 @@ cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, 
   const int smem = 1024 + expand_mid_bytes(r16) + 2 * expand_w_bytes(r16) +
                    expand_tiles(r16) * static_cast<int>(kTileBytes);
   const dim3 grid(static_cast<unsigned>(p.plan.slots), static_cast<unsigned>(ceil_div(col_tiles, a.col_tiles)));
-  const bool tma = tma_rows(p, C);
-  if (tma && (!make_tmap(&a.tmMid, map_type(p), mid, p.R, p.M, p.R * 2, 64, 128, kSwz) ||
+  const Copy copy = copy_of(p, C);
+  if (copy == kByTma && (!make_tmap(&a.tmMid, map_type(p), mid, p.R, p.M, p.R * 2, 64, 128, kSwz) ||
               !make_tmap(&a.tmAdd, map_type(p), addend != nullptr ? addend : out, C, p.M, C * 2, 64, 128, kSwz) ||
               !make_tmap(&a.tmOut, map_type(p), out, C, p.M, C * 2, 64, 128, kSwz) ||
               !(mn ? make_tmap_3d(&a.tmW, map_type(p), W, C, p.R, p.E, 2, 64, r16, kSwz)
                    : make_tmap_3d(&a.tmW, map_type(p), W, p.R, C, p.E, 2, 64, 64, kSwz))))
     return cudaErrorUnknown;
-  auto kernel = tma ? (mn ? expand_kernel<true, true> : expand_kernel<false, true>)
-                    : (mn ? expand_kernel<true, false> : expand_kernel<false, false>);
+  auto kernel = copy == kByTma     ? (mn ? expand_kernel<true, kByTma> : expand_kernel<false, kByTma>)
+                : copy == kByAsync ? (mn ? expand_kernel<true, kByAsync> : expand_kernel<false, kByAsync>)
+                                   : (mn ? expand_kernel<true, kByRegisters> : expand_kernel<false, kByRegisters>);
   return launch(kernel, a, grid, kExpandThreads, 1, smem, K_ADAPTERS, true, p.s);
 }
 
@@ -1687,7 +1792,10 @@ bool grad_side(const Problem& p, const void* mid, const void* X, int64_t C, bool
 cudaError_t grads(const Problem& p, const void* g, const void* t, void* gB, const void* x, const void* u, void* gA,
                   bool after) {
   GradArgs a;
-  const bool tma = tma_rows(p, gB != nullptr ? p.N : 8) && tma_rows(p, gA != nullptr ? p.K : 8);
+  a.rw = copy_width(p.R);
+  a.mw = std::min(copy_width(p.R), copy_width(p.M * p.R));
+  const Copy copy = std::max(copy_of(p, gB != nullptr ? p.N : 8), copy_of(p, gA != nullptr ? p.K : 8));
+  const bool tma = copy == kByTma;
   if (!grad_side(p, t, g, p.N, false, p.scale, gB, false, tma, &a.side[0]) ||
       !grad_side(p, u, x, p.K, true, nullptr, gA, true, tma, &a.side[1]))
     return cudaErrorUnknown;
@@ -1696,8 +1804,6 @@ cudaError_t grads(const Problem& p, const void* g, const void* t, void* gB, cons
   a.st = p.st;
   a.M = static_cast<int>(p.M);
   a.R = p.R;
-  a.rw = copy_width(p.R);
-  a.mw = std::min(copy_width(p.R), copy_width(p.M * p.R));
   a.bf16 = p.bf16;
   a.first = !after;
   const int r16 = rank16(p.R);
@@ -1712,8 +1818,9 @@ cudaError_t grads(const Problem& p, const void* g, const void* t, void* gB, cons
   }
   const int smem = 1024 + std::max(stages * grad_stage_bytes(r16), 128 * red_pitch(r16) * 4);
   const dim3 grid(static_cast<unsigned>(tiles * a.ranks));
-  auto kernel = tma ? (stages == 3 ? grad_kernel<3, true> : grad_kernel<2, true>)
-                    : (stages == 3 ? grad_kernel<3, false> : grad_kernel<2, false>);
+  auto kernel = tma                ? grad_of<kByTma>(stages)
+                : copy == kByAsync ? grad_of<kByAsync>(stages)
+                                   : grad_of<kByRegisters>(stages);
   return launch(kernel, a, grid, kThreads, a.ranks, smem, K_ADAPTERS_GRAD, after, p.s);
 }
 
