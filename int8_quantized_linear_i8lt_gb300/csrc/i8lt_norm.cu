@@ -142,8 +142,13 @@ __device__ __forceinline__ float row_sum(float v, float* scratch) {
 // or over the same slice of rows, in turn; bulk copies bring the next rows
 // into a ring of shared-memory stages while this row is worked on, so that
 // the bytes in flight do not depend on how many rows a block's registers
-// hold.  Rows that do not start on 16 bytes are copied from the boundary below
-// them and read element by element.
+// hold.
+// Rows of a length that is no multiple of 16 bytes are worked on in the same
+// packs, counted from the boundary below the row's start ("shifted": x, g, y
+// and gx lie alike): with a row step that is a multiple of W, all rows of a
+// block start equally far behind a boundary, so that a thread keeps its
+// columns.  16384 x 5001 bf16 takes 93 us forward and 121 us backward so, and
+// 167 and 191 us element by element.
 constexpr int kMaxStages = 8;
 constexpr int kRingBytes = 200 * 1024;   // shared memory per SM given to the rings
 
@@ -161,11 +166,11 @@ struct Ring {
   RingLayout L;
   int64_t N, n0, step, rows;
   unsigned long long end;   // bytes of a matrix
-  int cols;
+  int cols, shift;          // shift: elements from the boundary to a row
 
   __device__ __forceinline__ int64_t row(int64_t i) const { return blockIdx.x + i * step; }
   __device__ __forceinline__ unsigned long long start(int64_t i) const {
-    return static_cast<unsigned long long>((row(i) * N + n0) * static_cast<int64_t>(sizeof(T)));
+    return static_cast<unsigned long long>((row(i) * N - shift + n0) * static_cast<int64_t>(sizeof(T)));
   }
   // the end of the copy of a slice that starts at byte b: the boundary above
   // its end, or the last one inside the matrix
@@ -217,6 +222,56 @@ __device__ __forceinline__ void zero_tails(const Ring<T, kMats>& r, int threads)
   const int tail = (r.L.slot_bytes - r.cols * static_cast<int>(sizeof(T))) / 16;
   for (int i = threadIdx.x; i < tail * static_cast<int>(r.L.stages) * kMats; i += threads)
     *reinterpret_cast<uint4*>(r.base + (i / tail + 1) * r.L.slot_bytes - (i % tail + 1) * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// A shifted row: its first element's place in the first pack, its end, and
+// which packs reach over either.
+template <int W, bool kShift>
+struct Shift {
+  int first, end;   // the row's places, counted from the boundary
+  __device__ __forceinline__ Shift(int64_t row, int64_t N)
+      : first(kShift ? static_cast<int>(row * N % W) : 0), end(static_cast<int>(N) + first) {}
+  __device__ __forceinline__ bool edge(int c) const { return kShift && (c < W || c + W > end); }
+  __device__ __forceinline__ bool in(int c) const { return c >= first && c < end; }
+  __device__ __forceinline__ void clear(int c, float* f) const {   // what the pack at c holds of other rows
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+      if (!in(c + k)) f[k] = 0.f;
+  }
+  // the pack at place c of a parameter vector and of a row (o: its boundary)
+  __device__ __forceinline__ void param(const void* p, int dt, int c, float none, float* f) const {
+    if constexpr (!kShift) {
+      load_param<W>(p, dt, c, none, f);
+    } else {
+#pragma unroll
+      for (int k = 0; k < W; ++k) f[k] = p == nullptr ? none : in(c + k) ? load_any(p, dt, c + k - first) : 0.f;
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* o, int c, const float* f) const {
+    if (!edge(c)) {
+      store_floats<T, W>(o + c, f);
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+      if (in(c + k)) o[c + k] = from_float<T>(f[k]);
+  }
+};
+// The last elements of a matrix of shifted rows, which no copy of 16 bytes
+// covers, into the stage of its last row.  All threads of the block call it.
+template <typename T, int kMats>
+__device__ __forceinline__ void last_elements(const Ring<T, kMats>& r, int64_t i, int64_t M, int stage) {
+  const int left = static_cast<int>((r.end & 15) / sizeof(T));
+  if (left == 0 || r.row(i) != M - 1) return;
+  const unsigned long long b = r.start(i), at = r.end & ~15ull;
+  const int tid = threadIdx.x;
+  if (at >= b && at < b + static_cast<unsigned long long>(r.cols) * sizeof(T) && tid < left * kMats) {
+    const int k = tid / left, e = tid % left;
+    reinterpret_cast<T*>(r.base + (static_cast<size_t>(stage) * kMats + k) * r.L.slot_bytes + (at - b))[e] =
+        reinterpret_cast<const T*>(r.mat[k] + at)[e];
+  }
+  __syncthreads();
 }
 
 __device__ __forceinline__ void ring_setup(uint64_t* full, unsigned stages, int* abort_flag) {
@@ -290,19 +345,21 @@ __global__ void __launch_bounds__(kLanes > 32 ? kLanes : 256) norm_forward_row_k
   }
 }
 
-// Rows of up to 8192 elements: 32 elements, and their w and b, in each
-// thread's registers.
-template <typename T, int W, int kLanes, int kE>
+// Rows of up to 8192 elements (shifted: 16384): 32 elements, and their w and
+// b, in each thread's registers.
+template <typename T, int W, int kLanes, int kE, bool kShift>
 __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel(const ForwardArgs a,
                                                                                 const RingLayout L) {
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ uint64_t full[kMaxStages];
   __shared__ __align__(16) float scratch[2][kLanes / 32];
   __shared__ int abort_flag;
-  const int tid = threadIdx.x, N = static_cast<int>(a.N);
+  const int tid = threadIdx.x;
+  const Shift<W, kShift> shift(blockIdx.x, a.N);
+  const int end = shift.end;
   Ring<T, 1> ring{{static_cast<const uint8_t*>(a.x)}, stages, full, L, a.N, 0, gridDim.x,
                   (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
-                  static_cast<unsigned long long>(a.M) * a.N * sizeof(T), N};
+                  static_cast<unsigned long long>(a.M) * a.N * sizeof(T), end, shift.first};
   if (tid == 0) {
     ring_setup(full, L.stages, &abort_flag);
     for (int64_t i = 0; i < L.stages && i < ring.rows; ++i) ring.issue(i);
@@ -312,16 +369,17 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel
 #pragma unroll
   for (int i = 0; i < kE / W; ++i) {
     const int c = (tid + i * kLanes) * W;
-    if (c < N) {
-      load_param<W>(a.w, a.wt, c, 1.f, w + i * W);
-      load_param<W>(a.b, a.wt, c, 0.f, b + i * W);
+    if (c < end) {
+      shift.param(a.w, a.wt, c, 1.f, w + i * W);
+      shift.param(a.b, a.wt, c, 0.f, b + i * W);
     }
   }
-  const float inv_n = 1.0f / static_cast<float>(N);
+  const float inv_n = 1.0f / static_cast<float>(a.N);
   unsigned s = 0;
   uint32_t phase = 0;
   for (int64_t i = 0; i < ring.rows; ++i) {
     mbar_wait(&full[s], phase, &abort_flag, nullptr, 31);
+    if constexpr (kShift) last_elements(ring, i, a.M, s);
     const Slice<T> x = slice_of<T, W>(ring, 0, i, s);
     float t = 0.f;
 #pragma unroll
@@ -329,8 +387,9 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel
       const int c = (tid + e * kLanes) * W;
       // (a branch per pack, which keeps the loads apart: without it, on zeros
       // behind the row, 16384 x 8192 bf16 took 99 us instead of 90)
-      if (c < N) {
-        read<T, W>(x, c, N, v + e * W);
+      if (c < end) {
+        read<T, W>(x, c, end, v + e * W);
+        if (shift.edge(c)) shift.clear(c, v + e * W);
       } else {
 #pragma unroll
         for (int k = 0; k < W; ++k) v[e * W + k] = 0.f;
@@ -346,23 +405,25 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel
     }
     t = 0.f;
 #pragma unroll
-    for (int e = 0; e < kE / W; ++e)
-      if ((tid + e * kLanes) * W < N)
+    for (int e = 0; e < kE / W; ++e) {
+      const int c = (tid + e * kLanes) * W;
+      if (c >= end) continue;
 #pragma unroll
-        for (int k = 0; k < W; ++k) {
-          v[e * W + k] -= mu;
-          t += v[e * W + k] * v[e * W + k];
-        }
+      for (int k = 0; k < W; ++k) v[e * W + k] -= mu;
+      if (shift.edge(c)) shift.clear(c, v + e * W);
+#pragma unroll
+      for (int k = 0; k < W; ++k) t += v[e * W + k] * v[e * W + k];
+    }
     const float r = 1.0f / sqrtf(row_sum<kLanes>(t, scratch[1]) * inv_n + a.eps);
     const int64_t m = ring.row(i);
-    T* y = static_cast<T*>(a.y) + m * N;
+    T* y = static_cast<T*>(a.y) + m * a.N - shift.first;
 #pragma unroll
     for (int e = 0; e < kE / W; ++e) {
       const int c = (tid + e * kLanes) * W;
-      if (c >= N) continue;
+      if (c >= end) continue;
 #pragma unroll
       for (int k = 0; k < W; ++k) v[e * W + k] = fmaf(v[e * W + k] * r, w[e * W + k], b[e * W + k]);
-      store_floats<T, W>(y + c, v + e * W);
+      shift.store(y, c, v + e * W);
     }
     if (tid == 0) {
       if (a.mean != nullptr) a.mean[m] = mu;
@@ -382,7 +443,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_forward_wide_kernel(const F
   const int tid = threadIdx.x, N = static_cast<int>(a.N);
   Ring<T, 1> ring{{static_cast<const uint8_t*>(a.x)}, stages, full, L, a.N, 0, gridDim.x,
                   (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
-                  static_cast<unsigned long long>(a.M) * a.N * sizeof(T), N};
+                  static_cast<unsigned long long>(a.M) * a.N * sizeof(T), N, 0};
   if (tid == 0) {
     ring_setup(full, L.stages, &abort_flag);
     for (int64_t i = 0; i < L.stages && i < ring.rows; ++i) ring.issue(i);
@@ -489,28 +550,41 @@ cudaError_t launch_forward_row(const ForwardArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename T, int W, int kLanes, int kE>
+// Blocks (clusters) that take the rows in turn: of shifted rows each takes
+// one, or they are a multiple of the pack.
+int64_t row_blocks(int64_t M, int64_t most, int W, bool shifted) {
+  if (M <= std::max<int64_t>(most, W)) return M;
+  return shifted ? std::max<int64_t>(W, most / W * W) : most;
+}
+
+template <typename T, int W, int kLanes, int kE, bool kShift>
 cudaError_t launch_forward_ring(const ForwardArgs& a, cudaStream_t s) {
-  auto kernel = norm_forward_ring_kernel<T, W, kLanes, kE>;
+  auto kernel = norm_forward_ring_kernel<T, W, kLanes, kE, kShift>;
   constexpr int per_sm = 512 / kLanes;
-  const RingLayout L = ring_layout(a.N, round_up(a.N, 64), W > 1, sizeof(T), 1, per_sm);
+  const int64_t width = a.N + (kShift ? W - 1 : 0);
+  const RingLayout L = ring_layout(width, round_up(width, 64), true, sizeof(T), 1, per_sm);
   const int smem = static_cast<int>(L.stages) * L.slot_bytes;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
-  kernel<<<static_cast<unsigned>(std::min<int64_t>(a.M, sm_count() * per_sm)), kLanes, smem, s>>>(a, L);
+  kernel<<<static_cast<unsigned>(row_blocks(a.M, sm_count() * per_sm, W, kShift)), kLanes, smem, s>>>(a, L);
   return cudaGetLastError();
 }
 
-template <typename T, int W>
+// kW: elements in 16 bytes; kShift: rows are no multiple of that.
+template <typename T, int kW, bool kShift>
 cudaError_t forward_sized(const ForwardArgs& a, cudaStream_t s) {
+  constexpr int W = kShift ? 1 : kW;   // of the kernels without shifted packs
+  const int64_t width = a.N + (kShift ? kW - 1 : 0);
   if (a.N <= 64) return launch_forward_row<T, W, 8, 8>(a, s);
   if (a.N <= 256) return launch_forward_row<T, W, 32, 8>(a, s);
   if (a.N <= 512) return launch_forward_row<T, W, 32, 16>(a, s);
-  if (a.N <= 1024) return launch_forward_ring<T, W, 64, 16>(a, s);
-  if (a.N <= 2048) return launch_forward_ring<T, W, 64, 32>(a, s);
-  if (a.N <= 4096) return launch_forward_ring<T, W, 128, 32>(a, s);
-  if (a.N <= 8192) return launch_forward_ring<T, W, 256, 32>(a, s);
-  if constexpr (W > 1)
-    if (a.N <= 16384) return launch_forward_row<T, W, 512, 32>(a, s);
+  if (width <= 1024) return launch_forward_ring<T, kW, 64, 16, kShift>(a, s);
+  if (width <= 2048) return launch_forward_ring<T, kW, 64, 32, kShift>(a, s);
+  if (width <= 4096) return launch_forward_ring<T, kW, 128, 32, kShift>(a, s);
+  if (width <= 8192) return launch_forward_ring<T, kW, 256, 32, kShift>(a, s);
+  if (width <= 16384) {
+    if constexpr (kShift) return launch_forward_ring<T, kW, 512, 32, true>(a, s);
+    else return launch_forward_row<T, kW, 512, 32>(a, s);
+  }
   if (a.N * static_cast<int64_t>(sizeof(T)) <= kRingBytes / 2 - 256) {
     auto kernel = norm_forward_wide_kernel<T, W>;
     const RingLayout L = ring_layout(a.N, round_up(a.N, 64), W > 1, sizeof(T), 1, 1);
@@ -527,7 +601,7 @@ template <typename T>
 cudaError_t forward(const ForwardArgs& a, cudaStream_t s) {
   ProfScope ps(K_LAYER_NORM, s);
   constexpr int kW = 16 / sizeof(T);
-  return a.N % kW == 0 ? forward_sized<T, kW>(a, s) : forward_sized<T, 1>(a, s);
+  return a.N % kW == 0 ? forward_sized<T, kW, false>(a, s) : forward_sized<T, kW, true>(a, s);
 }
 
 // ---- backward --------------------------------------------------------------
@@ -665,7 +739,7 @@ __device__ __forceinline__ float warp_sums(float (&v)[kN]) {
 // Rows of up to 8192 elements through the ring, a block per row: 16 elements
 // in each thread's registers, with w and the gradient sums of their columns
 // over all the block's rows.
-template <typename T, int W, int kLanes, int kE>
+template <typename T, int W, int kLanes, int kE, bool kShift>
 __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kernel(const BackwardArgs a,
                                                                                  const RingLayout L) {
   extern __shared__ __align__(128) uint8_t stages[];
@@ -673,13 +747,15 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
   __shared__ uint64_t full[kMaxStages];
   __shared__ __align__(16) float2 scratch[2][kWarps];
   __shared__ int abort_flag;
-  const int tid = threadIdx.x, cols = L.cols;
+  const int tid = threadIdx.x;
+  const Shift<W, kShift> shift(blockIdx.x, a.N);
+  const int cols = shift.end;
   Ring<T, 2> ring{{static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.g)},
                   stages, full, L, a.N, 0, gridDim.x,
                   (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
-                  static_cast<unsigned long long>(a.M) * a.N * sizeof(T), cols};
+                  static_cast<unsigned long long>(a.M) * a.N * sizeof(T), cols, shift.first};
   const int rows = static_cast<int>(ring.rows);
-  if constexpr (W > 1) zero_tails(ring, kLanes);
+  zero_tails(ring, kLanes);
   if (tid == 0) {
     ring_setup(full, L.stages, &abort_flag);
     if (blockIdx.x == 0) *a.st = DevStatus{0, 0, 0, 0};
@@ -693,12 +769,12 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
     const int c = (tid + i * kLanes) * W;
 #pragma unroll
     for (int k = 0; k < W; ++k) w[i * W + k] = aw[i * W + k] = ab[i * W + k] = 0.f;
-    if (c < cols) load_param<W>(a.w, a.wt, c, 1.f, w + i * W);
+    if (c < cols) shift.param(a.w, a.wt, c, 1.f, w + i * W);
   }
   const float inv_n = 1.0f / static_cast<float>(a.N);
   const bool want_x = a.gx != nullptr;
   const float *mean = a.mean + blockIdx.x, *rstd = a.rstd + blockIdx.x;
-  T* out = static_cast<T*>(a.gx) + (want_x ? blockIdx.x * a.N : 0);
+  T* out = static_cast<T*>(a.gx) + (want_x ? blockIdx.x * a.N - shift.first : 0);
   float mu = mean[0], r = rstd[0];
   unsigned s = 0;
   uint32_t phase = 0;
@@ -712,25 +788,19 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
     }
     mbar_wait(&full[s], phase, &abort_flag, a.st, 30);
     float h[kE], g[kE], t0 = 0.f, t1 = 0.f;
-    Slice<T> xs, gs;
-    if constexpr (W == 1) {
-      xs = slice_of<T, W>(ring, 0, i, s);
-      gs = slice_of<T, W>(ring, 1, i, s);
-    } else {
-      xs.near = reinterpret_cast<const T*>(stages + 2 * s * L.slot_bytes);
-      gs.near = reinterpret_cast<const T*>(stages + (2 * s + 1) * L.slot_bytes);
-    }
+    if constexpr (kShift) last_elements(ring, i, a.M, s);
+    const T* xs = reinterpret_cast<const T*>(stages + 2 * s * L.slot_bytes);
+    const T* gs = reinterpret_cast<const T*>(stages + (2 * s + 1) * L.slot_bytes);
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
       const int c = (tid + e * kLanes) * W;
-      // Packs are read with the zeros behind their row: a branch per pack took
-      // 16384 x 8192 bf16 from 143 to 186 us. Single columns have more to skip:
-      // 8192 x 5001 bf16 takes 103 us with the branch and 130 us without.
-      if (W > 1 || c < cols) {
-        read<T, W>(xs, c, cols, h + e * W);
-        read<T, W>(gs, c, cols, g + e * W);
-      } else {
-        h[e] = g[e] = 0.f;
+      // with the zeros behind the row: a branch per pack took 16384 x 8192 bf16
+      // from 143 to 186 us
+      widen<T, W>(load_pack<T, W>(xs + c), h + e * W);
+      widen<T, W>(load_pack<T, W>(gs + c), g + e * W);
+      if (shift.edge(c)) {
+        shift.clear(c, h + e * W);
+        shift.clear(c, g + e * W);
       }
 #pragma unroll
       for (int k = e * W; k < (e + 1) * W; ++k) {
@@ -770,7 +840,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
       const int c = (tid + e * kLanes) * W;
 #pragma unroll
       for (int k = e * W; k < (e + 1) * W; ++k) g[k] = fmaf(h[k], c2, fmaf(g[k], cr, c1));
-      if (c < cols) store_floats<T, W>(out + c, g + e * W);
+      if (c < cols) shift.store(out, c, g + e * W);
     }
     out += gridDim.x * a.N;
   }
@@ -784,8 +854,9 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
     if (c >= cols) continue;
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-      pw[c + k] = aw[i * W + k];
-      pb[c + k] = ab[i * W + k];
+      if (kShift && !shift.in(c + k)) continue;
+      pw[c + k - shift.first] = aw[i * W + k];
+      pb[c + k - shift.first] = ab[i * W + k];
     }
   }
 }
@@ -795,7 +866,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
 // the rows' two sums and for gx, so that registers hold only w and the
 // gradient sums of the thread's columns.  The blocks send each other their
 // sums without waiting: gx follows one step later.
-template <typename T, int W, int kLanes, int kE, int kRows>
+template <typename T, int W, int kLanes, int kE, int kRows, bool kShift>
 __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_kernel(const BackwardArgs a,
                                                                                  const RingLayout L) {
   extern __shared__ __align__(128) uint8_t stages[];
@@ -807,13 +878,15 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ranks = static_cast<int>(gridDim.y), rank = static_cast<int>(blockIdx.y);
   const int64_t n0 = static_cast<int64_t>(rank) * L.cols;
-  const int cols = static_cast<int>(min(static_cast<int64_t>(L.cols), a.N - n0));
+  const Shift<W, kShift> shift(blockIdx.x, a.N);
+  const int first = static_cast<int>(n0);   // n0, like the slices, in places from the boundary
+  const int cols = min(L.cols, shift.end - first);
   Ring<T, 2> ring{{static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.g)},
                   stages, full, L, a.N, n0, gridDim.x,
                   (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
-                  static_cast<unsigned long long>(a.M) * a.N * sizeof(T), cols};
+                  static_cast<unsigned long long>(a.M) * a.N * sizeof(T), cols, shift.first};
   const int64_t rows = ring.rows, steps = (rows + kRows - 1) / kRows;
-  if constexpr (W > 1) zero_tails(ring, kLanes);
+  zero_tails(ring, kLanes);
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) mbar_init(&sent[i], 1);
     ring_setup(full, L.stages, &abort_flag);
@@ -829,8 +902,12 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
     const int c = (tid + i * kLanes) * W;
 #pragma unroll
     for (int k = 0; k < W; ++k) w[i * W + k] = aw[i * W + k] = ab[i * W + k] = 0.f;
-    if (c < cols) load_param<W>(a.w, a.wt, n0 + c, 1.f, w + i * W);
+    if (c < cols) shift.param(a.w, a.wt, first + c, 1.f, w + i * W);
   }
+  auto read_pack = [&](const T* slice, int c, float* f) {
+    widen<T, W>(load_pack<T, W>(slice + c), f);
+    if (c < cols && shift.edge(first + c)) shift.clear(first + c, f);
+  };
   const float inv_n = 1.0f / static_cast<float>(a.N);
   const bool want_x = a.gx != nullptr;
   const int lag = ranks > 1 && want_x ? 1 : 0;
@@ -844,14 +921,15 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
         if (row >= rows) continue;
         const int s = static_cast<int>(static_cast<unsigned>(row) % L.stages);
         mbar_wait(&full[s], static_cast<unsigned>(row) / L.stages & 1, &abort_flag, a.st, 30);
+        if constexpr (kShift) last_elements(ring, row, a.M, s);
         if (!want_x) continue;
         const float mu = __ldg(a.mean + ring.row(row)), r = __ldg(a.rstd + ring.row(row));
         const Slice<T> xs = slice_of<T, W>(ring, 0, row, s), gs = slice_of<T, W>(ring, 1, row, s);
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
           float x[W], g[W];
-          read<T, W>(xs, (tid + e * kLanes) * W, cols, x);
-          read<T, W>(gs, (tid + e * kLanes) * W, cols, g);
+          read_pack(xs.near, (tid + e * kLanes) * W, x);
+          read_pack(gs.near, (tid + e * kLanes) * W, g);
 #pragma unroll
           for (int k = 0; k < W; ++k) {
             g[k] *= w[e * W + k];
@@ -906,13 +984,13 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
       const float c1 = -r * inv_n * __shfl_sync(0xffffffffu, total, 2 * q * (32 / kSums));
       const float c2 = -r * inv_n * __shfl_sync(0xffffffffu, total, (2 * q + 1) * (32 / kSums));
       const Slice<T> xs = slice_of<T, W>(ring, 0, row, s), gs = slice_of<T, W>(ring, 1, row, s);
-      T* out = static_cast<T*>(a.gx) + ring.row(row) * a.N + n0;
+      T* out = static_cast<T*>(a.gx) + ring.row(row) * a.N - shift.first;
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         const int c = (tid + e * kLanes) * W;
         float x[W], g[W];
-        read<T, W>(xs, c, cols, x);
-        read<T, W>(gs, c, cols, g);
+        read_pack(xs.near, c, x);
+        read_pack(gs.near, c, g);
 #pragma unroll
         for (int k = 0; k < W; ++k) {
           x[k] = (x[k] - mu) * r;
@@ -920,13 +998,13 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
           ab[e * W + k] += g[k];
           g[k] = fmaf(x[k], c2, fmaf(g[k] * w[e * W + k], r, c1));
         }
-        if (want_x && c < cols) store_floats<T, W>(out + c, g);
+        if (want_x && c < cols) shift.store(out, first + c, g);
       }
     }
   }
   if (ranks > 1) cluster_sync();   // no block leaves while a peer may write to it
   if (a.partial == nullptr) return;
-  float* pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.N + n0;
+  float* pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.N;
   float* pb = pw + static_cast<int64_t>(gridDim.x) * a.N;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
@@ -934,8 +1012,10 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
     if (c >= cols) continue;
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-      pw[c + k] = aw[i * W + k];
-      pb[c + k] = ab[i * W + k];
+      const int n = first + c + k;
+      if (kShift && !shift.in(n)) continue;
+      pw[n - shift.first] = aw[i * W + k];
+      pb[n - shift.first] = ab[i * W + k];
     }
   }
 }
@@ -1031,15 +1111,15 @@ cudaError_t launch_short(Shape& h) {
   return cudaGetLastError();
 }
 
-template <typename T, int W, int kLanes, int kE>
+template <typename T, int W, int kLanes, int kE, bool kShift>
 cudaError_t launch_ring(Shape& h) {
   constexpr int per_sm = 512 / kLanes;
-  const RingLayout L = ring_layout(h.a.N, kLanes * kE, W > 1, sizeof(T), 2, per_sm);
-  auto kernel = norm_backward_ring_kernel<T, W, kLanes, kE>;
+  const RingLayout L = ring_layout(h.a.N, kLanes * kE, true, sizeof(T), 2, per_sm);
+  auto kernel = norm_backward_ring_kernel<T, W, kLanes, kE, kShift>;
   const int smem = static_cast<int>(L.stages) * 2 * L.slot_bytes;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
-  h.blocks = static_cast<int>(
-      std::min<int64_t>({h.a.M, static_cast<int64_t>(h.sms) * per_sm, partial_rows(h.a.M, h.a.N)}));
+  h.blocks = static_cast<int>(row_blocks(
+      h.a.M, std::min<int64_t>(static_cast<int64_t>(h.sms) * per_sm, partial_rows(h.a.M, h.a.N)), W, kShift));
   ProfScope ps(K_LAYER_NORM_BWD, h.s);
   kernel<<<h.blocks, kLanes, smem, h.s>>>(h.a, L);
   return cudaGetLastError();
@@ -1070,16 +1150,20 @@ int cached_clusters(const void* fn, int smem, int ranks, Query query) {
 
 // Two rows per step where the ring holds the rows of a step, of the one
 // before it and of the next.
-template <typename T, int W>
-cudaError_t launch_cluster(Shape& h, int ranks, int cols) {
-  const RingLayout L = ring_layout(cols, 512 * 16, W > 1, sizeof(T), 2, 1);
-  auto kernel = L.stages >= 6u ? norm_backward_cluster_kernel<T, W, 512, 16, 2>
-                               : norm_backward_cluster_kernel<T, W, 512, 16, 1>;
+template <typename T, int W, bool kShift, int kLanes>
+cudaError_t launch_cluster(Shape& h, int64_t width) {
+  constexpr int kE = 16, per_sm = 512 / kLanes;
+  const int64_t least = ceil_div(width, kLanes * kE);
+  const int64_t cols = round_up(ceil_div(width, least), 8);   // slices of whole packs
+  const int ranks = static_cast<int>(ceil_div(width, cols));
+  const RingLayout L = ring_layout(cols, kLanes * kE, true, sizeof(T), 2, per_sm);
+  auto kernel = L.stages >= 6u ? norm_backward_cluster_kernel<T, W, kLanes, kE, 2, kShift>
+                               : norm_backward_cluster_kernel<T, W, kLanes, kE, 1, kShift>;
   const int smem = static_cast<int>(L.stages) * 2 * L.slot_bytes;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1, static_cast<unsigned>(ranks));
-  cfg.blockDim = dim3(512);
+  cfg.blockDim = dim3(kLanes);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = h.s;
   cudaLaunchAttribute attr[1];
@@ -1095,34 +1179,33 @@ cudaError_t launch_cluster(Shape& h, int ranks, int cols) {
   const int resident = cached_clusters(reinterpret_cast<const void*>(kernel), smem, ranks, [&] {
     int n = 0;
     cudaLaunchConfig_t q = cfg;
-    q.gridDim.x = static_cast<unsigned>(std::max(1, h.sms / ranks));
+    q.gridDim.x = static_cast<unsigned>(std::max(1, h.sms * per_sm / ranks));
     return cudaOccupancyMaxActiveClusters(&n, kernel, &q) == cudaSuccess ? n : 0;
   });
-  h.blocks = static_cast<int>(
-      std::min<int64_t>({h.a.M, static_cast<int64_t>(std::max(1, std::min(resident, h.sms / ranks))),
-                         partial_rows(h.a.M, h.a.N)}));
+  h.blocks = static_cast<int>(row_blocks(
+      h.a.M, std::min<int64_t>(std::max(1, std::min(resident, h.sms * per_sm / ranks)), partial_rows(h.a.M, h.a.N)), W,
+      kShift));
   cfg.gridDim.x = static_cast<unsigned>(h.blocks);
   ProfScope ps(K_LAYER_NORM_BWD, h.s);
   return cudaLaunchKernelEx(&cfg, kernel, h.a, L);
 }
 
-template <typename T, int W>
+template <typename T, int kW, bool kShift>
 cudaError_t backward_sized(Shape& h) {
-  const int64_t N = h.a.N;
+  constexpr int W = kShift ? 1 : kW;
+  const int64_t N = h.a.N, width = N + (kShift ? kW - 1 : 0);
   if (N <= 64) return launch_short<T, W, 8>(h);
   if (N <= kShortRow) return launch_short<T, W, 32>(h);
-  if (N <= 512) return launch_ring<T, W, 64, 8>(h);
-  if (N <= 1024) return launch_ring<T, W, 64, 16>(h);
-  if (N <= 2048) return launch_ring<T, W, 128, 16>(h);
-  if (N <= 4096) return launch_ring<T, W, 256, 16>(h);
-  if (N <= 6144) return launch_ring<T, W, 384, 16>(h);
-  if (N <= kSliceCols) return launch_ring<T, W, 512, 16>(h);
-  const int64_t ranks = ceil_div(N, kSliceCols);
-  if (ranks <= kMaxCluster) {
-    // slices of 8 columns' multiples start on 16 bytes of an aligned row
-    const int64_t cols = round_up(ceil_div(N, ranks), 8);
-    return launch_cluster<T, W>(h, static_cast<int>(ceil_div(N, cols)), static_cast<int>(cols));
-  }
+  if (width <= 512) return launch_ring<T, kW, 64, 8, kShift>(h);
+  if (width <= 1024) return launch_ring<T, kW, 64, 16, kShift>(h);
+  if (width <= 2048) return launch_ring<T, kW, 128, 16, kShift>(h);
+  if (width <= 4096) return launch_ring<T, kW, 256, 16, kShift>(h);
+  if (width <= 6144) return launch_ring<T, kW, 384, 16, kShift>(h);
+  if (width <= kSliceCols) return launch_ring<T, kW, 512, 16, kShift>(h);
+  // two blocks per SM, of other clusters, where eight of their slices hold a
+  // row: 4096 x 12288 bf16 takes 94 us so and 109 us with one of twice the size
+  if (width <= kMaxCluster * kSliceCols / 2) return launch_cluster<T, kW, kShift, 256>(h, width);
+  if (width <= kMaxCluster * kSliceCols) return launch_cluster<T, kW, kShift, 512>(h, width);
   if (h.a.gx != nullptr) {
     ProfScope ps(K_LAYER_NORM_BWD, h.s);
     norm_backward_long_kernel<T><<<static_cast<unsigned>(h.a.M), kWideThreads, 0, h.s>>>(h.a);
@@ -1140,7 +1223,7 @@ template <typename T>
 cudaError_t backward(const BackwardArgs& a, void* gw, void* gb, cudaStream_t s) {
   constexpr int kW = 16 / sizeof(T);
   Shape h{a, sm_count(), 0, s};
-  if (cudaError_t e = a.N % kW == 0 ? backward_sized<T, kW>(h) : backward_sized<T, 1>(h)) return e;
+  if (cudaError_t e = a.N % kW == 0 ? backward_sized<T, kW, false>(h) : backward_sized<T, kW, true>(h)) return e;
   if (a.partial == nullptr) return cudaSuccess;
   ProfScope ps(K_LAYER_NORM_GRAD_SUM, s);
   // started while the backward kernel's last blocks run

@@ -106,6 +106,40 @@ def _check_backward(x, w, g, mean, rstd, got):
         assert ((gb.double() - ref).abs() <= U[pt] * ref.abs() + 1.01 * sums * gd.abs().sum(0) + TINY[pt]).all()
 
 
+# Rows that do not start on 16 bytes, more of them than blocks: every class of
+# lengths, either side of its limit.
+SHIFTED = [(2500, 513), (2500, 1017), (1300, 1018), (1300, 2041), (700, 2047), (700, 4090), (330, 4094), (330, 6141),
+           (170, 6143), (160, 8185), (160, 8190), (90, 8193), (90, 16377), (40, 16378), (40, 20003), (30, 32761),
+           (20, 32763), (20, 40003), (9, 8195), (1, 8193), (3, 12006)]
+
+
+@pytest.mark.parametrize("dt,wt", [(F16, F32), (BF16, BF16), (F32, F16)])
+@pytest.mark.parametrize("M,N", SHIFTED)
+def test_shifted_rows(M, N, dt, wt):
+    x, w, b, g = _data(M, N, dt, wt, M + 3 * N)
+    got = I.layer_norm(x, w, b)
+    _check_forward(x, w, b, 1e-5, got)
+    back = I.layer_norm_backward(g, x, got[1], got[2], w)
+    _check_backward(x, w, g, got[1], got[2], back)
+    for need in ((1, 0, 0), (0, 1, 1)):
+        some = I.layer_norm_backward(g, x, got[1], got[2], w, *map(bool, need))
+        assert all(p is None or torch.equal(p, q) for p, q in zip(some, back))
+
+
+@pytest.mark.parametrize("N", [75, 1001, 5003, 9001, 20003])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_do_not_touch_each_other(N, bad):
+    x, w, b, g = _data(41, N, BF16, F32, N)
+    y, mean, rstd = I.layer_norm(x, w, b)
+    gx, _, _ = I.layer_norm_backward(g, x, mean, rstd, w)
+    x2, g2 = x.clone(), g.clone()
+    x2[::2], g2[::2] = bad, bad             # every other row
+    y2, mean2, rstd2 = I.layer_norm(x2, w, b)
+    gx2, _, _ = I.layer_norm_backward(g2, x2, mean2, rstd2, w)
+    for one, two in ((y, y2), (mean, mean2), (rstd, rstd2), (gx, gx2)):
+        assert torch.equal(one[1::2], two[1::2]) and not two[::2].float().isfinite().all()
+
+
 @pytest.mark.parametrize("need", [(1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 0), (0, 1, 1)])
 def test_backward_parts(need):
     x, w, b, g = _data(700, 1032, BF16, F32, 5)
