@@ -178,44 +178,17 @@ struct Ring {
     return min((b + cols * sizeof(T) + 15ull) & ~15ull, end & ~15ull);
   }
   __device__ __forceinline__ void issue(int64_t i) {   // one thread
-    const unsigned long long b = start(i), lo = b & ~15ull, hi = stop(b);
-    const uint32_t bytes = hi > lo ? static_cast<uint32_t>(hi - lo) : 0u;
+    const unsigned long long b = start(i), e = stop(b);
+    const uint32_t bytes = e > b ? static_cast<uint32_t>(e - b) : 0u;
     const int s = static_cast<int>(static_cast<unsigned>(i) % L.stages);
     mbar_arrive_expect_tx(&full[s], kMats * bytes);
     if (bytes != 0)
 #pragma unroll
       for (int k = 0; k < kMats; ++k)
-        bulk_load(base + (static_cast<size_t>(s) * kMats + k) * L.slot_bytes, mat[k] + lo, bytes, &full[s]);
+        bulk_load(base + (static_cast<size_t>(s) * kMats + k) * L.slot_bytes, mat[k] + b, bytes, &full[s]);
   }
 };
 
-// A row's slice in its stage: elements [0, have) lie in shared memory, the
-// last few of the matrix, which no 16-byte copy covers, in global memory.
-template <typename T>
-struct Slice {
-  const T *near, *far;
-  int have;
-};
-template <typename T, int W, int kMats>
-__device__ __forceinline__ Slice<T> slice_of(const Ring<T, kMats>& r, int k, int64_t i, int stage) {
-  const unsigned long long b = r.start(i);
-  Slice<T> s;
-  s.near = reinterpret_cast<const T*>(r.base + (static_cast<size_t>(stage) * kMats + k) * r.L.slot_bytes + (b & 15));
-  s.far = reinterpret_cast<const T*>(r.mat[k] + b);
-  s.have = r.cols;
-  if constexpr (W == 1) {
-    const unsigned long long e = r.stop(b);
-    s.have = e > b ? static_cast<int>(min((e - b) / sizeof(T), static_cast<unsigned long long>(r.cols))) : 0;
-  }
-  return s;
-}
-// The pack at column c of a slice of `cols` columns; zeros past the end,
-// which a stage of aligned rows holds itself (zero_tails).
-template <typename T, int W>
-__device__ __forceinline__ void read(const Slice<T>& s, int c, int cols, float* f) {
-  if constexpr (W == 1) f[0] = c >= cols ? 0.f : to_float(c < s.have ? s.near[c] : s.far[c]);
-  else widen<T, W>(load_pack<T, W>(s.near + c), f);
-}
 // Zeros behind the slices of all stages (the copies never write there).
 template <typename T, int kMats>
 __device__ __forceinline__ void zero_tails(const Ring<T, kMats>& r, int threads) {
@@ -238,7 +211,7 @@ struct Shift {
     for (int k = 0; k < W; ++k)
       if (!in(c + k)) f[k] = 0.f;
   }
-  // the pack at place c of a parameter vector and of a row (o: its boundary)
+  // the pack at place c of a parameter vector, and of a row whose boundary is o
   __device__ __forceinline__ void param(const void* p, int dt, int c, float none, float* f) const {
     if constexpr (!kShift) {
       load_param<W>(p, dt, c, none, f);
@@ -294,7 +267,9 @@ struct ForwardArgs {
 
 // One row per kLanes threads (lanes of a warp for short rows, a block for rows
 // of 8192 to 16384), held in registers; the variance is summed around the
-// mean.  The block form has no ring, but several blocks per SM.
+// mean.  The block form has no ring, but several blocks per SM: 4096 x 11008
+// bf16 takes 50 us (3.6 TB/s) so, 83 us in three passes over the ring.  Bound
+// by the latency of a row: its loads, two sums over the block, its stores.
 template <typename T, int W, int kLanes, int kE>
 __global__ void __launch_bounds__(kLanes > 32 ? kLanes : 256) norm_forward_row_kernel(const ForwardArgs a) {
   constexpr int kRows = kLanes > 32 ? 1 : 256 / kLanes;
@@ -346,7 +321,8 @@ __global__ void __launch_bounds__(kLanes > 32 ? kLanes : 256) norm_forward_row_k
 }
 
 // Rows of up to 8192 elements (shifted: 16384): 32 elements, and their w and
-// b, in each thread's registers.
+// b, in each thread's registers (16 in rows of up to 1024).  Bound by HBM:
+// 16384 x 8192 bf16 takes 90 us, 6.0 TB/s.
 template <typename T, int W, int kLanes, int kE, bool kShift>
 __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel(const ForwardArgs a,
                                                                                 const RingLayout L) {
@@ -380,7 +356,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel
   for (int64_t i = 0; i < ring.rows; ++i) {
     mbar_wait(&full[s], phase, &abort_flag, nullptr, 31);
     if constexpr (kShift) last_elements(ring, i, a.M, s);
-    const Slice<T> x = slice_of<T, W>(ring, 0, i, s);
+    const T* x = reinterpret_cast<const T*>(stages + s * L.slot_bytes);
     float t = 0.f;
 #pragma unroll
     for (int e = 0; e < kE / W; ++e) {
@@ -388,7 +364,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel
       // (a branch per pack, which keeps the loads apart: without it, on zeros
       // behind the row, 16384 x 8192 bf16 took 99 us instead of 90)
       if (c < end) {
-        read<T, W>(x, c, end, v + e * W);
+        widen<T, W>(load_pack<T, W>(x + c), v + e * W);
         if (shift.edge(c)) shift.clear(c, v + e * W);
       } else {
 #pragma unroll
@@ -432,33 +408,40 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel
   }
 }
 
-// Longer rows: three passes over the row's stage in shared memory.
+// Longer rows: three passes over the row's stage in shared memory, w and b
+// from L2 (registers do not hold them).  Bound by these passes: 4096 x 28672
+// bf16 takes 134 us, 3.5 TB/s; shifted, where w and b are read singly, 4096 x
+// 21003 takes 191 us.
 constexpr int kWideThreads = 1024;
-template <typename T, int W>
+template <typename T, int W, bool kShift>
 __global__ void __launch_bounds__(kWideThreads) norm_forward_wide_kernel(const ForwardArgs a, const RingLayout L) {
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ uint64_t full[kMaxStages];
   __shared__ __align__(16) float scratch[2][kWideThreads / 32];
   __shared__ int abort_flag;
-  const int tid = threadIdx.x, N = static_cast<int>(a.N);
+  const int tid = threadIdx.x;
+  const Shift<W, kShift> shift(blockIdx.x, a.N);
+  const int end = shift.end;
   Ring<T, 1> ring{{static_cast<const uint8_t*>(a.x)}, stages, full, L, a.N, 0, gridDim.x,
                   (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
-                  static_cast<unsigned long long>(a.M) * a.N * sizeof(T), N, 0};
+                  static_cast<unsigned long long>(a.M) * a.N * sizeof(T), end, shift.first};
   if (tid == 0) {
     ring_setup(full, L.stages, &abort_flag);
     for (int64_t i = 0; i < L.stages && i < ring.rows; ++i) ring.issue(i);
   }
   __syncthreads();
-  const float inv_n = 1.0f / static_cast<float>(N);
+  const float inv_n = 1.0f / static_cast<float>(a.N);
   unsigned s = 0;
   uint32_t phase = 0;
   for (int64_t i = 0; i < ring.rows; ++i) {
     mbar_wait(&full[s], phase, &abort_flag, nullptr, 31);
-    const Slice<T> x = slice_of<T, W>(ring, 0, i, s);
+    if constexpr (kShift) last_elements(ring, i, a.M, s);
+    const T* x = reinterpret_cast<const T*>(stages + s * L.slot_bytes);
     float t = 0.f, v[W];
 #pragma unroll 4
-    for (int c = tid * W; c < N; c += kWideThreads * W) {
-      read<T, W>(x, c, N, v);
+    for (int c = tid * W; c < end; c += kWideThreads * W) {
+      widen<T, W>(load_pack<T, W>(x + c), v);
+      if (shift.edge(c)) shift.clear(c, v);
 #pragma unroll
       for (int k = 0; k < W; ++k) t += v[k];
     }
@@ -467,23 +450,26 @@ __global__ void __launch_bounds__(kWideThreads) norm_forward_wide_kernel(const F
     if (tid == 0 && i > 0 && i - 1 + L.stages < ring.rows) ring.issue(i - 1 + L.stages);
     t = 0.f;
 #pragma unroll 4
-    for (int c = tid * W; c < N; c += kWideThreads * W) {
-      read<T, W>(x, c, N, v);
+    for (int c = tid * W; c < end; c += kWideThreads * W) {
+      widen<T, W>(load_pack<T, W>(x + c), v);
 #pragma unroll
-      for (int k = 0; k < W; ++k) t += (v[k] - mu) * (v[k] - mu);
+      for (int k = 0; k < W; ++k) v[k] -= mu;
+      if (shift.edge(c)) shift.clear(c, v);
+#pragma unroll
+      for (int k = 0; k < W; ++k) t += v[k] * v[k];
     }
     const float r = 1.0f / sqrtf(row_sum<kWideThreads>(t, scratch[1]) * inv_n + a.eps);
     const int64_t m = ring.row(i);
-    T* y = static_cast<T*>(a.y) + m * N;
+    T* y = static_cast<T*>(a.y) + m * a.N - shift.first;
 #pragma unroll 4
-    for (int c = tid * W; c < N; c += kWideThreads * W) {
+    for (int c = tid * W; c < end; c += kWideThreads * W) {
       float w[W], b[W];
-      load_param<W>(a.w, a.wt, c, 1.f, w);
-      load_param<W>(a.b, a.wt, c, 0.f, b);
-      read<T, W>(x, c, N, v);
+      shift.param(a.w, a.wt, c, 1.f, w);
+      shift.param(a.b, a.wt, c, 0.f, b);
+      widen<T, W>(load_pack<T, W>(x + c), v);
 #pragma unroll
       for (int k = 0; k < W; ++k) v[k] = fmaf((v[k] - mu) * r, w[k], b[k]);
-      store_floats<T, W>(y + c, v);
+      shift.store(y, c, v);
     }
     if (tid == 0) {
       if (a.mean != nullptr) a.mean[m] = mu;
@@ -496,7 +482,8 @@ __global__ void __launch_bounds__(kWideThreads) norm_forward_wide_kernel(const F
   }
 }
 
-// Rows that do not fit shared memory twice: three passes over global memory.
+// Rows that do not fit shared memory twice: three passes over global memory
+// (the second and third mostly from L2).
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads) norm_forward_long_kernel(const ForwardArgs a) {
   __shared__ __align__(16) float scratch[2][kWideThreads / 32];
@@ -533,11 +520,10 @@ int sm_count() {
 
 // Stages of `mats` slices of `cols` elements, for per_sm blocks per SM.
 // width: the elements that the block's threads read of a slice.
-RingLayout ring_layout(int64_t cols, int64_t width, bool aligned, int elem, int mats, int per_sm) {
+RingLayout ring_layout(int64_t cols, int64_t width, int elem, int mats, int per_sm) {
   RingLayout L;
   L.cols = static_cast<int>(cols);
-  // up to 15 bytes before a slice that starts off a boundary
-  L.slot_bytes = static_cast<int>(aligned ? width * elem : round_up(cols * elem + 16, 128));
+  L.slot_bytes = static_cast<int>(width * elem);
   L.stages = static_cast<unsigned>(std::min(kMaxStages, kRingBytes / per_sm / (mats * L.slot_bytes)));
   return L;
 }
@@ -562,7 +548,7 @@ cudaError_t launch_forward_ring(const ForwardArgs& a, cudaStream_t s) {
   auto kernel = norm_forward_ring_kernel<T, W, kLanes, kE, kShift>;
   constexpr int per_sm = 512 / kLanes;
   const int64_t width = a.N + (kShift ? W - 1 : 0);
-  const RingLayout L = ring_layout(width, round_up(width, 64), true, sizeof(T), 1, per_sm);
+  const RingLayout L = ring_layout(width, round_up(width, 64), sizeof(T), 1, per_sm);
   const int smem = static_cast<int>(L.stages) * L.slot_bytes;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
   kernel<<<static_cast<unsigned>(row_blocks(a.M, sm_count() * per_sm, W, kShift)), kLanes, smem, s>>>(a, L);
@@ -585,12 +571,12 @@ cudaError_t forward_sized(const ForwardArgs& a, cudaStream_t s) {
     if constexpr (kShift) return launch_forward_ring<T, kW, 512, 32, true>(a, s);
     else return launch_forward_row<T, kW, 512, 32>(a, s);
   }
-  if (a.N * static_cast<int64_t>(sizeof(T)) <= kRingBytes / 2 - 256) {
-    auto kernel = norm_forward_wide_kernel<T, W>;
-    const RingLayout L = ring_layout(a.N, round_up(a.N, 64), W > 1, sizeof(T), 1, 1);
+  if (round_up(width, 64) * static_cast<int64_t>(sizeof(T)) <= kRingBytes / 2) {   // two rows
+    auto kernel = norm_forward_wide_kernel<T, kW, kShift>;
+    const RingLayout L = ring_layout(width, round_up(width, 64), sizeof(T), 1, 1);
     const int smem = static_cast<int>(L.stages) * L.slot_bytes;
     if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
-    kernel<<<static_cast<unsigned>(std::min<int64_t>(a.M, sm_count())), kWideThreads, smem, s>>>(a, L);
+    kernel<<<static_cast<unsigned>(row_blocks(a.M, sm_count(), kW, kShift)), kWideThreads, smem, s>>>(a, L);
     return cudaGetLastError();
   }
   norm_forward_long_kernel<T><<<static_cast<unsigned>(a.M), kWideThreads, 0, s>>>(a);
@@ -620,6 +606,7 @@ struct BackwardArgs {
 // Short rows: kLanes lanes of a warp per row, rows dealt out in turn, the
 // next row's loads issued before this row's arithmetic; every lane sums its
 // own columns' gradients over its rows, the block adds them up at the end.
+// Bound by the latency of a row: 32768 x 118 f32 takes 16 us, 2.9 TB/s.
 template <typename T, int W, int kLanes>
 __global__ void __launch_bounds__(256, 2) norm_backward_short_kernel(const BackwardArgs a) {
   constexpr int kE = 8, kSlots = 256 / kLanes, kVec = kE / W;
@@ -738,7 +725,11 @@ __device__ __forceinline__ float warp_sums(float (&v)[kN]) {
 
 // Rows of up to 8192 elements through the ring, a block per row: 16 elements
 // in each thread's registers, with w and the gradient sums of their columns
-// over all the block's rows.
+// over all the block's rows.  Bound by HBM on many rows (16384 x 8192 bf16:
+// 139 us, 5.8 TB/s), by the blocks' start, last row and sums on fewer
+// (8192 x 4096 f16: 46 us, 4.4 TB/s).  With 8 elements per thread and twice
+// the warps the former takes 180 us; reading each stage twice, for the sums
+// and for gx, as in the kernel for longer rows, 163 us.
 template <typename T, int W, int kLanes, int kE, bool kShift>
 __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kernel(const BackwardArgs a,
                                                                                  const RingLayout L) {
@@ -865,7 +856,9 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
 // rows are worked on between two barriers: their stages are read twice, for
 // the rows' two sums and for gx, so that registers hold only w and the
 // gradient sums of the thread's columns.  The blocks send each other their
-// sums without waiting: gx follows one step later.
+// sums without waiting: gx follows one step later.  Bound by instruction
+// issue and the steps' barriers: 4096 x 12288 bf16 takes 94 us, 3.2 TB/s,
+// 4096 x 28672 198 us, 3.6 TB/s.
 template <typename T, int W, int kLanes, int kE, int kRows, bool kShift>
 __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_kernel(const BackwardArgs a,
                                                                                  const RingLayout L) {
@@ -924,12 +917,13 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
         if constexpr (kShift) last_elements(ring, row, a.M, s);
         if (!want_x) continue;
         const float mu = __ldg(a.mean + ring.row(row)), r = __ldg(a.rstd + ring.row(row));
-        const Slice<T> xs = slice_of<T, W>(ring, 0, row, s), gs = slice_of<T, W>(ring, 1, row, s);
+        const T* xs = reinterpret_cast<const T*>(stages + 2 * s * L.slot_bytes);
+        const T* gs = reinterpret_cast<const T*>(stages + (2 * s + 1) * L.slot_bytes);
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
           float x[W], g[W];
-          read_pack(xs.near, (tid + e * kLanes) * W, x);
-          read_pack(gs.near, (tid + e * kLanes) * W, g);
+          read_pack(xs, (tid + e * kLanes) * W, x);
+          read_pack(gs, (tid + e * kLanes) * W, g);
 #pragma unroll
           for (int k = 0; k < W; ++k) {
             g[k] *= w[e * W + k];
@@ -983,14 +977,15 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
       const float mu = __ldg(a.mean + ring.row(row)), r = __ldg(a.rstd + ring.row(row));
       const float c1 = -r * inv_n * __shfl_sync(0xffffffffu, total, 2 * q * (32 / kSums));
       const float c2 = -r * inv_n * __shfl_sync(0xffffffffu, total, (2 * q + 1) * (32 / kSums));
-      const Slice<T> xs = slice_of<T, W>(ring, 0, row, s), gs = slice_of<T, W>(ring, 1, row, s);
+      const T* xs = reinterpret_cast<const T*>(stages + 2 * s * L.slot_bytes);
+      const T* gs = reinterpret_cast<const T*>(stages + (2 * s + 1) * L.slot_bytes);
       T* out = static_cast<T*>(a.gx) + ring.row(row) * a.N - shift.first;
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         const int c = (tid + e * kLanes) * W;
         float x[W], g[W];
-        read_pack(xs.near, c, x);
-        read_pack(gs.near, c, g);
+        read_pack(xs, c, x);
+        read_pack(gs, c, g);
 #pragma unroll
         for (int k = 0; k < W; ++k) {
           x[k] = (x[k] - mu) * r;
@@ -1058,7 +1053,8 @@ __global__ void __launch_bounds__(256) norm_grad_long_kernel(const BackwardArgs 
 }
 
 // gw[n], gb[n]: the blocks' partial sums added up in a fixed order, 32
-// columns per block (blockIdx.y: gw or gb), 32 threads per column.
+// columns per block (blockIdx.y: gw or gb), 32 threads per column.  Bound by
+// latency: 304 sums of 4096 columns add 5 us to the kernel before.
 __global__ void __launch_bounds__(1024) norm_grad_sum_kernel(const float* partial, int blocks, int64_t N, int wt,
                                                              void* gw, void* gb) {
   __shared__ float sums[32][33];
@@ -1114,7 +1110,7 @@ cudaError_t launch_short(Shape& h) {
 template <typename T, int W, int kLanes, int kE, bool kShift>
 cudaError_t launch_ring(Shape& h) {
   constexpr int per_sm = 512 / kLanes;
-  const RingLayout L = ring_layout(h.a.N, kLanes * kE, true, sizeof(T), 2, per_sm);
+  const RingLayout L = ring_layout(h.a.N, kLanes * kE, sizeof(T), 2, per_sm);
   auto kernel = norm_backward_ring_kernel<T, W, kLanes, kE, kShift>;
   const int smem = static_cast<int>(L.stages) * 2 * L.slot_bytes;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
@@ -1156,7 +1152,7 @@ cudaError_t launch_cluster(Shape& h, int64_t width) {
   const int64_t least = ceil_div(width, kLanes * kE);
   const int64_t cols = round_up(ceil_div(width, least), 8);   // slices of whole packs
   const int ranks = static_cast<int>(ceil_div(width, cols));
-  const RingLayout L = ring_layout(cols, kLanes * kE, true, sizeof(T), 2, per_sm);
+  const RingLayout L = ring_layout(cols, kLanes * kE, sizeof(T), 2, per_sm);
   auto kernel = L.stages >= 6u ? norm_backward_cluster_kernel<T, W, kLanes, kE, 2, kShift>
                                : norm_backward_cluster_kernel<T, W, kLanes, kE, 1, kShift>;
   const int smem = static_cast<int>(L.stages) * 2 * L.slot_bytes;

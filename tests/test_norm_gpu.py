@@ -110,7 +110,8 @@ def _check_backward(x, w, g, mean, rstd, got):
 # lengths, either side of its limit.
 SHIFTED = [(2500, 513), (2500, 1017), (1300, 1018), (1300, 2041), (700, 2047), (700, 4090), (330, 4094), (330, 6141),
            (170, 6143), (160, 8185), (160, 8190), (90, 8193), (90, 16377), (40, 16378), (40, 20003), (30, 32761),
-           (20, 32763), (20, 40003), (9, 8195), (1, 8193), (3, 12006)]
+           (20, 32763), (20, 40003), (9, 8195), (1, 8193), (3, 12006), (12, 25597), (12, 25598), (6, 51193),
+           (6, 51194), (160, 20003)]
 
 
 @pytest.mark.parametrize("dt,wt", [(F16, F32), (BF16, BF16), (F32, F16)])
