@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const int32_
   // second trip to memory
   constexpr int kStaged = kPlanThreads * kPer;
   __shared__ int counts[2][kWarpsPlan], own[kStaged];
+  grid_dependents_launch();   // a kernel that takes the plan may set itself up meanwhile
   const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto load = [&](int m0, int(&v)[kPer]) {   // the groups of 8 tokens, -1 past the end
     if (index == nullptr) {
@@ -160,6 +161,7 @@ __global__ void __launch_bounds__(kFewTokens) adapter_plan_few_kernel(const int3
                                                                       int few_slots) {
   __shared__ __align__(16) int group[kFewTokens];
   __shared__ int sorted[kFewTokens], place[kFewTokens], counts[kFewTokens / 32];
+  grid_dependents_launch();   // a kernel that takes the plan may set itself up meanwhile
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int g = E + 1;   // past the end: after every token
   if (tid < M) {
@@ -223,11 +225,10 @@ __global__ void __launch_bounds__(kFewTokens) adapter_plan_few_kernel(const int3
 // All three run on the tensor cores (tcgen05, 128-row tiles, fp32 accumulators
 // in TMEM) on operands staged in shared memory.  Where every row starts on 16
 // bytes, one warp fetches the operands by TMA, a tile of consecutive tokens
-// (one request, one adapter) as a box and others four rows at a time, and one
-// thread issues the products; else all threads gather them with narrower
-// asynchronous copies that fill what is past an edge with zeros.  Those cost
-// issue slots: 4096 -> 11008 at rank 64 on 8192 tokens took 28 + 92 us by
-// them, 24 + 63 us by TMA.  Matrices of a width C have rows of C 16-bit
+// (one request, one adapter) as a box, and one thread issues the products;
+// else all threads gather them with narrower asynchronous copies that fill
+// what is past an edge with zeros.  Those cost issue slots: 4096 -> 11008 at
+// rank 64 on 8192 tokens took 28 + 92 us by them, 24 + 63 us by TMA.  Matrices of a width C have rows of C 16-bit
 // elements; an operand tile is rows of 64 elements (128 bytes) in the
 // 128-byte swizzle, either with the reduction along the row ("K-major") or
 // across the rows ("MN-major").
@@ -420,14 +421,6 @@ __host__ __device__ constexpr uint32_t tmem_columns(int r16) { return r16 <= 32 
 // up: 16-byte accesses of 8 rows hit 8 different bank groups.
 __host__ __device__ constexpr int red_pitch(int r16) { return r16 + 4; }
 
-// The tokens at places 4 lane .. 4 lane + 3 of a tile, its last one repeated
-// past its end (whose products go nowhere).
-__device__ __forceinline__ void tile_rows(const int* perm, int start, int count, int (&rows)[4]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) rows[i] = perm[start + min(4 * lane + i, count - 1)];
-}
-
 // The CTA's accumulator (128 rows x r16) into shared memory.
 __device__ __forceinline__ void spill(uint32_t tmem, int r16, float* red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -464,7 +457,7 @@ __device__ __forceinline__ void cluster_sum4(uint32_t red, int at, int ranks, fl
 // ---- mid = X W^T (t and u) -------------------------------------------------
 
 struct ShrinkArgs {
-  CUtensorMap tmX, tmX1, tmW;   // with kTma: X, box 64 x 128 and 64 x 1; W, box 64 x r16 (K-major) or 64 x 64
+  CUtensorMap tmX, tmW;   // with kTma: X, box 64 x 128; W, box 64 x r16 (K-major) or 64 x 64
   const uint16_t* X;      // [M, C]
   const uint16_t* W;      // per group [R, C] (K-major) or [C, R] (MN-major)
   uint16_t* mid;          // [2, M, R] in the plan's order: the values, and what their rounding left
@@ -487,7 +480,9 @@ __host__ __device__ constexpr int shrink_stage_bytes(int r16, bool mn) {
 // accumulating in TMEM, and add up in the order of their ranks.  Bound by
 // reading X once, and W once per tile from L2: 8192 tokens of 11008 features,
 // rank 64, take 47 us, 3.9 TB/s of X.  Tiles of 256 tokens, which read W half
-// as often, make no difference.
+// as often, make no difference.  With kTma a tile of tokens here and there is
+// gathered by all threads, W by TMA all the same: 4 rows per TMA request took
+// 61 us for 8192 interleaved tokens of 8 adapters.
 template <bool kMN, int kStages, Copy kCopy>
 __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_constant__ ShrinkArgs a) {
   constexpr bool kTma = kCopy == kByTma;
@@ -498,11 +493,13 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
     tma_prefetch_desc(&a.tmX);
     tma_prefetch_desc(&a.tmW);
   }
+  const int tid = threadIdx.x, R = a.R, r16 = rank16(R);
+  sync_setup(y, tmem_columns(r16));
   grid_dependency_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.st = DevStatus{0, 0, 0, 0};
   const Tile t = a.tiles[blockIdx.x / ranks];
+  if (t.count == 0 || t.group >= a.E) sync_end(y, tmem_columns(r16));
   if (t.count == 0) return;
-  const int tid = threadIdx.x, R = a.R, r16 = rank16(R);
   if (t.group >= a.E) {
     if (rank == 0)
       for (int i = tid; i < t.count * R; i += kThreads) {
@@ -518,7 +515,6 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
   auto column = [&](int it) { return static_cast<int64_t>(rank + it * ranks) * 64; };
   const int64_t C = a.C;
   const uint16_t* W = a.W + static_cast<int64_t>(t.group) * R * C;
-  sync_setup(y, tmem_columns(r16));
 
   const uint32_t idesc = instruction(r16, false, kMN, a.bf16);
   auto multiply = [&](int it) {   // one thread: the products of a stage
@@ -531,27 +527,27 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
     umma_commit(&y.done[s]);
     if (it == n - 1) umma_commit(&y.last);
   };
-  if constexpr (kTma) {
-    if (tid < 32) {
-      uint8_t* stages = smem_raw + (base - smem_u32(smem_raw));
-      int rows[4];
-      if (t.row0 < 0) tile_rows(a.perm, t.start, t.count, rows);
+  const int cw = kTma ? 16 : a.cw;
+  // with kTma: the tile of W of step `it`, counted on its stage's barrier
+  auto load_w = [&](int it, uint8_t* ws, uint64_t* full) {
+    const int c0 = static_cast<int>(column(it));
+    if constexpr (kMN) {
+      tma_load_3d(ws, &a.tmW, 0, c0, t.group, full);
+      if (r16 > 64) tma_load_3d(ws + 64 * kRowBytes, &a.tmW, 64, c0, t.group, full);
+    } else {
+      tma_load_3d(ws, &a.tmW, c0, 0, t.group, full);
+    }
+  };
+  uint8_t* stages = smem_raw + (base - smem_u32(smem_raw));
+  if (kTma && t.row0 >= 0) {
+    if (tid == 0) {
       for (int it = 0; it < n; ++it) {
-        const int s = it % kStages, c0 = static_cast<int>(column(it));
-        uint8_t *xs = stages + s * stage_bytes, *ws = xs + 128 * kRowBytes;
+        const int s = it % kStages;
+        uint8_t* xs = stages + s * stage_bytes;
         if (it >= kStages) mbar_wait(&y.done[s], (it / kStages - 1) & 1, &y.abort, a.st, 20);
-        if (tid == 0) {
-          mbar_arrive_expect_tx(&y.full[s], stage_bytes);
-          if (t.row0 >= 0) tma_load_2d(xs, &a.tmX, c0, t.row0, &y.full[s]);
-          if constexpr (kMN) {
-            tma_load_3d(ws, &a.tmW, 0, c0, t.group, &y.full[s]);
-            if (r16 > 64) tma_load_3d(ws + 64 * kRowBytes, &a.tmW, 64, c0, t.group, &y.full[s]);
-          } else {
-            tma_load_3d(ws, &a.tmW, c0, 0, t.group, &y.full[s]);
-          }
-        }
-        __syncwarp();   // the stage is armed before its gathers arrive
-        if (t.row0 < 0) tma_gather4(xs + tid * 4 * kRowBytes, &a.tmX1, c0, rows, &y.full[s]);
+        mbar_arrive_expect_tx(&y.full[s], stage_bytes);
+        tma_load_2d(xs, &a.tmX, static_cast<int>(column(it)), t.row0, &y.full[s]);
+        load_w(it, xs + 128 * kRowBytes, &y.full[s]);
       }
     } else if (tid == 32) {
       for (int it = 0; it < n; ++it) {
@@ -573,11 +569,16 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
       const int64_t c0 = column(b);
       const uint32_t xs = base + s * stage_bytes, ws = xs + 128 * kRowBytes;
       const int64_t at = c0 + (tid & 7) * 8;
-      load_chunks<kCopy, 4>(a.cw, [&](int i) {   // of rows past the tile's tokens nothing is read
+      load_chunks<kCopy, 4>(cw, [&](int i) {   // of rows past the tile's tokens nothing is read
         const int row = (tid >> 3) + 32 * i;
         return Chunk{xs + swizzled(row, tid & 7), xrow[i], at, row < t.count ? C - at : 0};
       });
-      if constexpr (kMN) {
+      if constexpr (kTma) {
+        if (tid == 0) {
+          mbar_arrive_expect_tx(&y.full[s], stage_bytes - 128 * kRowBytes);
+          load_w(b, stages + s * stage_bytes + 128 * kRowBytes, &y.full[s]);
+        }
+      } else if constexpr (kMN) {
         const int chunks = r16 / 8;
         for (int i = tid; i < 64 * chunks; i += kThreads) {
           const int k = i / chunks, c = i % chunks;
@@ -599,7 +600,10 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
       cp_async_wait<kStages - 2>();
       fence_proxy_async_smem();
       __syncthreads();
-      if (tid == 0) multiply(it);
+      if (tid == 0) {
+        if (kTma) mbar_wait(&y.full[it % kStages], (it / kStages) & 1, &y.abort, a.st, 25);
+        multiply(it);
+      }
       const int next = it + kStages - 1;
       if (next < n) {
         // the stage to refill was read by the products of step it - 1
@@ -1719,7 +1723,6 @@ cudaError_t shrink(const Problem& p, const void* X, int64_t C, const void* W, bo
   const dim3 grid(static_cast<unsigned>(ranks * p.plan.slots));
   const Copy copy = copy_of(p, C);
   if (copy == kByTma && (!make_tmap(&a.tmX, map_type(p), X, C, p.M, C * 2, 64, 128, kSwz) ||
-              !make_tmap(&a.tmX1, map_type(p), X, C, p.M, C * 2, 64, 1, kSwz) ||
               !(mn ? make_tmap_3d(&a.tmW, map_type(p), W, p.R, C, p.E, 2, 64, 64, kSwz)
                    : make_tmap_3d(&a.tmW, map_type(p), W, C, p.R, p.E, 2, 64, r16, kSwz))))
     return cudaErrorUnknown;
