@@ -400,7 +400,8 @@ def i8lt_adapters_backward(g, x, t, dt, M, K, A, B, E, r, N, scale, plan, addend
 
 def i8lt_adamw_step(params, pt, grads, gt, sizes, count, m, v, step, lr, beta1, beta2, eps, weight_decay,
                     grad_scale=None, found_inf=None, stream=None) -> int:
-    """params, grads: ctypes arrays of device addresses; sizes: of int64."""
+    """params, grads: arrays of device addresses; sizes: of int64 (ctypes
+    arrays, or the addresses of such)."""
     return load().i8lt_adamw_step(params, pt, grads, gt, sizes, count, m, v, step, lr, beta1, beta2, eps,
                                   weight_decay, grad_scale, found_inf, stream)
 

@@ -9,6 +9,7 @@ efficient backward" (see include/i8lt.h for the formulas).
 """
 from __future__ import annotations
 
+import array
 import math
 import operator
 import warnings
@@ -872,9 +873,11 @@ _is_contiguous, _numel, _dtype_of = torch.Tensor.is_contiguous, torch.Tensor.num
 
 
 def _adamw_lists(what, params, grads):
-    """(a parameter, what must outlive the call, count, ctypes arrays of the
-    device addresses and sizes, dtypes, elements of a state), checked.  Called
-    for hundreds of tensors per step: each property is read in one sweep."""
+    """(a parameter, what must outlive the call, count, addresses of the lists
+    of device addresses and sizes, dtypes, elements of a state), checked.
+    Called for hundreds of tensors per step: each property is read in one
+    sweep, and the lists are plain arrays (128 tensors: 90 us; 119 us with
+    ctypes arrays, which convert element by element)."""
     n = len(params)
     if n != len(grads):
         raise I8LTError(f"{what}: {n} parameters, {len(grads)} gradients")
@@ -900,9 +903,10 @@ def _adamw_lists(what, params, grads):
     sizes = list(map(_numel, params))
     blk = _lib.I8LT_ADAMW_BLOCK
     total = sum([(k + blk - 1) // blk for k in sizes]) * blk
-    addresses = map(_data_ptr, held) if present[1] is grads else map(_ptr, held)
-    return (p0, held, n, (_lib.c_void_p * n)(*map(_data_ptr, params)), (_lib.c_void_p * n)(*addresses),
-            (_lib.c_int64 * n)(*sizes), _code(p0.dtype), _code(g0.dtype), total)
+    addresses = map(_data_ptr, held) if present[1] is grads else [0 if g is None else g.data_ptr() for g in held]
+    lists = array.array("Q", map(_data_ptr, params)), array.array("Q", addresses), array.array("q", sizes)
+    at = [a.buffer_info()[0] for a in lists]
+    return p0, (held, lists), n, *at, _code(p0.dtype), _code(g0.dtype), total
 
 
 def _adamw_state(what, size, dtype, device, *ts):
