@@ -147,8 +147,8 @@ __device__ __forceinline__ float row_sum(float v, float* scratch) {
 // packs, counted from the boundary below the row's start ("shifted": x, g, y
 // and gx lie alike): with a row step that is a multiple of W, all rows of a
 // block start equally far behind a boundary, so that a thread keeps its
-// columns.  16384 x 5001 bf16 takes 93 us forward and 121 us backward so, and
-// 167 and 191 us element by element.
+// columns.  16384 x 5001 bf16 takes 93 us forward and 115 us backward so;
+// element by element it took 74 and 70 us more.
 constexpr int kMaxStages = 8;
 constexpr int kRingBytes = 200 * 1024;   // shared memory per SM given to the rings
 
@@ -723,13 +723,40 @@ __device__ __forceinline__ float warp_sums(float (&v)[kN]) {
   return v[0];
 }
 
+// A block's two sums of columns, place c of which is the thread's element
+// W * i + k with c = (tid + i * kLanes) * W + k, to consecutive global memory:
+// places [skip, skip + n) of `cols`, through shared memory (the stages, no
+// longer needed): a thread's own stores hit a sector per element, and 8192 x
+// 4096 f16 took 52 us instead of 44.
+template <int W, int kLanes, int kVec>
+__device__ __forceinline__ void store_sums(float* buf, int cols, int skip, int n, const float* s0, const float* s1,
+                                           float* out, int64_t stride) {
+  const int pitch = (cols + W - 1) / W * W;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int c = (threadIdx.x + i * kLanes) * W;
+    if (c >= cols) continue;
+#pragma unroll
+    for (int k = 0; k < W; k += 4) {
+      *reinterpret_cast<float4*>(buf + c + k) = *reinterpret_cast<const float4*>(s0 + i * W + k);
+      *reinterpret_cast<float4*>(buf + pitch + c + k) = *reinterpret_cast<const float4*>(s1 + i * W + k);
+    }
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < n; c += kLanes) {
+    out[c] = buf[skip + c];
+    out[stride + c] = buf[pitch + skip + c];
+  }
+}
+
 // Rows of up to 8192 elements through the ring, a block per row: 16 elements
 // in each thread's registers, with w and the gradient sums of their columns
 // over all the block's rows.  Bound by HBM on many rows (16384 x 8192 bf16:
-// 139 us, 5.8 TB/s), by the blocks' start, last row and sums on fewer
-// (8192 x 4096 f16: 46 us, 4.4 TB/s).  With 8 elements per thread and twice
-// the warps the former takes 180 us; reading each stage twice, for the sums
-// and for gx, as in the kernel for longer rows, 163 us.
+// 129 us, 6.2 TB/s), by the blocks' start, last row and sums on fewer
+// (8192 x 4096 f16: 38 us, 5.3 TB/s).  With 8 elements per thread and twice
+// the warps the former took 38 us more; reading each stage twice, for the sums
+// and for gx, as in the kernel for longer rows, 21 us more.
 template <typename T, int W, int kLanes, int kE, bool kShift>
 __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kernel(const BackwardArgs a,
                                                                                  const RingLayout L) {
@@ -754,7 +781,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
   }
   __syncthreads();
 
-  float w[kE], aw[kE], ab[kE];
+  __align__(16) float w[kE], aw[kE], ab[kE];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int c = (tid + i * kLanes) * W;
@@ -785,8 +812,8 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
       const int c = (tid + e * kLanes) * W;
-      // with the zeros behind the row: a branch per pack took 16384 x 8192 bf16
-      // from 143 to 186 us
+      // with the zeros behind the row: a branch per pack cost 16384 x 8192 bf16
+      // 43 us more
       widen<T, W>(load_pack<T, W>(xs + c), h + e * W);
       widen<T, W>(load_pack<T, W>(gs + c), g + e * W);
       if (shift.edge(c)) {
@@ -837,19 +864,9 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
   }
   grid_dependents_launch();
   if (a.partial == nullptr) return;
-  float* pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.N;
-  float* pb = pw + static_cast<int64_t>(gridDim.x) * a.N;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int c = (tid + i * kLanes) * W;
-    if (c >= cols) continue;
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      if (kShift && !shift.in(c + k)) continue;
-      pw[c + k - shift.first] = aw[i * W + k];
-      pb[c + k - shift.first] = ab[i * W + k];
-    }
-  }
+  store_sums<W, kLanes, kVec>(reinterpret_cast<float*>(stages), cols, shift.first, static_cast<int>(a.N), aw, ab,
+                              a.partial + static_cast<int64_t>(blockIdx.x) * a.N,
+                              static_cast<int64_t>(gridDim.x) * a.N);
 }
 
 // Longer rows: a cluster of blocks per row, each on a slice of it.  kRows
@@ -857,8 +874,8 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
 // the rows' two sums and for gx, so that registers hold only w and the
 // gradient sums of the thread's columns.  The blocks send each other their
 // sums without waiting: gx follows one step later.  Bound by instruction
-// issue and the steps' barriers: 4096 x 12288 bf16 takes 94 us, 3.2 TB/s,
-// 4096 x 28672 198 us, 3.6 TB/s.
+// issue and the steps' barriers: 4096 x 12288 bf16 takes 84 us, 3.6 TB/s,
+// 4096 x 28672 184 us, 3.8 TB/s.
 template <typename T, int W, int kLanes, int kE, int kRows, bool kShift>
 __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_kernel(const BackwardArgs a,
                                                                                  const RingLayout L) {
@@ -889,7 +906,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
   __syncthreads();
   if (ranks > 1) cluster_sync();   // the peers' barriers are ready
 
-  float w[kE], aw[kE], ab[kE];
+  __align__(16) float w[kE], aw[kE], ab[kE];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int c = (tid + i * kLanes) * W;
@@ -999,20 +1016,12 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
   }
   if (ranks > 1) cluster_sync();   // no block leaves while a peer may write to it
   if (a.partial == nullptr) return;
-  float* pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.N;
-  float* pb = pw + static_cast<int64_t>(gridDim.x) * a.N;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int c = (tid + i * kLanes) * W;
-    if (c >= cols) continue;
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      const int n = first + c + k;
-      if (kShift && !shift.in(n)) continue;
-      pw[n - shift.first] = aw[i * W + k];
-      pb[n - shift.first] = ab[i * W + k];
-    }
-  }
+  // this slice's places [0, cols) are the columns from first - shift.first on,
+  // those of the row among them
+  const int skip = max(0, shift.first - first);
+  store_sums<W, kLanes, kVec>(reinterpret_cast<float*>(stages), cols, skip, cols - skip, aw, ab,
+                              a.partial + static_cast<int64_t>(blockIdx.x) * a.N + (first + skip - shift.first),
+                              static_cast<int64_t>(gridDim.x) * a.N);
 }
 
 // Rows beyond a cluster's reach: passes over global memory.
@@ -1199,7 +1208,7 @@ cudaError_t backward_sized(Shape& h) {
   if (width <= 6144) return launch_ring<T, kW, 384, 16, kShift>(h);
   if (width <= kSliceCols) return launch_ring<T, kW, 512, 16, kShift>(h);
   // two blocks per SM, of other clusters, where eight of their slices hold a
-  // row: 4096 x 12288 bf16 takes 94 us so and 109 us with one of twice the size
+  // row: 4096 x 12288 bf16 took 94 us so and 109 us with one of twice the size
   if (width <= kMaxCluster * kSliceCols / 2) return launch_cluster<T, kW, kShift, 256>(h, width);
   if (width <= kMaxCluster * kSliceCols) return launch_cluster<T, kW, kShift, 512>(h, width);
   if (h.a.gx != nullptr) {
