@@ -1250,7 +1250,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
 // accumulators into gradients, warp 4 fetches, warp 5 issues the products.
 // 8192 tokens of 32 adapters, 4096 -> 11008, rank 64: both gradients take 81 us
 // by it and 159 us by one CTA per strip; 8 adapters 70 us and 76 us.
-constexpr int kManyThreads = 192;
+constexpr int kManyThreads = 320, kGatherers = 128;
 struct ManySync {
   uint64_t full[kMaxStages], done[kMaxStages], acc_full[2], acc_free[2];
   uint32_t tmem;
@@ -1264,7 +1264,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
   if (a.first && blockIdx.x == 0 && tid == 0) *a.st = DevStatus{0, 0, 0, 0};
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&y.full[i], 1);
+      mbar_init(&y.full[i], 1 + kGatherers);
       mbar_init(&y.done[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -1303,16 +1303,19 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
     return t;
   };
   const int64_t step = gridDim.x;
-  if (warp == 4) {
-    const int half = lane >> 4, quad = lane & 15;   // lanes 0-15 fetch the first 64 columns, 16-31 the others
-    int rows[4], next[4];
-    auto rows_of = [&](const Strip& t, int it) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (t.tokens > 0) next[i] = a.perm[t.start + min(it * 64 + 4 * quad + i, t.tokens - 1)];
-    };
+  // a block's first and last token; 64 consecutive ones are a box (they ascend)
+  auto ends_of = [&](const Strip& t, int it, int(&e)[2]) {
+    if (it * 64 >= t.tokens) return;
+    e[0] = a.perm[t.start + it * 64];
+    e[1] = a.perm[t.start + min(it * 64 + 63, t.tokens - 1)];
+  };
+  auto is_box = [&](const Strip& t, int it, const int(&e)[2]) {
+    return it * 64 + 64 <= t.tokens && e[1] - e[0] == 63;
+  };
+  if (tid == 128) {
+    int ends[2] = {0, 0};
     Strip t = strip_of(blockIdx.x);
-    rows_of(t, 0);
+    ends_of(t, 0, ends);
     bool waited = false;
     int at = 0;   // steps so far
     for (int64_t i = blockIdx.x; i < strips; i += step) {
@@ -1324,33 +1327,84 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
         waited = true;
       }
       for (int it = 0; it < n; ++it, ++at) {
-        const int s = at % kStages;
+        const int s = at % kStages, row0 = ends[0];
+        const bool box = is_box(t, it, ends);
         uint8_t *xs = stages + s * stage_bytes, *us = xs + 2 * 64 * kRowBytes;
+        if (it + 1 < n) ends_of(t, it + 1, ends);
+        else ends_of(after, 0, ends);
+        if (at >= kStages) mbar_wait(&y.done[s], (at / kStages - 1) & 1, &y.abort, a.st, 23);
+        mbar_arrive_expect_tx(&y.full[s], box ? stage_bytes : stage_bytes - 2 * 64 * kRowBytes);
+        for (int k = 0; k < 2; ++k) {
+          uint8_t* u = us + k * grad_mid_bytes(r16);
+          tma_load_2d(u, &d.tmU, 0, k * a.M + t.start + it * 64, &y.full[s]);
+          if (r16 > 64) tma_load_2d(u + 64 * kRowBytes, &d.tmU, 64, k * a.M + t.start + it * 64, &y.full[s]);
+        }
+        if (box) {
+          tma_load_2d(xs, &d.tmX, c0, row0, &y.full[s]);
+          tma_load_2d(xs + 64 * kRowBytes, &d.tmX, c0 + 64, row0, &y.full[s]);
+        }
+      }
+      if (n == 0) ends_of(after, 0, ends);
+      t = after;
+    }
+  } else if (warp >= 6) {
+    // the other blocks' rows of X, 16 threads a row; a stage is passed on once
+    // the next one's copies are under way
+    const int g = tid - 6 * 32, q = g & 15, r0 = g >> 4;
+    int ends[2] = {0, 0}, next[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) rows[k] = next[k];
+    for (int k = 0; k < 8; ++k) next[k] = 0;
+    auto rows_of = [&](const Strip& t, int it) {
+      ends_of(t, it, ends);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (t.tokens > 0) next[k] = a.perm[t.start + min(it * 64 + r0 + 8 * k, t.tokens - 1)];
+    };
+    int pending = -1;   // the stage whose copies may still be under way
+    auto pass_on = [&] {
+      if (pending < 0) return;
+      fence_proxy_async_smem();
+      mbar_arrive(&y.full[pending]);
+      pending = -1;
+    };
+    Strip t = strip_of(blockIdx.x);
+    rows_of(t, 0);
+    int at = 0;
+    for (int64_t i = blockIdx.x; i < strips; i += step) {
+      const Strip after = strip_of(i + step);
+      const GradSide& d = a.side[t.second];
+      const int n = (t.tokens + 63) / 64;
+      const bool in = t.c0 + q * 8 < d.C;
+      const uint16_t* X = d.X + (in ? t.c0 + q * 8 : 0);
+      for (int it = 0; it < n; ++it, ++at) {
+        const int s = at % kStages;
+        const bool box = is_box(t, it, ends);
+        int rows[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) rows[k] = next[k];
         if (it + 1 < n) rows_of(t, it + 1);
         else rows_of(after, 0);
-        const int row0 = __shfl_sync(0xffffffffu, rows[0], 0);
-        const bool box = __all_sync(0xffffffffu, rows[0] == row0 + 4 * quad && rows[3] == rows[0] + 3);   // ascending
-        if (at >= kStages) mbar_wait(&y.done[s], (at / kStages - 1) & 1, &y.abort, a.st, 23);
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&y.full[s], stage_bytes);
-          for (int k = 0; k < 2; ++k) {
-            uint8_t* u = us + k * grad_mid_bytes(r16);
-            tma_load_2d(u, &d.tmU, 0, k * a.M + t.start + it * 64, &y.full[s]);
-            if (r16 > 64) tma_load_2d(u + 64 * kRowBytes, &d.tmU, 64, k * a.M + t.start + it * 64, &y.full[s]);
-          }
-          if (box) {
-            tma_load_2d(xs, &d.tmX, c0, row0, &y.full[s]);
-            tma_load_2d(xs + 64 * kRowBytes, &d.tmX, c0 + 64, row0, &y.full[s]);
-          }
+        if (at >= kStages) mbar_wait(&y.done[s], (at / kStages - 1) & 1, &y.abort, a.st, 34);
+        if (box) {
+          cp_async_wait<0>();
+          pass_on();
+          mbar_arrive(&y.full[s]);
+          continue;
         }
-        __syncwarp();   // the stage is armed before its gathers arrive
-        if (!box) tma_gather4(xs + (half * 64 + quad * 4) * kRowBytes, &d.tmX1, c0 + 64 * half, rows, &y.full[s]);
+        const uint32_t xs = smem_u32(stages + s * stage_bytes) + (q >> 3) * 64 * kRowBytes;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          cp_async<16>(xs + swizzled(r0 + 8 * k, q & 7), X + static_cast<int64_t>(rows[k]) * d.C, in);
+        cp_async_commit();
+        cp_async_wait<1>();
+        pass_on();
+        pending = s;
       }
       if (n == 0) rows_of(after, 0);
       t = after;
     }
+    cp_async_wait<0>();
+    pass_on();
   } else if (warp == 5) {
     const uint32_t idesc = instruction(r16, true, true, a.bf16);
     int at = 0, acc = 0;   // steps and strips with tokens so far
