@@ -1247,9 +1247,14 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
 // The same for more strips than CTAs (many adapters, or wide layers of few):
 // each CTA takes strip after strip, whole, with the fetches of the next one
 // under way while the last one leaves tensor memory.  Warps 0-3 turn
-// accumulators into gradients, warp 4 fetches, warp 5 issues the products.
+// accumulators into gradients, warp 4 fetches mid and blocks of consecutive
+// tokens of X by TMA, warps 6-9 gather the other blocks' rows, warp 5 issues
+// the products.
 // 8192 tokens of 32 adapters, 4096 -> 11008, rank 64: both gradients take 81 us
-// by it and 159 us by one CTA per strip; 8 adapters 70 us and 76 us.
+// by it and 159 us by one CTA per strip; 8 adapters, interleaved, 57 us, and
+// 92 us with the rows gathered by TMA, four a request.  Bound by reading X
+// where the adapters' shares of the batch are alike; 8 adapters of uneven
+// shares take 71 us (a CTA's strips are dealt out without regard to them).
 constexpr int kManyThreads = 320, kGatherers = 128;
 struct ManySync {
   uint64_t full[kMaxStages], done[kMaxStages], acc_full[2], acc_free[2];
