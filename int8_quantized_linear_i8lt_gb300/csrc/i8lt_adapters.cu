@@ -4,12 +4,10 @@
 //   u[m] = scale[e] g[m] B[e],     gx[m] = addend[m] + u[m] A[e],
 //   gA[e] = sum_m u[m]^T x[m],     gB[e] = scale[e] sum_m g[m]^T t[m],
 // with A [E, r, K], B [E, N, r].  Every sum is fp32; y, gx, gA and gB are
-// rounded once.  t and u are operands of a second 16-bit product.  For gA and
-// gB they are kept as two 16-bit values whose sum is t (u) to twice the
-// type's precision, and both take part: a rounded t would be off by as much
-// as the gradient's own rounding (and by more where few tokens make it up).
-// y and gx take the first value alone: its error is the type's rounding of a
-// correction to base and addend.  Their rows are in the plan's order, so that
+// rounded once.  t and u are operands of a second 16-bit product.  They are
+// kept as two 16-bit values whose sum is t (u) to twice the type's precision,
+// and both take part in every output: a rounded t would be off by as much as
+// the output's own rounding.  Their rows are in the plan's order, so that
 // the tokens of a tile are a box of consecutive rows whatever the batch's
 // order: 8192 interleaved tokens of 8 adapters, 4096 -> 11008, rank 64, took
 // 349 us forward and backward with t and u gathered by token, 290 us so.
@@ -657,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
 
 struct ExpandArgs {
   CUtensorMap tmMid, tmW, tmAdd, tmOut;   // with kTma: mid, addend and out, box 64 x 128; W, box 64 x 64 or 64 x r16
-  const uint16_t* mid;     // [M, R], in the plan's order
+  const uint16_t* mid;     // [2, M, R], in the plan's order
   const uint16_t* W;       // per group [C, R] (K-major) or [R, C] (MN-major)
   const uint16_t* addend;  // [M, C] or NULL; may be out
   uint16_t* out;           // [M, C]
@@ -666,7 +664,7 @@ struct ExpandArgs {
   const int* perm;
   DevStatus* st;
   int64_t C;
-  int M, R, E, cw, rw;
+  int M, R, E, cw, rw, mw; // mw: the copy width of mid's second part
   int col_tiles;           // 64-column tiles per CTA
   bool bf16;
 };
@@ -676,13 +674,21 @@ constexpr uint32_t kTileBytes = 128 * kRowBytes;           // addend / out tile:
 __host__ __device__ constexpr int expand_blocks(int r16) { return r16 > 64 ? 2 : 1; }
 __host__ __device__ constexpr int expand_mid_bytes(int r16) { return expand_blocks(r16) * 128 * kRowBytes; }
 __host__ __device__ constexpr int expand_w_bytes(int r16) { return expand_blocks(r16) * 64 * kRowBytes; }
-__host__ __device__ constexpr int expand_tiles(int r16) { return r16 > 64 ? 2 : 4; }   // addend tiles in flight
+constexpr int kAddTiles = 4;                               // addend tiles in flight
 
 struct ExpandSync {
   uint64_t w_full[2], w_free[2], acc_full[2], acc_free[2], add_full[4], add_free[4], mid_full;
   uint32_t tmem;
   int abort;
 };
+// Shared memory: mid's two parts, two tiles of W, the addend tiles and the
+// barriers, with room to align the first.  Up to rank 64 two CTAs fit an SM
+// exactly.
+__host__ __device__ constexpr int expand_smem(int r16) {
+  return 2 * expand_mid_bytes(r16) + 2 * expand_w_bytes(r16) + kAddTiles * static_cast<int>(kTileBytes) + 1024;
+}
+__host__ __device__ constexpr int expand_per_sm(int r16) { return r16 > 64 ? 1 : 2; }
+static_assert(2 * (expand_smem(64) + 1024) <= 228 * 1024 && sizeof(ExpandSync) <= 512, "two CTAs per SM");
 
 // One CTA per (tile of 128 tokens, run of 64-column tiles): mid stays in
 // shared memory; per column tile W is read from L2, the addend tile arrives
@@ -694,8 +700,7 @@ constexpr int kExpandThreads = 320;
 template <bool kMN, Copy kCopy>
 __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_constant__ ExpandArgs a) {
   constexpr bool kTma = kCopy == kByTma;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ ExpandSync y;
+  extern __shared__ __align__(1024) uint8_t expand_raw[];
   if (kTma && threadIdx.x == 256) {
     tma_prefetch_desc(&a.tmW);
     tma_prefetch_desc(&a.tmAdd);
@@ -713,10 +718,11 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
   const int64_t C = a.C;
   const int j0 = blockIdx.y * a.col_tiles;
   const int n = min(a.col_tiles, static_cast<int>((C + kCols - 1) / kCols) - j0);
-  const int bufs = expand_tiles(r16);
-  uint8_t* mids = smem_raw + (align1024(smem_u32(smem_raw)) - smem_u32(smem_raw));
-  uint8_t* wbuf = mids + expand_mid_bytes(r16);
+  constexpr int bufs = kAddTiles;
+  uint8_t* mids = expand_raw + (align1024(smem_u32(expand_raw)) - smem_u32(expand_raw));
+  uint8_t* wbuf = mids + 2 * expand_mid_bytes(r16);
   uint8_t* tiles = wbuf + 2 * expand_w_bytes(r16);
+  ExpandSync& y = *reinterpret_cast<ExpandSync*>(tiles + bufs * kTileBytes);
   const float scale = a.scale != nullptr && adapter ? a.scale[t.group] : 1.f;
   // a tile that ends inside the batch or is no run of tokens is stored row by row
   const bool tma_out = kTma && t.row0 >= 0 && (t.count == 128 || t.row0 + t.count == a.M);
@@ -746,9 +752,12 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
   const uint32_t idesc = instruction(kCols, false, kMN, a.bf16);
   auto multiply = [&](int j) {   // one thread: accumulator j & 1 = mid W^T
     const uint32_t ms = smem_u32(mids), ws = smem_u32(wbuf) + (j & 1) * expand_w_bytes(r16);
-    for (int k = 0; k < r16 / 16; ++k)
-      umma_f16(y.tmem + (j & 1) * kCols, desc_k(ms + (k >> 2) * 128 * kRowBytes, k & 3),
-               kMN ? desc_mn(ws, k, 0) : desc_k(ws + (k >> 2) * 64 * kRowBytes, k & 3), idesc, k > 0 ? 1u : 0u);
+    for (int k = 0; k < r16 / 16; ++k) {
+      const uint32_t m = ms + (k >> 2) * 128 * kRowBytes;
+      const uint64_t w = kMN ? desc_mn(ws, k, 0) : desc_k(ws + (k >> 2) * 64 * kRowBytes, k & 3);
+      umma_f16(y.tmem + (j & 1) * kCols, desc_k(m, k & 3), w, idesc, k > 0 ? 1u : 0u);
+      umma_f16(y.tmem + (j & 1) * kCols, desc_k(m + expand_mid_bytes(r16), k & 3), w, idesc, 1u);
+    }
     umma_commit(&y.w_free[j & 1]);
     umma_commit(&y.acc_full[j & 1]);
   };
@@ -873,9 +882,11 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
         if (j == 0 && adapter) {
           grid_dependency_wait();
           if (lane == 0) {
-            mbar_arrive_expect_tx(&y.mid_full, expand_mid_bytes(r16));
-            for (int k = 0; k < expand_blocks(r16); ++k)
-              tma_load_2d(mids + k * 128 * kRowBytes, &a.tmMid, 64 * k, t.start, &y.mid_full);
+            mbar_arrive_expect_tx(&y.mid_full, 2 * expand_mid_bytes(r16));
+            for (int p = 0; p < 2; ++p)
+              for (int k = 0; k < expand_blocks(r16); ++k)
+                tma_load_2d(mids + p * expand_mid_bytes(r16) + k * 128 * kRowBytes, &a.tmMid, 64 * k,
+                            p * a.M + t.start, &y.mid_full);
           }
         }
       }
@@ -918,8 +929,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
         uint8_t* buf = tiles + (j % bufs) * kTileBytes;
         load_addend(j + bufs - 1);
         cp_async_commit();
-        if (bufs == 4) cp_async_wait<3>();
-        else cp_async_wait<1>();
+        cp_async_wait<kAddTiles - 1>();
         named_bar_sync(1, 256);
         finish(j, buf);
         named_bar_sync(1, 256);
@@ -954,8 +964,10 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
     if (adapter)
       for (int i = tid; i < t.count * chunks; i += kThreads) {
         const int row = i / chunks, c = i % chunks;
-        load_chunk<kCopy>(a.rw, Chunk{smem_u32(mids) + (c >> 3) * 128 * kRowBytes + swizzled(row, c & 7),
-                                      a.mid + static_cast<int64_t>(t.start + row) * R, c * 8, R - c * 8});
+        const uint32_t dst = smem_u32(mids) + (c >> 3) * 128 * kRowBytes + swizzled(row, c & 7);
+        const uint16_t* m = a.mid + static_cast<int64_t>(t.start + row) * R;
+        load_chunk<kCopy>(a.rw, Chunk{dst, m, c * 8, R - c * 8});
+        load_chunk<kCopy>(a.mw, Chunk{dst + expand_mid_bytes(r16), m + static_cast<int64_t>(a.M) * R, c * 8, R - c * 8});
       }
     // Buffers of tile j + 1: w of tile j - 1 was read by products that tile
     // j - 1's outputs waited for, its addend buffer left before the barrier
@@ -1551,7 +1563,7 @@ constexpr int kFewRanks = 8;
 template <bool kBf16, int kMaxRankTiles>   // tiles of 16 ranks
 __global__ void __launch_bounds__(kThreads, kMaxRankTiles > 4 ? 2 : kMaxRankTiles > 1 ? 3 : 4) few_kernel(const FewArgs a) {
   __shared__ __align__(16) float part[kThreads / 32][kMaxRankTiles * 16 * kFewTile];   // per warp, then the CTA's sum
-  __shared__ __align__(16) uint16_t ts[kFewTile][kMaxRankTiles * 16 + 8];
+  __shared__ __align__(16) uint16_t ts[2][kFewTile][kMaxRankTiles * 16 + 8];   // t's two parts
   __shared__ __align__(16) float ys[2][kFewTile][128 + 4];
   grid_dependency_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.st = DevStatus{0, 0, 0, 0};
@@ -1619,12 +1631,13 @@ __global__ void __launch_bounds__(kThreads, kMaxRankTiles > 4 ? 2 : kMaxRankTile
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int tok = i % kFewTile + k;
-        const uint16_t hi = to_16(s[k], kBf16);
-        ts[tok][j] = hi;
+        const uint16_t hi = to_16(s[k], kBf16), lo = rest_16(s[k], hi, kBf16);
+        ts[0][tok][j] = hi;
+        ts[1][tok][j] = lo;
         if (rank == 0 && tok < tile.count && j < R) {
           uint16_t* o = a.t + static_cast<int64_t>(tile.start + tok) * R + j;
           o[0] = hi;
-          o[a.plane] = rest_16(s[k], hi, kBf16);
+          o[a.plane] = lo;
         }
       }
     }
@@ -1653,7 +1666,8 @@ __global__ void __launch_bounds__(kThreads, kMaxRankTiles > 4 ? 2 : kMaxRankTile
         const bool in = k < R;
         const uint2 u = in && c0 < N ? __ldg(reinterpret_cast<const uint2*>(B + c0 * R + k)) : zero;
         const uint2 v = in && c1 < N ? __ldg(reinterpret_cast<const uint2*>(B + c1 * R + k)) : zero;
-        mma_16x8<kBf16>(d, u, v, in ? *reinterpret_cast<const uint2*>(&ts[g][k]) : zero);
+        mma_16x8<kBf16>(d, u, v, in ? *reinterpret_cast<const uint2*>(&ts[0][g][k]) : zero);
+        mma_16x8<kBf16>(d, u, v, in ? *reinterpret_cast<const uint2*>(&ts[1][g][k]) : zero);
       }
       float(*buf)[128 + 4] = ys[s & 1];
       const int c = warp * 16 + g;
@@ -1809,19 +1823,20 @@ cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, 
   a.E = static_cast<int>(p.E);
   a.cw = copy_width(C);
   a.rw = copy_width(p.R);
+  a.mw = std::min(a.rw, copy_width(p.M * p.R));
   a.bf16 = p.bf16;
   const int r16 = rank16(p.R);
   const int64_t col_tiles = ceil_div(C, kCols);
-  // whole waves of two CTAs per SM, of at most 12 tiles each; about half of
-  // the groups' last slots are taken to be empty
+  // whole waves of the CTAs that fit at once, of at most 12 tiles each; about
+  // half of the groups' last slots are taken to be empty
   const int64_t work = std::min<int64_t>(p.plan.slots, ceil_div(p.M, kTile) + (p.E + 1) / 2) * col_tiles;
-  const int64_t waves = ceil_div(work, 2 * sm_count() * 12);
-  a.col_tiles = static_cast<int>(ceil_div(work, 2 * sm_count() * waves));
-  const int smem = 1024 + expand_mid_bytes(r16) + 2 * expand_w_bytes(r16) +
-                   expand_tiles(r16) * static_cast<int>(kTileBytes);
+  const int64_t ctas = expand_per_sm(r16) * sm_count();
+  const int64_t waves = ceil_div(work, ctas * 12);
+  a.col_tiles = static_cast<int>(ceil_div(work, ctas * waves));
+  const int smem = expand_smem(r16);
   const dim3 grid(static_cast<unsigned>(p.plan.slots), static_cast<unsigned>(ceil_div(col_tiles, a.col_tiles)));
   const Copy copy = copy_of(p, C);
-  if (copy == kByTma && (!make_tmap(&a.tmMid, map_type(p), mid, p.R, p.M, p.R * 2, 64, 128, kSwz) ||
+  if (copy == kByTma && (!make_tmap(&a.tmMid, map_type(p), mid, p.R, 2 * p.M, p.R * 2, 64, 128, kSwz) ||
               !make_tmap(&a.tmAdd, map_type(p), addend != nullptr ? addend : out, C, p.M, C * 2, 64, 128, kSwz) ||
               !make_tmap(&a.tmOut, map_type(p), out, C, p.M, C * 2, 64, 128, kSwz) ||
               !(mn ? make_tmap_3d(&a.tmW, map_type(p), W, C, p.R, p.E, 2, 64, r16, kSwz)
