@@ -506,8 +506,9 @@ int i8lt_layer_norm_backward(const void* g, const void* x, int xt, int64_t M,
  *   u[m]  = scale[e] g[m] B[e]              gx[m] = addend[m] + u[m] A[e]
  *   gA[e] = sum over e's tokens u[m]^T x[m] gB[e] = scale[e] sum g[m]^T t[m]
  *   x [M, K], g, base, y [M, N], addend, gx [M, K], t [2, M, r] (rounded to
- *   dt, and what that rounding left: t is their sum; rows in the plan's
- *   order),
+ *   dt, and what that rounding left, in fp16 times 2^11: t is the first plus
+ *   the second, in fp16 2^-11 of it, to 2^-22 of t or to 2^-36; rows in the
+ *   plan's order),
  *   A and gA [E, r, K], B and gB [E, N, r]: all of dtype dt (I8LT_F16 or
  *   I8LT_BF16, the compute types of the 4-bit layers); index [M] int32;
  *   scale [E] fp32, or NULL (1).  1 <= r <= I8LT_MAX_RANK.

@@ -7,7 +7,10 @@
 // rounded once.  t and u are operands of a second 16-bit product.  They are
 // kept as two 16-bit values whose sum is t (u) to twice the type's precision,
 // and both take part in every output: a rounded t would be off by as much as
-// the output's own rounding.  Their rows are in the plan's order, so that
+// the output's own rounding.  In fp16 the second is kept times 2^11, and its
+// products in an accumulator of their own: as they are, both parts of a u of
+// 1e-6 (gradients are that small) would end at fp16's smallest number, 2^-24,
+// 3 % of it.  Their rows are in the plan's order, so that
 // the tokens of a tile are a box of consecutive rows whatever the batch's
 // order: 8192 interleaved tokens of 8 adapters, 4096 -> 11008, rank 64, took
 // 349 us forward and backward with t and u gathered by token, 290 us so.
@@ -240,10 +243,14 @@ __device__ __forceinline__ uint16_t to_16(float v, bool bf16) {
 __device__ __forceinline__ float from_16(uint16_t v, bool bf16) {
   return bf16 ? __uint_as_float(static_cast<uint32_t>(v) << 16) : __half2float(__ushort_as_half(v));
 }
-// What rounding v to hi left over, rounded (0 where hi overflowed).
+// The second part of v: what rounding it to hi left over (0 where hi
+// overflowed).  fp16: times 2^11, which 2^4, half the last place of the
+// largest numbers, allows; together they are off by 2^-22 of v or by 2^-36.
+// bf16 has fp32's range and needs no factor.
+constexpr float kRestUp = 0x1p11f, kRestDown = 0x1p-11f;
 __device__ __forceinline__ uint16_t rest_16(float v, uint16_t hi, bool bf16) {
-  const float h = from_16(hi, bf16);
-  return isfinite(h) ? to_16(v - h, bf16) : uint16_t(0);
+  const float rest = v - from_16(hi, bf16);
+  return !isfinite(from_16(hi, bf16)) ? uint16_t(0) : to_16(bf16 ? rest : rest * kRestUp, bf16);
 }
 
 template <int kBytes>
@@ -419,13 +426,23 @@ __host__ __device__ constexpr uint32_t tmem_columns(int r16) { return r16 <= 32 
 // up: 16-byte accesses of 8 rows hit 8 different bank groups.
 __host__ __device__ constexpr int red_pitch(int r16) { return r16 + 4; }
 
-// The CTA's accumulator (128 rows x r16) into shared memory.
-__device__ __forceinline__ void spill(uint32_t tmem, int r16, float* red) {
+// 16 columns of the second parts' products, added to those of the first ones.
+__device__ __forceinline__ void add_rest(uint32_t tmem, uint32_t* v) {
+  uint32_t w[16];
+  tmem_ld16(tmem, w);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(fmaf(__uint_as_float(w[i]), kRestDown, __uint_as_float(v[i])));
+}
+
+// The CTA's accumulator (128 rows x r16) into shared memory; rest > 0: with
+// that of the second parts, `rest` columns on.
+__device__ __forceinline__ void spill(uint32_t tmem, int r16, float* red, uint32_t rest = 0) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = (warp & 3) * 32 + lane;
   for (int c = (warp >> 2) * 16; c < r16; c += 32) {
     uint32_t v[16];
     tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c, v);
+    if (rest != 0) add_rest(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + rest + c, v);
     float4* p = reinterpret_cast<float4*>(red + row * red_pitch(r16) + c);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -458,7 +475,7 @@ struct ShrinkArgs {
   CUtensorMap tmX, tmW;   // with kTma: X, box 64 x 128; W, box 64 x r16 (K-major) or 64 x 64
   const uint16_t* X;      // [M, C]
   const uint16_t* W;      // per group [R, C] (K-major) or [C, R] (MN-major)
-  uint16_t* mid;          // [2, M, R] in the plan's order: the values, and what their rounding left
+  uint16_t* mid;          // [2, M, R] in the plan's order: the values rounded, and rest_16 of them
   int64_t plane;          // M R
   const float* scale;     // applied when not NULL
   const Tile* tiles;
@@ -666,7 +683,6 @@ struct ExpandArgs {
   int64_t C;
   int M, R, E, cw, rw, mw; // mw: the copy width of mid's second part
   int col_tiles;           // 64-column tiles per CTA
-  bool bf16;
 };
 
 constexpr int kCols = 64;                                  // columns per tile
@@ -697,7 +713,7 @@ static_assert(2 * (expand_smem(64) + 1024) <= 228 * 1024 && sizeof(ExpandSync) <
 // the products.  Bound by reading the addend and writing out: 8192 tokens of
 // 11008 features, rank 64, take 63 us, 5.7 TB/s.
 constexpr int kExpandThreads = 320;
-template <bool kMN, Copy kCopy>
+template <bool kMN, Copy kCopy, bool kBf16>
 __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_constant__ ExpandArgs a) {
   constexpr bool kTma = kCopy == kByTma;
   extern __shared__ __align__(1024) uint8_t expand_raw[];
@@ -741,22 +757,25 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
     y.abort = 0;
     fence_mbar_init();
   }
+  // accumulator j & 1; in fp16 the second part's products beside it
+  constexpr uint32_t rest = kBf16 ? 0 : kCols, acc = rest + kCols;
   if (warp == 0) {
-    tmem_alloc(&y.tmem, 128);
+    tmem_alloc(&y.tmem, 2 * acc);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
 
-  const uint32_t idesc = instruction(kCols, false, kMN, a.bf16);
+  const uint32_t idesc = instruction(kCols, false, kMN, kBf16);
   auto multiply = [&](int j) {   // one thread: accumulator j & 1 = mid W^T
+    const uint32_t d = y.tmem + (j & 1) * acc;
     const uint32_t ms = smem_u32(mids), ws = smem_u32(wbuf) + (j & 1) * expand_w_bytes(r16);
     for (int k = 0; k < r16 / 16; ++k) {
       const uint32_t m = ms + (k >> 2) * 128 * kRowBytes;
       const uint64_t w = kMN ? desc_mn(ws, k, 0) : desc_k(ws + (k >> 2) * 64 * kRowBytes, k & 3);
-      umma_f16(y.tmem + (j & 1) * kCols, desc_k(m, k & 3), w, idesc, k > 0 ? 1u : 0u);
-      umma_f16(y.tmem + (j & 1) * kCols, desc_k(m + expand_mid_bytes(r16), k & 3), w, idesc, 1u);
+      umma_f16(d, desc_k(m, k & 3), w, idesc, k > 0 ? 1u : 0u);
+      umma_f16(d + rest, desc_k(m + expand_mid_bytes(r16), k & 3), w, idesc, k > 0 || rest == 0 ? 1u : 0u);
     }
     umma_commit(&y.w_free[j & 1]);
     umma_commit(&y.acc_full[j & 1]);
@@ -767,7 +786,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float lo = __uint_as_float(v[2 * i]), hi = __uint_as_float(v[2 * i + 1]);
-      if (a.bf16) {
+      if constexpr (kBf16) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(fmaf(scale, lo, __uint_as_float(e[i] << 16)),
                                                        fmaf(scale, hi, __uint_as_float(e[i] & 0xffff0000u)));
         e[i] = *reinterpret_cast<const uint32_t*>(&h);
@@ -787,7 +806,12 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
       mbar_wait(&y.acc_full[j & 1], (j >> 1) & 1, &y.abort, a.st, 22);
       __syncwarp();
       tc_fence_after();
-      tmem_ld32(y.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (j & 1) * kCols + c0, v);
+      const uint32_t d = y.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (j & 1) * acc + c0;
+      tmem_ld32(d, v);
+      if constexpr (rest != 0) {
+        add_rest(d + rest, v);
+        add_rest(d + rest + 16, v + 16);
+      }
       tc_fence_before();
       mbar_arrive(&y.acc_free[j & 1]);
     } else {
@@ -1010,7 +1034,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
   grid_dependency_wait();   // what follows this kernel may rely on what came before it
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(y.tmem, 128);
+  if (warp == 0) tmem_dealloc(y.tmem, 2 * acc);
 }
 
 // ---- gradients of A and B ---------------------------------------------------
@@ -1078,7 +1102,8 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
   const int b0 = static_cast<int>(static_cast<int64_t>(nb) * rank / ranks);
   const int n = static_cast<int>(static_cast<int64_t>(nb) * (rank + 1) / ranks) - b0;
   const int chunks = r16 / 8;
-  sync_setup(y, tmem_columns(r16));
+  const uint32_t rest = a.bf16 ? 0u : tmem_columns(r16), columns = tmem_columns(r16) + rest;
+  sync_setup(y, columns);
 
   const int first = a.perm[start];
   const bool run = a.perm[start + tokens - 1] - first == tokens - 1;   // consecutive tokens
@@ -1090,7 +1115,8 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
     for (int k = 0; k < 4; ++k) {
       const uint64_t x = desc_mn(xs, k, 64 * kRowBytes);
       umma_f16(y.tmem, x, desc_mn(us, k, 64 * kRowBytes), idesc, it > 0 || k > 0 ? 1u : 0u);
-      umma_f16(y.tmem, x, desc_mn(us + grad_mid_bytes(r16), k, 64 * kRowBytes), idesc, 1u);
+      umma_f16(y.tmem + rest, x, desc_mn(us + grad_mid_bytes(r16), k, 64 * kRowBytes), idesc,
+               it > 0 || k > 0 || rest == 0 ? 1u : 0u);
     }
     umma_commit(&y.done[s]);
     if (it == n - 1) umma_commit(&y.last);
@@ -1224,11 +1250,11 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
     __syncwarp();
     tc_fence_after();
     __syncthreads();
-    spill(y.tmem, r16, red);
+    spill(y.tmem, r16, red, rest);
   } else {   // a group with fewer token blocks than CTAs
     for (int i = tid; i < 128 * red_pitch(r16); i += kThreads) red[i] = 0.f;
   }
-  sync_end(y, tmem_columns(r16));
+  sync_end(y, columns);
   grid_dependents_launch();
   cluster_sync();
   const int rows = (128 + ranks - 1) / ranks, row0 = rank * rows;
@@ -1291,9 +1317,12 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
     y.abort = 0;
     fence_mbar_init();
   }
-  const uint32_t columns = tmem_columns(r16);   // of one accumulator
+  // of one accumulator, with that of the second parts; two of them where two
+  // CTAs' fit
+  const uint32_t rest = a.bf16 ? 0u : tmem_columns(r16), columns = tmem_columns(r16) + rest;
+  const int more = columns <= 128 ? 1 : 0;   // accumulator acc & more, its use acc >> more
   if (warp == 0) {
-    tmem_alloc(&y.tmem, 2 * columns);
+    tmem_alloc(&y.tmem, columns << more);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -1429,8 +1458,8 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
     for (int64_t i = blockIdx.x; i < strips; i += step) {
       const Strip after = strip_of(i + step);
       const int n = (t.tokens + 63) / 64;
-      if (n > 0 && acc >= 2) {
-        mbar_wait(&y.acc_free[acc & 1], ((acc >> 1) - 1) & 1, &y.abort, a.st, 33);
+      if (n > 0 && acc > more) {
+        mbar_wait(&y.acc_free[acc & more], ((acc >> more) - 1) & 1, &y.abort, a.st, 33);
         tc_fence_after();
       }
       for (int it = 0; it < n; ++it, ++at) {
@@ -1448,15 +1477,16 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
         if (lane == 0) {
           tc_fence_after();
           const uint32_t x0 = smem_u32(us) - 2 * 64 * kRowBytes, u0 = smem_u32(us);
-          const uint32_t out = y.tmem + (acc & 1) * columns;
+          const uint32_t out = y.tmem + (acc & more) * columns;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint64_t x = desc_mn(x0, k, 64 * kRowBytes);
             umma_f16(out, x, desc_mn(u0, k, 64 * kRowBytes), idesc, it > 0 || k > 0 ? 1u : 0u);
-            umma_f16(out, x, desc_mn(u0 + grad_mid_bytes(r16), k, 64 * kRowBytes), idesc, 1u);
+            umma_f16(out + rest, x, desc_mn(u0 + grad_mid_bytes(r16), k, 64 * kRowBytes), idesc,
+                     it > 0 || k > 0 || rest == 0 ? 1u : 0u);
           }
           umma_commit(&y.done[s]);
-          if (it == n - 1) umma_commit(&y.acc_full[acc & 1]);
+          if (it == n - 1) umma_commit(&y.acc_full[acc & more]);
         }
         __syncwarp();
       }
@@ -1473,7 +1503,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
       uint16_t* grad = d.grad + t.e * R * C;
       const float scale = d.scale != nullptr ? d.scale[t.e] : 1.f;
       if (t.tokens > 0) {
-        mbar_wait(&y.acc_full[acc & 1], (acc >> 1) & 1, &y.abort, a.st, 24);
+        mbar_wait(&y.acc_full[acc & more], (acc >> more) & 1, &y.abort, a.st, 24);
         __syncwarp();
         tc_fence_after();
       }
@@ -1481,7 +1511,9 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
         uint32_t v[16];
         __syncwarp();
         if (t.tokens > 0) {
-          tmem_ld16(y.tmem + (static_cast<uint32_t>(warp * 32) << 16) + (acc & 1) * columns + j, v);
+          const uint32_t d = y.tmem + (static_cast<uint32_t>(warp * 32) << 16) + (acc & more) * columns + j;
+          tmem_ld16(d, v);
+          if (rest != 0) add_rest(d + rest, v);
         } else {
 #pragma unroll
           for (int k = 0; k < 16; ++k) v[k] = 0u;
@@ -1506,7 +1538,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
       if (t.tokens > 0) {
         __syncwarp();
         tc_fence_before();
-        mbar_arrive(&y.acc_free[acc & 1]);
+        mbar_arrive(&y.acc_free[acc & more]);
         ++acc;
       }
       t = after;
@@ -1516,7 +1548,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
   grid_dependents_launch();
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(y.tmem, 2 * columns);
+  if (warp == 0) tmem_dealloc(y.tmem, columns << more);
   // what follows this kernel may rely on what came before it
   grid_dependency_wait();
 }
@@ -1657,7 +1689,7 @@ __global__ void __launch_bounds__(kThreads, kMaxRankTiles > 4 ? 2 : kMaxRankTile
     uint2 base = make_uint2(0, 0);
     if (out && a.base != nullptr) base = *reinterpret_cast<const uint2*>(a.base + m * N + col);
     if (adapter) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      float d[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f};   // r: of t's second part in fp16
       const int64_t c0 = s * 128 + warp * 16 + g, c1 = c0 + 8;
       const uint2 zero = make_uint2(0, 0);
 #pragma unroll 4
@@ -1666,9 +1698,21 @@ __global__ void __launch_bounds__(kThreads, kMaxRankTiles > 4 ? 2 : kMaxRankTile
         const bool in = k < R;
         const uint2 u = in && c0 < N ? __ldg(reinterpret_cast<const uint2*>(B + c0 * R + k)) : zero;
         const uint2 v = in && c1 < N ? __ldg(reinterpret_cast<const uint2*>(B + c1 * R + k)) : zero;
-        mma_16x8<kBf16>(d, u, v, in ? *reinterpret_cast<const uint2*>(&ts[0][g][k]) : zero);
-        mma_16x8<kBf16>(d, u, v, in ? *reinterpret_cast<const uint2*>(&ts[1][g][k]) : zero);
+        const uint2 hi = in ? *reinterpret_cast<const uint2*>(&ts[0][g][k]) : zero;
+        const uint2 lo = in ? *reinterpret_cast<const uint2*>(&ts[1][g][k]) : zero;
+        if constexpr (!kBf16 && kMaxRankTiles == 1) {   // one accumulator, scaled in between, spares registers
+          mma_16x8<kBf16>(d, u, v, lo);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) d[n] *= kRestDown;
+          mma_16x8<kBf16>(d, u, v, hi);
+        } else {
+          mma_16x8<kBf16>(d, u, v, hi);
+          mma_16x8<kBf16>(kBf16 ? d : r, u, v, lo);
+        }
       }
+      if constexpr (!kBf16 && kMaxRankTiles > 1)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) d[n] = fmaf(r[n], kRestDown, d[n]);
       float(*buf)[128 + 4] = ys[s & 1];
       const int c = warp * 16 + g;
       buf[2 * q][c] = d[0];
@@ -1767,6 +1811,13 @@ template <bool kMN, Copy kCopy>
 auto shrink_of(int stages) {
   return stages == 4 ? shrink_kernel<kMN, 4, kCopy> : shrink_kernel<kMN, 3, kCopy>;
 }
+template <bool kBf16>
+auto expand_of(bool mn, Copy copy) {
+  return copy == kByTma     ? (mn ? expand_kernel<true, kByTma, kBf16> : expand_kernel<false, kByTma, kBf16>)
+         : copy == kByAsync ? (mn ? expand_kernel<true, kByAsync, kBf16> : expand_kernel<false, kByAsync, kBf16>)
+         : mn               ? expand_kernel<true, kByRegisters, kBf16>
+                            : expand_kernel<false, kByRegisters, kBf16>;
+}
 template <Copy kCopy>
 auto grad_of(int stages) {
   return stages == 3 ? grad_kernel<3, kCopy> : grad_kernel<2, kCopy>;
@@ -1824,7 +1875,6 @@ cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, 
   a.cw = copy_width(C);
   a.rw = copy_width(p.R);
   a.mw = std::min(a.rw, copy_width(p.M * p.R));
-  a.bf16 = p.bf16;
   const int r16 = rank16(p.R);
   const int64_t col_tiles = ceil_div(C, kCols);
   // whole waves of the CTAs that fit at once, of at most 12 tiles each; about
@@ -1842,9 +1892,7 @@ cudaError_t expand(const Problem& p, const void* mid, const void* W, int64_t C, 
               !(mn ? make_tmap_3d(&a.tmW, map_type(p), W, C, p.R, p.E, 2, 64, r16, kSwz)
                    : make_tmap_3d(&a.tmW, map_type(p), W, p.R, C, p.E, 2, 64, 64, kSwz))))
     return cudaErrorUnknown;
-  auto kernel = copy == kByTma     ? (mn ? expand_kernel<true, kByTma> : expand_kernel<false, kByTma>)
-                : copy == kByAsync ? (mn ? expand_kernel<true, kByAsync> : expand_kernel<false, kByAsync>)
-                                   : (mn ? expand_kernel<true, kByRegisters> : expand_kernel<false, kByRegisters>);
+  auto kernel = p.bf16 ? expand_of<true>(mn, copy) : expand_of<false>(mn, copy);
   return launch(kernel, a, grid, kExpandThreads, 1, smem, K_ADAPTERS, true, p.s);
 }
 

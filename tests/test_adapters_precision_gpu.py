@@ -98,3 +98,24 @@ SIZES = [(64, 512, 640, 16, 8), (200, 256, 384, 64, 2), (256, 256, 256, 128, 1),
 @pytest.mark.parametrize("M,K,N,r,E", SIZES)
 def test_outputs_are_off_by_their_last_rounding(M, K, N, r, E, dt):
     _check(_data(M, K, N, r, E, dt, M + r))
+
+
+# Second factors and gradients so small that t and u fall to fp16's smallest
+# numbers (2^-24 = 6e-8): the outputs sum thousands of them, or multiply them
+# by large values, and are well inside the type's range.
+@pytest.mark.parametrize("u", [1e-4, 1e-5, 1e-6, 1e-7])
+@pytest.mark.parametrize("M,K,N,r,E", [(4096, 256, 512, 64, 1), (4000, 320, 512, 16, 3), (3000, 256, 384, 128, 2),
+                                       (2000, 520, 256, 64, 24), (2000, 258, 514, 10, 2), (1000, 257, 511, 7, 2)])
+def test_small_u_in_fp16(M, K, N, r, E, u):
+    """u = s g B of about `u` gives gA and gx."""
+    d = _data(M, K, N, r, E, F16, r, A=4.0, B=1e-3, g=u / (1e-3 * N ** 0.5))
+    _check(d, ("gA", "gx"))
+
+
+@pytest.mark.parametrize("t", [1e-4, 1e-5, 1e-6])
+@pytest.mark.parametrize("M,K,N,r,E", [(100, 256, 512, 64, 4), (1500, 320, 512, 16, 3), (900, 256, 384, 128, 2),
+                                       (600, 258, 514, 10, 2), (600, 257, 511, 7, 2)])
+def test_small_t_in_fp16(M, K, N, r, E, t):
+    """t = x A of about `t` gives y and gB."""
+    d = _data(M, K, N, r, E, F16, r, x=1e-2, A=100 * t * K ** -0.5, B=50.0, g=50.0)
+    _check(d, ("y", "gB"))
