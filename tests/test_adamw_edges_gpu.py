@@ -1,0 +1,102 @@
+"""AdamW at the edges of its numbers and of its lists of tensors.
+
+Values are compared with the same single fp32 operations in torch on the CPU
+(states: equal; a NaN equals a NaN) and parameters with the 64-bit formula on
+these states, within 8 * 2^-24 of the update and of the parameter."""
+import math
+
+import pytest
+import torch
+
+import int8_quantized_linear_i8lt_gb300 as I
+from int8_quantized_linear_i8lt_gb300.build import build
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF16, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+HYPER = dict(lr=3e-3, beta1=0.9, beta2=0.99, eps=1e-8, weight_decay=0.1)
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build()
+
+
+def _states(n, bits):
+    if bits == 32:
+        return torch.zeros(n, device=DEV), torch.zeros(n, device=DEV)
+    q = [torch.zeros(n, dtype=torch.uint8, device=DEV).view(F8) for _ in range(2)]
+    top = [torch.zeros(n // 256, device=DEV) for _ in range(2)]
+    return q[0], top[0], q[1], top[1]
+
+
+def _call(bits):
+    return I.adamw_step_8bit if bits == 8 else I.adamw_step
+
+
+def _moments(m, v, g):
+    b1, b2 = torch.tensor(HYPER["beta1"]), torch.tensor(HYPER["beta2"])
+    c1, c2 = torch.tensor(1 - HYPER["beta1"]), torch.tensor(1 - HYPER["beta2"])
+    return m * b1 + g * c1, v * b2 + (g * g) * c2
+
+
+def _decode(q, top):
+    return (q.cpu().view(-1, 256).float() * (top.cpu() * torch.tensor(1.0 / 448.0))[:, None]).view(-1)
+
+
+def _param64(p, m, r, step):
+    upd = HYPER["lr"] / (1 - HYPER["beta1"] ** step) * m.double() / \
+        (r.double() / math.sqrt(1 - HYPER["beta2"] ** step) + HYPER["eps"])
+    return p.double() * (1 - HYPER["lr"] * HYPER["weight_decay"]) - upd, upd
+
+
+def _grad(n, seed, std=1e-2):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return torch.randn(n, generator=g, device=DEV) * std
+
+
+@pytest.mark.parametrize("gt", [F32, BF16])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_gradient_whose_square_overflows(bits, gt):
+    """v is then infinite and the update zero: the parameter decays only,
+    whatever its neighbours' gradients are."""
+    n = 256 * 4
+    g = _grad(n, 1)
+    g[256:512] = 0.0                                # neighbours without a gradient
+    g[5], g[256 + 77], g[512] = 3e19, -2e30, 2e19
+    g = g.to(gt)
+    p = _grad(n, 2, 0.1)
+    before = p.cpu().clone()
+    st = _states(n, bits)
+    _call(bits)([p], [g], *st, step=1, **HYPER)
+    m, v = _moments(torch.zeros(n), torch.zeros(n), g.cpu().float())
+    assert v.isinf().sum() == 3
+    want, upd = _param64(before, m, v.sqrt(), 1)
+    assert ((p.cpu().double() - want).abs() <= 8 * 2.0 ** -24 * (upd.abs() + before.double().abs())).all()
+    if bits == 32:
+        assert torch.equal(st[0].cpu(), m) and torch.equal(st[1].cpu(), v)
+    else:
+        top = v.sqrt().view(-1, 256).amax(1)
+        assert torch.equal(st[3].cpu(), top) and torch.equal(st[1].cpu(), m.abs().view(-1, 256).amax(1))
+        r = _decode(st[2], st[3]).view(-1, 256)
+        assert not r[top.isinf()].isfinite().any() and r[top.isfinite()].isfinite().all()
+
+
+def test_roots_over_their_whole_range():
+    """r's absmax is the rounded root of v: blocks whose second moments span
+    every octave, subnormal numbers among them, and every significand of two
+    octaves in steps of 2^-13."""
+    v = torch.cat([2.0 ** torch.arange(-149, 127, 0.25, dtype=torch.double).float(),
+                   1 + torch.arange(0, 3 * 2 ** 13).double().mul(2.0 ** -13).float(),
+                   torch.nextafter(2.0 ** torch.arange(-140, 127).float(), torch.tensor(0.0)),
+                   torch.nextafter(2.0 ** torch.arange(-140, 127).float(), torch.tensor(1e38))])
+    # one value per block: g with c2 = 1 - 0 = 1 and v = g * g
+    g = v.sqrt()
+    n = 256 * len(g)
+    grad = torch.zeros(n, device=DEV)
+    grad[::256] = g.to(DEV)
+    st = _states(n, 8)
+    I.adamw_step_8bit([torch.zeros(n, device=DEV)], [grad], *st, step=1, lr=1e-3, beta1=0.9, beta2=0.0)
+    assert torch.equal(st[3].cpu(), (g * g).sqrt())
