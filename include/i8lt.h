@@ -573,8 +573,8 @@ int i8lt_adapters_backward(const void* g, const void* x, const void* t, int dt,
  *            they are rounded.
  * State arithmetic is single IEEE fp32 operations in the order above (r is
  * squared to give v), so the states' bits follow from the formulas.
- * Non-finite gradients make the states of their block non-finite; skip such
- * a step with found_inf.
+ * A gradient that is not finite makes its states non-finite, in 8 bits those
+ * of its whole block (the absmax is); skip such a step with found_inf.
  */
 #define I8LT_ADAMW_BLOCK 256
 int i8lt_adamw_step(void* const* params, int pt, const void* const* grads,

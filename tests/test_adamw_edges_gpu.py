@@ -100,3 +100,45 @@ def test_roots_over_their_whole_range():
     st = _states(n, 8)
     I.adamw_step_8bit([torch.zeros(n, device=DEV)], [grad], *st, step=1, lr=1e-3, beta1=0.9, beta2=0.0)
     assert torch.equal(st[3].cpu(), (g * g).sqrt())
+
+
+@pytest.mark.parametrize("gt", [F32, BF16])
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("rest", [1e-2, 0.0])
+def test_a_non_finite_gradient_makes_its_block_non_finite(rest, bad, gt):
+    """8 bits: all 256 values of both moments; other blocks keep theirs."""
+    n = 256 * 3
+    g = _grad(n, 3, rest)
+    g[256 + 100] = bad
+    g = g.to(gt)
+    st = _states(n, 8)
+    p = _grad(n, 4, 0.1)
+    clean = [t.clone() for t in st]
+    I.adamw_step_8bit([p], [g], *st, step=1, **HYPER)
+    hit = torch.zeros(n, dtype=torch.bool)
+    hit[256:512] = True
+    for q, top in ((st[0], st[1]), (st[2], st[3])):
+        value = _decode(q, top)
+        assert not value[hit].isfinite().any() and value[~hit].isfinite().all()
+        assert not top[1].isfinite()
+    assert not p[356].isfinite() and p[:256].isfinite().all() and p[512:].isfinite().all()
+    alone, q = _grad(n, 4, 0.1), clean
+    g[256 + 100] = 0.0
+    I.adamw_step_8bit([alone], [g], *q, step=1, **HYPER)
+    for a, b in zip(st, q):
+        assert torch.equal(a.view(torch.uint8).view(3, -1)[::2], b.view(torch.uint8).view(3, -1)[::2])
+    keep = torch.arange(n, device=DEV) != 356
+    assert torch.equal(p[keep], alone[keep])
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_a_non_finite_gradient_in_32_bits(bad):
+    """32 bits: the moments of that element."""
+    n = 600
+    g = _grad(n, 3)
+    g[300] = bad
+    st = _states(I.adamw_state_size([g]), 32)
+    p = _grad(n, 4, 0.1)
+    I.adamw_step([p], [g], *st, step=1, **HYPER)
+    for t in (*st, p):
+        assert not t[300].isfinite() and t[:300].isfinite().all() and t[301:].isfinite().all()
