@@ -294,11 +294,13 @@ __global__ void __launch_bounds__(kWarps * 32, 4) adamw8_kernel(const __grid_con
       if (scaled)
 #pragma unroll
         for (int k = 0; k < 8; ++k) gv[k] = __fmul_rn(gv[k], gs);
+      const int valid = whole ? 8 : min(rest - i * kBlockElems, 8);
       float low = INFINITY, mtop = 0.f, vtop = 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         v[k] = __fmul_rn(v[k], v[k]);
         moments(h, gv[k], m[k], v[k]);
+        if (!whole && k >= valid) m[k] = v[k] = 0.f;   // past the tensor's end, whatever its codes were
         low = fminf(low, v[k]);
         mtop = max_or_nan(mtop, fabsf(m[k]));
       }
@@ -309,7 +311,6 @@ __global__ void __launch_bounds__(kWarps * 32, 4) adamw8_kernel(const __grid_con
         vtop = max_or_nan(vtop, v[k]);
         pv[k] = updated(h, pv[k], m[k], v[k]);
       }
-      const int valid = whole ? 8 : min(rest - i * kBlockElems, 8);
       store_run<P, 8>(p + i * kBlockElems, whole || (pa && valid == 8), valid, pv);
       mtop = warp_max(mtop);
       vtop = warp_max(vtop);

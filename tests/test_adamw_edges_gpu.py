@@ -142,3 +142,28 @@ def test_a_non_finite_gradient_in_32_bits(bad):
     I.adamw_step([p], [g], *st, step=1, **HYPER)
     for t in (*st, p):
         assert not t[300].isfinite() and t[:300].isfinite().all() and t[301:].isfinite().all()
+
+
+@pytest.mark.parametrize("odd", [False, True])
+def test_what_lies_past_a_tensors_end_is_not_used(odd):
+    """8 bits: codes there enter neither the block's absmax nor its codes, and
+    are 0 afterwards."""
+    sizes = [300, 1, 513]
+    ps = [_grad(n + 1, n, 0.1)[1:] if odd else _grad(n, n, 0.1) for n in sizes]
+    gs = [_grad(n, n + 1) for n in sizes]
+    total = I.adamw_state_size(ps)
+    inside = torch.zeros(total, dtype=torch.bool, device=DEV)
+    for at, n in zip((0, 512, 768), sizes):
+        inside[at:at + n] = True
+    clean, dirty = _states(total, 8), _states(total, 8)
+    for st in (clean, dirty):
+        for top in (st[1], st[3]):
+            top.fill_(1e-2)
+    for k in (0, 2):
+        dirty[k].view(torch.uint8).masked_fill_(~inside, 0x7e)      # 448
+    qs = [p.clone() for p in ps]
+    for st, params in ((clean, ps), (dirty, qs)):
+        I.adamw_step_8bit(params, gs, *st, step=2, **HYPER)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(clean, dirty))
+    assert all(torch.equal(a, b) for a, b in zip(ps, qs))
+    assert not dirty[0].view(torch.uint8)[~inside].any() and not dirty[2].view(torch.uint8)[~inside].any()
