@@ -842,7 +842,7 @@ class AdaptersFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, base, A, B, scale, plan):
         x2 = x.reshape(-1, x.shape[-1])
-        b2 = None if base is None else base.reshape(x2.shape[0], -1)
+        b2 = None if base is None else base.reshape(x2.shape[0], base.shape[-1])
         y, t = adapters_forward(x2, A, B, scale, plan, base=b2)
         ctx.save_for_backward(x2, t, A, B, scale)
         ctx.plan, ctx.x_shape = plan, x.shape
@@ -854,7 +854,7 @@ class AdaptersFunction(torch.autograd.Function):
         need = ctx.needs_input_grad
         gx = gA = gB = None
         if need[0] or need[2] or need[3]:
-            gx, gA, gB = adapters_backward(gy.reshape(x2.shape[0], -1), x2, t, A, B, scale, ctx.plan, need_x=need[0],
+            gx, gA, gB = adapters_backward(gy.reshape(x2.shape[0], gy.shape[-1]), x2, t, A, B, scale, ctx.plan, need_x=need[0],
                                            need_A=need[2], need_B=need[3])
         if gx is not None:
             gx = gx.reshape(ctx.x_shape)
