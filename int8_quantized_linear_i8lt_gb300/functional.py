@@ -618,11 +618,17 @@ NF4LinearFunction = Linear4bitFunction
 # fine-tuning on top of the frozen layers: layer norm, low-rank adapters, AdamW
 # ---------------------------------------------------------------------------
 
-def _arg(what: str, t, dev: int, shape, dtype):
-    """An optional argument after its checks, contiguous: on CUDA device
-    ``dev``, of ``shape`` and of ``dtype`` (None: any)."""
-    if t is None:
-        return None
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """t, or a copy of it that is contiguous and starts on 16 bytes, as the
+    library wants it: views need not (x[1:] of odd rows, the parts of a
+    gradient that torch.cat's backward hands on)."""
+    if not t.is_contiguous():
+        return t.contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
+
+
+def _checked(what: str, t: torch.Tensor, dev: int, shape, dtype) -> torch.Tensor:
+    """t, on CUDA device ``dev``, of ``shape`` and of ``dtype`` (None: any)."""
     if t.get_device() != dev:
         raise I8LTError(f"{what}: a tensor on {t.device}, expected cuda:{dev}" if t.is_cuda else
                         "libi8lt runs on CUDA tensors only (no CPU path)")
@@ -630,14 +636,20 @@ def _arg(what: str, t, dev: int, shape, dtype):
         raise I8LTError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype is not dtype:
         raise I8LTError(f"{what}: dtype {t.dtype}, expected {dtype}")
-    return t if t.is_contiguous() else t.contiguous()
+    return t
+
+
+def _arg(what: str, t, dev: int, shape, dtype):
+    """An optional input after its checks, as the library wants it."""
+    return None if t is None else _aligned(_checked(what, t, dev, shape, dtype))
 
 
 def _out(what: str, t: torch.Tensor, dev: int, shape, dtype):
-    """A caller's output buffer after its checks."""
+    """A caller's output buffer after its checks (the library refuses one that
+    does not start on 16 bytes)."""
     if not t.is_contiguous():
         raise I8LTError(f"{what}: not contiguous")
-    return _arg(what, t, dev, shape, dtype)
+    return _checked(what, t, dev, shape, dtype)
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
@@ -651,8 +663,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     if not shape:
         raise I8LTError("layer_norm: x has no dimension to normalise")
     dev, dtype, N = x.get_device(), x.dtype, shape[-1]
-    if not x.is_contiguous():
-        x = x.contiguous()
+    x = _aligned(x)
     weight = _arg("layer_norm weight", weight, dev, (N,), None)
     par = weight if weight is not None else bias
     bias = _arg("layer_norm bias", bias, dev, (N,), None if par is None else par.dtype)
@@ -673,8 +684,7 @@ def layer_norm_backward(g: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rs
     _require_cuda(x)
     shape = x.shape
     dev, dtype, N = x.get_device(), x.dtype, shape[-1]
-    if not x.is_contiguous():
-        x = x.contiguous()
+    x = _aligned(x)
     g = _arg("layer_norm_backward g", g, dev, shape, dtype)
     mean = _arg("layer_norm_backward mean", mean, dev, shape[:-1], torch.float32)
     rstd = _arg("layer_norm_backward rstd", rstd, dev, shape[:-1], torch.float32)

@@ -55,3 +55,69 @@ def test_a_batch_without_tokens(shape):
     norm = I.LayerNorm(48, device=DEV)
     norm(x).backward(torch.empty_like(x))
     assert norm.weight.grad.shape == (48,) and not norm.weight.grad.any() and not norm.bias.grad.any()
+
+
+def _off(t, by=1):
+    """The same values, contiguous, `by` elements off a 16-byte boundary."""
+    flat = torch.empty(t.numel() + by, dtype=t.dtype, device=t.device)
+    v = flat[by:].view(t.shape)
+    v.copy_(t)
+    assert v.is_contiguous() and v.data_ptr() % 16 != 0
+    return v
+
+
+@pytest.mark.parametrize("dt", [F16, BF16, F32])
+@pytest.mark.parametrize("N", [64, 4099])
+def test_layer_norm_on_views(N, dt):
+    x, g, w, b = _normal(9, N, seed=1, dt=dt), _normal(9, N, seed=2, dt=dt), _normal(N, seed=3, dt=dt), _normal(N, seed=4, dt=dt)
+    ref = I.layer_norm(x, w, b)
+    got = I.layer_norm(_off(x), _off(w), _off(b, 3))
+    assert all(torch.equal(p, q) for p, q in zip(got, ref))
+    back = I.layer_norm_backward(g, x, ref[1], ref[2], w)
+    got = I.layer_norm_backward(_off(g), _off(x), _off(ref[1]), _off(ref[2]), _off(w))
+    assert all(torch.equal(p, q) for p, q in zip(got, back))
+    # what torch.cat's and narrow's backward hand on: parts of one gradient
+    norm = I.LayerNorm(N, device=DEV, dtype=dt)
+    parts = [x[:3].clone().requires_grad_(True), x[3:].clone().requires_grad_(True)]
+    torch.cat([norm(p) for p in parts]).backward(g)
+    for p, gy in zip(parts, (g[:3].clone(), g[3:].clone())):
+        alone = p.detach().clone().requires_grad_(True)
+        norm(alone).backward(gy)
+        assert torch.equal(p.grad, alone.grad)
+    with pytest.raises(I.I8LTError):                # a caller's output is not copied
+        I.layer_norm(x, w, b, out=_off(x))
+
+
+@pytest.mark.parametrize("K,N,r", [(64, 128, 8), (515, 257, 5)])
+@pytest.mark.parametrize("M", [40, 700])
+def test_adapters_on_views(M, K, N, r):
+    E = 3
+    A, B, scale = _normal(E, r, K, seed=1), _normal(E, N, r, seed=2), torch.rand(E, device=DEV)
+    x, base, g, addend = (_normal(M, c, seed=s) for c, s in ((K, 3), (N, 4), (N, 5), (K, 6)))
+    index = (torch.arange(M, device=DEV) * 7 % (E + 1) - 1).int()
+    plan, plan2 = I.adapter_plan(index, E), I.adapter_plan(_off(index), E)
+    y, t = I.adapters_forward(x, A, B, scale, plan, base=base)
+    y2, t2 = I.adapters_forward(_off(x), _off(A), _off(B), _off(scale), plan2, base=_off(base))
+    assert torch.equal(y, y2) and torch.equal(t, t2)
+    ref = I.adapters_backward(g, x, t, A, B, scale, plan, addend=addend)
+    got = I.adapters_backward(_off(g), _off(x), _off(t), _off(A), _off(B), scale, plan, addend=_off(addend))
+    assert all(torch.equal(p, q) for p, q in zip(got, ref))
+    ad = _layer(K, N, r, E)
+    cut = M // 2 + 1
+    parts = [x[:cut].clone().requires_grad_(True), x[cut:].clone().requires_grad_(True)]
+    ys = [ad(p, I.adapter_plan(i, E)) for p, i in zip(parts, (index[:cut], index[cut:]))]
+    torch.cat(ys).backward(g)
+    for p, i, gy in zip(parts, (index[:cut], index[cut:]), (g[:cut].clone(), g[cut:].clone())):
+        alone = p.detach().clone().requires_grad_(True)
+        ad(alone, I.adapter_plan(i.clone(), E)).backward(gy)
+        assert torch.equal(p.grad, alone.grad)
+    with pytest.raises(I.I8LTError):
+        I.adapters_forward(x, A, B, scale, plan, base=base, out=_off(base))
+
+
+def test_adamw_on_gradients_of_any_offset():
+    p, q, g = _normal(300, dt=F32), _normal(300, dt=F32), _normal(300, seed=1, dt=F32)
+    m, v, m2, v2 = (torch.zeros(512, device=DEV) for _ in range(4))
+    I.adamw_step([p], [g], m, v, step=1, lr=1e-2)
+    I.adamw_step([q], [_off(g)], m2, v2, step=1, lr=1e-2)
+    assert torch.equal(p, q) and torch.equal(m, m2) and torch.equal(v, v2)
