@@ -652,6 +652,11 @@ def _out(what: str, t: torch.Tensor, dev: int, shape, dtype):
     return _checked(what, t, dev, shape, dtype)
 
 
+# Tells autograd that tensors were written in place: a backward pass that
+# still needs what they held then raises instead of using what they hold now.
+_written = torch.autograd.graph.increment_version
+
+
 def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                eps: float = 1e-5, out: torch.Tensor | None = None):
     """(y, mean, rstd) of the layer norm over the last dimension of x [..., N]
@@ -673,6 +678,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     _check(_lib.i8lt_layer_norm_forward(x.data_ptr(), _code(dtype), mean.numel(), N, _ptr(weight), _ptr(bias),
                                         0 if par is None else _code(par.dtype), eps, y.data_ptr(), mean.data_ptr(),
                                         rstd.data_ptr(), _stream(x)), "i8lt_layer_norm_forward")
+    if out is not None:
+        _written(out)
     return y, mean, rstd
 
 
@@ -810,6 +817,8 @@ def adapters_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: t
     _check(_lib.i8lt_adapters_forward(x.data_ptr(), _code(dtype), M, K, A.data_ptr(), B.data_ptr(), E, r, N,
                                       _ptr(scale), plan.data.data_ptr(), _ptr(base), y.data_ptr(), t.data_ptr(),
                                       ws.data_ptr(), ws.numel(), _stream(x)), "i8lt_adapters_forward")
+    if out is not None:
+        _written(out)
     return y, t
 
 
@@ -883,8 +892,9 @@ _is_contiguous, _numel, _dtype_of = torch.Tensor.is_contiguous, torch.Tensor.num
 
 
 def _adamw_lists(what, params, grads):
-    """(a parameter, what must outlive the call, count, addresses of the lists
-    of device addresses and sizes, dtypes, elements of a state), checked.
+    """(the parameters with a gradient, what must outlive the call, count,
+    addresses of the lists of device addresses and sizes, dtypes, elements of a
+    state), checked.
     Called for hundreds of tensors per step: each property is read in one
     sweep, and the lists are plain arrays (128 tensors: 90 us; 119 us with
     ctypes arrays, which convert element by element)."""
@@ -916,7 +926,7 @@ def _adamw_lists(what, params, grads):
     addresses = map(_data_ptr, held) if present[1] is grads else [0 if g is None else g.data_ptr() for g in held]
     lists = array.array("Q", map(_data_ptr, params)), array.array("Q", addresses), array.array("q", sizes)
     at = [a.buffer_info()[0] for a in lists]
-    return p0, (held, lists), n, *at, _code(p0.dtype), _code(g0.dtype), total
+    return present[0], (held, lists), n, *at, _code(p0.dtype), _code(g0.dtype), total
 
 
 def _adamw_state(what, size, dtype, device, *ts):
@@ -942,12 +952,14 @@ def adamw_step(params, grads, m: torch.Tensor, v: torch.Tensor, step: int, lr: f
     lists = _adamw_lists("adamw_step", params, grads)
     if lists is None:
         return
-    p0, held, n, pp, gp, sizes, pt, gt, size = lists
+    changed, held, n, pp, gp, sizes, pt, gt, size = lists
+    p0 = changed[0]
     _adamw_state("adamw_step", size, torch.float32, p0.device, m, v)
     _adamw_scalar("adamw_step", grad_scale, p0.device)
     _adamw_scalar("adamw_step", found_inf, p0.device)
     _check(_lib.i8lt_adamw_step(pp, pt, gp, gt, sizes, n, m.data_ptr(), v.data_ptr(), step, lr, beta1, beta2, eps,
                                 weight_decay, _ptr(grad_scale), _ptr(found_inf), _stream(p0)), "i8lt_adamw_step")
+    _written((*changed, m, v))
 
 
 def adamw_step_8bit(params, grads, m: torch.Tensor, m_absmax: torch.Tensor, r: torch.Tensor, r_absmax: torch.Tensor,
@@ -960,7 +972,8 @@ def adamw_step_8bit(params, grads, m: torch.Tensor, m_absmax: torch.Tensor, r: t
     lists = _adamw_lists("adamw_step_8bit", params, grads)
     if lists is None:
         return
-    p0, held, n, pp, gp, sizes, pt, gt, size = lists
+    changed, held, n, pp, gp, sizes, pt, gt, size = lists
+    p0 = changed[0]
     _adamw_state("adamw_step_8bit", size, torch.float8_e4m3fn, p0.device, m, r)
     _adamw_state("adamw_step_8bit", size // _lib.I8LT_ADAMW_BLOCK, torch.float32, p0.device, m_absmax, r_absmax)
     _adamw_scalar("adamw_step_8bit", grad_scale, p0.device)
@@ -968,3 +981,4 @@ def adamw_step_8bit(params, grads, m: torch.Tensor, m_absmax: torch.Tensor, r: t
     _check(_lib.i8lt_adamw_step_8bit(pp, pt, gp, gt, sizes, n, m.data_ptr(), m_absmax.data_ptr(), r.data_ptr(),
                                      r_absmax.data_ptr(), step, lr, beta1, beta2, eps, weight_decay, _ptr(grad_scale),
                                      _ptr(found_inf), _stream(p0)), "i8lt_adamw_step_8bit")
+    _written((*changed, m, m_absmax, r, r_absmax))

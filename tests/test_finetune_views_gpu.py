@@ -121,3 +121,53 @@ def test_adamw_on_gradients_of_any_offset():
     I.adamw_step([p], [g], m, v, step=1, lr=1e-2)
     I.adamw_step([q], [_off(g)], m2, v2, step=1, lr=1e-2)
     assert torch.equal(p, q) and torch.equal(m, m2) and torch.equal(v, v2)
+
+
+def test_changes_in_place_are_reported():
+    """What a backward pass still needs may not change under it unnoticed."""
+    x, w = _normal(6, 64, dt=F32), _normal(64, seed=1, dt=F32)
+
+    def stale(change):
+        p = w.clone().requires_grad_(True)
+        h = _normal(6, 64, seed=2, dt=F32).requires_grad_(True)
+        y = (h * p).sum()                           # keeps p
+        change(p)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+
+    z = lambda *s: torch.zeros(*s, device=DEV)      # noqa: E731
+    codes = lambda: torch.zeros(256, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)   # noqa: E731
+    stale(lambda p: I.adamw_step([p], [w], z(256), z(256), step=1, lr=1e-2))
+    stale(lambda p: I.adamw_step_8bit([p], [w], codes(), z(1), codes(), z(1), step=1, lr=1e-2))
+
+    def by_optimizer(p):
+        opt = I.AdamW([p], lr=1e-2)
+        p.grad = w.clone()
+        opt.step()
+
+    stale(by_optimizer)
+    # outputs that a caller gives
+    a = torch.ones(6, 64, device=DEV)
+    p = w.clone().requires_grad_(True)
+    y = (a * p).sum()
+    I.layer_norm(x, out=a)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    a = torch.ones(6, 64, device=DEV, dtype=F16)
+    p = w.half().requires_grad_(True)
+    y = (a * p).sum()
+    I.adapters_forward(x.half(), _normal(1, 4, 64, dt=F16), _normal(1, 64, 4, dt=F16), None,
+                       I.adapter_plan(None, 1, 6, DEV), base=a, out=a)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+
+
+def test_a_step_between_a_forward_and_its_backward():
+    ad = _layer(64, 48, 8, 1)
+    opt = I.AdamW([ad.A, ad.B], lr=1e-2)
+    x = _normal(20, 64, seed=3).requires_grad_(True)
+    y = ad(x)
+    y.sum().backward(retain_graph=True)
+    opt.step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
