@@ -856,7 +856,8 @@ def adapters_backward(g: torch.Tensor, x: torch.Tensor | None, t: torch.Tensor |
 
 class AdaptersFunction(torch.autograd.Function):
     """y = base + the low-rank adapters' product of x (the gradient passes to
-    base unchanged)."""
+    base unchanged; scale has none, and a backward pass that wants one is
+    refused)."""
 
     @staticmethod
     def forward(ctx, x, base, A, B, scale, plan):
@@ -871,6 +872,8 @@ class AdaptersFunction(torch.autograd.Function):
     def backward(ctx, gy):
         x2, t, A, B, scale = ctx.saved_tensors
         need = ctx.needs_input_grad
+        if need[4]:
+            raise I8LTError("AdaptersFunction: scale requires a gradient, which the adapters do not compute")
         gx = gA = gB = None
         if need[0] or need[2] or need[3]:
             gx, gA, gB = adapters_backward(gy.reshape(x2.shape[0], gy.shape[-1]), x2, t, A, B, scale, ctx.plan, need_x=need[0],

@@ -171,3 +171,15 @@ def test_a_step_between_a_forward_and_its_backward():
     opt.step()
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.sum().backward()
+
+
+def test_a_scale_that_wants_a_gradient_is_refused():
+    ad = _layer(64, 48, 8, 2)
+    x = _normal(20, 64, seed=3).requires_grad_(True)
+    plan = I.adapter_plan(None, 2, 20, DEV)
+    scale = torch.ones(2, device=DEV, requires_grad=True)
+    y = I.AdaptersFunction.apply(x, ad.base(x), ad.A, ad.B, scale, plan)
+    with pytest.raises(I.I8LTError, match="scale"):
+        y.sum().backward()
+    y = I.AdaptersFunction.apply(x, ad.base(x), ad.A, ad.B, scale.detach(), plan)
+    y.sum().backward()
