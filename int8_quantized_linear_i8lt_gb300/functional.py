@@ -15,6 +15,7 @@ import operator
 import warnings
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -728,6 +729,7 @@ class LayerNormFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -869,6 +871,7 @@ class AdaptersFunction(torch.autograd.Function):
         return y.reshape(*x.shape[:-1], B.shape[1])
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy):
         x2, t, A, B, scale = ctx.saved_tensors
         need = ctx.needs_input_grad

@@ -183,3 +183,14 @@ def test_a_scale_that_wants_a_gradient_is_refused():
         y.sum().backward()
     y = I.AdaptersFunction.apply(x, ad.base(x), ad.A, ad.B, scale.detach(), plan)
     y.sum().backward()
+
+
+def test_second_derivatives_are_refused():
+    """A penalty on a gradient would otherwise lose its own gradient."""
+    ad, norm = _layer(64, 48, 8, 1), I.LayerNorm(64, device=DEV)
+    for f in (lambda x: ad(x), lambda x: norm(x)):
+        x = _normal(20, 64, seed=3).requires_grad_(True)
+        y = (f(x).float() ** 2).sum()
+        g, = torch.autograd.grad(y, x, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            (y + (g.float() ** 2).sum()).backward()
