@@ -553,7 +553,8 @@ int i8lt_adapters_backward(const void* g, const void* x, const void* t, int dt,
  *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
  *   params, grads, sizes   HOST arrays of `count` device pointers and element
  *            counts (read during the call); parameters of dtype pt (updated
- *            in place), gradients of dtype gt, each aligned to its element;
+ *            in place, no two may overlap), gradients of dtype gt, each
+ *            aligned to its element;
  *            a tensor whose gradient is NULL stays as it is, its states too
  *   step     this step's number, from 1
  *   grad_scale, found_inf  optional device fp32 scalars (NULL: 1 and 0): the

@@ -931,6 +931,10 @@ def _adamw_lists(what, params, grads):
     total = sum([(k + blk - 1) // blk for k in sizes]) * blk
     addresses = map(_data_ptr, held) if present[1] is grads else [0 if g is None else g.data_ptr() for g in held]
     lists = array.array("Q", map(_data_ptr, params)), array.array("Q", addresses), array.array("q", sizes)
+    if len(set(lists[0])) != n:                       # equal addresses: of empty tensors, or of one given twice
+        starts = [a for a, k in zip(lists[0], sizes) if k]
+        if len(set(starts)) != len(starts):
+            raise I8LTError(f"{what}: a parameter is given twice")
     at = [a.buffer_info()[0] for a in lists]
     return present[0], (held, lists), n, *at, _code(p0.dtype), _code(g0.dtype), total
 
@@ -952,7 +956,7 @@ def adamw_step(params, grads, m: torch.Tensor, v: torch.Tensor, step: int, lr: f
                grad_scale: torch.Tensor | None = None, found_inf: torch.Tensor | None = None) -> None:
     """One AdamW step, in place, over all ``params`` at once (i8lt_adamw_step).
     m and v: flat fp32 states of ``adamw_state_size(params)`` elements.
-    A parameter whose gradient is None stays as it is.  grad_scale multiplies
+    No two parameters may overlap.  A parameter whose gradient is None stays as it is.  grad_scale multiplies
     every gradient; a found_inf other than 0 makes the step change nothing
     (both fp32 CUDA tensors of one element)."""
     lists = _adamw_lists("adamw_step", params, grads)

@@ -250,6 +250,10 @@ class AdamW:
         for p in params:
             lists.setdefault((p.dtype, p.device), []).append(p)
         self.params = list(lists.values())
+        for ps in self.params:      # one launch updates them all at once
+            spans = sorted((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size()) for p in ps if p.numel())
+            if any(end > start for (_, end), (start, _) in zip(spans, spans[1:])):
+                raise F.I8LTError("AdamW: a parameter is given twice, or overlaps another one")
         self.states = []
         for ps in self.params:
             n, dev = F.adamw_state_size(ps), ps[0].device

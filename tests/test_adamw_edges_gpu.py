@@ -167,3 +167,17 @@ def test_what_lies_past_a_tensors_end_is_not_used(odd):
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(clean, dirty))
     assert all(torch.equal(a, b) for a, b in zip(ps, qs))
     assert not dirty[0].view(torch.uint8)[~inside].any() and not dirty[2].view(torch.uint8)[~inside].any()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_tensor_given_twice_is_refused(bits):
+    p, g = _grad(300, 1), _grad(300, 2)
+    flat = _grad(600, 3)
+    with pytest.raises(I.I8LTError):
+        I.AdamW([p, _grad(4, 4), p], bits=bits)
+    with pytest.raises(I.I8LTError):
+        I.AdamW([flat[:400], flat[300:]], bits=bits)
+    n = I.adamw_state_size([p, p])
+    with pytest.raises(I.I8LTError):
+        _call(bits)([p, p], [g, g], *_states(n, bits), step=1, lr=1e-3)
+    I.AdamW([flat[:300], flat[300:], flat[:0], flat[:0]], bits=bits)      # neighbours, and tensors of nothing
