@@ -556,7 +556,8 @@ int i8lt_adapters_backward(const void* g, const void* x, const void* t, int dt,
  *            in place, no two may overlap), gradients of dtype gt, each
  *            aligned to its element;
  *            a tensor whose gradient is NULL stays as it is, its states too
- *   step     this step's number, from 1
+ *   step     this step's number, from 1: the updates that m and v will have
+ *            seen
  *   grad_scale, found_inf  optional device fp32 scalars (NULL: 1 and 0): the
  *            factor of every gradient (1 / loss scale, a clip factor), and a
  *            value that, when it is not 0, makes the call change nothing
@@ -572,6 +573,11 @@ int i8lt_adapters_backward(const void* g, const void* x, const void* t, int dt,
  *            no code below the smallest, 2^-9; a block with absmax < 2^-100
  *            takes the code of 0.  The parameter uses the moments before
  *            they are rounded.
+ *   ..._counted  keep that number on the device, for each tensor: counts
+ *            [count][2], 16-byte aligned, zeros at first.  counts[i][0] is
+ *            tensor i's updates so far; a tensor without a gradient, and a
+ *            step that found_inf skips, do not add to it.  counts[i][1] is
+ *            scratch.  A replayed CUDA graph counts on, too.
  * State arithmetic is single IEEE fp32 operations in the order above (r is
  * squared to give v), so the states' bits follow from the formulas.
  * A gradient that is not finite makes its states non-finite, in 8 bits those
@@ -591,6 +597,21 @@ int i8lt_adamw_step_8bit(void* const* params, int pt, const void* const* grads,
                          double beta1, double beta2, double eps,
                          double weight_decay, const float* grad_scale,
                          const float* found_inf, void* stream);
+int i8lt_adamw_step_counted(void* const* params, int pt,
+                            const void* const* grads, int gt,
+                            const int64_t* sizes, int64_t count, float* m,
+                            float* v, int64_t* counts, double lr, double beta1,
+                            double beta2, double eps, double weight_decay,
+                            const float* grad_scale, const float* found_inf,
+                            void* stream);
+int i8lt_adamw_step_8bit_counted(void* const* params, int pt,
+                                 const void* const* grads, int gt,
+                                 const int64_t* sizes, int64_t count,
+                                 uint8_t* m, float* m_absmax, uint8_t* r,
+                                 float* r_absmax, int64_t* counts, double lr,
+                                 double beta1, double beta2, double eps,
+                                 double weight_decay, const float* grad_scale,
+                                 const float* found_inf, void* stream);
 
 /* SiLU between the two layers of an MLP: out = h * sigmoid(h), and its
  * backward out = g * silu'(h).  n elements of dtype dt. */

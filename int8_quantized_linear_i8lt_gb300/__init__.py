@@ -18,7 +18,7 @@ include/i8lt.h); build it with ``python -m int8_quantized_linear_i8lt_gb300.buil
 """
 from .functional import (AdapterPlan, AdaptersFunction, I8LTError, Int8LinearFunction, Int8LinearTrainableFunction,
                          Int8MLPFunction, LayerNormFunction, Linear4bitFunction, NF4LinearFunction, SiLUFunction,
-                         adamw_state_size, adamw_step, adamw_step_8bit, adapter_plan, adapters_backward,
+                         adamw_counts, adamw_state_size, adamw_step, adamw_step_8bit, adapter_plan, adapters_backward,
                          adapters_forward, backward_input, backward_input_4bit,
                          default_max_outliers, dequantize_4bit, dequantize_absmax, device_status,
                          double_quantize_absmax, forward, forward_4bit,
@@ -39,4 +39,4 @@ __all__ = ["Linear8bitLt", "Linear8bitLtTrainable", "Int8MLP", "I8LTError", "Int
            "double_quantize_absmax", "dequantize_absmax",
            "LayerNorm", "LayerNormFunction", "layer_norm", "layer_norm_backward",
            "LowRankAdapters", "AdaptersFunction", "AdapterPlan", "adapter_plan", "adapters_forward",
-           "adapters_backward", "AdamW", "adamw_step", "adamw_step_8bit", "adamw_state_size"]
+           "adapters_backward", "AdamW", "adamw_step", "adamw_step_8bit", "adamw_state_size", "adamw_counts"]

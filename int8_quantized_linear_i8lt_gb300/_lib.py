@@ -132,6 +132,12 @@ SIGNATURES = {
     "i8lt_adamw_step_8bit": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_int64, c_void_p, c_void_p,
                                      c_void_p, c_void_p, c_int64, c_double, c_double, c_double, c_double, c_double,
                                      c_void_p, c_void_p, c_void_p]),
+    "i8lt_adamw_step_counted": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_int64, c_void_p, c_void_p,
+                                        c_void_p, c_double, c_double, c_double, c_double, c_double, c_void_p, c_void_p,
+                                        c_void_p]),
+    "i8lt_adamw_step_8bit_counted": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_int64, c_void_p, c_void_p,
+                                             c_void_p, c_void_p, c_void_p, c_double, c_double, c_double, c_double,
+                                             c_double, c_void_p, c_void_p, c_void_p]),
     "i8lt_silu_forward": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_void_p]),
     "i8lt_silu_backward": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_void_p, c_void_p]),
     "i8lt_profile_start": (c_int, [c_int]),
@@ -411,6 +417,18 @@ def i8lt_adamw_step_8bit(params, pt, grads, gt, sizes, count, m, m_absmax, r, r_
     return load().i8lt_adamw_step_8bit(params, pt, grads, gt, sizes, count, m, m_absmax, r, r_absmax,
                                        step, lr, beta1, beta2, eps, weight_decay, grad_scale, found_inf,
                                        stream)
+
+
+def i8lt_adamw_step_counted(params, pt, grads, gt, sizes, count, m, v, counts, lr, beta1, beta2, eps, weight_decay,
+                            grad_scale=None, found_inf=None, stream=None) -> int:
+    return load().i8lt_adamw_step_counted(params, pt, grads, gt, sizes, count, m, v, counts, lr, beta1, beta2, eps,
+                                          weight_decay, grad_scale, found_inf, stream)
+
+
+def i8lt_adamw_step_8bit_counted(params, pt, grads, gt, sizes, count, m, m_absmax, r, r_absmax, counts, lr, beta1,
+                                 beta2, eps, weight_decay, grad_scale=None, found_inf=None, stream=None) -> int:
+    return load().i8lt_adamw_step_8bit_counted(params, pt, grads, gt, sizes, count, m, m_absmax, r, r_absmax, counts,
+                                               lr, beta1, beta2, eps, weight_decay, grad_scale, found_inf, stream)
 
 
 def i8lt_silu_forward(h, dt, n, out, stream=None) -> int:

@@ -1,7 +1,9 @@
 // One AdamW step over many tensors, states in 32 bits or in 8 bits:
 //   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
 //   p = p (1 - lr wd) - size m / (sqrt(v) root + eps),
-//   size = lr / (1 - b1^step), root = 1 / sqrt(1 - b2^step).
+//   size = lr / (1 - b1^step), root = 1 / sqrt(1 - b2^step),
+// where step is the number of updates that m and v have seen: the caller's, or
+// a count per tensor on the device, which a skipped step does not raise.
 // 8 bits: m and r = sqrt(v) are E4M3 codes in blocks of 256 elements with
 // one fp32 absmax each (the block storage of the double-quantized 4-bit
 // absmax).  r rather than v is stored: its block spans half the octaves, so
@@ -35,6 +37,12 @@ struct Hyper {
   const float* found_inf;    // optional device scalar: a value other than 0 skips the step
 };
 
+// A tensor's updates so far, and the corrections of the one under way.
+struct Count {
+  int64_t updates;
+  float size, root;
+};
+
 // A list of tensors travels in the kernel's parameters: no device copy whose
 // host source would have to outlive the call.  kMaxTensors of them fit the
 // 32764 bytes a launch may pass; the short list keeps the launch of a few
@@ -47,12 +55,14 @@ struct TensorList {
   int first[kCap + 1];       // first 256-element block of each tensor in this list's numbering
   int count;
   int64_t block0;            // the list's first block in the flat state
+  int64_t tensor0;           // and its first tensor among the call's
 };
 constexpr int kFewTensors = 32;
 constexpr int kMaxTensors = 1024;
 static_assert(sizeof(TensorList<kMaxTensors>) + sizeof(Hyper) + 64 <= 32764, "kernel parameter space");
 
-// The tensor that holds block `b` (a list holds no empty tensors).
+// The tensor that holds block `b` (of several with the same first block, the
+// last: the others are empty).
 template <int kCap>
 __device__ __forceinline__ int find_tensor(const TensorList<kCap>& L, int b) {
   int lo = 0, hi = L.count;   // first[lo] <= b < first[hi]
@@ -174,15 +184,32 @@ __device__ __forceinline__ void moments(const Hyper& h, float g, float& m, float
   m = __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.c1));
   v = __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, g), h.c2));
 }
-__device__ __forceinline__ float updated(const Hyper& h, float p, float m, float r) {
+__device__ __forceinline__ float updated(const Hyper& h, float size, float root, float p, float m, float r) {
   float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(r, h.root, h.eps)));
-  return fmaf(-(m * h.size), inv, p * h.keep);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(r, root, h.eps)));
+  return fmaf(-(m * size), inv, p * h.keep);
 }
 
-// The blocks [b, end) of a list, tensor by tensor: f(p, g, valid, blocks, state)
-// with the run's first block, its elements left in the tensor and its place in
-// the flat state.  Tensors without a gradient are left out.
+// One more update of the tensors with a gradient: its number and corrections,
+// by the host's formulas.  In a kernel of its own, so that a block of 256
+// elements reads two floats instead of computing two powers; 2 us.
+template <int kCap>
+__global__ void __launch_bounds__(128) adamw_count_kernel(const __grid_constant__ TensorList<kCap> L, double lr,
+                                                          double beta1, double beta2, const float* found_inf,
+                                                          Count* counts) {
+  const int t = blockIdx.x * 128 + threadIdx.x;
+  if (t >= L.count || L.g[t] == nullptr) return;
+  if (found_inf != nullptr && *found_inf != 0.f) return;
+  Count& c = counts[L.tensor0 + t];
+  const int64_t n = c.updates + 1;
+  c = Count{n, static_cast<float>(lr / (1.0 - pow(beta1, static_cast<double>(n)))),
+            static_cast<float>(1.0 / sqrt(1.0 - pow(beta2, static_cast<double>(n))))};
+}
+
+// The blocks [b, end) of a list, tensor by tensor: f(t, p, g, left, blocks,
+// state) with the tensor, the run's first block, its elements left in the
+// tensor and its place in the flat state.  Tensors without a gradient are left
+// out.
 template <int kCap, typename P, typename G, typename F>
 __device__ __forceinline__ void each_run(const TensorList<kCap>& L, int b, int end, F f) {
   for (int t = find_tensor(L, b); b < end; ++t) {
@@ -190,7 +217,7 @@ __device__ __forceinline__ void each_run(const TensorList<kCap>& L, int b, int e
     if (stop <= b) continue;
     const int64_t e0 = static_cast<int64_t>(b - L.first[t]) * kBlockElems;
     if (L.g[t] != nullptr)
-      f(static_cast<P*>(L.p[t]) + e0, static_cast<const G*>(L.g[t]) + e0, L.n[t] - e0, stop - b, L.block0 + b);
+      f(t, static_cast<P*>(L.p[t]) + e0, static_cast<const G*>(L.g[t]) + e0, L.n[t] - e0, stop - b, L.block0 + b);
     b = stop;
   }
 }
@@ -201,18 +228,20 @@ __device__ __forceinline__ void each_run(const TensorList<kCap>& L, int b, int e
 // tensor is paid once.  Bound by HBM: 16 bytes of states, and the parameter
 // and gradient, read or written once.  90 million f32 parameters: 364 us,
 // 6.9 TB/s.
-template <int kCap, typename P, typename G>
+template <int kCap, typename P, typename G, bool kCounted>
 __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constant__ TensorList<kCap> L,
                                                             const __grid_constant__ Hyper h, float* mv, float* rv,
-                                                            int per_warp) {
+                                                            const Count* counts, int per_warp) {
   const int lane = threadIdx.x & 31;
   const int b = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * per_warp;
   const int end = min(b + per_warp, L.first[L.count]);
   if (b >= end) return;
   if (h.found_inf != nullptr && *h.found_inf != 0.f) return;
   const float gs = h.grad_scale != nullptr ? *h.grad_scale : 1.f;
-  each_run<kCap, P, G>(L, b, end, [&](P* p, const G* g, int64_t left, int blocks, int64_t state) {
+  each_run<kCap, P, G>(L, b, end, [&](int t, P* p, const G* g, int64_t left, int blocks, int64_t state) {
     const bool pa = aligned_run<P, 4>(p), ga = aligned_run<G, 4>(g);
+    const float size = kCounted ? counts[L.tensor0 + t].size : h.size;
+    const float root = kCounted ? counts[L.tensor0 + t].root : h.root;
     float *ms = mv + state * kBlockElems, *vs = rv + state * kBlockElems;
     for (; blocks > 0; --blocks, p += kBlockElems, g += kBlockElems, ms += kBlockElems, vs += kBlockElems,
                        left -= kBlockElems) {
@@ -233,7 +262,7 @@ __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constan
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           moments(h, __fmul_rn(gv[i][k], gs), m[i][k], v[i][k]);
-          pv[i][k] = updated(h, pv[i][k], m[i][k], sqrtf(v[i][k]));
+          pv[i][k] = updated(h, size, root, pv[i][k], m[i][k], sqrtf(v[i][k]));
         }
         store_run<P, 4>(p + e, pa && e + 4 <= valid, valid - e, pv[i]);
         *reinterpret_cast<float4*>(ms + e) = *reinterpret_cast<const float4*>(m[i]);
@@ -249,11 +278,11 @@ __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constan
 // blocks are loaded before either is worked on, and the codes of zero are
 // behind a branch that a block without them does not take.  90 million f16
 // parameters: 185 us, 4.9 TB/s.
-template <int kCap, typename P, typename G>
+template <int kCap, typename P, typename G, bool kCounted>
 __global__ void __launch_bounds__(kWarps * 32, 4) adamw8_kernel(const __grid_constant__ TensorList<kCap> L,
                                                                 const __grid_constant__ Hyper h, uint8_t* mv,
                                                                 uint8_t* rv, float* m_top, float* r_top,
-                                                                int per_warp) {
+                                                                const Count* counts, int per_warp) {
   const int lane = threadIdx.x & 31;
   const int b = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * per_warp;
   const int end = min(b + per_warp, L.first[L.count]);
@@ -267,8 +296,10 @@ __global__ void __launch_bounds__(kWarps * 32, 4) adamw8_kernel(const __grid_con
     uint2 m, r;
     float mt, rt;
   };
-  each_run<kCap, P, G>(L, b, end, [&](P* p, const G* g, int64_t left, int blocks, int64_t state) {
+  each_run<kCap, P, G>(L, b, end, [&](int t, P* p, const G* g, int64_t left, int blocks, int64_t state) {
     const bool pa = aligned_run<P, 8>(p), ga = aligned_run<G, 8>(g);
+    const float size = kCounted ? counts[L.tensor0 + t].size : h.size;
+    const float root = kCounted ? counts[L.tensor0 + t].root : h.root;
     p += 8 * lane;
     g += 8 * lane;
     // this lane's elements from here to the tensor's end
@@ -309,7 +340,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) adamw8_kernel(const __grid_con
       for (int k = 0; k < 8; ++k) {
         v[k] = __fsqrt_rn(v[k]);
         vtop = max_or_nan(vtop, v[k]);
-        pv[k] = updated(h, pv[k], m[k], v[k]);
+        pv[k] = updated(h, size, root, pv[k], m[k], v[k]);
       }
       store_run<P, 8>(p + i * kBlockElems, whole || (pa && valid == 8), valid, pv);
       mtop = warp_max(mtop);
@@ -351,38 +382,59 @@ __global__ void __launch_bounds__(kWarps * 32, 4) adamw8_kernel(const __grid_con
   });
 }
 
-template <int kCap, typename P, typename G, bool k8>
-cudaError_t launch_list(const TensorList<kCap>& L, const Hyper& h, void* m, void* r, float* mt, float* rt,
-                        cudaStream_t s) {
+// What all lists of a call share.
+struct Call {
+  Hyper h;
+  double lr, beta1, beta2;
+  Count* counts;             // or NULL: h's corrections for every tensor
+  void *m, *r;
+  float *m_top, *r_top;
+  cudaStream_t s;
+};
+
+template <int kCap, typename P, typename G, bool k8, bool kCounted>
+cudaError_t launch_kernel(const TensorList<kCap>& L, const Call& c) {
   const int blocks = L.first[L.count];
-  if (blocks == 0) return cudaSuccess;
   // more blocks per warp only when every SM still gets several rounds of warps
   const int per_warp = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(k8 ? 8 : 4, blocks / (152 * 64))));
   const unsigned grid = static_cast<unsigned>(ceil_div(blocks, kWarps * per_warp));
-  ProfScope ps(K_ADAMW, s);
+  ProfScope ps(K_ADAMW, c.s);
   if constexpr (k8)
-    adamw8_kernel<kCap, P, G><<<grid, kWarps * 32, 0, s>>>(L, h, static_cast<uint8_t*>(m), static_cast<uint8_t*>(r),
-                                                           mt, rt, per_warp);
+    adamw8_kernel<kCap, P, G, kCounted><<<grid, kWarps * 32, 0, c.s>>>(
+        L, c.h, static_cast<uint8_t*>(c.m), static_cast<uint8_t*>(c.r), c.m_top, c.r_top, c.counts, per_warp);
   else
-    adamw_kernel<kCap, P, G><<<grid, kWarps * 32, 0, s>>>(L, h, static_cast<float*>(m), static_cast<float*>(r),
-                                                          per_warp);
+    adamw_kernel<kCap, P, G, kCounted>
+        <<<grid, kWarps * 32, 0, c.s>>>(L, c.h, static_cast<float*>(c.m), static_cast<float*>(c.r), c.counts, per_warp);
   return cudaGetLastError();
+}
+
+template <int kCap, typename P, typename G, bool k8>
+cudaError_t launch_list(const TensorList<kCap>& L, const Call& c) {
+  if (L.first[L.count] == 0) return cudaSuccess;
+  if (c.counts == nullptr) return launch_kernel<kCap, P, G, k8, false>(L, c);
+  {
+    ProfScope ps(K_ADAMW, c.s);
+    adamw_count_kernel<kCap><<<static_cast<unsigned>(ceil_div(L.count, 128)), 128, 0, c.s>>>(
+        L, c.lr, c.beta1, c.beta2, c.h.found_inf, c.counts);
+    if (cudaError_t e = cudaGetLastError()) return e;
+  }
+  return launch_kernel<kCap, P, G, k8, true>(L, c);
 }
 
 // The tensors in lists of kCap; a list also ends before its blocks pass 2^30.
 template <int kCap, typename P, typename G, bool k8>
 cudaError_t run_lists(void* const* params, const void* const* grads, const int64_t* sizes, int64_t count,
-                      const Hyper& h, void* m, void* r, float* mt, float* rt, cudaStream_t s) {
+                      const Call& c) {
   TensorList<kCap> L;
   L.count = 0;
   L.first[0] = 0;
-  L.block0 = 0;
+  L.block0 = L.tensor0 = 0;
   for (int64_t i = 0; i < count; ++i) {
     const int64_t blocks = ceil_div(sizes[i], kBlockElems);
-    if (blocks == 0) continue;
     if (L.count == kCap || L.first[L.count] + blocks > (int64_t(1) << 30)) {
-      if (cudaError_t e = launch_list<kCap, P, G, k8>(L, h, m, r, mt, rt, s)) return e;
+      if (cudaError_t e = launch_list<kCap, P, G, k8>(L, c)) return e;
       L.block0 += L.first[L.count];
+      L.tensor0 = i;
       L.count = 0;
     }
     L.p[L.count] = params[i];
@@ -391,28 +443,29 @@ cudaError_t run_lists(void* const* params, const void* const* grads, const int64
     L.first[L.count + 1] = L.first[L.count] + static_cast<int>(blocks);
     ++L.count;
   }
-  return launch_list<kCap, P, G, k8>(L, h, m, r, mt, rt, s);
+  return launch_list<kCap, P, G, k8>(L, c);
 }
 
 template <typename P, typename G, bool k8>
 cudaError_t run_sized(void* const* params, const void* const* grads, const int64_t* sizes, int64_t count,
-                      const Hyper& h, void* m, void* r, float* mt, float* rt, cudaStream_t s) {
-  if (count <= kFewTensors) return run_lists<kFewTensors, P, G, k8>(params, grads, sizes, count, h, m, r, mt, rt, s);
-  return run_lists<kMaxTensors, P, G, k8>(params, grads, sizes, count, h, m, r, mt, rt, s);
+                      const Call& c) {
+  if (count <= kFewTensors) return run_lists<kFewTensors, P, G, k8>(params, grads, sizes, count, c);
+  return run_lists<kMaxTensors, P, G, k8>(params, grads, sizes, count, c);
 }
 
 template <typename P, bool k8>
 cudaError_t run_grad(int gt, void* const* params, const void* const* grads, const int64_t* sizes, int64_t count,
-                     const Hyper& h, void* m, void* r, float* mt, float* rt, cudaStream_t s) {
-  if (gt == DT_F16) return run_sized<P, __half, k8>(params, grads, sizes, count, h, m, r, mt, rt, s);
-  if (gt == DT_BF16) return run_sized<P, __nv_bfloat16, k8>(params, grads, sizes, count, h, m, r, mt, rt, s);
-  return run_sized<P, float, k8>(params, grads, sizes, count, h, m, r, mt, rt, s);
+                     const Call& c) {
+  if (gt == DT_F16) return run_sized<P, __half, k8>(params, grads, sizes, count, c);
+  if (gt == DT_BF16) return run_sized<P, __nv_bfloat16, k8>(params, grads, sizes, count, c);
+  return run_sized<P, float, k8>(params, grads, sizes, count, c);
 }
 
+// counts NULL: update number `step` of every tensor.
 template <bool k8>
 int adamw(void* const* params, int pt, const void* const* grads, int gt, const int64_t* sizes, int64_t count,
-          void* m, float* mt, void* r, float* rt, int64_t step, double lr, double beta1, double beta2, double eps,
-          double weight_decay, const float* grad_scale, const float* found_inf, void* stream) {
+          void* m, float* mt, void* r, float* rt, int64_t step, void* counts, double lr, double beta1, double beta2,
+          double eps, double weight_decay, const float* grad_scale, const float* found_inf, void* stream) {
   if (!valid_dt(pt) || !valid_dt(gt)) return I8LT_ERR_UNSUPPORTED_DTYPE;
   if (count < 0 || step < 1) return I8LT_ERR_INVALID_ARG;
   if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0)) return I8LT_ERR_INVALID_ARG;
@@ -428,24 +481,31 @@ int adamw(void* const* params, int pt, const void* const* grads, int gt, const i
   }
   if (total == 0) return I8LT_OK;
   if (m == nullptr || r == nullptr || (k8 && (mt == nullptr || rt == nullptr))) return I8LT_ERR_INVALID_ARG;
-  if (!aligned16(m) || !aligned16(r)) return I8LT_ERR_MISALIGNED;
+  if (!aligned16(m) || !aligned16(r) || !aligned16(counts)) return I8LT_ERR_MISALIGNED;
   if (int d = check_device()) return d;
-  Hyper h;
-  h.b1 = static_cast<float>(beta1);
-  h.b2 = static_cast<float>(beta2);
-  h.c1 = static_cast<float>(1.0 - beta1);
-  h.c2 = static_cast<float>(1.0 - beta2);
-  h.keep = static_cast<float>(1.0 - lr * weight_decay);
-  h.size = static_cast<float>(lr / (1.0 - std::pow(beta1, static_cast<double>(step))));
-  h.root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, static_cast<double>(step))));
-  h.eps = static_cast<float>(eps);
-  h.grad_scale = grad_scale;
-  h.found_inf = found_inf;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (pt == DT_F16) return cuda_status(run_grad<__half, k8>(gt, params, grads, sizes, count, h, m, r, mt, rt, s));
-  if (pt == DT_BF16)
-    return cuda_status(run_grad<__nv_bfloat16, k8>(gt, params, grads, sizes, count, h, m, r, mt, rt, s));
-  return cuda_status(run_grad<float, k8>(gt, params, grads, sizes, count, h, m, r, mt, rt, s));
+  Call c;
+  c.h.b1 = static_cast<float>(beta1);
+  c.h.b2 = static_cast<float>(beta2);
+  c.h.c1 = static_cast<float>(1.0 - beta1);
+  c.h.c2 = static_cast<float>(1.0 - beta2);
+  c.h.keep = static_cast<float>(1.0 - lr * weight_decay);
+  c.h.size = static_cast<float>(lr / (1.0 - std::pow(beta1, static_cast<double>(step))));
+  c.h.root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, static_cast<double>(step))));
+  c.h.eps = static_cast<float>(eps);
+  c.h.grad_scale = grad_scale;
+  c.h.found_inf = found_inf;
+  c.lr = lr;
+  c.beta1 = beta1;
+  c.beta2 = beta2;
+  c.counts = static_cast<Count*>(counts);
+  c.m = m;
+  c.r = r;
+  c.m_top = mt;
+  c.r_top = rt;
+  c.s = static_cast<cudaStream_t>(stream);
+  if (pt == DT_F16) return cuda_status(run_grad<__half, k8>(gt, params, grads, sizes, count, c));
+  if (pt == DT_BF16) return cuda_status(run_grad<__nv_bfloat16, k8>(gt, params, grads, sizes, count, c));
+  return cuda_status(run_grad<float, k8>(gt, params, grads, sizes, count, c));
 }
 
 }  // namespace
@@ -456,16 +516,34 @@ extern "C" {
 int i8lt_adamw_step(void* const* params, int pt, const void* const* grads, int gt, const int64_t* sizes,
                     int64_t count, float* m, float* v, int64_t step, double lr, double beta1, double beta2, double eps,
                     double weight_decay, const float* grad_scale, const float* found_inf, void* stream) {
-  return i8lt::adamw<false>(params, pt, grads, gt, sizes, count, m, nullptr, v, nullptr, step, lr, beta1, beta2, eps,
-                            weight_decay, grad_scale, found_inf, stream);
+  return i8lt::adamw<false>(params, pt, grads, gt, sizes, count, m, nullptr, v, nullptr, step, nullptr, lr, beta1,
+                            beta2, eps, weight_decay, grad_scale, found_inf, stream);
 }
 
 int i8lt_adamw_step_8bit(void* const* params, int pt, const void* const* grads, int gt, const int64_t* sizes,
                          int64_t count, uint8_t* m, float* m_absmax, uint8_t* r, float* r_absmax, int64_t step,
                          double lr, double beta1, double beta2, double eps, double weight_decay,
                          const float* grad_scale, const float* found_inf, void* stream) {
-  return i8lt::adamw<true>(params, pt, grads, gt, sizes, count, m, m_absmax, r, r_absmax, step, lr, beta1, beta2, eps,
-                           weight_decay, grad_scale, found_inf, stream);
+  return i8lt::adamw<true>(params, pt, grads, gt, sizes, count, m, m_absmax, r, r_absmax, step, nullptr, lr, beta1,
+                           beta2, eps, weight_decay, grad_scale, found_inf, stream);
+}
+
+int i8lt_adamw_step_counted(void* const* params, int pt, const void* const* grads, int gt, const int64_t* sizes,
+                            int64_t count, float* m, float* v, int64_t* counts, double lr, double beta1, double beta2,
+                            double eps, double weight_decay, const float* grad_scale, const float* found_inf,
+                            void* stream) {
+  if (count > 0 && counts == nullptr) return I8LT_ERR_INVALID_ARG;
+  return i8lt::adamw<false>(params, pt, grads, gt, sizes, count, m, nullptr, v, nullptr, 1, counts, lr, beta1, beta2,
+                            eps, weight_decay, grad_scale, found_inf, stream);
+}
+
+int i8lt_adamw_step_8bit_counted(void* const* params, int pt, const void* const* grads, int gt, const int64_t* sizes,
+                                 int64_t count, uint8_t* m, float* m_absmax, uint8_t* r, float* r_absmax,
+                                 int64_t* counts, double lr, double beta1, double beta2, double eps,
+                                 double weight_decay, const float* grad_scale, const float* found_inf, void* stream) {
+  if (count > 0 && counts == nullptr) return I8LT_ERR_INVALID_ARG;
+  return i8lt::adamw<true>(params, pt, grads, gt, sizes, count, m, m_absmax, r, r_absmax, 1, counts, lr, beta1, beta2,
+                           eps, weight_decay, grad_scale, found_inf, stream);
 }
 
 }  // extern "C"

@@ -897,6 +897,21 @@ _data_ptr, _size, _get_device = torch.Tensor.data_ptr, torch.Tensor.size, torch.
 _is_contiguous, _numel, _dtype_of = torch.Tensor.is_contiguous, torch.Tensor.numel, operator.attrgetter("dtype")
 
 
+def adamw_counts(params) -> torch.Tensor:
+    """Update counts of ``params`` for ``adamw_step`` and ``adamw_step_8bit``
+    in place of a step number: zeros, int64 [len(params), 2] on their device,
+    whose first column the calls keep."""
+    return torch.zeros(len(params), 2, dtype=torch.int64, device=params[0].device)
+
+
+def _adamw_counts(what, step, count, device) -> int:
+    """The address of update counts after their checks."""
+    if step.dtype != torch.int64 or step.shape != (count, 2) or not step.is_contiguous() or step.device != device:
+        raise I8LTError(f"{what}: update counts of shape {tuple(step.shape)}, {step.dtype} on {step.device}, expected "
+                        f"contiguous ({count}, 2), torch.int64 on {device}")
+    return step.data_ptr()
+
+
 def _adamw_lists(what, params, grads):
     """(the parameters with a gradient, what must outlive the call, count,
     addresses of the lists of device addresses and sizes, dtypes, elements of a
@@ -951,14 +966,18 @@ def _adamw_scalar(what, t, device):
         raise I8LTError(f"{what}: grad_scale and found_inf are fp32 tensors of one element on {device}")
 
 
-def adamw_step(params, grads, m: torch.Tensor, v: torch.Tensor, step: int, lr: float, beta1: float = 0.9,
+def adamw_step(params, grads, m: torch.Tensor, v: torch.Tensor, step: int | torch.Tensor, lr: float, beta1: float = 0.9,
                beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01,
                grad_scale: torch.Tensor | None = None, found_inf: torch.Tensor | None = None) -> None:
     """One AdamW step, in place, over all ``params`` at once (i8lt_adamw_step).
     m and v: flat fp32 states of ``adamw_state_size(params)`` elements.
-    No two parameters may overlap.  A parameter whose gradient is None stays as it is.  grad_scale multiplies
-    every gradient; a found_inf other than 0 makes the step change nothing
-    (both fp32 CUDA tensors of one element)."""
+    No two parameters may overlap.  A parameter whose gradient is None stays as
+    it is.  grad_scale multiplies every gradient; a found_inf other than 0 makes
+    the step change nothing (both fp32 CUDA tensors of one element).  ``step``:
+    the number of updates, this one included, that m and v of every parameter
+    will have seen; or ``adamw_counts(params)``, which counts them on the device
+    for each parameter, without those that had no gradient or that found_inf
+    skipped."""
     lists = _adamw_lists("adamw_step", params, grads)
     if lists is None:
         return
@@ -967,13 +986,16 @@ def adamw_step(params, grads, m: torch.Tensor, v: torch.Tensor, step: int, lr: f
     _adamw_state("adamw_step", size, torch.float32, p0.device, m, v)
     _adamw_scalar("adamw_step", grad_scale, p0.device)
     _adamw_scalar("adamw_step", found_inf, p0.device)
-    _check(_lib.i8lt_adamw_step(pp, pt, gp, gt, sizes, n, m.data_ptr(), v.data_ptr(), step, lr, beta1, beta2, eps,
-                                weight_decay, _ptr(grad_scale), _ptr(found_inf), _stream(p0)), "i8lt_adamw_step")
+    call = _lib.i8lt_adamw_step
+    if isinstance(step, torch.Tensor):
+        call, step = _lib.i8lt_adamw_step_counted, _adamw_counts("adamw_step", step, n, p0.device)
+    _check(call(pp, pt, gp, gt, sizes, n, m.data_ptr(), v.data_ptr(), step, lr, beta1, beta2, eps, weight_decay,
+                _ptr(grad_scale), _ptr(found_inf), _stream(p0)), "i8lt_adamw_step")
     _written((*changed, m, v))
 
 
 def adamw_step_8bit(params, grads, m: torch.Tensor, m_absmax: torch.Tensor, r: torch.Tensor, r_absmax: torch.Tensor,
-                    step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                    step: int | torch.Tensor, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                     weight_decay: float = 0.01, grad_scale: torch.Tensor | None = None,
                     found_inf: torch.Tensor | None = None) -> None:
     """``adamw_step`` with 8-bit states (i8lt_adamw_step_8bit): m and
@@ -988,7 +1010,10 @@ def adamw_step_8bit(params, grads, m: torch.Tensor, m_absmax: torch.Tensor, r: t
     _adamw_state("adamw_step_8bit", size // _lib.I8LT_ADAMW_BLOCK, torch.float32, p0.device, m_absmax, r_absmax)
     _adamw_scalar("adamw_step_8bit", grad_scale, p0.device)
     _adamw_scalar("adamw_step_8bit", found_inf, p0.device)
-    _check(_lib.i8lt_adamw_step_8bit(pp, pt, gp, gt, sizes, n, m.data_ptr(), m_absmax.data_ptr(), r.data_ptr(),
-                                     r_absmax.data_ptr(), step, lr, beta1, beta2, eps, weight_decay, _ptr(grad_scale),
-                                     _ptr(found_inf), _stream(p0)), "i8lt_adamw_step_8bit")
+    call = _lib.i8lt_adamw_step_8bit
+    if isinstance(step, torch.Tensor):
+        call, step = _lib.i8lt_adamw_step_8bit_counted, _adamw_counts("adamw_step_8bit", step, n, p0.device)
+    _check(call(pp, pt, gp, gt, sizes, n, m.data_ptr(), m_absmax.data_ptr(), r.data_ptr(), r_absmax.data_ptr(), step,
+                lr, beta1, beta2, eps, weight_decay, _ptr(grad_scale), _ptr(found_inf), _stream(p0)),
+           "i8lt_adamw_step_8bit")
     _written((*changed, m, m_absmax, r, r_absmax))

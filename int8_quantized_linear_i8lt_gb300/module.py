@@ -238,7 +238,10 @@ class AdamW:
     elements.  A parameter without a gradient is left as it is.  step() takes
     the optional device scalars of a loss scaler or a gradient clip:
     ``grad_scale`` multiplies every gradient, a ``found_inf`` other than 0
-    makes the step change nothing (the step still counts)."""
+    makes the step change nothing.  ``steps`` counts the calls; the bias
+    corrections of a parameter are those of its own updates, without steps in
+    which it had no gradient or that were skipped (``counts``, on the
+    device)."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
                  bits: int = 32):
@@ -254,6 +257,7 @@ class AdamW:
             spans = sorted((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size()) for p in ps if p.numel())
             if any(end > start for (_, end), (start, _) in zip(spans, spans[1:])):
                 raise F.I8LTError("AdamW: a parameter is given twice, or overlaps another one")
+        self.counts = [F.adamw_counts(ps) for ps in self.params]
         self.states = []
         for ps in self.params:
             n, dev = F.adamw_state_size(ps), ps[0].device
@@ -269,8 +273,8 @@ class AdamW:
     def step(self, grad_scale: torch.Tensor | None = None, found_inf: torch.Tensor | None = None) -> None:
         self.steps += 1
         call = F.adamw_step_8bit if self.bits == 8 else F.adamw_step
-        for ps, st in zip(self.params, self.states):
-            call(ps, [p.grad for p in ps], *st, step=self.steps, lr=self.lr, beta1=self.betas[0],
+        for ps, st, counts in zip(self.params, self.states, self.counts):
+            call(ps, [p.grad for p in ps], *st, step=counts, lr=self.lr, beta1=self.betas[0],
                  beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay, grad_scale=grad_scale,
                  found_inf=found_inf)
 
@@ -280,13 +284,18 @@ class AdamW:
                 p.grad = None
 
     def state_dict(self) -> dict:
-        return {"steps": self.steps, "bits": self.bits, "states": [tuple(t.clone() for t in st) for st in self.states]}
+        return {"steps": self.steps, "bits": self.bits, "states": [tuple(t.clone() for t in st) for st in self.states],
+                "counts": [c[:, 0].clone() for c in self.counts]}
 
     def load_state_dict(self, d: dict) -> None:
         if d["bits"] != self.bits or [[t.shape for t in st] for st in d["states"]] != \
-                [[t.shape for t in st] for st in self.states]:
+                [[t.shape for t in st] for st in self.states] or \
+                [len(c) for c in d.get("counts", self.counts)] != [len(c) for c in self.counts]:
             raise F.I8LTError("AdamW: the state was saved for other parameters")
         self.steps = d["steps"]
+        for k, counts in enumerate(self.counts):
+            # a state saved without counts: every step was an update
+            counts[:, 0] = d["counts"][k] if "counts" in d else self.steps
         for st, src in zip(self.states, d["states"]):
             for t, v in zip(st, src):
                 t.copy_(v)

@@ -181,3 +181,127 @@ def test_a_tensor_given_twice_is_refused(bits):
     with pytest.raises(I.I8LTError):
         _call(bits)([p, p], [g, g], *_states(n, bits), step=1, lr=1e-3)
     I.AdamW([flat[:300], flat[300:], flat[:0], flat[:0]], bits=bits)      # neighbours, and tensors of nothing
+
+
+def _adamw64(p, grads, lr, b1=0.9, b2=0.95, eps=1e-8, wd=0.01):
+    """The formulas in 64 bits over one tensor's gradients, its own steps
+    counted (None: no update)."""
+    p, m, v, n = p.double().cpu(), 0.0, 0.0, 0
+    for g in grads:
+        if g is None:
+            continue
+        g, n = g.double().cpu(), n + 1
+        m, v = b1 * m + (1 - b1) * g, b2 * v + (1 - b2) * g * g
+        p = p * (1 - lr * wd) - lr / (1 - b1 ** n) * m / ((v / (1 - b2 ** n)) ** 0.5 + eps)
+    return p
+
+
+# An E4M3 code is off by 2^-4 of the value: an update of 8-bit states by about
+# an eighth of lr a step, against 0.55 lr where the bias corrections are those
+# of step 100 (0.1 / 0.2236 in place of 1).  32 bits: 2^-24 of p and of 16
+# operations a step.
+def _near(got, want, steps, lr, bits):
+    tol = steps * (lr / 4 if bits == 8 else 16 * 2.0 ** -24 * (lr + float(want.abs().max())))
+    return float((got.double().cpu() - want).abs().max()) <= tol
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_late_first_gradient(bits):
+    """A parameter whose first gradient comes with the optimizer's 100th step:
+    its first update is of size lr."""
+    lr = 1e-2
+    ps = [_grad(700, 1, 0.1), _grad(300, 2, 0.1), _grad(256, 3, 0.1)]
+    start = [p.clone() for p in ps]
+    opt = I.AdamW(ps, lr=lr, betas=(0.9, 0.95), bits=bits)
+    seen = [[], [], []]
+    for step in range(101):
+        gs = [_grad(700, 10), None if step < 99 else _grad(300, 20 + step), _grad(256, 11) if step % 2 else None]
+        for p, g, s in zip(ps, gs, seen):
+            p.grad = g
+            s.append(g)
+        opt.step()
+    assert _near(ps[1], _adamw64(start[1], seen[1], lr), 2, lr, bits)
+    if bits == 32:
+        for k in (0, 2):
+            assert _near(ps[k], _adamw64(start[k], seen[k], lr), 101, lr, bits)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_skipped_first_steps(bits):
+    """Steps that found_inf skips (a loss scaler's first ones) do not count,
+    for the tensors they concern."""
+    lr = 1e-2
+    ps = [_grad(700, 1, 0.1), _grad(300, 2, 0.1)]
+    start = [p.clone() for p in ps]
+    opt = I.AdamW(ps, lr=lr, betas=(0.9, 0.95), bits=bits)
+    for step in range(40):
+        ps[0].grad, ps[1].grad = _grad(700, 7) * INF, _grad(300, 8) * INF
+        opt.step(found_inf=torch.ones(1, device=DEV))
+    gs = [_grad(700, 9), _grad(300, 10)]
+    for p, g in zip(ps, gs):
+        p.grad = g
+    opt.step(found_inf=torch.zeros(1, device=DEV))
+    for p, s, g in zip(ps, start, gs):
+        assert _near(p, _adamw64(s, [g], lr), 1, lr, bits)
+    opt.step()
+    for p, s, g in zip(ps, start, gs):
+        assert _near(p, _adamw64(s, [g, g], lr), 2, lr, bits)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_counts_in_the_state_dict(bits):
+    def made():
+        ps = [_grad(700, 1, 0.1), _grad(300, 2, 0.1), _grad(64, 2, 0.1).bfloat16()]
+        return ps, I.AdamW(ps, lr=1e-2, bits=bits)
+
+    def steps(ps, opt, first, last):
+        for step in range(first, last):
+            for k, p in enumerate(ps):
+                p.grad = _grad(p.numel(), 30 * k + step).to(p.dtype) if (step + k) % 3 else None
+            opt.step(found_inf=torch.full((1,), float(step % 4 == 1), device=DEV))
+
+    whole, opt = made()
+    steps(whole, opt, 0, 12)
+    half, opt = made()
+    steps(half, opt, 0, 5)
+    fresh = I.AdamW(half, lr=1e-2, bits=bits)
+    fresh.load_state_dict(opt.state_dict())
+    steps(half, fresh, 5, 12)
+    assert all(torch.equal(a, b) for a, b in zip(whole, half))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_counted_steps(bits):
+    """Update counts in place of a step number: the same bits, in lists of any
+    length, with empty tensors and with several lists, and in a replayed CUDA
+    graph."""
+    sizes = [300, 0, 13, 513] * 300
+    p0, gs = [_grad(n, n, 0.1) for n in sizes], [_grad(n, n + 1) for n in sizes]
+    ps, qs, rs = ([p.clone() for p in p0] for _ in range(3))
+    n = I.adamw_state_size(ps)
+    one, two, three = _states(n, bits), _states(n, bits), _states(n, bits)
+    counts, again = I.adamw_counts(ps), I.adamw_counts(ps)
+    for step in (1, 2, 3):
+        some = [g if k % 7 else None for k, g in enumerate(gs)]
+        _call(bits)(ps, some, *one, step=step, **HYPER)
+        _call(bits)(qs, some, *two, step=counts, **HYPER)
+    for a, b in zip((*ps, *one), (*qs, *two)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert counts[:, 0].tolist() == [3 if k % 7 and sizes[k] else 0 for k in range(len(sizes))]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _call(bits)([p.clone() for p in p0], some, *_states(n, bits), step=I.adamw_counts(ps), **HYPER)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _call(bits)(rs, some, *three, step=again, **HYPER)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip((*ps, *one), (*rs, *three)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    for bad in (counts[:5], counts.int(), counts.cpu(), counts.t().contiguous().t()):
+        with pytest.raises(I.I8LTError):
+            _call(bits)(ps, gs, *one, step=bad, **HYPER)

@@ -1,0 +1,31 @@
+"""More argument checks of the fine-tuning entry points through the C ABI (no
+GPU: every call returns before it touches the device)."""
+import ctypes
+
+import pytest
+
+from int8_quantized_linear_i8lt_gb300 import _lib
+from int8_quantized_linear_i8lt_gb300.build import build
+
+P = 1 << 20          # 256-byte aligned, never dereferenced
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_counted(bits):
+    def call(counts=P, count=2, sizes=(5, 300), state=P, lr=1e-3, pt=2):
+        lists = ((ctypes.c_void_p * 2)(P, P + 4096), (ctypes.c_void_p * 2)(P, P), (ctypes.c_int64 * 2)(*sizes))
+        if bits == 8:
+            return _lib.i8lt_adamw_step_8bit_counted(lists[0], pt, lists[1], 2, lists[2], count, state, P, state, P,
+                                                     counts, lr, 0.9, 0.99, 1e-8, 0.0)
+        return _lib.i8lt_adamw_step_counted(lists[0], pt, lists[1], 2, lists[2], count, state, state, counts, lr, 0.9,
+                                            0.99, 1e-8, 0.0)
+
+    assert call(counts=None) == _lib.I8LT_ERR_INVALID_ARG and call(counts=P + 8) == _lib.I8LT_ERR_MISALIGNED
+    assert call(lr=float("nan")) == _lib.I8LT_ERR_INVALID_ARG and call(pt=3) == _lib.I8LT_ERR_UNSUPPORTED_DTYPE
+    assert call(state=None) == _lib.I8LT_ERR_INVALID_ARG and call(count=-1) == _lib.I8LT_ERR_INVALID_ARG
+    assert call(count=0, counts=None) == _lib.I8LT_OK and call(sizes=(0, 0)) == _lib.I8LT_OK
