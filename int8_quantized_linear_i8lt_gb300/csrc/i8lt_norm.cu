@@ -1028,6 +1028,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads) norm_backward_long_kernel(const BackwardArgs a) {
   __shared__ __align__(16) float scratch[2][kWideThreads / 32];
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.st = DevStatus{0, 0, 0, 0};
   const int64_t m = blockIdx.x, N = a.N;
   const T* g = static_cast<const T*>(a.g) + m * N;
   const T* x = static_cast<const T*>(a.x) + m * N;
@@ -1048,6 +1049,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_backward_long_kernel(const 
 }
 template <typename T>
 __global__ void __launch_bounds__(256) norm_grad_long_kernel(const BackwardArgs a, int64_t rows) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.st = DevStatus{0, 0, 0, 0};
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, N = a.N;
   if (n >= N) return;
   const int64_t c = blockIdx.y, m0 = c * rows, m1 = min(m0 + rows, a.M);
@@ -1288,6 +1290,7 @@ int i8lt_layer_norm_backward(const void* g, const void* x, int xt, int64_t M, in
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (M == 0) {
     const size_t bytes = static_cast<size_t>(N) * (wt == DT_F32 ? 4 : 2);
+    if (cudaMemsetAsync(ws, 0, sizeof(DevStatus), s) != cudaSuccess) return I8LT_ERR_CUDA;
     if (gw != nullptr && cudaMemsetAsync(gw, 0, bytes, s) != cudaSuccess) return I8LT_ERR_CUDA;
     if (gb != nullptr && cudaMemsetAsync(gb, 0, bytes, s) != cudaSuccess) return I8LT_ERR_CUDA;
     return I8LT_OK;
