@@ -3,11 +3,14 @@
 //   h = (x - mean) * rstd, y = h * w + b;
 //   gx = rstd * (g w - mean_n(g w) - h * mean_n(g w h)),
 //   gw = sum_m g h, gb = sum_m g.
+// The forward has no workspace, so no status word: should a wait run out, the
+// rows that it kept from coming are NaN.
 // Statistics and sums are fp32; each output is rounded once.  Both
 // directions are bound by HBM: the forward reads x and writes y, the backward
 // reads x and g and writes gx, each once; everything between stays in
 // registers and shared memory.
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 #include <type_traits>
 
@@ -354,10 +357,9 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel
   unsigned s = 0;
   uint32_t phase = 0;
   for (int64_t i = 0; i < ring.rows; ++i) {
-    mbar_wait(&full[s], phase, &abort_flag, nullptr, 31);
+    float t = mbar_wait(&full[s], phase, &abort_flag, nullptr, 31) ? 0.f : NAN;   // of the row: all its y is NaN
     if constexpr (kShift) last_elements(ring, i, a.M, s);
     const T* x = reinterpret_cast<const T*>(stages + s * L.slot_bytes);
-    float t = 0.f;
 #pragma unroll
     for (int e = 0; e < kE / W; ++e) {
       const int c = (tid + e * kLanes) * W;
@@ -434,10 +436,9 @@ __global__ void __launch_bounds__(kWideThreads) norm_forward_wide_kernel(const F
   unsigned s = 0;
   uint32_t phase = 0;
   for (int64_t i = 0; i < ring.rows; ++i) {
-    mbar_wait(&full[s], phase, &abort_flag, nullptr, 31);
+    float t = mbar_wait(&full[s], phase, &abort_flag, nullptr, 31) ? 0.f : NAN, v[W];
     if constexpr (kShift) last_elements(ring, i, a.M, s);
     const T* x = reinterpret_cast<const T*>(stages + s * L.slot_bytes);
-    float t = 0.f, v[W];
 #pragma unroll 4
     for (int c = tid * W; c < end; c += kWideThreads * W) {
       widen<T, W>(load_pack<T, W>(x + c), v);
