@@ -653,6 +653,16 @@ def _out(what: str, t: torch.Tensor, dev: int, shape, dtype):
     return _checked(what, t, dev, shape, dtype)
 
 
+def _workspace(what: str, ws, size: int, device) -> torch.Tensor:
+    """The caller's workspace after its checks (the library checks its size),
+    or a new one."""
+    if ws is None:
+        return torch.empty(max(size, 256), dtype=torch.uint8, device=device)
+    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise I8LTError(f"{what}: a workspace is a contiguous uint8 tensor on {device}")
+    return ws
+
+
 # Tells autograd that tensors were written in place: a backward pass that
 # still needs what they held then raises instead of using what they hold now.
 _written = torch.autograd.graph.increment_version
@@ -686,9 +696,12 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
 
 def layer_norm_backward(g: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
                         weight: torch.Tensor | None = None, need_x: bool = True, need_weight: bool = True,
-                        need_bias: bool = True, param_dtype: torch.dtype | None = None):
+                        need_bias: bool = True, param_dtype: torch.dtype | None = None,
+                        ws: torch.Tensor | None = None):
     """(gx, gw, gb) of ``layer_norm`` (None where not needed).  gw and gb have
-    ``param_dtype`` (default: weight's, else x's)."""
+    ``param_dtype`` (default: weight's, else x's).  ``ws``: a workspace of
+    i8lt_layer_norm_backward_workspace_size bytes, for a caller that reads its
+    ``device_status``."""
     _require_cuda(x)
     shape = x.shape
     dev, dtype, N = x.get_device(), x.dtype, shape[-1]
@@ -710,10 +723,10 @@ def layer_norm_backward(g: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rs
     gw = torch.empty(N, dtype=ptype, device=x.device) if need_weight else None
     gb = torch.empty(N, dtype=ptype, device=x.device) if need_bias else None
     n = _lib.i8lt_layer_norm_backward_workspace_size(M, N)
-    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    ws = _workspace("layer_norm_backward", ws, n, x.device)
     _check(_lib.i8lt_layer_norm_backward(g.data_ptr(), x.data_ptr(), _code(dtype), M, N, mean.data_ptr(),
                                          rstd.data_ptr(), _ptr(weight), _code(ptype), _ptr(gx), _ptr(gw), _ptr(gb),
-                                         ws.data_ptr(), n, _stream(x)), "i8lt_layer_norm_backward")
+                                         ws.data_ptr(), ws.numel(), _stream(x)), "i8lt_layer_norm_backward")
     return gx, gw, gb
 
 
@@ -794,17 +807,16 @@ def _adapter_args(what, tokens, A, B, scale, plan):
     return dev, M, K, E, r, N, A, B, _arg(f"{what} scale", scale, dev, (E,), torch.float32)
 
 
-def _adapter_workspace(M, K, N, E, r, device):
-    return torch.empty(max(_lib.i8lt_adapters_workspace_size(M, K, N, E, r), 256), dtype=torch.uint8, device=device)
-
-
 def adapters_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor | None,
-                     plan: AdapterPlan, base: torch.Tensor | None = None, out: torch.Tensor | None = None):
+                     plan: AdapterPlan, base: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     ws: torch.Tensor | None = None):
     """(y, t) with t = x A[e]^T and y = base + scale[e] t B[e]^T for each
     token's adapter e (i8lt_adapters_forward): x [M, K] (f16 / bf16),
     A [E, r, K], B [E, N, r], scale fp32 [E] or None, base [M, N] or None.
     ``out`` may be base itself (not x).  t [2, M, r], two 16-bit parts of one
-    value with the tokens in the plan's order, is what the backward needs."""
+    value with the tokens in the plan's order, is what the backward needs.
+    ``ws``: a workspace of i8lt_adapters_workspace_size bytes, for a caller
+    that reads its ``device_status``."""
     what = "adapters_forward"
     dev, M, K, E, r, N, A, B, scale = _adapter_args(what, x, A, B, scale, plan)
     dtype, device = x.dtype, x.device
@@ -815,7 +827,7 @@ def adapters_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: t
     else:
         y = torch.empty((M, N), dtype=dtype, device=device) if base is None else torch.empty_like(base)
     t = torch.empty((2, M, r), dtype=dtype, device=device)
-    ws = _adapter_workspace(M, K, N, E, r, device)
+    ws = _workspace(what, ws, _lib.i8lt_adapters_workspace_size(M, K, N, E, r), device)
     _check(_lib.i8lt_adapters_forward(x.data_ptr(), _code(dtype), M, K, A.data_ptr(), B.data_ptr(), E, r, N,
                                       _ptr(scale), plan.data.data_ptr(), _ptr(base), y.data_ptr(), t.data_ptr(),
                                       ws.data_ptr(), ws.numel(), _stream(x)), "i8lt_adapters_forward")
@@ -827,10 +839,10 @@ def adapters_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: t
 def adapters_backward(g: torch.Tensor, x: torch.Tensor | None, t: torch.Tensor | None, A: torch.Tensor,
                       B: torch.Tensor, scale: torch.Tensor | None, plan: AdapterPlan,
                       addend: torch.Tensor | None = None, need_x: bool = True, need_A: bool = True,
-                      need_B: bool = True):
+                      need_B: bool = True, ws: torch.Tensor | None = None):
     """(gx, gA, gB) of ``adapters_forward`` (None where not needed), gx with
     ``addend`` (the shared projection's input gradient) added.  x is used for
-    gA only, t for gB only."""
+    gA only, t for gB only; ``ws`` as in ``adapters_forward``."""
     what = "adapters_backward"
     dev, M, K, E, r, N, A, B, scale = _adapter_args(what, g, A, B, scale, plan)
     if need_A and x is None or need_B and t is None:
@@ -848,7 +860,7 @@ def adapters_backward(g: torch.Tensor, x: torch.Tensor | None, t: torch.Tensor |
         gx = torch.empty((M, K), dtype=dtype, device=device) if like is None else torch.empty_like(like)
     gA = torch.empty_like(A) if need_A else None
     gB = torch.empty_like(B) if need_B else None
-    ws = _adapter_workspace(M, K, N, E, r, device)
+    ws = _workspace(what, ws, _lib.i8lt_adapters_workspace_size(M, K, N, E, r), device)
     _check(_lib.i8lt_adapters_backward(g.data_ptr(), _ptr(x), _ptr(t), _code(dtype), M, K, A.data_ptr(),
                                        B.data_ptr(), E, r, N, _ptr(scale), plan.data.data_ptr(), _ptr(addend),
                                        _ptr(gx), _ptr(gA), _ptr(gB), ws.data_ptr(), ws.numel(), _stream(g)),

@@ -29,3 +29,26 @@ def test_layer_norm_backward_clears_the_status(M, N, need):
     assert _lib.i8lt_layer_norm_backward(x.data_ptr(), x.data_ptr(), 2, M, N, mean.data_ptr(), rstd.data_ptr(), None, 2,
                                          *ptr, ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream) == 0
     assert I.device_status(ws) == (0, 0)
+
+
+def test_callers_may_give_the_workspace_and_read_its_status():
+    x, w = torch.randn(300, 520, device=DEV), torch.randn(520, device=DEV)
+    _, mean, rstd = I.layer_norm(x, w)
+    ws = torch.full((_lib.i8lt_layer_norm_backward_workspace_size(300, 520),), 255, dtype=torch.uint8, device=DEV)
+    ref = I.layer_norm_backward(x, x, mean, rstd, w)
+    got = I.layer_norm_backward(x, x, mean, rstd, w, ws=ws)
+    assert all(torch.equal(a, b) for a, b in zip(ref, got)) and I.device_status(ws) == (0, 0)
+    for M in (0, 20, 700):
+        h, A, B = (torch.randn(*s, device=DEV).half() for s in ((M, 64), (2, 8, 64), (2, 48, 8)))
+        g = torch.randn(M, 48, device=DEV).half()
+        plan = I.adapter_plan((torch.arange(M, device=DEV) % 3 - 1).int(), 2)
+        ws = torch.full((_lib.i8lt_adapters_workspace_size(M, 64, 48, 2, 8),), 255, dtype=torch.uint8, device=DEV)
+        y, t = I.adapters_forward(h, A, B, None, plan, ws=ws)
+        assert I.device_status(ws) == (0, 0)
+        ws.fill_(255)
+        I.adapters_backward(g, h, t, A, B, None, plan, ws=ws)
+        assert I.device_status(ws) == (0, 0)
+        with pytest.raises(I.I8LTError):
+            I.adapters_forward(h, A, B, None, plan, ws=ws[:128])
+    with pytest.raises(I.I8LTError):
+        I.layer_norm_backward(x, x, mean, rstd, w, ws=torch.empty(256, dtype=torch.uint8, device=DEV))
