@@ -488,8 +488,8 @@ int i8lt_absmax8_dequantize(const uint8_t* q, const float* absmax2,
  * All arithmetic is fp32, every output is rounded once; the sums over the
  * tokens are taken in a fixed order (no atomics): equal inputs give equal
  * bits.  M == 0 writes zeros to gw and gb.  The forward has no workspace and
- * no status word: should one of its bounded waits run out, the rows concerned
- * are NaN.
+ * no status word: should one of its bounded waits run out, the rows from there
+ * on that this block was to write are NaN.
  */
 int i8lt_layer_norm_forward(const void* x, int xt, int64_t M, int64_t N,
                             const void* w, const void* b, int wt, float eps,

@@ -256,6 +256,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   return mbar_wait_limit(bar, parity, abort_flag, st, where, sleep_ns, kWaitTimeoutNs);
 }
 
+// The same while a kernel winds down after a wait that ran out: for copies and
+// products already issued, whatever the CTA's abort flag says.
+__device__ __forceinline__ void mbar_wait_out(uint64_t* bar, uint32_t parity, DevStatus* st, int where) {
+  int own = 0;
+  mbar_wait(bar, parity, &own, st, where);
+}
+
 // ---------------------------------------------------------------------------
 // TMA
 // ---------------------------------------------------------------------------

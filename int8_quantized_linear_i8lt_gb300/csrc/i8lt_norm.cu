@@ -3,8 +3,8 @@
 //   h = (x - mean) * rstd, y = h * w + b;
 //   gx = rstd * (g w - mean_n(g w) - h * mean_n(g w h)),
 //   gw = sum_m g h, gb = sum_m g.
-// The forward has no workspace, so no status word: should a wait run out, the
-// rows that it kept from coming are NaN.
+// The forward has no workspace, so no status word: should a wait run out, its
+// block's row and those after it are NaN.
 // Statistics and sums are fp32; each output is rounded once.  Both
 // directions are bound by HBM: the forward reads x and writes y, the backward
 // reads x and g and writes gx, each once; everything between stays in
@@ -161,11 +161,19 @@ struct RingLayout {
   unsigned stages;
 };
 
+// A wait that runs out raises `abort`: nothing more is issued, and the block
+// leaves once the copies under way have landed.
+struct RingSync {
+  uint64_t full[kMaxStages];
+  int64_t issued;   // rows
+  int abort;
+};
+
 template <typename T, int kMats>
 struct Ring {
   const uint8_t* mat[kMats];
   uint8_t* base;
-  uint64_t* full;
+  RingSync* y;
   RingLayout L;
   int64_t N, n0, step, rows;
   unsigned long long end;   // bytes of a matrix
@@ -180,15 +188,22 @@ struct Ring {
   __device__ __forceinline__ unsigned long long stop(unsigned long long b) const {
     return min((b + cols * sizeof(T) + 15ull) & ~15ull, end & ~15ull);
   }
-  __device__ __forceinline__ void issue(int64_t i) {   // one thread
+  __device__ __forceinline__ void issue(int64_t i) {   // one thread, row after row
+    if (*static_cast<volatile int*>(&y->abort)) return;
+    y->issued = i + 1;
     const unsigned long long b = start(i), e = stop(b);
     const uint32_t bytes = e > b ? static_cast<uint32_t>(e - b) : 0u;
     const int s = static_cast<int>(static_cast<unsigned>(i) % L.stages);
-    mbar_arrive_expect_tx(&full[s], kMats * bytes);
+    mbar_arrive_expect_tx(&y->full[s], kMats * bytes);
     if (bytes != 0)
 #pragma unroll
       for (int k = 0; k < kMats; ++k)
-        bulk_load(base + (static_cast<size_t>(s) * kMats + k) * L.slot_bytes, mat[k] + b, bytes, &full[s]);
+        bulk_load(base + (static_cast<size_t>(s) * kMats + k) * L.slot_bytes, mat[k] + b, bytes, &y->full[s]);
+  }
+  __device__ __forceinline__ void wind_down(DevStatus* st) {   // the same thread, at the end
+    if (!*static_cast<volatile int*>(&y->abort)) return;
+    for (int64_t i = max(y->issued - static_cast<int64_t>(L.stages), static_cast<int64_t>(0)); i < y->issued; ++i)
+      mbar_wait_out(&y->full[static_cast<unsigned>(i) % L.stages], static_cast<unsigned>(i) / L.stages & 1, st, 35);
   }
 };
 
@@ -250,9 +265,10 @@ __device__ __forceinline__ void last_elements(const Ring<T, kMats>& r, int64_t i
   __syncthreads();
 }
 
-__device__ __forceinline__ void ring_setup(uint64_t* full, unsigned stages, int* abort_flag) {
-  for (unsigned i = 0; i < stages; ++i) mbar_init(&full[i], 1);
-  *abort_flag = 0;
+__device__ __forceinline__ void ring_setup(RingSync& y, unsigned stages) {
+  for (unsigned i = 0; i < stages; ++i) mbar_init(&y.full[i], 1);
+  y.issued = 0;
+  y.abort = 0;
   fence_mbar_init();
 }
 
@@ -330,17 +346,16 @@ template <typename T, int W, int kLanes, int kE, bool kShift>
 __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel(const ForwardArgs a,
                                                                                 const RingLayout L) {
   extern __shared__ __align__(128) uint8_t stages[];
-  __shared__ uint64_t full[kMaxStages];
+  __shared__ RingSync y;
   __shared__ __align__(16) float scratch[2][kLanes / 32];
-  __shared__ int abort_flag;
   const int tid = threadIdx.x;
   const Shift<W, kShift> shift(blockIdx.x, a.N);
   const int end = shift.end;
-  Ring<T, 1> ring{{static_cast<const uint8_t*>(a.x)}, stages, full, L, a.N, 0, gridDim.x,
+  Ring<T, 1> ring{{static_cast<const uint8_t*>(a.x)}, stages, &y, L, a.N, 0, gridDim.x,
                   (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
                   static_cast<unsigned long long>(a.M) * a.N * sizeof(T), end, shift.first};
   if (tid == 0) {
-    ring_setup(full, L.stages, &abort_flag);
+    ring_setup(y, L.stages);
     for (int64_t i = 0; i < L.stages && i < ring.rows; ++i) ring.issue(i);
   }
   __syncthreads();
@@ -354,10 +369,12 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel
     }
   }
   const float inv_n = 1.0f / static_cast<float>(a.N);
+  float lost = 0.f;   // NaN once a wait of this thread ran out: this row's and all further sums are NaN
   unsigned s = 0;
   uint32_t phase = 0;
   for (int64_t i = 0; i < ring.rows; ++i) {
-    float t = mbar_wait(&full[s], phase, &abort_flag, nullptr, 31) ? 0.f : NAN;   // of the row: all its y is NaN
+    if (!mbar_wait(&y.full[s], phase, &y.abort, nullptr, 31)) lost = NAN;
+    float t = lost;
     if constexpr (kShift) last_elements(ring, i, a.M, s);
     const T* x = reinterpret_cast<const T*>(stages + s * L.slot_bytes);
 #pragma unroll
@@ -394,20 +411,21 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel
     }
     const float r = 1.0f / sqrtf(row_sum<kLanes>(t, scratch[1]) * inv_n + a.eps);
     const int64_t m = ring.row(i);
-    T* y = static_cast<T*>(a.y) + m * a.N - shift.first;
+    T* out = static_cast<T*>(a.y) + m * a.N - shift.first;
 #pragma unroll
     for (int e = 0; e < kE / W; ++e) {
       const int c = (tid + e * kLanes) * W;
       if (c >= end) continue;
 #pragma unroll
       for (int k = 0; k < W; ++k) v[e * W + k] = fmaf(v[e * W + k] * r, w[e * W + k], b[e * W + k]);
-      shift.store(y, c, v + e * W);
+      shift.store(out, c, v + e * W);
     }
     if (tid == 0) {
       if (a.mean != nullptr) a.mean[m] = mu;
       if (a.rstd != nullptr) a.rstd[m] = r;
     }
   }
+  if (tid == 0) ring.wind_down(nullptr);
 }
 
 // Longer rows: three passes over the row's stage in shared memory, w and b
@@ -418,25 +436,26 @@ constexpr int kWideThreads = 1024;
 template <typename T, int W, bool kShift>
 __global__ void __launch_bounds__(kWideThreads) norm_forward_wide_kernel(const ForwardArgs a, const RingLayout L) {
   extern __shared__ __align__(128) uint8_t stages[];
-  __shared__ uint64_t full[kMaxStages];
+  __shared__ RingSync y;
   __shared__ __align__(16) float scratch[2][kWideThreads / 32];
-  __shared__ int abort_flag;
   const int tid = threadIdx.x;
   const Shift<W, kShift> shift(blockIdx.x, a.N);
   const int end = shift.end;
-  Ring<T, 1> ring{{static_cast<const uint8_t*>(a.x)}, stages, full, L, a.N, 0, gridDim.x,
+  Ring<T, 1> ring{{static_cast<const uint8_t*>(a.x)}, stages, &y, L, a.N, 0, gridDim.x,
                   (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
                   static_cast<unsigned long long>(a.M) * a.N * sizeof(T), end, shift.first};
   if (tid == 0) {
-    ring_setup(full, L.stages, &abort_flag);
+    ring_setup(y, L.stages);
     for (int64_t i = 0; i < L.stages && i < ring.rows; ++i) ring.issue(i);
   }
   __syncthreads();
   const float inv_n = 1.0f / static_cast<float>(a.N);
+  float lost = 0.f;   // NaN once a wait of this thread ran out: this row's and all further sums are NaN
   unsigned s = 0;
   uint32_t phase = 0;
   for (int64_t i = 0; i < ring.rows; ++i) {
-    float t = mbar_wait(&full[s], phase, &abort_flag, nullptr, 31) ? 0.f : NAN, v[W];
+    if (!mbar_wait(&y.full[s], phase, &y.abort, nullptr, 31)) lost = NAN;
+    float t = lost, v[W];
     if constexpr (kShift) last_elements(ring, i, a.M, s);
     const T* x = reinterpret_cast<const T*>(stages + s * L.slot_bytes);
 #pragma unroll 4
@@ -461,7 +480,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_forward_wide_kernel(const F
     }
     const float r = 1.0f / sqrtf(row_sum<kWideThreads>(t, scratch[1]) * inv_n + a.eps);
     const int64_t m = ring.row(i);
-    T* y = static_cast<T*>(a.y) + m * a.N - shift.first;
+    T* out = static_cast<T*>(a.y) + m * a.N - shift.first;
 #pragma unroll 4
     for (int c = tid * W; c < end; c += kWideThreads * W) {
       float w[W], b[W];
@@ -470,7 +489,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_forward_wide_kernel(const F
       widen<T, W>(load_pack<T, W>(x + c), v);
 #pragma unroll
       for (int k = 0; k < W; ++k) v[k] = fmaf((v[k] - mu) * r, w[k], b[k]);
-      shift.store(y, c, v);
+      shift.store(out, c, v);
     }
     if (tid == 0) {
       if (a.mean != nullptr) a.mean[m] = mu;
@@ -481,6 +500,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_forward_wide_kernel(const F
       phase ^= 1;
     }
   }
+  if (tid == 0) ring.wind_down(nullptr);
 }
 
 // Rows that do not fit shared memory twice: three passes over global memory
@@ -763,20 +783,19 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
                                                                                  const RingLayout L) {
   extern __shared__ __align__(128) uint8_t stages[];
   constexpr int kWarps = kLanes / 32, kVec = kE / W;
-  __shared__ uint64_t full[kMaxStages];
+  __shared__ RingSync y;
   __shared__ __align__(16) float2 scratch[2][kWarps];
-  __shared__ int abort_flag;
   const int tid = threadIdx.x;
   const Shift<W, kShift> shift(blockIdx.x, a.N);
   const int cols = shift.end;
   Ring<T, 2> ring{{static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.g)},
-                  stages, full, L, a.N, 0, gridDim.x,
+                  stages, &y, L, a.N, 0, gridDim.x,
                   (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
                   static_cast<unsigned long long>(a.M) * a.N * sizeof(T), cols, shift.first};
   const int rows = static_cast<int>(ring.rows);
   zero_tails(ring, kLanes);
   if (tid == 0) {
-    ring_setup(full, L.stages, &abort_flag);
+    ring_setup(y, L.stages);
     if (blockIdx.x == 0) *a.st = DevStatus{0, 0, 0, 0};
     for (int i = 0; i < static_cast<int>(L.stages) && i < rows; ++i) ring.issue(i);
   }
@@ -805,7 +824,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
       mu = *mean;
       r = *rstd;
     }
-    mbar_wait(&full[s], phase, &abort_flag, a.st, 30);
+    mbar_wait(&y.full[s], phase, &y.abort, a.st, 30);
     float h[kE], g[kE], t0 = 0.f, t1 = 0.f;
     if constexpr (kShift) last_elements(ring, i, a.M, s);
     const T* xs = reinterpret_cast<const T*>(stages + 2 * s * L.slot_bytes);
@@ -864,6 +883,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_ring_kerne
     out += gridDim.x * a.N;
   }
   grid_dependents_launch();
+  if (tid == 0) ring.wind_down(a.st);
   if (a.partial == nullptr) return;
   store_sums<W, kLanes, kVec>(reinterpret_cast<float*>(stages), cols, shift.first, static_cast<int>(a.N), aw, ab,
                               a.partial + static_cast<int64_t>(blockIdx.x) * a.N,
@@ -882,10 +902,10 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
                                                                                  const RingLayout L) {
   extern __shared__ __align__(128) uint8_t stages[];
   constexpr int kWarps = kLanes / 32, kVec = kE / W, kSums = 2 * kRows;
-  __shared__ uint64_t full[kMaxStages], sent[4];
+  __shared__ RingSync y;
+  __shared__ uint64_t sent[4];
   __shared__ float scratch[2][kSums][kWarps];
   __shared__ __align__(16) float peer[4][8][kSums];   // the cluster's slice sums of a step, by rank
-  __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ranks = static_cast<int>(gridDim.y), rank = static_cast<int>(blockIdx.y);
   const int64_t n0 = static_cast<int64_t>(rank) * L.cols;
@@ -893,14 +913,14 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
   const int first = static_cast<int>(n0);   // n0, like the slices, in places from the boundary
   const int cols = min(L.cols, shift.end - first);
   Ring<T, 2> ring{{static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.g)},
-                  stages, full, L, a.N, n0, gridDim.x,
+                  stages, &y, L, a.N, n0, gridDim.x,
                   (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x,
                   static_cast<unsigned long long>(a.M) * a.N * sizeof(T), cols, shift.first};
   const int64_t rows = ring.rows, steps = (rows + kRows - 1) / kRows;
   zero_tails(ring, kLanes);
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) mbar_init(&sent[i], 1);
-    ring_setup(full, L.stages, &abort_flag);
+    ring_setup(y, L.stages);
     if (blockIdx.x == 0 && rank == 0) *a.st = DevStatus{0, 0, 0, 0};
     for (int64_t i = 0; i < L.stages && i < rows; ++i) ring.issue(i);
   }
@@ -922,6 +942,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
   const float inv_n = 1.0f / static_cast<float>(a.N);
   const bool want_x = a.gx != nullptr;
   const int lag = ranks > 1 && want_x ? 1 : 0;
+  int64_t armed = 0;   // steps whose sums the peers were told to send (lane 0 of warp 0)
   for (int64_t i = 0; i < steps + lag; ++i) {
     if (i < steps) {
       float sums[kSums];
@@ -931,7 +952,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
         const int64_t row = i * kRows + q;
         if (row >= rows) continue;
         const int s = static_cast<int>(static_cast<unsigned>(row) % L.stages);
-        mbar_wait(&full[s], static_cast<unsigned>(row) / L.stages & 1, &abort_flag, a.st, 30);
+        mbar_wait(&y.full[s], static_cast<unsigned>(row) / L.stages & 1, &y.abort, a.st, 30);
         if constexpr (kShift) last_elements(ring, row, a.M, s);
         if (!want_x) continue;
         const float mu = __ldg(a.mean + ring.row(row)), r = __ldg(a.rstd + ring.row(row));
@@ -971,7 +992,8 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
 #pragma unroll
       for (int o = 16 / kSums; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     }
-    if (lag != 0 && i < steps && warp == 0) {
+    if (lag != 0 && i < steps && warp == 0 && !*static_cast<volatile int*>(&y.abort)) {
+      if (lane == 0) armed = i + 1;
       if (lane == 0) mbar_arrive_expect_tx(&sent[i & 3], 4u * kSums * ranks);
       // lane group v sends value v, lane `sub` of it to rank sub
       if (sub < ranks)
@@ -983,7 +1005,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
     const int64_t j = i - lag;
     if (j < 0) continue;
     if (lag != 0) {
-      mbar_wait(&sent[j & 3], static_cast<uint32_t>(j >> 2) & 1, &abort_flag, a.st, 32);
+      mbar_wait(&sent[j & 3], static_cast<uint32_t>(j >> 2) & 1, &y.abort, a.st, 32);
       total = 0.f;
       for (int k = 0; k < ranks; ++k) total += peer[j & 3][k][v];
     }
@@ -1015,6 +1037,13 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_backward_cluster_ke
       }
     }
   }
+  if (tid == 0) {
+    ring.wind_down(a.st);
+    if (*static_cast<volatile int*>(&y.abort))   // the peers' sums under way, of two steps at most
+      for (int64_t i = max(armed - 2, static_cast<int64_t>(0)); i < armed; ++i)
+        mbar_wait_out(&sent[i & 3], static_cast<uint32_t>(i >> 2) & 1, a.st, 36);
+  }
+  __syncwarp();
   if (ranks > 1) cluster_sync();   // no block leaves while a peer may write to it
   if (a.partial == nullptr) return;
   // this slice's places [0, cols) are the columns from first - shift.first on,
