@@ -414,6 +414,16 @@ __device__ __forceinline__ void sync_setup(Sync& y, uint32_t columns) {
   __syncthreads();
   tc_fence_after();
 }
+// A wait that runs out raises `abort`: every role stops issuing, and before
+// tensor memory is freed and shared memory reused, the copies and products
+// under way are waited for: the last `stages` fetches of `fetched`, counted on
+// full, and the last of `multiplied` products, on done.
+__device__ __forceinline__ bool aborted(const int& flag) { return *static_cast<const volatile int*>(&flag) != 0; }
+__device__ __forceinline__ void wind_down(uint64_t* full, int fetched, uint64_t* done, int multiplied, int stages,
+                                          DevStatus* st) {
+  for (int i = max(0, fetched - stages); i < fetched; ++i) mbar_wait_out(&full[i % stages], (i / stages) & 1, st, 37);
+  if (multiplied > 0) mbar_wait_out(&done[(multiplied - 1) % stages], ((multiplied - 1) / stages) & 1, st, 38);
+}
 __device__ __forceinline__ void sync_end(const Sync& y, uint32_t columns) {
   tc_fence_before();
   __syncthreads();
@@ -554,19 +564,20 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
     }
   };
   uint8_t* stages = smem_raw + (base - smem_u32(smem_raw));
+  int fetched = 0, multiplied = 0;   // steps, by the thread that issues them
   if (kTma && t.row0 >= 0) {
     if (tid == 0) {
-      for (int it = 0; it < n; ++it) {
+      for (int it = 0; it < n; fetched = ++it) {
         const int s = it % kStages;
         uint8_t* xs = stages + s * stage_bytes;
-        if (it >= kStages) mbar_wait(&y.done[s], (it / kStages - 1) & 1, &y.abort, a.st, 20);
+        if (it >= kStages && !mbar_wait(&y.done[s], (it / kStages - 1) & 1, &y.abort, a.st, 20)) break;
         mbar_arrive_expect_tx(&y.full[s], stage_bytes);
         tma_load_2d(xs, &a.tmX, static_cast<int>(column(it)), t.row0, &y.full[s]);
         load_w(it, xs + 128 * kRowBytes, &y.full[s]);
       }
     } else if (tid == 32) {
-      for (int it = 0; it < n; ++it) {
-        mbar_wait(&y.full[it % kStages], (it / kStages) & 1, &y.abort, a.st, 25);
+      for (int it = 0; it < n; multiplied = ++it) {
+        if (!mbar_wait(&y.full[it % kStages], (it / kStages) & 1, &y.abort, a.st, 25)) break;
         tc_fence_after();
         multiply(it);
       }
@@ -589,9 +600,10 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
         return Chunk{xs + swizzled(row, tid & 7), xrow[i], at, row < t.count ? C - at : 0};
       });
       if constexpr (kTma) {
-        if (tid == 0) {
+        if (tid == 0 && !aborted(y.abort)) {
           mbar_arrive_expect_tx(&y.full[s], stage_bytes - 128 * kRowBytes);
           load_w(b, stages + s * stage_bytes + 128 * kRowBytes, &y.full[s]);
+          fetched = b + 1;
         }
       } else if constexpr (kMN) {
         const int chunks = r16 / 8;
@@ -615,9 +627,10 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
       cp_async_wait<kStages - 2>();
       fence_proxy_async_smem();
       __syncthreads();
-      if (tid == 0) {
-        if (kTma) mbar_wait(&y.full[it % kStages], (it / kStages) & 1, &y.abort, a.st, 25);
+      if (tid == 0 && (!kTma || mbar_wait(&y.full[it % kStages], (it / kStages) & 1, &y.abort, a.st, 25)) &&
+          !aborted(y.abort)) {
         multiply(it);
+        multiplied = it + 1;
       }
       const int next = it + kStages - 1;
       if (next < n) {
@@ -635,6 +648,10 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
   grid_dependents_launch();
   float* red = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)));
   __syncthreads();
+  if (aborted(y.abort)) {
+    wind_down(y.full, fetched, y.done, multiplied, kStages, a.st);
+    __syncthreads();
+  }
   spill(y.tmem, r16, red);
   sync_end(y, tmem_columns(r16));
   cluster_sync();
@@ -878,13 +895,15 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
     }
   };
 
+  int fetched = 0, added = 0, multiplied = 0;   // column tiles, by the thread that issues them
   if constexpr (kTma) {
     if (warp == 8) {
       for (int j = 0; j < n; ++j) {
         const int c0 = (j0 + j) * kCols;
-        if (adapter && lane == 0) {
+        if (adapter && lane == 0 && fetched == j &&
+            (j < 2 || mbar_wait(&y.w_free[j & 1], ((j >> 1) - 1) & 1, &y.abort, a.st, 28))) {
+          fetched = j + 1;
           uint8_t* ws = wbuf + (j & 1) * expand_w_bytes(r16);
-          if (j >= 2) mbar_wait(&y.w_free[j & 1], ((j >> 1) - 1) & 1, &y.abort, a.st, 28);
           if constexpr (kMN) {
             mbar_arrive_expect_tx(&y.w_full[j & 1], r16 * kRowBytes);
             tma_load_3d(ws, &a.tmW, c0, 0, t.group, &y.w_full[j & 1]);
@@ -894,9 +913,10 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
               tma_load_3d(ws + k * 64 * kRowBytes, &a.tmW, 64 * k, c0, t.group, &y.w_full[j & 1]);
           }
         }
-        if (a.addend != nullptr && tma_out && lane == 0) {
+        if (a.addend != nullptr && tma_out && lane == 0 && added == j &&
+            (j < bufs || mbar_wait(&y.add_free[j % bufs], (j / bufs - 1) & 1, &y.abort, a.st, 29))) {
+          added = j + 1;
           uint64_t* bar = &y.add_full[j % bufs];
-          if (j >= bufs) mbar_wait(&y.add_free[j % bufs], (j / bufs - 1) & 1, &y.abort, a.st, 29);
           mbar_arrive_expect_tx(bar, kTileBytes);
           tma_load_2d(tiles + (j % bufs) * kTileBytes, &a.tmAdd, c0, t.row0, bar);
         }
@@ -915,11 +935,10 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
         }
       }
     } else if (tid == 288) {
-      if (adapter) {
-        mbar_wait(&y.mid_full, 0, &y.abort, a.st, 30);
-        for (int j = 0; j < n; ++j) {
-          mbar_wait(&y.w_full[j & 1], (j >> 1) & 1, &y.abort, a.st, 31);
-          if (j >= 2) mbar_wait(&y.acc_free[j & 1], ((j >> 1) - 1) & 1, &y.abort, a.st, 32);
+      if (adapter && mbar_wait(&y.mid_full, 0, &y.abort, a.st, 30)) {
+        for (int j = 0; j < n; multiplied = ++j) {
+          if (!mbar_wait(&y.w_full[j & 1], (j >> 1) & 1, &y.abort, a.st, 31)) break;
+          if (j >= 2 && !mbar_wait(&y.acc_free[j & 1], ((j >> 1) - 1) & 1, &y.abort, a.st, 32)) break;
           tc_fence_after();
           multiply(j);
         }
@@ -1019,6 +1038,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
       if (adapter && tid == 0) {
         tc_fence_after();
         multiply(j);
+        multiplied = j + 1;
       }
       __syncwarp();
       if (!ahead) fetch(j + 1);
@@ -1034,6 +1054,12 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
   grid_dependency_wait();   // what follows this kernel may rely on what came before it
   tc_fence_before();
   __syncthreads();
+  if (aborted(y.abort)) {
+    wind_down(y.w_full, fetched, y.acc_full, multiplied, 2, a.st);
+    wind_down(y.add_full, added, nullptr, 0, bufs, a.st);
+    if (fetched > 0) mbar_wait_out(&y.mid_full, 0, a.st, 37);
+    __syncthreads();
+  }
   if (warp == 0) tmem_dealloc(y.tmem, 2 * acc);
 }
 
@@ -1126,6 +1152,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
   // 64 must not reach into other groups' rows of X (whatever they hold would
   // be multiplied by zero): its last token is repeated, and the rows of mid
   // past it are set to zero before its products.
+  int fetched = 0, multiplied = 0;   // steps, by the warps that issue them
   if constexpr (kTma) {
     if (tid < 32) {
       uint8_t* stages = smem_raw + (base - smem_u32(smem_raw));
@@ -1148,7 +1175,10 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
         rows_of(it + 1, next);
         const int row0 = __shfl_sync(0xffffffffu, rows[0], 0);
         const bool box = __all_sync(0xffffffffu, rows[0] == row0 + 4 * quad && rows[3] == rows[0] + 3);   // ascending
-        if (it >= kStages) mbar_wait(&y.done[s], (it / kStages - 1) & 1, &y.abort, a.st, 23);
+        if (it >= kStages &&
+            !__all_sync(0xffffffffu, mbar_wait(&y.done[s], (it / kStages - 1) & 1, &y.abort, a.st, 23)))
+          break;
+        fetched = it + 1;
         if (tid == 0) {
           mbar_arrive_expect_tx(&y.full[s], stage_bytes);
           for (int k = 0; k < 2; ++k) {
@@ -1167,8 +1197,8 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
                       &y.full[s]);
       }
     } else if (tid < 64) {
-      for (int it = 0; it < n; ++it) {
-        mbar_wait(&y.full[it % kStages], (it / kStages) & 1, &y.abort, a.st, 26);
+      for (int it = 0; it < n; multiplied = ++it) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&y.full[it % kStages], (it / kStages) & 1, &y.abort, a.st, 26))) break;
         const int left = tokens - (b0 + it) * 64;
         if (left < 64) {
           uint8_t* us = smem_raw + (base - smem_u32(smem_raw)) + it % kStages * stage_bytes + 2 * 64 * kRowBytes;
@@ -1235,6 +1265,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
       fence_proxy_async_smem();
       __syncthreads();
       if (tid == 0) multiply(it);
+      multiplied = it + 1;
       const int next = it + kStages - 1;
       if (next < n) {
         if (it > 0) mbar_wait(&y.done[(it - 1) % kStages], ((it - 1) / kStages) & 1, &y.abort, a.st, 23);
@@ -1250,6 +1281,10 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
     __syncwarp();
     tc_fence_after();
     __syncthreads();
+    if (aborted(y.abort)) {
+      wind_down(y.full, fetched, y.done, multiplied, kStages, a.st);
+      __syncthreads();
+    }
     spill(y.tmem, r16, red, rest);
   } else {   // a group with fewer token blocks than CTAs
     for (int i = tid; i < 128 * red_pitch(r16); i += kThreads) red[i] = 0.f;
@@ -1358,13 +1393,15 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
   auto is_box = [&](const Strip& t, int it, const int(&e)[2]) {
     return it * 64 + 64 <= t.tokens && e[1] - e[0] == 63;
   };
+  int fetched = 0, multiplied = 0;   // steps, by the threads that issue them
+  bool going = true;                 // false once a wait of this thread ran out
   if (tid == 128) {
     int ends[2] = {0, 0};
     Strip t = strip_of(blockIdx.x);
     ends_of(t, 0, ends);
     bool waited = false;
-    int at = 0;   // steps so far
-    for (int64_t i = blockIdx.x; i < strips; i += step) {
+    int& at = fetched;
+    for (int64_t i = blockIdx.x; i < strips && going; i += step) {
       const Strip after = strip_of(i + step);
       const GradSide& d = a.side[t.second];
       const int n = (t.tokens + 63) / 64, c0 = static_cast<int>(t.c0);
@@ -1378,7 +1415,10 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
         uint8_t *xs = stages + s * stage_bytes, *us = xs + 2 * 64 * kRowBytes;
         if (it + 1 < n) ends_of(t, it + 1, ends);
         else ends_of(after, 0, ends);
-        if (at >= kStages) mbar_wait(&y.done[s], (at / kStages - 1) & 1, &y.abort, a.st, 23);
+        if (at >= kStages && !mbar_wait(&y.done[s], (at / kStages - 1) & 1, &y.abort, a.st, 23)) {
+          going = false;
+          break;
+        }
         mbar_arrive_expect_tx(&y.full[s], box ? stage_bytes : stage_bytes - 2 * 64 * kRowBytes);
         for (int k = 0; k < 2; ++k) {
           uint8_t* u = us + k * grad_mid_bytes(r16);
@@ -1416,7 +1456,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
     Strip t = strip_of(blockIdx.x);
     rows_of(t, 0);
     int at = 0;
-    for (int64_t i = blockIdx.x; i < strips; i += step) {
+    for (int64_t i = blockIdx.x; i < strips && going; i += step) {
       const Strip after = strip_of(i + step);
       const GradSide& d = a.side[t.second];
       const int n = (t.tokens + 63) / 64;
@@ -1430,7 +1470,10 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
         for (int k = 0; k < 8; ++k) rows[k] = next[k];
         if (it + 1 < n) rows_of(t, it + 1);
         else rows_of(after, 0);
-        if (at >= kStages) mbar_wait(&y.done[s], (at / kStages - 1) & 1, &y.abort, a.st, 34);
+        if (at >= kStages && !mbar_wait(&y.done[s], (at / kStages - 1) & 1, &y.abort, a.st, 34)) {
+          going = false;
+          break;
+        }
         if (box) {
           cp_async_wait<0>();
           pass_on();
@@ -1453,18 +1496,21 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
     pass_on();
   } else if (warp == 5) {
     const uint32_t idesc = instruction(r16, true, true, a.bf16);
-    int at = 0, acc = 0;   // steps and strips with tokens so far
+    int& at = multiplied;
+    int acc = 0;   // strips with tokens so far
     Strip t = strip_of(blockIdx.x);
-    for (int64_t i = blockIdx.x; i < strips; i += step) {
+    for (int64_t i = blockIdx.x; i < strips && going; i += step) {
       const Strip after = strip_of(i + step);
       const int n = (t.tokens + 63) / 64;
       if (n > 0 && acc > more) {
-        mbar_wait(&y.acc_free[acc & more], ((acc >> more) - 1) & 1, &y.abort, a.st, 33);
+        going = __all_sync(0xffffffffu, mbar_wait(&y.acc_free[acc & more], ((acc >> more) - 1) & 1, &y.abort, a.st, 33));
+        if (!going) break;
         tc_fence_after();
       }
       for (int it = 0; it < n; ++it, ++at) {
         const int s = at % kStages;
-        mbar_wait(&y.full[s], (at / kStages) & 1, &y.abort, a.st, 26);
+        going = __all_sync(0xffffffffu, mbar_wait(&y.full[s], (at / kStages) & 1, &y.abort, a.st, 26));
+        if (!going) break;
         uint8_t* us = stages + s * stage_bytes + 2 * 64 * kRowBytes;
         const int left = t.tokens - it * 64;
         if (left < 64) {
@@ -1548,6 +1594,10 @@ __global__ void __launch_bounds__(kManyThreads, 2) grad_many_kernel(const __grid
   grid_dependents_launch();
   tc_fence_before();
   __syncthreads();
+  if (aborted(y.abort)) {
+    wind_down(y.full, fetched, y.done, multiplied, kStages, a.st);
+    __syncthreads();
+  }
   if (warp == 0) tmem_dealloc(y.tmem, columns << more);
   // what follows this kernel may rely on what came before it
   grid_dependency_wait();
