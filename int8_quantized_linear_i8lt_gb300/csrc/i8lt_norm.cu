@@ -1122,12 +1122,14 @@ __global__ void __launch_bounds__(1024) norm_grad_sum_kernel(const float* partia
 constexpr int kShortRow = 256;         // columns up to which a warp takes a row
 constexpr int kSliceCols = 8192;       // largest slice of a row per block of the ring kernel
 constexpr int kMaxCluster = 8;
-constexpr int kMaxBlocks = 1216;       // eight blocks of each of 152 SMs
+constexpr int kSms = 152;
 
-// Rows of partial sums the workspace has room for.
+// Rows of partial sums the workspace has room for, and so the most blocks (or
+// clusters) of a launch: those that fit the SMs at once in the length's class.
+// Shifted rows take at least a pack's 8, as far as there are rows.
 int64_t partial_rows(int64_t M, int64_t N) {
-  const int64_t per_block = N <= kShortRow ? 8 : 1;
-  return std::max<int64_t>(1, std::min<int64_t>(kMaxBlocks, ceil_div(M, per_block)));
+  const int64_t per_sm = N <= kShortRow ? 4 : N <= 1024 ? 8 : N <= 2048 ? 4 : N <= 4096 ? 2 : 1;
+  return std::max<int64_t>(1, std::min<int64_t>(kSms * per_sm, N <= kShortRow ? ceil_div(M, 8) : M));
 }
 
 struct Shape {

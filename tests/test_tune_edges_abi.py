@@ -29,3 +29,12 @@ def test_adamw_counted(bits):
     assert call(lr=float("nan")) == _lib.I8LT_ERR_INVALID_ARG and call(pt=3) == _lib.I8LT_ERR_UNSUPPORTED_DTYPE
     assert call(state=None) == _lib.I8LT_ERR_INVALID_ARG and call(count=-1) == _lib.I8LT_ERR_INVALID_ARG
     assert call(count=0, counts=None) == _lib.I8LT_OK and call(sizes=(0, 0)) == _lib.I8LT_OK
+
+
+@pytest.mark.parametrize("M,N,rows", [(32768, 64, 608), (32768, 256, 608), (16384, 1000, 1216), (16384, 2048, 608),
+                                      (8192, 4096, 304), (16384, 8192, 152), (16384, 28672, 152), (1 << 20, 1 << 20, 152),
+                                      (3, 4096, 3), (100, 64, 13), (0, 64, 1)])
+def test_layer_norm_workspace_holds_the_sums_of_the_blocks_that_run(M, N, rows):
+    """Two fp32 sums per column and block: blocks of one residency of 152 SMs."""
+    size = _lib.i8lt_layer_norm_backward_workspace_size(M, N)
+    assert 8 * N <= size - 256 <= 8 * N * rows + 256
