@@ -514,7 +514,8 @@ int i8lt_layer_norm_backward(const void* g, const void* x, int xt, int64_t M,
  *   A and gA [E, r, K], B and gB [E, N, r]: all of dtype dt (I8LT_F16 or
  *   I8LT_BF16, the compute types of the 4-bit layers); index [M] int32;
  *   scale [E] fp32, or NULL (1).  1 <= r <= I8LT_MAX_RANK.
- *   base and addend may be NULL (0) and may be the same buffer as y and gx.
+ *   base and addend may be NULL (0) and may be the same buffer as y and gx; y
+ *   may not be x, nor gx be x or g.
  * Sums are fp32.  Every output takes both parts of t and u; y, gx, gA and gB
  * are rounded once.  An adapter without tokens gets zero gradients.  Equal
  * inputs give equal bits.

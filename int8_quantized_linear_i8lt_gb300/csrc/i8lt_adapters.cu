@@ -2088,6 +2088,7 @@ int i8lt_adapters_forward(const void* x, int dt, int64_t M, int64_t K, const voi
       !aligned256(plan) || !aligned256(ws))
     return I8LT_ERR_MISALIGNED;
   if (ws == nullptr || ws_bytes < i8lt_adapters_workspace_size(M, K, N, E, r)) return I8LT_ERR_WORKSPACE;
+  if (M > 0 && y == x) return I8LT_ERR_INVALID_ARG;   // a tile's y is written while others read x
   if (int d = check_device()) return d;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (M == 0) return cuda_status(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s));
@@ -2110,6 +2111,7 @@ int i8lt_adapters_backward(const void* g, const void* x, const void* t, int dt, 
       !aligned16(gx) || !aligned16(gA) || !aligned16(gB) || !aligned256(plan) || !aligned256(ws))
     return I8LT_ERR_MISALIGNED;
   if (ws == nullptr || ws_bytes < i8lt_adapters_workspace_size(M, K, N, E, r)) return I8LT_ERR_WORKSPACE;
+  if (M > 0 && gx != nullptr && (gx == g || gx == x)) return I8LT_ERR_INVALID_ARG;   // likewise
   if (int d = check_device()) return d;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (M == 0) {   // no tokens: the weight gradients are zeros

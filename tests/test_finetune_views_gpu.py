@@ -194,3 +194,13 @@ def test_second_derivatives_are_refused():
         g, = torch.autograd.grad(y, x, create_graph=True)
         with pytest.raises(RuntimeError, match="once_differentiable"):
             (y + (g.float() ** 2).sum()).backward()
+
+
+@pytest.mark.parametrize("M", [20, 700])
+def test_an_output_over_the_tokens_is_refused(M):
+    x, plan = _normal(M, 64), I.adapter_plan(None, 1, M, DEV)
+    A, B = _normal(1, 8, 64, seed=1), _normal(1, 64, 8, seed=2)
+    with pytest.raises(I.I8LTError):
+        I.adapters_forward(x, A, B, None, plan, out=x)
+    y, _ = I.adapters_forward(x, A, B, None, plan, base=x)
+    assert torch.equal(I.adapters_forward(x, A, B, None, plan, base=x.clone())[0], y)

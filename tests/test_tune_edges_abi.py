@@ -38,3 +38,15 @@ def test_layer_norm_workspace_holds_the_sums_of_the_blocks_that_run(M, N, rows):
     """Two fp32 sums per column and block: blocks of one residency of 152 SMs."""
     size = _lib.i8lt_layer_norm_backward_workspace_size(M, N)
     assert 8 * N <= size - 256 <= 8 * N * rows + 256
+
+
+def test_adapters_outputs_over_their_inputs():
+    def fwd(x, y, M=4):
+        return _lib.i8lt_adapters_forward(x, 0, M, 8, P, P, 2, 8, 8, P, P, P, y, P, P, 1 << 40)
+
+    def bwd(g, x, gx, gA=P):
+        return _lib.i8lt_adapters_backward(g, x, P, 0, 4, 8, P, P, 2, 8, 8, P, P, P, gx, gA, P, P, 1 << 40)
+
+    for call in (lambda: fwd(P, P), lambda: bwd(P, P + 4096, P), lambda: bwd(P + 4096, P, P),
+                 lambda: bwd(P, None, P, gA=None)):
+        assert call() == _lib.I8LT_ERR_INVALID_ARG
