@@ -236,6 +236,7 @@ def silu_backward(g: torch.Tensor, h: torch.Tensor) -> torch.Tensor:
 def device_status(ws: torch.Tensor):
     """(status code, outlier columns found) of the last call that used ``ws``
     (synchronizes the current stream; clears a recorded error)."""
+    _require_cuda(ws)
     r, st, found = _lib.i8lt_read_device_status(ws.data_ptr(), _stream(ws))
     return st, found
 

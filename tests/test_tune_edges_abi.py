@@ -50,3 +50,10 @@ def test_adapters_outputs_over_their_inputs():
     for call in (lambda: fwd(P, P), lambda: bwd(P, P + 4096, P), lambda: bwd(P + 4096, P, P),
                  lambda: bwd(P, None, P, gA=None)):
         assert call() == _lib.I8LT_ERR_INVALID_ARG
+
+
+def test_device_status_of_host_memory_is_refused():
+    torch = pytest.importorskip("torch")
+    import int8_quantized_linear_i8lt_gb300 as I
+    with pytest.raises(I.I8LTError):
+        I.device_status(torch.zeros(256, dtype=torch.uint8))
