@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constan
 // bytes of states per element the arithmetic weighs as much as HBM: two
 // blocks are loaded before either is worked on, and the codes of zero are
 // behind a branch that a block without them does not take.  90 million f16
-// parameters: 185 us, 4.9 TB/s.
+// parameters: 186 us, 4.9 TB/s, with neither HBM nor issue saturated: 64
+// registers a thread, and spills.
 template <int kCap, typename P, typename G, bool kCounted>
 __global__ void __launch_bounds__(kWarps * 32, 4) adamw8_kernel(const __grid_constant__ TensorList<kCap> L,
                                                                 const __grid_constant__ Hyper h, uint8_t* mv,

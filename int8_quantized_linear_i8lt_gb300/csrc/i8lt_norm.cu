@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kLanes > 32 ? kLanes : 256) norm_forward_row_k
 
 // Rows of up to 8192 elements (shifted: 16384): 32 elements, and their w and
 // b, in each thread's registers (16 in rows of up to 1024).  Bound by HBM:
-// 16384 x 8192 bf16 takes 90 us, 6.0 TB/s.
+// 16384 x 8192 bf16 takes 88 us, 6.1 TB/s.
 template <typename T, int W, int kLanes, int kE, bool kShift>
 __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel(const ForwardArgs a,
                                                                                 const RingLayout L) {
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kLanes, 512 / kLanes) norm_forward_ring_kernel
 
 // Longer rows: three passes over the row's stage in shared memory, w and b
 // from L2 (registers do not hold them).  Bound by these passes: 4096 x 28672
-// bf16 takes 134 us, 3.5 TB/s; shifted, where w and b are read singly, 4096 x
+// bf16 takes 135 us, 3.5 TB/s; shifted, where w and b are read singly, 4096 x
 // 21003 takes 191 us.
 constexpr int kWideThreads = 1024;
 template <typename T, int W, bool kShift>

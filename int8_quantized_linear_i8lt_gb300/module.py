@@ -233,7 +233,7 @@ class LowRankAdapters(torch.nn.Module):
 
 
 class AdamW:
-    """AdamW over all its parameters in one launch per dtype, with the states
+    """AdamW over all its parameters at once per dtype, with the states
     in 32 bits or (``bits=8``) as FP8 E4M3 with one fp32 absmax per 256
     elements.  A parameter without a gradient is left as it is.  step() takes
     the optional device scalars of a loss scaler or a gradient clip:
