@@ -516,9 +516,9 @@ int i8lt_layer_norm_backward(const void* g, const void* x, int xt, int64_t M,
  *   scale [E] fp32, or NULL (1).  1 <= r <= I8LT_MAX_RANK.
  *   base and addend may be NULL (0) and may be the same buffer as y and gx; y
  *   may not be x, nor gx be x or g.
- * Sums are fp32.  Every output takes both parts of t and u; y, gx, gA and gB
- * are rounded once.  An adapter without tokens gets zero gradients.  Equal
- * inputs give equal bits.
+ * Sums are fp32.  Every output takes both parts of t and u (in fp16 a t or u
+ * beyond 65504 is infinite); y, gx, gA and gB are rounded once.  An adapter
+ * without tokens gets zero gradients.  Equal inputs give equal bits.
  *
  * i8lt_adapter_plan sorts the tokens of a batch by adapter (on the device,
  * asynchronously) into `plan` (i8lt_adapter_plan_bytes(M, E) bytes, 256-byte
