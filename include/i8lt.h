@@ -616,6 +616,115 @@ int i8lt_adamw_step_8bit_counted(void* const* params, int pt,
                                  double weight_decay, const float* grad_scale,
                                  const float* found_inf, void* stream);
 
+/*
+ * The norm of all gradients of a step, and the factor that clips it:
+ *   norm  = |c| sqrt(sum over all tensors of g^2)
+ *   scale = c min(1, max_norm / (norm + 1e-6))
+ *   grads, dtypes, sizes   HOST arrays of `count` device pointers, dtypes
+ *            (each its own) and element counts, read during the call; each
+ *            tensor aligned to its element; one with a NULL pointer is left
+ *            out
+ *   grad_scale  c, an optional device fp32 scalar (NULL: 1), e.g. 1 / loss
+ *            scale
+ *   found_inf   optional device fp32 scalar, passed on
+ *   max_norm >= 0; infinity: scale is c
+ *   result   fp32 [3], device: norm, scale and found_inf (1 when the norm is
+ *            not finite in fp32 or *found_inf is not 0, else 0): the
+ *            grad_scale and found_inf of the AdamW step.  A norm that is a
+ *            NaN makes scale one; an infinite one makes it 0.
+ *   ws       i8lt_grad_norm_workspace_size() bytes of scratch, 256-byte
+ *            aligned (no status word)
+ * Squares are summed in fp32 over 32 elements, then in fp64; no square that a
+ * finite gradient gives overflows.  The sums have a fixed order: equal inputs
+ * (and alignments) give equal bits.
+ *
+ * i8lt_scale_grads: g *= *scale in place, rounded once, over all tensors
+ * (none may overlap another; a device scale of 1 reads and writes nothing).
+ */
+size_t i8lt_grad_norm_workspace_size(void);
+int i8lt_grad_norm(const void* const* grads, const int32_t* dtypes,
+                   const int64_t* sizes, int64_t count,
+                   const float* grad_scale, const float* found_inf,
+                   double max_norm, float* result, void* ws, size_t ws_bytes,
+                   void* stream);
+int i8lt_scale_grads(void* const* grads, const int32_t* dtypes,
+                     const int64_t* sizes, int64_t count, const float* scale,
+                     void* stream);
+
+/*
+ * ---- Block-scaled FP8 linear layers ---------------------------------------
+ *
+ * E4M3 codes (1 sign, 4 exponent bits with bias 7, 3 mantissa bits, largest
+ * finite 448) with one fp32 scale per block: 128 columns of a token's row,
+ * 128 x 128 of a weight.  For every block
+ *   a = max |x|, r = fp32(448 / a) (0 when a < 2^-100),
+ *   code = E4M3(fp32(x r)), nearest, ties to even; scale = fp32(a fp32(1/448))
+ * and a NaN or an infinity makes what is computed from its block NaN (or
+ * infinite, where only the scale of a block is).
+ *   codes of tokens   [M, i8lt_fp8_ld(C)] u8, columns past C zero
+ *   scales of tokens  [i8lt_fp8_blocks(C), M] fp32: a block's scales of
+ *                     consecutive tokens are consecutive
+ *   codes of weights  [E, N, i8lt_fp8_ld(K)] u8, columns past K zero
+ *   scales of weights [E, i8lt_fp8_blocks(N), i8lt_fp8_blocks(K)] fp32
+ * i8lt_fp8_quantize: x [M, C] (dtype xt, any of the three) -> codes, scales.
+ * i8lt_fp8_quantize_weight: W [E, N, K] (dtype wt) -> codes, scales; E = 1 for
+ *   one weight, at most I8LT_FP8_MAX_EXPERTS.
+ * i8lt_fp8_dequantize_weight: fp32(code * scale) as dt, [E, N, K].
+ *
+ * The layer (x, y, g, gx of one dtype, I8LT_F16 or I8LT_BF16):
+ *   i8lt_fp8_forward         y [M, N] = x [M, K] W^T + bias [N] (dtype bt, or
+ *                            NULL), x quantized along K
+ *   i8lt_fp8_backward_input  grad_x [M, K] = g [M, N] W, g quantized along N,
+ *                            and grad_bias [N] (dtype bt) = the sum of the
+ *                            unquantized g over the tokens; each may be NULL,
+ *                            not both
+ * Products of codes are accumulated in fp32 over a block's 128 columns, and
+ * each block's sum times the two scales is added in fp32, in order; the output
+ * is rounded once.
+ * For experts, tokens sorted by expert: rows offsets[e] <= m < offsets[e + 1]
+ * take weight e (offsets [E + 1] int32, device memory, ascending; a value
+ * below the one before it, or outside [0, M], counts as the nearest that is
+ * not).  Rows of no expert (before the first, behind the last) are left as
+ * they are in the output, or written as zeros when zero_rest is not 0.
+ *   ws   i8lt_fp8_workspace_size(M, C) bytes, 256-byte aligned, status word
+ *        first, C the reduction (K forward, N backward); with grad_bias,
+ *        i8lt_fp8_grad_bias_bytes(M, N) more
+ * out may not overlap an input.
+ */
+#define I8LT_FP8_MAX_EXPERTS 1024
+int64_t i8lt_fp8_ld(int64_t C);
+int64_t i8lt_fp8_blocks(int64_t C);
+int i8lt_fp8_quantize(const void* x, int xt, int64_t M, int64_t C,
+                      uint8_t* codes, float* scales, void* stream);
+int i8lt_fp8_quantize_weight(const void* W, int wt, int64_t E, int64_t N,
+                             int64_t K, uint8_t* codes, float* scales,
+                             void* stream);
+int i8lt_fp8_dequantize_weight(const uint8_t* codes, const float* scales,
+                               int64_t E, int64_t N, int64_t K, void* out,
+                               int dt, void* stream);
+size_t i8lt_fp8_workspace_size(int64_t M, int64_t C);
+size_t i8lt_fp8_grad_bias_bytes(int64_t M, int64_t N);
+int i8lt_fp8_forward(const void* x, int xt, int64_t M, const uint8_t* codes,
+                     const float* scales, int64_t N, int64_t K,
+                     const void* bias, int bt, void* out, void* ws,
+                     size_t ws_bytes, void* stream);
+int i8lt_fp8_backward_input(const void* g, int gt, int64_t M,
+                            const uint8_t* codes, const float* scales,
+                            int64_t N, int64_t K, void* grad_x,
+                            void* grad_bias, int bt, void* ws, size_t ws_bytes,
+                            void* stream);
+int i8lt_fp8_experts_forward(const void* x, int xt, int64_t M,
+                             const uint8_t* codes, const float* scales,
+                             int64_t E, int64_t N, int64_t K,
+                             const int32_t* offsets, int zero_rest, void* out,
+                             void* ws, size_t ws_bytes, void* stream);
+int i8lt_fp8_experts_backward_input(const void* g, int gt, int64_t M,
+                                    const uint8_t* codes, const float* scales,
+                                    int64_t E, int64_t N, int64_t K,
+                                    const int32_t* offsets, int zero_rest,
+                                    void* grad_x, void* ws, size_t ws_bytes,
+                                    void* stream);
+
 /* SiLU between the two layers of an MLP: out = h * sigmoid(h), and its
  * backward out = g * silu'(h).  n elements of dtype dt. */
 int i8lt_silu_forward(const void* h, int dt, int64_t n, void* out, void* stream);
@@ -637,7 +746,8 @@ typedef enum {
   I8LT_K_DEQUANT_WEIGHT = 12, I8LT_K_COL_QUANTIZE = 13, I8LT_K_WGRAD_GEMM = 14, I8LT_K_UNIT_PLAN = 15,
   I8LT_K_NF4_QUANTIZE = 16, I8LT_K_NF4_DEQUANTIZE = 17, I8LT_K_NF4_GEMM_FWD = 18, I8LT_K_NF4_GEMM_BWD = 19,
   I8LT_K_ABSMAX8 = 20, I8LT_K_LAYER_NORM = 21, I8LT_K_LAYER_NORM_BWD = 22, I8LT_K_LAYER_NORM_GRAD_SUM = 23,
-  I8LT_K_ADAPTER_PLAN = 24, I8LT_K_ADAPTERS = 25, I8LT_K_ADAPTERS_GRAD = 26, I8LT_K_ADAMW = 27, I8LT_K_COUNT = 28
+  I8LT_K_ADAPTER_PLAN = 24, I8LT_K_ADAPTERS = 25, I8LT_K_ADAPTERS_GRAD = 26, I8LT_K_ADAMW = 27,
+  I8LT_K_FP8_QUANTIZE = 28, I8LT_K_FP8_GEMM = 29, I8LT_K_GRAD_NORM = 30, I8LT_K_SCALE_GRADS = 31, I8LT_K_COUNT = 32
 } i8lt_kernel_id;
 typedef struct {
   int kernel;

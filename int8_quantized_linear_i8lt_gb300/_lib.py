@@ -34,6 +34,7 @@ I8LT_F16, I8LT_BF16, I8LT_F32 = 0, 1, 2
 I8LT_MAX_K = 133144
 I8LT_MAX_RANK = 128
 I8LT_ADAMW_BLOCK = 256
+I8LT_FP8_MAX_EXPERTS = 1024
 
 
 class i8lt_fwd_layout(Structure):
@@ -55,7 +56,7 @@ KERNELS = ("quantize_weight", "colmax", "outlier_index", "row_quantize", "build_
            "gradout_prepass", "grad_bias_finalize", "bwd_gemm", "silu", "silu_backward", "widen_codes",
            "dequant_weight", "col_quantize", "wgrad_gemm", "unit_plan", "nf4_quantize", "nf4_dequantize",
            "nf4_gemm_fwd", "nf4_gemm_bwd", "absmax8", "layer_norm", "layer_norm_backward", "layer_norm_grad_sum",
-           "adapter_plan", "adapters", "adapters_grad", "adamw")
+           "adapter_plan", "adapters", "adapters_grad", "adamw", "fp8_quantize", "fp8_gemm", "grad_norm", "scale_grads")
 
 
 # name -> (restype, argtypes); the same names and order as include/i8lt.h
@@ -138,6 +139,25 @@ SIGNATURES = {
     "i8lt_adamw_step_8bit_counted": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_int64, c_void_p, c_void_p,
                                              c_void_p, c_void_p, c_void_p, c_double, c_double, c_double, c_double,
                                              c_double, c_void_p, c_void_p, c_void_p]),
+    "i8lt_grad_norm_workspace_size": (c_size_t, []),
+    "i8lt_grad_norm": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_double, c_void_p, c_void_p,
+                               c_size_t, c_void_p]),
+    "i8lt_scale_grads": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p]),
+    "i8lt_fp8_ld": (c_int64, [c_int64]),
+    "i8lt_fp8_blocks": (c_int64, [c_int64]),
+    "i8lt_fp8_quantize": (c_int, [c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p, c_void_p]),
+    "i8lt_fp8_quantize_weight": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p]),
+    "i8lt_fp8_dequantize_weight": (c_int, [c_void_p, c_void_p, c_int64, c_int64, c_int64, c_void_p, c_int, c_void_p]),
+    "i8lt_fp8_workspace_size": (c_size_t, [c_int64, c_int64]),
+    "i8lt_fp8_grad_bias_bytes": (c_size_t, [c_int64, c_int64]),
+    "i8lt_fp8_forward": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int,
+                                 c_void_p, c_void_p, c_size_t, c_void_p]),
+    "i8lt_fp8_backward_input": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_void_p, c_int64, c_int64, c_void_p,
+                                        c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
+    "i8lt_fp8_experts_forward": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_void_p, c_int64, c_int64, c_int64,
+                                         c_void_p, c_int, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "i8lt_fp8_experts_backward_input": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_void_p, c_int64, c_int64, c_int64,
+                                                c_void_p, c_int, c_void_p, c_void_p, c_size_t, c_void_p]),
     "i8lt_silu_forward": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_void_p]),
     "i8lt_silu_backward": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_void_p, c_void_p]),
     "i8lt_profile_start": (c_int, [c_int]),
@@ -429,6 +449,74 @@ def i8lt_adamw_step_8bit_counted(params, pt, grads, gt, sizes, count, m, m_absma
                                  beta2, eps, weight_decay, grad_scale=None, found_inf=None, stream=None) -> int:
     return load().i8lt_adamw_step_8bit_counted(params, pt, grads, gt, sizes, count, m, m_absmax, r, r_absmax, counts,
                                                lr, beta1, beta2, eps, weight_decay, grad_scale, found_inf, stream)
+
+
+def i8lt_grad_norm_workspace_size() -> int:
+    return load().i8lt_grad_norm_workspace_size()
+
+
+def i8lt_grad_norm(grads, dtypes, sizes, count, grad_scale, found_inf, max_norm, result, ws, ws_bytes,
+                   stream=None) -> int:
+    """grads, dtypes, sizes: arrays of device addresses, int32 and int64
+    (ctypes arrays, or the addresses of such)."""
+    return load().i8lt_grad_norm(grads, dtypes, sizes, count, grad_scale, found_inf, max_norm, result, ws, ws_bytes,
+                                 stream)
+
+
+def i8lt_scale_grads(grads, dtypes, sizes, count, scale, stream=None) -> int:
+    return load().i8lt_scale_grads(grads, dtypes, sizes, count, scale, stream)
+
+
+@functools.lru_cache(maxsize=1024)   # a function of the size alone
+def i8lt_fp8_ld(C) -> int:
+    return load().i8lt_fp8_ld(C)
+
+
+@functools.lru_cache(maxsize=1024)   # a function of the size alone
+def i8lt_fp8_blocks(C) -> int:
+    return load().i8lt_fp8_blocks(C)
+
+
+def i8lt_fp8_quantize(x, xt, M, C, codes, scales, stream=None) -> int:
+    return load().i8lt_fp8_quantize(x, xt, M, C, codes, scales, stream)
+
+
+def i8lt_fp8_quantize_weight(W, wt, E, N, K, codes, scales, stream=None) -> int:
+    return load().i8lt_fp8_quantize_weight(W, wt, E, N, K, codes, scales, stream)
+
+
+def i8lt_fp8_dequantize_weight(codes, scales, E, N, K, out, dt, stream=None) -> int:
+    return load().i8lt_fp8_dequantize_weight(codes, scales, E, N, K, out, dt, stream)
+
+
+@functools.lru_cache(maxsize=1024)   # a function of the sizes alone
+def i8lt_fp8_workspace_size(M, C) -> int:
+    return load().i8lt_fp8_workspace_size(M, C)
+
+
+@functools.lru_cache(maxsize=1024)   # a function of the sizes alone
+def i8lt_fp8_grad_bias_bytes(M, N) -> int:
+    return load().i8lt_fp8_grad_bias_bytes(M, N)
+
+
+def i8lt_fp8_forward(x, xt, M, codes, scales, N, K, bias, bt, out, ws, ws_bytes, stream=None) -> int:
+    return load().i8lt_fp8_forward(x, xt, M, codes, scales, N, K, bias, bt, out, ws, ws_bytes, stream)
+
+
+def i8lt_fp8_backward_input(g, gt, M, codes, scales, N, K, grad_x, grad_bias, bt, ws, ws_bytes, stream=None) -> int:
+    return load().i8lt_fp8_backward_input(g, gt, M, codes, scales, N, K, grad_x, grad_bias, bt, ws, ws_bytes, stream)
+
+
+def i8lt_fp8_experts_forward(x, xt, M, codes, scales, E, N, K, offsets, zero_rest, out, ws, ws_bytes,
+                             stream=None) -> int:
+    return load().i8lt_fp8_experts_forward(x, xt, M, codes, scales, E, N, K, offsets, zero_rest, out, ws, ws_bytes,
+                                           stream)
+
+
+def i8lt_fp8_experts_backward_input(g, gt, M, codes, scales, E, N, K, offsets, zero_rest, grad_x, ws, ws_bytes,
+                                    stream=None) -> int:
+    return load().i8lt_fp8_experts_backward_input(g, gt, M, codes, scales, E, N, K, offsets, zero_rest, grad_x, ws,
+                                                  ws_bytes, stream)
 
 
 def i8lt_silu_forward(h, dt, n, out, stream=None) -> int:

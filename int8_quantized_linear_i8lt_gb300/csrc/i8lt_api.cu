@@ -870,7 +870,8 @@ const char* i8lt_kernel_name(int k) {
                                 "dequant_weight",  "col_quantize",    "wgrad_gemm",         "unit_plan",
                                 "nf4_quantize",    "nf4_dequantize",  "nf4_gemm_fwd",       "nf4_gemm_bwd",
                                 "absmax8",        "layer_norm",    "layer_norm_backward", "layer_norm_grad_sum",
-                                "adapter_plan",   "adapters",      "adapters_grad",      "adamw"};
+                                "adapter_plan",   "adapters",      "adapters_grad",      "adamw",
+                                "fp8_quantize",   "fp8_gemm",      "grad_norm",          "scale_grads"};
   return (k >= 0 && k < K_COUNT) ? names[k] : "unknown";
 }
 

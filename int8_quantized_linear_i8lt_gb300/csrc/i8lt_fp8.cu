@@ -1,0 +1,671 @@
+// Block-scaled FP8 linear layer (sm_103a): E4M3 codes with one fp32 scale per
+// 128 columns of a row (tokens) and per 128 x 128 block (weight), multiplied
+// on the FP8 tensor cores; one weight, or one per expert with the tokens of
+// an expert in consecutive rows.
+//
+//   quantising a block:  a = max |x|, r = fp32(448 / a) (0 for a < 2^-100),
+//                        code = E4M3(fp32(x r)), scale = fp32(a fp32(1/448))
+//   forward   y[m, n] = sum_b sx[m, b] sw[n / 128, b] sum_(k in b) qx[m, k] qw[n, k] + bias[n]
+//   backward gx[m, k] = sum_b sg[m, b] sw[b, k / 128] sum_(n in b) qg[m, n] qw[n, k]
+//
+// Both products are D[m, r] = sum_b s[m, b] w[r / 128, b] sum_(c in b) X[m, c] W(r, c)
+// with R outputs and a reduction over C; the backward reads the same weight
+// codes as an MN-major operand, so no transposed copy is kept.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "i8lt.h"
+#include "i8lt_internal.h"
+
+namespace i8lt {
+namespace {
+
+constexpr int kBlk = 128;            // columns (of a weight: and rows) per scale
+constexpr float kE4M3Max = 448.0f;
+constexpr float kTinyMax = 0x1p-100f;   // blocks below it are blocks of zeros: 448 / a could overflow
+constexpr int kMaxExperts = 1024;
+
+int64_t code_ld(int64_t C) { return round_up(C, 16); }
+
+// ---------------------------------------------------------------------------
+// quantising
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// 448 / a, and 0 for a block of zeros (for a NaN, too: NaN * 0 stays NaN).
+__device__ __forceinline__ float code_scale(float a) { return a >= kTinyMax ? __fdiv_rn(kE4M3Max, a) : 0.f; }
+__device__ __forceinline__ float block_scale(float a) { return __fmul_rn(a, 1.0f / kE4M3Max); }
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// Rows.  A thread takes 16 consecutive columns, 8 threads a block of 128, a
+// warp 512 columns of one row; the maximum is taken over the bits of |x|, so
+// that a NaN stands above all.  Bound by HBM: 2 bytes read and 1 written per
+// element.
+template <typename T>
+__global__ void __launch_bounds__(256) fp8_quantize_kernel(const T* __restrict__ x, int64_t M, int C, int ld, bool vec,
+                                                           uint8_t* __restrict__ codes, float* __restrict__ scales,
+                                                           DevStatus* st) {
+  grid_dependents_launch();
+  if (st != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *st = DevStatus{0, 0, 0, 0};
+  const int lane = threadIdx.x & 31;
+  const int segs = (C + 511) / 512;
+  const int64_t items = M * segs, step = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items; it += step) {
+    const int64_t m = it / segs;
+    const int c = static_cast<int>(it - m * segs) * 512 + lane * 16;
+    float f[16];
+    const T* p = x + m * C + c;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float (&g)[8] = *reinterpret_cast<float (*)[8]>(f + 8 * h);
+      load8_float(p + 8 * h, C - c - 8 * h, vec && c + 8 * h + 8 <= C, g);
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, abs_bits(f[i]));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float a = __uint_as_float(top), r = code_scale(a);
+    if (c < ld) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) f[i] = __fmul_rn(f[i], r);
+      uint4 q;
+      q.x = encode4(f[0], f[1], f[2], f[3]);
+      q.y = encode4(f[4], f[5], f[6], f[7]);
+      q.z = encode4(f[8], f[9], f[10], f[11]);
+      q.w = encode4(f[12], f[13], f[14], f[15]);
+      *reinterpret_cast<uint4*>(codes + m * ld + c) = q;
+      if ((lane & 7) == 0) scales[static_cast<int64_t>(c / kBlk) * M + m] = block_scale(a);
+    }
+  }
+}
+
+// Weights: one thread block per block of 128 x 128 (once per weight).
+template <typename T>
+__global__ void __launch_bounds__(256) fp8_quantize_weight_kernel(const T* __restrict__ W, int N, int K, int ld,
+                                                                  uint8_t* __restrict__ codes,
+                                                                  float* __restrict__ scales) {
+  __shared__ uint32_t top_s;
+  const int kb = static_cast<int>(gridDim.x), nb = static_cast<int>(gridDim.y);
+  const int k0 = blockIdx.x * kBlk, n0 = blockIdx.y * kBlk;
+  const T* w = W + static_cast<int64_t>(blockIdx.z) * N * K;
+  if (threadIdx.x == 0) top_s = 0;
+  __syncthreads();
+  const int k = k0 + (threadIdx.x & 127);
+  uint32_t top = 0;
+  for (int i = threadIdx.x >> 7; i < kBlk; i += 2)
+    if (k < K && n0 + i < N) top = max(top, abs_bits(to_float(w[static_cast<int64_t>(n0 + i) * K + k])));
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) atomicMax(&top_s, top);
+  __syncthreads();
+  const float a = __uint_as_float(top_s), r = code_scale(a);
+  if (threadIdx.x == 0)
+    scales[(static_cast<int64_t>(blockIdx.z) * nb + blockIdx.y) * kb + blockIdx.x] = block_scale(a);
+  uint8_t* q = codes + static_cast<int64_t>(blockIdx.z) * N * ld;
+  for (int i = threadIdx.x >> 7; i < kBlk; i += 2) {
+    const int n = n0 + i;
+    if (k < ld && n < N) {
+      const float f = k < K ? to_float(w[static_cast<int64_t>(n) * K + k]) : 0.f;
+      q[static_cast<int64_t>(n) * ld + k] = __nv_cvt_float_to_fp8(__fmul_rn(f, r), __NV_SATFINITE, __NV_E4M3);
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) fp8_dequantize_weight_kernel(const uint8_t* __restrict__ codes,
+                                                                    const float* __restrict__ scales, int64_t rows,
+                                                                    int N, int K, int ld, T* __restrict__ out) {
+  const int kb = (K + kBlk - 1) / kBlk, nb = (N + kBlk - 1) / kBlk;
+  const int64_t total = rows * K, step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += step) {
+    const int64_t row = i / K;
+    const int k = static_cast<int>(i - row * K);
+    const int64_t e = row / N;
+    const int n = static_cast<int>(row - e * N);
+    const float s = scales[(e * nb + n / kBlk) * kb + k / kBlk];
+    const __half v(__nv_cvt_fp8_to_halfraw(codes[row * ld + k], __NV_E4M3));
+    out[i] = from_float<T>(__fmul_rn(__half2float(v), s));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// products
+// ---------------------------------------------------------------------------
+
+struct Product {
+  CUtensorMap tmX;           // codes of the tokens [M, ld(C)], box 128 columns x 128 rows
+  CUtensorMap tmW;           // codes of the weight [E][N, ld(K)], box 128 k x 128 n
+  const float* xs;           // scales of the tokens [ceil(C / 128)][M]
+  const float* ws;           // scales of the weight [E][ceil(N / 128)][ceil(K / 128)]
+  const int32_t* offsets;    // [E + 1] row ranges of the experts, or NULL: one weight for all rows
+  const void* bias;          // [R], or NULL
+  void* out;                 // [M, R]
+  DevStatus* st;
+  int M, R, C, E;
+  int nb, kb;                // blocks of the weight along N and K
+  int bias_dt;
+  bool bf16;                 // type of out: bf16, else fp16
+  bool vec;                  // rows of out start on 16 bytes
+  bool zero_rest;            // rows of no expert are written as zeros (else left as they are)
+};
+
+constexpr int kTileM = 128, kTileR = 128;
+constexpr int kStages = 6;
+constexpr int kTileBytes = 128 * 128;
+constexpr int kStageBytes = 2 * kTileBytes;
+constexpr int kThreads = 192;
+constexpr int kEpiWarp0 = 2;         // warps 2 to 5: lanes 32 (w % 4) of the accumulators
+constexpr int kStoreBytes = 4096;    // per epilogue warp: 32 rows of 128 bytes on their way out
+enum { kWhereFetch = 1, kWhereProduct = 2, kWhereOut = 3 };
+
+struct Shared {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t last;                     // all products have completed
+  uint32_t tmem;
+  int abort;
+  float bias[4][kTileR];
+};
+// of several experts: their first rows and first token tiles
+struct Groups {
+  int begin[kMaxExperts + 1];        // begin[E]: the end of the last expert's rows
+  int tile[kMaxExperts + 1];
+};
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 4 * kStoreBytes + static_cast<int>(sizeof(Shared));
+
+__device__ __forceinline__ void umma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The row ranges of the experts, by one warp.  They are data: each start is
+// taken as at least the one before it and at most M, so that no range leaves
+// the tokens or overlaps another one whatever the values are.
+__device__ __forceinline__ void plan_groups(const Product& p, Groups& g, int lane) {
+  int first = 0, tiles = 0;
+  // begin[e] = min(M, max(0, offsets[0 .. e]))
+  for (int e0 = 0; e0 <= p.E; e0 += 32) {
+    const int e = e0 + lane;
+    int b = e <= p.E ? min(max(p.offsets[e], 0), p.M) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, b, o);
+      if (lane >= o) b = max(b, up);
+    }
+    b = max(b, first);
+    first = __shfl_sync(0xffffffffu, b, 31);
+    if (e <= p.E) g.begin[e] = b;
+  }
+  __syncwarp();
+  for (int e0 = 0; e0 <= p.E; e0 += 32) {
+    const int e = e0 + lane;
+    int t = e < p.E ? (g.begin[e + 1] - g.begin[e] + kTileM - 1) / kTileM : 0;
+    const int own = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += up;
+    }
+    if (e <= p.E) g.tile[e] = tiles + t - own;
+    tiles += __shfl_sync(0xffffffffu, t, 31);
+  }
+}
+
+struct Tile {
+  int e, m0, end, r0;   // expert, first row, end of the expert's rows, first output
+};
+// Tile t: runs of 8 token tiles for each tile of outputs, so that tiles at
+// work together share tokens and weights in L2.
+__device__ __forceinline__ Tile tile_at(const Product& p, const Groups& g, int t, int num_m, int num_r) {
+  constexpr int kRun = 8;
+  const int run = t / (kRun * num_r), first = run * kRun, in = t - run * (kRun * num_r);
+  const int width = min(kRun, num_m - first);
+  const int mt = first + in % width;
+  Tile x;
+  x.r0 = in / width * kTileR;
+  if (p.offsets == nullptr) {
+    x.e = 0;
+    x.m0 = mt * kTileM;
+    x.end = p.M;
+    return x;
+  }
+  int lo = 0, hi = p.E;   // the last expert whose first tile is at most mt (experts without rows share it)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (g.tile[mid] <= mt) lo = mid;
+    else hi = mid;
+  }
+  x.e = lo;
+  x.m0 = g.begin[lo] + (mt - g.tile[lo]) * kTileM;
+  x.end = g.begin[lo + 1];
+  return x;
+}
+
+__device__ __forceinline__ uint32_t pack16(bool bf16, float a, float b) {
+  if (bf16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// D tile by tile (persistent).  Warp 0 fetches, warp 1 multiplies: one
+// accumulator in TMEM per 128 columns of the reduction, two of them in turn.
+// Warps 2 to 5 add each, times its two scales, to the sums that they hold in
+// registers: a thread has one token and 128 outputs, so the product of the
+// scales is one number.
+template <bool kT>
+__global__ void __launch_bounds__(kThreads, 1) fp8_product_kernel(const __grid_constant__ Product p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Groups groups;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* store = smem + kStages * kStageBytes;
+  Shared& y = *reinterpret_cast<Shared*>(store + 4 * kStoreBytes);
+  volatile int* abort = &y.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&y.full[i], 1);
+      mbar_init(&y.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&y.acc_full[i], 1);
+      mbar_init(&y.acc_empty[i], 4);
+    }
+    mbar_init(&y.last, 1);
+    y.abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tmX);
+    tma_prefetch_desc(&p.tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc(&y.tmem, 256);
+    tmem_relinquish();
+  }
+  if (warp == 2 && p.offsets != nullptr) plan_groups(p, groups, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = y.tmem;
+  const int num_m = p.offsets == nullptr ? (p.M + kTileM - 1) / kTileM : groups.tile[p.E];
+  const int num_r = (p.R + kTileR - 1) / kTileR;
+  const int tiles = num_m * num_r, blocks = (p.C + kBlk - 1) / kBlk;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      grid_dependency_wait();
+      asm volatile("fence.proxy.async;" ::: "memory");
+      int it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        const Tile x = tile_at(p, groups, t, num_m, num_r);
+        for (int b = 0; b < blocks; ++b, ++it) {
+          const int s = it % kStages;
+          if (!mbar_wait(&y.empty[s], ((it / kStages) & 1) ^ 1, abort, p.st, kWhereFetch)) {
+            ok = false;
+            break;
+          }
+          uint8_t* xd = smem + s * kStageBytes;
+          mbar_arrive_expect_tx(&y.full[s], kStageBytes);
+          tma_load_2d(xd, &p.tmX, b * kBlk, x.m0, &y.full[s]);
+          if (kT) tma_load_3d(xd + kTileBytes, &p.tmW, x.r0, b * kBlk, x.e, &y.full[s]);
+          else tma_load_3d(xd + kTileBytes, &p.tmW, b * kBlk, x.r0, x.e, &y.full[s]);
+        }
+      }
+      // what is under way lands before the block may end
+      for (int j = max(0, it - kStages); j < it; ++j) mbar_wait_out(&y.full[j % kStages], (j / kStages) & 1, p.st, kWhereFetch);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = make_idesc_f16(kTileM, kTileR, false, kT);   // E4M3 has the format number of fp16
+      const uint32_t base = smem_u32(smem);
+      int it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int b = 0; b < blocks; ++b, ++it) {
+          const int s = it % kStages, a = it & 1;
+          if (!mbar_wait(&y.acc_empty[a], ((it >> 1) & 1) ^ 1, abort, p.st, kWhereProduct) ||
+              !mbar_wait(&y.full[s], (it / kStages) & 1, abort, p.st, kWhereProduct)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t xa = base + s * kStageBytes, wa = xa + kTileBytes;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_fp8(tmem + a * kTileR, make_sdesc(xa + 32 * k, 16, 1024, kSwizzle128B),
+                     kT ? make_sdesc(wa + 4096 * k, kTileBytes, 1024, kSwizzle128B)
+                        : make_sdesc(wa + 32 * k, 16, 1024, kSwizzle128B),
+                     idesc, k > 0 ? 1u : 0u);
+          umma_commit(&y.empty[s]);
+          umma_commit(&y.acc_full[a]);
+        }
+      }
+      umma_commit(&y.last);
+      mbar_wait_out(&y.last, 0, p.st, kWhereProduct);
+    }
+  } else {
+    const int quad = warp & 3;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    uint8_t* out_s = store + quad * kStoreBytes;
+    float* bias_s = y.bias[quad];
+    grid_dependency_wait();
+    if (p.offsets != nullptr && p.zero_rest) {
+      const int64_t head = groups.begin[0], rest = head + p.M - groups.begin[p.E];
+      uint16_t* out = static_cast<uint16_t*>(p.out);
+      for (int64_t i = blockIdx.x * 4 + quad; i < rest; i += gridDim.x * 4) {
+        uint16_t* row = out + (i < head ? i : i - head + groups.begin[p.E]) * p.R;
+        for (int c = lane; c < p.R; c += 32) row[c] = 0;
+      }
+    }
+    int it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const Tile x = tile_at(p, groups, t, num_m, num_r);
+      const int m = x.m0 + quad * 32 + lane;
+      const float* xs = p.xs + min(m, p.M - 1);
+      const float* ws = p.ws + static_cast<int64_t>(x.e) * p.nb * p.kb + (kT ? x.r0 / kBlk : x.r0 / kBlk * p.kb);
+      const int wstep = kT ? p.kb : 1;
+      float acc[kTileR];
+#pragma unroll
+      for (int i = 0; i < kTileR; ++i) acc[i] = 0.f;
+      __syncwarp();
+      for (int i = lane; i < kTileR; i += 32) {
+        const int r = x.r0 + i;
+        float v = 0.f;
+        if (p.bias != nullptr && r < p.R)
+          v = p.bias_dt == DT_F32    ? static_cast<const float*>(p.bias)[r]
+              : p.bias_dt == DT_BF16 ? to_float(static_cast<const __nv_bfloat16*>(p.bias)[r])
+                                     : to_float(static_cast<const __half*>(p.bias)[r]);
+        bias_s[i] = v;
+      }
+      __syncwarp();
+      float next = xs[0] * ws[0];
+      for (int b = 0; b < blocks; ++b, ++it) {
+        const int a = it & 1;
+        const float scale = next;
+        if (b + 1 < blocks) next = xs[static_cast<int64_t>(b + 1) * p.M] * ws[(b + 1) * wstep];
+        if (!__all_sync(0xffffffffu, mbar_wait(&y.acc_full[a], (it >> 1) & 1, abort, p.st, kWhereOut))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kTileR; c += 32) {
+          uint32_t d[32];
+          tmem_ld32(lanes + a * kTileR + c, d);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(d[i]), scale, acc[c + i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&y.acc_empty[a]);
+      }
+      if (!ok) break;
+      // out through shared memory: 64 outputs of 32 rows at a time, so that
+      // each row is written in whole lines
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t q[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int k = h * 64 + c * 8 + 2 * i;
+            q[i] = pack16(p.bf16, acc[k] + bias_s[k], acc[k + 1] + bias_s[k + 1]);
+          }
+          st_shared_v4(out_s + lane * 128 + ((c ^ (lane & 7)) << 4), make_uint4(q[0], q[1], q[2], q[3]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = i * 4 + (lane >> 3), c = lane & 7;
+          const uint4 v = ld_shared_v4(out_s + row * 128 + ((c ^ (row & 7)) << 4));
+          const int mm = x.m0 + quad * 32 + row, r = x.r0 + h * 64 + c * 8;
+          if (mm < x.end && r < p.R) {
+            uint16_t* dst = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(mm) * p.R + r;
+            if (p.vec && r + 8 <= p.R) {
+              *reinterpret_cast<uint4*>(dst) = v;
+            } else {
+              const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (r + k < p.R) dst[k] = static_cast<uint16_t>(q[k >> 1] >> (16 * (k & 1)));
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 256);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+int sm_count() {
+  int dev = 0, sms = 152;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+cudaError_t launch_quantize(const void* x, int xt, int64_t M, int64_t C, uint8_t* codes, float* scales, DevStatus* st,
+                            cudaStream_t s) {
+  const bool vec = C % (xt == DT_F32 ? 4 : 8) == 0;
+  const int64_t items = M * ceil_div(C, 512);
+  const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(items, 8), sm_count() * 8)));
+  const int c = static_cast<int>(C), ld = static_cast<int>(code_ld(C));
+  ProfScope ps(K_FP8_QUANTIZE, s);
+  if (xt == DT_F16) fp8_quantize_kernel<<<grid, 256, 0, s>>>(static_cast<const __half*>(x), M, c, ld, vec, codes, scales, st);
+  else if (xt == DT_BF16)
+    fp8_quantize_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), M, c, ld, vec, codes, scales, st);
+  else fp8_quantize_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(x), M, c, ld, vec, codes, scales, st);
+  return cudaGetLastError();
+}
+
+// The kernel after the quantising one: it sets itself up while that one runs.
+template <bool kT>
+cudaError_t launch_product(const Product& p, cudaStream_t s) {
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(fp8_product_kernel<kT>), kSmemBytes)) return cudaGetLastError();
+  const int64_t num_m = ceil_div(p.M, kTileM) + (p.offsets == nullptr ? 0 : p.E);
+  const int64_t tiles = num_m * ceil_div(p.R, kTileR);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, sm_count())));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  ProfScope ps(K_FP8_GEMM, s);
+  return cudaLaunchKernelEx(&cfg, fp8_product_kernel<kT>, p);
+}
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & (kAlign - 1)) == 0; }
+constexpr int64_t kMaxSize = INT32_MAX / 2;
+
+size_t codes_bytes(int64_t M, int64_t C) { return align_up(static_cast<size_t>(M) * static_cast<size_t>(code_ld(C))); }
+size_t scales_bytes(int64_t M, int64_t C) { return align_up(static_cast<size_t>(M) * static_cast<size_t>(ceil_div(C, kBlk)) * 4); }
+
+// The product of one direction.  Workspace: [status][codes of the tokens]
+// [their scales][partial sums of grad_bias].
+int product(bool transposed, const void* x, int xt, int64_t M, const uint8_t* codes, const float* scales, int64_t E,
+            int64_t N, int64_t K, const int32_t* offsets, int zero_rest, const void* bias, int bt, void* out,
+            void* grad_bias, void* ws, size_t ws_bytes, void* stream) {
+  const int64_t C = transposed ? N : K, R = transposed ? K : N;
+  if (xt != DT_F16 && xt != DT_BF16) return ST_UNSUPPORTED_DTYPE;
+  if ((bias != nullptr || grad_bias != nullptr) && !valid_dt(bt)) return ST_UNSUPPORTED_DTYPE;
+  if (M < 0 || N <= 0 || K <= 0 || M > kMaxSize || N > kMaxSize || K > kMaxSize) return ST_INVALID_ARG;
+  if (E < 1 || E > kMaxExperts || (E > 1 && offsets == nullptr)) return ST_INVALID_ARG;
+  if (codes == nullptr || scales == nullptr) return ST_INVALID_ARG;
+  if (M > 0 && (x == nullptr || (out == nullptr && grad_bias == nullptr))) return ST_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(out)) return ST_MISALIGNED;
+  if (ws == nullptr) return ST_WORKSPACE;
+  if (!aligned256(ws)) return ST_MISALIGNED;
+  const int64_t chunks = grad_bias != nullptr ? gradout_partial_chunks(M) : 0;
+  const size_t need = kAlign + codes_bytes(M, C) + scales_bytes(M, C) + align_up(static_cast<size_t>(chunks) * static_cast<size_t>(N) * 4);
+  if (ws_bytes < need) return ST_WORKSPACE;
+  if (M == 0 && grad_bias == nullptr) return ST_OK;
+  if (int d = check_device()) return d;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* q = static_cast<uint8_t*>(ws) + kAlign;
+  float* qs = reinterpret_cast<float*>(q + codes_bytes(M, C));
+  DevStatus* st = static_cast<DevStatus*>(ws);
+  if (grad_bias != nullptr) {
+    float* partial = reinterpret_cast<float*>(q + codes_bytes(M, C) + scales_bytes(M, C));
+    if (cudaError_t e = launch_gradout_prepass(x, xt, M, N, N % 8 == 0, nullptr, 0, grad_bias, bt, partial, chunks, s))
+      return cuda_status(e);
+    if (M == 0 || out == nullptr) return cuda_status(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
+  }
+  Product p;
+  std::memset(&p, 0, sizeof(p));
+  if (!make_tmap(&p.tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, code_ld(C), M, code_ld(C), kBlk, kTileM,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_3d(&p.tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, code_ld(K), N, E, 1, kBlk, kTileR,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+    return ST_CUDA;
+  p.xs = qs;
+  p.ws = scales;
+  p.offsets = offsets;
+  p.bias = bias;
+  p.bias_dt = bt;
+  p.out = out;
+  p.st = st;
+  p.M = static_cast<int>(M);
+  p.R = static_cast<int>(R);
+  p.C = static_cast<int>(C);
+  p.E = static_cast<int>(E);
+  p.nb = static_cast<int>(ceil_div(N, kBlk));
+  p.kb = static_cast<int>(ceil_div(K, kBlk));
+  p.bf16 = xt == DT_BF16;
+  p.vec = R % 8 == 0;
+  p.zero_rest = zero_rest != 0;
+  if (cudaError_t e = launch_quantize(x, xt, M, C, q, qs, st, s)) return cuda_status(e);
+  return cuda_status(transposed ? launch_product<true>(p, s) : launch_product<false>(p, s));
+}
+
+bool sizes_ok(int64_t E, int64_t N, int64_t K) {
+  return E >= 0 && N >= 0 && K >= 0 && E <= kMaxExperts && N <= kMaxSize && K <= kMaxSize;
+}
+
+}  // namespace
+}  // namespace i8lt
+
+extern "C" {
+
+using namespace i8lt;
+
+int64_t i8lt_fp8_ld(int64_t C) { return C < 0 ? -1 : code_ld(C); }
+int64_t i8lt_fp8_blocks(int64_t C) { return C < 0 ? -1 : ceil_div(C, kBlk); }
+
+int i8lt_fp8_quantize(const void* x, int xt, int64_t M, int64_t C, uint8_t* codes, float* scales, void* stream) {
+  if (!valid_dt(xt)) return ST_UNSUPPORTED_DTYPE;
+  if (M < 0 || C < 0 || M > kMaxSize || C > kMaxSize) return ST_INVALID_ARG;
+  if (M == 0 || C == 0) return ST_OK;
+  if (x == nullptr || codes == nullptr || scales == nullptr) return ST_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(codes)) return ST_MISALIGNED;
+  if (int d = check_device()) return d;
+  return cuda_status(launch_quantize(x, xt, M, C, codes, scales, nullptr, static_cast<cudaStream_t>(stream)));
+}
+
+int i8lt_fp8_quantize_weight(const void* W, int wt, int64_t E, int64_t N, int64_t K, uint8_t* codes, float* scales,
+                             void* stream) {
+  if (!valid_dt(wt)) return ST_UNSUPPORTED_DTYPE;
+  if (!sizes_ok(E, N, K)) return ST_INVALID_ARG;
+  if (E == 0 || N == 0 || K == 0) return ST_OK;
+  if (W == nullptr || codes == nullptr || scales == nullptr) return ST_INVALID_ARG;
+  if (!aligned16(W) || !aligned16(codes)) return ST_MISALIGNED;
+  if (ceil_div(N, kBlk) > 65535) return ST_INVALID_ARG;
+  if (int d = check_device()) return d;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const dim3 grid(static_cast<unsigned>(ceil_div(K, kBlk)), static_cast<unsigned>(ceil_div(N, kBlk)),
+                  static_cast<unsigned>(E));
+  const int n = static_cast<int>(N), k = static_cast<int>(K), ld = static_cast<int>(code_ld(K));
+  ProfScope ps(K_FP8_QUANTIZE, s);
+  if (wt == DT_F16) fp8_quantize_weight_kernel<<<grid, 256, 0, s>>>(static_cast<const __half*>(W), n, k, ld, codes, scales);
+  else if (wt == DT_BF16)
+    fp8_quantize_weight_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(W), n, k, ld, codes, scales);
+  else fp8_quantize_weight_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(W), n, k, ld, codes, scales);
+  return cuda_status(cudaGetLastError());
+}
+
+int i8lt_fp8_dequantize_weight(const uint8_t* codes, const float* scales, int64_t E, int64_t N, int64_t K, void* out,
+                               int dt, void* stream) {
+  if (!valid_dt(dt)) return ST_UNSUPPORTED_DTYPE;
+  if (!sizes_ok(E, N, K)) return ST_INVALID_ARG;
+  if (E == 0 || N == 0 || K == 0) return ST_OK;
+  if (codes == nullptr || scales == nullptr || out == nullptr) return ST_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(out)) return ST_MISALIGNED;
+  if (int d = check_device()) return d;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t rows = E * N;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(ceil_div(rows * K, 256), sm_count() * 8));
+  const int n = static_cast<int>(N), k = static_cast<int>(K), ld = static_cast<int>(code_ld(K));
+  ProfScope ps(K_FP8_QUANTIZE, s);
+  if (dt == DT_F16) fp8_dequantize_weight_kernel<<<grid, 256, 0, s>>>(codes, scales, rows, n, k, ld, static_cast<__half*>(out));
+  else if (dt == DT_BF16)
+    fp8_dequantize_weight_kernel<<<grid, 256, 0, s>>>(codes, scales, rows, n, k, ld, static_cast<__nv_bfloat16*>(out));
+  else fp8_dequantize_weight_kernel<<<grid, 256, 0, s>>>(codes, scales, rows, n, k, ld, static_cast<float*>(out));
+  return cuda_status(cudaGetLastError());
+}
+
+size_t i8lt_fp8_workspace_size(int64_t M, int64_t C) {
+  if (M < 0 || C <= 0 || M > kMaxSize || C > kMaxSize) return 0;
+  return kAlign + codes_bytes(M, C) + scales_bytes(M, C);
+}
+
+size_t i8lt_fp8_grad_bias_bytes(int64_t M, int64_t N) {
+  if (M < 0 || N < 0 || M > kMaxSize || N > kMaxSize) return 0;
+  return align_up(static_cast<size_t>(gradout_partial_chunks(M)) * static_cast<size_t>(N) * 4);
+}
+
+int i8lt_fp8_forward(const void* x, int xt, int64_t M, const uint8_t* codes, const float* scales, int64_t N, int64_t K,
+                     const void* bias, int bt, void* out, void* ws, size_t ws_bytes, void* stream) {
+  if (M > 0 && out == nullptr) return ST_INVALID_ARG;
+  return product(false, x, xt, M, codes, scales, 1, N, K, nullptr, 0, bias, bt, out, nullptr, ws, ws_bytes, stream);
+}
+
+int i8lt_fp8_backward_input(const void* g, int gt, int64_t M, const uint8_t* codes, const float* scales, int64_t N,
+                            int64_t K, void* grad_x, void* grad_bias, int bt, void* ws, size_t ws_bytes, void* stream) {
+  return product(true, g, gt, M, codes, scales, 1, N, K, nullptr, 0, nullptr, bt, grad_x, grad_bias, ws, ws_bytes,
+                 stream);
+}
+
+int i8lt_fp8_experts_forward(const void* x, int xt, int64_t M, const uint8_t* codes, const float* scales, int64_t E,
+                             int64_t N, int64_t K, const int32_t* offsets, int zero_rest, void* out, void* ws,
+                             size_t ws_bytes, void* stream) {
+  if (offsets == nullptr || (M > 0 && out == nullptr)) return ST_INVALID_ARG;
+  return product(false, x, xt, M, codes, scales, E, N, K, offsets, zero_rest, nullptr, 0, out, nullptr, ws, ws_bytes,
+                 stream);
+}
+
+int i8lt_fp8_experts_backward_input(const void* g, int gt, int64_t M, const uint8_t* codes, const float* scales,
+                                    int64_t E, int64_t N, int64_t K, const int32_t* offsets, int zero_rest,
+                                    void* grad_x, void* ws, size_t ws_bytes, void* stream) {
+  if (offsets == nullptr || (M > 0 && grad_x == nullptr)) return ST_INVALID_ARG;
+  return product(true, g, gt, M, codes, scales, E, N, K, offsets, zero_rest, nullptr, 0, grad_x, nullptr, ws, ws_bytes,
+                 stream);
+}
+
+}  // extern "C"

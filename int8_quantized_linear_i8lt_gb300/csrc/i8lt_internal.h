@@ -261,7 +261,8 @@ enum KernelId {
   K_QUANTIZE_WEIGHT = 0, K_COLMAX, K_OUTLIER_INDEX, K_ROW_QUANTIZE, K_SUBB, K_FWD_GEMM, K_GRADOUT_PREPASS,
   K_GRAD_BIAS_FINALIZE, K_BWD_GEMM, K_SILU, K_SILU_BACKWARD, K_WIDEN_CODES, K_DEQUANT_WEIGHT, K_COL_QUANTIZE,
   K_WGRAD_GEMM, K_UNIT_PLAN, K_NF4_QUANTIZE, K_NF4_DEQUANTIZE, K_NF4_GEMM_FWD, K_NF4_GEMM_BWD, K_ABSMAX8, K_LAYER_NORM,
-  K_LAYER_NORM_BWD, K_LAYER_NORM_GRAD_SUM, K_ADAPTER_PLAN, K_ADAPTERS, K_ADAPTERS_GRAD, K_ADAMW, K_COUNT
+  K_LAYER_NORM_BWD, K_LAYER_NORM_GRAD_SUM, K_ADAPTER_PLAN, K_ADAPTERS, K_ADAPTERS_GRAD, K_ADAMW, K_FP8_QUANTIZE,
+  K_FP8_GEMM, K_GRAD_NORM, K_SCALE_GRADS, K_COUNT
 };
 
 // Box sizes of the tensor maps (each CTA of a pair stages 128 rows of each

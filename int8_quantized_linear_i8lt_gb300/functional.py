@@ -1030,3 +1030,283 @@ def adamw_step_8bit(params, grads, m: torch.Tensor, m_absmax: torch.Tensor, r: t
                 lr, beta1, beta2, eps, weight_decay, _ptr(grad_scale), _ptr(found_inf), _stream(p0)),
            "i8lt_adamw_step_8bit")
     _written((*changed, m, m_absmax, r, r_absmax))
+
+
+# ---------------------------------------------------------------------------
+# the gradients of a step: their norm, clipping and scaling
+# ---------------------------------------------------------------------------
+
+def _on(dev: int, call, *args) -> int:
+    """call(*args) with CUDA device ``dev`` as the current one."""
+    if torch.cuda.current_device() == dev:
+        return call(*args)
+    with torch.cuda.device(dev):
+        return call(*args)
+
+
+def _grad_lists(what, grads):
+    """(what must outlive the call, device, count, addresses of the lists of
+    device addresses, dtypes and sizes) of contiguous ``grads``, checked."""
+    dev = grads[0].get_device()
+    _require_cuda(grads[0])
+    if set(map(_get_device, grads)) != {dev}:
+        raise I8LTError(f"{what}: tensors on {grads[0].device} and another device")
+    codes = {t: _code(t) for t in set(map(_dtype_of, grads))}
+    lists = (array.array("Q", map(_data_ptr, grads)), array.array("i", [codes[t.dtype] for t in grads]),
+             array.array("q", map(_numel, grads)))
+    return (grads, lists), dev, len(grads), [a.buffer_info()[0] for a in lists]
+
+
+def grad_norm(grads, max_norm: float | None = None, grad_scale: torch.Tensor | None = None,
+              found_inf: torch.Tensor | None = None):
+    """(norm, scale, found_inf), fp32 device scalars, of all ``grads``
+    together (f16 / bf16 / f32, mixed; None is left out), without a copy to
+    the host (i8lt_grad_norm): norm = |c| sqrt(sum g^2) with c = grad_scale (or
+    1), scale = c min(1, max_norm / (norm + 1e-6)), found_inf 1 when the norm
+    is not finite or the given found_inf is not 0: what ``adamw_step`` and
+    ``AdamW.step`` take."""
+    grads = [g if g.is_contiguous() else g.contiguous() for g in grads if g is not None]
+    if not grads:
+        raise I8LTError("grad_norm: no gradients")
+    held, dev, n, at = _grad_lists("grad_norm", grads)
+    device = grads[0].device
+    _adamw_scalar("grad_norm", grad_scale, device)
+    _adamw_scalar("grad_norm", found_inf, device)
+    result = torch.empty(3, dtype=torch.float32, device=device)
+    ws = torch.empty(_lib.i8lt_grad_norm_workspace_size(), dtype=torch.uint8, device=device)
+    _check(_on(dev, _lib.i8lt_grad_norm, *at, n, _ptr(grad_scale), _ptr(found_inf),
+               math.inf if max_norm is None else max_norm, result.data_ptr(), ws.data_ptr(), ws.numel(),
+               _stream(ws)), "i8lt_grad_norm")
+    return tuple(result.unbind())
+
+
+def scale_grads_(grads, scale: torch.Tensor) -> None:
+    """Multiply all ``grads`` (None is left out) by the fp32 device scalar
+    ``scale``, in place (i8lt_scale_grads); a scale of 1 moves nothing.  None
+    may overlap another one."""
+    grads = [g for g in grads if g is not None]
+    if not grads:
+        return
+    dense = [g if g.is_contiguous() else g.contiguous() for g in grads]
+    held, dev, n, at = _grad_lists("scale_grads_", dense)
+    _adamw_scalar("scale_grads_", scale, grads[0].device)
+    _check(_on(dev, _lib.i8lt_scale_grads, *at, n, scale.data_ptr(), _stream(grads[0])), "i8lt_scale_grads")
+    for g, d in zip(grads, dense):
+        if d is not g:
+            g.copy_(d)
+    _written(grads)
+
+
+def clip_grad_norm_(parameters, max_norm: float, grad_scale: torch.Tensor | None = None) -> torch.Tensor:
+    """Clip the gradients of ``parameters`` (a tensor or several) in place to
+    the norm ``max_norm`` of all of them together, times ``grad_scale``;
+    returns their norm before that, a device scalar."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
+    grads = [p.grad for p in parameters if p.grad is not None]
+    norm, scale, _ = grad_norm(grads, max_norm, grad_scale)
+    scale_grads_(grads, scale)
+    return norm
+
+
+# ---------------------------------------------------------------------------
+# block-scaled FP8 layers, dense and of experts
+# ---------------------------------------------------------------------------
+
+FP8 = torch.float8_e4m3fn
+
+
+def _zeros_fp8(shape, device) -> torch.Tensor:
+    return torch.zeros(shape, dtype=torch.uint8, device=device).view(FP8)   # code 0 is E4M3's zero
+
+
+def _fp8_shapes(N: int, K: int):
+    """Shapes of the codes and of the scales of a weight [N, K]."""
+    return (N, _lib.i8lt_fp8_ld(K)), (_lib.i8lt_fp8_blocks(N), _lib.i8lt_fp8_blocks(K))
+
+
+def fp8_quantize_weight(W: torch.Tensor):
+    """W [N, K], or [E, N, K] of experts (f16 / bf16 / f32, CUDA) -> (codes
+    float8_e4m3fn [..., N, K rounded up to 16], scales fp32 [..., N / 128,
+    K / 128]), a scale for each block of 128 x 128 (i8lt_fp8_quantize_weight)."""
+    _require_cuda(W)
+    if W.dim() not in (2, 3):
+        raise I8LTError(f"fp8_quantize_weight: {W.dim()}-dimensional weight, expected [N, K] or [E, N, K]")
+    W = _aligned(W)
+    N, K = W.shape[-2:]
+    lead = tuple(W.shape[:-2])
+    cs, ss = _fp8_shapes(N, K)
+    codes = torch.empty(lead + cs, dtype=torch.uint8, device=W.device).view(FP8)
+    scales = torch.empty(lead + ss, dtype=torch.float32, device=W.device)
+    _check(_on(W.get_device(), _lib.i8lt_fp8_quantize_weight, _ptr(W), _code(W.dtype), lead[0] if lead else 1, N, K,
+               _ptr(codes), _ptr(scales), _stream(W)), "i8lt_fp8_quantize_weight")
+    return codes, scales
+
+
+def fp8_dequantize_weight(codes: torch.Tensor, scales: torch.Tensor, K: int, dtype: torch.dtype) -> torch.Tensor:
+    """The weight [..., N, K] that codes and scales stand for, in ``dtype``."""
+    _require_cuda(codes)
+    if codes.dim() not in (2, 3):
+        raise I8LTError(f"fp8_dequantize_weight: {codes.dim()}-dimensional codes")
+    dev, N, lead = codes.get_device(), codes.shape[-2], tuple(codes.shape[:-2])
+    cs, ss = _fp8_shapes(N, K)
+    codes = _arg("fp8_dequantize_weight codes", codes, dev, lead + cs, FP8)
+    scales = _arg("fp8_dequantize_weight scales", scales, dev, lead + ss, torch.float32)
+    out = torch.empty(lead + (N, K), dtype=dtype, device=codes.device)
+    _check(_on(dev, _lib.i8lt_fp8_dequantize_weight, _ptr(codes), _ptr(scales), lead[0] if lead else 1, N, K, _ptr(out),
+               _code(dtype), _stream(codes)), "i8lt_fp8_dequantize_weight")
+    return out
+
+
+def fp8_quantize(x: torch.Tensor):
+    """x [M, C] (f16 / bf16 / f32) -> (codes float8_e4m3fn [M, C rounded up to
+    16], scales fp32 [C / 128, M]), a scale for each 128 columns of a row: what
+    the layer multiplies (i8lt_fp8_quantize)."""
+    _require_cuda(x)
+    if x.dim() != 2:
+        raise I8LTError(f"fp8_quantize: {x.dim()}-dimensional x, expected [M, C]")
+    x = _aligned(x)
+    M, C = x.shape
+    codes = torch.empty(M, _lib.i8lt_fp8_ld(C), dtype=torch.uint8, device=x.device).view(FP8)
+    scales = torch.empty(_lib.i8lt_fp8_blocks(C), M, dtype=torch.float32, device=x.device)
+    _check(_on(x.get_device(), _lib.i8lt_fp8_quantize, _ptr(x), _code(x.dtype), M, C, _ptr(codes), _ptr(scales),
+               _stream(x)), "i8lt_fp8_quantize")
+    return codes, scales
+
+
+def _fp8_args(what, t, codes, scales, K, lead, transposed):
+    """(device, M, N, t, codes, scales) of a product of tokens t, checked."""
+    _require_cuda(t)
+    dev = t.get_device()
+    if t.dim() != 2:
+        raise I8LTError(f"{what}: {t.dim()}-dimensional tokens, expected [tokens, features]")
+    if codes.dim() != len(lead) + 2:
+        raise I8LTError(f"{what}: {codes.dim()}-dimensional codes")
+    M, N = t.shape[0], codes.shape[-2]
+    cs, ss = _fp8_shapes(N, K)
+    t = _arg(what, t, dev, (M, N if transposed else K), None)
+    codes = _arg(f"{what} codes", codes, dev, lead + cs, FP8)
+    scales = _arg(f"{what} scales", scales, dev, lead + ss, torch.float32)
+    return dev, M, N, t, codes, scales
+
+
+def fp8_forward(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, K: int, bias: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """out [M, N] = x [M, K] W^T (+ bias) in x's dtype (f16 or bf16), W the
+    weight that codes and scales (``fp8_quantize_weight``) stand for and x
+    rounded to FP8 in blocks of 128 columns (i8lt_fp8_forward).  ``ws``: a
+    workspace of i8lt_fp8_workspace_size bytes, for a caller that reads its
+    ``device_status``."""
+    what = "fp8_forward"
+    dev, M, N, x, codes, scales = _fp8_args(what, x, codes, scales, K, (), False)
+    bias = _arg("fp8_forward bias", bias, dev, (N,), None)
+    y = torch.empty((M, N), dtype=x.dtype, device=x.device) if out is None else _out("fp8_forward out", out, dev, (M, N), x.dtype)
+    ws = _workspace(what, ws, _lib.i8lt_fp8_workspace_size(M, K), x.device)
+    _check(_on(dev, _lib.i8lt_fp8_forward, _ptr(x), _code(x.dtype), M, _ptr(codes), _ptr(scales), N, K, _ptr(bias),
+               0 if bias is None else _code(bias.dtype), _ptr(y), ws.data_ptr(), ws.numel(), _stream(x)),
+           "i8lt_fp8_forward")
+    if out is not None:
+        _written(out)
+    return y
+
+
+def fp8_backward_input(G: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, K: int, need_grad_A: bool = True,
+                       bias_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                       ws: torch.Tensor | None = None):
+    """(grad_A [M, K] = G [M, N] W in G's dtype (f16 or bf16) or None,
+    grad_bias [N] in ``bias_dtype`` or None), G rounded to FP8 in blocks of 128
+    columns for grad_A and taken as it is for grad_bias."""
+    what = "fp8_backward_input"
+    dev, M, N, G, codes, scales = _fp8_args(what, G, codes, scales, K, (), True)
+    gx = gb = None
+    if need_grad_A:
+        gx = torch.empty((M, K), dtype=G.dtype, device=G.device) if out is None else \
+            _out("fp8_backward_input out", out, dev, (M, K), G.dtype)
+    if bias_dtype is not None:
+        gb = torch.empty(N, dtype=bias_dtype, device=G.device)
+    if gx is None and gb is None:
+        return None, None
+    size = _lib.i8lt_fp8_workspace_size(M, N) + (_lib.i8lt_fp8_grad_bias_bytes(M, N) if gb is not None else 0)
+    ws = _workspace(what, ws, size, G.device)
+    _check(_on(dev, _lib.i8lt_fp8_backward_input, _ptr(G), _code(G.dtype), M, _ptr(codes), _ptr(scales), N, K,
+               _ptr(gx), _ptr(gb), 0 if gb is None else _code(bias_dtype), ws.data_ptr(), ws.numel(), _stream(G)),
+           "i8lt_fp8_backward_input")
+    if need_grad_A and out is not None:
+        _written(out)
+    return gx, gb
+
+
+def _fp8_experts(what, call, t, codes, scales, K, offsets, transposed, out, ws):
+    if codes.dim() != 3:
+        raise I8LTError(f"{what}: {codes.dim()}-dimensional codes, expected [experts, N, K rounded up to 16]")
+    E = codes.shape[0]
+    dev, M, N, t, codes, scales = _fp8_args(what, t, codes, scales, K, (E,), transposed)
+    offsets = _arg(f"{what} offsets", offsets, dev, (E + 1,), torch.int32)
+    shape = (M, K if transposed else N)
+    y = torch.empty(shape, dtype=t.dtype, device=t.device) if out is None else _out(f"{what} out", out, dev, shape, t.dtype)
+    ws = _workspace(what, ws, _lib.i8lt_fp8_workspace_size(M, N if transposed else K), t.device)
+    _check(_on(dev, call, _ptr(t), _code(t.dtype), M, _ptr(codes), _ptr(scales), E, N, K, _ptr(offsets),
+               1 if out is None else 0, _ptr(y), ws.data_ptr(), ws.numel(), _stream(t)), f"i8lt_{what}")
+    if out is not None:
+        _written(out)
+    return y
+
+
+def fp8_experts_forward(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, K: int, offsets: torch.Tensor,
+                        out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """``fp8_forward`` with a weight for each expert: rows offsets[e] up to
+    offsets[e + 1] of x [M, K] take expert e's, codes [E, N, ...] and scales
+    [E, ...] (i8lt_fp8_experts_forward).  ``offsets``: ascending int32 [E + 1]
+    on the device.  Rows of no expert are zeros, or left as they are in a
+    given ``out``."""
+    return _fp8_experts("fp8_experts_forward", _lib.i8lt_fp8_experts_forward, x, codes, scales, K, offsets, False, out, ws)
+
+
+def fp8_experts_backward_input(G: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, K: int,
+                               offsets: torch.Tensor, out: torch.Tensor | None = None,
+                               ws: torch.Tensor | None = None) -> torch.Tensor:
+    """grad_x [M, K] of ``fp8_experts_forward`` from G [M, N], with the same
+    rule for rows of no expert."""
+    return _fp8_experts("fp8_experts_backward_input", _lib.i8lt_fp8_experts_backward_input, G, codes, scales, K, offsets,
+                        True, out, ws)
+
+
+class LinearFP8Function(torch.autograd.Function):
+    """y = x W^T + bias with the frozen FP8 weight; gradients to x and to the
+    bias."""
+
+    @staticmethod
+    def forward(ctx, x, codes, scales, K, bias):
+        y = fp8_forward(x.reshape(-1, x.shape[-1]), codes, scales, K, bias)
+        ctx.save_for_backward(codes, scales)
+        ctx.K, ctx.shape = K, x.shape
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return y.reshape(*x.shape[:-1], codes.shape[0])
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gy):
+        codes, scales = ctx.saved_tensors
+        need_b = ctx.needs_input_grad[4] and ctx.bias_dtype is not None
+        gx, gb = fp8_backward_input(gy.reshape(-1, codes.shape[0]), codes, scales, ctx.K,
+                                    need_grad_A=ctx.needs_input_grad[0], bias_dtype=ctx.bias_dtype if need_b else None)
+        return (None if gx is None else gx.reshape(ctx.shape)), None, None, None, gb
+
+
+class ExpertsFP8Function(torch.autograd.Function):
+    """The experts' frozen FP8 weights times the tokens x [M, K] sorted by
+    expert; the gradient goes to x."""
+
+    @staticmethod
+    def forward(ctx, x, codes, scales, K, offsets):
+        y = fp8_experts_forward(x, codes, scales, K, offsets)
+        ctx.save_for_backward(codes, scales, offsets)
+        ctx.K = K
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gy):
+        codes, scales, offsets = ctx.saved_tensors
+        gx = fp8_experts_backward_input(gy, codes, scales, ctx.K, offsets) if ctx.needs_input_grad[0] else None
+        return gx, None, None, None, None

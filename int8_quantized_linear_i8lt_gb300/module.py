@@ -184,6 +184,70 @@ class LinearFP4(Linear4bit):
     fmt = "fp4"
 
 
+class LinearFP8(torch.nn.Module):
+    """Frozen FP8 linear layer: E4M3 codes with one fp32 scale per 128 x 128
+    block of the weight; tokens (f16 or bf16) and output gradients are rounded
+    to FP8 in blocks of 128 columns inside the call and multiplied on the FP8
+    tensor cores.  The weight takes no gradient; the bias does."""
+
+    def __init__(self, in_features: int, out_features: int, bias: bool = True, device=None,
+                 bias_dtype: torch.dtype = torch.bfloat16):
+        super().__init__()
+        self.in_features, self.out_features = in_features, out_features
+        codes, scales = F._fp8_shapes(out_features, in_features)
+        self.register_buffer("codes", F._zeros_fp8(codes, device))
+        self.register_buffer("scales", torch.zeros(scales, dtype=torch.float32, device=device))
+        if bias:
+            self.bias = torch.nn.Parameter(torch.zeros(out_features, dtype=bias_dtype, device=device))
+        else:
+            self.register_parameter("bias", None)
+
+    @classmethod
+    def from_float(cls, weight: torch.Tensor, bias: torch.Tensor | None = None) -> "LinearFP8":
+        """Quantize a float weight [out, in] on its CUDA device."""
+        N, K = weight.shape
+        layer = cls(K, N, bias=bias is not None, device="meta",
+                    bias_dtype=bias.dtype if bias is not None else torch.bfloat16)
+        layer.codes, layer.scales = F.fp8_quantize_weight(weight.detach())
+        if bias is not None:
+            layer.bias = torch.nn.Parameter(bias.detach().to(weight.device, copy=True))
+        return layer
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        return F.LinearFP8Function.apply(x, self.codes, self.scales, self.in_features, self.bias)
+
+    def extra_repr(self) -> str:
+        return f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}"
+
+
+class ExpertsFP8(torch.nn.Module):
+    """``LinearFP8`` for ``experts`` weights at once, without bias: rows
+    offsets[e] up to offsets[e + 1] of x [tokens, in_features], sorted by
+    expert, take expert e's (``offsets``: int32 [experts + 1] on the device).
+    Rows of no expert give zeros, and get a gradient of zero."""
+
+    def __init__(self, experts: int, in_features: int, out_features: int, device=None):
+        super().__init__()
+        self.experts, self.in_features, self.out_features = experts, in_features, out_features
+        codes, scales = F._fp8_shapes(out_features, in_features)
+        self.register_buffer("codes", F._zeros_fp8((experts, *codes), device))
+        self.register_buffer("scales", torch.zeros((experts, *scales), dtype=torch.float32, device=device))
+
+    @classmethod
+    def from_float(cls, weight: torch.Tensor) -> "ExpertsFP8":
+        """Quantize float weights [experts, out, in] on their CUDA device."""
+        E, N, K = weight.shape
+        layer = cls(E, K, N, device="meta")
+        layer.codes, layer.scales = F.fp8_quantize_weight(weight.detach())
+        return layer
+
+    def forward(self, x: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
+        return F.ExpertsFP8Function.apply(x, self.codes, self.scales, self.in_features, offsets)
+
+    def extra_repr(self) -> str:
+        return f"experts={self.experts}, in_features={self.in_features}, out_features={self.out_features}"
+
+
 class LayerNorm(torch.nn.Module):
     """Layer norm over the last dimension with trainable weight and bias."""
 
@@ -241,7 +305,10 @@ class AdamW:
     makes the step change nothing.  ``steps`` counts the calls; the bias
     corrections of a parameter are those of its own updates, without steps in
     which it had no gradient or that were skipped (``counts``, on the
-    device)."""
+    device).  With ``max_norm`` the step clips: the gradients (times
+    grad_scale) enter it scaled to at most that norm of all of them together,
+    and a norm that is not finite skips it; nothing is copied to the host, the
+    gradients stay as they are, and step() returns their norm."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
                  bits: int = 32):
@@ -270,13 +337,20 @@ class AdamW:
                 self.states.append(tuple(torch.zeros(n, dtype=torch.float32, device=dev) for _ in range(2)))
 
     @torch.no_grad()
-    def step(self, grad_scale: torch.Tensor | None = None, found_inf: torch.Tensor | None = None) -> None:
+    def step(self, grad_scale: torch.Tensor | None = None, found_inf: torch.Tensor | None = None,
+             max_norm: float | None = None) -> torch.Tensor | None:
+        norm = None
+        if max_norm is not None:
+            grads = [p.grad for ps in self.params for p in ps if p.grad is not None]
+            if grads:
+                norm, grad_scale, found_inf = F.grad_norm(grads, max_norm, grad_scale, found_inf)
         self.steps += 1
         call = F.adamw_step_8bit if self.bits == 8 else F.adamw_step
         for ps, st, counts in zip(self.params, self.states, self.counts):
             call(ps, [p.grad for p in ps], *st, step=counts, lr=self.lr, beta1=self.betas[0],
                  beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay, grad_scale=grad_scale,
                  found_inf=found_inf)
+        return norm
 
     def zero_grad(self) -> None:
         for ps in self.params:
