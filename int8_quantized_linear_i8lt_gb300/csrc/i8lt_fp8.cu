@@ -190,6 +190,7 @@ __device__ __forceinline__ void umma_fp8(uint32_t d, uint64_t a, uint64_t b, uin
 // The row ranges of the experts, by one warp.  They are data: each start is
 // taken as at least the one before it and at most M, so that no range leaves
 // the tokens or overlaps another one whatever the values are.
+template <int kTileM>
 __device__ __forceinline__ void plan_groups(const Product& p, Groups& g, int lane) {
   int first = 0, tiles = 0;
   // begin[e] = min(M, max(0, offsets[0 .. e]))
@@ -225,6 +226,7 @@ struct Tile {
 };
 // Tile t: runs of 8 token tiles for each tile of outputs, so that tiles at
 // work together share tokens and weights in L2.
+template <int kTileM, int kTileR>
 __device__ __forceinline__ Tile tile_at(const Product& p, const Groups& g, int t, int num_m, int num_r) {
   constexpr int kRun = 8;
   const int run = t / (kRun * num_r), first = run * kRun, in = t - run * (kRun * num_r);
@@ -257,6 +259,36 @@ __device__ __forceinline__ uint32_t pack16(bool bf16, float a, float b) {
   }
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float bias_at(const Product& p, int r) {
+  if (p.bias == nullptr || r >= p.R) return 0.f;
+  return p.bias_dt == DT_F32    ? static_cast<const float*>(p.bias)[r]
+         : p.bias_dt == DT_BF16 ? to_float(static_cast<const __nv_bfloat16*>(p.bias)[r])
+                                : to_float(static_cast<const __half*>(p.bias)[r]);
+}
+
+// Zeros in the rows of no expert, by warp `w` of `count`.
+__device__ __forceinline__ void zero_rest(const Product& p, const Groups& g, int64_t w, int64_t count, int lane) {
+  const int64_t head = g.begin[0], rest = head + p.M - g.begin[p.E];
+  uint16_t* out = static_cast<uint16_t*>(p.out);
+  for (int64_t i = w; i < rest; i += count) {
+    uint16_t* row = out + (i < head ? i : i - head + g.begin[p.E]) * p.R;
+    for (int c = lane; c < p.R; c += 32) row[c] = 0;
+  }
+}
+
+// 8 consecutive outputs (16 bytes) from output r on of a row.
+__device__ __forceinline__ void store_out8(const Product& p, int64_t m, int r, const uint4& v) {
+  uint16_t* dst = static_cast<uint16_t*>(p.out) + m * p.R + r;
+  if (p.vec && r + 8 <= p.R) {
+    *reinterpret_cast<uint4*>(dst) = v;
+  } else {
+    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (r + k < p.R) dst[k] = static_cast<uint16_t>(q[k >> 1] >> (16 * (k & 1)));
+  }
 }
 
 // D tile by tile (persistent).  Warp 0 fetches, warp 1 multiplies: one
@@ -293,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_product_kernel(const __grid_c
     tmem_alloc(&y.tmem, 256);
     tmem_relinquish();
   }
-  if (warp == 2 && p.offsets != nullptr) plan_groups(p, groups, lane);
+  if (warp == 2 && p.offsets != nullptr) plan_groups<kTileM>(p, groups, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -309,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_product_kernel(const __grid_c
       int it = 0;
       bool ok = true;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const Tile x = tile_at(p, groups, t, num_m, num_r);
+        const Tile x = tile_at<kTileM, kTileR>(p, groups, t, num_m, num_r);
         for (int b = 0; b < blocks; ++b, ++it) {
           const int s = it % kStages;
           if (!mbar_wait(&y.empty[s], ((it / kStages) & 1) ^ 1, abort, p.st, kWhereFetch)) {
@@ -361,18 +393,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_product_kernel(const __grid_c
     uint8_t* out_s = store + quad * kStoreBytes;
     float* bias_s = y.bias[quad];
     grid_dependency_wait();
-    if (p.offsets != nullptr && p.zero_rest) {
-      const int64_t head = groups.begin[0], rest = head + p.M - groups.begin[p.E];
-      uint16_t* out = static_cast<uint16_t*>(p.out);
-      for (int64_t i = blockIdx.x * 4 + quad; i < rest; i += gridDim.x * 4) {
-        uint16_t* row = out + (i < head ? i : i - head + groups.begin[p.E]) * p.R;
-        for (int c = lane; c < p.R; c += 32) row[c] = 0;
-      }
-    }
+    if (p.offsets != nullptr && p.zero_rest)
+      zero_rest(p, groups, blockIdx.x * 4 + quad, gridDim.x * 4, lane);
     int it = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile x = tile_at(p, groups, t, num_m, num_r);
+      const Tile x = tile_at<kTileM, kTileR>(p, groups, t, num_m, num_r);
       const int m = x.m0 + quad * 32 + lane;
       const float* xs = p.xs + min(m, p.M - 1);
       const float* ws = p.ws + static_cast<int64_t>(x.e) * p.nb * p.kb + (kT ? x.r0 / kBlk : x.r0 / kBlk * p.kb);
@@ -381,15 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_product_kernel(const __grid_c
 #pragma unroll
       for (int i = 0; i < kTileR; ++i) acc[i] = 0.f;
       __syncwarp();
-      for (int i = lane; i < kTileR; i += 32) {
-        const int r = x.r0 + i;
-        float v = 0.f;
-        if (p.bias != nullptr && r < p.R)
-          v = p.bias_dt == DT_F32    ? static_cast<const float*>(p.bias)[r]
-              : p.bias_dt == DT_BF16 ? to_float(static_cast<const __nv_bfloat16*>(p.bias)[r])
-                                     : to_float(static_cast<const __half*>(p.bias)[r]);
-        bias_s[i] = v;
-      }
+      for (int i = lane; i < kTileR; i += 32) bias_s[i] = bias_at(p, x.r0 + i);
       __syncwarp();
       float next = xs[0] * ws[0];
       for (int b = 0; b < blocks; ++b, ++it) {
@@ -434,17 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_product_kernel(const __grid_c
           const int row = i * 4 + (lane >> 3), c = lane & 7;
           const uint4 v = ld_shared_v4(out_s + row * 128 + ((c ^ (row & 7)) << 4));
           const int mm = x.m0 + quad * 32 + row, r = x.r0 + h * 64 + c * 8;
-          if (mm < x.end && r < p.R) {
-            uint16_t* dst = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(mm) * p.R + r;
-            if (p.vec && r + 8 <= p.R) {
-              *reinterpret_cast<uint4*>(dst) = v;
-            } else {
-              const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                if (r + k < p.R) dst[k] = static_cast<uint16_t>(q[k >> 1] >> (16 * (k & 1)));
-            }
-          }
+          if (mm < x.end && r < p.R) store_out8(p, mm, r, v);
         }
       }
     }
@@ -453,6 +461,241 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_product_kernel(const __grid_c
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 256);
+}
+
+// ---- pairs of CTAs --------------------------------------------------------
+
+constexpr int kWideThreads = 320;
+constexpr int kWideStoreBytes = 2048;     // per epilogue warp: 32 rows of 64 bytes
+constexpr int kWideEpiWarps = 8;
+struct WideShared {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t last;
+  uint32_t tmem;
+  int abort;
+  float bias[kWideEpiWarps][128];
+};
+constexpr int kWideSmemBytes = 1024 + kStages * kStageBytes + kWideEpiWarps * kWideStoreBytes + static_cast<int>(sizeof(WideShared));
+
+__device__ __forceinline__ void umma_fp8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&a)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(a[i]));
+}
+// two fp32 sums += two products
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t scale2) {
+  asm("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n fma.rn.f32x2 %0, d, %3, %0;\n}" : "+l"(acc) : "r"(lo), "r"(hi), "l"(scale2));
+}
+__device__ __forceinline__ uint64_t splat2(float f) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "r"(__float_as_uint(f)));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+  return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+
+// Tiles of 256 tokens x 256 outputs by pairs of CTAs: each CTA fetches and
+// holds half of either operand, the even CTA multiplies for both, and each
+// CTA's eight epilogue warps keep the sums of its own 128 tokens in registers
+// (128 outputs a thread).
+template <bool kT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+    fp8_product_wide_kernel(const __grid_constant__ Product p) {
+  constexpr int kTileM = 256, kTileR = 256;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Groups groups;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* store = smem + kStages * kStageBytes;
+  WideShared& y = *reinterpret_cast<WideShared*>(store + kWideEpiWarps * kWideStoreBytes);
+  volatile int* abort = &y.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int pair = static_cast<int>(cluster_id_x()), pairs = static_cast<int>(num_clusters_x());
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&y.full[i], 1);
+      mbar_init(&y.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&y.acc_full[i], 1);
+      mbar_init(&y.acc_empty[i], 2 * kWideEpiWarps);
+    }
+    mbar_init(&y.last, 1);
+    y.abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tmX);
+    tma_prefetch_desc(&p.tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&y.tmem, 512);
+    tmem_relinquish_pair();
+  }
+  if (warp == 2 && p.offsets != nullptr) plan_groups<kTileM>(p, groups, lane);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = y.tmem;
+  const int num_m = p.offsets == nullptr ? (p.M + kTileM - 1) / kTileM : groups.tile[p.E];
+  const int num_r = (p.R + kTileR - 1) / kTileR;
+  const int tiles = num_m * num_r, blocks = (p.C + kBlk - 1) / kBlk;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      grid_dependency_wait();
+      asm volatile("fence.proxy.async;" ::: "memory");
+      const uint32_t full0 = mapa_shared(&y.full[0], 0);   // both CTAs' copies count on the even CTA's barriers
+      int it = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        const Tile x = tile_at<kTileM, kTileR>(p, groups, t, num_m, num_r);
+        const int m = x.m0 + rank * 128, r = x.r0 + rank * 128;
+        for (int b = 0; b < blocks; ++b, ++it) {
+          const int s = it % kStages;
+          if (!mbar_wait(&y.empty[s], ((it / kStages) & 1) ^ 1, abort, p.st, kWhereFetch)) {
+            ok = false;
+            break;
+          }
+          uint8_t* xd = smem + s * kStageBytes;
+          const uint32_t full = full0 + static_cast<uint32_t>(s) * 8u;
+          if (rank == 0) mbar_arrive_expect_tx(&y.full[s], 2 * kStageBytes);
+          tma_load_2d_pair(xd, &p.tmX, b * kBlk, m, full);
+          if (kT) tma_load_3d_pair(xd + kTileBytes, &p.tmW, r, b * kBlk, x.e, full);
+          else tma_load_3d_pair(xd + kTileBytes, &p.tmW, b * kBlk, r, x.e, full);
+        }
+      }
+      // what is under way lands before the pair may end
+      if (rank == 0)
+        for (int j = max(0, it - kStages); j < it; ++j) mbar_wait_out(&y.full[j % kStages], (j / kStages) & 1, p.st, kWhereFetch);
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      const uint32_t idesc = make_idesc_f16(kTileM, kTileR, false, kT);   // E4M3 has the format number of fp16
+      const uint32_t base = smem_u32(smem);
+      int it = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        for (int b = 0; b < blocks; ++b, ++it) {
+          const int s = it % kStages, a = it & 1;
+          if (!mbar_wait(&y.full[s], (it / kStages) & 1, abort, p.st, kWhereProduct) ||
+              !mbar_wait_cluster(&y.acc_empty[a], ((it >> 1) & 1) ^ 1, abort, p.st, kWhereProduct)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t xa = base + s * kStageBytes, wa = xa + kTileBytes;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_fp8_pair(tmem + a * kTileR, make_sdesc(xa + 32 * k, 16, 1024, kSwizzle128B),
+                          kT ? make_sdesc(wa + 4096 * k, kTileBytes, 1024, kSwizzle128B)
+                             : make_sdesc(wa + 32 * k, 16, 1024, kSwizzle128B),
+                          idesc, k > 0 ? 1u : 0u);
+          umma_commit_pair_mc(&y.empty[s], 0x3);
+          umma_commit_pair_mc(&y.acc_full[a], 0x3);
+        }
+      }
+      umma_commit_pair(&y.last);
+      mbar_wait_out(&y.last, 0, p.st, kWhereProduct);
+    }
+  } else {
+    const int quad = warp & 3, ew = warp - 2, half = ew >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
+    const uint32_t acc_empty0 = mapa_shared(&y.acc_empty[0], 0);
+    uint8_t* out_s = store + ew * kWideStoreBytes;
+    float* bias_s = y.bias[ew];
+    grid_dependency_wait();
+    if (p.offsets != nullptr && p.zero_rest)
+      zero_rest(p, groups, blockIdx.x * kWideEpiWarps + ew, gridDim.x * kWideEpiWarps, lane);
+    int it = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      const Tile x = tile_at<kTileM, kTileR>(p, groups, t, num_m, num_r);
+      const int row0 = x.m0 + rank * 128 + quad * 32, r0 = x.r0 + half * 128;
+      const float* xs = p.xs + min(row0 + lane, p.M - 1);
+      const int rb = min(r0 / kBlk, (p.R - 1) / kBlk);
+      const float* ws = p.ws + static_cast<int64_t>(x.e) * p.nb * p.kb + (kT ? rb : rb * p.kb);
+      const int wstep = kT ? p.kb : 1;
+      uint64_t acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      __syncwarp();
+      for (int i = lane; i < 128; i += 32) bias_s[i] = bias_at(p, r0 + i);
+      __syncwarp();
+      float next = xs[0] * ws[0];
+      for (int b = 0; b < blocks; ++b, ++it) {
+        const int a = it & 1;
+        const uint64_t scale = splat2(next);
+        if (b + 1 < blocks) next = xs[static_cast<int64_t>(b + 1) * p.M] * ws[(b + 1) * wstep];
+        if (!__all_sync(0xffffffffu, mbar_wait(&y.acc_full[a], (it >> 1) & 1, abort, p.st, kWhereOut))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t d[2][16];
+        tmem_ld16_nowait(lanes + a * kTileR, d[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          tmem_ld_wait16(d[c & 1]);
+          if (c < 7) tmem_ld16_nowait(lanes + a * kTileR + 16 * (c + 1), d[(c + 1) & 1]);
+          if (c == 7) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(acc_empty0 + static_cast<uint32_t>(a) * 8u);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) fma2(acc[8 * c + i], d[c & 1][2 * i], d[c & 1][2 * i + 1], scale);
+        }
+      }
+      if (!ok) break;
+      // out through shared memory, 32 outputs of 32 rows at a time, so that
+      // rows are written in whole sectors
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t q[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int k = h * 32 + c * 8 + 2 * i;
+            const float2 v = unpack2(acc[k >> 1]);
+            q[i] = pack16(p.bf16, v.x + bias_s[k], v.y + bias_s[k + 1]);
+          }
+          st_shared_v4(out_s + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), make_uint4(q[0], q[1], q[2], q[3]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = i * 8 + (lane >> 2), c = lane & 3;
+          const uint4 v = ld_shared_v4(out_s + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+          const int mm = row0 + row, r = r0 + h * 32 + c * 8;
+          if (mm < x.end && r < p.R) store_out8(p, mm, r, v);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -481,15 +724,12 @@ cudaError_t launch_quantize(const void* x, int xt, int64_t M, int64_t C, uint8_t
 }
 
 // The kernel after the quantising one: it sets itself up while that one runs.
-template <bool kT>
-cudaError_t launch_product(const Product& p, cudaStream_t s) {
-  if (!ensure_smem_attr(reinterpret_cast<const void*>(fp8_product_kernel<kT>), kSmemBytes)) return cudaGetLastError();
-  const int64_t num_m = ceil_div(p.M, kTileM) + (p.offsets == nullptr ? 0 : p.E);
-  const int64_t tiles = num_m * ceil_div(p.R, kTileR);
+cudaError_t launch_after(void (*kernel)(Product), unsigned grid, int threads, int smem, const Product& p, cudaStream_t s) {
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, sm_count())));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -497,7 +737,20 @@ cudaError_t launch_product(const Product& p, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   ProfScope ps(K_FP8_GEMM, s);
-  return cudaLaunchKernelEx(&cfg, fp8_product_kernel<kT>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <bool kT>
+cudaError_t launch_product(const Product& p, cudaStream_t s) {
+  const int sms = sm_count();
+  const int64_t extra = p.offsets == nullptr ? 0 : p.E;   // experts' last tiles, at most
+  const int64_t wide = (ceil_div(p.M, 256) + extra) * ceil_div(p.R, 256);
+  if (p.M / p.E >= 256 && wide >= sms / 2)
+    return launch_after(fp8_product_wide_kernel<kT>, 2 * static_cast<unsigned>(std::min<int64_t>(wide, sms / 2)),
+                        kWideThreads, kWideSmemBytes, p, s);
+  const int64_t tiles = (ceil_div(p.M, kTileM) + extra) * ceil_div(p.R, kTileR);
+  return launch_after(fp8_product_kernel<kT>, static_cast<unsigned>(std::min<int64_t>(tiles, sms)), kThreads, kSmemBytes,
+                      p, s);
 }
 
 constexpr size_t kAlign = 256;

@@ -56,7 +56,8 @@ def test_quantize_weight(N, K, dtype):
 
 
 SIZES = [(1, 1, 1), (1, 128, 128), (2, 130, 127), (3, 16, 8), (1, 4096, 520), (17, 300, 200), (128, 256, 128),
-         (129, 384, 257), (64, 2048, 1024), (300, 1000, 1000), (513, 640, 640), (777, 1100, 519), (1025, 512, 1536)]
+         (129, 384, 257), (64, 2048, 1024), (300, 1000, 1000), (513, 640, 640), (777, 1100, 519), (1025, 512, 1536),
+         (2300, 300, 2600), (2600, 2310, 280)]
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
@@ -100,7 +101,7 @@ GROUPS = [
     (1, [0, 1], 128, 128), (5, [0, 0, 0, 5, 5], 300, 200), (40, [0, 7, 7, 19, 40], 256, 384),
     (300, [0, 130, 131, 290], 640, 257), (520, [3, 260, 511], 130, 520), (64, [0, 0], 128, 16),
     (200, list(range(0, 201, 2)), 144, 136), (1333, [0, 300, 300, 811, 1000, 1312], 1100, 519),
-    (0, [0, 0, 0], 64, 64),
+    (0, [0, 0, 0], 64, 64), (2650, [11, 700, 700, 1500, 2640], 200, 2100), (2600, [0, 255, 513, 1300, 2600], 2200, 136),
 ]
 
 
