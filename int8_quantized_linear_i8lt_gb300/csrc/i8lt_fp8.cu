@@ -639,11 +639,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       __syncwarp();
       for (int i = lane; i < 128; i += 32) bias_s[i] = bias_at(p, r0 + i);
       __syncwarp();
-      float next = xs[0] * ws[0];
+      // the scales are fetched two blocks ahead and multiplied when they are
+      // used: their latency in L2 is longer than a block's product
+      float x1 = xs[0], w1 = ws[0], x2 = 0.f, w2 = 0.f;
+      if (blocks > 1) {
+        x2 = xs[p.M];
+        w2 = ws[wstep];
+      }
       for (int b = 0; b < blocks; ++b, ++it) {
         const int a = it & 1;
-        const uint64_t scale = splat2(next);
-        if (b + 1 < blocks) next = xs[static_cast<int64_t>(b + 1) * p.M] * ws[(b + 1) * wstep];
         if (!__all_sync(0xffffffffu, mbar_wait(&y.acc_full[a], (it >> 1) & 1, abort, p.st, kWhereOut))) {
           ok = false;
           break;
@@ -651,6 +655,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         tc_fence_after();
         uint32_t d[2][16];
         tmem_ld16_nowait(lanes + a * kTileR, d[0]);
+        const uint64_t scale = splat2(x1 * w1);
+        x1 = x2;
+        w1 = w2;
+        if (b + 2 < blocks) {
+          x2 = xs[static_cast<int64_t>(b + 2) * p.M];
+          w2 = ws[(b + 2) * wstep];
+        }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           tmem_ld_wait16(d[c & 1]);
