@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(256) fp8_dequantize_weight_kernel(const uint8_
 
 struct Product {
   CUtensorMap tmX;           // codes of the tokens [M, ld(C)], box 128 columns x 128 rows
+  CUtensorMap tmOut;         // out, box 32 outputs x 32 rows (wide kernel, rows on 16 bytes)
   CUtensorMap tmW;           // codes of the weight [E][N, ld(K)], box 128 k x 128 n
   const float* xs;           // scales of the tokens [ceil(C / 128)][M]
   const float* ws;           // scales of the weight [E][ceil(N / 128)][ceil(K / 128)]
@@ -231,9 +232,9 @@ __device__ __forceinline__ Tile tile_at(const Product& p, const Groups& g, int t
   constexpr int kRun = 8;
   const int run = t / (kRun * num_r), first = run * kRun, in = t - run * (kRun * num_r);
   const int width = min(kRun, num_m - first);
-  const int mt = first + in % width;
+  const int rt = width == kRun ? in / kRun : in / width, mt = first + in - rt * width;
   Tile x;
-  x.r0 = in / width * kTileR;
+  x.r0 = rt * kTileR;
   if (p.offsets == nullptr) {
     x.e = 0;
     x.m0 = mt * kTileM;
@@ -463,40 +464,61 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_product_kernel(const __grid_c
   if (warp == 1) tmem_dealloc(tmem, 256);
 }
 
-// ---- pairs of CTAs --------------------------------------------------------
+// ---- many tokens ----------------------------------------------------------
 
-constexpr int kWideThreads = 320;
-constexpr int kWideStoreBytes = 2048;     // per epilogue warp: 32 rows of 64 bytes
-constexpr int kWideEpiWarps = 8;
+constexpr int kWideThreads = 384;
+constexpr int kWideEpiWarps = 8;          // warps 4 to 11
+constexpr int kWideStages = 4;
+constexpr int kWideStageBytes = 3 * kTileBytes;
+constexpr int kWideCols = 128;            // outputs of an epilogue warp
+constexpr int kWideStoreBytes = 2048;     // per epilogue warp: 32 rows of 32 outputs
+// Registers a thread: 168 at launch (384 x 168 = 64512); of those the first
+// four warps keep 40 and the epilogue's take 232 (128 x 40 + 256 x 232 = 64512).
+constexpr int kWideRegs = 40, kWideEpiRegs = 232;
+static_assert(128 * kWideRegs + 256 * kWideEpiRegs <= kWideThreads * 168, "register split");
+constexpr int kScaleRing = 8;             // blocks whose scales are in shared memory
+constexpr int kScaleAhead = 6;            // ... of which so many are on their way
 struct WideShared {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full[2], acc_empty[2];
+  uint64_t full[kWideStages], empty[kWideStages];
+  uint64_t acc_full[2];                   // an accumulator is there, and the scales of its block and the next
+  uint64_t acc_empty[2];                  // it has been read
+  uint64_t scale_read[2];                 // the next block's scales have been read
   uint64_t last;
   uint32_t tmem;
   int abort;
-  float bias[kWideEpiWarps][128];
+  float bias[kWideEpiWarps][kWideCols];
+  float xs[kScaleRing][128], ws[kScaleRing][2];
 };
-constexpr int kWideSmemBytes = 1024 + kStages * kStageBytes + kWideEpiWarps * kWideStoreBytes + static_cast<int>(sizeof(WideShared));
+constexpr int kWideSmemBytes = 1024 + kWideStages * kWideStageBytes + kWideEpiWarps * kWideStoreBytes + static_cast<int>(sizeof(WideShared));
 
-__device__ __forceinline__ void umma_fp8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&a)[16]) {
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&a)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(a[i]));
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(a[i]));
 }
+// whether the phase has completed, without waiting for it
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void cp_async4(void* dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory"); }
+
+template <int kRegs>
+__device__ __forceinline__ void keep_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <int kRegs>
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 // two fp32 sums += two products
 __device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t scale2) {
   asm("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n fma.rn.f32x2 %0, d, %3, %0;\n}" : "+l"(acc) : "r"(lo), "r"(hi), "l"(scale2));
@@ -512,113 +534,161 @@ __device__ __forceinline__ float2 unpack2(uint64_t v) {
   return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
 
-// Tiles of 256 tokens x 256 outputs by pairs of CTAs: each CTA fetches and
-// holds half of either operand, the even CTA multiplies for both, and each
-// CTA's eight epilogue warps keep the sums of its own 128 tokens in registers
-// (128 outputs a thread).
+// Tiles of 128 tokens x 256 outputs; two accumulators in turn fill TMEM, and
+// eight warps keep the sums in registers (128 outputs a thread).
+// What bounds it is how fast an accumulator is handed back: a block's product
+// takes 512 clocks, and so do, from the other accumulator, its loads and fused
+// multiply-adds (2 clocks each and scheduler).  So the epilogue keeps a load
+// under way at all times, asks for the next accumulator before it needs it and
+// has its scales one block early; two threads multiply in turn, each for one
+// accumulator, since a wait costs over a tenth of a block's product even when
+// there is nothing to wait for; and warp 3 brings the scales to shared memory,
+// blocks and tiles ahead.
 template <bool kT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
-    fp8_product_wide_kernel(const __grid_constant__ Product p) {
-  constexpr int kTileM = 256, kTileR = 256;
+__global__ void __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const __grid_constant__ Product p) {
+  constexpr int kTileM = 128, kTileR = 256;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Groups groups;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* store = smem + kStages * kStageBytes;
+  uint8_t* store = smem + kWideStages * kWideStageBytes;
   WideShared& y = *reinterpret_cast<WideShared*>(store + kWideEpiWarps * kWideStoreBytes);
   volatile int* abort = &y.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int pair = static_cast<int>(cluster_id_x()), pairs = static_cast<int>(num_clusters_x());
+  const int first = blockIdx.x, step = gridDim.x;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kWideStages; ++i) {
       mbar_init(&y.full[i], 1);
       mbar_init(&y.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&y.acc_full[i], 1);
-      mbar_init(&y.acc_empty[i], 2 * kWideEpiWarps);
+      mbar_init(&y.acc_full[i], 2);
+      mbar_init(&y.acc_empty[i], kWideEpiWarps);
+      mbar_init(&y.scale_read[i], kWideEpiWarps);
     }
-    mbar_init(&y.last, 1);
+    mbar_init(&y.last, 2);
     y.abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.tmX);
     tma_prefetch_desc(&p.tmW);
+    if (p.vec) tma_prefetch_desc(&p.tmOut);
   }
   if (warp == 1) {
-    tmem_alloc_pair(&y.tmem, 512);
-    tmem_relinquish_pair();
+    tmem_alloc(&y.tmem, 512);
+    tmem_relinquish();
   }
-  if (warp == 2 && p.offsets != nullptr) plan_groups<kTileM>(p, groups, lane);
+  if (warp == 4 && p.offsets != nullptr) plan_groups<kTileM>(p, groups, lane);
   tc_fence_before();
-  cluster_sync();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = y.tmem;
   const int num_m = p.offsets == nullptr ? (p.M + kTileM - 1) / kTileM : groups.tile[p.E];
   const int num_r = (p.R + kTileR - 1) / kTileR;
   const int tiles = num_m * num_r, blocks = (p.C + kBlk - 1) / kBlk;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    keep_registers<kWideRegs>();
+    const int total = first < tiles ? ((tiles - 1 - first) / step + 1) * blocks : 0;   // of all of this CTA's tiles
+    if (warp == 0 && lane == 0) {
       grid_dependency_wait();
       asm volatile("fence.proxy.async;" ::: "memory");
-      const uint32_t full0 = mapa_shared(&y.full[0], 0);   // both CTAs' copies count on the even CTA's barriers
       int it = 0;
       bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs) {
+      for (int t = first; t < tiles && ok; t += step) {
         const Tile x = tile_at<kTileM, kTileR>(p, groups, t, num_m, num_r);
-        const int m = x.m0 + rank * 128, r = x.r0 + rank * 128;
         for (int b = 0; b < blocks; ++b, ++it) {
-          const int s = it % kStages;
-          if (!mbar_wait(&y.empty[s], ((it / kStages) & 1) ^ 1, abort, p.st, kWhereFetch)) {
+          const int s = it % kWideStages;
+          if (!mbar_wait(&y.empty[s], ((it / kWideStages) & 1) ^ 1, abort, p.st, kWhereFetch)) {
             ok = false;
             break;
           }
-          uint8_t* xd = smem + s * kStageBytes;
-          const uint32_t full = full0 + static_cast<uint32_t>(s) * 8u;
-          if (rank == 0) mbar_arrive_expect_tx(&y.full[s], 2 * kStageBytes);
-          tma_load_2d_pair(xd, &p.tmX, b * kBlk, m, full);
-          if (kT) tma_load_3d_pair(xd + kTileBytes, &p.tmW, r, b * kBlk, x.e, full);
-          else tma_load_3d_pair(xd + kTileBytes, &p.tmW, b * kBlk, r, x.e, full);
+          uint8_t* xd = smem + s * kWideStageBytes;
+          mbar_arrive_expect_tx(&y.full[s], kWideStageBytes);
+          tma_load_2d(xd, &p.tmX, b * kBlk, x.m0, &y.full[s]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint8_t* wd = xd + (1 + i) * kTileBytes;
+            if (kT) tma_load_3d(wd, &p.tmW, x.r0 + 128 * i, b * kBlk, x.e, &y.full[s]);
+            else tma_load_3d(wd, &p.tmW, b * kBlk, x.r0 + 128 * i, x.e, &y.full[s]);
+          }
         }
       }
-      // what is under way lands before the pair may end
-      if (rank == 0)
-        for (int j = max(0, it - kStages); j < it; ++j) mbar_wait_out(&y.full[j % kStages], (j / kStages) & 1, p.st, kWhereFetch);
+      // what is under way lands before the block may end
+      for (int j = max(0, it - kWideStages); j < it; ++j)
+        mbar_wait_out(&y.full[j % kWideStages], (j / kWideStages) & 1, p.st, kWhereFetch);
     }
-  } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if ((warp == 1 || warp == 2) && lane == 0) {
       const uint32_t idesc = make_idesc_f16(kTileM, kTileR, false, kT);   // E4M3 has the format number of fp16
       const uint32_t base = smem_u32(smem);
-      int it = 0;
-      bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs) {
-        for (int b = 0; b < blocks; ++b, ++it) {
-          const int s = it % kStages, a = it & 1;
-          if (!mbar_wait(&y.full[s], (it / kStages) & 1, abort, p.st, kWhereProduct) ||
-              !mbar_wait_cluster(&y.acc_empty[a], ((it >> 1) & 1) ^ 1, abort, p.st, kWhereProduct)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t xa = base + s * kStageBytes, wa = xa + kTileBytes;
+      const int a = warp - 1;
+      const uint32_t acc = tmem + a * kTileR;
+      for (int it = a; it < total; it += 2) {
+        const int s = it % kWideStages;
+        if (!mbar_wait(&y.full[s], (it / kWideStages) & 1, abort, p.st, kWhereProduct) ||
+            !mbar_wait(&y.acc_empty[a], ((it >> 1) & 1) ^ 1, abort, p.st, kWhereProduct))
+          break;
+        tc_fence_after();
+        const uint32_t xa = base + s * kWideStageBytes, wa = xa + kTileBytes;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_fp8_pair(tmem + a * kTileR, make_sdesc(xa + 32 * k, 16, 1024, kSwizzle128B),
-                          kT ? make_sdesc(wa + 4096 * k, kTileBytes, 1024, kSwizzle128B)
-                             : make_sdesc(wa + 32 * k, 16, 1024, kSwizzle128B),
-                          idesc, k > 0 ? 1u : 0u);
-          umma_commit_pair_mc(&y.empty[s], 0x3);
-          umma_commit_pair_mc(&y.acc_full[a], 0x3);
-        }
+        for (int k = 0; k < 4; ++k)
+          umma_fp8(acc, make_sdesc(xa + 32 * k, 16, 1024, kSwizzle128B),
+                   kT ? make_sdesc(wa + 4096 * k, kTileBytes, 1024, kSwizzle128B)
+                      : make_sdesc(wa + 32 * k, 16, 1024, kSwizzle128B),
+                   idesc, k > 0 ? 1u : 0u);
+        umma_commit(&y.acc_full[a]);
+        umma_commit(&y.empty[s]);
       }
-      umma_commit_pair(&y.last);
+      umma_commit(&y.last);
       mbar_wait_out(&y.last, 0, p.st, kWhereProduct);
     }
+    if (warp == 3) {
+      grid_dependency_wait();
+      int ft = first, fb = 0, fi = 0;   // the next block to fetch: its tile, its number there and in all
+      int rows[4];
+      const float* ws = p.ws;
+      auto aim = [&]() {
+        if (ft >= tiles) return;
+        const Tile x = tile_at<kTileM, kTileR>(p, groups, ft, num_m, num_r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rows[i] = min(x.m0 + i * 32 + lane, p.M - 1);
+        const int rb = min(x.r0 / kBlk + (lane & 1), (p.R - 1) / kBlk);
+        ws = p.ws + static_cast<int64_t>(x.e) * p.nb * p.kb + (kT ? rb : rb * p.kb);
+      };
+      auto fetch = [&]() {
+        if (ft < tiles) {
+          const int s = fi % kScaleRing;
+          const float* xs = p.xs + static_cast<int64_t>(fb) * p.M;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) cp_async4(&y.xs[s][i * 32 + lane], xs + rows[i]);
+          if (lane < 2) cp_async4(&y.ws[s][lane], ws);
+          ws += kT ? p.kb : 1;
+          ++fi;
+          if (++fb == blocks) {
+            fb = 0;
+            ft += step;
+            aim();
+          }
+        }
+        cp_async_commit();
+      };
+      aim();
+      for (int i = 0; i < kScaleAhead; ++i) fetch();
+      for (int it = 0; it < total; ++it) {
+        // with block it - 2 the scales of block it - 1 have been read; this
+        // fetch takes the place of an older one's
+        static_assert(kScaleAhead + 1 <= kScaleRing - 1, "scale ring");
+        if (!__all_sync(0xffffffffu, mbar_wait(&y.scale_read[it & 1], ((it >> 1) & 1) ^ 1, abort, p.st, kWhereOut))) break;
+        fetch();
+        cp_async_wait<kScaleAhead - 1>();   // block it + 1 is there
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&y.acc_full[it & 1]);
+      }
+      cp_async_wait<0>();
+    }
   } else {
-    const int quad = warp & 3, ew = warp - 2, half = ew >> 2;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
-    const uint32_t acc_empty0 = mapa_shared(&y.acc_empty[0], 0);
+    take_registers<kWideEpiRegs>();
+    const int quad = warp & 3, ew = warp - 4, half = ew >> 2;   // its lanes, and half of the outputs
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kWideCols;
     uint8_t* out_s = store + ew * kWideStoreBytes;
     float* bias_s = y.bias[ew];
     grid_dependency_wait();
@@ -626,87 +696,103 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       zero_rest(p, groups, blockIdx.x * kWideEpiWarps + ew, gridDim.x * kWideEpiWarps, lane);
     int it = 0;
     bool ok = true;
-    for (int t = pair; t < tiles && ok; t += pairs) {
+    float now = 0.f;   // the product of the scales of block it
+    auto scale_of = [&](int i) { return y.xs[i % kScaleRing][quad * 32 + lane] * y.ws[i % kScaleRing][half]; };
+    auto wait = [&]() { return __all_sync(0xffffffffu, mbar_wait(&y.acc_full[it & 1], (it >> 1) & 1, abort, p.st, kWhereOut)); };
+    for (int t = first; t < tiles && ok; t += step) {
       const Tile x = tile_at<kTileM, kTileR>(p, groups, t, num_m, num_r);
-      const int row0 = x.m0 + rank * 128 + quad * 32, r0 = x.r0 + half * 128;
-      const float* xs = p.xs + min(row0 + lane, p.M - 1);
-      const int rb = min(r0 / kBlk, (p.R - 1) / kBlk);
-      const float* ws = p.ws + static_cast<int64_t>(x.e) * p.nb * p.kb + (kT ? rb : rb * p.kb);
-      const int wstep = kT ? p.kb : 1;
-      uint64_t acc[64];
+      const int row0 = x.m0 + quad * 32, r0 = x.r0 + half * kWideCols;
+      float bias[4];   // used at the tile's end
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
-      __syncwarp();
-      for (int i = lane; i < 128; i += 32) bias_s[i] = bias_at(p, r0 + i);
-      __syncwarp();
-      // the scales are fetched two blocks ahead and multiplied when they are
-      // used: their latency in L2 is longer than a block's product
-      float x1 = xs[0], w1 = ws[0], x2 = 0.f, w2 = 0.f;
-      if (blocks > 1) {
-        x2 = xs[p.M];
-        w2 = ws[wstep];
-      }
-      for (int b = 0; b < blocks; ++b, ++it) {
+      for (int i = 0; i < 4; ++i) bias[i] = bias_at(p, r0 + lane + 32 * i);
+      uint64_t acc[kWideCols / 2];
+#pragma unroll
+      for (int i = 0; i < kWideCols / 2; ++i) acc[i] = 0;
+      uint32_t d[2][32];
+      if (!(ok = wait())) break;
+      tc_fence_after();
+      tmem_ld32_nowait(lanes + (it & 1) * kTileR, d[0]);
+      if (it == 0) now = scale_of(0);
+      for (int b = 0; b < blocks; ++b) {
         const int a = it & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&y.acc_full[a], (it >> 1) & 1, abort, p.st, kWhereOut))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        uint32_t d[2][16];
-        tmem_ld16_nowait(lanes + a * kTileR, d[0]);
-        const uint64_t scale = splat2(x1 * w1);
-        x1 = x2;
-        w1 = w2;
-        if (b + 2 < blocks) {
-          x2 = xs[static_cast<int64_t>(b + 2) * p.M];
-          w2 = ws[(b + 2) * wstep];
-        }
+        const uint64_t scale = splat2(now);
+        bool ready = true;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          tmem_ld_wait16(d[c & 1]);
-          if (c < 7) tmem_ld16_nowait(lanes + a * kTileR + 16 * (c + 1), d[(c + 1) & 1]);
-          if (c == 7) {
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait(d[c & 1]);
+          if (c < 3) tmem_ld32_nowait(lanes + a * kTileR + 32 * (c + 1), d[(c + 1) & 1]);
+          if (c == 1) {
+            now = scale_of(it + 1);
+            ready = mbar_test(&y.acc_full[a ^ 1], ((it + 1) >> 1) & 1);
+          }
+          if (c == 3) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(acc_empty0 + static_cast<uint32_t>(a) * 8u);
+            if (lane == 0) {
+              mbar_arrive(&y.acc_empty[a]);
+              mbar_arrive(&y.scale_read[a]);
+            }
+            ++it;
+            if (b + 1 < blocks) {
+              if (!__all_sync(0xffffffffu, ready)) ok = wait();
+              if (!ok) break;
+              tc_fence_after();
+              tmem_ld32_nowait(lanes + (a ^ 1) * kTileR, d[0]);
+            }
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) fma2(acc[8 * c + i], d[c & 1][2 * i], d[c & 1][2 * i + 1], scale);
+          for (int i = 0; i < 16; ++i) fma2(acc[16 * c + i], d[c & 1][2 * i], d[c & 1][2 * i + 1], scale);
         }
+        if (!ok) break;
       }
       if (!ok) break;
-      // out through shared memory, 32 outputs of 32 rows at a time, so that
-      // rows are written in whole sectors
+      // out through shared memory, 32 outputs of 32 rows at a time
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
+      for (int i = 0; i < 4; ++i) bias_s[lane + 32 * i] = bias[i];
+      const bool inside = p.vec && row0 + 32 <= x.end;
+#pragma unroll
+      for (int h = 0; h < kWideCols / 32; ++h) {
+        if (lane == 0) bulk_wait_read<0>();   // the store ahead has left the buffer
         __syncwarp();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t q[4];
+          const float4 b0 = *reinterpret_cast<const float4*>(bias_s + h * 32 + c * 8);
+          const float4 b1 = *reinterpret_cast<const float4*>(bias_s + h * 32 + c * 8 + 4);
+          const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int k = h * 32 + c * 8 + 2 * i;
-            const float2 v = unpack2(acc[k >> 1]);
-            q[i] = pack16(p.bf16, v.x + bias_s[k], v.y + bias_s[k + 1]);
+            const float2 v = unpack2(acc[h * 16 + c * 4 + i]);
+            q[i] = pack16(p.bf16, v.x + bv[2 * i], v.y + bv[2 * i + 1]);
           }
           st_shared_v4(out_s + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), make_uint4(q[0], q[1], q[2], q[3]));
         }
-        __syncwarp();
+        const int r = r0 + h * 32;
+        if (inside) {   // outputs past the last are not written
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && r < p.R) {
+            tma_store_2d(&p.tmOut, r, row0, out_s);
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = i * 8 + (lane >> 2), c = lane & 3;
-          const uint4 v = ld_shared_v4(out_s + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
-          const int mm = row0 + row, r = r0 + h * 32 + c * 8;
-          if (mm < x.end && r < p.R) store_out8(p, mm, r, v);
+          for (int i = 0; i < 4; ++i) {
+            const int row = i * 8 + (lane >> 2), c = lane & 3;
+            const uint4 v = ld_shared_v4(out_s + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+            if (row0 + row < x.end && r + c * 8 < p.R) store_out8(p, row0 + row, r + c * 8, v);
+          }
         }
       }
+      __syncwarp();
     }
+    if (lane == 0) bulk_wait_all();
   }
   tc_fence_before();
-  cluster_sync();
+  __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -755,10 +841,10 @@ template <bool kT>
 cudaError_t launch_product(const Product& p, cudaStream_t s) {
   const int sms = sm_count();
   const int64_t extra = p.offsets == nullptr ? 0 : p.E;   // experts' last tiles, at most
-  const int64_t wide = (ceil_div(p.M, 256) + extra) * ceil_div(p.R, 256);
-  if (p.M / p.E >= 256 && wide >= sms / 2)
-    return launch_after(fp8_product_wide_kernel<kT>, 2 * static_cast<unsigned>(std::min<int64_t>(wide, sms / 2)),
-                        kWideThreads, kWideSmemBytes, p, s);
+  const int64_t wide = (ceil_div(p.M, 128) + extra) * ceil_div(p.R, 256);
+  if (p.M / p.E >= 256 && wide >= sms)
+    return launch_after(fp8_product_wide_kernel<kT>, static_cast<unsigned>(std::min<int64_t>(wide, sms)), kWideThreads,
+                        kWideSmemBytes, p, s);
   const int64_t tiles = (ceil_div(p.M, kTileM) + extra) * ceil_div(p.R, kTileR);
   return launch_after(fp8_product_kernel<kT>, static_cast<unsigned>(std::min<int64_t>(tiles, sms)), kThreads, kSmemBytes,
                       p, s);
@@ -809,6 +895,10 @@ int product(bool transposed, const void* x, int xt, int64_t M, const uint8_t* co
       !make_tmap_3d(&p.tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, code_ld(K), N, E, 1, kBlk, kTileR,
                     CU_TENSOR_MAP_SWIZZLE_128B))
     return ST_CUDA;
+  p.vec = R % 8 == 0;
+  if (p.vec && !make_tmap(&p.tmOut, xt == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, out,
+                          R, M, R * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    return ST_CUDA;
   p.xs = qs;
   p.ws = scales;
   p.offsets = offsets;
@@ -823,7 +913,6 @@ int product(bool transposed, const void* x, int xt, int64_t M, const uint8_t* co
   p.nb = static_cast<int>(ceil_div(N, kBlk));
   p.kb = static_cast<int>(ceil_div(K, kBlk));
   p.bf16 = xt == DT_BF16;
-  p.vec = R % 8 == 0;
   p.zero_rest = zero_rest != 0;
   if (cudaError_t e = launch_quantize(x, xt, M, C, q, qs, st, s)) return cuda_status(e);
   return cuda_status(transposed ? launch_product<true>(p, s) : launch_product<false>(p, s));
