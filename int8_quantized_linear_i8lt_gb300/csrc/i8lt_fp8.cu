@@ -139,9 +139,9 @@ __global__ void __launch_bounds__(256) fp8_dequantize_weight_kernel(const uint8_
 // ---------------------------------------------------------------------------
 
 struct Product {
-  CUtensorMap tmX;           // codes of the tokens [M, ld(C)], box 128 columns x 128 rows
+  CUtensorMap tmX;           // codes of the tokens [M, ld(C)], box 128 columns x a tile's tokens
+  CUtensorMap tmW;           // codes of the weight [E][N, ld(K)], box of a block and up to 128 outputs
   CUtensorMap tmOut;         // out, box 32 outputs x 32 rows (wide kernel, rows on 16 bytes)
-  CUtensorMap tmW;           // codes of the weight [E][N, ld(K)], box 128 k x 128 n
   const float* xs;           // scales of the tokens [ceil(C / 128)][M]
   const float* ws;           // scales of the weight [E][ceil(N / 128)][ceil(K / 128)]
   const int32_t* offsets;    // [E + 1] row ranges of the experts, or NULL: one weight for all rows
@@ -150,36 +150,21 @@ struct Product {
   DevStatus* st;
   int M, R, C, E;
   int nb, kb;                // blocks of the weight along N and K
+  int tile_m, stages, split; // small kernel: tokens of a tile, stages, CTAs that share a tile's reduction
   int bias_dt;
   bool bf16;                 // type of out: bf16, else fp16
   bool vec;                  // rows of out start on 16 bytes
   bool zero_rest;            // rows of no expert are written as zeros (else left as they are)
 };
 
-constexpr int kTileM = 128, kTileR = 128;
-constexpr int kStages = 6;
 constexpr int kTileBytes = 128 * 128;
-constexpr int kStageBytes = 2 * kTileBytes;
-constexpr int kThreads = 192;
-constexpr int kEpiWarp0 = 2;         // warps 2 to 5: lanes 32 (w % 4) of the accumulators
-constexpr int kStoreBytes = 4096;    // per epilogue warp: 32 rows of 128 bytes on their way out
 enum { kWhereFetch = 1, kWhereProduct = 2, kWhereOut = 3 };
 
-struct Shared {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full[2], acc_empty[2];
-  uint64_t last;                     // all products have completed
-  uint32_t tmem;
-  int abort;
-  float bias[4][kTileR];
-};
 // of several experts: their first rows and first token tiles
 struct Groups {
   int begin[kMaxExperts + 1];        // begin[E]: the end of the last expert's rows
   int tile[kMaxExperts + 1];
 };
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 4 * kStoreBytes + static_cast<int>(sizeof(Shared));
-
 __device__ __forceinline__ void umma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
@@ -191,8 +176,7 @@ __device__ __forceinline__ void umma_fp8(uint32_t d, uint64_t a, uint64_t b, uin
 // The row ranges of the experts, by one warp.  They are data: each start is
 // taken as at least the one before it and at most M, so that no range leaves
 // the tokens or overlaps another one whatever the values are.
-template <int kTileM>
-__device__ __forceinline__ void plan_groups(const Product& p, Groups& g, int lane) {
+__device__ __forceinline__ void plan_groups(const Product& p, Groups& g, int tile_m, int lane) {
   int first = 0, tiles = 0;
   // begin[e] = min(M, max(0, offsets[0 .. e]))
   for (int e0 = 0; e0 <= p.E; e0 += 32) {
@@ -210,7 +194,7 @@ __device__ __forceinline__ void plan_groups(const Product& p, Groups& g, int lan
   __syncwarp();
   for (int e0 = 0; e0 <= p.E; e0 += 32) {
     const int e = e0 + lane;
-    int t = e < p.E ? (g.begin[e + 1] - g.begin[e] + kTileM - 1) / kTileM : 0;
+    int t = e < p.E ? (g.begin[e + 1] - g.begin[e] + tile_m - 1) / tile_m : 0;
     const int own = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -227,8 +211,8 @@ struct Tile {
 };
 // Tile t: runs of 8 token tiles for each tile of outputs, so that tiles at
 // work together share tokens and weights in L2.
-template <int kTileM, int kTileR>
-__device__ __forceinline__ Tile tile_at(const Product& p, const Groups& g, int t, int num_m, int num_r) {
+template <int kTileR>
+__device__ __forceinline__ Tile tile_at(const Product& p, const Groups& g, int t, int num_m, int num_r, int tile_m) {
   constexpr int kRun = 8;
   const int run = t / (kRun * num_r), first = run * kRun, in = t - run * (kRun * num_r);
   const int width = min(kRun, num_m - first);
@@ -237,7 +221,7 @@ __device__ __forceinline__ Tile tile_at(const Product& p, const Groups& g, int t
   x.r0 = rt * kTileR;
   if (p.offsets == nullptr) {
     x.e = 0;
-    x.m0 = mt * kTileM;
+    x.m0 = mt * tile_m;
     x.end = p.M;
     return x;
   }
@@ -248,7 +232,7 @@ __device__ __forceinline__ Tile tile_at(const Product& p, const Groups& g, int t
     else hi = mid;
   }
   x.e = lo;
-  x.m0 = g.begin[lo] + (mt - g.tile[lo]) * kTileM;
+  x.m0 = g.begin[lo] + (mt - g.tile[lo]) * tile_m;
   x.end = g.begin[lo + 1];
   return x;
 }
@@ -292,29 +276,87 @@ __device__ __forceinline__ void store_out8(const Product& p, int64_t m, int r, c
   }
 }
 
-// D tile by tile (persistent).  Warp 0 fetches, warp 1 multiplies: one
-// accumulator in TMEM per 128 columns of the reduction, two of them in turn.
-// Warps 2 to 5 add each, times its two scales, to the sums that they hold in
-// registers: a thread has one token and 128 outputs, so the product of the
-// scales is one number.
-template <bool kT>
-__global__ void __launch_bounds__(kThreads, 1) fp8_product_kernel(const __grid_constant__ Product p) {
+constexpr uint32_t kSwizzle64B = 4;
+
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&a)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(a[i]));
+}
+// two fp32 sums += two products
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t scale2) {
+  asm("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n fma.rn.f32x2 %0, d, %3, %0;\n}" : "+l"(acc) : "r"(lo), "r"(hi), "l"(scale2));
+}
+__device__ __forceinline__ uint64_t splat2(float f) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "r"(__float_as_uint(f)));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+  return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+// ---- few tokens, small products -------------------------------------------
+
+constexpr int kThreads = 192;
+constexpr int kEpiWarps = 4;         // warps 2 to 5: lanes 32 (w % 4) of the accumulators
+constexpr int kMaxStages = 8;
+template <int kTileR>
+struct Shared {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t last;                     // all products have completed
+  uint32_t tmem;
+  int abort;
+  float bias[kEpiWarps][kTileR];
+};
+// Shared memory of a CTA: the stages, what a product reads past the tokens of
+// the last one (it takes 128 rows, fetched or not: those of no token give
+// accumulator lanes that nobody reads), barriers.
+template <int kTileR>
+constexpr int small_smem(int tile_m, int stages) {
+  return 1024 + stages * (tile_m + kTileR) * 128 + (128 - tile_m) * 128 + static_cast<int>(sizeof(Shared<kTileR>));
+}
+
+// Tiles of 16 to 128 tokens x kTileR outputs.  Warp 0 fetches, warp 1
+// multiplies: one accumulator in TMEM per 128 columns of the reduction, two of
+// them in turn.  Warps 2 to 5 add each, times its two scales, to the sums that
+// they hold in registers: a thread has one token and kTileR outputs, so the
+// product of the scales is one number.  The weight does not depend on the
+// kernel before, so its first stages are on their way while the tokens are
+// being quantized.  With few tiles a cluster of `split` CTAs shares a tile:
+// each has a part of the reduction, and the parts are added in the order of
+// the ranks.
+template <bool kT, int kTileR>
+__global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_constant__ Product p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Groups groups;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* store = smem + kStages * kStageBytes;
-  Shared& y = *reinterpret_cast<Shared*>(store + 4 * kStoreBytes);
+  const int tile_m = p.tile_m, x_bytes = tile_m * 128, stage_bytes = x_bytes + kTileR * 128, stages = p.stages;
+  Shared<kTileR>& y = *reinterpret_cast<Shared<kTileR>*>(smem + stages * stage_bytes + (128 - tile_m) * 128);
   volatile int* abort = &y.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = static_cast<int>(blockIdx.x) / p.split, step = static_cast<int>(gridDim.x) / p.split;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < stages; ++i) {
       mbar_init(&y.full[i], 1);
       mbar_init(&y.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&y.acc_full[i], 1);
-      mbar_init(&y.acc_empty[i], 4);
+      mbar_init(&y.acc_empty[i], kEpiWarps);
     }
     mbar_init(&y.last, 1);
     y.abort = 0;
@@ -323,66 +365,76 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_product_kernel(const __grid_c
     tma_prefetch_desc(&p.tmW);
   }
   if (warp == 1) {
-    tmem_alloc(&y.tmem, 256);
+    tmem_alloc(&y.tmem, 2 * kTileR);
     tmem_relinquish();
   }
-  if (warp == 2 && p.offsets != nullptr) plan_groups<kTileM>(p, groups, lane);
+  if (warp == 2 && p.offsets != nullptr) plan_groups(p, groups, tile_m, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = y.tmem;
-  const int num_m = p.offsets == nullptr ? (p.M + kTileM - 1) / kTileM : groups.tile[p.E];
+  const int num_m = p.offsets == nullptr ? (p.M + tile_m - 1) / tile_m : groups.tile[p.E];
   const int num_r = (p.R + kTileR - 1) / kTileR;
-  const int tiles = num_m * num_r, blocks = (p.C + kBlk - 1) / kBlk;
+  const int tiles = num_m * num_r, all = (p.C + kBlk - 1) / kBlk;
+  const int b0 = all * rank / p.split, b1 = all * (rank + 1) / p.split;   // this CTA's blocks of a tile's reduction
 
   if (warp == 0) {
     if (lane == 0) {
+      auto fetch_w = [&](int s, const Tile& x, int b) {
+        uint8_t* wd = smem + s * stage_bytes + x_bytes;
+        mbar_arrive_expect_tx(&y.full[s], stage_bytes);
+        if (kT) tma_load_3d(wd, &p.tmW, x.r0, b * kBlk, x.e, &y.full[s]);
+        else tma_load_3d(wd, &p.tmW, b * kBlk, x.r0, x.e, &y.full[s]);
+      };
+      int it = 0, ahead = 0;
+      bool ok = true;
+      if (first < tiles) {
+        const Tile x = tile_at<kTileR>(p, groups, first, num_m, num_r, tile_m);
+        ahead = min(stages, b1 - b0);
+        for (int s = 0; s < ahead; ++s) fetch_w(s, x, b0 + s);
+      }
       grid_dependency_wait();
       asm volatile("fence.proxy.async;" ::: "memory");
-      int it = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const Tile x = tile_at<kTileM, kTileR>(p, groups, t, num_m, num_r);
-        for (int b = 0; b < blocks; ++b, ++it) {
-          const int s = it % kStages;
-          if (!mbar_wait(&y.empty[s], ((it / kStages) & 1) ^ 1, abort, p.st, kWhereFetch)) {
-            ok = false;
+      for (int t = first; t < tiles && ok; t += step) {
+        const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, tile_m);
+        for (int b = b0; b < b1; ++b, ++it) {
+          const int s = it % stages;
+          if (!mbar_wait(&y.empty[s], ((it / stages) & 1) ^ 1, abort, p.st, kWhereFetch)) {
+            ok = false;   // not before the fetches ahead have their tokens: those stages are empty
             break;
           }
-          uint8_t* xd = smem + s * kStageBytes;
-          mbar_arrive_expect_tx(&y.full[s], kStageBytes);
-          tma_load_2d(xd, &p.tmX, b * kBlk, x.m0, &y.full[s]);
-          if (kT) tma_load_3d(xd + kTileBytes, &p.tmW, x.r0, b * kBlk, x.e, &y.full[s]);
-          else tma_load_3d(xd + kTileBytes, &p.tmW, b * kBlk, x.r0, x.e, &y.full[s]);
+          if (it >= ahead) fetch_w(s, x, b);
+          tma_load_2d(smem + s * stage_bytes, &p.tmX, b * kBlk, x.m0, &y.full[s]);
         }
       }
       // what is under way lands before the block may end
-      for (int j = max(0, it - kStages); j < it; ++j) mbar_wait_out(&y.full[j % kStages], (j / kStages) & 1, p.st, kWhereFetch);
+      for (int j = max(0, it - stages); j < it; ++j) mbar_wait_out(&y.full[j % stages], (j / stages) & 1, p.st, kWhereFetch);
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = make_idesc_f16(kTileM, kTileR, false, kT);   // E4M3 has the format number of fp16
+      const uint32_t idesc = make_idesc_f16(128, kTileR, false, kT);   // E4M3 has the format number of fp16
       const uint32_t base = smem_u32(smem);
       int it = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        for (int b = 0; b < blocks; ++b, ++it) {
-          const int s = it % kStages, a = it & 1;
-          if (!mbar_wait(&y.acc_empty[a], ((it >> 1) & 1) ^ 1, abort, p.st, kWhereProduct) ||
-              !mbar_wait(&y.full[s], (it / kStages) & 1, abort, p.st, kWhereProduct)) {
+      for (int t = first; t < tiles && ok; t += step) {
+        for (int b = b0; b < b1; ++b, ++it) {
+          const int s = it % stages, a = it & 1;
+          if (!mbar_wait(&y.full[s], (it / stages) & 1, abort, p.st, kWhereProduct) ||
+              !mbar_wait(&y.acc_empty[a], ((it >> 1) & 1) ^ 1, abort, p.st, kWhereProduct)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t xa = base + s * kStageBytes, wa = xa + kTileBytes;
+          const uint32_t xa = base + s * stage_bytes, wa = xa + x_bytes;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             umma_fp8(tmem + a * kTileR, make_sdesc(xa + 32 * k, 16, 1024, kSwizzle128B),
-                     kT ? make_sdesc(wa + 4096 * k, kTileBytes, 1024, kSwizzle128B)
-                        : make_sdesc(wa + 32 * k, 16, 1024, kSwizzle128B),
+                     !kT            ? make_sdesc(wa + 32 * k, 16, 1024, kSwizzle128B)
+                     : kTileR == 64 ? make_sdesc(wa + 2048 * k, 64 * 128, 512, kSwizzle64B)
+                                    : make_sdesc(wa + 4096 * k, kTileBytes, 1024, kSwizzle128B),
                      idesc, k > 0 ? 1u : 0u);
-          umma_commit(&y.empty[s]);
           umma_commit(&y.acc_full[a]);
+          umma_commit(&y.empty[s]);
         }
       }
       umma_commit(&y.last);
@@ -391,77 +443,147 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_product_kernel(const __grid_c
   } else {
     const int quad = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    uint8_t* out_s = store + quad * kStoreBytes;
     float* bias_s = y.bias[quad];
     grid_dependency_wait();
     if (p.offsets != nullptr && p.zero_rest)
-      zero_rest(p, groups, blockIdx.x * 4 + quad, gridDim.x * 4, lane);
+      zero_rest(p, groups, blockIdx.x * kEpiWarps + quad, gridDim.x * kEpiWarps, lane);
+    const int wstep = kT ? p.kb : 1;
     int it = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile x = tile_at<kTileM, kTileR>(p, groups, t, num_m, num_r);
-      const int m = x.m0 + quad * 32 + lane;
-      const float* xs = p.xs + min(m, p.M - 1);
-      const float* ws = p.ws + static_cast<int64_t>(x.e) * p.nb * p.kb + (kT ? x.r0 / kBlk : x.r0 / kBlk * p.kb);
-      const int wstep = kT ? p.kb : 1;
-      float acc[kTileR];
+    for (int t = first; t < tiles && ok; t += step) {
+      const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, tile_m);
+      const int last = min(x.end, x.m0 + tile_m), row0 = x.m0 + quad * 32, m = row0 + lane;
+      const bool any = row0 < last;   // a warp without tokens hands the accumulators on
+      const float* xs = p.xs + static_cast<int64_t>(b0) * p.M + min(m, p.M - 1);
+      const float* ws = p.ws + static_cast<int64_t>(x.e) * p.nb * p.kb + (kT ? x.r0 / kBlk : x.r0 / kBlk * p.kb) +
+                        static_cast<int64_t>(b0) * wstep;
+      uint64_t acc[kTileR / 2];
 #pragma unroll
-      for (int i = 0; i < kTileR; ++i) acc[i] = 0.f;
-      __syncwarp();
-      for (int i = lane; i < kTileR; i += 32) bias_s[i] = bias_at(p, x.r0 + i);
-      __syncwarp();
-      float next = xs[0] * ws[0];
-      for (int b = 0; b < blocks; ++b, ++it) {
+      for (int i = 0; i < kTileR / 2; ++i) acc[i] = 0;
+      float bias[kTileR / 32];   // used at the tile's end
+#pragma unroll
+      for (int i = 0; i < kTileR / 32; ++i) bias[i] = any ? bias_at(p, x.r0 + lane + 32 * i) : 0.f;
+      // the scales are fetched two blocks ahead and multiplied when they are used
+      float x1 = 0.f, w1 = 0.f, x2 = 0.f, w2 = 0.f;
+      if (any && b0 < b1) {
+        x1 = xs[0];
+        w1 = ws[0];
+        if (b0 + 1 < b1) {
+          x2 = xs[p.M];
+          w2 = ws[wstep];
+        }
+      }
+      for (int b = 0; b < b1 - b0; ++b, ++it) {
         const int a = it & 1;
-        const float scale = next;
-        if (b + 1 < blocks) next = xs[static_cast<int64_t>(b + 1) * p.M] * ws[(b + 1) * wstep];
         if (!__all_sync(0xffffffffu, mbar_wait(&y.acc_full[a], (it >> 1) & 1, abort, p.st, kWhereOut))) {
           ok = false;
           break;
         }
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < kTileR; c += 32) {
+        if (any) {
+          tc_fence_after();
           uint32_t d[32];
-          tmem_ld32(lanes + a * kTileR + c, d);
+          tmem_ld32_nowait(lanes + a * kTileR, d);
+          const uint64_t scale = splat2(x1 * w1);
+          x1 = x2;
+          w1 = w2;
+          if (b + 2 < b1 - b0) {
+            x2 = xs[static_cast<int64_t>(b + 2) * p.M];
+            w2 = ws[static_cast<int64_t>(b + 2) * wstep];
+          }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(d[i]), scale, acc[c + i]);
+          for (int c = 0; c < kTileR / 32; ++c) {
+            tmem_ld_wait(d);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) fma2(acc[16 * c + i], d[2 * i], d[2 * i + 1], scale);
+            if (c + 1 < kTileR / 32) tmem_ld32_nowait(lanes + a * kTileR + 32 * (c + 1), d);
+          }
+          tc_fence_before();
         }
-        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&y.acc_empty[a]);
       }
       if (!ok) break;
-      // out through shared memory: 64 outputs of 32 rows at a time, so that
-      // each row is written in whole lines
+      if (p.split > 1) {
+        // all of this CTA's products have completed: its stages hold the sums
+        // now, one row of the tile after another, 16-byte chunks permuted
+        const int row = quad * 32 + lane;
+        if (row < tile_m) {
+          float4* dst = reinterpret_cast<float4*>(smem) + row * (kTileR / 4);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+          for (int i = 0; i < kTileR / 4; ++i) {
+            const float2 lo = unpack2(acc[2 * i]), hi = unpack2(acc[2 * i + 1]);
+            dst[i ^ (row & 7)] = make_float4(lo.x, lo.y, hi.x, hi.y);
+          }
+        }
+      } else if (any) {
         __syncwarp();
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t q[4];
+        for (int i = 0; i < kTileR / 32; ++i) bias_s[lane + 32 * i] = bias[i];
+        __syncwarp();
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(m) * p.R + x.r0;
+        if (m < last) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int k = h * 64 + c * 8 + 2 * i;
-            q[i] = pack16(p.bf16, acc[k] + bias_s[k], acc[k + 1] + bias_s[k + 1]);
+          for (int i = 0; i < kTileR / 8; ++i) {
+            const float4 lo = *reinterpret_cast<const float4*>(bias_s + 8 * i);
+            const float4 hi = *reinterpret_cast<const float4*>(bias_s + 8 * i + 4);
+            const float bv[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            uint32_t q[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 v = unpack2(acc[4 * i + k]);
+              q[k] = pack16(p.bf16, v.x + bv[2 * k], v.y + bv[2 * k + 1]);
+            }
+            const int r = x.r0 + 8 * i;
+            if (p.vec) {
+              if (r < p.R) *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(q[0], q[1], q[2], q[3]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (r + k < p.R) dst[8 * i + k] = static_cast<uint16_t>(q[k >> 1] >> (16 * (k & 1)));
+            }
           }
-          st_shared_v4(out_s + lane * 128 + ((c ^ (lane & 7)) << 4), make_uint4(q[0], q[1], q[2], q[3]));
         }
         __syncwarp();
+      }
+    }
+  }
+  if (p.split > 1) {
+    // one tile a cluster; every rank adds up its share of the tile, 4 outputs
+    // at a time
+    cluster_sync();
+    if (warp >= 2 && first < tiles && *abort == 0) {
+      const Tile x = tile_at<kTileR>(p, groups, first, num_m, num_r, tile_m);
+      const int rows = min(tile_m, x.end - x.m0), count = rows * (kTileR / 4);
+      for (int g = rank * (kEpiWarps * 32) + static_cast<int>(threadIdx.x) - 64; g < count; g += p.split * kEpiWarps * 32) {
+        const int row = g / (kTileR / 4), i = g % (kTileR / 4), r = x.r0 + 4 * i;
+        if (r >= p.R) continue;
+        const float4* src = reinterpret_cast<const float4*>(smem) + row * (kTileR / 4) + (i ^ (row & 7));
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < p.split; ++k) {
+          const float4 part = ld_cluster4(mapa_shared(src, static_cast<uint32_t>(k)));
+          v.x += part.x;
+          v.y += part.y;
+          v.z += part.z;
+          v.w += part.w;
+        }
+        const uint32_t q[2] = {pack16(p.bf16, v.x + bias_at(p, r), v.y + bias_at(p, r + 1)),
+                               pack16(p.bf16, v.z + bias_at(p, r + 2), v.w + bias_at(p, r + 3))};
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(x.m0 + row) * p.R + r;
+        if (p.vec) {
+          *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = i * 4 + (lane >> 3), c = lane & 7;
-          const uint4 v = ld_shared_v4(out_s + row * 128 + ((c ^ (row & 7)) << 4));
-          const int mm = x.m0 + quad * 32 + row, r = x.r0 + h * 64 + c * 8;
-          if (mm < x.end && r < p.R) store_out8(p, mm, r, v);
+          for (int k = 0; k < 4; ++k)
+            if (r + k < p.R) dst[k] = static_cast<uint16_t>(q[k >> 1] >> (16 * (k & 1)));
         }
       }
     }
+    cluster_sync();   // no CTA leaves while another reads its sums
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 256);
+  if (warp == 1) tmem_dealloc(tmem, 2 * kTileR);
 }
 
 // ---- many tokens ----------------------------------------------------------
@@ -491,11 +613,6 @@ struct WideShared {
 };
 constexpr int kWideSmemBytes = 1024 + kWideStages * kWideStageBytes + kWideEpiWarps * kWideStoreBytes + static_cast<int>(sizeof(WideShared));
 
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&a)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(a[i]));
-}
 // whether the phase has completed, without waiting for it
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -519,21 +636,6 @@ template <int kRegs>
 __device__ __forceinline__ void keep_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 template <int kRegs>
 __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-// two fp32 sums += two products
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t scale2) {
-  asm("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n fma.rn.f32x2 %0, d, %3, %0;\n}" : "+l"(acc) : "r"(lo), "r"(hi), "l"(scale2));
-}
-__device__ __forceinline__ uint64_t splat2(float f) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "r"(__float_as_uint(f)));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  uint32_t a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
-  return make_float2(__uint_as_float(a), __uint_as_float(b));
-}
-
 // Tiles of 128 tokens x 256 outputs; two accumulators in turn fill TMEM, and
 // eight warps keep the sums in registers (128 outputs a thread).
 // What bounds it is how fast an accumulator is handed back: a block's product
@@ -577,7 +679,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const
     tmem_alloc(&y.tmem, 512);
     tmem_relinquish();
   }
-  if (warp == 4 && p.offsets != nullptr) plan_groups<kTileM>(p, groups, lane);
+  if (warp == 4 && p.offsets != nullptr) plan_groups(p, groups, kTileM, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -595,7 +697,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const
       int it = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
-        const Tile x = tile_at<kTileM, kTileR>(p, groups, t, num_m, num_r);
+        const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, kTileM);
         for (int b = 0; b < blocks; ++b, ++it) {
           const int s = it % kWideStages;
           if (!mbar_wait(&y.empty[s], ((it / kWideStages) & 1) ^ 1, abort, p.st, kWhereFetch)) {
@@ -648,7 +750,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const
       const float* ws = p.ws;
       auto aim = [&]() {
         if (ft >= tiles) return;
-        const Tile x = tile_at<kTileM, kTileR>(p, groups, ft, num_m, num_r);
+        const Tile x = tile_at<kTileR>(p, groups, ft, num_m, num_r, kTileM);
 #pragma unroll
         for (int i = 0; i < 4; ++i) rows[i] = min(x.m0 + i * 32 + lane, p.M - 1);
         const int rb = min(x.r0 / kBlk + (lane & 1), (p.R - 1) / kBlk);
@@ -700,7 +802,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const
     auto scale_of = [&](int i) { return y.xs[i % kScaleRing][quad * 32 + lane] * y.ws[i % kScaleRing][half]; };
     auto wait = [&]() { return __all_sync(0xffffffffu, mbar_wait(&y.acc_full[it & 1], (it >> 1) & 1, abort, p.st, kWhereOut)); };
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile x = tile_at<kTileM, kTileR>(p, groups, t, num_m, num_r);
+      const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, kTileM);
       const int row0 = x.m0 + quad * 32, r0 = x.r0 + half * kWideCols;
       float bias[4];   // used at the tile's end
 #pragma unroll
@@ -821,33 +923,71 @@ cudaError_t launch_quantize(const void* x, int xt, int64_t M, int64_t C, uint8_t
 }
 
 // The kernel after the quantising one: it sets itself up while that one runs.
-cudaError_t launch_after(void (*kernel)(Product), unsigned grid, int threads, int smem, const Product& p, cudaStream_t s) {
+cudaError_t launch_after(void (*kernel)(Product), int64_t grid, int threads, int smem, int cluster, const Product& p,
+                         cudaStream_t s) {
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem)) return cudaGetLastError();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   ProfScope ps(K_FP8_GEMM, s);
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// The tensor maps of a variant whose boxes have `rows` tokens and `outputs`
+// outputs (of one block of the reduction).
+bool make_maps(Product& p, bool kt, const void* x, const void* w, int rows, int outputs) {
+  const int64_t N = kt ? p.C : p.R, K = kt ? p.R : p.C;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  return make_tmap(&p.tmX, u8, x, code_ld(p.C), p.M, code_ld(p.C), kBlk, rows, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         make_tmap_3d(&p.tmW, u8, w, code_ld(K), N, p.E, 1, kt ? outputs : kBlk, kt ? kBlk : outputs,
+                      kt && outputs == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <bool kT, int kTileR>
+int launch_small(Product& p, const void* x, const void* w, int64_t tiles, cudaStream_t s) {
+  constexpr int kBudget = 107000;   // two CTAs an SM
+  const int sms = sm_count(), blocks = static_cast<int>(ceil_div(p.C, kBlk));
+  p.stages = kMaxStages;
+  while (p.stages > 2 && small_smem<kTileR>(p.tile_m, p.stages) > kBudget) --p.stages;
+  p.split = 1;
+  while (p.split < 8 && 2 * p.split * tiles <= 2 * sms && 2 * p.split <= blocks / 2) p.split *= 2;
+  if (!make_maps(p, kT, x, w, p.tile_m, kTileR)) return ST_CUDA;
+  const int64_t grid = p.split > 1 ? tiles * p.split : std::min<int64_t>(tiles, 2 * sms);
+  return cuda_status(launch_after(fp8_product_kernel<kT, kTileR>, grid, kThreads, small_smem<kTileR>(p.tile_m, p.stages),
+                                  p.split, p, s));
+}
+
 template <bool kT>
-cudaError_t launch_product(const Product& p, cudaStream_t s) {
+int launch_product(Product& p, const void* x, const void* w, cudaStream_t s) {
   const int sms = sm_count();
   const int64_t extra = p.offsets == nullptr ? 0 : p.E;   // experts' last tiles, at most
+  const int mean = p.M / p.E;
   const int64_t wide = (ceil_div(p.M, 128) + extra) * ceil_div(p.R, 256);
-  if (p.M / p.E >= 256 && wide >= sms)
-    return launch_after(fp8_product_wide_kernel<kT>, static_cast<unsigned>(std::min<int64_t>(wide, sms)), kWideThreads,
-                        kWideSmemBytes, p, s);
-  const int64_t tiles = (ceil_div(p.M, kTileM) + extra) * ceil_div(p.R, kTileR);
-  return launch_after(fp8_product_kernel<kT>, static_cast<unsigned>(std::min<int64_t>(tiles, sms)), kThreads, kSmemBytes,
-                      p, s);
+  if (mean >= 256 && wide >= sms) {
+    if (!make_maps(p, kT, x, w, 128, 128)) return ST_CUDA;
+    if (p.vec && !make_tmap(&p.tmOut, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.out,
+                            p.R, p.M, static_cast<uint64_t>(p.R) * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+      return ST_CUDA;
+    return cuda_status(launch_after(fp8_product_wide_kernel<kT>, std::min<int64_t>(wide, sms), kWideThreads,
+                                    kWideSmemBytes, 1, p, s));
+  }
+  // experts' shares differ: tiles of up to twice the mean
+  const int most = p.offsets == nullptr ? p.M : 2 * mean;
+  p.tile_m = most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : 128;
+  const int64_t num_m = ceil_div(p.M, p.tile_m) + extra;
+  if (p.tile_m == 128 && num_m * ceil_div(p.R, 128) >= 2 * sms)
+    return launch_small<kT, 128>(p, x, w, num_m * ceil_div(p.R, 128), s);
+  return launch_small<kT, 64>(p, x, w, num_m * ceil_div(p.R, 64), s);
 }
 
 constexpr size_t kAlign = 256;
@@ -890,15 +1030,6 @@ int product(bool transposed, const void* x, int xt, int64_t M, const uint8_t* co
   }
   Product p;
   std::memset(&p, 0, sizeof(p));
-  if (!make_tmap(&p.tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, code_ld(C), M, code_ld(C), kBlk, kTileM,
-                 CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_3d(&p.tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, code_ld(K), N, E, 1, kBlk, kTileR,
-                    CU_TENSOR_MAP_SWIZZLE_128B))
-    return ST_CUDA;
-  p.vec = R % 8 == 0;
-  if (p.vec && !make_tmap(&p.tmOut, xt == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, out,
-                          R, M, R * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
-    return ST_CUDA;
   p.xs = qs;
   p.ws = scales;
   p.offsets = offsets;
@@ -913,9 +1044,10 @@ int product(bool transposed, const void* x, int xt, int64_t M, const uint8_t* co
   p.nb = static_cast<int>(ceil_div(N, kBlk));
   p.kb = static_cast<int>(ceil_div(K, kBlk));
   p.bf16 = xt == DT_BF16;
+  p.vec = R % 8 == 0;
   p.zero_rest = zero_rest != 0;
   if (cudaError_t e = launch_quantize(x, xt, M, C, q, qs, st, s)) return cuda_status(e);
-  return cuda_status(transposed ? launch_product<true>(p, s) : launch_product<false>(p, s));
+  return transposed ? launch_product<true>(p, q, codes, s) : launch_product<false>(p, q, codes, s);
 }
 
 bool sizes_ok(int64_t E, int64_t N, int64_t K) {
