@@ -150,7 +150,7 @@ struct Product {
   DevStatus* st;
   int M, R, C, E;
   int nb, kb;                // blocks of the weight along N and K
-  int tile_m, stages, split; // small kernel: tokens of a tile, stages, CTAs that share a tile's reduction
+  int stages, split;         // few tokens, small products: stages, CTAs that share a tile's reduction
   int bias_dt;
   bool bf16;                 // type of out: bf16, else fp16
   bool vec;                  // rows of out start on 16 bytes
@@ -306,10 +306,264 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
   return v;
 }
 
-// ---- few tokens, small products -------------------------------------------
+constexpr int kEpiWarps = 4;         // warps 2 to 5: lanes 32 (w % 4) of the accumulators
+
+// ---- few tokens -----------------------------------------------------------
+
+// Tiles of 128 outputs x kN tokens, kN = 16, 32 or 64: the weight is the first
+// operand, an accumulator has kN columns, and the 256 columns of TMEM that a
+// CTA takes hold two groups of 128 / kN blocks of the reduction: one hand-over
+// between the thread that multiplies and the warps that add for so many blocks
+// (one a block costs 400 ns a block, three times what its 16 KB of weight take
+// to arrive).  A thread has one output of every token; the scales of a group's
+// blocks and tokens lie across the warp's registers, four a lane, fetched a
+// group ahead.  Bound by HBM: each weight is read once.
+// The weight does not depend on the kernel before, so its first stages are on
+// their way while the tokens are being quantized.  With few tiles a cluster of
+// `split` CTAs shares a tile: each has a part of the reduction, and the parts
+// are added in the order of the ranks.
+constexpr int kFewThreads = 192;
+template <int kN>
+constexpr int few_stages() { return kN == 64 ? 4 : 5; }   // two CTAs an SM
+template <int kN>
+struct FewShared {
+  uint64_t full[few_stages<kN>()], empty[few_stages<kN>()];
+  uint64_t acc_full[2], acc_empty[2];   // of a group
+  uint64_t last;                        // all products have completed
+  uint32_t tmem;
+  int abort;
+};
+template <int kN>
+constexpr int few_smem() {
+  return 1024 + few_stages<kN>() * (kTileBytes + kN * 128) + static_cast<int>(sizeof(FewShared<kN>));
+}
+
+template <bool kT, int kN>
+__global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const __grid_constant__ Product p) {
+  constexpr int kGroup = 128 / kN;             // blocks
+  constexpr int kStageBytes = kTileBytes + kN * 128, kFewStages = few_stages<kN>();
+  static_assert(kFewStages * kStageBytes >= kN * 128 * 4, "the sums of a tile fit the stages");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Groups groups;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  FewShared<kN>& y = *reinterpret_cast<FewShared<kN>*>(smem + kFewStages * kStageBytes);
+  volatile int* abort = &y.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = static_cast<int>(blockIdx.x) / p.split, step = static_cast<int>(gridDim.x) / p.split;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kFewStages; ++i) {
+      mbar_init(&y.full[i], 1);
+      mbar_init(&y.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&y.acc_full[i], 1);
+      mbar_init(&y.acc_empty[i], kEpiWarps);
+    }
+    mbar_init(&y.last, 1);
+    y.abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tmX);
+    tma_prefetch_desc(&p.tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc(&y.tmem, 256);
+    tmem_relinquish();
+  }
+  if (warp == 2 && p.offsets != nullptr) plan_groups(p, groups, kN, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = y.tmem;
+  const int num_m = p.offsets == nullptr ? (p.M + kN - 1) / kN : groups.tile[p.E];
+  const int num_r = (p.R + 127) / 128;
+  const int tiles = num_m * num_r, all = (p.C + kBlk - 1) / kBlk;
+  const int b0 = all * rank / p.split, count = all * (rank + 1) / p.split - b0;   // this CTA's blocks of a reduction
+
+  if (warp == 0) {
+    if (lane == 0) {
+      auto fetch_w = [&](int s, const Tile& x, int b) {
+        uint8_t* wd = smem + s * kStageBytes;
+        mbar_arrive_expect_tx(&y.full[s], kStageBytes);
+        if (kT) tma_load_3d(wd, &p.tmW, x.r0, b * kBlk, x.e, &y.full[s]);
+        else tma_load_3d(wd, &p.tmW, b * kBlk, x.r0, x.e, &y.full[s]);
+      };
+      int it = 0, ahead = 0;
+      bool ok = true;
+      if (first < tiles) {
+        const Tile x = tile_at<128>(p, groups, first, num_m, num_r, kN);
+        ahead = min(kFewStages, count);
+        for (int s = 0; s < ahead; ++s) fetch_w(s, x, b0 + s);
+      }
+      grid_dependency_wait();
+      asm volatile("fence.proxy.async;" ::: "memory");
+      for (int t = first; t < tiles && ok; t += step) {
+        const Tile x = tile_at<128>(p, groups, t, num_m, num_r, kN);
+        for (int b = 0; b < count; ++b, ++it) {
+          const int s = it % kFewStages;
+          if (!mbar_wait(&y.empty[s], ((it / kFewStages) & 1) ^ 1, abort, p.st, kWhereFetch)) {
+            ok = false;   // not before the fetches ahead have their tokens: those stages are empty
+            break;
+          }
+          if (it >= ahead) fetch_w(s, x, b0 + b);
+          tma_load_2d(smem + s * kStageBytes + kTileBytes, &p.tmX, (b0 + b) * kBlk, x.m0, &y.full[s]);
+        }
+      }
+      // what is under way lands before the block may end
+      for (int j = max(0, it - kFewStages); j < it; ++j)
+        mbar_wait_out(&y.full[j % kFewStages], (j / kFewStages) & 1, p.st, kWhereFetch);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = make_idesc_f16(128, kN, kT, false);   // E4M3 has the format number of fp16
+      const uint32_t base = smem_u32(smem);
+      int it = 0, grp = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        for (int b = 0; b < count && ok; b += kGroup, ++grp) {
+          const int a = grp & 1;
+          if (!mbar_wait(&y.acc_empty[a], ((grp >> 1) & 1) ^ 1, abort, p.st, kWhereProduct)) {
+            ok = false;
+            break;
+          }
+          for (int g = 0; g < min(kGroup, count - b); ++g, ++it) {
+            const int s = it % kFewStages;
+            if (!mbar_wait(&y.full[s], (it / kFewStages) & 1, abort, p.st, kWhereProduct)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t wa = base + s * kStageBytes, xa = wa + kTileBytes;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_fp8(tmem + a * 128 + g * kN,
+                       kT ? make_sdesc(wa + 4096 * k, kTileBytes, 1024, kSwizzle128B)
+                          : make_sdesc(wa + 32 * k, 16, 1024, kSwizzle128B),
+                       make_sdesc(xa + 32 * k, 16, 1024, kSwizzle128B), idesc, k > 0 ? 1u : 0u);
+            umma_commit(&y.empty[s]);
+          }
+          if (ok) umma_commit(&y.acc_full[a]);
+        }
+      }
+      umma_commit(&y.last);
+      mbar_wait_out(&y.last, 0, p.st, kWhereProduct);
+    }
+  } else {
+    const int quad = warp & 3;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    grid_dependency_wait();
+    if (p.offsets != nullptr && p.zero_rest)
+      zero_rest(p, groups, blockIdx.x * kEpiWarps + quad, gridDim.x * kEpiWarps, lane);
+    int grp = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      const Tile x = tile_at<128>(p, groups, t, num_m, num_r, kN);
+      const int r = x.r0 + quad * 32 + lane;
+      const float* ws = p.ws + static_cast<int64_t>(x.e) * p.nb * p.kb + (kT ? x.r0 / kBlk : x.r0 / kBlk * p.kb);
+      const int wstep = kT ? p.kb : 1;
+      const float bias = bias_at(p, r);
+      float acc[kN];
+#pragma unroll
+      for (int i = 0; i < kN; ++i) acc[i] = 0.f;
+      // the scales of a group: block g, token j at place g kN + j of 128, four a lane
+      float xv[4], wv[4];
+      auto fetch = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = i * 32 + lane, blk = min(b0 + b + at / kN, b0 + count - 1);
+          xv[i] = p.xs[static_cast<int64_t>(blk) * p.M + min(x.m0 + at % kN, p.M - 1)];
+          wv[i] = ws[static_cast<int64_t>(blk) * wstep];
+        }
+      };
+      if (count > 0) fetch(0);
+      for (int b = 0; b < count; b += kGroup, ++grp) {
+        const int a = grp & 1;
+        float s[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = xv[i] * wv[i];
+        if (b + kGroup < count) fetch(b + kGroup);
+        if (!__all_sync(0xffffffffu, mbar_wait(&y.acc_full[a], (grp >> 1) & 1, abort, p.st, kWhereOut))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t d[2][32];
+        tmem_ld32_nowait(lanes + a * 128, d[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {   // 32 columns: 32 / kN blocks, or a part of one
+          tmem_ld_wait(d[c & 1]);
+          if (c < 3) {
+            tmem_ld32_nowait(lanes + a * 128 + 32 * (c + 1), d[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&y.acc_empty[a]);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float scale = __shfl_sync(0xffffffffu, s[c], i);
+            // columns of blocks past the last hold an older group's products
+            if (b + (32 * c + i) / kN < count)
+              acc[(32 * c + i) % kN] = fmaf(__uint_as_float(d[c & 1][i]), scale, acc[(32 * c + i) % kN]);
+          }
+        }
+      }
+      if (!ok) break;
+      if (p.split > 1) {
+        // all of this CTA's products have completed: its stages hold the sums now, [token][output]
+        float* dst = reinterpret_cast<float*>(smem) + quad * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) dst[i * 128] = acc[i];
+      } else if (r < p.R) {
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(x.m0) * p.R + r;
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (x.m0 + i < x.end) dst[static_cast<int64_t>(i) * p.R] = static_cast<uint16_t>(pack16(p.bf16, acc[i] + bias, 0.f));
+      }
+    }
+  }
+  if (p.split > 1) {
+    // one tile a cluster; every rank adds up its share of the tokens, a warp
+    // four outputs a lane
+    cluster_sync();
+    if (warp >= 2 && first < tiles && *abort == 0) {
+      const Tile x = tile_at<128>(p, groups, first, num_m, num_r, kN);
+      const int r = x.r0 + 4 * lane;
+      for (int i = rank * kEpiWarps + warp - 2; i < min(kN, x.end - x.m0); i += p.split * kEpiWarps) {
+        if (r >= p.R) continue;
+        const float* src = reinterpret_cast<const float*>(smem) + i * 128 + 4 * lane;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < p.split; ++k) {
+          const float4 part = ld_cluster4(mapa_shared(src, static_cast<uint32_t>(k)));
+          v.x += part.x;
+          v.y += part.y;
+          v.z += part.z;
+          v.w += part.w;
+        }
+        const uint32_t q[2] = {pack16(p.bf16, v.x + bias_at(p, r), v.y + bias_at(p, r + 1)),
+                               pack16(p.bf16, v.z + bias_at(p, r + 2), v.w + bias_at(p, r + 3))};
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(x.m0 + i) * p.R + r;
+        if (p.vec) {
+          *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (r + k < p.R) dst[k] = static_cast<uint16_t>(q[k >> 1] >> (16 * (k & 1)));
+        }
+      }
+    }
+    cluster_sync();   // no CTA leaves while another reads its sums
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 256);
+}
+
+// ---- small products -------------------------------------------------------
 
 constexpr int kThreads = 192;
-constexpr int kEpiWarps = 4;         // warps 2 to 5: lanes 32 (w % 4) of the accumulators
 constexpr int kMaxStages = 8;
 template <int kTileR>
 struct Shared {
@@ -320,15 +574,12 @@ struct Shared {
   int abort;
   float bias[kEpiWarps][kTileR];
 };
-// Shared memory of a CTA: the stages, what a product reads past the tokens of
-// the last one (it takes 128 rows, fetched or not: those of no token give
-// accumulator lanes that nobody reads), barriers.
 template <int kTileR>
-constexpr int small_smem(int tile_m, int stages) {
-  return 1024 + stages * (tile_m + kTileR) * 128 + (128 - tile_m) * 128 + static_cast<int>(sizeof(Shared<kTileR>));
+constexpr int small_smem(int stages) {
+  return 1024 + stages * (128 + kTileR) * 128 + static_cast<int>(sizeof(Shared<kTileR>));
 }
 
-// Tiles of 16 to 128 tokens x kTileR outputs.  Warp 0 fetches, warp 1
+// Tiles of 128 tokens x kTileR outputs.  Warp 0 fetches, warp 1
 // multiplies: one accumulator in TMEM per 128 columns of the reduction, two of
 // them in turn.  Warps 2 to 5 add each, times its two scales, to the sums that
 // they hold in registers: a thread has one token and kTileR outputs, so the
@@ -342,8 +593,9 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
   extern __shared__ uint8_t smem_raw[];
   __shared__ Groups groups;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int tile_m = p.tile_m, x_bytes = tile_m * 128, stage_bytes = x_bytes + kTileR * 128, stages = p.stages;
-  Shared<kTileR>& y = *reinterpret_cast<Shared<kTileR>*>(smem + stages * stage_bytes + (128 - tile_m) * 128);
+  constexpr int kTileM = 128, x_bytes = kTileBytes, stage_bytes = x_bytes + kTileR * 128;
+  const int stages = p.stages;
+  Shared<kTileR>& y = *reinterpret_cast<Shared<kTileR>*>(smem + stages * stage_bytes);
   volatile int* abort = &y.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -368,12 +620,12 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
     tmem_alloc(&y.tmem, 2 * kTileR);
     tmem_relinquish();
   }
-  if (warp == 2 && p.offsets != nullptr) plan_groups(p, groups, tile_m, lane);
+  if (warp == 2 && p.offsets != nullptr) plan_groups(p, groups, kTileM, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = y.tmem;
-  const int num_m = p.offsets == nullptr ? (p.M + tile_m - 1) / tile_m : groups.tile[p.E];
+  const int num_m = p.offsets == nullptr ? (p.M + kTileM - 1) / kTileM : groups.tile[p.E];
   const int num_r = (p.R + kTileR - 1) / kTileR;
   const int tiles = num_m * num_r, all = (p.C + kBlk - 1) / kBlk;
   const int b0 = all * rank / p.split, b1 = all * (rank + 1) / p.split;   // this CTA's blocks of a tile's reduction
@@ -389,14 +641,14 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
       int it = 0, ahead = 0;
       bool ok = true;
       if (first < tiles) {
-        const Tile x = tile_at<kTileR>(p, groups, first, num_m, num_r, tile_m);
+        const Tile x = tile_at<kTileR>(p, groups, first, num_m, num_r, kTileM);
         ahead = min(stages, b1 - b0);
         for (int s = 0; s < ahead; ++s) fetch_w(s, x, b0 + s);
       }
       grid_dependency_wait();
       asm volatile("fence.proxy.async;" ::: "memory");
       for (int t = first; t < tiles && ok; t += step) {
-        const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, tile_m);
+        const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, kTileM);
         for (int b = b0; b < b1; ++b, ++it) {
           const int s = it % stages;
           if (!mbar_wait(&y.empty[s], ((it / stages) & 1) ^ 1, abort, p.st, kWhereFetch)) {
@@ -451,8 +703,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
     int it = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, tile_m);
-      const int last = min(x.end, x.m0 + tile_m), row0 = x.m0 + quad * 32, m = row0 + lane;
+      const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, kTileM);
+      const int last = min(x.end, x.m0 + kTileM), row0 = x.m0 + quad * 32, m = row0 + lane;
       const bool any = row0 < last;   // a warp without tokens hands the accumulators on
       const float* xs = p.xs + static_cast<int64_t>(b0) * p.M + min(m, p.M - 1);
       const float* ws = p.ws + static_cast<int64_t>(x.e) * p.nb * p.kb + (kT ? x.r0 / kBlk : x.r0 / kBlk * p.kb) +
@@ -507,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
         // all of this CTA's products have completed: its stages hold the sums
         // now, one row of the tile after another, 16-byte chunks permuted
         const int row = quad * 32 + lane;
-        if (row < tile_m) {
+        if (row < kTileM) {
           float4* dst = reinterpret_cast<float4*>(smem) + row * (kTileR / 4);
 #pragma unroll
           for (int i = 0; i < kTileR / 4; ++i) {
@@ -552,8 +804,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
     // at a time
     cluster_sync();
     if (warp >= 2 && first < tiles && *abort == 0) {
-      const Tile x = tile_at<kTileR>(p, groups, first, num_m, num_r, tile_m);
-      const int rows = min(tile_m, x.end - x.m0), count = rows * (kTileR / 4);
+      const Tile x = tile_at<kTileR>(p, groups, first, num_m, num_r, kTileM);
+      const int rows = min(kTileM, x.end - x.m0), count = rows * (kTileR / 4);
       for (int g = rank * (kEpiWarps * 32) + static_cast<int>(threadIdx.x) - 64; g < count; g += p.split * kEpiWarps * 32) {
         const int row = g / (kTileR / 4), i = g % (kTileR / 4), r = x.r0 + 4 * i;
         if (r >= p.R) continue;
@@ -953,18 +1205,34 @@ bool make_maps(Product& p, bool kt, const void* x, const void* w, int rows, int 
                       kt && outputs == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// CTAs that share a tile: enough that all of them together have HBM's latency
+// covered (each has up to 90 KB under way).
+int split_of(int64_t tiles, int blocks, int64_t want) {
+  int split = 1;
+  while (split < 8 && split * tiles < want && 4 * split <= blocks) split *= 2;
+  return split;
+}
+
+template <bool kT, int kN>
+int launch_few(Product& p, const void* x, const void* w, int64_t extra, cudaStream_t s) {
+  const int sms = sm_count();
+  const int64_t tiles = (ceil_div(p.M, kN) + extra) * ceil_div(p.R, 128);
+  p.split = split_of(tiles, static_cast<int>(ceil_div(p.C, kBlk)), sms - sms / 8);
+  if (!make_maps(p, kT, x, w, kN, 128)) return ST_CUDA;
+  const int64_t grid = p.split > 1 ? tiles * p.split : std::min<int64_t>(tiles, 2 * sms);
+  return cuda_status(launch_after(fp8_product_few_kernel<kT, kN>, grid, kFewThreads, few_smem<kN>(), p.split, p, s));
+}
+
 template <bool kT, int kTileR>
 int launch_small(Product& p, const void* x, const void* w, int64_t tiles, cudaStream_t s) {
   constexpr int kBudget = 107000;   // two CTAs an SM
-  const int sms = sm_count(), blocks = static_cast<int>(ceil_div(p.C, kBlk));
+  const int sms = sm_count();
   p.stages = kMaxStages;
-  while (p.stages > 2 && small_smem<kTileR>(p.tile_m, p.stages) > kBudget) --p.stages;
-  p.split = 1;
-  while (p.split < 8 && 2 * p.split * tiles <= 2 * sms && 2 * p.split <= blocks / 2) p.split *= 2;
-  if (!make_maps(p, kT, x, w, p.tile_m, kTileR)) return ST_CUDA;
+  while (p.stages > 2 && small_smem<kTileR>(p.stages) > kBudget) --p.stages;
+  p.split = split_of(tiles, static_cast<int>(ceil_div(p.C, kBlk)), sms);
+  if (!make_maps(p, kT, x, w, 128, kTileR)) return ST_CUDA;
   const int64_t grid = p.split > 1 ? tiles * p.split : std::min<int64_t>(tiles, 2 * sms);
-  return cuda_status(launch_after(fp8_product_kernel<kT, kTileR>, grid, kThreads, small_smem<kTileR>(p.tile_m, p.stages),
-                                  p.split, p, s));
+  return cuda_status(launch_after(fp8_product_kernel<kT, kTileR>, grid, kThreads, small_smem<kTileR>(p.stages), p.split, p, s));
 }
 
 template <bool kT>
@@ -983,10 +1251,11 @@ int launch_product(Product& p, const void* x, const void* w, cudaStream_t s) {
   }
   // experts' shares differ: tiles of up to twice the mean
   const int most = p.offsets == nullptr ? p.M : 2 * mean;
-  p.tile_m = most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : 128;
-  const int64_t num_m = ceil_div(p.M, p.tile_m) + extra;
-  if (p.tile_m == 128 && num_m * ceil_div(p.R, 128) >= 2 * sms)
-    return launch_small<kT, 128>(p, x, w, num_m * ceil_div(p.R, 128), s);
+  if (most <= 16) return launch_few<kT, 16>(p, x, w, extra, s);
+  if (most <= 32) return launch_few<kT, 32>(p, x, w, extra, s);
+  if (most <= 64) return launch_few<kT, 64>(p, x, w, extra, s);
+  const int64_t num_m = ceil_div(p.M, 128) + extra;
+  if (num_m * ceil_div(p.R, 128) >= 2 * sms) return launch_small<kT, 128>(p, x, w, num_m * ceil_div(p.R, 128), s);
   return launch_small<kT, 64>(p, x, w, num_m * ceil_div(p.R, 64), s);
 }
 
