@@ -691,7 +691,7 @@ int i8lt_scale_grads(void* const* grads, const int32_t* dtypes,
  *        i8lt_fp8_grad_bias_bytes(M, N) more
  * out may not overlap an input.
  */
-#define I8LT_FP8_MAX_EXPERTS 1024
+#define I8LT_FP8_MAX_EXPERTS 512
 int64_t i8lt_fp8_ld(int64_t C);
 int64_t i8lt_fp8_blocks(int64_t C);
 int i8lt_fp8_quantize(const void* x, int xt, int64_t M, int64_t C,

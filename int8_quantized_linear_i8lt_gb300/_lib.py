@@ -34,7 +34,7 @@ I8LT_F16, I8LT_BF16, I8LT_F32 = 0, 1, 2
 I8LT_MAX_K = 133144
 I8LT_MAX_RANK = 128
 I8LT_ADAMW_BLOCK = 256
-I8LT_FP8_MAX_EXPERTS = 1024
+I8LT_FP8_MAX_EXPERTS = 512
 
 
 class i8lt_fwd_layout(Structure):
@@ -451,6 +451,7 @@ def i8lt_adamw_step_8bit_counted(params, pt, grads, gt, sizes, count, m, m_absma
                                                lr, beta1, beta2, eps, weight_decay, grad_scale, found_inf, stream)
 
 
+@functools.lru_cache(maxsize=1)
 def i8lt_grad_norm_workspace_size() -> int:
     return load().i8lt_grad_norm_workspace_size()
 

@@ -15,9 +15,10 @@ namespace i8lt {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPerThread = 32;                     // elements of a unit that a thread has
-constexpr int kUnit = kThreads * kPerThread;
-constexpr int kMaxBlocks = 2048;                   // partial sums of a call
+constexpr int kPacks = 8;                          // 16-byte accesses of a thread and unit
+constexpr int kUnitBytes = kThreads * kPacks * 16;
+constexpr int kBlocks = 152 * 4;                   // at most, and so the partial sums of a call
+constexpr int kCluster = 8, kSmallGroups = 4, kClusterUnits = 64;    // gradients of 2 MB in all: one cluster, one launch
 constexpr double kClipEps = 1e-6;
 
 // A list of tensors travels in the kernel's parameters.  A tensor's first
@@ -63,7 +64,7 @@ __device__ __forceinline__ void each_unit(const GradList<kCap>& L, int u, int en
     auto run = [&](auto* base) {
       const int64_t head = head_of(reinterpret_cast<uintptr_t>(base), sizeof(*base), L.n[t]);
       for (; u < stop; ++u) {
-        const int64_t at = head + static_cast<int64_t>(u - L.first[t]) * kUnit;
+        const int64_t at = head + static_cast<int64_t>(u - L.first[t]) * (kUnitBytes / static_cast<int>(sizeof(*base)));
         f(base + at, L.n[t] - at, u == L.first[t] ? head : 0);
       }
     };
@@ -79,76 +80,104 @@ struct alignas(16) Pack {
 };
 template <typename T>
 constexpr int kPack = 16 / sizeof(T);
-template <typename T>
-constexpr int kPacks = kPerThread / kPack<T>;     // 16-byte accesses of a thread and unit
-
 __device__ __forceinline__ double squares(float x) { return static_cast<double>(x) * static_cast<double>(x); }
 
-// One block's part of the sum of squares.  A thread sums the squares of its 32
-// elements of a unit in fp32 and those sums in fp64 (one fp64 addition per 32
-// elements: the machine has few fp64 units).  A sum so large or small that
-// squares may have left fp32's range is taken again in fp64.
-template <int kCap>
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ GradList<kCap> L, double* partial,
-                                                             bool first) {
-  grid_dependents_launch();
-  __shared__ double sums[kThreads / 32];
-  const int64_t units = L.first[L.count];
-  const int u0 = static_cast<int>(units * blockIdx.x / gridDim.x), u1 = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
+// One block's part of the sum of squares: the units [from, to).
+// A thread sums the squares of 32 or 64 elements of a unit in fp32 and those
+// sums in fp64 (one fp64 addition for so many elements: the machine has few
+// fp64 units).  A sum so large or small that squares may have left fp32's
+// range is taken again in fp64.  Bound by HBM: 8 loads of 16 bytes a thread
+// under way.
+template <int kGroups, int kCap>
+__device__ __forceinline__ double block_sum(const GradList<kCap>& L, int from, int to) {
+  __shared__ double sums[kGroups * kThreads / 32];
   double sum = 0.0;
+  // groups of kThreads threads take a part of the units each
+  const int group = threadIdx.x / kThreads, thread = threadIdx.x % kThreads;
+  const int u0 = from + (to - from) * group / kGroups, u1 = from + (to - from) * (group + 1) / kGroups;
   if (u0 < u1)
     each_unit(L, u0, u1, [&](auto* p, int64_t left, int64_t head) {
       using T = std::remove_pointer_t<decltype(p)>;
       constexpr int V = kPack<T>;
-      if (threadIdx.x < head) sum += squares(to_float(p[-1 - static_cast<int>(threadIdx.x)]));
-      Pack<T> x[kPacks<T>];
-#pragma unroll
-      for (int j = 0; j < kPacks<T>; ++j) {
-        const int e = (j * kThreads + static_cast<int>(threadIdx.x)) * V;
-        if (e + V <= left) {
-          x[j] = *reinterpret_cast<const Pack<T>*>(p + e);
-        } else {
-#pragma unroll
-          for (int i = 0; i < V; ++i) x[j].v[i] = e + i < left ? p[e + i] : from_float<T>(0.f);
-        }
-      }
+      if (thread < head) sum += squares(to_float(p[-1 - thread]));
       float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < kPacks<T>; ++j)
+      auto add = [&](const Pack<T>& x) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float f = to_float(x[j].v[i]);
+          const float f = to_float(x.v[i]);
           s[i & 3] = fmaf(f, f, s[i & 3]);
         }
+      };
+      const T* q = p + thread * V;
+      if (left >= kUnitBytes / static_cast<int>(sizeof(T))) {
+        Pack<T> x[kPacks];
+#pragma unroll
+        for (int j = 0; j < kPacks; ++j) x[j] = *reinterpret_cast<const Pack<T>*>(q + j * kThreads * V);
+#pragma unroll
+        for (int j = 0; j < kPacks; ++j) add(x[j]);
+      } else {
+#pragma unroll 1
+        for (int e = thread * V; e < left; e += kThreads * V) {
+          if (e + V <= left) {
+            add(*reinterpret_cast<const Pack<T>*>(p + e));
+          } else {
+            for (int i = e; i < left; ++i) {
+              const float f = to_float(p[i]);
+              s[0] = fmaf(f, f, s[0]);
+            }
+          }
+        }
+      }
       const float all = (s[0] + s[1]) + (s[2] + s[3]);
       if (all >= 0x1p-80f && all <= 0x1p100f) {
         sum += all;
       } else {
-        double d = 0.0;
-#pragma unroll
-        for (int j = 0; j < kPacks<T>; ++j)
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float f = to_float(x[j].v[i]);
-            if (f != 0.f) d += squares(f);
-          }
-        sum += d;
+#pragma unroll 1
+        for (int j = 0; j < kPacks * V; ++j) {
+          const int e = (j / V * kThreads + thread) * V + j % V;
+          const float f = e < left ? to_float(p[e]) : 0.f;
+          if (f != 0.f) sum += squares(f);
+        }
       }
     });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double s = 0.0;
-    for (int i = 0; i < kThreads / 32; ++i) s += sums[i];
-    partial[blockIdx.x] = first ? s : partial[blockIdx.x] + s;
-  }
+  double s = 0.0;
+  for (int i = 0; i < kGroups * kThreads / 32; ++i) s += sums[i];
+  return s;
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double* partial, int n, const float* grad_scale,
-                                                                    const float* found_inf, double max_norm,
-                                                                    float* result) {
+struct Clip {
+  const float *grad_scale, *found_inf;
+  double max_norm;
+  float* result;
+};
+
+__device__ __forceinline__ void write_result(const Clip& c, double s) {
+  const double f = c.grad_scale != nullptr ? *c.grad_scale : 1.0;
+  const double norm = fabs(f) * sqrt(s), q = c.max_norm / (norm + kClipEps);
+  const float rounded = static_cast<float>(norm);
+  c.result[0] = rounded;
+  c.result[1] = static_cast<float>(q >= 1.0 || c.max_norm == INFINITY ? f : f * q);   // a NaN stays one
+  c.result[2] = isfinite(rounded) && (c.found_inf == nullptr || *c.found_inf == 0.f) ? 0.f : 1.f;
+}
+
+template <int kCap>
+__device__ __forceinline__ int unit_at(const GradList<kCap>& L, unsigned block) {
+  return static_cast<int>(static_cast<int64_t>(L.first[L.count]) * block / gridDim.x);
+}
+
+template <int kCap>
+__global__ void __launch_bounds__(kThreads, 4) grad_norm_kernel(const __grid_constant__ GradList<kCap> L,
+                                                                double* partial, bool first) {
+  grid_dependents_launch();
+  const double s = block_sum<1>(L, unit_at(L, blockIdx.x), unit_at(L, blockIdx.x + 1));
+  if (threadIdx.x == 0) partial[blockIdx.x] = first ? s : partial[blockIdx.x] + s;
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double* partial, int n, const Clip c) {
   grid_dependency_wait();
   __shared__ double sums[kThreads / 32];
   double sum = 0.0;
@@ -160,23 +189,37 @@ __global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double
   if (threadIdx.x == 0) {
     double s = 0.0;
     for (int i = 0; i < kThreads / 32; ++i) s += sums[i];
-    const double c = grad_scale != nullptr ? *grad_scale : 1.0;
-    const double norm = fabs(c) * sqrt(s), q = max_norm / (norm + kClipEps);
-    const float rounded = static_cast<float>(norm);
-    result[0] = rounded;
-    result[1] = static_cast<float>(q >= 1.0 || max_norm == INFINITY ? c : c * q);   // a NaN stays one
-    result[2] = isfinite(rounded) && (found_inf == nullptr || *found_inf == 0.f) ? 0.f : 1.f;
+    write_result(c, s);
   }
+}
+
+// Few gradients: one cluster, whose first block adds up the others' sums from
+// their shared memory.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallGroups * kThreads)
+    grad_norm_small_kernel(const __grid_constant__ GradList<kFewTensors> L, const Clip c) {
+  __shared__ double part;
+  const double s = block_sum<kSmallGroups>(L, unit_at(L, blockIdx.x), unit_at(L, blockIdx.x + 1));
+  if (threadIdx.x == 0) part = s;
+  cluster_sync();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    double sum = 0.0;
+    for (int k = 0; k < kCluster; ++k) {
+      double v;
+      asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(mapa_shared(&part, static_cast<uint32_t>(k))) : "memory");
+      sum += v;
+    }
+    write_result(c, sum);
+  }
+  cluster_sync();   // no block leaves before its sum has been read
 }
 
 // g *= scale, rounded once; nothing is read or written for a scale of 1.
 template <int kCap>
-__global__ void __launch_bounds__(kThreads) scale_grads_kernel(const __grid_constant__ GradList<kCap> L,
+__global__ void __launch_bounds__(kThreads, 4) scale_grads_kernel(const __grid_constant__ GradList<kCap> L,
                                                                const float* scale) {
   const float c = *scale;
   if (c == 1.f) return;
-  const int64_t units = L.first[L.count];
-  const int u0 = static_cast<int>(units * blockIdx.x / gridDim.x), u1 = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
+  const int u0 = unit_at(L, blockIdx.x), u1 = unit_at(L, blockIdx.x + 1);
   if (u0 >= u1) return;
   each_unit(L, u0, u1, [&](auto* p, int64_t left, int64_t head) {
     using T = std::remove_pointer_t<decltype(p)>;
@@ -185,23 +228,26 @@ __global__ void __launch_bounds__(kThreads) scale_grads_kernel(const __grid_cons
       T* q = p - 1 - static_cast<int>(threadIdx.x);
       *q = from_float<T>(__fmul_rn(to_float(*q), c));
     }
-    Pack<T> x[kPacks<T>];
+    auto scaled = [c](Pack<T> x) {
 #pragma unroll
-    for (int j = 0; j < kPacks<T>; ++j) {
-      const int e = (j * kThreads + static_cast<int>(threadIdx.x)) * V;
-      if (e + V <= left) x[j] = *reinterpret_cast<const Pack<T>*>(p + e);
-    }
+      for (int i = 0; i < V; ++i) x.v[i] = from_float<T>(__fmul_rn(to_float(x.v[i]), c));
+      return x;
+    };
+    T* q = p + static_cast<int>(threadIdx.x) * V;
+    if (left >= kUnitBytes / static_cast<int>(sizeof(T))) {
+      Pack<T> x[kPacks];
 #pragma unroll
-    for (int j = 0; j < kPacks<T>; ++j) {
-      const int e = (j * kThreads + static_cast<int>(threadIdx.x)) * V;
-      if (e + V <= left) {
+      for (int j = 0; j < kPacks; ++j) x[j] = *reinterpret_cast<const Pack<T>*>(q + j * kThreads * V);
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[j].v[i] = from_float<T>(__fmul_rn(to_float(x[j].v[i]), c));
-        *reinterpret_cast<Pack<T>*>(p + e) = x[j];
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (e + i < left) p[e + i] = from_float<T>(__fmul_rn(to_float(p[e + i]), c));
+      for (int j = 0; j < kPacks; ++j) *reinterpret_cast<Pack<T>*>(q + j * kThreads * V) = scaled(x[j]);
+    } else {
+#pragma unroll 1
+      for (int e = static_cast<int>(threadIdx.x) * V; e < left; e += kThreads * V) {
+        if (e + V <= left) {
+          *reinterpret_cast<Pack<T>*>(p + e) = scaled(*reinterpret_cast<const Pack<T>*>(p + e));
+        } else {
+          for (int i = e; i < left; ++i) p[i] = from_float<T>(__fmul_rn(to_float(p[i]), c));
+        }
       }
     }
   });
@@ -215,8 +261,9 @@ cudaError_t each_list(void* const* grads, const int32_t* dtypes, const int64_t* 
   L.first[0] = 0;
   for (int64_t i = 0; i < count; ++i) {
     if (sizes[i] == 0 || grads[i] == nullptr) continue;
-    const int64_t body = sizes[i] - head_of(reinterpret_cast<uintptr_t>(grads[i]), elem_bytes(dtypes[i]), sizes[i]);
-    const int64_t units = std::max<int64_t>(1, ceil_div(body, kUnit));
+    const int elem = elem_bytes(dtypes[i]);
+    const int64_t body = sizes[i] - head_of(reinterpret_cast<uintptr_t>(grads[i]), elem, sizes[i]);
+    const int64_t units = std::max<int64_t>(1, ceil_div(body * elem, kUnitBytes));
     if (L.count == kCap || L.first[L.count] + units > (int64_t(1) << 30)) {
       if (cudaError_t e = launch(L)) return e;
       L.count = 0;
@@ -230,10 +277,9 @@ cudaError_t each_list(void* const* grads, const int32_t* dtypes, const int64_t* 
   return L.count > 0 ? launch(L) : cudaSuccess;
 }
 
-constexpr int kBlocksPerSm = 4;
 template <int kCap>
 unsigned blocks_of(const GradList<kCap>& L) {
-  return static_cast<unsigned>(std::min(L.first[L.count], std::min(kMaxBlocks, 152 * kBlocksPerSm)));
+  return static_cast<unsigned>(std::min(L.first[L.count], kBlocks));
 }
 
 int check_list(void* const* grads, const int32_t* dtypes, const int64_t* sizes, int64_t count) {
@@ -248,19 +294,27 @@ int check_list(void* const* grads, const int32_t* dtypes, const int64_t* sizes, 
 }
 
 template <int kCap>
-cudaError_t norm_lists(void* const* grads, const int32_t* dtypes, const int64_t* sizes, int64_t count,
-                       const float* grad_scale, const float* found_inf, double max_norm, float* result, double* partial,
-                       cudaStream_t s) {
+cudaError_t norm_lists(void* const* grads, const int32_t* dtypes, const int64_t* sizes, int64_t count, const Clip& c,
+                       double* partial, cudaStream_t s) {
   unsigned used = 0;
+  bool done = false;
   cudaError_t e = each_list<kCap>(grads, dtypes, sizes, count, [&](const GradList<kCap>& L) {
+    if constexpr (kCap == kFewTensors) {
+      if (L.first[L.count] <= kClusterUnits) {   // so it is the only list
+        done = true;
+        ProfScope ps(K_GRAD_NORM, s);
+        grad_norm_small_kernel<<<kCluster, kSmallGroups * kThreads, 0, s>>>(L, c);
+        return cudaGetLastError();
+      }
+    }
     // every list but the first adds to the sums of the same number of blocks
     const bool first = used == 0;
-    if (first) used = count > kCap ? static_cast<unsigned>(152 * kBlocksPerSm) : blocks_of(L);
+    if (first) used = count > kCap ? static_cast<unsigned>(kBlocks) : blocks_of(L);
     ProfScope ps(K_GRAD_NORM, s);
     grad_norm_kernel<kCap><<<used, kThreads, 0, s>>>(L, partial, first);
     return cudaGetLastError();
   });
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || done) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1);
   cfg.blockDim = dim3(kThreads);
@@ -271,8 +325,7 @@ cudaError_t norm_lists(void* const* grads, const int32_t* dtypes, const int64_t*
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   ProfScope ps(K_GRAD_NORM, s);
-  return cudaLaunchKernelEx(&cfg, grad_norm_finish_kernel, static_cast<const double*>(partial), static_cast<int>(used),
-                            grad_scale, found_inf, max_norm, result);
+  return cudaLaunchKernelEx(&cfg, grad_norm_finish_kernel, static_cast<const double*>(partial), static_cast<int>(used), c);
 }
 
 template <int kCap>
@@ -292,7 +345,7 @@ extern "C" {
 
 using namespace i8lt;
 
-size_t i8lt_grad_norm_workspace_size(void) { return kMaxBlocks * sizeof(double); }
+size_t i8lt_grad_norm_workspace_size(void) { return kBlocks * sizeof(double); }
 
 int i8lt_grad_norm(const void* const* grads, const int32_t* dtypes, const int64_t* sizes, int64_t count,
                    const float* grad_scale, const float* found_inf, double max_norm, float* result, void* ws,
@@ -305,9 +358,9 @@ int i8lt_grad_norm(const void* const* grads, const int32_t* dtypes, const int64_
   if (int d = check_device()) return d;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   double* partial = static_cast<double*>(ws);
-  return cuda_status(count <= kFewTensors
-                         ? norm_lists<kFewTensors>(g, dtypes, sizes, count, grad_scale, found_inf, max_norm, result, partial, s)
-                         : norm_lists<kMaxTensors>(g, dtypes, sizes, count, grad_scale, found_inf, max_norm, result, partial, s));
+  const Clip c{grad_scale, found_inf, max_norm, result};
+  return cuda_status(count <= kFewTensors ? norm_lists<kFewTensors>(g, dtypes, sizes, count, c, partial, s)
+                                          : norm_lists<kMaxTensors>(g, dtypes, sizes, count, c, partial, s));
 }
 
 int i8lt_scale_grads(void* const* grads, const int32_t* dtypes, const int64_t* sizes, int64_t count, const float* scale,

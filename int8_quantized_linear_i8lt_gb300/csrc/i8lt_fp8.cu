@@ -25,7 +25,7 @@ namespace {
 constexpr int kBlk = 128;            // columns (of a weight: and rows) per scale
 constexpr float kE4M3Max = 448.0f;
 constexpr float kTinyMax = 0x1p-100f;   // blocks below it are blocks of zeros: 448 / a could overflow
-constexpr int kMaxExperts = 1024;
+constexpr int kMaxExperts = I8LT_FP8_MAX_EXPERTS;
 
 int64_t code_ld(int64_t C) { return round_up(C, 16); }
 
@@ -44,34 +44,43 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
 }
 
 // Rows.  A thread takes 16 consecutive columns, 8 threads a block of 128, a
-// warp 512 columns of one row; the maximum is taken over the bits of |x|, so
-// that a NaN stands above all.  Bound by HBM: 2 bytes read and 1 written per
-// element.
-template <typename T>
+// warp 512 columns of a row, a thread block a range of rows of them; the
+// maximum is taken over the bits of |x|, so that a NaN stands above all.
+// kSum: also the columns' sums over the block's rows (of the values before
+// they are rounded), partial [row ranges][C], for the bias gradient.
+// Bound by HBM: 2 bytes read and 1 written per element, two rows under way.
+template <typename T, bool kSum>
 __global__ void __launch_bounds__(256) fp8_quantize_kernel(const T* __restrict__ x, int64_t M, int C, int ld, bool vec,
-                                                           uint8_t* __restrict__ codes, float* __restrict__ scales,
+                                                           int rows, uint8_t* __restrict__ codes,
+                                                           float* __restrict__ scales, float* __restrict__ partial,
                                                            DevStatus* st) {
   grid_dependents_launch();
-  if (st != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *st = DevStatus{0, 0, 0, 0};
-  const int lane = threadIdx.x & 31;
-  const int segs = (C + 511) / 512;
-  const int64_t items = M * segs, step = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items; it += step) {
-    const int64_t m = it / segs;
-    const int c = static_cast<int>(it - m * segs) * 512 + lane * 16;
-    float f[16];
-    const T* p = x + m * C + c;
+  if (st != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *st = DevStatus{0, 0, 0, 0};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x * 512 + lane * 16;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * rows, m1 = min(M, m0 + rows);
+  const bool whole = vec && c + 16 <= C;
+  float sum[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sum[i] = 0.f;
+  auto load = [&](int64_t m, float (&f)[16]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float (&g)[8] = *reinterpret_cast<float (*)[8]>(f + 8 * h);
-      load8_float(p + 8 * h, C - c - 8 * h, vec && c + 8 * h + 8 <= C, g);
+      load8_float(x + m * C + c + 8 * h, C - c - 8 * h, whole || (vec && c + 8 * h + 8 <= C), g);
     }
+  };
+  auto quantize = [&](int64_t m, float (&f)[16]) {
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = max(top, abs_bits(f[i]));
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float a = __uint_as_float(top), r = code_scale(a);
+    if constexpr (kSum) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum[i] += f[i];
+    }
     if (c < ld) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) f[i] = __fmul_rn(f[i], r);
@@ -83,8 +92,45 @@ __global__ void __launch_bounds__(256) fp8_quantize_kernel(const T* __restrict__
       *reinterpret_cast<uint4*>(codes + m * ld + c) = q;
       if ((lane & 7) == 0) scales[static_cast<int64_t>(c / kBlk) * M + m] = block_scale(a);
     }
+  };
+  int64_t m = m0 + warp;
+  for (; m + 8 < m1; m += 16) {
+    float f[16], g[16];
+    load(m, f);
+    load(m + 8, g);
+    quantize(m, f);
+    quantize(m + 8, g);
+  }
+  if (m < m1) {
+    float f[16];
+    load(m, f);
+    quantize(m, f);
+  }
+  if constexpr (kSum) {
+    __shared__ float4 sums[8][4][32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[warp][i][lane] = make_float4(sum[4 * i], sum[4 * i + 1], sum[4 * i + 2], sum[4 * i + 3]);
+    __syncthreads();
+    // column k of the 512: part (k / 4) % 4 of lane k / 16
+    for (int k = threadIdx.x; k < 512; k += 256) {
+      const int col = blockIdx.x * 512 + k;
+      if (col >= C) continue;
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) s += reinterpret_cast<const float*>(&sums[w][(k >> 2) & 3][k >> 4])[k & 3];
+      partial[static_cast<int64_t>(blockIdx.y) * C + col] = s;
+    }
   }
 }
+
+// Row ranges of the kernel above: about eight thread blocks an SM, of 16 rows
+// at least.
+constexpr int64_t kQuantizeBlocks = 152 * 8;
+int64_t quantize_rows(int64_t M, int64_t C) {
+  const int64_t ranges = std::max<int64_t>(1, kQuantizeBlocks / ceil_div(C, 512));
+  return std::max<int64_t>(16, ceil_div(M, ranges));
+}
+int64_t quantize_ranges(int64_t M, int64_t C) { return std::max<int64_t>(1, ceil_div(M, quantize_rows(M, C))); }
 
 // Weights: one thread block per block of 128 x 128 (once per weight).
 template <typename T>
@@ -148,10 +194,13 @@ struct Product {
   const void* bias;          // [R], or NULL
   void* out;                 // [M, R]
   DevStatus* st;
+  const float* partial;      // sums of the tokens' columns over row ranges, or NULL
+  void* grad_bias;           // [C]
   int M, R, C, E;
   int nb, kb;                // blocks of the weight along N and K
   int stages, split;         // few tokens, small products: stages, CTAs that share a tile's reduction
-  int bias_dt;
+  int bias_dt;               // of bias or grad_bias
+  int ranges;                // of partial
   bool bf16;                 // type of out: bf16, else fp16
   bool vec;                  // rows of out start on 16 bytes
   bool zero_rest;            // rows of no expert are written as zeros (else left as they are)
@@ -263,6 +312,22 @@ __device__ __forceinline__ void zero_rest(const Product& p, const Groups& g, int
   }
 }
 
+// grad_bias from the sums of the row ranges, in their order, by thread `i` of
+// `count`.
+__device__ __forceinline__ void sum_bias(const Product& p, int64_t i, int64_t count) {
+  for (int64_t c = i; c < p.C; c += count) {
+    float s = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < p.ranges; ++k) s += p.partial[static_cast<int64_t>(k) * p.C + c];
+    if (p.bias_dt == DT_F32) static_cast<float*>(p.grad_bias)[c] = s;
+    else if (p.bias_dt == DT_BF16) static_cast<__nv_bfloat16*>(p.grad_bias)[c] = __float2bfloat16_rn(s);
+    else static_cast<__half*>(p.grad_bias)[c] = __float2half_rn(s);
+  }
+}
+__global__ void __launch_bounds__(256) fp8_sum_bias_kernel(const __grid_constant__ Product p) {
+  sum_bias(p, static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, static_cast<int64_t>(gridDim.x) * 256);
+}
+
 // 8 consecutive outputs (16 bytes) from output r on of a row.
 __device__ __forceinline__ void store_out8(const Product& p, int64_t m, int r, const uint4& v) {
   uint16_t* dst = static_cast<uint16_t*>(p.out) + m * p.R + r;
@@ -303,6 +368,26 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(a)
                : "memory");
+  return v;
+}
+
+// The sum of the same place in every CTA of the cluster, in the order of the
+// ranks, with all loads under way.
+constexpr int kMaxSplit = 8;
+__device__ __forceinline__ float4 cluster_sum(const float* src, int split) {
+  float4 part[kMaxSplit];
+#pragma unroll
+  for (int k = 0; k < kMaxSplit; ++k)
+    if (k < split) part[k] = ld_cluster4(mapa_shared(src, static_cast<uint32_t>(k)));
+  float4 v = part[0];
+#pragma unroll
+  for (int k = 1; k < kMaxSplit; ++k)
+    if (k < split) {
+      v.x += part[k].x;
+      v.y += part[k].y;
+      v.z += part[k].z;
+      v.w += part[k].w;
+    }
   return v;
 }
 
@@ -379,7 +464,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const _
   const int num_m = p.offsets == nullptr ? (p.M + kN - 1) / kN : groups.tile[p.E];
   const int num_r = (p.R + 127) / 128;
   const int tiles = num_m * num_r, all = (p.C + kBlk - 1) / kBlk;
-  const int b0 = all * rank / p.split, count = all * (rank + 1) / p.split - b0;   // this CTA's blocks of a reduction
+  // this CTA's blocks of a reduction: every `split`th, so that the CTAs of a
+  // cluster read neighbouring memory at a time
+  const int split = p.split, count = (all - rank + split - 1) / split;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -394,7 +481,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const _
       if (first < tiles) {
         const Tile x = tile_at<128>(p, groups, first, num_m, num_r, kN);
         ahead = min(kFewStages, count);
-        for (int s = 0; s < ahead; ++s) fetch_w(s, x, b0 + s);
+        for (int s = 0; s < ahead; ++s) fetch_w(s, x, rank + s * split);
       }
       grid_dependency_wait();
       asm volatile("fence.proxy.async;" ::: "memory");
@@ -406,8 +493,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const _
             ok = false;   // not before the fetches ahead have their tokens: those stages are empty
             break;
           }
-          if (it >= ahead) fetch_w(s, x, b0 + b);
-          tma_load_2d(smem + s * kStageBytes + kTileBytes, &p.tmX, (b0 + b) * kBlk, x.m0, &y.full[s]);
+          if (it >= ahead) fetch_w(s, x, rank + b * split);
+          tma_load_2d(smem + s * kStageBytes + kTileBytes, &p.tmX, (rank + b * split) * kBlk, x.m0, &y.full[s]);
         }
       }
       // what is under way lands before the block may end
@@ -455,6 +542,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const _
     grid_dependency_wait();
     if (p.offsets != nullptr && p.zero_rest)
       zero_rest(p, groups, blockIdx.x * kEpiWarps + quad, gridDim.x * kEpiWarps, lane);
+    if (p.partial != nullptr)
+      sum_bias(p, (static_cast<int64_t>(blockIdx.x) * kEpiWarps + quad) * 32 + lane, static_cast<int64_t>(gridDim.x) * kEpiWarps * 32);
     int grp = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
@@ -471,7 +560,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const _
       auto fetch = [&](int b) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int at = i * 32 + lane, blk = min(b0 + b + at / kN, b0 + count - 1);
+          const int at = i * 32 + lane, blk = rank + min(b + at / kN, count - 1) * split;
           xv[i] = p.xs[static_cast<int64_t>(blk) * p.M + min(x.m0 + at % kN, p.M - 1)];
           wv[i] = ws[static_cast<int64_t>(blk) * wstep];
         }
@@ -510,7 +599,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const _
         }
       }
       if (!ok) break;
-      if (p.split > 1) {
+      if (split > 1) {
         // all of this CTA's products have completed: its stages hold the sums now, [token][output]
         float* dst = reinterpret_cast<float*>(smem) + quad * 32 + lane;
 #pragma unroll
@@ -523,24 +612,17 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const _
       }
     }
   }
-  if (p.split > 1) {
+  if (split > 1) {
     // one tile a cluster; every rank adds up its share of the tokens, a warp
     // four outputs a lane
     cluster_sync();
     if (warp >= 2 && first < tiles && *abort == 0) {
       const Tile x = tile_at<128>(p, groups, first, num_m, num_r, kN);
       const int r = x.r0 + 4 * lane;
-      for (int i = rank * kEpiWarps + warp - 2; i < min(kN, x.end - x.m0); i += p.split * kEpiWarps) {
+      for (int i = rank * kEpiWarps + warp - 2; i < min(kN, x.end - x.m0); i += split * kEpiWarps) {
         if (r >= p.R) continue;
         const float* src = reinterpret_cast<const float*>(smem) + i * 128 + 4 * lane;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < p.split; ++k) {
-          const float4 part = ld_cluster4(mapa_shared(src, static_cast<uint32_t>(k)));
-          v.x += part.x;
-          v.y += part.y;
-          v.z += part.z;
-          v.w += part.w;
-        }
+        const float4 v = cluster_sum(src, split);
         const uint32_t q[2] = {pack16(p.bf16, v.x + bias_at(p, r), v.y + bias_at(p, r + 1)),
                                pack16(p.bf16, v.z + bias_at(p, r + 2), v.w + bias_at(p, r + 3))};
         uint16_t* dst = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(x.m0 + i) * p.R + r;
@@ -564,6 +646,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const _
 // ---- small products -------------------------------------------------------
 
 constexpr int kThreads = 192;
+constexpr int kStoreBytes = 2048;    // per epilogue warp: 32 rows of 32 outputs on their way out
 constexpr int kMaxStages = 8;
 template <int kTileR>
 struct Shared {
@@ -576,7 +659,7 @@ struct Shared {
 };
 template <int kTileR>
 constexpr int small_smem(int stages) {
-  return 1024 + stages * (128 + kTileR) * 128 + static_cast<int>(sizeof(Shared<kTileR>));
+  return 1024 + stages * (128 + kTileR) * 128 + kEpiWarps * kStoreBytes + static_cast<int>(sizeof(Shared<kTileR>));
 }
 
 // Tiles of 128 tokens x kTileR outputs.  Warp 0 fetches, warp 1
@@ -595,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int kTileM = 128, x_bytes = kTileBytes, stage_bytes = x_bytes + kTileR * 128;
   const int stages = p.stages;
-  Shared<kTileR>& y = *reinterpret_cast<Shared<kTileR>*>(smem + stages * stage_bytes);
+  Shared<kTileR>& y = *reinterpret_cast<Shared<kTileR>*>(smem + stages * stage_bytes + kEpiWarps * kStoreBytes);
   volatile int* abort = &y.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -628,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
   const int num_m = p.offsets == nullptr ? (p.M + kTileM - 1) / kTileM : groups.tile[p.E];
   const int num_r = (p.R + kTileR - 1) / kTileR;
   const int tiles = num_m * num_r, all = (p.C + kBlk - 1) / kBlk;
-  const int b0 = all * rank / p.split, b1 = all * (rank + 1) / p.split;   // this CTA's blocks of a tile's reduction
+  const int b0 = all * rank / p.split, b1 = all * (rank + 1) / p.split;   // this CTA's blocks of a reduction
 
   if (warp == 0) {
     if (lane == 0) {
@@ -696,9 +779,12 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
     const int quad = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     float* bias_s = y.bias[quad];
+    uint8_t* out_s = smem + stages * stage_bytes + quad * kStoreBytes;
     grid_dependency_wait();
     if (p.offsets != nullptr && p.zero_rest)
       zero_rest(p, groups, blockIdx.x * kEpiWarps + quad, gridDim.x * kEpiWarps, lane);
+    if (p.partial != nullptr)
+      sum_bias(p, (static_cast<int64_t>(blockIdx.x) * kEpiWarps + quad) * 32 + lane, static_cast<int64_t>(gridDim.x) * kEpiWarps * 32);
     const int wstep = kT ? p.kb : 1;
     int it = 0;
     bool ok = true;
@@ -772,28 +858,43 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
 #pragma unroll
         for (int i = 0; i < kTileR / 32; ++i) bias_s[lane + 32 * i] = bias[i];
         __syncwarp();
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(m) * p.R + x.r0;
-        if (m < last) {
+        // through shared memory, 32 outputs of 32 rows at a time, so that rows
+        // are written in whole sectors
 #pragma unroll
-          for (int i = 0; i < kTileR / 8; ++i) {
-            const float4 lo = *reinterpret_cast<const float4*>(bias_s + 8 * i);
-            const float4 hi = *reinterpret_cast<const float4*>(bias_s + 8 * i + 4);
+        for (int h = 0; h < kTileR / 32; ++h) {
+          if (x.r0 + 32 * h >= p.R) break;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float4 lo = *reinterpret_cast<const float4*>(bias_s + 32 * h + 8 * c);
+            const float4 hi = *reinterpret_cast<const float4*>(bias_s + 32 * h + 8 * c + 4);
             const float bv[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             uint32_t q[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float2 v = unpack2(acc[4 * i + k]);
+              const float2 v = unpack2(acc[16 * h + 4 * c + k]);
               q[k] = pack16(p.bf16, v.x + bv[2 * k], v.y + bv[2 * k + 1]);
             }
-            const int r = x.r0 + 8 * i;
-            if (p.vec) {
-              if (r < p.R) *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(q[0], q[1], q[2], q[3]);
-            } else {
+            st_shared_v4(out_s + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), make_uint4(q[0], q[1], q[2], q[3]));
+          }
+          __syncwarp();
+          const int r = x.r0 + 32 * h;
+          uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(row0) * p.R + r;
+          if (p.vec) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                if (r + k < p.R) dst[8 * i + k] = static_cast<uint16_t>(q[k >> 1] >> (16 * (k & 1)));
+            for (int i = 0; i < 4; ++i) {
+              const int row = i * 8 + (lane >> 2), c = lane & 3;
+              const uint4 v = ld_shared_v4(out_s + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+              if (row0 + row < last && r + 8 * c < p.R)
+                *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row) * p.R + 8 * c) = v;
+            }
+          } else {
+            const int rows = min(32, last - row0);
+            for (int row = 0; row < rows; ++row) {
+              const uint16_t v = *reinterpret_cast<const uint16_t*>(out_s + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + (lane & 7) * 2);
+              if (r + lane < p.R) out[static_cast<int64_t>(row) * p.R + lane] = v;
             }
           }
+          __syncwarp();
         }
         __syncwarp();
       }
@@ -809,15 +910,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
       for (int g = rank * (kEpiWarps * 32) + static_cast<int>(threadIdx.x) - 64; g < count; g += p.split * kEpiWarps * 32) {
         const int row = g / (kTileR / 4), i = g % (kTileR / 4), r = x.r0 + 4 * i;
         if (r >= p.R) continue;
-        const float4* src = reinterpret_cast<const float4*>(smem) + row * (kTileR / 4) + (i ^ (row & 7));
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < p.split; ++k) {
-          const float4 part = ld_cluster4(mapa_shared(src, static_cast<uint32_t>(k)));
-          v.x += part.x;
-          v.y += part.y;
-          v.z += part.z;
-          v.w += part.w;
-        }
+        const float* src = reinterpret_cast<const float*>(smem) + 4 * (row * (kTileR / 4) + (i ^ (row & 7)));
+        const float4 v = cluster_sum(src, p.split);
         const uint32_t q[2] = {pack16(p.bf16, v.x + bias_at(p, r), v.y + bias_at(p, r + 1)),
                                pack16(p.bf16, v.z + bias_at(p, r + 2), v.w + bias_at(p, r + 3))};
         uint16_t* dst = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(x.m0 + row) * p.R + r;
@@ -1048,6 +1142,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const
     grid_dependency_wait();
     if (p.offsets != nullptr && p.zero_rest)
       zero_rest(p, groups, blockIdx.x * kWideEpiWarps + ew, gridDim.x * kWideEpiWarps, lane);
+    if (p.partial != nullptr)
+      sum_bias(p, (static_cast<int64_t>(blockIdx.x) * kWideEpiWarps + ew) * 32 + lane, static_cast<int64_t>(gridDim.x) * kWideEpiWarps * 32);
     int it = 0;
     bool ok = true;
     float now = 0.f;   // the product of the scales of block it
@@ -1160,18 +1256,23 @@ int sm_count() {
   return sms;
 }
 
-cudaError_t launch_quantize(const void* x, int xt, int64_t M, int64_t C, uint8_t* codes, float* scales, DevStatus* st,
-                            cudaStream_t s) {
-  const bool vec = C % (xt == DT_F32 ? 4 : 8) == 0;
-  const int64_t items = M * ceil_div(C, 512);
-  const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(items, 8), sm_count() * 8)));
-  const int c = static_cast<int>(C), ld = static_cast<int>(code_ld(C));
+// partial: NULL, or room for the sums of quantize_ranges(M, C) row ranges.
+template <typename T>
+cudaError_t launch_quantize_typed(const T* x, int64_t M, int64_t C, uint8_t* codes, float* scales, float* partial,
+                                  DevStatus* st, cudaStream_t s) {
+  const bool vec = C % (16 / static_cast<int>(sizeof(T))) == 0;
+  const int c = static_cast<int>(C), ld = static_cast<int>(code_ld(C)), rows = static_cast<int>(quantize_rows(M, C));
+  const dim3 grid(static_cast<unsigned>(ceil_div(C, 512)), static_cast<unsigned>(quantize_ranges(M, C)));
   ProfScope ps(K_FP8_QUANTIZE, s);
-  if (xt == DT_F16) fp8_quantize_kernel<<<grid, 256, 0, s>>>(static_cast<const __half*>(x), M, c, ld, vec, codes, scales, st);
-  else if (xt == DT_BF16)
-    fp8_quantize_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), M, c, ld, vec, codes, scales, st);
-  else fp8_quantize_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(x), M, c, ld, vec, codes, scales, st);
+  if (partial != nullptr) fp8_quantize_kernel<T, true><<<grid, 256, 0, s>>>(x, M, c, ld, vec, rows, codes, scales, partial, st);
+  else fp8_quantize_kernel<T, false><<<grid, 256, 0, s>>>(x, M, c, ld, vec, rows, codes, scales, partial, st);
   return cudaGetLastError();
+}
+cudaError_t launch_quantize(const void* x, int xt, int64_t M, int64_t C, uint8_t* codes, float* scales, float* partial,
+                            DevStatus* st, cudaStream_t s) {
+  if (xt == DT_F16) return launch_quantize_typed(static_cast<const __half*>(x), M, C, codes, scales, partial, st, s);
+  if (xt == DT_BF16) return launch_quantize_typed(static_cast<const __nv_bfloat16*>(x), M, C, codes, scales, partial, st, s);
+  return launch_quantize_typed(static_cast<const float*>(x), M, C, codes, scales, partial, st, s);
 }
 
 // The kernel after the quantising one: it sets itself up while that one runs.
@@ -1209,7 +1310,7 @@ bool make_maps(Product& p, bool kt, const void* x, const void* w, int rows, int 
 // covered (each has up to 90 KB under way).
 int split_of(int64_t tiles, int blocks, int64_t want) {
   int split = 1;
-  while (split < 8 && split * tiles < want && 4 * split <= blocks) split *= 2;
+  while (split < kMaxSplit && split * tiles < want && 4 * split <= blocks) split *= 2;
   return split;
 }
 
@@ -1225,7 +1326,7 @@ int launch_few(Product& p, const void* x, const void* w, int64_t extra, cudaStre
 
 template <bool kT, int kTileR>
 int launch_small(Product& p, const void* x, const void* w, int64_t tiles, cudaStream_t s) {
-  constexpr int kBudget = 107000;   // two CTAs an SM
+  constexpr int kBudget = 111000;   // two CTAs an SM
   const int sms = sm_count();
   p.stages = kMaxStages;
   while (p.stages > 2 && small_smem<kTileR>(p.stages) > kBudget) --p.stages;
@@ -1282,23 +1383,24 @@ int product(bool transposed, const void* x, int xt, int64_t M, const uint8_t* co
   if (!aligned16(x) || !aligned16(codes) || !aligned16(out)) return ST_MISALIGNED;
   if (ws == nullptr) return ST_WORKSPACE;
   if (!aligned256(ws)) return ST_MISALIGNED;
-  const int64_t chunks = grad_bias != nullptr ? gradout_partial_chunks(M) : 0;
-  const size_t need = kAlign + codes_bytes(M, C) + scales_bytes(M, C) + align_up(static_cast<size_t>(chunks) * static_cast<size_t>(N) * 4);
-  if (ws_bytes < need) return ST_WORKSPACE;
+  const size_t partial_bytes = grad_bias != nullptr ? i8lt_fp8_grad_bias_bytes(M, N) : 0;
+  if (ws_bytes < kAlign + codes_bytes(M, C) + scales_bytes(M, C) + partial_bytes) return ST_WORKSPACE;
   if (M == 0 && grad_bias == nullptr) return ST_OK;
   if (int d = check_device()) return d;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* q = static_cast<uint8_t*>(ws) + kAlign;
   float* qs = reinterpret_cast<float*>(q + codes_bytes(M, C));
   DevStatus* st = static_cast<DevStatus*>(ws);
-  if (grad_bias != nullptr) {
-    float* partial = reinterpret_cast<float*>(q + codes_bytes(M, C) + scales_bytes(M, C));
-    if (cudaError_t e = launch_gradout_prepass(x, xt, M, N, N % 8 == 0, nullptr, 0, grad_bias, bt, partial, chunks, s))
-      return cuda_status(e);
-    if (M == 0 || out == nullptr) return cuda_status(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
+  if (M == 0) {
+    if (cudaMemsetAsync(grad_bias, 0, static_cast<size_t>(N) * (bt == DT_F32 ? 4 : 2), s) != cudaSuccess) return ST_CUDA;
+    return cuda_status(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
   }
+  float* partial = grad_bias != nullptr ? reinterpret_cast<float*>(q + codes_bytes(M, C) + scales_bytes(M, C)) : nullptr;
   Product p;
   std::memset(&p, 0, sizeof(p));
+  p.partial = partial;
+  p.grad_bias = grad_bias;
+  p.ranges = static_cast<int>(quantize_ranges(M, C));
   p.xs = qs;
   p.ws = scales;
   p.offsets = offsets;
@@ -1315,7 +1417,12 @@ int product(bool transposed, const void* x, int xt, int64_t M, const uint8_t* co
   p.bf16 = xt == DT_BF16;
   p.vec = R % 8 == 0;
   p.zero_rest = zero_rest != 0;
-  if (cudaError_t e = launch_quantize(x, xt, M, C, q, qs, st, s)) return cuda_status(e);
+  if (cudaError_t e = launch_quantize(x, xt, M, C, q, qs, partial, st, s)) return cuda_status(e);
+  if (out == nullptr) {   // the bias gradient alone
+    ProfScope ps(K_FP8_GEMM, s);
+    fp8_sum_bias_kernel<<<static_cast<unsigned>(std::min<int64_t>(ceil_div(C, 256), 4 * sm_count())), 256, 0, s>>>(p);
+    return cuda_status(cudaGetLastError());
+  }
   return transposed ? launch_product<true>(p, q, codes, s) : launch_product<false>(p, q, codes, s);
 }
 
@@ -1340,7 +1447,7 @@ int i8lt_fp8_quantize(const void* x, int xt, int64_t M, int64_t C, uint8_t* code
   if (x == nullptr || codes == nullptr || scales == nullptr) return ST_INVALID_ARG;
   if (!aligned16(x) || !aligned16(codes)) return ST_MISALIGNED;
   if (int d = check_device()) return d;
-  return cuda_status(launch_quantize(x, xt, M, C, codes, scales, nullptr, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_quantize(x, xt, M, C, codes, scales, nullptr, nullptr, static_cast<cudaStream_t>(stream)));
 }
 
 int i8lt_fp8_quantize_weight(const void* W, int wt, int64_t E, int64_t N, int64_t K, uint8_t* codes, float* scales,
@@ -1391,7 +1498,8 @@ size_t i8lt_fp8_workspace_size(int64_t M, int64_t C) {
 
 size_t i8lt_fp8_grad_bias_bytes(int64_t M, int64_t N) {
   if (M < 0 || N < 0 || M > kMaxSize || N > kMaxSize) return 0;
-  return align_up(static_cast<size_t>(gradout_partial_chunks(M)) * static_cast<size_t>(N) * 4);
+  if (N == 0) return 0;
+  return align_up(static_cast<size_t>(quantize_ranges(M, N)) * static_cast<size_t>(N) * 4);
 }
 
 int i8lt_fp8_forward(const void* x, int xt, int64_t M, const uint8_t* codes, const float* scales, int64_t N, int64_t K,

@@ -10,6 +10,7 @@ efficient backward" (see include/i8lt.h for the formulas).
 from __future__ import annotations
 
 import array
+import functools
 import math
 import operator
 import warnings
@@ -1036,25 +1037,39 @@ def adamw_step_8bit(params, grads, m: torch.Tensor, m_absmax: torch.Tensor, r: t
 # the gradients of a step: their norm, clipping and scaling
 # ---------------------------------------------------------------------------
 
+_current_device = torch._C._cuda_getDevice
+
+
 def _on(dev: int, call, *args) -> int:
     """call(*args) with CUDA device ``dev`` as the current one."""
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         return call(*args)
     with torch.cuda.device(dev):
         return call(*args)
 
 
+def _present(ts) -> list:
+    ts = list(ts)
+    return [t for t in ts if t is not None] if any([t is None for t in ts]) else ts
+
+
 def _grad_lists(what, grads):
     """(what must outlive the call, device, count, addresses of the lists of
-    device addresses, dtypes and sizes) of contiguous ``grads``, checked."""
-    dev = grads[0].get_device()
+    device addresses, dtypes and sizes) of contiguous ``grads``, checked.
+    Called for hundreds of tensors per step: each property is read in one
+    sweep."""
+    n, dev = len(grads), grads[0].get_device()
     _require_cuda(grads[0])
-    if set(map(_get_device, grads)) != {dev}:
+    if n > 1 and set(map(_get_device, grads)) != {dev}:
         raise I8LTError(f"{what}: tensors on {grads[0].device} and another device")
-    codes = {t: _code(t) for t in set(map(_dtype_of, grads))}
-    lists = (array.array("Q", map(_data_ptr, grads)), array.array("i", [codes[t.dtype] for t in grads]),
-             array.array("q", map(_numel, grads)))
-    return (grads, lists), dev, len(grads), [a.buffer_info()[0] for a in lists]
+    dtypes = set(map(_dtype_of, grads))
+    if len(dtypes) == 1:
+        kinds = array.array("i", [_code(grads[0].dtype)]) * n
+    else:
+        codes = {t: _code(t) for t in dtypes}
+        kinds = array.array("i", [codes[t.dtype] for t in grads])
+    lists = array.array("Q", map(_data_ptr, grads)), kinds, array.array("q", map(_numel, grads))
+    return (grads, lists), dev, n, [a.buffer_info()[0] for a in lists]
 
 
 def grad_norm(grads, max_norm: float | None = None, grad_scale: torch.Tensor | None = None,
@@ -1065,35 +1080,41 @@ def grad_norm(grads, max_norm: float | None = None, grad_scale: torch.Tensor | N
     1), scale = c min(1, max_norm / (norm + 1e-6)), found_inf 1 when the norm
     is not finite or the given found_inf is not 0: what ``adamw_step`` and
     ``AdamW.step`` take."""
-    grads = [g if g.is_contiguous() else g.contiguous() for g in grads if g is not None]
+    grads = _present(grads)
     if not grads:
         raise I8LTError("grad_norm: no gradients")
+    if not all(map(_is_contiguous, grads)):
+        grads = [g.contiguous() for g in grads]
     held, dev, n, at = _grad_lists("grad_norm", grads)
-    device = grads[0].device
-    _adamw_scalar("grad_norm", grad_scale, device)
-    _adamw_scalar("grad_norm", found_inf, device)
-    result = torch.empty(3, dtype=torch.float32, device=device)
-    ws = torch.empty(_lib.i8lt_grad_norm_workspace_size(), dtype=torch.uint8, device=device)
+    if grad_scale is not None or found_inf is not None:
+        _adamw_scalar("grad_norm", grad_scale, grads[0].device)
+        _adamw_scalar("grad_norm", found_inf, grads[0].device)
+    # the results and, behind them, the scratch of the sums
+    size = _lib.i8lt_grad_norm_workspace_size()
+    ws = grads[0].new_empty(64 + size // 4, dtype=torch.float32)
+    start = ws.data_ptr()
     _check(_on(dev, _lib.i8lt_grad_norm, *at, n, _ptr(grad_scale), _ptr(found_inf),
-               math.inf if max_norm is None else max_norm, result.data_ptr(), ws.data_ptr(), ws.numel(),
-               _stream(ws)), "i8lt_grad_norm")
-    return tuple(result.unbind())
+               math.inf if max_norm is None else max_norm, start, start + 256, size, _stream(ws)), "i8lt_grad_norm")
+    norm, scale, inf = ws[:3].unbind()
+    return norm, scale, inf
 
 
 def scale_grads_(grads, scale: torch.Tensor) -> None:
     """Multiply all ``grads`` (None is left out) by the fp32 device scalar
     ``scale``, in place (i8lt_scale_grads); a scale of 1 moves nothing.  None
     may overlap another one."""
-    grads = [g for g in grads if g is not None]
+    grads = dense = _present(grads)
     if not grads:
         return
-    dense = [g if g.is_contiguous() else g.contiguous() for g in grads]
+    if not all(map(_is_contiguous, grads)):
+        dense = [g.contiguous() for g in grads]
     held, dev, n, at = _grad_lists("scale_grads_", dense)
     _adamw_scalar("scale_grads_", scale, grads[0].device)
     _check(_on(dev, _lib.i8lt_scale_grads, *at, n, scale.data_ptr(), _stream(grads[0])), "i8lt_scale_grads")
-    for g, d in zip(grads, dense):
-        if d is not g:
-            g.copy_(d)
+    if dense is not grads:
+        for g, d in zip(grads, dense):
+            if d is not g:
+                g.copy_(d)
     _written(grads)
 
 
@@ -1120,6 +1141,12 @@ def _zeros_fp8(shape, device) -> torch.Tensor:
     return torch.zeros(shape, dtype=torch.uint8, device=device).view(FP8)   # code 0 is E4M3's zero
 
 
+def _scratch(what, ws, size: int, t: torch.Tensor) -> torch.Tensor:
+    """``_workspace`` on t's device."""
+    return t.new_empty(max(size, 256), dtype=torch.uint8) if ws is None else _workspace(what, ws, size, t.device)
+
+
+@functools.lru_cache(maxsize=1024)   # a function of the sizes alone
 def _fp8_shapes(N: int, K: int):
     """Shapes of the codes and of the scales of a weight [N, K]."""
     return (N, _lib.i8lt_fp8_ld(K)), (_lib.i8lt_fp8_blocks(N), _lib.i8lt_fp8_blocks(K))
@@ -1200,8 +1227,8 @@ def fp8_forward(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, K: i
     what = "fp8_forward"
     dev, M, N, x, codes, scales = _fp8_args(what, x, codes, scales, K, (), False)
     bias = _arg("fp8_forward bias", bias, dev, (N,), None)
-    y = torch.empty((M, N), dtype=x.dtype, device=x.device) if out is None else _out("fp8_forward out", out, dev, (M, N), x.dtype)
-    ws = _workspace(what, ws, _lib.i8lt_fp8_workspace_size(M, K), x.device)
+    y = x.new_empty((M, N)) if out is None else _out("fp8_forward out", out, dev, (M, N), x.dtype)
+    ws = _scratch(what, ws, _lib.i8lt_fp8_workspace_size(M, K), x)
     _check(_on(dev, _lib.i8lt_fp8_forward, _ptr(x), _code(x.dtype), M, _ptr(codes), _ptr(scales), N, K, _ptr(bias),
                0 if bias is None else _code(bias.dtype), _ptr(y), ws.data_ptr(), ws.numel(), _stream(x)),
            "i8lt_fp8_forward")
@@ -1220,14 +1247,13 @@ def fp8_backward_input(G: torch.Tensor, codes: torch.Tensor, scales: torch.Tenso
     dev, M, N, G, codes, scales = _fp8_args(what, G, codes, scales, K, (), True)
     gx = gb = None
     if need_grad_A:
-        gx = torch.empty((M, K), dtype=G.dtype, device=G.device) if out is None else \
-            _out("fp8_backward_input out", out, dev, (M, K), G.dtype)
+        gx = G.new_empty((M, K)) if out is None else _out("fp8_backward_input out", out, dev, (M, K), G.dtype)
     if bias_dtype is not None:
-        gb = torch.empty(N, dtype=bias_dtype, device=G.device)
+        gb = G.new_empty(N, dtype=bias_dtype)
     if gx is None and gb is None:
         return None, None
     size = _lib.i8lt_fp8_workspace_size(M, N) + (_lib.i8lt_fp8_grad_bias_bytes(M, N) if gb is not None else 0)
-    ws = _workspace(what, ws, size, G.device)
+    ws = _scratch(what, ws, size, G)
     _check(_on(dev, _lib.i8lt_fp8_backward_input, _ptr(G), _code(G.dtype), M, _ptr(codes), _ptr(scales), N, K,
                _ptr(gx), _ptr(gb), 0 if gb is None else _code(bias_dtype), ws.data_ptr(), ws.numel(), _stream(G)),
            "i8lt_fp8_backward_input")
@@ -1243,8 +1269,8 @@ def _fp8_experts(what, call, t, codes, scales, K, offsets, transposed, out, ws):
     dev, M, N, t, codes, scales = _fp8_args(what, t, codes, scales, K, (E,), transposed)
     offsets = _arg(f"{what} offsets", offsets, dev, (E + 1,), torch.int32)
     shape = (M, K if transposed else N)
-    y = torch.empty(shape, dtype=t.dtype, device=t.device) if out is None else _out(f"{what} out", out, dev, shape, t.dtype)
-    ws = _workspace(what, ws, _lib.i8lt_fp8_workspace_size(M, N if transposed else K), t.device)
+    y = t.new_empty(shape) if out is None else _out(f"{what} out", out, dev, shape, t.dtype)
+    ws = _scratch(what, ws, _lib.i8lt_fp8_workspace_size(M, N if transposed else K), t)
     _check(_on(dev, call, _ptr(t), _code(t.dtype), M, _ptr(codes), _ptr(scales), E, N, K, _ptr(offsets),
                1 if out is None else 0, _ptr(y), ws.data_ptr(), ws.numel(), _stream(t)), f"i8lt_{what}")
     if out is not None:
