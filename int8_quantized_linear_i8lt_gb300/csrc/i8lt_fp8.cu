@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(256) fp8_dequantize_weight_kernel(const uint8_
 struct Product {
   CUtensorMap tmX;           // codes of the tokens [M, ld(C)], box 128 columns x a tile's tokens
   CUtensorMap tmW;           // codes of the weight [E][N, ld(K)], box of a block and up to 128 outputs
-  CUtensorMap tmOut;         // out, box 64 outputs x 32 rows (wide kernel, rows on 16 bytes)
+  CUtensorMap tmOut;         // out, box 32 outputs x 32 rows (wide kernel, rows on 16 bytes)
   const float* xs;           // scales of the tokens [ceil(C / 128)][M]
   const float* ws;           // scales of the weight [E][ceil(N / 128)][ceil(K / 128)]
   const int32_t* offsets;    // [E + 1] row ranges of the experts, or NULL: one weight for all rows
@@ -937,16 +937,15 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
 constexpr int kWideThreads = 384;
 constexpr int kWideEpiWarps = 8;          // warps 4 to 11
 constexpr int kWideStages = 4;
-constexpr int kWideStageBytes = 2 * kTileBytes;
+constexpr int kWideStageBytes = 3 * kTileBytes;
 constexpr int kWideCols = 128;            // outputs of an epilogue warp
-constexpr int kWideStoreBytes = 8192;     // per epilogue warp: 32 rows of 128 outputs, two boxes of 64
+constexpr int kWideStoreBytes = 2048;     // per epilogue warp: 32 rows of 32 outputs
 // Registers a thread: 168 at launch (384 x 168 = 64512); of those the first
 // four warps keep 40 and the epilogue's take 232 (128 x 40 + 256 x 232 = 64512).
 constexpr int kWideRegs = 40, kWideEpiRegs = 232;
 static_assert(128 * kWideRegs + 256 * kWideEpiRegs <= kWideThreads * 168, "register split");
 constexpr int kScaleRing = 8;             // blocks whose scales are in shared memory
 constexpr int kScaleAhead = 6;            // ... of which so many are on their way
-constexpr int kTileRing = 16;             // tiles whose places are in shared memory: more than there are blocks on their way
 struct WideShared {
   uint64_t full[kWideStages], empty[kWideStages];
   uint64_t acc_full[2];                   // an accumulator is there, and the scales of its block and the next
@@ -957,24 +956,9 @@ struct WideShared {
   int abort;
   float bias[kWideEpiWarps][kWideCols];
   float xs[kScaleRing][128], ws[kScaleRing][2];
-  Tile tiles[kTileRing];
 };
 constexpr int kWideSmemBytes = 1024 + kWideStages * kWideStageBytes + kWideEpiWarps * kWideStoreBytes + static_cast<int>(sizeof(WideShared));
 
-__device__ __forceinline__ void umma_fp8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
 // whether the phase has completed, without waiting for it
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -998,43 +982,6 @@ template <int kRegs>
 __device__ __forceinline__ void keep_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 template <int kRegs>
 __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-__device__ __forceinline__ void add2(uint64_t& acc, uint64_t v) {
-  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(v));
-}
-template <bool kBf16>
-__device__ __forceinline__ uint32_t round2(uint64_t v) {
-  const float2 f = unpack2(v);
-  return pack16(kBf16, f.x, f.y);
-}
-// A warp's 32 rows of 128 outputs, through shared memory of its own: the
-// stores are under way while the next tile's sums are taken.
-template <bool kBf16>
-__device__ __forceinline__ void write_tile(const Product& p, int row0, int end, int r0, uint8_t* out_s, int lane,
-                                           const uint64_t (&acc)[kWideCols / 2]) {
-  bulk_wait_read<0>();   // the tile ahead has left the buffer
-  __syncwarp();
-#pragma unroll
-  for (int c = 0; c < 16; ++c)
-    st_shared_v4(out_s + (c >> 3) * 4096 + lane * 128 + (((c & 7) ^ (lane & 7)) << 4),
-                 make_uint4(round2<kBf16>(acc[4 * c]), round2<kBf16>(acc[4 * c + 1]), round2<kBf16>(acc[4 * c + 2]),
-                            round2<kBf16>(acc[4 * c + 3])));
-  if (p.vec && row0 + 32 <= end) {   // outputs past the last are not written
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane < 2 && r0 + 64 * lane < p.R) tma_store_2d(&p.tmOut, r0 + 64 * lane, row0, out_s + 4096 * lane);
-    bulk_commit();
-    return;
-  }
-  __syncwarp();
-#pragma unroll 1
-  for (int i = 0; i < 16; ++i) {
-    const int row = i * 2 + (lane >> 4), c = lane & 15;
-    const uint4 v = ld_shared_v4(out_s + (c >> 3) * 4096 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-    if (row0 + row < end && r0 + c * 8 < p.R) store_out8(p, row0 + row, r0 + c * 8, v);
-  }
-  __syncwarp();
-}
-
 // Tiles of 128 tokens x 256 outputs; two accumulators in turn fill TMEM, and
 // eight warps keep the sums in registers (128 outputs a thread).
 // What bounds it is how fast an accumulator is handed back: a block's product
@@ -1046,8 +993,8 @@ __device__ __forceinline__ void write_tile(const Product& p, int row0, int end, 
 // there is nothing to wait for; and warp 3 brings the scales to shared memory,
 // blocks and tiles ahead.
 template <bool kT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const __grid_constant__ Product p) {
-  constexpr int kTileM = 256, kTileR = 256;
+__global__ void __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const __grid_constant__ Product p) {
+  constexpr int kTileM = 128, kTileR = 256;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Groups groups;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1055,8 +1002,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) fp8
   WideShared& y = *reinterpret_cast<WideShared*>(store + kWideEpiWarps * kWideStoreBytes);
   volatile int* abort = &y.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int first = blockIdx.x, step = gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWideStages; ++i) {
@@ -1065,7 +1011,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) fp8
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&y.acc_full[i], 2);
-      mbar_init(&y.acc_empty[i], 2 * kWideEpiWarps);
+      mbar_init(&y.acc_empty[i], kWideEpiWarps);
       mbar_init(&y.scale_read[i], kWideEpiWarps);
     }
     mbar_init(&y.last, 2);
@@ -1076,12 +1022,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) fp8
     if (p.vec) tma_prefetch_desc(&p.tmOut);
   }
   if (warp == 1) {
-    tmem_alloc_pair(&y.tmem, 512);
-    tmem_relinquish_pair();
+    tmem_alloc(&y.tmem, 512);
+    tmem_relinquish();
   }
   if (warp == 4 && p.offsets != nullptr) plan_groups(p, groups, kTileM, lane);
   tc_fence_before();
-  cluster_sync();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = y.tmem;
   const int num_m = p.offsets == nullptr ? (p.M + kTileM - 1) / kTileM : groups.tile[p.E];
@@ -1105,18 +1051,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) fp8
             break;
           }
           uint8_t* xd = smem + s * kWideStageBytes;
-          const uint32_t full = mapa_shared(&y.full[s], 0);
-          if (rank == 0) mbar_arrive_expect_tx(&y.full[s], 2 * kWideStageBytes);
-          tma_load_2d_pair(xd, &p.tmX, b * kBlk, x.m0 + rank * 128, full);
-          if (kT) tma_load_3d_pair(xd + kTileBytes, &p.tmW, x.r0 + rank * 128, b * kBlk, x.e, full);
-          else tma_load_3d_pair(xd + kTileBytes, &p.tmW, b * kBlk, x.r0 + rank * 128, x.e, full);
+          mbar_arrive_expect_tx(&y.full[s], kWideStageBytes);
+          tma_load_2d(xd, &p.tmX, b * kBlk, x.m0, &y.full[s]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint8_t* wd = xd + (1 + i) * kTileBytes;
+            if (kT) tma_load_3d(wd, &p.tmW, x.r0 + 128 * i, b * kBlk, x.e, &y.full[s]);
+            else tma_load_3d(wd, &p.tmW, b * kBlk, x.r0 + 128 * i, x.e, &y.full[s]);
+          }
         }
       }
       // what is under way lands before the block may end
-      if (rank == 0) for (int j = max(0, it - kWideStages); j < it; ++j)
+      for (int j = max(0, it - kWideStages); j < it; ++j)
         mbar_wait_out(&y.full[j % kWideStages], (j / kWideStages) & 1, p.st, kWhereFetch);
     }
-    if ((warp == 1 || warp == 2) && lane == 0 && rank == 0) {
+    if ((warp == 1 || warp == 2) && lane == 0) {
       const uint32_t idesc = make_idesc_f16(kTileM, kTileR, false, kT);   // E4M3 has the format number of fp16
       const uint32_t base = smem_u32(smem);
       const int a = warp - 1;
@@ -1130,27 +1079,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) fp8
         const uint32_t xa = base + s * kWideStageBytes, wa = xa + kTileBytes;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          umma_fp8_pair(acc, make_sdesc(xa + 32 * k, 16, 1024, kSwizzle128B),
+          umma_fp8(acc, make_sdesc(xa + 32 * k, 16, 1024, kSwizzle128B),
                    kT ? make_sdesc(wa + 4096 * k, kTileBytes, 1024, kSwizzle128B)
                       : make_sdesc(wa + 32 * k, 16, 1024, kSwizzle128B),
                    idesc, k > 0 ? 1u : 0u);
-        umma_commit_pair_mc(&y.acc_full[a], 0x3);
-        umma_commit_pair_mc(&y.empty[s], 0x3);
+        umma_commit(&y.acc_full[a]);
+        umma_commit(&y.empty[s]);
       }
-      umma_commit_pair(&y.last);
+      umma_commit(&y.last);
       mbar_wait_out(&y.last, 0, p.st, kWhereProduct);
     }
     if (warp == 3) {
       grid_dependency_wait();
-      int ft = first, fn = 0, fb = 0, fi = 0;   // the next block to fetch: its tile (and their number), its number there and in all
+      int ft = first, fb = 0, fi = 0;   // the next block to fetch: its tile, its number there and in all
       int rows[4];
       const float* ws = p.ws;
       auto aim = [&]() {
         if (ft >= tiles) return;
         const Tile x = tile_at<kTileR>(p, groups, ft, num_m, num_r, kTileM);
-        if (lane == 0) y.tiles[fn++ % kTileRing] = x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) rows[i] = min(x.m0 + rank * 128 + i * 32 + lane, p.M - 1);
+        for (int i = 0; i < 4; ++i) rows[i] = min(x.m0 + i * 32 + lane, p.M - 1);
         const int rb = min(x.r0 / kBlk + (lane & 1), (p.R - 1) / kBlk);
         ws = p.ws + static_cast<int64_t>(x.e) * p.nb * p.kb + (kT ? rb : rb * p.kb);
       };
@@ -1199,11 +1147,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) fp8
     int it = 0;
     bool ok = true;
     float now = 0.f;   // the product of the scales of block it
-    float bias[4] = {0.f, 0.f, 0.f, 0.f};
     auto scale_of = [&](int i) { return y.xs[i % kScaleRing][quad * 32 + lane] * y.ws[i % kScaleRing][half]; };
     auto wait = [&]() { return __all_sync(0xffffffffu, mbar_wait(&y.acc_full[it & 1], (it >> 1) & 1, abort, p.st, kWhereOut)); };
-    int n = 0;   // tiles so far
-    for (int t = first; t < tiles && ok; t += step, ++n) {
+    for (int t = first; t < tiles && ok; t += step) {
+      const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, kTileM);
+      const int row0 = x.m0 + quad * 32, r0 = x.r0 + half * kWideCols;
+      float bias[4];   // used at the tile's end
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bias[i] = bias_at(p, r0 + lane + 32 * i);
       uint64_t acc[kWideCols / 2];
 #pragma unroll
       for (int i = 0; i < kWideCols / 2; ++i) acc[i] = 0;
@@ -1211,11 +1162,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) fp8
       if (!(ok = wait())) break;
       tc_fence_after();
       tmem_ld32_nowait(lanes + (it & 1) * kTileR, d[0]);
-      if (p.bias != nullptr) {
-        const int r = y.tiles[n % kTileRing].r0 + half * kWideCols + lane;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) bias[i] = bias_at(p, r + 32 * i);   // used at the tile's end
-      }
       if (it == 0) now = scale_of(0);
       for (int b = 0; b < blocks; ++b) {
         const int a = it & 1;
@@ -1233,7 +1179,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) fp8
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-              if (rank == 0) mbar_arrive(&y.acc_empty[a]); else mbar_arrive_remote(mapa_shared(&y.acc_empty[a], 0));
+              mbar_arrive(&y.acc_empty[a]);
               mbar_arrive(&y.scale_read[a]);
             }
             ++it;
@@ -1250,29 +1196,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) fp8
         if (!ok) break;
       }
       if (!ok) break;
-      if (p.bias != nullptr) {
+      // out through shared memory, 32 outputs of 32 rows at a time
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bias_s[lane + 32 * i] = bias[i];
+      const bool inside = p.vec && row0 + 32 <= x.end;
+#pragma unroll
+      for (int h = 0; h < kWideCols / 32; ++h) {
+        if (lane == 0) bulk_wait_read<0>();   // the store ahead has left the buffer
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) bias_s[lane + 32 * i] = bias[i];
-        __syncwarp();
+        for (int c = 0; c < 4; ++c) {
+          uint32_t q[4];
+          const float4 b0 = *reinterpret_cast<const float4*>(bias_s + h * 32 + c * 8);
+          const float4 b1 = *reinterpret_cast<const float4*>(bias_s + h * 32 + c * 8 + 4);
+          const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
-        for (int i = 0; i < kWideCols / 4; ++i) {
-          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(bias_s + 4 * i);
-          add2(acc[2 * i], v.x);
-          add2(acc[2 * i + 1], v.y);
+          for (int i = 0; i < 4; ++i) {
+            const float2 v = unpack2(acc[h * 16 + c * 4 + i]);
+            q[i] = pack16(p.bf16, v.x + bv[2 * i], v.y + bv[2 * i + 1]);
+          }
+          st_shared_v4(out_s + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), make_uint4(q[0], q[1], q[2], q[3]));
+        }
+        const int r = r0 + h * 32;
+        if (inside) {   // outputs past the last are not written
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && r < p.R) {
+            tma_store_2d(&p.tmOut, r, row0, out_s);
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = i * 8 + (lane >> 2), c = lane & 3;
+            const uint4 v = ld_shared_v4(out_s + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+            if (row0 + row < x.end && r + c * 8 < p.R) store_out8(p, row0 + row, r + c * 8, v);
+          }
         }
       }
-      const Tile x = y.tiles[n % kTileRing];
-      const int row0 = x.m0 + rank * 128 + quad * 32, r0 = x.r0 + half * kWideCols;
-      if (p.bf16) write_tile<true>(p, row0, x.end, r0, out_s, lane, acc);
-      else write_tile<false>(p, row0, x.end, r0, out_s, lane, acc);
+      __syncwarp();
     }
-    bulk_wait_all();
+    if (lane == 0) bulk_wait_all();
   }
   tc_fence_before();
-  cluster_sync();
+  __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -1371,14 +1341,14 @@ int launch_product(Product& p, const void* x, const void* w, cudaStream_t s) {
   const int sms = sm_count();
   const int64_t extra = p.offsets == nullptr ? 0 : p.E;   // experts' last tiles, at most
   const int mean = p.M / p.E;
-  const int64_t wide = (ceil_div(p.M, 256) + extra) * ceil_div(p.R, 256);
-  if (mean >= 256 && wide >= sms / 2) {
+  const int64_t wide = (ceil_div(p.M, 128) + extra) * ceil_div(p.R, 256);
+  if (mean >= 256 && wide >= sms) {
     if (!make_maps(p, kT, x, w, 128, 128)) return ST_CUDA;
     if (p.vec && !make_tmap(&p.tmOut, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.out,
-                            p.R, p.M, static_cast<uint64_t>(p.R) * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+                            p.R, p.M, static_cast<uint64_t>(p.R) * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
       return ST_CUDA;
-    return cuda_status(launch_after(fp8_product_wide_kernel<kT>, 2 * std::min<int64_t>(wide, sms / 2), kWideThreads,
-                                    kWideSmemBytes, 2, p, s));
+    return cuda_status(launch_after(fp8_product_wide_kernel<kT>, std::min<int64_t>(wide, sms), kWideThreads,
+                                    kWideSmemBytes, 1, p, s));
   }
   // experts' shares differ: tiles of up to twice the mean
   const int most = p.offsets == nullptr ? p.M : 2 * mean;
