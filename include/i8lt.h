@@ -21,7 +21,8 @@
  * trainable-weight mode, the 4-bit (NF4 and FP4) weight-only layers of QLoRA
  * fine-tuning, an entry point that allocates nothing, the operators that
  * fine-tune on top of the frozen layers (low-rank adapters, layer norm,
- * AdamW), per-launch timing and a diagnostic of the bounded waits (each
+ * AdamW, the gradients' norm and clipping), frozen FP8 layers with a scale per
+ * block of 128 and their form for experts, per-launch timing and a diagnostic of the bounded waits (each
  * documented below).
  *
  * Conventions for every entry point:
@@ -679,8 +680,10 @@ int i8lt_scale_grads(void* const* grads, const int32_t* dtypes,
  *                            unquantized g over the tokens; each may be NULL,
  *                            not both
  * Products of codes are accumulated in fp32 over a block's 128 columns, and
- * each block's sum times the two scales is added in fp32, in order; the output
- * is rounded once.
+ * each block's sum times the two scales is added in fp32, in an order that the
+ * sizes fix: equal inputs give equal bits.  The output is rounded once.  The
+ * product of two scales is taken in fp32, too: where it overflows, the outputs
+ * of that block are infinite or NaN.
  * For experts, tokens sorted by expert: rows offsets[e] <= m < offsets[e + 1]
  * take weight e (offsets [E + 1] int32, device memory, ascending; a value
  * below the one before it, or outside [0, M], counts as the nearest that is

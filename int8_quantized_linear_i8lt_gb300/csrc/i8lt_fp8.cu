@@ -14,6 +14,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 #include "i8lt.h"
@@ -1249,11 +1250,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const
 // host side
 // ---------------------------------------------------------------------------
 
+// SMs of the current device, asked for once per device.
 int sm_count() {
-  int dev = 0, sms = 152;
+  static std::atomic<int> known[64];
+  int dev = 0;
   cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
+  if (dev < 0 || dev >= 64) return 152;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 152;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 // partial: NULL, or room for the sums of quantize_ranges(M, C) row ranges.
@@ -1385,14 +1393,13 @@ int product(bool transposed, const void* x, int xt, int64_t M, const uint8_t* co
   if (!aligned256(ws)) return ST_MISALIGNED;
   const size_t partial_bytes = grad_bias != nullptr ? i8lt_fp8_grad_bias_bytes(M, N) : 0;
   if (ws_bytes < kAlign + codes_bytes(M, C) + scales_bytes(M, C) + partial_bytes) return ST_WORKSPACE;
-  if (M == 0 && grad_bias == nullptr) return ST_OK;
   if (int d = check_device()) return d;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* q = static_cast<uint8_t*>(ws) + kAlign;
   float* qs = reinterpret_cast<float*>(q + codes_bytes(M, C));
   DevStatus* st = static_cast<DevStatus*>(ws);
   if (M == 0) {
-    if (cudaMemsetAsync(grad_bias, 0, static_cast<size_t>(N) * (bt == DT_F32 ? 4 : 2), s) != cudaSuccess) return ST_CUDA;
+    if (grad_bias != nullptr && cudaMemsetAsync(grad_bias, 0, static_cast<size_t>(N) * (bt == DT_F32 ? 4 : 2), s) != cudaSuccess) return ST_CUDA;
     return cuda_status(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
   }
   float* partial = grad_bias != nullptr ? reinterpret_cast<float*>(q + codes_bytes(M, C) + scales_bytes(M, C)) : nullptr;

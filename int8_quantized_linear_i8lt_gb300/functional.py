@@ -1091,7 +1091,7 @@ def grad_norm(grads, max_norm: float | None = None, grad_scale: torch.Tensor | N
         _adamw_scalar("grad_norm", found_inf, grads[0].device)
     # the results and, behind them, the scratch of the sums
     size = _lib.i8lt_grad_norm_workspace_size()
-    ws = grads[0].new_empty(64 + size // 4, dtype=torch.float32)
+    ws = torch.empty(64 + size // 4, dtype=torch.float32, device=grads[0].device)
     start = ws.data_ptr()
     _check(_on(dev, _lib.i8lt_grad_norm, *at, n, _ptr(grad_scale), _ptr(found_inf),
                math.inf if max_norm is None else max_norm, start, start + 256, size, _stream(ws)), "i8lt_grad_norm")
@@ -1122,9 +1122,10 @@ def clip_grad_norm_(parameters, max_norm: float, grad_scale: torch.Tensor | None
     """Clip the gradients of ``parameters`` (a tensor or several) in place to
     the norm ``max_norm`` of all of them together, times ``grad_scale``;
     returns their norm before that, a device scalar."""
-    if isinstance(parameters, torch.Tensor):
-        parameters = [parameters]
+    parameters = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
     grads = [p.grad for p in parameters if p.grad is not None]
+    if not grads:
+        return torch.zeros((), device=parameters[0].device if parameters else None)
     norm, scale, _ = grad_norm(grads, max_norm, grad_scale)
     scale_grads_(grads, scale)
     return norm
@@ -1139,11 +1140,6 @@ FP8 = torch.float8_e4m3fn
 
 def _zeros_fp8(shape, device) -> torch.Tensor:
     return torch.zeros(shape, dtype=torch.uint8, device=device).view(FP8)   # code 0 is E4M3's zero
-
-
-def _scratch(what, ws, size: int, t: torch.Tensor) -> torch.Tensor:
-    """``_workspace`` on t's device."""
-    return t.new_empty(max(size, 256), dtype=torch.uint8) if ws is None else _workspace(what, ws, size, t.device)
 
 
 @functools.lru_cache(maxsize=1024)   # a function of the sizes alone
@@ -1227,8 +1223,8 @@ def fp8_forward(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, K: i
     what = "fp8_forward"
     dev, M, N, x, codes, scales = _fp8_args(what, x, codes, scales, K, (), False)
     bias = _arg("fp8_forward bias", bias, dev, (N,), None)
-    y = x.new_empty((M, N)) if out is None else _out("fp8_forward out", out, dev, (M, N), x.dtype)
-    ws = _scratch(what, ws, _lib.i8lt_fp8_workspace_size(M, K), x)
+    y = torch.empty((M, N), dtype=x.dtype, device=x.device) if out is None else _out("fp8_forward out", out, dev, (M, N), x.dtype)
+    ws = _workspace(what, ws, _lib.i8lt_fp8_workspace_size(M, K), x.device)
     _check(_on(dev, _lib.i8lt_fp8_forward, _ptr(x), _code(x.dtype), M, _ptr(codes), _ptr(scales), N, K, _ptr(bias),
                0 if bias is None else _code(bias.dtype), _ptr(y), ws.data_ptr(), ws.numel(), _stream(x)),
            "i8lt_fp8_forward")
@@ -1247,13 +1243,14 @@ def fp8_backward_input(G: torch.Tensor, codes: torch.Tensor, scales: torch.Tenso
     dev, M, N, G, codes, scales = _fp8_args(what, G, codes, scales, K, (), True)
     gx = gb = None
     if need_grad_A:
-        gx = G.new_empty((M, K)) if out is None else _out("fp8_backward_input out", out, dev, (M, K), G.dtype)
+        gx = torch.empty((M, K), dtype=G.dtype, device=G.device) if out is None else \
+            _out("fp8_backward_input out", out, dev, (M, K), G.dtype)
     if bias_dtype is not None:
-        gb = G.new_empty(N, dtype=bias_dtype)
+        gb = torch.empty(N, dtype=bias_dtype, device=G.device)
     if gx is None and gb is None:
         return None, None
     size = _lib.i8lt_fp8_workspace_size(M, N) + (_lib.i8lt_fp8_grad_bias_bytes(M, N) if gb is not None else 0)
-    ws = _scratch(what, ws, size, G)
+    ws = _workspace(what, ws, size, G.device)
     _check(_on(dev, _lib.i8lt_fp8_backward_input, _ptr(G), _code(G.dtype), M, _ptr(codes), _ptr(scales), N, K,
                _ptr(gx), _ptr(gb), 0 if gb is None else _code(bias_dtype), ws.data_ptr(), ws.numel(), _stream(G)),
            "i8lt_fp8_backward_input")
@@ -1269,8 +1266,8 @@ def _fp8_experts(what, call, t, codes, scales, K, offsets, transposed, out, ws):
     dev, M, N, t, codes, scales = _fp8_args(what, t, codes, scales, K, (E,), transposed)
     offsets = _arg(f"{what} offsets", offsets, dev, (E + 1,), torch.int32)
     shape = (M, K if transposed else N)
-    y = t.new_empty(shape) if out is None else _out(f"{what} out", out, dev, shape, t.dtype)
-    ws = _scratch(what, ws, _lib.i8lt_fp8_workspace_size(M, N if transposed else K), t)
+    y = torch.empty(shape, dtype=t.dtype, device=t.device) if out is None else _out(f"{what} out", out, dev, shape, t.dtype)
+    ws = _workspace(what, ws, _lib.i8lt_fp8_workspace_size(M, N if transposed else K), t.device)
     _check(_on(dev, call, _ptr(t), _code(t.dtype), M, _ptr(codes), _ptr(scales), E, N, K, _ptr(offsets),
                1 if out is None else 0, _ptr(y), ws.data_ptr(), ws.numel(), _stream(t)), f"i8lt_{what}")
     if out is not None:

@@ -68,8 +68,6 @@ def test_products():
         assert call(ws_bytes=need - 1) == WS
         if i > 1:
             assert call(offsets=None) == call(E=0) == call(E=1025) == call(out=None) == INVALID
-        if i != 1:
-            assert call(M=0, x=None, out=None) == OK
     assert fwd(bt=5) == DTYPE and fwd(out=None) == INVALID
     assert bwd(bt=5) == DTYPE and bwd(out=None, gb=None) == INVALID
 
