@@ -18,7 +18,7 @@ constexpr int kThreads = 256;
 constexpr int kPacks = 8;                          // 16-byte accesses of a thread and unit
 constexpr int kUnitBytes = kThreads * kPacks * 16;
 constexpr int kBlocks = 152 * 4;                   // at most, and so the partial sums of a call
-constexpr int kCluster = 8, kSmallGroups = 4, kClusterUnits = 64;    // gradients of 2 MB in all: one cluster, one launch
+constexpr int kCluster = 8, kSmallGroups = 2, kClusterUnits = 64;    // gradients of 2 MB in all: one cluster, one launch
 constexpr double kClipEps = 1e-6;
 
 // A list of tensors travels in the kernel's parameters.  A tensor's first
@@ -82,7 +82,24 @@ template <typename T>
 constexpr int kPack = 16 / sizeof(T);
 __device__ __forceinline__ double squares(float x) { return static_cast<double>(x) * static_cast<double>(x); }
 
-// One block's part of the sum of squares: the units [from, to).
+// The sum over the block, in thread 0 (elsewhere a part of it): every addition
+// that another thread need not make is left out, fp64 runs at 2 a clock and SM.
+template <int kWarps>
+__device__ __forceinline__ double block_total(double sum, double* sums) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const double other = __shfl_down_sync(0xffffffffu, sum, o);
+    if (lane < o) sum += other;
+  }
+  if (lane == 0) sums[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int i = 1; i < kWarps; ++i) sum += sums[i];
+  return sum;
+}
+
+// One block's part of the sum of squares, in thread 0: the units [from, to).
 // A thread sums the squares of 32 or 64 elements of a unit in fp32 and those
 // sums in fp64 (one fp64 addition for so many elements: the machine has few
 // fp64 units).  A sum so large or small that squares may have left fp32's
@@ -140,13 +157,7 @@ __device__ __forceinline__ double block_sum(const GradList<kCap>& L, int from, i
         }
       }
     });
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  double s = 0.0;
-  for (int i = 0; i < kGroups * kThreads / 32; ++i) s += sums[i];
-  return s;
+  return block_total<kGroups * kThreads / 32>(sum, sums);
 }
 
 struct Clip {
@@ -182,15 +193,8 @@ __global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double
   __shared__ double sums[kThreads / 32];
   double sum = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) sum += partial[i];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double s = 0.0;
-    for (int i = 0; i < kThreads / 32; ++i) s += sums[i];
-    write_result(c, s);
-  }
+  sum = block_total<kThreads / 32>(sum, sums);
+  if (threadIdx.x == 0) write_result(c, sum);
 }
 
 // Few gradients: one cluster, whose first block adds up the others' sums from
