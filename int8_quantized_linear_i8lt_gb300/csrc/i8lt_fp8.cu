@@ -329,16 +329,23 @@ __global__ void __launch_bounds__(256) fp8_sum_bias_kernel(const __grid_constant
   sum_bias(p, static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, static_cast<int64_t>(gridDim.x) * 256);
 }
 
-// 8 consecutive outputs (16 bytes) from output r on of a row.
-__device__ __forceinline__ void store_out8(const Product& p, int64_t m, int r, const uint4& v) {
-  uint16_t* dst = static_cast<uint16_t*>(p.out) + m * p.R + r;
-  if (p.vec && r + 8 <= p.R) {
-    *reinterpret_cast<uint4*>(dst) = v;
-  } else {
-    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+// 32 outputs from output r on of up to 32 rows, from a warp's shared memory
+// (rows of 64 bytes, 16-byte chunks permuted): whole sectors at a time, or, with
+// rows off 16-byte boundaries, a row at a time.
+__device__ __forceinline__ void write_rows(const Product& p, int row0, int rows, int r, const uint8_t* out_s, int lane) {
+  uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(row0) * p.R + r;
+  if (p.vec) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (r + k < p.R) dst[k] = static_cast<uint16_t>(q[k >> 1] >> (16 * (k & 1)));
+    for (int i = 0; i < 4; ++i) {
+      const int row = i * 8 + (lane >> 2), c = lane & 3;
+      const uint4 v = ld_shared_v4(out_s + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+      if (row < rows && r + 8 * c < p.R) *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row) * p.R + 8 * c) = v;
+    }
+  } else {
+    for (int row = 0; row < rows; ++row) {
+      const uint8_t* src = out_s + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + (lane & 7) * 2;
+      if (r + lane < p.R) out[static_cast<int64_t>(row) * p.R + lane] = *reinterpret_cast<const uint16_t*>(src);
+    }
   }
 }
 
@@ -649,7 +656,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const _
 constexpr int kThreads = 192;
 constexpr int kStoreBytes = 2048;    // per epilogue warp: 32 rows of 32 outputs on their way out
 constexpr int kMaxStages = 8;
-template <int kTileR>
+constexpr int kTileR = 64;           // outputs of a tile
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];
@@ -658,12 +665,11 @@ struct Shared {
   int abort;
   float bias[kEpiWarps][kTileR];
 };
-template <int kTileR>
 constexpr int small_smem(int stages) {
-  return 1024 + stages * (128 + kTileR) * 128 + kEpiWarps * kStoreBytes + static_cast<int>(sizeof(Shared<kTileR>));
+  return 1024 + stages * (128 + kTileR) * 128 + kEpiWarps * kStoreBytes + static_cast<int>(sizeof(Shared));
 }
 
-// Tiles of 128 tokens x kTileR outputs.  Warp 0 fetches, warp 1
+// Tiles of 128 tokens x 64 outputs.  Warp 0 fetches, warp 1
 // multiplies: one accumulator in TMEM per 128 columns of the reduction, two of
 // them in turn.  Warps 2 to 5 add each, times its two scales, to the sums that
 // they hold in registers: a thread has one token and kTileR outputs, so the
@@ -672,14 +678,14 @@ constexpr int small_smem(int stages) {
 // being quantized.  With few tiles a cluster of `split` CTAs shares a tile:
 // each has a part of the reduction, and the parts are added in the order of
 // the ranks.
-template <bool kT, int kTileR>
+template <bool kT>
 __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_constant__ Product p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Groups groups;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int kTileM = 128, x_bytes = kTileBytes, stage_bytes = x_bytes + kTileR * 128;
   const int stages = p.stages;
-  Shared<kTileR>& y = *reinterpret_cast<Shared<kTileR>*>(smem + stages * stage_bytes + kEpiWarps * kStoreBytes);
+  Shared& y = *reinterpret_cast<Shared*>(smem + stages * stage_bytes + kEpiWarps * kStoreBytes);
   volatile int* abort = &y.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -765,9 +771,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             umma_fp8(tmem + a * kTileR, make_sdesc(xa + 32 * k, 16, 1024, kSwizzle128B),
-                     !kT            ? make_sdesc(wa + 32 * k, 16, 1024, kSwizzle128B)
-                     : kTileR == 64 ? make_sdesc(wa + 2048 * k, 64 * 128, 512, kSwizzle64B)
-                                    : make_sdesc(wa + 4096 * k, kTileBytes, 1024, kSwizzle128B),
+                     kT ? make_sdesc(wa + 2048 * k, kTileR * 128, 512, kSwizzle64B)
+                        : make_sdesc(wa + 32 * k, 16, 1024, kSwizzle128B),
                      idesc, k > 0 ? 1u : 0u);
           umma_commit(&y.acc_full[a]);
           umma_commit(&y.empty[s]);
@@ -879,22 +884,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
           }
           __syncwarp();
           const int r = x.r0 + 32 * h;
-          uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(row0) * p.R + r;
-          if (p.vec) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = i * 8 + (lane >> 2), c = lane & 3;
-              const uint4 v = ld_shared_v4(out_s + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
-              if (row0 + row < last && r + 8 * c < p.R)
-                *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row) * p.R + 8 * c) = v;
-            }
-          } else {
-            const int rows = min(32, last - row0);
-            for (int row = 0; row < rows; ++row) {
-              const uint16_t v = *reinterpret_cast<const uint16_t*>(out_s + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + (lane & 7) * 2);
-              if (r + lane < p.R) out[static_cast<int64_t>(row) * p.R + lane] = v;
-            }
-          }
+          write_rows(p, row0, min(32, last - row0), r, out_s, lane);
           __syncwarp();
         }
         __syncwarp();
@@ -1228,12 +1218,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const
           }
         } else {
           __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = i * 8 + (lane >> 2), c = lane & 3;
-            const uint4 v = ld_shared_v4(out_s + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
-            if (row0 + row < x.end && r + c * 8 < p.R) store_out8(p, row0 + row, r + c * 8, v);
-          }
+          write_rows(p, row0, min(32, x.end - row0), r, out_s, lane);
         }
       }
       __syncwarp();
@@ -1332,40 +1317,49 @@ int launch_few(Product& p, const void* x, const void* w, int64_t extra, cudaStre
   return cuda_status(launch_after(fp8_product_few_kernel<kT, kN>, grid, kFewThreads, few_smem<kN>(), p.split, p, s));
 }
 
-template <bool kT, int kTileR>
+template <bool kT>
 int launch_small(Product& p, const void* x, const void* w, int64_t tiles, cudaStream_t s) {
   constexpr int kBudget = 111000;   // two CTAs an SM
   const int sms = sm_count();
   p.stages = kMaxStages;
-  while (p.stages > 2 && small_smem<kTileR>(p.stages) > kBudget) --p.stages;
+  while (p.stages > 2 && small_smem(p.stages) > kBudget) --p.stages;
   p.split = split_of(tiles, static_cast<int>(ceil_div(p.C, kBlk)), sms);
   if (!make_maps(p, kT, x, w, 128, kTileR)) return ST_CUDA;
   const int64_t grid = p.split > 1 ? tiles * p.split : std::min<int64_t>(tiles, 2 * sms);
-  return cuda_status(launch_after(fp8_product_kernel<kT, kTileR>, grid, kThreads, small_smem<kTileR>(p.stages), p.split, p, s));
+  return cuda_status(launch_after(fp8_product_kernel<kT>, grid, kThreads, small_smem(p.stages), p.split, p, s));
 }
 
+template <bool kT>
+int launch_wide(Product& p, const void* x, const void* w, int64_t tiles, cudaStream_t s) {
+  if (!make_maps(p, kT, x, w, 128, 128)) return ST_CUDA;
+  if (p.vec && !make_tmap(&p.tmOut, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.out, p.R,
+                          p.M, static_cast<uint64_t>(p.R) * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    return ST_CUDA;
+  return cuda_status(launch_after(fp8_product_wide_kernel<kT>, std::min<int64_t>(tiles, sm_count()), kWideThreads,
+                                  kWideSmemBytes, 1, p, s));
+}
+
+// The kernel by sizes (times of a call, K = 4096, weights in L2):
+//   up to 64 tokens a weight: the weight as first operand, the smallest tile
+//     that has them.  N = 11008, 16 tokens: 15 us, tiles of 32 tokens 15, of 64
+//     19, small products 33, wide 21; 64 tokens: 20, small 24, wide 21.  With
+//     few tiles of 64 tokens, tiles of 32: N = 4096, 64 tokens: 18 and 13 us.
+//   more: wide tiles as soon as the small ones would give every SM one.
+//     128 tokens, N = 4096 (64 small tiles): small 15 us, wide 21; N = 11008
+//     (172): 25 and 21; 512 tokens, N = 4096 (256): 27 and 23; 1024 tokens,
+//     N = 11008: 95 and 55.  Experts of 64 tokens each, N = 2048: 44 and 35.
 template <bool kT>
 int launch_product(Product& p, const void* x, const void* w, cudaStream_t s) {
   const int sms = sm_count();
   const int64_t extra = p.offsets == nullptr ? 0 : p.E;   // experts' last tiles, at most
-  const int mean = p.M / p.E;
-  const int64_t wide = (ceil_div(p.M, 128) + extra) * ceil_div(p.R, 256);
-  if (mean >= 256 && wide >= sms) {
-    if (!make_maps(p, kT, x, w, 128, 128)) return ST_CUDA;
-    if (p.vec && !make_tmap(&p.tmOut, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.out,
-                            p.R, p.M, static_cast<uint64_t>(p.R) * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
-      return ST_CUDA;
-    return cuda_status(launch_after(fp8_product_wide_kernel<kT>, std::min<int64_t>(wide, sms), kWideThreads,
-                                    kWideSmemBytes, 1, p, s));
-  }
   // experts' shares differ: tiles of up to twice the mean
-  const int most = p.offsets == nullptr ? p.M : 2 * mean;
+  const int most = p.offsets == nullptr ? p.M : 2 * (p.M / p.E);
   if (most <= 16) return launch_few<kT, 16>(p, x, w, extra, s);
-  if (most <= 32) return launch_few<kT, 32>(p, x, w, extra, s);
+  if (most <= 32 || (most <= 64 && extra == 0 && p.R < 64 * 128)) return launch_few<kT, 32>(p, x, w, extra, s);
   if (most <= 64) return launch_few<kT, 64>(p, x, w, extra, s);
-  const int64_t num_m = ceil_div(p.M, 128) + extra;
-  if (num_m * ceil_div(p.R, 128) >= 2 * sms) return launch_small<kT, 128>(p, x, w, num_m * ceil_div(p.R, 128), s);
-  return launch_small<kT, 64>(p, x, w, num_m * ceil_div(p.R, 64), s);
+  const int64_t num_m = ceil_div(p.M, 128) + extra, small = num_m * ceil_div(p.R, kTileR);
+  if (small >= sms) return launch_wide<kT>(p, x, w, num_m * ceil_div(p.R, 256), s);
+  return launch_small<kT>(p, x, w, small, s);
 }
 
 constexpr size_t kAlign = 256;

@@ -57,7 +57,8 @@ def test_quantize_weight(N, K, dtype):
 
 SIZES = [(1, 1, 1), (1, 128, 128), (2, 130, 127), (3, 16, 8), (1, 4096, 520), (17, 300, 200), (128, 256, 128),
          (129, 384, 257), (64, 2048, 1024), (300, 1000, 1000), (513, 640, 640), (777, 1100, 519), (1025, 512, 1536),
-         (2300, 300, 2600), (2600, 2310, 280)]
+         (2300, 300, 2600), (2600, 2310, 280),
+         (40, 520, 260), (64, 256, 8200), (33, 8200, 130), (200, 130, 9001)]
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
