@@ -179,6 +179,70 @@ def test_not_finite():
     assert y[:, 128:].isnan().all() and torch.equal(y[rest][:, :128], clean[rest][:, :128])
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("M,K,N", [(1, 300, 39200), (16, 9001, 130), (7, 1111, 520), (16, 2056, 4100), (5, 136, 40001)])
+def test_few_tokens(M, K, N, dtype):
+    """Several tiles a CTA, many blocks a CTA, rows on no 16 bytes; a bias gradient
+    beside it changes no bit of the product."""
+    x, W = tokens(M, K, dtype, 31), weights(N, K, 32)
+    q, s = I.fp8_quantize_weight(W.cuda())
+    y = I.fp8_forward(x.cuda(), q, s, K)
+    ref, size = R.product(x, R.expand_weight(*R.weight(W)))
+    R.check(y, ref, size, K, "y")
+    G = tokens(M, N, dtype, 33).cuda()
+    assert torch.equal(I.fp8_backward_input(G, q, s, K)[0], I.fp8_backward_input(G, q, s, K, bias_dtype=F32)[0])
+
+
+def test_few_rows_of_an_uneven_share():
+    M, K, N, E = 500, 200, 130, 64
+    W = torch.stack([weights(N, K, 40 + e) for e in range(E)])
+    q, s = I.fp8_quantize_weight(W.cuda())
+    cuts = [0, 0, 3] + [403] * 20 + list(range(404, 404 + 40)) + [450, 490]
+    off = torch.tensor(cuts, dtype=torch.int32)
+    assert len(cuts) == E + 1
+    for transposed in (False, True):
+        x = tokens(M, N if transposed else K, F16, 34)
+        call = I.fp8_experts_backward_input if transposed else I.fp8_experts_forward
+        y = call(x.cuda(), q, s, K, off.cuda())
+        assert not y[490:].any()
+        for e in range(E):
+            a, b = cuts[e], cuts[e + 1]
+            if a < b:
+                ref, size = R.product(x[a:b], R.expand_weight(*R.weight(W[e])), transposed=transposed)
+                R.check(y[a:b], ref, size, x.shape[1], f"expert {e}")
+
+
+@pytest.mark.parametrize("M", [3, 16, 40, 300])
+def test_output_over_its_input(M):
+    K = 384
+    q, s = I.fp8_quantize_weight(weights(K, K, 35).cuda())
+    x = tokens(M, K, BF16, 36).cuda()
+    y = I.fp8_forward(x, q, s, K)
+    assert torch.equal(I.fp8_forward(x, q, s, K, out=x), y) and torch.equal(x, y)
+
+
+def test_few_tokens_captured_on_two_streams():
+    K, N = 1024, 640
+    q, s = I.fp8_quantize_weight(weights(N, K, 37).cuda())
+    x = torch.zeros(4, K, dtype=F16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        I.fp8_forward(x, q, s, K)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            x.add_(1)                                # the product sees what the kernel before it wrote
+            outs.append(I.fp8_forward(x, q, s, K))
+    x.copy_(tokens(4, K, F16, 38))
+    for _ in range(3):
+        for graph, out in zip(graphs, outs):
+            graph.replay()
+            assert torch.equal(out, I.fp8_forward(x, q, s, K))
+
+
 def test_linear_on_the_grid_has_exact_differences():
     """Values the codes hold exactly: the layer is linear between them, and
     <g, f(x + e) - f(x)> = <gx, e>."""
