@@ -692,7 +692,8 @@ int i8lt_scale_grads(void* const* grads, const int32_t* dtypes,
  *   ws   i8lt_fp8_workspace_size(M, C) bytes, 256-byte aligned, status word
  *        first, C the reduction (K forward, N backward); with grad_bias,
  *        i8lt_fp8_grad_bias_bytes(M, N) more
- * out may not overlap an input.
+ * out may not overlap an input.  Tokens, codes and outputs are 16-byte
+ * aligned; scales, offsets, bias and grad_bias to their elements.
  */
 #define I8LT_FP8_MAX_EXPERTS 512
 int64_t i8lt_fp8_ld(int64_t C);

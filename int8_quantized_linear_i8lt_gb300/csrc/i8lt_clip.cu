@@ -372,7 +372,9 @@ int i8lt_grad_norm(const void* const* grads, const int32_t* dtypes, const int64_
   if (int e = check_list(g, dtypes, sizes, count)) return e;
   if (!(max_norm >= 0.0) || result == nullptr) return ST_INVALID_ARG;
   if (ws == nullptr || ws_bytes < i8lt_grad_norm_workspace_size()) return ST_WORKSPACE;
-  if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0 || (reinterpret_cast<uintptr_t>(result) & 3) != 0) return ST_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0) return ST_MISALIGNED;
+  for (const float* p : {static_cast<const float*>(result), grad_scale, found_inf})
+    if ((reinterpret_cast<uintptr_t>(p) & 3) != 0) return ST_MISALIGNED;
   if (int d = check_device()) return d;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   double* partial = static_cast<double*>(ws);

@@ -1377,6 +1377,8 @@ int launch_product(Product& p, const void* x, const void* w, cudaStream_t s) {
 
 constexpr size_t kAlign = 256;
 size_t align_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
+bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+int elem_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & (kAlign - 1)) == 0; }
 constexpr int64_t kMaxSize = INT32_MAX / 2;
 
@@ -1396,6 +1398,9 @@ int product(bool transposed, const void* x, int xt, int64_t M, const uint8_t* co
   if (codes == nullptr || scales == nullptr) return ST_INVALID_ARG;
   if (M > 0 && (x == nullptr || (out == nullptr && grad_bias == nullptr))) return ST_INVALID_ARG;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(out)) return ST_MISALIGNED;
+  if (!aligned_to(scales, 4) || !aligned_to(offsets, 4) || !aligned_to(bias, elem_bytes(bt)) ||
+      !aligned_to(grad_bias, elem_bytes(bt)))
+    return ST_MISALIGNED;
   if (ws == nullptr) return ST_WORKSPACE;
   if (!aligned256(ws)) return ST_MISALIGNED;
   const size_t partial_bytes = grad_bias != nullptr ? i8lt_fp8_grad_bias_bytes(M, N) : 0;
@@ -1459,7 +1464,7 @@ int i8lt_fp8_quantize(const void* x, int xt, int64_t M, int64_t C, uint8_t* code
   if (M < 0 || C < 0 || M > kMaxSize || C > kMaxSize) return ST_INVALID_ARG;
   if (M == 0 || C == 0) return ST_OK;
   if (x == nullptr || codes == nullptr || scales == nullptr) return ST_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(codes)) return ST_MISALIGNED;
+  if (!aligned16(x) || !aligned16(codes) || !aligned_to(scales, 4)) return ST_MISALIGNED;
   if (int d = check_device()) return d;
   return cuda_status(launch_quantize(x, xt, M, C, codes, scales, nullptr, nullptr, static_cast<cudaStream_t>(stream)));
 }
@@ -1470,7 +1475,7 @@ int i8lt_fp8_quantize_weight(const void* W, int wt, int64_t E, int64_t N, int64_
   if (!sizes_ok(E, N, K)) return ST_INVALID_ARG;
   if (E == 0 || N == 0 || K == 0) return ST_OK;
   if (W == nullptr || codes == nullptr || scales == nullptr) return ST_INVALID_ARG;
-  if (!aligned16(W) || !aligned16(codes)) return ST_MISALIGNED;
+  if (!aligned16(W) || !aligned16(codes) || !aligned_to(scales, 4)) return ST_MISALIGNED;
   if (ceil_div(N, kBlk) > 65535) return ST_INVALID_ARG;
   if (int d = check_device()) return d;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1491,7 +1496,7 @@ int i8lt_fp8_dequantize_weight(const uint8_t* codes, const float* scales, int64_
   if (!sizes_ok(E, N, K)) return ST_INVALID_ARG;
   if (E == 0 || N == 0 || K == 0) return ST_OK;
   if (codes == nullptr || scales == nullptr || out == nullptr) return ST_INVALID_ARG;
-  if (!aligned16(codes) || !aligned16(out)) return ST_MISALIGNED;
+  if (!aligned16(codes) || !aligned16(out) || !aligned_to(scales, 4)) return ST_MISALIGNED;
   if (int d = check_device()) return d;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t rows = E * N;

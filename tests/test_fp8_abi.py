@@ -72,10 +72,11 @@ def test_products():
     assert bwd(bt=5) == DTYPE and bwd(out=None, gb=None) == INVALID
 
 
-def clip(grads=(P, P + 4096), dtypes=(0, 2), sizes=(5, 300), count=None, max_norm=1.0, result=P, ws=P, ws_bytes=BIG):
+def clip(grads=(P, P + 4096), dtypes=(0, 2), sizes=(5, 300), count=None, max_norm=1.0, result=P, ws=P, ws_bytes=BIG,
+         grad_scale=None, found_inf=None):
     n = len(grads)
     lists = ((ctypes.c_void_p * n)(*grads), (ctypes.c_int32 * n)(*dtypes), (ctypes.c_int64 * n)(*sizes))
-    return _lib.i8lt_grad_norm(*lists, n if count is None else count, None, None, max_norm, result, ws, ws_bytes)
+    return _lib.i8lt_grad_norm(*lists, n if count is None else count, grad_scale, found_inf, max_norm, result, ws, ws_bytes)
 
 
 def scale(grads=(P, P + 4096), dtypes=(0, 2), sizes=(5, 300), count=None, factor=P):
@@ -100,3 +101,15 @@ def test_gradients_that_overlap_are_not_scaled():
     assert scale(grads=(P, P)) == INVALID
     assert scale(grads=(P, P + 8), dtypes=(0, 0)) == INVALID          # 5 elements of 2 bytes end at P + 10
     assert scale(grads=(P + 1196, P), dtypes=(0, 2)) == INVALID       # 300 of 4 bytes end at P + 1200
+
+
+def test_small_operands_are_aligned_to_their_elements():
+    """A scale, an offset or a bias that starts inside an element would fault on the device."""
+    assert _lib.i8lt_fp8_quantize(P, 0, 4, 8, P, P + 2) == ALIGN
+    assert _lib.i8lt_fp8_quantize_weight(P, 0, 2, 4, 8, P, P + 2) == ALIGN
+    assert _lib.i8lt_fp8_dequantize_weight(P, P + 1, 2, 4, 8, P, 0) == ALIGN
+    assert fwd(scales=P + 2) == fwd(bias=P + 1) == fwd(bias=P + 2, bt=2) == ALIGN
+    assert bwd(scales=P + 1) == bwd(gb=P + 1) == bwd(gb=P + 2, bt=2) == ALIGN
+    for call in (_lib.i8lt_fp8_experts_forward, _lib.i8lt_fp8_experts_backward_input):
+        assert experts(call, scales=P + 2) == experts(call, offsets=P + 2) == ALIGN
+    assert clip(grad_scale=P + 2) == clip(found_inf=P + 1) == ALIGN
