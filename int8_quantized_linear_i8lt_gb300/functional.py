@@ -1107,6 +1107,9 @@ def scale_grads_(grads, scale: torch.Tensor) -> None:
     if not grads:
         return
     if not all(map(_is_contiguous, grads)):
+        # refused before any of them has been scaled
+        if any(0 in g.stride() and any(s == 0 and n > 1 for s, n in zip(g.stride(), g.shape)) for g in grads):
+            raise I8LTError("scale_grads_: an expanded tensor, whose elements share memory")
         dense = [g.contiguous() for g in grads]
     held, dev, n, at = _grad_lists("scale_grads_", dense)
     _adamw_scalar("scale_grads_", scale, grads[0].device)

@@ -191,3 +191,16 @@ def test_refusals():
             call()
     I.scale_grads_([], torch.ones(1).cuda())
     I.scale_grads_([None], torch.ones(1).cuda())
+
+
+def test_an_expanded_gradient_is_refused_before_any_is_scaled():
+    a = torch.ones(40, device="cuda")
+    wide = torch.ones(1, 8, device="cuda").expand(5, 8)
+    with pytest.raises(I.I8LTError, match="expanded"):
+        I.scale_grads_([a, wide], torch.full((), 0.5, device="cuda"))
+    assert bool((a == 1).all()) and bool((wide == 1).all())
+    norm = I.grad_norm([a, wide])[0]                 # it may be read
+    assert abs(norm.item() - 80 ** 0.5) <= 80 ** 0.5 * 2.0 ** -22
+    column = torch.ones(6, 3, device="cuda")[:, 1:2]     # a step of 0 along one element is no sharing
+    I.scale_grads_([column], torch.full((), 0.5, device="cuda"))
+    assert bool((column == 0.5).all())
