@@ -212,7 +212,7 @@ def test_few_rows_of_an_uneven_share():
                 R.check(y[a:b], ref, size, x.shape[1], f"expert {e}")
 
 
-def test_few_tokens_captured_on_two_streams():
+def test_few_tokens_in_two_graphs():
     K, N = 1024, 640
     q, s = I.fp8_quantize_weight(weights(N, K, 37).cuda())
     x = torch.zeros(4, K, dtype=F16, device="cuda")
@@ -308,6 +308,72 @@ def test_views_streams_and_workspaces():
     assert torch.equal(y, z)
     ws = torch.empty(_lib.i8lt_fp8_workspace_size(69, 160), dtype=torch.uint8, device="cuda").fill_(255)
     assert torch.equal(y, I.fp8_forward(flat, q, s, 160, ws=ws)) and I.device_status(ws)[0] == 0
+
+
+def test_offsets_beyond_32_bits():
+    """Tokens of 2^31 elements and more, forward and back, and experts' codes of
+    as many bytes: the last rows and the last expert."""
+    M, K, N = 265000, 8192, 160
+    q, s = I.fp8_quantize_weight(weights(N, K, 50).cuda())
+    x = torch.zeros(M, K, dtype=BF16, device="cuda")
+    x[-200:] = tokens(200, K, BF16, 51).cuda()
+    y = I.fp8_forward(x, q, s, K)
+    assert torch.equal(y[-200:], I.fp8_forward(x, q, s, K)[-200:]) and not y[:-200].any()
+    ref, size = R.product(x[-200:].cpu(), R.expand_weight(*R.weight(weights(N, K, 50))))
+    R.check(y[-200:], ref, size, K, "y")
+    del x
+    G = torch.zeros(M, N, dtype=BF16, device="cuda")
+    G[-200:] = tokens(200, N, BF16, 52).cuda()
+    gx = I.fp8_backward_input(G, q, s, K)[0]
+    ref, size = R.product(G[-200:].cpu(), R.expand_weight(*R.weight(weights(N, K, 50))), transposed=True)
+    R.check(gx[-200:], ref, size, N, "gx")
+    assert not gx[:100].any() and not gx[-300:-200].any()
+    del gx, G
+    E, N, K = 130, 4096, 4200                        # 130 x 4096 x 4208 codes
+    last = weights(N, K, 53)
+    W = torch.zeros(E, N, K, dtype=BF16, device="cuda")
+    W[-1] = last.cuda()
+    q, s = I.fp8_quantize_weight(W)
+    assert q.numel() > 2 ** 31
+    for rows in (3, 200):
+        x = tokens(rows, K, BF16, 54)
+        off = torch.tensor([0] * E + [rows], dtype=torch.int32).cuda()
+        y = I.fp8_experts_forward(x.cuda(), q, s, K, off)
+        ref, size = R.product(x, R.expand_weight(*R.weight(last.to(BF16))))
+        R.check(y, ref, size, K, f"{rows} rows")
+
+
+def test_two_threads_at_once():
+    """Calls from two threads on streams of their own share nothing."""
+    import threading
+    sizes = [(5, 2048, 1500), (300, 640, 900), (2600, 512, 1800), (40, 1100, 260)]
+    work = []
+    for i, (M, K, N) in enumerate(sizes):
+        q, s = I.fp8_quantize_weight(weights(N, K, 60 + i).cuda())
+        x, G = tokens(M, K, F16, 70 + i).cuda(), tokens(M, N, F16, 80 + i).cuda()
+        call = lambda x=x, G=G, q=q, s=s, K=K: (I.fp8_forward(x, q, s, K),
+                                                *I.fp8_backward_input(G, q, s, K, bias_dtype=F32),
+                                                *I.grad_norm([x, G], 1.0))
+        work.append((call, call()))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(order):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                for i in order:
+                    call, expect = work[i]
+                    if not all(torch.equal(a, b) for a, b in zip(call(), expect)):
+                        wrong.append(i)
+        stream.synchronize()
+
+    threads = [threading.Thread(target=run, args=(order,)) for order in ([0, 1, 2, 3], [2, 3, 1, 0])]
+    for thread in threads:
+        thread.start()
+    for thread in threads:
+        thread.join()
+    assert not wrong
 
 
 def test_captured_and_replayed():
