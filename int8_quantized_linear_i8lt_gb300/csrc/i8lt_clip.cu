@@ -19,7 +19,7 @@ constexpr int kPacks = 8;                          // 16-byte accesses of a thre
 constexpr int kUnitBytes = kThreads * kPacks * 16;
 constexpr int kBlocks = 152 * 4;                   // at most, and so the partial sums of a call
 constexpr int kCluster = 8, kSmallGroups = 2, kClusterUnits = 64;    // gradients of 2 MB in all: one cluster, one launch
-constexpr float kClipEps = 1e-6f;
+constexpr double kClipEps = 1e-6;
 
 // A list of tensors travels in the kernel's parameters.  A tensor's first
 // elements, up to a 16-byte boundary, belong to its first unit; units start on
@@ -163,28 +163,21 @@ __device__ __forceinline__ double block_sum(const GradList<kCap>& L, int from, i
 
 struct Clip {
   const float *grad_scale, *found_inf;
-  float max_norm;
+  double max_norm;
   float* result;
 };
 
-// In fp32 (a double's square root and division take 4 us here): s = m 4^k with
-// 1 <= m < 4, so that norm = sqrt(m) 2^k, off by less than a step of fp32.
+// In fp64, each result rounded once: neither the norm without c nor c need keep
+// the product inside fp32's range (1e39 times 2^-16).
 __device__ __forceinline__ void write_result(const Clip& c, double s) {
-  float norm;
-  const int hi = __double2hiint(s), e = ((hi >> 20) & 0x7ff) - 1023;
-  if (s > 0.0 && e < 1024) {   // no sum of squares of fp32 numbers is below double's normal ones
-    const int k = e >> 1;
-    const float m = static_cast<float>(__hiloint2double(hi - ((2 * k) << 20), __double2loint(s)));
-    norm = ldexpf(__fsqrt_rn(m), k);
-  } else {
-    norm = static_cast<float>(s);   // 0, infinity, NaN
-  }
   const float f = c.grad_scale != nullptr ? *c.grad_scale : 1.f;
-  norm = __fmul_rn(fabsf(f), norm);
-  const float q = __fdiv_rn(c.max_norm, __fadd_rn(norm, kClipEps));
-  c.result[0] = norm;
-  c.result[1] = q >= 1.f || c.max_norm == INFINITY ? f : __fmul_rn(f, q);   // a NaN stays one
-  c.result[2] = isfinite(norm) && (c.found_inf == nullptr || *c.found_inf == 0.f) ? 0.f : 1.f;
+  const bool found = c.found_inf != nullptr && *c.found_inf != 0.f;
+  const double norm = __dmul_rn(fabs(static_cast<double>(f)), sqrt(s));
+  const float norm32 = static_cast<float>(norm);
+  const double q = isinf(norm32) ? 0.0 : c.max_norm / (norm + kClipEps);
+  c.result[0] = norm32;
+  c.result[1] = q >= 1.0 || isinf(c.max_norm) ? f : static_cast<float>(f * q);   // a NaN stays one
+  c.result[2] = isfinite(norm32) && !found ? 0.f : 1.f;
 }
 
 template <int kCap>
@@ -378,7 +371,7 @@ int i8lt_grad_norm(const void* const* grads, const int32_t* dtypes, const int64_
   if (int d = check_device()) return d;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   double* partial = static_cast<double*>(ws);
-  const Clip c{grad_scale, found_inf, static_cast<float>(max_norm), result};
+  const Clip c{grad_scale, found_inf, max_norm, result};
   return cuda_status(count <= kFewTensors ? norm_lists<kFewTensors>(g, dtypes, sizes, count, c, partial, s)
                                           : norm_lists<kMaxTensors>(g, dtypes, sizes, count, c, partial, s));
 }

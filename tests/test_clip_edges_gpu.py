@@ -1,0 +1,51 @@
+"""The gradient norm, scaling and clipping where they are easily wrong: the ends
+of fp32's range, zeros, views that share memory."""
+import math
+
+import pytest
+import torch
+
+import int8_quantized_linear_i8lt_gb300 as I
+
+pytestmark = pytest.mark.gpu
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+# 32 squares summed in fp32 (each rounded, up to 32 additions), the rest in
+# fp64: 33 half steps of the sum of squares, half of that of the norm; and the
+# rounding to fp32
+NORM_TOL = (33 / 2 + 1) * 2.0 ** -24
+
+
+def norm64(ts):
+    return math.sqrt(math.fsum(float((t.double() ** 2).sum()) for t in ts))
+
+
+@pytest.mark.parametrize("n", [3000, 1000000])
+@pytest.mark.parametrize("size,c", [(3e38, 2.0 ** -16), (3e38, 2.0 ** -60), (2.0 ** -146, 2.0 ** 30), (2.0 ** -149, 2.0 ** 100)])
+def test_grad_scale_at_the_ends_of_the_range(n, size, c):
+    """|c| times the root is rounded once: the norm of the gradients as they are
+    may leave fp32's range, above or below."""
+    t = torch.full((n,), size, device="cuda")
+    norm, scale, inf = I.grad_norm([t], max_norm=1.0, grad_scale=torch.tensor([c], device="cuda"))
+    ref = c * norm64([t])
+    assert math.isfinite(ref) and 2.0 ** -126 < ref < 3e38
+    assert abs(float(norm) - ref) <= ref * NORM_TOL and float(inf) == 0
+    expect = c * min(1.0, 1.0 / (ref + 1e-6))
+    assert abs(float(scale) - expect) <= expect * (NORM_TOL + 2.0 ** -24) + 2.0 ** -150
+
+
+def test_a_norm_beyond_the_range_after_scaling():
+    t = torch.full((100000,), 3e38, device="cuda")
+    norm, scale, inf = I.grad_norm([t], max_norm=1.0, grad_scale=torch.tensor([0.5], device="cuda"))
+    assert float(norm) == math.inf and float(scale) == 0 and float(inf) == 1
+
+
+def test_results_are_rounded_once():
+    """Two numbers whose squares and their sum are exact leave only the roundings
+    of the norm and of the factor, from 64 bits."""
+    for a, b, limit, c in ((3.0, 1.0, 0.7, 1.0), (5.0, 2.0, 3.3, 0.3), (1.0, 1.0, 1.0, 1.0), (4095.0, 77.0, 1e-3, 7e-5)):
+        t, k = torch.tensor([a, b], device="cuda"), torch.tensor([c], device="cuda")
+        norm, scale, _ = I.grad_norm([t], max_norm=limit, grad_scale=k)
+        ref = float(k) * math.sqrt(a * a + b * b)
+        assert float(norm) == float(torch.tensor(ref, dtype=torch.float64).float())
+        expect = float(k) * min(1.0, limit / (ref + 1e-6))
+        assert float(scale) == float(torch.tensor(expect, dtype=torch.float64).float())
