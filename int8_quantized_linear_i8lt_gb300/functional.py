@@ -1099,10 +1099,51 @@ def grad_norm(grads, max_norm: float | None = None, grad_scale: torch.Tensor | N
     return norm, scale, inf
 
 
+def _apart(a: int, A: list, b: int, B: list) -> bool:
+    """Whether two views share no byte, as far as their layout shows it: a and b
+    are where they start, A and B their (step, count) in bytes, the largest
+    step first and an element's bytes as (1, bytes) last.  Both are folded to
+    what lies between two of the largest steps, as long as neither crosses one."""
+    span = lambda dims: sum([step * (count - 1) for step, count in dims]) + 1
+    if a + span(A) <= b or b + span(B) <= a:
+        return True
+    step = max(A[0][0], B[0][0])
+    if step == 1:
+        return False
+    A, B = ([d for d in dims if d[0] != step] for dims in (A, B))
+    for x, X, y, Y in ((a, A, b, B), (b, B, a, A)):
+        at = (y - x) % step
+        if span(X) <= step and at + span(Y) <= step:
+            return _apart(0, X, at, Y)
+    return False
+
+
+def _require_apart(what, ts) -> None:
+    """Refuses tensors of which two may share memory.  Pairs of contiguous ones
+    are left to the library."""
+    views = []
+    for t in ts:
+        if t.numel():
+            size = t.element_size()
+            dims = sorted([(s * size, n) for s, n in zip(t.stride(), t.shape) if n > 1], reverse=True) + [(1, size)]
+            start = t.data_ptr()
+            views.append((start, start + sum([s * (n - 1) for s, n in dims]) + 1, dims, t.is_contiguous()))
+    views.sort(key=lambda v: v[0])
+    open_ = []
+    for v in views:
+        open_ = [o for o in open_ if o[1] > v[0]]
+        for o in open_:
+            if not (o[3] and v[3]) and not _apart(o[0], o[2], v[0], v[2]):
+                raise I8LTError(f"{what}: two tensors that share memory, or lie between one another in a way that does not "
+                                "show that they share none")
+        open_.append(v)
+
+
 def scale_grads_(grads, scale: torch.Tensor) -> None:
     """Multiply all ``grads`` (None is left out) by the fp32 device scalar
     ``scale``, in place (i8lt_scale_grads); a scale of 1 moves nothing.  None
-    may overlap another one."""
+    may overlap another one; columns and steps of one matrix may lie between
+    one another."""
     grads = dense = _present(grads)
     if not grads:
         return
@@ -1110,6 +1151,7 @@ def scale_grads_(grads, scale: torch.Tensor) -> None:
         # refused before any of them has been scaled
         if any(0 in g.stride() and any(s == 0 and n > 1 for s, n in zip(g.stride(), g.shape)) for g in grads):
             raise I8LTError("scale_grads_: an expanded tensor, whose elements share memory")
+        _require_apart("scale_grads_", grads)
         dense = [g.contiguous() for g in grads]
     held, dev, n, at = _grad_lists("scale_grads_", dense)
     _adamw_scalar("scale_grads_", scale, grads[0].device)

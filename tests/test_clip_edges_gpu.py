@@ -49,3 +49,32 @@ def test_results_are_rounded_once():
         assert float(norm) == float(torch.tensor(ref, dtype=torch.float64).float())
         expect = float(k) * min(1.0, limit / (ref + 1e-6))
         assert float(scale) == float(torch.tensor(expect, dtype=torch.float64).float())
+
+
+def test_scaled_views_that_share_memory_are_refused():
+    """Each is scaled through a copy of its own, so one of two scalings would be lost."""
+    half = torch.full((), 0.5, device="cuda")
+    m = torch.ones(6, 8, device="cuda")
+    flat = m.view(-1)
+    for views in ([m[:, ::2], m], [m, m[:, ::2]], [m[:, ::2], m[:, ::2]], [m[:, :5], m[:, 4:]], [m[1:, ::2], flat[12:15]],
+                  [m.T, m], [m.T, m.T], [m[:, 1:3], m[2:4, 2:5]], [m[:, ::3], m[:, 1::2]]):
+        with pytest.raises(I.I8LTError, match="share"):
+            I.scale_grads_(views, half)
+        assert bool((m == 1).all())
+
+
+def test_scaled_views_beside_one_another():
+    half = torch.full((), 0.5, device="cuda")
+    cases = (((6, 8), lambda m: [m[:, ::2], m[:, 1::2]]), ((6, 7), lambda m: [m[:, ::2], m[:, 1::2]]),
+             ((6, 7), lambda m: [m[:, 4:], m[:, :2], m[:, 2:3]]), ((6, 8), lambda m: [m[::2], m[1::2, 3:], m[1::2, :2]]),
+             ((6, 8), lambda m: [m[:, ::2], m.view(-1)[9:10], m.view(-1)[15:16]]),
+             ((3, 5, 4), lambda m: [m[:, :2, 1:], m[:, :2, :1], m[:, 2:, ::2], m[1:, 4, 1:2]]),
+             ((8, 9), lambda m: [m[:4].T, m[4:, ::2]]), ((5, 6), lambda m: [m[:0, ::2], m[:, 1:1], m[:, ::5]]))
+    for shape, views in cases:
+        for dtype in (F32, F16, BF16):
+            m = torch.randn(shape, device="cuda").to(dtype)
+            expect = m.clone()
+            for v in views(expect):
+                v.mul_(0.5)
+            I.scale_grads_(views(m), half)
+            assert torch.equal(m, expect)
