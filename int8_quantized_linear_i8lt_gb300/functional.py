@@ -1157,9 +1157,10 @@ def scale_grads_(grads, scale: torch.Tensor) -> None:
     _adamw_scalar("scale_grads_", scale, grads[0].device)
     _check(_on(dev, _lib.i8lt_scale_grads, *at, n, scale.data_ptr(), _stream(grads[0])), "i8lt_scale_grads")
     if dense is not grads:
-        for g, d in zip(grads, dense):
-            if d is not g:
-                g.copy_(d)
+        with torch.no_grad():   # as the kernel's own writes: also into leaves
+            for g, d in zip(grads, dense):
+                if d is not g:
+                    g.copy_(d)
     _written(grads)
 
 

@@ -78,3 +78,20 @@ def test_scaled_views_beside_one_another():
                 v.mul_(0.5)
             I.scale_grads_(views(m), half)
             assert torch.equal(m, expect)
+
+
+def test_tensors_that_require_a_gradient_are_scaled_in_any_layout():
+    half = torch.full((), 0.5, device="cuda")
+    dense = torch.nn.Parameter(torch.ones(5, device="cuda"))
+    loose = torch.nn.Parameter(torch.ones(4, 6, device="cuda").T)
+    assert not loose.is_contiguous()
+    versions = dense._version, loose._version
+    I.scale_grads_([dense, loose], half)
+    assert bool((dense == 0.5).all()) and bool((loose == 0.5).all()) and loose.is_leaf and loose.requires_grad
+    assert dense._version > versions[0] and loose._version > versions[1]
+    p = torch.nn.Parameter(torch.ones(6, 4, device="cuda"))
+    p.grad = (torch.ones(4, 6, device="cuda", requires_grad=True) * 1).T     # a gradient with a history
+    assert p.grad.requires_grad and not p.grad.is_contiguous()
+    norm = I.clip_grad_norm_(p, 1.0)
+    f = I.grad_norm([torch.ones(24, device="cuda")], 1.0)[1]
+    assert abs(float(norm) - 24 ** 0.5) <= 1e-5 and bool((p.grad == f).all())
