@@ -640,7 +640,8 @@ int i8lt_adamw_step_8bit_counted(void* const* params, int pt,
  * (and alignments) give equal bits.
  *
  * i8lt_scale_grads: g *= *scale in place, rounded once, over all tensors
- * (none may overlap another; a device scale of 1 reads and writes nothing).
+ * (none may overlap another or the scale; a device scale of 1 reads and writes
+ * nothing).
  */
 size_t i8lt_grad_norm_workspace_size(void);
 int i8lt_grad_norm(const void* const* grads, const int32_t* dtypes,

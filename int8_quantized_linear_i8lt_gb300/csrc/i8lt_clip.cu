@@ -384,13 +384,15 @@ int i8lt_scale_grads(void* const* grads, const int32_t* dtypes, const int64_t* s
   // one launch scales all of them at once: none may share memory with another
   try {
     std::vector<std::pair<uintptr_t, uintptr_t>> spans;
-    spans.reserve(static_cast<size_t>(count));
+    spans.reserve(static_cast<size_t>(count) + 1);
     for (int64_t i = 0; i < count; ++i)
       if (grads[i] != nullptr && sizes[i] > 0) {
         const uintptr_t a = reinterpret_cast<uintptr_t>(grads[i]);
         spans.emplace_back(a, a + static_cast<uintptr_t>(sizes[i]) * static_cast<uintptr_t>(elem_bytes(dtypes[i])));
       }
     if (spans.empty()) return ST_OK;
+    // nor with the scale, which some thread blocks would read before and some after its change
+    spans.emplace_back(reinterpret_cast<uintptr_t>(scale), reinterpret_cast<uintptr_t>(scale) + sizeof(float));
     std::sort(spans.begin(), spans.end());
     for (size_t i = 1; i < spans.size(); ++i)
       if (spans[i - 1].second > spans[i].first) return ST_INVALID_ARG;

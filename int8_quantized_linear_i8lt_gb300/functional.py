@@ -1142,7 +1142,7 @@ def _require_apart(what, ts) -> None:
 def scale_grads_(grads, scale: torch.Tensor) -> None:
     """Multiply all ``grads`` (None is left out) by the fp32 device scalar
     ``scale``, in place (i8lt_scale_grads); a scale of 1 moves nothing.  None
-    may overlap another one; columns and steps of one matrix may lie between
+    may overlap another one or the scale; columns and steps of one matrix may lie between
     one another."""
     grads = dense = _present(grads)
     if not grads:
