@@ -184,7 +184,26 @@ class LinearFP4(Linear4bit):
     fmt = "fp4"
 
 
-class LinearFP8(torch.nn.Module):
+class _FP8Weight(torch.nn.Module):
+    """A module with FP8 ``codes`` and fp32 ``scales``, which keep their types
+    when the module's dtype is converted (``half()``, ``to(dtype)``): while
+    the buffers are moved they are integers, as the codes of the int8 and 4-bit
+    layers are."""
+
+    def _apply(self, fn, recurse=True):
+        types = {"codes": (torch.uint8, F.FP8), "scales": (torch.int32, torch.float32)}
+        for name, (raw, own) in types.items():
+            if self._buffers[name].dtype == own:
+                self._buffers[name] = self._buffers[name].view(raw)
+        try:
+            return super()._apply(fn, recurse)
+        finally:
+            for name, (raw, own) in types.items():
+                if self._buffers[name].dtype == raw:
+                    self._buffers[name] = self._buffers[name].view(own)
+
+
+class LinearFP8(_FP8Weight):
     """Frozen FP8 linear layer: E4M3 codes with one fp32 scale per 128 x 128
     block of the weight; tokens (f16 or bf16) and output gradients are rounded
     to FP8 in blocks of 128 columns inside the call and multiplied on the FP8
@@ -220,7 +239,7 @@ class LinearFP8(torch.nn.Module):
         return f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}"
 
 
-class ExpertsFP8(torch.nn.Module):
+class ExpertsFP8(_FP8Weight):
     """``LinearFP8`` for ``experts`` weights at once, without bias: rows
     offsets[e] up to offsets[e + 1] of x [tokens, in_features], sorted by
     expert, take expert e's (``offsets``: int32 [experts + 1] on the device).
