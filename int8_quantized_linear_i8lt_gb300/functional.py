@@ -1037,12 +1037,9 @@ def adamw_step_8bit(params, grads, m: torch.Tensor, m_absmax: torch.Tensor, r: t
 # the gradients of a step: their norm, clipping and scaling
 # ---------------------------------------------------------------------------
 
-_current_device = torch._C._cuda_getDevice
-
-
 def _on(dev: int, call, *args) -> int:
     """call(*args) with CUDA device ``dev`` as the current one."""
-    if _current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:   # read here: a PyTorch without CUDA has no such name
         return call(*args)
     with torch.cuda.device(dev):
         return call(*args)
