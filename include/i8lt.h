@@ -693,6 +693,7 @@ int i8lt_scale_grads(void* const* grads, const int32_t* dtypes,
  *   ws   i8lt_fp8_workspace_size(M, C) bytes, 256-byte aligned, status word
  *        first, C the reduction (K forward, N backward); with grad_bias,
  *        i8lt_fp8_grad_bias_bytes(M, N) more
+ * After a wait that ran out (status word) the outputs that were to come are NaN.
  * out may not overlap an input.  Tokens, codes and outputs are 16-byte
  * aligned; scales, offsets, bias and grad_bias to their elements.
  */
@@ -774,6 +775,20 @@ int i8lt_debug_wait_timeout(int64_t limit_ns, void* ws, size_t ws_bytes, void* s
  * the forward workspace); each records I8LT_ERR_TIMEOUT (role 7) and
  * returns.  ws: at least 256 bytes, 256-byte aligned, cleared first. */
 int i8lt_debug_grid_wait_timeout(int64_t limit_ns, void* ws, size_t ws_bytes, void* stream);
+/* The same inside the products of the FP8 layers: i8lt_fp8_experts_forward or
+ * (transposed not 0) i8lt_fp8_experts_backward_input, offsets NULL for one
+ * weight (E = 1), with waits of limit_ns, whose thread blocks after `fetches`
+ * stages of operands (more where the kernel has more under way from its start;
+ * with many tokens, up to the end of a tile) wait for what never comes.  The status word then holds I8LT_ERR_TIMEOUT, and
+ * outputs that were to come are NaN.  A thread block with fewer stages in all
+ * works as ever. */
+int i8lt_debug_fp8_wait_timeout(int64_t limit_ns, int32_t fetches,
+                                int transposed, const void* x, int xt,
+                                int64_t M, const uint8_t* codes,
+                                const float* scales, int64_t E, int64_t N,
+                                int64_t K, const int32_t* offsets,
+                                int zero_rest, void* out, void* ws,
+                                size_t ws_bytes, void* stream);
 
 /* Launch shape the library uses for the persistent GEMM kernels
  * (kernel = I8LT_K_FWD_GEMM or I8LT_K_BWD_GEMM): CTAs (pairs x 2), threads

@@ -81,6 +81,9 @@ SIGNATURES = {
     "i8lt_backward_workspace_size": (c_size_t, [c_int64, c_int64, c_int]),
     "i8lt_debug_wait_timeout": (c_int, [c_int64, c_void_p, c_size_t, c_void_p]),
     "i8lt_debug_grid_wait_timeout": (c_int, [c_int64, c_void_p, c_size_t, c_void_p]),
+    "i8lt_debug_fp8_wait_timeout": (c_int, [c_int64, c_int32, c_int, c_void_p, c_int, c_int64, c_void_p, c_void_p,
+                                            c_int64, c_int64, c_int64, c_void_p, c_int, c_void_p, c_void_p, c_size_t,
+                                            c_void_p]),
     "i8lt_grad_weight_workspace_size": (c_size_t, [c_int64, c_int64, c_int64]),
     "i8lt_grad_weight": (c_int, [c_void_p, c_int, c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_int,
                                  c_void_p, c_size_t, c_void_p]),
@@ -268,6 +271,12 @@ def i8lt_debug_wait_timeout(limit_ns, ws, ws_bytes, stream=None) -> int:
 
 def i8lt_debug_grid_wait_timeout(limit_ns, ws, ws_bytes, stream=None) -> int:
     return load().i8lt_debug_grid_wait_timeout(limit_ns, _p(ws), ws_bytes, _p(stream))
+
+
+def i8lt_debug_fp8_wait_timeout(limit_ns, fetches, transposed, x, xt, M, codes, scales, E, N, K, offsets, zero_rest, out,
+                                ws, ws_bytes, stream=None) -> int:
+    return load().i8lt_debug_fp8_wait_timeout(limit_ns, fetches, transposed, x, xt, M, codes, scales, E, N, K, offsets,
+                                              zero_rest, out, ws, ws_bytes, stream)
 
 
 def i8lt_backward_workspace_size(M, N, gt) -> int:

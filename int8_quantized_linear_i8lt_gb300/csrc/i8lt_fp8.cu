@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(256) fp8_dequantize_weight_kernel(const uint8_
 // products
 // ---------------------------------------------------------------------------
 
+constexpr uint16_t kNaN16 = 0x7fff;   // in fp16 and in bf16
 struct Product {
   CUtensorMap tmX;           // codes of the tokens [M, ld(C)], box 128 columns x a tile's tokens
   CUtensorMap tmW;           // codes of the weight [E][N, ld(K)], box of a block and up to 128 outputs
@@ -198,6 +199,8 @@ struct Product {
   const void* bias;          // [R], or NULL
   void* out;                 // [M, R]
   DevStatus* st;
+  unsigned long long limit;  // of a wait, ns
+  int hold;                  // fetches after which a CTA waits for what never comes (the test of the waits), else INT_MAX
   const float* partial;      // sums of the tokens' columns over row ranges, or NULL
   void* grad_bias;           // [C]
   int M, R, C, E;
@@ -209,6 +212,18 @@ struct Product {
   bool vec;                  // rows of out start on 16 bytes
   bool zero_rest;            // rows of no expert are written as zeros (else left as they are)
 };
+
+__device__ __forceinline__ bool wait_for(const Product& p, uint64_t* bar, uint32_t parity, volatile int* abort, int where) {
+  return mbar_wait_limit(bar, parity, abort, p.st, where, 0, p.limit);
+}
+
+// After a wait that ran out: NaN in the outputs that are not to come, `rows`
+// rows from row0 on and `count` outputs from r on, by a warp.
+__device__ __forceinline__ void lose_rows(const Product& p, int row0, int rows, int r, int count, int lane) {
+  uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(row0) * p.R + r;
+  for (int row = 0; row < rows; ++row)
+    for (int c = lane; c < min(count, p.R - r); c += 32) out[static_cast<int64_t>(row) * p.R + c] = kNaN16;
+}
 
 constexpr int kTileBytes = 128 * 128;
 enum { kWhereFetch = 1, kWhereProduct = 2, kWhereOut = 3 };
@@ -402,6 +417,12 @@ __device__ __forceinline__ float4 cluster_sum(const float* src, int split) {
   return v;
 }
 
+// After a wait that ran out: NaN for a CTA's part of its cluster's sums, by its
+// epilogue's threads, once nothing more writes to its shared memory.
+__device__ __forceinline__ void lose_sums(uint8_t* smem, int count) {
+  for (int i = static_cast<int>(threadIdx.x) - 64; i < count; i += 128) reinterpret_cast<float*>(smem)[i] = __int_as_float(0x7fffffff);
+}
+
 constexpr int kEpiWarps = 4;         // warps 2 to 5: lanes 32 (w % 4) of the accumulators
 
 // ---- few tokens -----------------------------------------------------------
@@ -504,7 +525,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const _
         const Tile x = tile_at<128>(p, groups, t, num_m, num_r, kN);
         for (int b = 0; b < count; ++b, ++it) {
           const int s = it % kFewStages;
-          if (!mbar_wait(&y.empty[s], ((it / kFewStages) & 1) ^ 1, abort, p.st, kWhereFetch)) {
+          if ((it == max(p.hold, ahead) && !wait_for(p, &y.last, 0, abort, kWhereFetch)) ||
+              !wait_for(p, &y.empty[s], ((it / kFewStages) & 1) ^ 1, abort, kWhereFetch)) {
             ok = false;   // not before the fetches ahead have their tokens: those stages are empty
             break;
           }
@@ -525,13 +547,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const _
       for (int t = first; t < tiles && ok; t += step) {
         for (int b = 0; b < count && ok; b += kGroup, ++grp) {
           const int a = grp & 1;
-          if (!mbar_wait(&y.acc_empty[a], ((grp >> 1) & 1) ^ 1, abort, p.st, kWhereProduct)) {
+          if (!wait_for(p, &y.acc_empty[a], ((grp >> 1) & 1) ^ 1, abort, kWhereProduct)) {
             ok = false;
             break;
           }
           for (int g = 0; g < min(kGroup, count - b); ++g, ++it) {
             const int s = it % kFewStages;
-            if (!mbar_wait(&y.full[s], (it / kFewStages) & 1, abort, p.st, kWhereProduct)) {
+            if (!wait_for(p, &y.full[s], (it / kFewStages) & 1, abort, kWhereProduct)) {
               ok = false;
               break;
             }
@@ -559,9 +581,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const _
       zero_rest(p, groups, blockIdx.x * kEpiWarps + quad, gridDim.x * kEpiWarps, lane);
     if (p.partial != nullptr)
       sum_bias(p, (static_cast<int64_t>(blockIdx.x) * kEpiWarps + quad) * 32 + lane, static_cast<int64_t>(gridDim.x) * kEpiWarps * 32);
-    int grp = 0;
+    int grp = 0, t = first;
     bool ok = true;
-    for (int t = first; t < tiles && ok; t += step) {
+    for (; t < tiles; t += step) {
       const Tile x = tile_at<128>(p, groups, t, num_m, num_r, kN);
       const int r = x.r0 + quad * 32 + lane;
       const float* ws = p.ws + static_cast<int64_t>(x.e) * p.nb * p.kb + (kT ? x.r0 / kBlk : x.r0 / kBlk * p.kb);
@@ -587,7 +609,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const _
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] = xv[i] * wv[i];
         if (b + kGroup < count) fetch(b + kGroup);
-        if (!__all_sync(0xffffffffu, mbar_wait(&y.acc_full[a], (grp >> 1) & 1, abort, p.st, kWhereOut))) {
+        if (!__all_sync(0xffffffffu, wait_for(p, &y.acc_full[a], (grp >> 1) & 1, abort, kWhereOut))) {
           ok = false;
           break;
         }
@@ -626,12 +648,19 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_product_few_kernel(const _
           if (x.m0 + i < x.end) dst[static_cast<int64_t>(i) * p.R] = static_cast<uint16_t>(pack16(p.bf16, acc[i] + bias, 0.f));
       }
     }
+    if (split == 1)   // the tiles that a wait that ran out cut off
+      for (; t < tiles; t += step) {
+        const Tile x = tile_at<128>(p, groups, t, num_m, num_r, kN);
+        lose_rows(p, x.m0, min(kN, x.end - x.m0), x.r0 + quad * 32, 32, lane);
+      }
   }
   if (split > 1) {
     // one tile a cluster; every rank adds up its share of the tokens, a warp
     // four outputs a lane
+    __syncthreads();
+    if (warp >= 2 && *abort) lose_sums(smem, kN * 128);
     cluster_sync();
-    if (warp >= 2 && first < tiles && *abort == 0) {
+    if (warp >= 2 && first < tiles) {
       const Tile x = tile_at<128>(p, groups, first, num_m, num_r, kN);
       const int r = x.r0 + 4 * lane;
       for (int i = rank * kEpiWarps + warp - 2; i < min(kN, x.end - x.m0); i += split * kEpiWarps) {
@@ -749,7 +778,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
         const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, kTileM);
         for (int b = b0; b < b1; ++b, ++it) {
           const int s = it % stages;
-          if (!mbar_wait(&y.empty[s], ((it / stages) & 1) ^ 1, abort, p.st, kWhereFetch)) {
+          if ((it == max(p.hold, ahead) && !wait_for(p, &y.last, 0, abort, kWhereFetch)) ||
+              !wait_for(p, &y.empty[s], ((it / stages) & 1) ^ 1, abort, kWhereFetch)) {
             ok = false;   // not before the fetches ahead have their tokens: those stages are empty
             break;
           }
@@ -769,8 +799,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
       for (int t = first; t < tiles && ok; t += step) {
         for (int b = b0; b < b1; ++b, ++it) {
           const int s = it % stages, a = it & 1;
-          if (!mbar_wait(&y.full[s], (it / stages) & 1, abort, p.st, kWhereProduct) ||
-              !mbar_wait(&y.acc_empty[a], ((it >> 1) & 1) ^ 1, abort, p.st, kWhereProduct)) {
+          if (!wait_for(p, &y.full[s], (it / stages) & 1, abort, kWhereProduct) ||
+              !wait_for(p, &y.acc_empty[a], ((it >> 1) & 1) ^ 1, abort, kWhereProduct)) {
             ok = false;
             break;
           }
@@ -800,9 +830,9 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
     if (p.partial != nullptr)
       sum_bias(p, (static_cast<int64_t>(blockIdx.x) * kEpiWarps + quad) * 32 + lane, static_cast<int64_t>(gridDim.x) * kEpiWarps * 32);
     const int wstep = kT ? p.kb : 1;
-    int it = 0;
+    int it = 0, t = first;
     bool ok = true;
-    for (int t = first; t < tiles && ok; t += step) {
+    for (; t < tiles; t += step) {
       const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, kTileM);
       const int last = min(x.end, x.m0 + kTileM), row0 = x.m0 + quad * 32, m = row0 + lane;
       const bool any = row0 < last;   // a warp without tokens hands the accumulators on
@@ -827,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
       }
       for (int b = 0; b < b1 - b0; ++b, ++it) {
         const int a = it & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&y.acc_full[a], (it >> 1) & 1, abort, p.st, kWhereOut))) {
+        if (!__all_sync(0xffffffffu, wait_for(p, &y.acc_full[a], (it >> 1) & 1, abort, kWhereOut))) {
           ok = false;
           break;
         }
@@ -898,12 +928,20 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_product_kernel(const __grid_c
         __syncwarp();
       }
     }
+    if (p.split == 1)   // the tiles that a wait that ran out cut off
+      for (; t < tiles; t += step) {
+        const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, kTileM);
+        const int row0 = x.m0 + quad * 32;
+        lose_rows(p, row0, min(32, min(x.end, x.m0 + kTileM) - row0), x.r0, kTileR, lane);
+      }
   }
   if (p.split > 1) {
     // one tile a cluster; every rank adds up its share of the tile, 4 outputs
     // at a time
+    __syncthreads();
+    if (warp >= 2 && *abort) lose_sums(smem, kTileM * kTileR);
     cluster_sync();
-    if (warp >= 2 && first < tiles && *abort == 0) {
+    if (warp >= 2 && first < tiles) {
       const Tile x = tile_at<kTileR>(p, groups, first, num_m, num_r, kTileM);
       const int rows = min(kTileM, x.end - x.m0), count = rows * (kTileR / 4);
       for (int g = rank * (kEpiWarps * 32) + static_cast<int>(threadIdx.x) - 64; g < count; g += p.split * kEpiWarps * 32) {
@@ -1048,9 +1086,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, kTileM);
+        // by tiles: a test of every fetch costs 0.5 % of 4096 tokens, 4096 -> 11008
+        if (it >= p.hold && !wait_for(p, &y.last, 0, abort, kWhereFetch)) break;
         for (int b = 0; b < blocks; ++b, ++it) {
           const int s = it % kWideStages;
-          if (!mbar_wait(&y.empty[s], ((it / kWideStages) & 1) ^ 1, abort, p.st, kWhereFetch)) {
+          if (!wait_for(p, &y.empty[s], ((it / kWideStages) & 1) ^ 1, abort, kWhereFetch)) {
             ok = false;
             break;
           }
@@ -1076,8 +1116,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const
       const uint32_t acc = tmem + a * kTileR;
       for (int it = a; it < total; it += 2) {
         const int s = it % kWideStages;
-        if (!mbar_wait(&y.full[s], (it / kWideStages) & 1, abort, p.st, kWhereProduct) ||
-            !mbar_wait(&y.acc_empty[a], ((it >> 1) & 1) ^ 1, abort, p.st, kWhereProduct))
+        if (!wait_for(p, &y.full[s], (it / kWideStages) & 1, abort, kWhereProduct) ||
+            !wait_for(p, &y.acc_empty[a], ((it >> 1) & 1) ^ 1, abort, kWhereProduct))
           break;
         tc_fence_after();
         const uint32_t xa = base + s * kWideStageBytes, wa = xa + kTileBytes;
@@ -1129,7 +1169,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const
         // with block it - 2 the scales of block it - 1 have been read; this
         // fetch takes the place of an older one's
         static_assert(kScaleAhead + 1 <= kScaleRing - 1, "scale ring");
-        if (!__all_sync(0xffffffffu, mbar_wait(&y.scale_read[it & 1], ((it >> 1) & 1) ^ 1, abort, p.st, kWhereOut))) break;
+        if (!__all_sync(0xffffffffu, wait_for(p, &y.scale_read[it & 1], ((it >> 1) & 1) ^ 1, abort, kWhereOut))) break;
         fetch();
         cp_async_wait<kScaleAhead - 1>();   // block it + 1 is there
         __syncwarp();
@@ -1148,12 +1188,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const
       zero_rest(p, groups, blockIdx.x * kWideEpiWarps + ew, gridDim.x * kWideEpiWarps, lane);
     if (p.partial != nullptr)
       sum_bias(p, (static_cast<int64_t>(blockIdx.x) * kWideEpiWarps + ew) * 32 + lane, static_cast<int64_t>(gridDim.x) * kWideEpiWarps * 32);
-    int it = 0;
+    int it = 0, t = first;
     bool ok = true;
     float now = 0.f;   // the product of the scales of block it
     auto scale_of = [&](int i) { return y.xs[i % kScaleRing][quad * 32 + lane] * y.ws[i % kScaleRing][half]; };
-    auto wait = [&]() { return __all_sync(0xffffffffu, mbar_wait(&y.acc_full[it & 1], (it >> 1) & 1, abort, p.st, kWhereOut)); };
-    for (int t = first; t < tiles && ok; t += step) {
+    auto wait = [&]() { return __all_sync(0xffffffffu, wait_for(p, &y.acc_full[it & 1], (it >> 1) & 1, abort, kWhereOut)); };
+    for (; t < tiles; t += step) {
       const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, kTileM);
       const int row0 = x.m0 + quad * 32, r0 = x.r0 + half * kWideCols;
       float bias[4];   // used at the tile's end
@@ -1235,6 +1275,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_product_wide_kernel(const
         }
       }
       __syncwarp();
+    }
+    for (; t < tiles; t += step) {   // the tiles that a wait that ran out cut off
+      const Tile x = tile_at<kTileR>(p, groups, t, num_m, num_r, kTileM);
+      const int row0 = x.m0 + quad * 32;
+      lose_rows(p, row0, min(32, x.end - row0), x.r0 + half * kWideCols, kWideCols, lane);
     }
     if (lane == 0) bulk_wait_all();
   }
@@ -1389,7 +1434,8 @@ size_t scales_bytes(int64_t M, int64_t C) { return align_up(static_cast<size_t>(
 // [their scales][partial sums of grad_bias].
 int product(bool transposed, const void* x, int xt, int64_t M, const uint8_t* codes, const float* scales, int64_t E,
             int64_t N, int64_t K, const int32_t* offsets, int zero_rest, const void* bias, int bt, void* out,
-            void* grad_bias, void* ws, size_t ws_bytes, void* stream) {
+            void* grad_bias, void* ws, size_t ws_bytes, void* stream, unsigned long long limit = kWaitTimeoutNs,
+            int hold = INT32_MAX) {
   const int64_t C = transposed ? N : K, R = transposed ? K : N;
   if (xt != DT_F16 && xt != DT_BF16) return ST_UNSUPPORTED_DTYPE;
   if ((bias != nullptr || grad_bias != nullptr) && !valid_dt(bt)) return ST_UNSUPPORTED_DTYPE;
@@ -1427,6 +1473,8 @@ int product(bool transposed, const void* x, int xt, int64_t M, const uint8_t* co
   p.bias_dt = bt;
   p.out = out;
   p.st = st;
+  p.limit = limit;
+  p.hold = hold;
   p.M = static_cast<int>(M);
   p.R = static_cast<int>(R);
   p.C = static_cast<int>(C);
@@ -1539,6 +1587,15 @@ int i8lt_fp8_experts_forward(const void* x, int xt, int64_t M, const uint8_t* co
   if (offsets == nullptr || (M > 0 && out == nullptr)) return ST_INVALID_ARG;
   return product(false, x, xt, M, codes, scales, E, N, K, offsets, zero_rest, nullptr, 0, out, nullptr, ws, ws_bytes,
                  stream);
+}
+
+int i8lt_debug_fp8_wait_timeout(int64_t limit_ns, int32_t fetches, int transposed, const void* x, int xt, int64_t M,
+                                const uint8_t* codes, const float* scales, int64_t E, int64_t N, int64_t K,
+                                const int32_t* offsets, int zero_rest, void* out, void* ws, size_t ws_bytes,
+                                void* stream) {
+  if (limit_ns <= 0 || limit_ns > 2000000000LL || fetches < 0 || (M > 0 && out == nullptr)) return ST_INVALID_ARG;
+  return product(transposed != 0, x, xt, M, codes, scales, E, N, K, offsets, zero_rest, nullptr, 0, out, nullptr, ws,
+                 ws_bytes, stream, static_cast<unsigned long long>(limit_ns), fetches);
 }
 
 int i8lt_fp8_experts_backward_input(const void* g, int gt, int64_t M, const uint8_t* codes, const float* scales,
