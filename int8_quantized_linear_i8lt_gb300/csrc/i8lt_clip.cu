@@ -119,7 +119,10 @@ __device__ __forceinline__ double block_sum(const GradList<kCap>& L, int from, i
       constexpr int V = kPack<T>;
       if (thread < head) sum += squares(to_float(p[-1 - thread]));
       float s[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t any = 0;   // the bits of all elements, to tell zeros from squares that were lost
       auto add = [&](const Pack<T>& x) {
+        const uint4 w = *reinterpret_cast<const uint4*>(&x);
+        any |= w.x | w.y | w.z | w.w;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const float f = to_float(x.v[i]);
@@ -141,6 +144,7 @@ __device__ __forceinline__ double block_sum(const GradList<kCap>& L, int from, i
           } else {
             for (int i = e; i < left; ++i) {
               const float f = to_float(p[i]);
+              any |= __float_as_uint(f);
               s[0] = fmaf(f, f, s[0]);
             }
           }
@@ -149,12 +153,15 @@ __device__ __forceinline__ double block_sum(const GradList<kCap>& L, int from, i
       const float all = (s[0] + s[1]) + (s[2] + s[3]);
       if (all >= 0x1p-80f && all <= 0x1p100f) {
         sum += all;
-      } else {
+      } else if ((any & (sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu)) != 0) {
 #pragma unroll 1
-        for (int j = 0; j < kPacks * V; ++j) {
-          const int e = (j / V * kThreads + thread) * V + j % V;
-          const float f = e < left ? to_float(p[e]) : 0.f;
-          if (f != 0.f) sum += squares(f);
+        for (int j = 0; j < kPacks; ++j) {
+          const int e = (j * kThreads + thread) * V;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float f = e + i < left ? to_float(p[e + i]) : 0.f;
+            if (f != 0.f) sum += squares(f);
+          }
         }
       }
     });

@@ -95,3 +95,44 @@ def test_tensors_that_require_a_gradient_are_scaled_in_any_layout():
     norm = I.clip_grad_norm_(p, 1.0)
     f = I.grad_norm([torch.ones(24, device="cuda")], 1.0)[1]
     assert abs(float(norm) - 24 ** 0.5) <= 1e-5 and bool((p.grad == f).all())
+
+
+def median_time(call):
+    times = []
+    for _ in range(12):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        torch.cuda._sleep(200000)
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    return sorted(times[2:])[5]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_zeros_are_read_once(dtype):
+    """Gradients of zeros are ordinary (unused layers, the first step of an
+    adapter); reading them again, to look for squares lost below fp32's range,
+    took five times as long."""
+    zeros = torch.zeros(60000000, dtype=dtype, device="cuda")
+    zeros[::3] = -0.0
+    ones = torch.full_like(zeros, 1e-2)
+    assert [float(v) for v in I.grad_norm([zeros], 1.0)] == [0, 1, 0]
+    assert median_time(lambda: I.grad_norm([zeros], 1.0)) <= 1.5 * median_time(lambda: I.grad_norm([ones], 1.0))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("n", [5, 8191, 300007])
+def test_few_values_among_zeros(n, dtype):
+    """Small ones, whose squares fp32 does not hold, beside zeros, in every place of a unit."""
+    g = torch.Generator().manual_seed(n)
+    smallest = {F32: 2.0 ** -149, BF16: 2.0 ** -133, F16: 2.0 ** -24}[dtype]
+    for value in (smallest, -smallest, 2.0 ** -24):
+        for place in (0, n - 1, *torch.randint(0, n, (6,), generator=g).tolist()):
+            t = torch.zeros(n, dtype=dtype, device="cuda")
+            t[place] = value
+            assert float(I.grad_norm([t])[0]) == abs(value)
+    rows = torch.zeros(n, 40, dtype=dtype, device="cuda")
+    rows[::7] = torch.randn(rows[::7].shape, generator=g).to(dtype).cuda()
+    assert abs(float(I.grad_norm([rows])[0]) - norm64([rows])) <= norm64([rows]) * NORM_TOL
