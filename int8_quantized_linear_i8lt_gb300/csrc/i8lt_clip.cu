@@ -100,9 +100,9 @@ __device__ __forceinline__ double block_total(double sum, double* sums) {
 }
 
 // One block's part of the sum of squares, in thread 0: the units [from, to).
-// A thread sums the squares of 32 or 64 elements of a unit in fp32 and those
-// sums in fp64 (one fp64 addition for so many elements: the machine has few
-// fp64 units).  A sum so large or small that squares may have left fp32's
+// A thread sums the squares of 32 elements of a unit in fp32 and those sums in
+// fp64 (one fp64 addition for so many elements: the machine has few fp64
+// units).  A sum so large or small that squares may have left fp32's
 // range is taken again in fp64.  Bound by HBM: 8 loads of 16 bytes a thread
 // under way.  90 million f32 gradients: 57 us, 6.3 TB/s; 62 million bf16 ones in
 // 128 tensors 25 us, 4.9 TB/s, start and end of the launch included.
@@ -129,16 +129,40 @@ __device__ __forceinline__ double block_sum(const GradList<kCap>& L, int from, i
           s[i & 3] = fmaf(f, f, s[i & 3]);
         }
       };
+      // the sums of packs [j - kRun, j), 32 elements, to fp64
+      constexpr int kRun = 32 / V;
+      auto close = [&](int j) {
+        const float all = (s[0] + s[1]) + (s[2] + s[3]);
+        if (all >= 0x1p-80f && all <= 0x1p100f) {
+          sum += all;
+        } else if ((any & (sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu)) != 0) {
+#pragma unroll 1
+          for (int k = j - kRun; k < j; ++k) {
+            const int e = (k * kThreads + thread) * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const float f = e + i < left ? to_float(p[e + i]) : 0.f;
+              if (f != 0.f) sum += squares(f);
+            }
+          }
+        }
+        s[0] = s[1] = s[2] = s[3] = 0.f;
+        any = 0;
+      };
       const T* q = p + thread * V;
       if (left >= kUnitBytes / static_cast<int>(sizeof(T))) {
         Pack<T> x[kPacks];
 #pragma unroll
         for (int j = 0; j < kPacks; ++j) x[j] = *reinterpret_cast<const Pack<T>*>(q + j * kThreads * V);
 #pragma unroll
-        for (int j = 0; j < kPacks; ++j) add(x[j]);
+        for (int j = 0; j < kPacks; ++j) {
+          add(x[j]);
+          if ((j + 1) % kRun == 0) close(j + 1);
+        }
       } else {
 #pragma unroll 1
-        for (int e = thread * V; e < left; e += kThreads * V) {
+        for (int j = 0; j < kPacks; ++j) {
+          const int e = (j * kThreads + thread) * V;
           if (e + V <= left) {
             add(*reinterpret_cast<const Pack<T>*>(p + e));
           } else {
@@ -148,20 +172,7 @@ __device__ __forceinline__ double block_sum(const GradList<kCap>& L, int from, i
               s[0] = fmaf(f, f, s[0]);
             }
           }
-        }
-      }
-      const float all = (s[0] + s[1]) + (s[2] + s[3]);
-      if (all >= 0x1p-80f && all <= 0x1p100f) {
-        sum += all;
-      } else if ((any & (sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu)) != 0) {
-#pragma unroll 1
-        for (int j = 0; j < kPacks; ++j) {
-          const int e = (j * kThreads + thread) * V;
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float f = e + i < left ? to_float(p[e + i]) : 0.f;
-            if (f != 0.f) sum += squares(f);
-          }
+          if ((j + 1) % kRun == 0) close(j + 1);
         }
       }
     });

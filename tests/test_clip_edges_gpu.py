@@ -136,3 +136,18 @@ def test_few_values_among_zeros(n, dtype):
     rows = torch.zeros(n, 40, dtype=dtype, device="cuda")
     rows[::7] = torch.randn(rows[::7].shape, generator=g).to(dtype).cuda()
     assert abs(float(I.grad_norm([rows])[0]) - norm64([rows])) <= norm64([rows]) * NORM_TOL
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_fp32_sums_end_after_32_elements(dtype):
+    """Every sum in fp32 starts with a 1 whose half step is above each of the
+    squares that follow: those of the same sum are lost, 7 beside each 1 as long as
+    a sum of 32 elements has four parts of 8 squares.  That is 7 half steps of
+    the sum, 3.5 of the norm, and one for its rounding; parts of 16 squares
+    lose 15."""
+    b = 2.0 ** -12 * (1 - torch.finfo(dtype).eps / 2)
+    t = torch.full((100, 8, 256, 8), b, device="cuda").to(dtype)      # 8 times 8 elements a thread
+    assert float(t[0, 0, 0, 0]) == b
+    t[:, 0, :, :4] = 1
+    ref = norm64([t])
+    assert abs(float(I.grad_norm([t])[0]) - ref) <= 4.5 * 2.0 ** -24 * ref
