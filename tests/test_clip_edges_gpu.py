@@ -151,3 +151,11 @@ def test_fp32_sums_end_after_32_elements(dtype):
     t[:, 0, :, :4] = 1
     ref = norm64([t])
     assert abs(float(I.grad_norm([t])[0]) - ref) <= 4.5 * 2.0 ** -24 * ref
+
+
+def test_every_scaled_tensor_has_a_new_version():
+    ts = [torch.ones(n, dtype=d, device="cuda") for n, d in ((5, F32), (70, BF16), (9000, F16), (33, F32))]
+    ts.append(torch.ones(4, 6, device="cuda")[:, ::2])
+    versions = [t._version for t in ts]
+    I.scale_grads_([ts[0], None, *ts[1:]], torch.full((), 0.5, device="cuda"))
+    assert all(t._version > v for t, v in zip(ts, versions))
