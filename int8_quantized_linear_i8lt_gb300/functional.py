@@ -1115,25 +1115,33 @@ def _apart(a: int, A: list, b: int, B: list) -> bool:
     return False
 
 
+def _layout(t: torch.Tensor) -> list:
+    size = t.element_size()
+    return sorted([(s * size, n) for s, n in zip(t.stride(), t.shape) if n > 1], reverse=True) + [(1, size)]
+
+
 def _require_apart(what, ts) -> None:
     """Refuses tensors of which two may share memory.  Pairs of contiguous ones
-    are left to the library."""
-    views = []
+    are left to the library; layouts are looked at only where one tensor
+    starts before another one's end."""
+    spans = []
     for t in ts:
-        if t.numel():
-            size = t.element_size()
-            dims = sorted([(s * size, n) for s, n in zip(t.stride(), t.shape) if n > 1], reverse=True) + [(1, size)]
+        n = t.numel()
+        if n:
+            if not t.is_contiguous():
+                n = sum([s * (k - 1) for s, k in zip(t.stride(), t.shape)]) + 1
             start = t.data_ptr()
-            views.append((start, start + sum([s * (n - 1) for s, n in dims]) + 1, dims, t.is_contiguous()))
-    views.sort(key=lambda v: v[0])
-    open_ = []
-    for v in views:
-        open_ = [o for o in open_ if o[1] > v[0]]
-        for o in open_:
-            if not (o[3] and v[3]) and not _apart(o[0], o[2], v[0], v[2]):
-                raise I8LTError(f"{what}: two tensors that share memory, or lie between one another in a way that does not "
-                                "show that they share none")
-        open_.append(v)
+            spans.append((start, start + n * t.element_size(), t))
+    spans.sort(key=operator.itemgetter(0))
+    before = []
+    for start, end, t in spans:
+        if before:
+            before = [o for o in before if o[1] > start]
+            for a, _, o in before:
+                if not (o.is_contiguous() and t.is_contiguous()) and not _apart(a, _layout(o), start, _layout(t)):
+                    raise I8LTError(f"{what}: two tensors that share memory, or lie between one another in a way that does not "
+                                    "show that they share none")
+        before.append((start, end, t))
 
 
 def scale_grads_(grads, scale: torch.Tensor) -> None:
