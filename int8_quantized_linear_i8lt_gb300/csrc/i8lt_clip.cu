@@ -102,10 +102,12 @@ __device__ __forceinline__ double block_total(double sum, double* sums) {
 // One block's part of the sum of squares, in thread 0: the units [from, to).
 // A thread sums the squares of 32 elements of a unit in fp32 and those sums in
 // fp64 (one fp64 addition for so many elements: the machine has few fp64
-// units).  A sum so large or small that squares may have left fp32's
-// range is taken again in fp64.  Bound by HBM: 8 loads of 16 bytes a thread
-// under way.  90 million f32 gradients: 57 us, 6.3 TB/s; 62 million bf16 ones in
-// 128 tensors 25 us, 4.9 TB/s, start and end of the launch included.
+// units; 62 million bf16 values, 64 elements: 1 us less).  A sum so large or
+// small that squares may have left fp32's range is taken again in fp64, unless
+// all bits that were loaded are zeros.  Bound by HBM: 8 loads of 16 bytes a
+// thread under way.  90 million f32 gradients: 58 us, 6.2 TB/s; 62 million bf16
+// ones in 128 tensors 26 us, 4.8 TB/s, start and end of the launch included;
+// zeros the same.
 template <int kGroups, int kCap>
 __device__ __forceinline__ double block_sum(const GradList<kCap>& L, int from, int to) {
   __shared__ double sums[kGroups * kThreads / 32];
